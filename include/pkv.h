@@ -474,6 +474,139 @@ pkv_status pkv_encoder_merge(const void *buffer, int64_t num_blocks, int64_t blo
                              void *hidden, int64_t num_tokens, int64_t hidden_row_stride_bytes,
                              uint64_t *filled, int32_t *err_flags, pkv_stream_t stream);
 
+/*
+ * The 4-bit K/V pool: pkv_quant_store, pkv_quant_gather, pkv_quant_decode and
+ * pkv_quant_extend.
+ *
+ * The calls above keep K and V in bf16.  These four keep them in 4 bits: 9/16 of a
+ * byte per element, 3.6 times less memory and traffic.  16 consecutive head dims of
+ * one row are a block: 16 e2m1 codes (0, 0.5, 1, 1.5, 2, 3, 4, 6 and their negatives)
+ * and one e4m3 scale s.  A kv head has an fp32 scale g for K and one for V besides
+ * (k_scale, v_scale: device fp32 [kv_heads], NULL for 1), which keeps s in e4m3's
+ * range; a good one is the head's largest magnitude / 2688.  Every g is positive and
+ * finite; another value raises PKV_DEVERR_RANGE.
+ *     s = e4m3(max |x_i| / (6 g)),   code_i = e2m1(x_i / (s g)),   value_i = code_i s g
+ * in fp32, both roundings to nearest, ties to even, saturating (448, 6).  s = 0 stores
+ * zeros.  A block that holds an infinity or a NaN reads back as NaN in all its dims.
+ *
+ * The pool is uint8: slots in tiles of t = min(page_size, 64) consecutive ones, each
+ * tile kv_heads pieces of pkv_quant_tile_bytes(page_size, head_dim) bytes, tiles
+ * tile_stride bytes apart (a multiple of 16; the pool is 16-byte aligned).  Slot n of
+ * a kv head is entry n % t of its piece of tile n / t.  A piece is
+ *     K codes [t][head_dim/2], V codes [t][head_dim/2],
+ *     K scales [t][head_dim/16], V scales [t][head_dim/16],
+ * (two codes per byte, the even dim in the low half), rounded up to 16 bytes.  Slots,
+ * pages and req_to_token are those of the bf16 pool: pkv_alloc_extend,
+ * pkv_write_req_to_token, pkv_build_indices and pkv_span_plan serve both.  page_size
+ * is a power of two in [1, 1024], head_dim 64 or 128 (K and V alike); an MLA latent
+ * pool has no 4-bit form.
+ */
+
+/* Bytes of one kv head's piece of a tile (0 for an unsupported page_size or head_dim). */
+size_t pkv_quant_tile_bytes(int32_t page_size, int32_t head_dim);
+
+/*
+ * pkv_quant_store -- pkv_store into a 4-bit pool: quantise this step's K/V rows.
+ *
+ * k_new, v_new  bf16, token i's rows [kv_heads, head_dim] at i * k_token_stride (in
+ *               elements; v_token_stride alike), so they may be slices of a wider row
+ * slot_mapping  int32 [n_tokens]; a negative entry is a padded token and is skipped; an
+ *               entry past the pool raises PKV_DEVERR_RANGE and is skipped, as are the
+ *               rows of a head whose scale is not usable.
+ * Nothing but the rows of the named slots is written.  A slot that one call names
+ * twice holds a mixture of the two rows.
+ */
+pkv_status pkv_quant_store(void *pool, int64_t num_tiles, int64_t tile_stride, int32_t kv_heads,
+                           int32_t head_dim, int32_t page_size, const float *k_scale, const float *v_scale,
+                           const void *k_new, const void *v_new, int64_t k_token_stride,
+                           int64_t v_token_stride, const int32_t *slot_mapping, int32_t n_tokens,
+                           int32_t *err_flags, pkv_stream_t stream);
+
+/*
+ * pkv_quant_gather -- pkv_ragged_gather from a 4-bit pool: rows read back as bf16.
+ *
+ * The same rows in the same order, cu_seqlens included, with k_out, v_out bf16
+ * [out_rows_cap, kv_heads, head_dim] holding value_i rounded to bf16 (nearest even).
+ * Rows past the batch's last are left as they were.  The checks, flags and zero rows
+ * are pkv_ragged_gather's.
+ */
+pkv_status pkv_quant_gather(const void *pool, int64_t num_tiles, int64_t tile_stride, int32_t kv_heads,
+                            int32_t head_dim, int32_t page_size, const float *k_scale,
+                            const float *v_scale, const int32_t *req_to_token, int64_t r2t_rows,
+                            int64_t r2t_row_stride, int64_t r2t_width, const int32_t *req_pool_idx,
+                            const int32_t *kv_start, const int32_t *seq_lens, int32_t batch,
+                            int32_t max_seq_len, void *k_out, void *v_out, int64_t out_rows_cap,
+                            int32_t *cu_seqlens, int32_t *err_flags, pkv_stream_t stream);
+
+/* Arguments of pkv_quant_decode and pkv_quant_extend. */
+typedef struct pkv_quant_args {
+    int32_t layout;            /* PKV_LAYOUT_CSR, PKV_LAYOUT_BLOCK_TABLE or PKV_LAYOUT_REQ_TO_TOKEN */
+    int32_t batch;             /* B >= 0 */
+    int32_t num_q_heads;       /* Hq */
+    int32_t num_kv_heads;      /* Hkv; Hq / Hkv any whole number in [1, 16] */
+    int32_t head_dim;          /* 64 or 128 */
+    int32_t page_size;
+    float sm_scale;            /* softmax scale, positive and finite */
+    int32_t max_seq_len;       /* host upper bound on every request's key count */
+    int32_t kv_chunk;          /* keys per split, a multiple of 64; 0 lets the library choose */
+    int32_t block_table_width;
+    int64_t total_q;           /* query rows: B for pkv_quant_decode, qo_indptr[B] for pkv_quant_extend */
+    int64_t total_kv;          /* pkv_quant_extend: host upper bound on the sum of the key counts (sizes the
+                                  workspace); 0: batch * max_seq_len */
+    int64_t num_tiles;         /* the pool (see above) */
+    int64_t tile_stride;
+    int64_t q_row_stride;      /* elements between query rows (>= Hq * head_dim, a multiple of 8) */
+    int64_t kv_indices_len;    /* CSR: entries of kv_indices */
+    const void *q;             /* bf16 [total_q, Hq, head_dim], rows q_row_stride apart */
+    const void *pool;
+    const float *k_scale;      /* fp32 [Hkv] or NULL */
+    const float *v_scale;
+    const int32_t *qo_indptr;  /* pkv_quant_extend [B+1]; NULL for pkv_quant_decode */
+    const int32_t *kv_end;     /* pkv_quant_extend [total_q] or NULL (causal), as for pkv_extend */
+    const int32_t *kv_indptr;        /* CSR [B+1] */
+    const int32_t *kv_indices;       /* CSR pages */
+    const int32_t *kv_last_page_len; /* CSR [B] */
+    const int32_t *block_table;      /* BLOCK_TABLE [B, block_table_width] */
+    const int32_t *seq_lens;         /* BLOCK_TABLE and REQ_TO_TOKEN [B] */
+    const int32_t *req_to_token;     /* REQ_TO_TOKEN: as in pkv_decode_args */
+    int64_t r2t_rows;
+    int64_t r2t_row_stride;
+    int64_t r2t_width;
+    const int32_t *req_pool_idx;
+    const int32_t *kv_start;
+    void *out;                 /* bf16 [total_q, Hq, head_dim] */
+    float *lse;                /* fp32 [total_q, Hq], natural log; nullable */
+} pkv_quant_args;
+
+/*
+ * pkv_quant_decode -- pkv_decode (GQA / MHA) over a 4-bit pool.
+ *
+ * One query row per request over all its keys; the same formulas with K and V the
+ * pool's values.  Page lists, checks and flags are pkv_decode's.  Arithmetic: K and V
+ * enter the tensor cores as code * s, exact in 16 bits; scores, softmax and sums are
+ * fp32, the weights fp16 or bf16, the output bf16 rounded to nearest even.  What the
+ * pool holds at slots past a request's keys does not matter, NaN patterns included.
+ * workspace: at least pkv_quant_decode_workspace_size(args) bytes, 256-byte aligned, not
+ * shared with a call that may run at the same time; it needs no initialisation.
+ */
+pkv_status pkv_quant_decode(const pkv_quant_args *args, void *workspace, size_t workspace_bytes,
+                            int32_t *err_flags, pkv_stream_t stream);
+/* Workspace bytes pkv_quant_decode needs for these arguments (at least 256; 0 on invalid arguments). */
+size_t pkv_quant_decode_workspace_size(const pkv_quant_args *args);
+
+/*
+ * pkv_quant_extend -- pkv_extend over a 4-bit pool.
+ *
+ * The query rows of request b are qo_indptr[b] .. qo_indptr[b+1]-1, each over the keys
+ * below its bound (kv_end, or causal over the last positions); a row with bound 0 gives
+ * out = 0, lse = -inf.  The new tokens must be in the pool already (pkv_quant_store).
+ * Checks and flags are pkv_extend's; more than total_kv keys raise PKV_DEVERR_CAPACITY.
+ * workspace as for pkv_quant_decode, of pkv_quant_extend_workspace_size(args) bytes.
+ */
+pkv_status pkv_quant_extend(const pkv_quant_args *args, void *workspace, size_t workspace_bytes,
+                            int32_t *err_flags, pkv_stream_t stream);
+size_t pkv_quant_extend_workspace_size(const pkv_quant_args *args);
+
 /* Static description of a status code. */
 const char *pkv_status_string(pkv_status status);
 

@@ -25,7 +25,9 @@ EXPORTED_SYMBOLS = ("pkv_build_indices", "pkv_store", "pkv_decode", "pkv_decode_
                     "pkv_decode_no_alloc", "pkv_ragged_gather", "pkv_alloc_extend", "pkv_write_req_to_token",
                     "pkv_encoder_merge", "pkv_extend", "pkv_extend_workspace_size", "pkv_span_plan",
                     "pkv_status_string", "pkv_last_error", "pkv_abi_version", "pkv_set_wait_limit",
-                    "pkv_wait_limit")
+                    "pkv_wait_limit", "pkv_quant_tile_bytes", "pkv_quant_store", "pkv_quant_gather",
+                    "pkv_quant_decode", "pkv_quant_decode_workspace_size", "pkv_quant_extend",
+                    "pkv_quant_extend_workspace_size")
 
 
 class PkvError(RuntimeError):
@@ -78,6 +80,25 @@ class ExtendArgs(ctypes.Structure):
     ]
 
 
+class QuantArgs(ctypes.Structure):
+    """Mirror of ``pkv_quant_args`` (field order and types must match include/pkv.h)."""
+    _fields_ = [
+        ("layout", ctypes.c_int32), ("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("sm_scale", ctypes.c_float), ("max_seq_len", ctypes.c_int32), ("kv_chunk", ctypes.c_int32),
+        ("block_table_width", ctypes.c_int32), ("total_q", ctypes.c_int64), ("total_kv", ctypes.c_int64),
+        ("num_tiles", ctypes.c_int64), ("tile_stride", ctypes.c_int64), ("q_row_stride", ctypes.c_int64),
+        ("kv_indices_len", ctypes.c_int64),
+        ("q", ctypes.c_void_p), ("pool", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
+        ("qo_indptr", ctypes.c_void_p), ("kv_end", ctypes.c_void_p),
+        ("kv_indptr", ctypes.c_void_p), ("kv_indices", ctypes.c_void_p), ("kv_last_page_len", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+        ("req_to_token", ctypes.c_void_p), ("r2t_rows", ctypes.c_int64), ("r2t_row_stride", ctypes.c_int64),
+        ("r2t_width", ctypes.c_int64), ("req_pool_idx", ctypes.c_void_p), ("kv_start", ctypes.c_void_p),
+        ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p),
+    ]
+
+
 def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError("libpkv.so is not built (%s); run `python -m paged_kv_cache_req_gb300.build`" % path)
@@ -99,6 +120,18 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
     lib.pkv_extend_workspace_size.argtypes = [ctypes.POINTER(ExtendArgs)]
     lib.pkv_extend_workspace_size.restype = SZ
     lib.pkv_span_plan.argtypes = [I32, P, P, P, P, P, P, P, I64, P, P]
+    lib.pkv_quant_tile_bytes.argtypes = [I32, I32]
+    lib.pkv_quant_store.argtypes = [P, I64, I64, I32, I32, I32, P, P, P, P, I64, I64, P, I32, P, P]
+    lib.pkv_quant_gather.argtypes = [P, I64, I64, I32, I32, I32, P, P, P, I64, I64, I64, P, P, P, I32, I32, P, P, I64,
+                                     P, P, P]
+    for fn in (lib.pkv_quant_decode, lib.pkv_quant_extend):
+        fn.argtypes = [ctypes.POINTER(QuantArgs), P, SZ, P, P]
+    for fn in (lib.pkv_quant_decode_workspace_size, lib.pkv_quant_extend_workspace_size):
+        fn.argtypes = [ctypes.POINTER(QuantArgs)]
+    for fn in (lib.pkv_quant_tile_bytes, lib.pkv_quant_decode_workspace_size, lib.pkv_quant_extend_workspace_size):
+        fn.restype = SZ
+    for fn in (lib.pkv_quant_store, lib.pkv_quant_gather, lib.pkv_quant_decode, lib.pkv_quant_extend):
+        fn.restype = ctypes.c_int
     for fn in (lib.pkv_alloc_extend, lib.pkv_write_req_to_token, lib.pkv_encoder_merge, lib.pkv_extend,
                lib.pkv_span_plan):
         fn.restype = ctypes.c_int
@@ -329,6 +362,146 @@ def pkv_span_plan(seg_indptr, seg_kind, seg_start, seg_end, qo_indptr, q_pos, kv
                             _p(_i32(qo_indptr, "qo_indptr")), _p(_i32(q_pos, "q_pos")), _p(_i32(kv_end, "kv_end")),
                             q_pos.numel(), _p(err_flags), _stream(stream))
     _check(st, "pkv_span_plan")
+
+
+def _typed(t: Optional[torch.Tensor], name: str, dtype, shape=None, device=None):
+    """t, checked: its type, row-major order, shape where given, and (with `device`) its device."""
+    if t is not None:
+        if t.dtype != dtype or not t.is_contiguous() or (shape is not None and tuple(t.shape) != tuple(shape)):
+            raise ValueError("%s must be a contiguous %s tensor%s" % (
+                name, str(dtype).replace("torch.", ""), "" if shape is None else " of shape %s" % (tuple(shape),)))
+        if device is not None and t.device != device:
+            raise ValueError("%s is on %s, the pool on %s" % (name, t.device, device))
+    return t
+
+
+def _quant_pool(pool, page_size, head_dim):
+    """Checks a 4-bit pool [tiles, kv heads, tile bytes] against the page size and head_dim."""
+    nbytes = int(_lib.pkv_quant_tile_bytes(int(page_size), int(head_dim)))
+    if nbytes == 0:
+        raise PkvError(PKV_ERR_UNSUPPORTED, "4-bit pool", "page_size a power of two in [1, 1024], head_dim 64 or 128")
+    if pool.dim() != 3 or pool.dtype != torch.uint8 or pool.shape[2] != nbytes or pool.stride(2) != 1 or \
+            (pool.shape[1] > 1 and pool.stride(1) != nbytes):
+        raise ValueError("the 4-bit pool must be uint8 [tiles, kv heads, %d] with contiguous tiles" % nbytes)
+    if pool.is_cuda and pool.device.index != torch.cuda.current_device():
+        raise ValueError("the pool is on %s, which is not the current device" % pool.device)
+    # a pool of one tile may carry any stride
+    return pool.stride(0) if pool.shape[0] > 1 else pool.shape[1] * nbytes
+
+
+def pkv_quant_tile_bytes(page_size: int, head_dim: int) -> int:
+    """Bytes of one kv head's piece of a tile of min(page_size, 64) slots."""
+    return int(_lib.pkv_quant_tile_bytes(int(page_size), int(head_dim)))
+
+
+def pkv_quant_store(pool, k_new, v_new, slot_mapping, err_flags, *, page_size, k_scale=None, v_scale=None, stream=None):
+    """pool uint8 [tiles, Hkv, tile bytes]; k_new, v_new bf16 [n, Hkv, D], tokens any stride apart; scales fp32 [Hkv]."""
+    n, hkv, d = k_new.shape
+    ts = _quant_pool(pool, page_size, d)
+    dev = pool.device
+    for name, t in (("k_new", k_new), ("v_new", v_new)):
+        if t.dtype != torch.bfloat16 or tuple(t.shape) != (n, pool.shape[1], d) or t.stride(2) != 1 or \
+                (hkv > 1 and t.stride(1) != d) or t.device != dev:
+            raise ValueError("%s must be bf16 [n, %d, %d] on the pool's device, its rows contiguous" % (name, pool.shape[1], d))
+    _typed(slot_mapping, "slot_mapping", torch.int32, (n,), dev)
+    _typed(k_scale, "k_scale", torch.float32, (hkv,), dev)
+    _typed(v_scale, "v_scale", torch.float32, (hkv,), dev)
+    row = hkv * d
+    st = _lib.pkv_quant_store(_p(pool), pool.shape[0], ts, hkv, d, int(page_size), _p(k_scale), _p(v_scale), _p(k_new),
+                              _p(v_new), k_new.stride(0) if n > 1 else row, v_new.stride(0) if n > 1 else row,
+                              _p(slot_mapping), n, _p(err_flags), _stream(stream))
+    _check(st, "pkv_quant_store")
+
+
+def pkv_quant_gather(pool, req_to_token, req_pool_idx, seq_lens, max_seq_len, k_out, v_out, cu_seqlens, err_flags, *,
+                     page_size, k_scale=None, v_scale=None, kv_start=None, stream=None):
+    """k_out, v_out bf16 [rows, Hkv, D] receive the requests' rows in order (see pkv_ragged_gather)."""
+    rows, hkv, d = k_out.shape
+    ts = _quant_pool(pool, page_size, d)
+    dev, B = pool.device, seq_lens.numel()
+    _typed(k_out, "k_out", torch.bfloat16, (rows, pool.shape[1], d), dev)
+    _typed(v_out, "v_out", torch.bfloat16, (rows, pool.shape[1], d), dev)
+    _typed(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
+    for name, t in (("seq_lens", seq_lens), ("req_pool_idx", req_pool_idx), ("kv_start", kv_start)):
+        _typed(t, name, torch.int32, (B,), dev)
+    _typed(req_to_token, "req_to_token", torch.int32, None, dev)
+    _typed(k_scale, "k_scale", torch.float32, (hkv,), dev)
+    _typed(v_scale, "v_scale", torch.float32, (hkv,), dev)
+    st = _lib.pkv_quant_gather(_p(pool), pool.shape[0], ts, hkv, d, int(page_size), _p(k_scale), _p(v_scale),
+                               _p(req_to_token), req_to_token.shape[0], req_to_token.stride(0), req_to_token.shape[1],
+                               _p(req_pool_idx), _p(kv_start), _p(seq_lens), B, int(max_seq_len), _p(k_out), _p(v_out),
+                               rows, _p(cu_seqlens), _p(err_flags), _stream(stream))
+    _check(st, "pkv_quant_gather")
+
+
+def make_quant_args(layout, q, pool, out, *, page_size, sm_scale, max_seq_len, k_scale=None, v_scale=None, lse=None,
+                    qo_indptr=None, kv_end=None, kv_indptr=None, kv_indices=None, kv_last_page_len=None,
+                    block_table=None, seq_lens=None, req_to_token=None, req_pool_idx=None, kv_start=None, total_kv=0,
+                    kv_chunk=0) -> QuantArgs:
+    """Arguments of pkv_quant_decode (no qo_indptr) or pkv_quant_extend: q bf16 [rows, Hq, D], rows any
+    stride apart; pool uint8 [tiles, Hkv, tile bytes]; out bf16 [rows, Hq, D]."""
+    T, hq, d = q.shape
+    ts = _quant_pool(pool, page_size, d)
+    dev, hkv = pool.device, pool.shape[1]
+    if q.dtype != torch.bfloat16 or q.stride(2) != 1 or (hq > 1 and q.stride(1) != d) or q.device != dev:
+        raise ValueError("q must be bf16 [rows, Hq, D] on the pool's device, its rows contiguous")
+    B = T if qo_indptr is None else qo_indptr.numel() - 1
+    _typed(out, "out", torch.bfloat16, (T, hq, d), dev)
+    _typed(lse, "lse", torch.float32, (T, hq), dev)
+    _typed(k_scale, "k_scale", torch.float32, (hkv,), dev)
+    _typed(v_scale, "v_scale", torch.float32, (hkv,), dev)
+    for name, t, n in (("qo_indptr", qo_indptr, B + 1), ("kv_end", kv_end, T), ("kv_indptr", kv_indptr, B + 1),
+                       ("kv_last_page_len", kv_last_page_len, B), ("seq_lens", seq_lens, B),
+                       ("req_pool_idx", req_pool_idx, B), ("kv_start", kv_start, B)):
+        _typed(t, name, torch.int32, (n,), dev)
+    _typed(kv_indices, "kv_indices", torch.int32, None, dev)
+    _typed(req_to_token, "req_to_token", torch.int32, None, dev)
+    if block_table is not None:
+        _typed(block_table, "block_table", torch.int32, (B, block_table.shape[1]), dev)
+    a = QuantArgs()
+    a.layout, a.batch = layout, B
+    a.num_q_heads, a.num_kv_heads, a.head_dim = hq, hkv, d
+    a.page_size, a.sm_scale, a.max_seq_len, a.kv_chunk = int(page_size), float(sm_scale), int(max_seq_len), int(kv_chunk)
+    a.block_table_width = block_table.shape[1] if block_table is not None else 0
+    a.total_q, a.total_kv = T, int(total_kv)
+    a.num_tiles, a.tile_stride = pool.shape[0], ts
+    a.q_row_stride = q.stride(0) if T > 1 else hq * d
+    a.kv_indices_len = kv_indices.numel() if kv_indices is not None else 0
+    if req_to_token is not None:
+        a.r2t_rows, a.r2t_width = req_to_token.shape
+        a.r2t_row_stride = req_to_token.stride(0)
+    tensors = (("q", q), ("pool", pool), ("k_scale", k_scale), ("v_scale", v_scale), ("qo_indptr", qo_indptr),
+               ("kv_end", kv_end), ("kv_indptr", kv_indptr), ("kv_indices", kv_indices),
+               ("kv_last_page_len", kv_last_page_len), ("block_table", block_table), ("seq_lens", seq_lens),
+               ("req_to_token", req_to_token), ("req_pool_idx", req_pool_idx), ("kv_start", kv_start), ("out", out),
+               ("lse", lse))
+    for name, t in tensors:
+        setattr(a, name, None if t is None else _p(t).value)
+    # the struct holds raw pointers: keep the tensors alive as long as it lives
+    a._keep = tuple(t for _, t in tensors if t is not None)
+    return a
+
+
+def pkv_quant_decode_workspace_size(args: QuantArgs) -> int:
+    return int(_lib.pkv_quant_decode_workspace_size(ctypes.byref(args)))
+
+
+def pkv_quant_extend_workspace_size(args: QuantArgs) -> int:
+    return int(_lib.pkv_quant_extend_workspace_size(ctypes.byref(args)))
+
+
+def _quant_attend(fn, who, args, workspace, err_flags, stream):
+    ws_ptr = _p(workspace) if workspace is not None else None
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(fn(ctypes.byref(args), ws_ptr, ws_bytes, _p(err_flags), _stream(stream)), who)
+
+
+def pkv_quant_decode(args: QuantArgs, workspace: torch.Tensor, err_flags, stream=None):
+    _quant_attend(_lib.pkv_quant_decode, "pkv_quant_decode", args, workspace, err_flags, stream)
+
+
+def pkv_quant_extend(args: QuantArgs, workspace: torch.Tensor, err_flags, stream=None):
+    _quant_attend(_lib.pkv_quant_extend, "pkv_quant_extend", args, workspace, err_flags, stream)
 
 
 def pkv_status_string(status: int) -> str:
