@@ -443,12 +443,15 @@ def test_attention_flags(B):
     rng = np.random.default_rng(31)
     cache = Cache(rng, [100, 70, 50], 16, 2, 128)
     q = to_bf16(values(rng, (3, 4, 128)))
-    good, glse, e = decode(B, cache, q, "csr")
-    assert e == 0
 
     def one(layout="csr", **kw):
+        """The output and flags; the requests that nothing is wrong with hold the right values."""
         out, lse, e = decode(B, cache, q, layout, **kw)
+        if "k_scale" not in kw and "v_scale" not in kw and "kv_indptr" not in kw and "kv_last_page_len" not in kw:
+            check(cache, q, out, lse, only=[1, 2])
         return out, e
+
+    assert one()[1] == 0
 
     _, f = cache.layout(B, "csr")
     idx = f["kv_indices"].cpu().numpy()
@@ -456,7 +459,7 @@ def test_attention_flags(B):
         bad = idx.copy()
         bad[2] = page
         out, e = one(kv_indices=up(bad))
-        assert e == 1 and torch.equal(out[1:], good[1:])
+        assert e == 1
         assert torch.isfinite(out[0].float()).all()
     for bad in ([0, 999, 11, 15], [-3, 7, 12, 16], [0, 12, 7, 16]):
         out, e = one(kv_indptr=up(np.array(bad, dtype=np.int32)))
@@ -465,19 +468,18 @@ def test_attention_flags(B):
         out, e = one(kv_last_page_len=up(np.array(bad, dtype=np.int32)))
         assert e & 1
     out, e = one(max_seq_len=80)
-    assert e == 4 and torch.equal(out[1:], good[1:])
+    assert e == 4
     # token table: rows and regions outside it, a page start off its page
     for kw in (dict(req_pool_idx=up(np.array([99, cache.rpi[1], cache.rpi[2]], dtype=np.int32))),
                dict(kv_start=up(np.array([8, 0, 0], dtype=np.int32))), dict(kv_start=up(np.array([-16, 0, 0], dtype=np.int32))),
                dict(seq_lens=up(np.array([-5, 70, 50], dtype=np.int32))),
                dict(kv_start=up(np.array([16 * 1000, 0, 0], dtype=np.int32)))):
         out, e = one("table", **kw)
-        assert e == 1 and torch.equal(out[1:], good[1:])
-        assert (out[0] == 0).all()
+        assert e == 1 and (out[0] == 0).all()
     bad = cache.r2t.copy()
     bad[cache.rpi[0], 32] += 1
     out, e = one("table", req_to_token=up(bad))
-    assert e == 2 and torch.equal(out[1:], good[1:])
+    assert e == 2
     bad[cache.rpi[0], 32] = -4
     assert one("table", req_to_token=up(bad))[1] == 1
     assert one(k_scale=up(np.array([1.0, -1.0], dtype=np.float32)))[1] == 1
@@ -490,22 +492,24 @@ def test_extend_flags(B, rows):
     lens = [400, 300]
     cache = Cache(rng, lens, 16, 2, 128)
     q = to_bf16(values(rng, (sum(rows), 8, 128)))
-    good, _, e = extend(B, cache, q, rows)
+    out, lse, e = extend(B, cache, q, rows)
     assert e == 0
+    check(cache, q, out, lse, rows)
     ends = np.concatenate([np.arange(l - n + 1, l + 1) for l, n in zip(lens, rows)])
-    same, _, e = extend(B, cache, q, rows, kv_end=ends)
-    assert e == 0
     bad = ends.copy()
     bad[1], bad[rows[0] - 1] = -1, 401
     out, lse, e = extend(B, cache, q, rows, kv_end=bad)
-    assert e == 1 and (out[1] == 0).all() and (out[rows[0] - 1] == 0).all() and torch.equal(out[rows[0]:], same[rows[0]:])
+    assert e == 1 and (out[1] == 0).all() and (out[rows[0] - 1] == 0).all()
+    check(cache, q, out, lse, rows, only=[1])
     # more causal rows than keys: the request has no rows
     cache.lens[0] = rows[0] - 1
     out, lse, e = extend(B, cache, q, rows)
-    assert e == 1 and (out[:rows[0]] == 3).all() and torch.equal(out[rows[0]:], good[rows[0]:])
+    assert e == 1 and (out[:rows[0]] == 3).all()
+    check(cache, q, out, lse, rows, only=[1])
     cache.lens[0] = 400
     out, lse, e = extend(B, cache, q, rows, max_seq_len=350)
-    assert e == 4 and torch.equal(out[rows[0]:], good[rows[0]:])
+    assert e == 4
+    check(cache, q, out, lse, rows, only=[1])
 
 
 # --------------------------------------------------------------------------- together
