@@ -550,6 +550,7 @@ typedef struct pkv_quant_args {
     int32_t max_seq_len;       /* host upper bound on every request's key count */
     int32_t kv_chunk;          /* keys per split, a multiple of 64; 0 lets the library choose */
     int32_t block_table_width;
+    int32_t max_q_len;         /* pkv_quant_extend: host upper bound on a request's query rows; 0: unknown */
     int64_t total_q;           /* query rows: B for pkv_quant_decode, qo_indptr[B] for pkv_quant_extend */
     int64_t total_kv;          /* pkv_quant_extend: host upper bound on the sum of the key counts (sizes the
                                   workspace); 0: batch * max_seq_len */
@@ -601,6 +602,11 @@ size_t pkv_quant_decode_workspace_size(const pkv_quant_args *args);
  * below its bound (kv_end, or causal over the last positions); a row with bound 0 gives
  * out = 0, lse = -inf.  The new tokens must be in the pool already (pkv_quant_store).
  * Checks and flags are pkv_extend's; more than total_kv keys raise PKV_DEVERR_CAPACITY.
+ * Requests with more than 64 (row, query head) pairs per kv head have their keys and
+ * values copied out of the pool into the workspace as 16-bit floats first (exactly), which
+ * total_kv sizes; a step of which max_q_len, or without it the average, says that there is
+ * no such request needs no room for that, and computes a larger request all the same.  A
+ * row that sees a key whose V holds a NaN block may be NaN in all its dims there.
  * workspace as for pkv_quant_decode, of pkv_quant_extend_workspace_size(args) bytes.
  */
 pkv_status pkv_quant_extend(const pkv_quant_args *args, void *workspace, size_t workspace_bytes,

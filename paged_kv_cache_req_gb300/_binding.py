@@ -86,7 +86,8 @@ class QuantArgs(ctypes.Structure):
         ("layout", ctypes.c_int32), ("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
         ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
         ("sm_scale", ctypes.c_float), ("max_seq_len", ctypes.c_int32), ("kv_chunk", ctypes.c_int32),
-        ("block_table_width", ctypes.c_int32), ("total_q", ctypes.c_int64), ("total_kv", ctypes.c_int64),
+        ("block_table_width", ctypes.c_int32), ("max_q_len", ctypes.c_int32), ("total_q", ctypes.c_int64),
+        ("total_kv", ctypes.c_int64),
         ("num_tiles", ctypes.c_int64), ("tile_stride", ctypes.c_int64), ("q_row_stride", ctypes.c_int64),
         ("kv_indices_len", ctypes.c_int64),
         ("q", ctypes.c_void_p), ("pool", ctypes.c_void_p), ("k_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p),
@@ -437,7 +438,7 @@ def pkv_quant_gather(pool, req_to_token, req_pool_idx, seq_lens, max_seq_len, k_
 def make_quant_args(layout, q, pool, out, *, page_size, sm_scale, max_seq_len, k_scale=None, v_scale=None, lse=None,
                     qo_indptr=None, kv_end=None, kv_indptr=None, kv_indices=None, kv_last_page_len=None,
                     block_table=None, seq_lens=None, req_to_token=None, req_pool_idx=None, kv_start=None, total_kv=0,
-                    kv_chunk=0) -> QuantArgs:
+                    max_q_len=0, kv_chunk=0) -> QuantArgs:
     """Arguments of pkv_quant_decode (no qo_indptr) or pkv_quant_extend: q bf16 [rows, Hq, D], rows any
     stride apart; pool uint8 [tiles, Hkv, tile bytes]; out bf16 [rows, Hq, D]."""
     T, hq, d = q.shape
@@ -463,7 +464,7 @@ def make_quant_args(layout, q, pool, out, *, page_size, sm_scale, max_seq_len, k
     a.num_q_heads, a.num_kv_heads, a.head_dim = hq, hkv, d
     a.page_size, a.sm_scale, a.max_seq_len, a.kv_chunk = int(page_size), float(sm_scale), int(max_seq_len), int(kv_chunk)
     a.block_table_width = block_table.shape[1] if block_table is not None else 0
-    a.total_q, a.total_kv = T, int(total_kv)
+    a.total_q, a.total_kv, a.max_q_len = T, int(total_kv), int(max_q_len)
     a.num_tiles, a.tile_stride = pool.shape[0], ts
     a.q_row_stride = q.stride(0) if T > 1 else hq * d
     a.kv_indices_len = kv_indices.numel() if kv_indices is not None else 0

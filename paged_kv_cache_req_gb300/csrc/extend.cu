@@ -34,9 +34,15 @@
 // item to the next costs no global loads.  Items whose block is cut into
 // several key chunks write fp32 (o, lse) partials that ext_merge_kernel
 // combines.  Every wait is bounded (~2 s).
+//
+// kHeld: the same kernel for pkv_quant_extend, over keys and values that quant_attn.cu has
+// taken out of the 4-bit pool: K bf16 and V fp16 (both exact) in workspace tensors
+// [D/64][kv heads][rows][64], so that a box is 128 consecutive rows, 16 KB in one piece.  The
+// heads' fp32 scales go into the score scale and the epilogue, P is rounded to fp16 instead
+// of bf16 (three more bits), and a NaN key makes the rows that see it NaN.
 #include <algorithm>
 
-#include "pkv_internal.cuh"
+#include "extend_held.cuh"
 #include "tc05.cuh"
 
 namespace pkv {
@@ -52,6 +58,7 @@ constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLazy = 8.f;
 constexpr int kRing = 8;                   // slots of the item queue
 constexpr int kItemReaders = 16;           // warps that read every queued item
+constexpr int kLayoutHeld = 4;             // Params::layout: key t of request b is row kv_indptr[b] + t of the held tensors
 
 template <int D>
 struct Cfg {
@@ -100,6 +107,11 @@ struct Params {
     // PKV_LAYOUT_REQ_TO_TOKEN: the token table itself
     const int32_t *r2t, *req_pool_idx, *kv_start;
     int64_t r2t_rows, r2t_stride, r2t_width;
+    // kLayoutHeld
+    const float *k_scale, *v_scale;    // fp32 [Hkv] or null
+    int64_t held_rows;                 // rows per head and 64-dim slab of the held tensors
+    int32_t heads;                     // query heads per kv head (g is the next power of two)
+    int32_t min_rows;                  // requests with at most this many rows per kv head are left out
 };
 
 // Keys of request b (0 and a flag for malformed inputs).
@@ -127,6 +139,9 @@ __device__ __forceinline__ int key_count(const Params &p, int b, int64_t &base, 
         }
         base = row * p.r2t_stride + st;
         cap = L;
+    } else if (p.layout == kLayoutHeld) {
+        base = p.kv_indptr[b];
+        L = cap = p.kv_indptr[b + 1] - base;
     } else {
         base = static_cast<int64_t>(b) * p.bt_width;
         L = p.seq_lens[b];
@@ -185,6 +200,7 @@ __device__ __forceinline__ Req load_req(const Params &p, int b, bool report) {
     Req r;
     r.L = key_count(p, b, r.base, report);
     r.n = q_count(p, b, report);
+    if (p.layout == kLayoutHeld && r.n * p.heads <= p.min_rows) r.n = 0;
     if (!p.kv_end && r.n > r.L) {
         if (report) raise_flag(p.err, PKV_DEVERR_RANGE);
         r.n = 0;
@@ -419,7 +435,7 @@ __device__ __forceinline__ Item ring_read(const Item *ring, uint64_t *bars, uint
 
 // Sixteen warps: four of them on one SM sub-partition share its 16K registers, so
 // at most 128 registers a thread.
-template <int D>
+template <int D, bool kHeld>
 __global__ void __maxnreg__(128)
 ext_kernel(const Params p, const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
            const __grid_constant__ CUtensorMap tmv) {
@@ -581,6 +597,7 @@ ext_kernel(const Params p, const __grid_constant__ CUtensorMap tmq, const __grid
                 // pool row of key k of the item: -2 for a page outside the pool, -3 for a
                 // token-table page start that is not a multiple of the page size
                 auto pool_row = [&](int k) -> int {
+                    if (kHeld) return static_cast<int>(it.base) + k;
                     if (p.layout == PKV_LAYOUT_REQ_TO_TOKEN) {   // the slot of the page's first key, + the offset
                         const int first = __ldg(p.r2t + it.base + (k & ~p.ps_mask));
                         if (first < 0 || first >= (p.num_pages << p.ps_shift)) return -2;
@@ -672,7 +689,13 @@ ext_kernel(const Params p, const __grid_constant__ CUtensorMap tmq, const __grid
                         __syncwarp();
                         if (lane == 0) mbar_arrive_expect_tx(&fulls[s], __popc(valid) * static_cast<uint32_t>(box) * 128u);
                         __syncwarp();
-                        if (row >= 0) tma_load_2d(dst, is_v ? &tmv : &tmk, it.kh * D + sl_op * 64, row, &fulls[s]);
+                        if (row >= 0) {
+                            if (kHeld)
+                                tma_load_2d(dst, is_v ? &tmv : &tmk, 0,
+                                            static_cast<int>((sl_op * p.hkv + it.kh) * p.held_rows) + row, &fulls[s]);
+                            else
+                                tma_load_2d(dst, is_v ? &tmv : &tmk, it.kh * D + sl_op * 64, row, &fulls[s]);
+                        }
                         ++issued;
                     }
                 }
@@ -704,7 +727,7 @@ ext_kernel(const Params p, const __grid_constant__ CUtensorMap tmq, const __grid
                 mbar_arrive_expect_tx(&bars[kQFull0 + sl], C::kQBytes);
                 const int tok = qi.qo0 + qi.qblk * p.T;
                 for (int k = 0; k < C::kSl; ++k)
-                    tma_load_3d(sQ + sl * C::kQBytes + k * kRows * 128, &tmq, k * 64, qi.kh * p.g, tok,
+                    tma_load_3d(sQ + sl * C::kQBytes + k * kRows * 128, &tmq, k * 64, qi.kh * (kHeld ? p.heads : p.g), tok,
                                 &bars[kQFull0 + sl]);
             }
             __syncwarp();
@@ -765,7 +788,7 @@ ext_kernel(const Params p, const __grid_constant__ CUtensorMap tmq, const __grid
         // Group g's half of tile n (keys 64 g ... 64 g + 63) into its accumulator.  An
         // item's first tile starts both accumulators afresh, once the epilogue has read
         // the previous item's.
-        const uint32_t idesc = tc05::idesc_bf16_f32(kRows, D, false, true);
+        const uint32_t idesc = kHeld ? tc05::idesc_f16_f32(kRows, D, false, true) : tc05::idesc_bf16_f32(kRows, D, false, true);
         uint32_t n = 0, io = 0;
         bool ok = true;
         for (uint32_t k = 0; ok; ++k) {
@@ -842,14 +865,24 @@ ext_kernel(const Params p, const __grid_constant__ CUtensorMap tmq, const __grid
             ok = warp_wait(ok, &bars[kODone0 + ko], (io >> 1) & 1, abort_flag, p.err, p.wait_ns);
             tc05::fence_after_sync();
             const float M = fmaxf(sa.x, sb2.x);
-            const float wa = sa.y > 0.f ? ex2(sa.x - M) : 0.f, wb = sb2.y > 0.f ? ex2(sb2.x - M) : 0.f;
+            float wa, wb, inv;
+            if (kHeld) {   // a sum that is NaN stays
+                wa = sa.y != 0.f ? ex2(sa.x - M) : 0.f;
+                wb = sb2.y != 0.f ? ex2(sb2.x - M) : 0.f;
+            } else {
+                wa = sa.y > 0.f ? ex2(sa.x - M) : 0.f;
+                wb = sb2.y > 0.f ? ex2(sb2.x - M) : 0.f;
+            }
             const float den = sa.y * wa + sb2.y * wb;
-            const float inv = den > 0.f ? 1.f / den : 0.f;
+            if (kHeld)
+                inv = den == 0.f ? 0.f : (p.v_scale ? __ldg(p.v_scale + it.kh) : 1.f) / den;
+            else
+                inv = den > 0.f ? 1.f / den : 0.f;
             const float ca = wa * inv, cb2 = wb * inv;
             const int tq = it.qblk * p.T + tok;
-            const bool valid = tq < it.n;
+            const bool valid = tq < it.n && (!kHeld || hh < p.heads);
             const int64_t qrow = static_cast<int64_t>(it.qo0) + tq;
-            const int head = it.kh * p.g + hh;
+            const int head = it.kh * (kHeld ? p.heads : p.g) + hh;
             const bool single = it.nch == 1;
             const int64_t prow = it.w * kRows + r;
 #pragma unroll 1
@@ -892,7 +925,7 @@ ext_kernel(const Params p, const __grid_constant__ CUtensorMap tmq, const __grid
                 }
             }
             if (valid) {
-                const float lse2 = den > 0.f ? M + log2f(den) : -INFINITY;
+                const float lse2 = (kHeld ? den != 0.f : den > 0.f) ? M + log2f(den) : -INFINITY;
                 if (single) {
                     if (p.lse) p.lse[qrow * p.hq + head] = lse2 * kLn2;
                 } else {
@@ -932,9 +965,10 @@ ext_kernel(const Params p, const __grid_constant__ CUtensorMap tmq, const __grid
             const Item nx = ring_read(ring, bars, kr++, ok, abort_flag, p.err, p.wait_ns);   // may be the end
             const int kend_nx = nx.w >= 0 ? row_bound(nx) : 0;
             const int tq = it.qblk * p.T + tok;                  // token within the request
-            const bool valid = tq < it.n;
+            const bool valid = tq < it.n && (!kHeld || hh < p.heads);
             const int64_t qrow = static_cast<int64_t>(it.qo0) + tq;
-            const int head = it.kh * p.g + hh;
+            const int head = it.kh * (kHeld ? p.heads : p.g) + hh;
+            const float scale = kHeld && p.k_scale ? p.scale_log2 * __ldg(p.k_scale + it.kh) : p.scale_log2;
             float m = -INFINITY, l = 0.f;
             if (it.n_tiles == 0) {   // no keys: out = 0, lse = -inf
                 if (grp == 0 && valid && it.nch == 1) {
@@ -980,7 +1014,7 @@ ext_kernel(const Params p, const __grid_constant__ CUtensorMap tmq, const __grid
                     for (int j = 0; j < 7; ++j) u[j] = fmax3(t[3 * j], t[3 * j + 1], t[3 * j + 2]);
                     u[7] = t[21];
                     mx = fmax3(fmax3(u[0], u[1], u[2]), fmax3(u[3], u[4], u[5]), fmaxf(u[6], u[7])) *
-                         p.scale_log2;   // scores are unscaled up to here (the scale is positive)
+                         scale;   // scores are unscaled up to here (the scale is positive)
                 }
                 const bool raise = mx > m + kLazy || (m == -INFINITY && mx != -INFINITY);
                 const float corr = raise ? ex2(m - mx) : 1.f;
@@ -1010,7 +1044,7 @@ ext_kernel(const Params p, const __grid_constant__ CUtensorMap tmq, const __grid
                 const float nm = m == -INFINITY ? 0.f : -m;
                 // scaling and the row sum two keys per instruction (the softmax groups
                 // are bound by instruction issue)
-                const uint64_t sc2 = pair(p.scale_log2, p.scale_log2), nm2 = pair(nm, nm);
+                const uint64_t sc2 = pair(scale, scale), nm2 = pair(nm, nm);
                 uint64_t acc = pair(0.f, 0.f);
 #pragma unroll
                 for (int j = 0; j < 16; ++j) {   // p = 2^(scale log2(e) s - m)
@@ -1019,8 +1053,8 @@ ext_kernel(const Params p, const __grid_constant__ CUtensorMap tmq, const __grid
                     const float a0 = ex2(ya.x), a1 = ex2(ya.y), b0 = ex2(yb.x), b1 = ex2(yb.y);
                     acc = add2(acc, pair(a0, a1));
                     acc = add2(acc, pair(b0, b1));
-                    h0[j] = pack_bf16x2(a0, a1);
-                    h1[j] = pack_bf16x2(b0, b1);
+                    h0[j] = kHeld ? pack_f16x2(a0, a1) : pack_bf16x2(a0, a1);
+                    h1[j] = kHeld ? pack_f16x2(b0, b1) : pack_bf16x2(b0, b1);
                 }
                 const float2 ls = unpair(acc);
                 l += ls.x + ls.y;
@@ -1056,7 +1090,7 @@ ext_kernel(const Params p, const __grid_constant__ CUtensorMap tmq, const __grid
 // Log-sum-exp merge of the key chunks of one (request, kv head, query block):
 // one CTA per such group (found in the prefix tables the attention kernel left),
 // rows x head_dim.
-template <int D>
+template <int D, bool kHeld>
 __global__ void __launch_bounds__(256) ext_merge_kernel(const Params p, int64_t groups) {
     pdl_wait();          // inputs may come from the previous kernel of the stream
     pdl_launch_next();
@@ -1083,12 +1117,12 @@ __global__ void __launch_bounds__(256) ext_merge_kernel(const Params p, int64_t 
         const int r = i / (D / 4), d4 = i % (D / 4);
         const int tok = r >> p.g_shift, hh = r & (p.g - 1);
         const int tb = qblk * p.T + tok;
-        if (tb >= n) continue;
+        if (tb >= n || (kHeld && hh >= p.heads)) continue;
         float M = -INFINITY;
         for (int c = 0; c < nch; ++c) M = fmaxf(M, p.part_lse[(w0 + c) * kRows + r]);
         float den = 0.f;
         float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (M != -INFINITY) {
+        if (kHeld || M != -INFINITY) {
             for (int c = 0; c < nch; ++c) {
                 const float lc = p.part_lse[(w0 + c) * kRows + r];
                 if (lc == -INFINITY) continue;
@@ -1101,14 +1135,15 @@ __global__ void __launch_bounds__(256) ext_merge_kernel(const Params p, int64_t 
                 den += wgt;
             }
         }
-        const float inv = den > 0.f ? 1.f / den : 0.f;
+        const bool some = kHeld ? den != 0.f : den > 0.f;   // held: a NaN stays
+        const float inv = some ? 1.f / den : 0.f;
         const int64_t qrow = static_cast<int64_t>(rq.qo0) + tb;
-        const int head = kh * p.g + hh;
+        const int head = kh * (kHeld ? p.heads : p.g) + hh;
         uint2 o;
         o.x = pack_bf16x2(acc.x * inv, acc.y * inv);
         o.y = pack_bf16x2(acc.z * inv, acc.w * inv);
         reinterpret_cast<uint2 *>(p.out + (qrow * p.hq + head) * D)[d4] = o;
-        if (d4 == 0 && p.lse) p.lse[qrow * p.hq + head] = den > 0.f ? (M + log2f(den)) * kLn2 : -INFINITY;
+        if (d4 == 0 && p.lse) p.lse[qrow * p.hq + head] = some ? (M + log2f(den)) * kLn2 : -INFINITY;
     }
 }
 
@@ -1164,7 +1199,7 @@ struct Plan {
 };
 
 static bool make_plan(const pkv_extend_args *a, Plan &pl) {
-    pl.g = a->num_q_heads / a->num_kv_heads;
+    pl.g = 1 << ilog2(a->num_q_heads / a->num_kv_heads);   // a power of two but for held keys
     pl.T = kRows / pl.g;
     const int64_t blocks_max = a->total_q / pl.T + a->batch;      // query blocks, upper bound
     pl.groups_max = static_cast<int64_t>(a->num_kv_heads) * blocks_max;
@@ -1234,8 +1269,9 @@ static pkv_status validate(const pkv_extend_args *a, bool check_ptrs) {
     return PKV_OK;
 }
 
-template <int D>
-static pkv_status launch_t(const pkv_extend_args *a, const Plan &pl, void *ws, int32_t *err, cudaStream_t s) {
+template <int D, bool kHeld>
+static pkv_status launch_t(const pkv_extend_args *a, const Plan &pl, void *ws, int32_t *err, cudaStream_t s,
+                           const Held *held = nullptr) {
     using C = Cfg<D>;
     Params p{};
     p.layout = a->layout;
@@ -1283,14 +1319,36 @@ static pkv_status launch_t(const pkv_extend_args *a, const Plan &pl, void *ws, i
     p.r2t_stride = a->r2t_row_stride;
     p.r2t_width = a->r2t_width;
 
+    if (kHeld) {
+        p.layout = kLayoutHeld;
+        p.kv_indptr = held->first_row;
+        p.ps_shift = ilog2(kTile);
+        p.ps_mask = kTile - 1;
+        p.box_rows = kTile;
+        p.k_scale = held->k_scale;
+        p.v_scale = held->v_scale;
+        p.held_rows = held->rows;
+        p.heads = a->num_q_heads / a->num_kv_heads;
+        p.min_rows = held->min_rows;
+    }
     CUtensorMap tmq, tmk, tmv;
     {   // q [total_q, Hq, D]: boxes of 64 dims x g heads x T tokens = 128 rows of 128 bytes
         const uint64_t dq[3] = {static_cast<uint64_t>(D), static_cast<uint64_t>(a->num_q_heads),
                                 static_cast<uint64_t>(std::max<int64_t>(a->total_q, 1))};
-        const uint64_t sq[2] = {static_cast<uint64_t>(D) * 2, static_cast<uint64_t>(a->num_q_heads) * D * 2};
+        const uint64_t sq[2] = {static_cast<uint64_t>(D) * 2,
+                                static_cast<uint64_t>(kHeld ? held->q_row_stride : static_cast<int64_t>(a->num_q_heads) * D) * 2};
         const uint32_t bq[3] = {64, static_cast<uint32_t>(pl.g), static_cast<uint32_t>(pl.T)};
         if (!encode_tmap_bf16(&tmq, a->q, 3, dq, sq, bq))
             return fail(PKV_ERR_CUDA, "pkv_extend: cuTensorMapEncodeTiled rejected q");
+    }
+    if (kHeld) {   // 64 dims wide, slabs x heads x rows high: a box is 128 rows
+        const uint64_t dk[2] = {64, static_cast<uint64_t>(D / 64 * a->num_kv_heads * held->rows)};
+        const uint64_t sk[1] = {128};
+        const uint32_t bk[2] = {64, kTile};
+        // (the copies move 16-bit words: V's are fp16)
+        if (!encode_tmap_bf16(&tmk, held->k, 2, dk, sk, bk) || !encode_tmap_bf16(&tmv, held->v, 2, dk, sk, bk))
+            return fail(PKV_ERR_CUDA, "pkv_quant_extend: cuTensorMapEncodeTiled rejected the workspace");
+    } else {
         // pool rows as a 2-D tensor (kv heads x head_dim wide): a box is 64 dims of one
         // kv head over a page's rows
         const uint64_t dk[2] = {static_cast<uint64_t>(a->num_kv_heads) * D, static_cast<uint64_t>(a->num_slots)};
@@ -1300,17 +1358,17 @@ static pkv_status launch_t(const pkv_extend_args *a, const Plan &pl, void *ws, i
         if (!encode_tmap_bf16(&tmk, a->k_pool, 2, dk, sk, bk) || !encode_tmap_bf16(&tmv, a->v_pool, 2, dk, sv, bk))
             return fail(PKV_ERR_CUDA, "pkv_extend: cuTensorMapEncodeTiled rejected the pools");
     }
-    std::atomic<int64_t> *m_lim = device_memo(reinterpret_cast<const void *>(ext_kernel<D>));
+    std::atomic<int64_t> *m_lim = device_memo(reinterpret_cast<const void *>(ext_kernel<D, kHeld>));
     if (!m_lim) return fail(PKV_ERR_CUDA, "pkv_extend: cannot query the current device");
     if (m_lim->load() == 0) {   // kernel attributes are per device
         int optin = 0, dev = 0;
         cudaFuncAttributes fa{};
         if (cudaGetDevice(&dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
-            cudaFuncGetAttributes(&fa, ext_kernel<D>) != cudaSuccess)
+            cudaFuncGetAttributes(&fa, ext_kernel<D, kHeld>) != cudaSuccess)
             return fail(PKV_ERR_CUDA, "pkv_extend: cannot query shared-memory limits");
         const size_t l = static_cast<size_t>(optin) - fa.sharedSizeBytes;
-        if (cudaFuncSetAttribute(ext_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(l)) !=
+        if (cudaFuncSetAttribute(ext_kernel<D, kHeld>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(l)) !=
             cudaSuccess)
             return fail(PKV_ERR_CUDA, "pkv_extend: cannot raise the shared-memory limit");
         m_lim->store(static_cast<int64_t>(l));
@@ -1325,14 +1383,40 @@ static pkv_status launch_t(const pkv_extend_args *a, const Plan &pl, void *ws, i
     p.cache_requests = cached <= lim && bases_fit ? 1 : 0;
     if (p.cache_requests) smem = cached;
     const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(pl.items_max, sm_count()));
-    if (cudaMemsetAsync(p.counter, 0, sizeof(int32_t), s) != cudaSuccess)
-        return fail(PKV_ERR_CUDA, "pkv_extend: cannot reset the item counter");
-    ext_kernel<D><<<static_cast<unsigned>(grid), kThreads, smem, s>>>(p, tmq, tmk, tmv);
-    pkv_status st = check_launch("pkv_extend (attention kernel)");
+    pkv_status st;
+    if (kHeld) {   // the kernel before it zeroed the item counter
+        st = launch_status(launch_chained(ext_kernel<D, kHeld>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, s, p,
+                                          tmq, tmk, tmv),
+                           "pkv_quant_extend (attention kernel)");
+    } else {
+        if (cudaMemsetAsync(p.counter, 0, sizeof(int32_t), s) != cudaSuccess)
+            return fail(PKV_ERR_CUDA, "pkv_extend: cannot reset the item counter");
+        ext_kernel<D, kHeld><<<static_cast<unsigned>(grid), kThreads, smem, s>>>(p, tmq, tmk, tmv);
+        st = check_launch("pkv_extend (attention kernel)");
+    }
     if (st != PKV_OK || pl.nch_max <= 1) return st;
-    return launch_status(launch_chained(ext_merge_kernel<D>, dim3(static_cast<unsigned>(pl.groups_max)), dim3(256), 0, s,
+    return launch_status(launch_chained(ext_merge_kernel<D, kHeld>, dim3(static_cast<unsigned>(pl.groups_max)), dim3(256), 0, s,
                                         p, pl.groups_max),
                          "pkv_extend (merge kernel)");
+}
+
+// ------------------------------------------------------------------ held keys (pkv_quant_extend)
+size_t held_workspace(const pkv_extend_args *a) {
+    Plan pl;
+    if (!make_plan(a, pl)) return 0;
+    return pl.part_o_bytes + pl.part_lse_bytes + Plan::kCounterBytes + pl.table_bytes;
+}
+
+size_t held_counter_offset(const pkv_extend_args *a) {
+    Plan pl;
+    return make_plan(a, pl) ? pl.part_o_bytes + pl.part_lse_bytes : 0;
+}
+
+pkv_status held_launch(const pkv_extend_args *a, const Held &held, void *workspace, int32_t *err, cudaStream_t s) {
+    Plan pl;
+    if (!make_plan(a, pl)) return fail(PKV_ERR_UNSUPPORTED, "pkv_quant_extend: too many work items");
+    return a->head_dim == 128 ? launch_t<128, true>(a, pl, workspace, err, s, &held)
+                              : launch_t<64, true>(a, pl, workspace, err, s, &held);
 }
 
 }  // namespace ext
@@ -1363,8 +1447,8 @@ extern "C" pkv_status pkv_extend(const pkv_extend_args *args, void *workspace, s
     if (!workspace || !aligned(workspace, 256))
         return fail(PKV_ERR_INVALID_ARG, "pkv_extend: workspace must be non-null and 256-byte aligned");
     auto s = reinterpret_cast<cudaStream_t>(stream);
-    return args->head_dim == 128 ? launch_t<128>(args, pl, workspace, err_flags, s)
-                                 : launch_t<64>(args, pl, workspace, err_flags, s);
+    return args->head_dim == 128 ? launch_t<128, false>(args, pl, workspace, err_flags, s)
+                                 : launch_t<64, false>(args, pl, workspace, err_flags, s);
 }
 
 extern "C" pkv_status pkv_span_plan(int32_t batch, const int32_t *seg_indptr, const int32_t *seg_kind,

@@ -21,6 +21,7 @@
 #include <algorithm>
 #include <cmath>
 
+#include "extend_held.cuh"
 #include "quant.cuh"
 
 namespace pkv {
@@ -52,18 +53,16 @@ struct Params {
     float *part_o, *part_ml; // per span two slots: [rows][D], and [rows] of (m, l)
     int64_t *off;            // [B + 1] first tile of each request, then the tiles of a span
     int32_t off_ready;       // written by plan_kernel (large batches)
+    // per span: the unit that its first tile continues, {request (-1: none), row block * Hkv + kv
+    // head, 2 x spans back to its first + (1 if it began inside that span), spans on to its last}
+    int4 *cuts;
+    int32_t max_rows;        // > 0: requests with more rows per kv head are left to the held path
 };
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
-}
-// Two floats -> fp16 pair (to nearest even), lo in the low half.
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
 }
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     uint32_t r;
@@ -112,6 +111,7 @@ __device__ __forceinline__ Req load_req(const Params &p, int b, bool report) {
             if (report) raise_flag(p.err, PKV_DEVERR_RANGE);
             r.n = 0;
         }
+        if (p.max_rows && r.n * p.g > p.max_rows) r.n = 0;
     }
     return r;
 }
@@ -589,8 +589,6 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attend_kernel(const
     if (!p.off_ready) {
         int64_t *mine = reinterpret_cast<int64_t *>(smem + static_cast<uint32_t>(kWarps * p.stages) * stage_bytes);
         build_table<NT, kThreads>(p, mine, scratch, blockIdx.x == 0);
-        if (blockIdx.x == 0)   // for merge_kernel
-            for (int i = threadIdx.x; i < p.batch + 2; i += kThreads) p.off[i] = mine[i];
         off = mine;
     }
     if (blockIdx.x == 0 && warp < 2) {   // unusable head scales
@@ -603,9 +601,13 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attend_kernel(const
     bool ok = true;
     const uint32_t S = p.stages;
     State<D, NT> st;
-    for (int64_t sp = static_cast<int64_t>(blockIdx.x) * kWarps + warp; ok && sp * per < total;
+    for (int64_t sp = static_cast<int64_t>(blockIdx.x) * kWarps + warp; ok && sp < p.spans_max;
          sp += static_cast<int64_t>(gridDim.x) * kWarps) {
         const int64_t begin = sp * per, end = min(total, begin + per);
+        if (begin >= total) {
+            if (lane == 0) p.cuts[sp] = make_int4(-1, 0, 0, 0);
+            continue;
+        }
         Fetcher<NT> f;
         f.start(p, off, begin, end);
         Pieces ahead = look_up(p, f, lane);   // of the next tile to fetch
@@ -623,6 +625,12 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attend_kernel(const
         for (int64_t pos = begin; ok && pos < end;) {
             const Segment s = segment_at<NT>(p, off, pos, end);
             const int keys = unit_keys<NT>(p, s);
+            if (pos == begin && lane == 0) {
+                const int64_t u0 = pos - s.t0, u1 = u0 + s.tiles - 1;
+                p.cuts[sp] = s.t0 ? make_int4(s.b, s.rb * p.hkv + s.kh, static_cast<int>(sp - u0 / per) * 2 + (u0 % per ? 1 : 0),
+                                              static_cast<int>(u1 / per - sp))
+                                  : make_int4(-1, 0, 0, 0);
+            }
             start_segment<D, NT>(p, s, st, lane);
             int low = s.L;   // every row sees the keys below it
 #pragma unroll
@@ -655,84 +663,195 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attend_kernel(const
     }
 }
 
-// Combines the partials of one row of a unit that spans cut: o = sum 2^(m_i - M) o_i / sum
-// 2^(m_i - M) l_i, a warp per share of the partials.
+// Combines the partials of the units that span boundaries cut: o = sum 2^(m_i - M) o_i /
+// sum 2^(m_i - M) l_i.  A block per boundary; the P - 1 boundaries that cut a unit into P
+// partials share its tasks, a task being 32 dims of a row: a warp reads four partials at a
+// time, eight lanes of four dims each.
 constexpr int kMergeThreads = 256;
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
     pdl_wait();          // inputs may come from the previous kernel of the stream
     pdl_launch_next();
-    constexpr int W = kMergeThreads / 32, V = D / 32;
-    __shared__ float red[W][D];
-    __shared__ float red_m[W], red_l[W];
-    const int64_t *off = p.off;
-    const int64_t per = off[p.batch + 1];
-    // grid: (query row, query head)
-    const int64_t row = blockIdx.x / p.hq;
-    const int head = static_cast<int>(blockIdx.x - row * p.hq), kh = head / p.g;
-    int b = static_cast<int>(row);
-    if (p.qo_indptr) {
-        int lo = 0, hi = p.batch;
+    const int64_t sp = blockIdx.x;
+    const int4 c = p.cuts[sp];
+    if (c.x < 0) return;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane >> 3;
+    const int back = c.z >> 1, parts = back + c.w + 1, rb = c.y / p.hkv, kh = c.y - rb * p.hkv;
+    const int64_t s0 = sp - back;
+    const int qo0 = p.qo_indptr ? p.qo_indptr[c.x] : c.x, n = p.qo_indptr ? p.qo_indptr[c.x + 1] - qo0 : 1;
+    constexpr int kTasks = 8 * NT * (D / 32);
+    for (int task = (back - 1) * (kMergeThreads / 32) + warp; task < kTasks; task += (parts - 1) * (kMergeThreads / 32)) {
+        const int lr = task / (D / 32), d0 = (task % (D / 32)) * 32 + (lane & 7) * 4;
+        const int row = rb * 8 * NT + lr, tok = row / p.g, hh = row - tok * p.g;
+        if (tok >= n) continue;
+        float m = -INFINITY, l = 0.f;
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+        for (int i = sub; i < parts; i += 4) {
+            const int64_t at = ((s0 + i) * 2 + (i == 0 ? c.z & 1 : 0)) * 8 * NT + lr;
+            const float2 ml = reinterpret_cast<const float2 *>(p.part_ml)[at];
+            const float4 x = *reinterpret_cast<const float4 *>(p.part_o + at * D + d0);
+            const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
+            const float c0 = ex2(m - base), c1 = ex2(ml.x - base);
+            m = mn;
+            l = l * c0 + ml.y * c1;
+            o.x = o.x * c0 + x.x * c1;
+            o.y = o.y * c0 + x.y * c1;
+            o.z = o.z * c0 + x.z * c1;
+            o.w = o.w * c0 + x.w * c1;
+        }
+#pragma unroll
+        for (int off = 8; off < 32; off <<= 1) {
+            const float m2 = __shfl_xor_sync(0xffffffffu, m, off), l2 = __shfl_xor_sync(0xffffffffu, l, off);
+            const float4 x = make_float4(__shfl_xor_sync(0xffffffffu, o.x, off), __shfl_xor_sync(0xffffffffu, o.y, off),
+                                         __shfl_xor_sync(0xffffffffu, o.z, off), __shfl_xor_sync(0xffffffffu, o.w, off));
+            const float mn = fmaxf(m, m2), base = mn == -INFINITY ? 0.f : mn;
+            const float c0 = ex2(m - base), c1 = ex2(m2 - base);
+            m = mn;
+            l = l * c0 + l2 * c1;
+            o.x = o.x * c0 + x.x * c1;
+            o.y = o.y * c0 + x.y * c1;
+            o.z = o.z * c0 + x.z * c1;
+            o.w = o.w * c0 + x.w * c1;
+        }
+        if (sub) continue;
+        const int64_t at = static_cast<int64_t>(qo0 + tok) * p.hq + kh * p.g + hh;
+        const float inv = l == 0.f ? 0.f : (p.v_scale ? p.v_scale[kh] : 1.f) / l;
+        *reinterpret_cast<uint2 *>(p.out + at * D + d0) =
+            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+        if (d0 == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+    }
+}
+
+// ---------------------------------------------------------------- held keys
+// Requests with many query rows: their keys and values are taken out of the pool once, K as
+// bf16 and V as fp16 (both exact, without the head scales), for the tcgen05 kernel of
+// extend.cu: per key and head that moves 4.6 D bytes once, against 4 D flops for each of the
+// many rows.  Layout [D/64][kv heads][rows][64], request after request.  A key whose V
+// holds a NaN block gets a NaN K and a zero V: a zero weight times NaN would reach rows that
+// do not see the key.
+constexpr int kHoldThreads = 256;
+
+struct HoldParams {
+    uint16_t *k, *v;
+    int64_t rows;
+    int32_t *first_row, *counter;
+    int32_t min_rows;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kHoldThreads) hold_kernel(const Params p, const HoldParams h) {
+    extern __shared__ __align__(16) int32_t table[];   // [B + 1] first rows, [B + 1] first tiles
+    __shared__ long long scratch[kHoldThreads / 32];
+    __shared__ long long carry_s[2];
+    pdl_wait();          // inputs may come from the previous kernel of the stream
+    pdl_launch_next();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = p.batch;
+    int32_t *first = table, *tile0 = table + B + 1;
+    if (tid < 2) carry_s[tid] = 0;
+    if (tid == 0) first[0] = tile0[0] = 0;
+    __syncthreads();
+    for (int b0 = 0; b0 < B; b0 += kHoldThreads) {
+        const int b = b0 + tid;
+        int L = 0;
+        if (b < B) {
+            const Req r = load_req(p, b, blockIdx.x == 0);
+            if (static_cast<int64_t>(r.n) * p.g > h.min_rows) L = r.L;
+        }
+        // one scan of both sums: rows below, tiles above bit 36
+        long long v = L + (static_cast<long long>((L + kTile - 1) / kTile) << 36), incl = v;
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        if (lane == 31) scratch[warp] = incl;
+        __syncthreads();
+        long long before = carry_s[0];
+        for (int w = 0; w < warp; ++w) before += scratch[w];
+        incl += before;
+        __syncthreads();
+        if (tid == kHoldThreads - 1) carry_s[0] = incl;
+        if (b < B) {
+            first[b + 1] = static_cast<int32_t>(incl & ((1ll << 36) - 1));
+            tile0[b + 1] = static_cast<int32_t>(incl >> 36);
+        }
+        __syncthreads();
+    }
+    if (blockIdx.x == 0) {
+        for (int i = tid; i <= B; i += kHoldThreads) h.first_row[i] = first[i];
+        if (tid == 0) {
+            *h.counter = 0;
+            if (first[B] > h.rows) raise_flag(p.err, PKV_DEVERR_CAPACITY);
+        }
+        if (warp < 2) {   // unusable head scales
+            const float *g = warp ? p.v_scale : p.k_scale;
+            for (int i = lane; g && i < p.hkv; i += 32)
+                if (!quant::good_scale(g[i])) raise_flag(p.err, PKV_DEVERR_RANGE);
+        }
+    }
+    constexpr int kPerRow = D / 16, kRowThreads = 2 * kPerRow;   // threads of a row: K blocks, then V blocks
+    constexpr int kRowsAtOnce = kHoldThreads / kRowThreads;
+    const int j = tid % kPerRow, row_in = tid / kRowThreads;
+    const bool is_v = (tid / kPerRow) & 1;
+    const uint32_t group = (kRowThreads == 16 ? 0xffffu : 0xffu) << (lane / kRowThreads * kRowThreads);
+    const int t = 1 << p.t_shift;
+    const int64_t items = static_cast<int64_t>(tile0[B]) * p.hkv;
+    for (int64_t w = blockIdx.x; w < items; w += gridDim.x) {
+        const int tl = static_cast<int>(w / p.hkv), kh = static_cast<int>(w - static_cast<int64_t>(tl) * p.hkv);
+        int lo = 0, hi = B;
         while (hi - lo > 1) {
             const int mid = (lo + hi) >> 1;
-            if (p.qo_indptr[mid] <= row) lo = mid; else hi = mid;
+            if (tile0[mid] <= tl) lo = mid; else hi = mid;
         }
-        b = lo;
-    }
-    const Req rq = load_req(p, b, false);
-    const int64_t tok = row - rq.qo0;
-    if (tok < 0 || tok >= rq.n) return;
-    const int64_t ur = tok * p.g + (head - kh * p.g);
-    const int rb = static_cast<int>(ur / (8 * NT)), lr = static_cast<int>(ur - static_cast<int64_t>(rb) * 8 * NT);
-    const int tiles = unit_tiles(rq.L);
-    const int64_t u0 = off[b] + (static_cast<int64_t>(rb) * p.hkv + kh) * tiles, u1 = u0 + tiles;
-    const int64_t s0 = u0 / per, s1 = (u1 - 1) / per;
-    if (s0 == s1) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    float m = -INFINITY, l = 0.f, o[V];
+        const int L = first[lo + 1] - first[lo];
+        int64_t base;
+        quant::key_count(p.tab, lo, base, p.err, false);
+        const int key0 = (tl - tile0[lo]) * kTile;
+        uint16_t *dst = (is_v ? h.v : h.k) + ((static_cast<int64_t>(j / 4) * p.hkv + kh) * h.rows + first[lo]) * 64 + (j % 4) * 16;
 #pragma unroll
-    for (int i = 0; i < V; ++i) o[i] = 0.f;
-#pragma unroll 2
-    for (int64_t s = s0 + warp; s <= s1; s += W) {
-        const int64_t at = (s * 2 + (s == s0 && u0 > s * per ? 1 : 0)) * 8 * NT + lr;
-        const float2 ml = reinterpret_cast<const float2 *>(p.part_ml)[at];
-        if (ml.y == 0.f) continue;   // no key of this row in the span
-        float x[V];
+        for (int i = 0; i < kTile / kRowsAtOnce; ++i) {
+            const int key = key0 + i * kRowsAtOnce + row_in;
+            const bool in = key < L && first[lo] + key < h.rows;
+            const int64_t slot = in ? quant::slot_of(p.tab, base, key) : -3;
+            uint2 codes = make_uint2(0, 0);
+            uint32_t scale = 0;
+            if (slot >= 0) {
+                const int at = static_cast<int>(slot & (t - 1));
+                const uint8_t *tile = p.pool + (slot >> p.t_shift) * p.tile_stride + static_cast<int64_t>(kh) * quant::tile_bytes(t, D);
+                codes = __ldg(reinterpret_cast<const uint2 *>(tile + (is_v ? t * (D / 2) : 0) + at * (D / 2) + j * 8));
+                scale = __ldg(tile + t * D + (is_v ? t * kPerRow : 0) + at * kPerRow + j);
+            } else if (slot != -3 && kh == 0 && j == 0 && !is_v) {
+                raise_flag(p.err, slot == -1 ? PKV_DEVERR_RANGE : PKV_DEVERR_CONTIG);
+            }
+            const bool nan = is_v && (scale & 0x7f) == 0x7f;
+            const uint32_t any = __ballot_sync(0xffffffffu, nan) & group;
+            if (any) scale = is_v ? 0 : quant::kNanScale;
+            const uint32_t s2 = quant::scales_to_f16(scale | (scale << 8));
+            uint32_t x[8];
+            quant::codes_to_f16(codes.x, *reinterpret_cast<uint32_t(*)[4]>(x));
+            quant::codes_to_f16(codes.y, *reinterpret_cast<uint32_t(*)[4]>(x + 4));
 #pragma unroll
-        for (int i = 0; i < V; ++i) x[i] = p.part_o[at * D + lane * V + i];
-        const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
-        const float c0 = ex2(m - base), c1 = ex2(ml.x - base);
-        m = mn;
-        l = l * c0 + ml.y * c1;
-#pragma unroll
-        for (int i = 0; i < V; ++i) o[i] = o[i] * c0 + x[i] * c1;
+            for (int e = 0; e < 8; ++e) {
+                x[e] = quant::mul_f16x2(x[e], s2);
+                if (!is_v) {
+                    const float2 f = quant::f16x2_to_f32(x[e]);
+                    x[e] = pack_bf16x2(f.x, f.y);
+                }
+            }
+            if (in) {
+                uint4 *o = reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(key) * 64);
+                o[0] = make_uint4(x[0], x[1], x[2], x[3]);
+                o[1] = make_uint4(x[4], x[5], x[6], x[7]);
+            }
+        }
     }
-#pragma unroll
-    for (int i = 0; i < V; ++i) red[warp][lane * V + i] = o[i];
-    if (lane == 0) {
-        red_m[warp] = m;
-        red_l[warp] = l;
-    }
-    __syncthreads();
-    float M = -INFINITY, den = 0.f;
-    for (int w = 0; w < W; ++w) M = fmaxf(M, red_m[w]);
-    const float base = M == -INFINITY ? 0.f : M;
-    for (int w = 0; w < W; ++w) den += red_l[w] * ex2(red_m[w] - base);
-    const int64_t at = row * p.hq + head;
-    const float gv = p.v_scale ? p.v_scale[kh] : 1.f;
-    for (int d = threadIdx.x; d < D; d += kMergeThreads) {
-        float num = 0.f;
-        for (int w = 0; w < W; ++w) num = fmaf(red[w][d], ex2(red_m[w] - base), num);
-        p.out[at * D + d] = static_cast<uint16_t>(pack_bf16x2(den == 0.f ? 0.f : num * (gv / den), 0.f));
-    }
-    if (threadIdx.x == 0 && p.lse) p.lse[at] = den == 0.f ? -INFINITY : (M + log2f(den)) * kLn2;
 }
 
 // ------------------------------------------------------------------ host side
 static pkv_status validate(const char *who, const pkv_quant_args *a, bool extend, bool check_ptrs) {
     if (a->batch < 0 || a->num_q_heads < 1 || a->num_kv_heads < 1 || a->total_q < 0 || a->total_kv < 0 ||
-        a->max_seq_len < 0 || a->num_tiles < 0)
+        a->max_seq_len < 0 || a->max_q_len < 0 || a->num_tiles < 0)
         return fail(PKV_ERR_INVALID_ARG, "%s: negative or zero size", who);
     if (a->num_q_heads % a->num_kv_heads) return fail(PKV_ERR_INVALID_ARG, "%s: Hq not a multiple of Hkv", who);
     if (a->num_q_heads / a->num_kv_heads > 16) return fail(PKV_ERR_UNSUPPORTED, "%s: Hq/Hkv must be 16 or less", who);
@@ -770,49 +889,90 @@ static pkv_status validate(const char *who, const pkv_quant_args *a, bool extend
     return PKV_OK;
 }
 
-// The launch of attend_kernel: rows per unit, grid, spans and the workspace.
+// How a call runs: the span kernel (its rows per unit, grid, spans), and for requests with
+// many query rows the held path; with the workspace of each.
+constexpr int kHeldRows = 64;   // rows per request and kv head up to which the span kernel is used
+
 struct Plan {
+    bool spans, held, plan_launch;
     int nt, grid, stages, spans_max, span_tiles;
-    bool plan_launch;
-    size_t smem, part_o, part_ml, table;
-    size_t bytes() const { return part_o + part_ml + table; }
+    size_t smem, part_o, part_ml, cuts, table;          // span kernel
+    size_t hold_k, hold_first, ext;                     // held path: one of the two tensors, row table, extend.cu's own
+    int64_t hold_rows;
+    size_t span_bytes() const { return part_o + part_ml + cuts + table; }
+    size_t bytes() const { return (spans ? span_bytes() : 0) + (held ? 2 * hold_k + hold_first + ext : 0); }
 };
 
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-static bool make_plan(const pkv_quant_args *a, Plan &pl) {
+// The part of the arguments that extend.cu's kernel takes.
+static pkv_extend_args extend_args(const pkv_quant_args *a) {
+    pkv_extend_args e{};
+    e.batch = a->batch;
+    e.num_q_heads = a->num_q_heads;
+    e.num_kv_heads = a->num_kv_heads;
+    e.head_dim = a->head_dim;
+    e.page_size = 1;
+    e.sm_scale = a->sm_scale;
+    e.max_seq_len = a->max_seq_len;
+    e.kv_chunk = a->kv_chunk;
+    e.total_q = a->total_q;
+    e.q = a->q;
+    e.qo_indptr = a->qo_indptr;
+    e.kv_end = a->kv_end;
+    e.out = a->out;
+    e.lse = a->lse;
+    return e;
+}
+
+static bool make_plan(const pkv_quant_args *a, bool extend, Plan &pl) {
+    pl = Plan{};
     const int g = a->num_q_heads / a->num_kv_heads;
-    // rows of a request and kv head, on average: up to 8 fill one n = 8 tile
-    const int64_t rows = (std::max<int64_t>(a->total_q, 1) + std::max(a->batch, 1) - 1) / std::max(a->batch, 1) * g;
-    pl.nt = rows <= 8 ? 1 : 2;
-    const int t = std::min(a->page_size, quant::kMaxTile);
-    const size_t stage = static_cast<size_t>(kTile / t) * quant::tile_bytes(t, a->head_dim);
-    pl.stages = a->head_dim == 128 ? 2 : 4;
-    if (pl.nt == 2) pl.stages = a->head_dim == 128 ? 3 : 4;
-    const int sms = std::max(1, sm_count());
-    pl.grid = sms * (pl.nt == 1 ? 3 : 2);
-    pl.plan_launch = a->batch > kTableInSmem;
-    pl.smem = kWarps * pl.stages * stage + (pl.plan_launch ? 0 : (static_cast<size_t>(a->batch) + 2) * 8);
-    int64_t spans = static_cast<int64_t>(pl.grid) * kWarps;
-    pl.span_tiles = 0;
-    if (a->kv_chunk > 0) {
-        pl.span_tiles = a->kv_chunk / kTile;
-        const int64_t blocks = (a->total_q * g + 8 * pl.nt - 1) / (8 * pl.nt) + a->batch;
-        const int64_t tiles = blocks * a->num_kv_heads * ((std::max(1, a->max_seq_len) + kTile - 1) / kTile);
-        spans = (tiles + pl.span_tiles - 1) / pl.span_tiles;
+    const int64_t batch = std::max(a->batch, 1), total_q = std::max<int64_t>(a->total_q, 1);
+    // rows of a request and kv head: at most max_q_len's, or what the average says
+    const int64_t rows = (extend && a->max_q_len > 0 ? a->max_q_len : (total_q + batch - 1) / batch) * g;
+    pl.held = extend && rows > kHeldRows;
+    pl.spans = !pl.held || batch > 1;
+    if (pl.spans) {
+        const int64_t few = pl.held ? kHeldRows : rows;
+        pl.nt = few <= 8 ? 1 : 2;
+        const int t = std::min(a->page_size, quant::kMaxTile);
+        const size_t stage = static_cast<size_t>(kTile / t) * quant::tile_bytes(t, a->head_dim);
+        pl.stages = a->head_dim == 128 ? (pl.nt == 1 ? 2 : 3) : 4;
+        pl.grid = std::max(1, sm_count()) * (pl.nt == 1 ? 3 : 2);
+        pl.plan_launch = a->batch > kTableInSmem;
+        pl.smem = kWarps * pl.stages * stage + (pl.plan_launch ? 0 : (static_cast<size_t>(a->batch) + 2) * 8);
+        int64_t spans = static_cast<int64_t>(pl.grid) * kWarps;
+        if (a->kv_chunk > 0) {
+            pl.span_tiles = a->kv_chunk / kTile;
+            const int64_t blocks = (a->total_q * g + 8 * pl.nt - 1) / (8 * pl.nt) + a->batch;
+            const int64_t tiles = blocks * a->num_kv_heads * ((std::max(1, a->max_seq_len) + kTile - 1) / kTile);
+            spans = (tiles + pl.span_tiles - 1) / pl.span_tiles;
+        }
+        if (spans > INT32_MAX / 64) return false;
+        pl.spans_max = static_cast<int>(spans);
+        const size_t slots = static_cast<size_t>(spans) * 2 * 8 * pl.nt;
+        pl.part_o = up256(slots * a->head_dim * 4);
+        pl.part_ml = up256(slots * 8);
+        pl.cuts = up256(static_cast<size_t>(spans) * 16);
+        pl.table = up256((static_cast<size_t>(a->batch) + 2) * 8);
     }
-    if (spans > INT32_MAX / 64) return false;
-    pl.spans_max = static_cast<int>(spans);
-    const size_t slots = static_cast<size_t>(spans) * 2 * 8 * pl.nt;
-    pl.part_o = up256(slots * a->head_dim * 4);
-    pl.part_ml = up256(slots * 8);
-    pl.table = up256((static_cast<size_t>(a->batch) + 2) * 8);
+    if (pl.held) {
+        pl.hold_rows = a->total_kv > 0 ? a->total_kv : batch * a->max_seq_len;
+        pl.hold_rows = std::max<int64_t>(pl.hold_rows, 1);
+        if (pl.hold_rows > INT32_MAX / (a->num_kv_heads * (a->head_dim / 64))) return false;
+        pl.hold_k = up256(static_cast<size_t>(pl.hold_rows) * a->num_kv_heads * a->head_dim * 2);
+        pl.hold_first = up256((static_cast<size_t>(a->batch) + 1) * 4);
+        const pkv_extend_args e = extend_args(a);
+        pl.ext = up256(ext::held_workspace(&e));
+        if (pl.ext == 0 || (static_cast<size_t>(a->batch) + 1) * 8 > 64 * 1024) return false;
+    }
     return true;
 }
 
-static size_t workspace_size(const pkv_quant_args *a) {
+static size_t workspace_size(const pkv_quant_args *a, bool extend) {
     Plan pl;
-    return make_plan(a, pl) ? pl.bytes() : 0;
+    return make_plan(a, extend, pl) ? std::max<size_t>(pl.bytes(), 256) : 0;
 }
 
 static Params params(const pkv_quant_args *a, int32_t *err) {
@@ -876,8 +1036,38 @@ static pkv_status launch(const char *who, const Params &p, const Plan &pl, cudaS
     }
     st = launch_status(launch_chained(kern, dim3(pl.grid), dim3(kThreads), pl.smem, s, p), who);
     if (st != PKV_OK) return st;
-    return launch_status(launch_chained(merge_kernel<D, NT>, dim3(static_cast<unsigned>(p.total_q * p.hq)),
-                                        dim3(kMergeThreads), 0, s, p), who);
+    return launch_status(launch_chained(merge_kernel<D, NT>, dim3(pl.spans_max), dim3(kMergeThreads), 0, s, p), who);
+}
+
+template <int D>
+static pkv_status launch_held(const pkv_quant_args *a, const Params &p, const Plan &pl, char *ws, cudaStream_t s) {
+    const pkv_extend_args e = extend_args(a);
+    char *own = ws + 2 * pl.hold_k + pl.hold_first;
+    HoldParams h{};
+    h.k = reinterpret_cast<uint16_t *>(ws);
+    h.v = reinterpret_cast<uint16_t *>(ws + pl.hold_k);
+    h.rows = pl.hold_rows;
+    h.first_row = reinterpret_cast<int32_t *>(ws + 2 * pl.hold_k);
+    h.counter = reinterpret_cast<int32_t *>(own + ext::held_counter_offset(&e));
+    h.min_rows = pl.spans ? kHeldRows : 0;
+    const size_t smem = (static_cast<size_t>(a->batch) + 1) * 8;
+    std::atomic<int64_t> *set = device_memo(reinterpret_cast<const void *>(hold_kernel<D>));
+    if (!set) return fail(PKV_ERR_CUDA, "pkv_quant_extend: cannot query the current device");
+    if (set->load() == 0) {
+        if (cudaFuncSetAttribute(hold_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return fail(PKV_ERR_CUDA, "pkv_quant_extend: cannot raise the shared-memory limit");
+        }
+        set->store(1);
+    }
+    const int64_t items = (pl.hold_rows / kTile + a->batch) * a->num_kv_heads;
+    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(items, 8ll * std::max(1, sm_count())));
+    const pkv_status st = launch_status(launch_chained(hold_kernel<D>, dim3(static_cast<unsigned>(grid)), dim3(kHoldThreads),
+                                                       smem, s, p, h),
+                                        "pkv_quant_extend (hold kernel)");
+    if (st != PKV_OK) return st;
+    const ext::Held held{h.k, h.v, h.rows, h.first_row, a->k_scale, a->v_scale, a->q_row_stride, h.min_rows};
+    return ext::held_launch(&e, held, own, p.err, s);
 }
 
 static pkv_status attend(const char *who, const pkv_quant_args *a, bool extend, void *ws, size_t ws_bytes, int32_t *err,
@@ -888,20 +1078,28 @@ static pkv_status attend(const char *who, const pkv_quant_args *a, bool extend, 
     if (st != PKV_OK) return st;
     if (a->batch == 0 || a->total_q == 0) return ok();
     Plan pl;
-    if (!make_plan(a, pl)) return fail(PKV_ERR_UNSUPPORTED, "%s: too many splits", who);
-    const size_t need = pl.bytes();
+    if (!make_plan(a, extend, pl)) return fail(PKV_ERR_UNSUPPORTED, "%s: too many splits, keys or requests", who);
+    const size_t need = std::max<size_t>(pl.bytes(), 256);
     if (ws_bytes < need) return fail(PKV_ERR_CAPACITY, "%s: workspace of %zu bytes, %zu needed", who, ws_bytes, need);
     if (!ws || !aligned(ws, 256))
         return fail(PKV_ERR_INVALID_ARG, "%s: workspace must be non-null and 256-byte aligned", who);
     if (a->total_q * a->num_q_heads > INT32_MAX) return fail(PKV_ERR_UNSUPPORTED, "%s: too many query rows", who);
     Params p = params(a, err);
-    p.stages = pl.stages;
     p.wait_ns = wait_limit_ns();
+    char *at = static_cast<char *>(ws);
+    if (pl.held) {
+        const pkv_status r = a->head_dim == 128 ? launch_held<128>(a, p, pl, at, s) : launch_held<64>(a, p, pl, at, s);
+        if (r != PKV_OK || !pl.spans) return r;
+        p.max_rows = kHeldRows;
+        at += 2 * pl.hold_k + pl.hold_first + pl.ext;
+    }
+    p.stages = pl.stages;
     p.span_tiles = pl.span_tiles;
     p.spans_max = pl.spans_max;
-    p.part_o = static_cast<float *>(ws);
-    p.part_ml = reinterpret_cast<float *>(static_cast<char *>(ws) + pl.part_o);
-    p.off = reinterpret_cast<int64_t *>(static_cast<char *>(ws) + pl.part_o + pl.part_ml);
+    p.part_o = reinterpret_cast<float *>(at);
+    p.part_ml = reinterpret_cast<float *>(at + pl.part_o);
+    p.cuts = reinterpret_cast<int4 *>(at + pl.part_o + pl.part_ml);
+    p.off = reinterpret_cast<int64_t *>(at + pl.part_o + pl.part_ml + pl.cuts);
     p.off_ready = pl.plan_launch;
     if (a->head_dim == 128)
         return pl.nt == 1 ? launch<128, 1>(who, p, pl, s) : launch<128, 2>(who, p, pl, s);
@@ -914,12 +1112,12 @@ static pkv_status attend(const char *who, const pkv_quant_args *a, bool extend, 
 extern "C" size_t pkv_quant_decode_workspace_size(const pkv_quant_args *args) {
     using namespace pkv::qattn;
     if (!args || validate("pkv_quant_decode", args, false, false) != PKV_OK) return 0;
-    return workspace_size(args);
+    return workspace_size(args, false);
 }
 extern "C" size_t pkv_quant_extend_workspace_size(const pkv_quant_args *args) {
     using namespace pkv::qattn;
     if (!args || validate("pkv_quant_extend", args, true, false) != PKV_OK) return 0;
-    return workspace_size(args);
+    return workspace_size(args, true);
 }
 extern "C" pkv_status pkv_quant_decode(const pkv_quant_args *args, void *workspace, size_t workspace_bytes,
                                        int32_t *err_flags, pkv_stream_t stream) {
