@@ -17,7 +17,10 @@
 // assigned to the MMA's contraction (and output row) indices so that a lane reads
 // contiguous codes: lane (r, c) = (lane / 4, lane % 4) holds dims D/4 c ... of key row r for
 // K, and dims D/8 r ... of keys of column c for V.  Softmax in base 2 with a running
-// maximum per row.
+// maximum per row that is raised only past 2^8.  The instructions, not the copies, are what
+// a tile costs most (a conversion of two codes issues every second cycle), so V's codes of
+// two keys are interleaved before they are converted: a conversion then gives the pair
+// of keys that the MMA wants (half the permutes).
 #include <algorithm>
 #include <cmath>
 
@@ -32,8 +35,10 @@ using quant::Table;
 constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kTile = 64;           // keys per stage
 constexpr int kMaxStages = 4;
+constexpr int kMostTiles = 1 << 30; // of all units together
 constexpr int kTableInSmem = 256;   // requests whose tile offsets every CTA computes for itself
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.44269504088896341f;
+constexpr float kLazy = 8.f;        // the running maximum is raised only past 2^8 (weights stay below 2^8 in fp16)
 
 struct Params {
     Table tab;
@@ -51,7 +56,7 @@ struct Params {
     int32_t span_tiles;      // tiles per span; 0: all spans of the grid's warps equal
     int32_t spans_max;
     float *part_o, *part_ml; // per span two slots: [rows][D], and [rows] of (m, l)
-    int64_t *off;            // [B + 1] first tile of each request, then the tiles of a span
+    int32_t *off;            // [B + 1] first tile of each request, then the tiles of a span
     int32_t off_ready;       // written by plan_kernel (large batches)
     // per span: the unit that its first tile continues, {request (-1: none), row block * Hkv + kv
     // head, 2 x spans back to its first + (1 if it began inside that span), spans on to its last}
@@ -120,16 +125,17 @@ template <int NT>
 __device__ __forceinline__ int row_blocks(const Params &p, int n) { return (n * p.g + 8 * NT - 1) / (8 * NT); }
 
 // off[b] = first tile of request b's units, off[B] = all tiles, off[B + 1] = tiles per
-// span, by the block's threads.
+// span, by the block's threads.  The host has checked that the tiles of well-formed inputs
+// fit; row ranges that overlap could exceed that, and then no request has any.
 template <int NT, int kBlock>
-__device__ __forceinline__ void build_table(const Params &p, int64_t *off, long long *scratch, bool report) {
+__device__ __forceinline__ void build_table(const Params &p, int *off, long long *scratch, bool report) {
     const int B = p.batch, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int seg = (B + kBlock - 1) / kBlock, lo = min(B, tid * seg), hi = min(B, lo + seg);
     long long local = 0;
     for (int b = lo; b < hi; ++b) {
         const Req r = load_req(p, b, report);
         local += static_cast<long long>(row_blocks<NT>(p, r.n)) * p.hkv * unit_tiles(r.L);
-        off[b + 1] = local;
+        off[b + 1] = static_cast<int>(local);
     }
     long long incl = local;
     for (int o = 1; o < 32; o <<= 1) {
@@ -143,10 +149,12 @@ __device__ __forceinline__ void build_table(const Params &p, int64_t *off, long 
         if (w < warp) before += scratch[w];
         total += scratch[w];
     }
-    for (int b = lo; b < hi; ++b) off[b + 1] += before;
+    const bool fits = total <= kMostTiles;
+    for (int b = lo; b < hi; ++b) off[b + 1] = fits ? off[b + 1] + static_cast<int>(before) : 0;
     if (tid == 0) {
+        if (!fits && report) raise_flag(p.err, PKV_DEVERR_RANGE);
         off[0] = 0;
-        off[B + 1] = p.span_tiles ? p.span_tiles : max(1ll, (total + p.spans_max - 1) / p.spans_max);
+        off[B + 1] = p.span_tiles ? p.span_tiles : max(1, (static_cast<int>(fits ? total : 0) + p.spans_max - 1) / p.spans_max);
     }
     __syncthreads();
 }
@@ -162,14 +170,14 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Params p) {
 // The part of one unit that lies in one span.
 struct Segment {
     int64_t base;            // of the request's page list
-    int64_t pos, end;        // its tiles in the sequence of all tiles
+    int pos, end;            // its tiles in the sequence of all tiles
     int b, kh, rb, L, n, qo0;
     int t0, t1;              // its tiles within the unit
     int tiles;               // of the unit
 };
 
 template <int NT>
-__device__ __forceinline__ Segment segment_at(const Params &p, const int64_t *off, int64_t pos, int64_t span_end) {
+__device__ __forceinline__ Segment segment_at(const Params &p, const int *off, int pos, int span_end) {
     int lo = 0, hi = p.batch;   // the last request with off[b] <= pos (those without rows have no tiles)
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
@@ -183,12 +191,12 @@ __device__ __forceinline__ Segment segment_at(const Params &p, const int64_t *of
     s.qo0 = r.qo0;
     s.base = r.base;
     s.tiles = unit_tiles(r.L);
-    const int64_t rem = pos - off[lo];
-    const int64_t u = rem / s.tiles;
-    s.t0 = static_cast<int>(rem - u * s.tiles);
-    s.rb = static_cast<int>(u / p.hkv);
-    s.kh = static_cast<int>(u - static_cast<int64_t>(s.rb) * p.hkv);
-    s.t1 = static_cast<int>(min(static_cast<int64_t>(s.tiles), s.t0 + span_end - pos));
+    const int rem = pos - off[lo];
+    const int u = rem / s.tiles;
+    s.t0 = rem - u * s.tiles;
+    s.rb = u / p.hkv;
+    s.kh = u - s.rb * p.hkv;
+    s.t1 = min(s.tiles, s.t0 + span_end - pos);
     s.pos = pos;
     s.end = pos + (s.t1 - s.t0);
     return s;
@@ -202,15 +210,47 @@ __device__ __forceinline__ int unit_keys(const Params &p, const Segment &s) {
     return s.L - s.n + last;
 }
 
-// Walks the tiles of a span that have keys to fetch, one call per tile.
-template <int NT>
+// Walks the tiles of a span that have keys, one call of fetch() per tile, and issues their
+// copies.  A tile is 64 / t pieces (pages, or a page's next 64 keys); the pool addresses of
+// 64 consecutive pieces (a window) are held by the lanes, two each, and each lane issues the
+// copies of its own pieces.  The next window's slots are looked up a window ahead.
+template <int D, int NT>
 struct Fetcher {
     Segment s;
-    int64_t span_end;
+    int span_end;
     int t, t_end, keys;      // next tile of the segment; end of those with keys; unit_keys
     bool done;
+    const uint8_t *src[2];   // pieces 64 w + lane, + 32 of the window; nullptr: past the keys, or a bad page
+    bool bad;                // one of them is a bad page
+    int nxt[2];              // slots of the next window's
 
-    __device__ __forceinline__ void enter(const Params &p, const int64_t *off, int64_t pos) {
+    __device__ __forceinline__ void look_up(const Params &p, int window, int lane) {
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int64_t key = static_cast<int64_t>(window * 64 + 32 * i + lane) << p.t_shift;
+            nxt[i] = key < keys && key < static_cast<int64_t>(t_end) * kTile 
+                         ? static_cast<int>(quant::slot_of(p.tab, s.base, static_cast<int>(key)))
+                         : -3;
+        }
+    }
+    // the looked-up window becomes the current one
+    __device__ __forceinline__ void enter_window(const Params &p, int window, int lane) {
+        const int64_t head = static_cast<int64_t>(s.kh) * quant::tile_bytes(1 << p.t_shift, D);
+        int flags = 0;
+        bad = false;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            src[i] = nxt[i] >= 0 ? p.pool + static_cast<int64_t>(nxt[i] >> p.t_shift) * p.tile_stride + head : nullptr;
+            if (nxt[i] == -1 || nxt[i] == -2) {
+                bad = true;
+                flags |= nxt[i] == -1 ? PKV_DEVERR_RANGE : PKV_DEVERR_CONTIG;
+            }
+        }
+        if (flags) raise_flag(p.err, flags);
+        bad = __any_sync(0xffffffffu, bad);
+        look_up(p, window + 1, lane);
+    }
+    __device__ __forceinline__ void enter(const Params &p, const int *off, int pos, int lane) {
         for (;;) {
             if (pos >= span_end) {
                 done = true;
@@ -220,85 +260,80 @@ struct Fetcher {
             keys = unit_keys<NT>(p, s);
             t = s.t0;
             t_end = min(s.t1, (keys + kTile - 1) / kTile);
-            if (t < t_end) return;
+            if (t < t_end) break;
             pos = s.end;
         }
+        const int w = t >> p.t_shift;   // 64 pieces are t = 2^t_shift tiles
+        look_up(p, w, lane);
+        enter_window(p, w, lane);
     }
-    __device__ __forceinline__ void start(const Params &p, const int64_t *off, int64_t begin, int64_t end) {
+    __device__ __forceinline__ void start(const Params &p, const int *off, int begin, int end, int lane) {
         span_end = end;
         done = false;
-        enter(p, off, begin);
+        enter(p, off, begin, lane);
     }
-    __device__ __forceinline__ void next(const Params &p, const int64_t *off) {
-        if (++t >= t_end) enter(p, off, s.end);
-    }
-};
-
-// Pieces (pages, or their first 64 keys) of a tile that lane `lane` fetches: piece lane and,
-// on pages of one key, lane + 32.  -3: past the unit's keys.
-struct Pieces {
-    int64_t slot[2];
-};
-template <int NT>
-__device__ __forceinline__ Pieces look_up(const Params &p, const Fetcher<NT> &f, int lane) {
-    Pieces x;
+    // Copies the next tile into `stage`, completing on `bar`, and moves on.
+    __device__ __forceinline__ void fetch(const Params &p, const int *off, uint8_t *stage, uint64_t *bar, int lane) {
+        const int shift = 6 - p.t_shift;            // log2 of the pieces of a tile
+        const uint32_t bytes = quant::tile_bytes(1 << p.t_shift, D);
+        const int first = (t & ((1 << p.t_shift) - 1)) << shift;   // the tile's first piece within the window
+        const int n = min(1 << shift, (keys - t * kTile + (1 << p.t_shift) - 1) >> p.t_shift);
+        uint32_t live = n;
+        if (bad) {
+            live = 0;
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const int key = f.t * kTile + ((lane + 32 * i) << p.t_shift);
-        x.slot[i] = -3;
-        if (!f.done && ((lane + 32 * i) << p.t_shift) < kTile && key < f.keys) x.slot[i] = quant::slot_of(p.tab, f.s.base, key);
-    }
-    return x;
-}
-template <int D>
-__device__ __forceinline__ void fetch(const Params &p, const Pieces &x, int kh, uint8_t *stage, uint64_t *bar, int lane) {
-    const uint32_t bytes = quant::tile_bytes(1 << p.t_shift, D);
-    const uint32_t live = __popc(__ballot_sync(0xffffffffu, x.slot[0] >= 0)) +
-                          __popc(__ballot_sync(0xffffffffu, x.slot[1] >= 0));
-    if (lane == 0) mbar_arrive_expect_tx(bar, live * bytes);
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        uint8_t *dst = stage + (lane + 32 * i) * bytes;
-        if (x.slot[i] >= 0) {
-            bulk_load(dst, p.pool + (x.slot[i] >> p.t_shift) * p.tile_stride + static_cast<int64_t>(kh) * bytes, bytes, bar);
-        } else if (x.slot[i] != -3) {   // a bad page reads as zeros
-            raise_flag(p.err, x.slot[i] == -1 ? PKV_DEVERR_RANGE : PKV_DEVERR_CONTIG);
-            for (uint32_t o = 0; o < bytes; o += 16) *reinterpret_cast<uint4 *>(dst + o) = make_uint4(0, 0, 0, 0);
-            fence_proxy_async_smem();   // before later copies into this stage
+            for (int i = 0; i < 2; ++i) {
+                const int j = 32 * i + lane - first;
+                const bool mine = j >= 0 && j < n;
+                live += __popc(__ballot_sync(0xffffffffu, mine && src[i]));
+                if (mine && !src[i]) {   // a bad page reads as zeros
+                    for (uint32_t o = 0; o < bytes; o += 16) *reinterpret_cast<uint4 *>(stage + j * bytes + o) = make_uint4(0, 0, 0, 0);
+                    fence_proxy_async_smem();   // before later copies into this stage
+                }
+            }
         }
+        if (lane == 0) mbar_arrive_expect_tx(bar, live * bytes);
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int j = 32 * i + lane - first;
+            if (j >= 0 && j < n && src[i]) bulk_load(stage + j * bytes, src[i], bytes, bar);
+        }
+        __syncwarp();
+        if (++t >= t_end)
+            enter(p, off, s.end, lane);
+        else if ((t & ((1 << p.t_shift) - 1)) == 0)
+            enter_window(p, t >> p.t_shift, lane);
     }
-    __syncwarp();
-}
+};
 
-// Where the rows of a 16-key group lie in a stage.
-template <int D, bool kSmall>
+// Where key `k` (a lane's part) of the 16-key group `kt` lies in a stage.  kT is the tile of
+// the pool: with 64 or 16 slots known to the compiler every address is a lane's base and a
+// constant; kT = 0 works it out for any.
+template <int D, int kT>
 struct Rows {
-    const uint8_t *base;   // pages of >= 16 keys: the piece, moved to the group's first key
-    int t_shift, in;       // group's first key within its piece
     const uint8_t *stage;
-    int key0;
-    __device__ __forceinline__ Rows(const uint8_t *st, int k0, int shift) : t_shift(shift), stage(st), key0(k0) {
-        const int t = 1 << shift;
-        in = k0 & (t - 1);
-        base = st + (k0 >> shift) * quant::tile_bytes(t, D);
-    }
-    // codes of row k of the group (part 0 = K, 1 = V), and its scales
-    __device__ __forceinline__ const uint8_t *codes(int part, int k) const {
-        const int t = 1 << t_shift;
-        if (kSmall) {
-            const int key = key0 + k;
-            return stage + (key >> t_shift) * quant::tile_bytes(t, D) + part * t * (D / 2) + (key & (t - 1)) * (D / 2);
+    int t_shift;
+    __device__ __forceinline__ const uint8_t *piece(int kt, int k, int &at, int &t) const {
+        if (kT >= 16) {
+            t = kT;
+            at = kt * 16 % kT + k;
+            return stage + kt * 16 / kT * quant::tile_bytes(kT ? kT : 1, D);
         }
-        return base + part * t * (D / 2) + (in + k) * (D / 2);
+        t = 1 << t_shift;
+        at = (kt * 16 + k) & (t - 1);
+        return stage + ((kt * 16 + k) >> t_shift) * quant::tile_bytes(t, D);
     }
-    __device__ __forceinline__ const uint8_t *scales(int part, int k) const {
-        const int t = 1 << t_shift;
-        if (kSmall) {
-            const int key = key0 + k;
-            return stage + (key >> t_shift) * quant::tile_bytes(t, D) + t * D + part * t * (D / 16) + (key & (t - 1)) * (D / 16);
-        }
-        return base + t * D + part * t * (D / 16) + (in + k) * (D / 16);
+    // its codes (part 0 = K, 1 = V), and its scales
+    __device__ __forceinline__ const uint8_t *codes(int part, int kt, int k) const {
+        int at, t;
+        const uint8_t *b = piece(kt, k, at, t);
+        return b + part * t * (D / 2) + at * (D / 2);
+    }
+    __device__ __forceinline__ const uint8_t *scales(int part, int kt, int k) const {
+        int at, t;
+        const uint8_t *b = piece(kt, k, at, t);
+        return b + t * D + part * t * (D / 16) + at * (D / 16);
     }
 };
 
@@ -317,11 +352,12 @@ struct State {
 
 // One tile: keys 64 t ... of the unit.  With kMask some row's bound or the unit's last key
 // lies inside the tile.
-template <int D, int NT, bool kSmall, bool kMask>
+template <int D, int NT, int kT, bool kMask>
 __device__ __forceinline__ void tile_step(const Params &p, State<D, NT> &st, const uint8_t *stage, int key0, int keys,
                                           int lane) {
     const int r = lane >> 2, c = lane & 3;
     constexpr int KS = D / 16;     // contraction steps of q.k, and 16-row blocks of O^T
+    const Rows<D, kT> rows{stage, p.t_shift};
     float s[4][NT][4];
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt) {
@@ -329,12 +365,11 @@ __device__ __forceinline__ void tile_step(const Params &p, State<D, NT> &st, con
         for (int n = 0; n < NT; ++n)
 #pragma unroll
             for (int i = 0; i < 4; ++i) s[kt][n][i] = 0.f;
-        const Rows<D, kSmall> rows(stage, kt * 16, p.t_shift);
         uint32_t h[2][D / 8];      // fp16 pairs of this lane's D/4 dims of rows r and r + 8
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int k = key_of(r) + 8 * u;
-            const uint8_t *cp = rows.codes(0, k) + c * (D / 8), *sp = rows.scales(0, k) + c * (D / 64);
+            const uint8_t *cp = rows.codes(0, kt, k) + c * (D / 8), *sp = rows.scales(0, kt, k) + c * (D / 64);
             if (D == 128) {
                 const uint4 w = *reinterpret_cast<const uint4 *>(cp);
                 const uint32_t sc = quant::scales_to_f16(*reinterpret_cast<const uint16_t *>(sp));
@@ -384,10 +419,20 @@ __device__ __forceinline__ void tile_step(const Params &p, State<D, NT> &st, con
                 }
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float mn = fmaxf(st.m[n][w], top * st.f[n][w]);
-            const float base = mn == -INFINITY ? 0.f : mn;   // no key yet: every weight is 2^-inf
-            const float corr = ex2(st.m[n][w] - base);
-            st.m[n][w] = mn;
+            const float mx = top * st.f[n][w];
+            const bool raise = mx > st.m[n][w] + kLazy || (st.m[n][w] == -INFINITY && mx != -INFINITY);
+            if (__any_sync(0xffffffffu, raise)) {   // rare: the sums so far are rescaled
+                const float mn = raise ? mx : st.m[n][w];
+                const float corr = mn == -INFINITY ? 1.f : ex2(st.m[n][w] - mn);
+                st.m[n][w] = mn;
+                st.l[n][w] *= corr;
+#pragma unroll
+                for (int t = 0; t < KS; ++t) {
+                    st.o[t][n][w] *= corr;
+                    st.o[t][n][2 + w] *= corr;
+                }
+            }
+            const float base = st.m[n][w] == -INFINITY ? 0.f : st.m[n][w];   // no key yet: every weight is 2^-inf
             float sum = 0.f;
 #pragma unroll
             for (int kt = 0; kt < 4; ++kt)
@@ -397,12 +442,7 @@ __device__ __forceinline__ void tile_step(const Params &p, State<D, NT> &st, con
                     x = ex2(fmaf(x, st.f[n][w], -base));
                     sum += x;
                 }
-            st.l[n][w] = fmaf(st.l[n][w], corr, sum);
-#pragma unroll
-            for (int t = 0; t < KS; ++t) {
-                st.o[t][n][w] *= corr;
-                st.o[t][n][2 + w] *= corr;
-            }
+            st.l[n][w] += sum;
         }
 #pragma unroll
         for (int kt = 0; kt < 4; ++kt)
@@ -412,18 +452,17 @@ __device__ __forceinline__ void tile_step(const Params &p, State<D, NT> &st, con
     }
 #pragma unroll
     for (int kt = 0; kt < 4; ++kt) {
-        const Rows<D, kSmall> rows(stage, kt * 16, p.t_shift);
         uint32_t a[2][2][KS];      // [keys 2c.. / 2c + 8..][even / odd dim][16-row block]
         bool bad = false;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            uint32_t x[2][KS];
+            uint32_t w[2][D / 64];   // codes of the two keys, D/8 dims each
             uint32_t sc[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 const int k = key_of(2 * c + e) + 8 * u;
-                const uint8_t *cp = rows.codes(1, k) + r * (D / 16);
-                sc[e] = rows.scales(1, k)[D == 128 ? r : r >> 1];
+                const uint8_t *cp = rows.codes(1, kt, k) + r * (D / 16);
+                sc[e] = rows.scales(1, kt, k)[D == 128 ? r : r >> 1];
                 if (kMask) {
                     // nothing of a key past the unit's last, and no NaN that only some rows may see
                     const bool in = key0 + kt * 16 + k < keys;
@@ -432,18 +471,27 @@ __device__ __forceinline__ void tile_step(const Params &p, State<D, NT> &st, con
                     if (!in || nan) sc[e] = 0;
                 }
                 if (D == 128) {
-                    const uint2 w = *reinterpret_cast<const uint2 *>(cp);
-                    quant::codes_to_f16(w.x, *reinterpret_cast<uint32_t(*)[4]>(x[e]));
-                    quant::codes_to_f16(w.y, *reinterpret_cast<uint32_t(*)[4]>(x[e] + KS / 2));
+                    const uint2 x = *reinterpret_cast<const uint2 *>(cp);
+                    w[e][0] = x.x;
+                    w[e][D / 64 - 1] = x.y;
                 } else {
-                    quant::codes_to_f16(*reinterpret_cast<const uint32_t *>(cp), *reinterpret_cast<uint32_t(*)[4]>(x[e]));
+                    w[e][0] = *reinterpret_cast<const uint32_t *>(cp);
                 }
             }
             const uint32_t sp = quant::scales_to_f16(sc[0] | (sc[1] << 8));
 #pragma unroll
-            for (int t = 0; t < KS; ++t) {
-                a[u][0][t] = quant::mul_f16x2(__byte_perm(x[0][t], x[1][t], 0x5410), sp);
-                a[u][1][t] = quant::mul_f16x2(__byte_perm(x[0][t], x[1][t], 0x7632), sp);
+            for (int i = 0; i < D / 64; ++i) {
+                // bytes (first key, second key) of the even dims, and of the odd ones
+                const uint32_t even = (w[0][i] & 0x0f0f0f0fu) | ((w[1][i] << 4) & 0xf0f0f0f0u);
+                const uint32_t odd = ((w[0][i] >> 4) & 0x0f0f0f0fu) | (w[1][i] & 0xf0f0f0f0u);
+                uint32_t x[4], y[4];
+                quant::codes_to_f16(even, x);
+                quant::codes_to_f16(odd, y);
+#pragma unroll
+                for (int t = 0; t < 4; ++t) {
+                    a[u][0][4 * i + t] = quant::mul_f16x2(x[t], sp);
+                    a[u][1][4 * i + t] = quant::mul_f16x2(y[t], sp);
+                }
             }
         }
 #pragma unroll
@@ -455,7 +503,7 @@ __device__ __forceinline__ void tile_step(const Params &p, State<D, NT> &st, con
             // the rows that see a key whose V block is NaN get it in that block's dims
             for (int k = 0; k < 16; ++k) {
                 const int key = key0 + kt * 16 + k;
-                if (key >= keys || (rows.scales(1, k)[D == 128 ? r : r >> 1] & 0x7f) != 0x7f) continue;
+                if (key >= keys || (rows.scales(1, kt, k)[D == 128 ? r : r >> 1] & 0x7f) != 0x7f) continue;
 #pragma unroll
                 for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -569,7 +617,7 @@ __device__ __forceinline__ void finish_segment(const Params &p, const Segment &s
         }
 }
 
-template <int D, int NT, bool kSmall>
+template <int D, int NT, int kT>
 __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attend_kernel(const Params p) {
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[kWarps * kMaxStages];
@@ -585,9 +633,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attend_kernel(const
     __syncwarp();
     pdl_wait();          // inputs may come from the previous kernel of the stream
     pdl_launch_next();
-    const int64_t *off = p.off;
+    const int *off = p.off;
     if (!p.off_ready) {
-        int64_t *mine = reinterpret_cast<int64_t *>(smem + static_cast<uint32_t>(kWarps * p.stages) * stage_bytes);
+        int *mine = reinterpret_cast<int *>(smem + static_cast<uint32_t>(kWarps * p.stages) * stage_bytes);
         build_table<NT, kThreads>(p, mine, scratch, blockIdx.x == 0);
         off = mine;
     }
@@ -596,39 +644,33 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attend_kernel(const
         for (int h = lane; g && h < p.hkv; h += 32)
             if (!quant::good_scale(g[h])) raise_flag(p.err, PKV_DEVERR_RANGE);
     }
-    const int64_t total = off[p.batch], per = off[p.batch + 1];
+    const int total = off[p.batch], per = off[p.batch + 1];
     uint32_t issued = 0, used = 0;   // tiles whose copies were issued, and awaited
     bool ok = true;
     const uint32_t S = p.stages;
     State<D, NT> st;
-    for (int64_t sp = static_cast<int64_t>(blockIdx.x) * kWarps + warp; ok && sp < p.spans_max;
-         sp += static_cast<int64_t>(gridDim.x) * kWarps) {
-        const int64_t begin = sp * per, end = min(total, begin + per);
+    for (int sp = blockIdx.x * kWarps + warp; ok && sp < p.spans_max; sp += gridDim.x * kWarps) {
+        // (sp * per stays below total + spans_max * per: checked to fit on the host)
+        const int begin = sp * per, end = min(total, begin + per);
         if (begin >= total) {
             if (lane == 0) p.cuts[sp] = make_int4(-1, 0, 0, 0);
             continue;
         }
-        Fetcher<NT> f;
-        f.start(p, off, begin, end);
-        Pieces ahead = look_up(p, f, lane);   // of the next tile to fetch
+        Fetcher<D, NT> f;
+        f.start(p, off, begin, end, lane);
         auto fetch_next = [&]() {
             if (f.done) return;
-            const uint32_t s = issued % S;
-            const int kh = f.s.kh;
-            const Pieces now = ahead;
-            f.next(p, off);
-            ahead = look_up(p, f, lane);
-            fetch<D>(p, now, kh, ring + s * stage_bytes, &bar[s], lane);
+            const uint32_t b = issued % S;
+            f.fetch(p, off, ring + b * stage_bytes, &bar[b], lane);
             ++issued;
         };
         for (uint32_t i = 0; i < S; ++i) fetch_next();
-        for (int64_t pos = begin; ok && pos < end;) {
+        for (int pos = begin; ok && pos < end;) {
             const Segment s = segment_at<NT>(p, off, pos, end);
             const int keys = unit_keys<NT>(p, s);
             if (pos == begin && lane == 0) {
-                const int64_t u0 = pos - s.t0, u1 = u0 + s.tiles - 1;
-                p.cuts[sp] = s.t0 ? make_int4(s.b, s.rb * p.hkv + s.kh, static_cast<int>(sp - u0 / per) * 2 + (u0 % per ? 1 : 0),
-                                              static_cast<int>(u1 / per - sp))
+                const int u0 = pos - s.t0, u1 = u0 + s.tiles - 1, s0 = u0 / per;
+                p.cuts[sp] = s.t0 ? make_int4(s.b, s.rb * p.hkv + s.kh, (sp - s0) * 2 + (u0 > s0 * per ? 1 : 0), u1 / per - sp)
                                   : make_int4(-1, 0, 0, 0);
             }
             start_segment<D, NT>(p, s, st, lane);
@@ -645,15 +687,15 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attend_kernel(const
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 if ((t + 1) * kTile <= low)
-                    tile_step<D, NT, kSmall, false>(p, st, ring + b * stage_bytes, t * kTile, keys, lane);
+                    tile_step<D, NT, kT, false>(p, st, ring + b * stage_bytes, t * kTile, keys, lane);
                 else
-                    tile_step<D, NT, kSmall, true>(p, st, ring + b * stage_bytes, t * kTile, keys, lane);
+                    tile_step<D, NT, kT, true>(p, st, ring + b * stage_bytes, t * kTile, keys, lane);
                 ++used;
                 __syncwarp();
                 fetch_next();
             }
             if (!ok) break;
-            finish_segment<D, NT>(p, s, st, sp * 2 + (s.t0 == 0 && pos > begin ? 1 : 0), lane);
+            finish_segment<D, NT>(p, s, st, static_cast<int64_t>(sp) * 2 + (s.t0 == 0 && pos > begin ? 1 : 0), lane);
             pos = s.end;
         }
     }
@@ -941,21 +983,22 @@ static bool make_plan(const pkv_quant_args *a, bool extend, Plan &pl) {
         pl.stages = a->head_dim == 128 ? (pl.nt == 1 ? 2 : 3) : 4;
         pl.grid = std::max(1, sm_count()) * (pl.nt == 1 ? 3 : 2);
         pl.plan_launch = a->batch > kTableInSmem;
-        pl.smem = kWarps * pl.stages * stage + (pl.plan_launch ? 0 : (static_cast<size_t>(a->batch) + 2) * 8);
+        pl.smem = kWarps * pl.stages * stage + (pl.plan_launch ? 0 : (static_cast<size_t>(a->batch) + 2) * 4);
         int64_t spans = static_cast<int64_t>(pl.grid) * kWarps;
+        // all units' tiles, at most
+        const int64_t blocks = (a->total_q * g + 8 * pl.nt - 1) / (8 * pl.nt) + a->batch;
+        const int64_t tiles = blocks * a->num_kv_heads * ((std::max(1, a->max_seq_len) + kTile - 1) / kTile);
         if (a->kv_chunk > 0) {
             pl.span_tiles = a->kv_chunk / kTile;
-            const int64_t blocks = (a->total_q * g + 8 * pl.nt - 1) / (8 * pl.nt) + a->batch;
-            const int64_t tiles = blocks * a->num_kv_heads * ((std::max(1, a->max_seq_len) + kTile - 1) / kTile);
             spans = (tiles + pl.span_tiles - 1) / pl.span_tiles;
         }
-        if (spans > INT32_MAX / 64) return false;
+        if (spans > INT32_MAX / 64 || tiles > kMostTiles) return false;
         pl.spans_max = static_cast<int>(spans);
         const size_t slots = static_cast<size_t>(spans) * 2 * 8 * pl.nt;
         pl.part_o = up256(slots * a->head_dim * 4);
         pl.part_ml = up256(slots * 8);
         pl.cuts = up256(static_cast<size_t>(spans) * 16);
-        pl.table = up256((static_cast<size_t>(a->batch) + 2) * 8);
+        pl.table = up256((static_cast<size_t>(a->batch) + 2) * 4);
     }
     if (pl.held) {
         pl.hold_rows = a->total_kv > 0 ? a->total_kv : batch * a->max_seq_len;
@@ -1019,7 +1062,7 @@ static Params params(const pkv_quant_args *a, int32_t *err) {
 
 template <int D, int NT>
 static pkv_status launch(const char *who, const Params &p, const Plan &pl, cudaStream_t s) {
-    auto *kern = p.t_shift < 4 ? attend_kernel<D, NT, true> : attend_kernel<D, NT, false>;
+    auto *kern = p.t_shift == 6 ? attend_kernel<D, NT, 64> : p.t_shift == 4 ? attend_kernel<D, NT, 16> : attend_kernel<D, NT, 0>;
     std::atomic<int64_t> *set = device_memo(reinterpret_cast<const void *>(kern));
     if (!set) return fail(PKV_ERR_CUDA, "%s: cannot query the current device", who);
     if (set->load() < static_cast<int64_t>(pl.smem)) {   // kernel attributes are per device
@@ -1099,7 +1142,7 @@ static pkv_status attend(const char *who, const pkv_quant_args *a, bool extend, 
     p.part_o = reinterpret_cast<float *>(at);
     p.part_ml = reinterpret_cast<float *>(at + pl.part_o);
     p.cuts = reinterpret_cast<int4 *>(at + pl.part_o + pl.part_ml);
-    p.off = reinterpret_cast<int64_t *>(at + pl.part_o + pl.part_ml + pl.cuts);
+    p.off = reinterpret_cast<int32_t *>(at + pl.part_o + pl.part_ml + pl.cuts);
     p.off_ready = pl.plan_launch;
     if (a->head_dim == 128)
         return pl.nt == 1 ? launch<128, 1>(who, p, pl, s) : launch<128, 2>(who, p, pl, s);
