@@ -33,8 +33,13 @@ namespace qattn {
 using quant::Table;
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kTile = 64;           // keys per stage
-constexpr int kMaxStages = 4;
+constexpr int kTile = 32;           // keys per stage
+constexpr int kGroups = kTile / 16; // of 16 keys: the MMAs' key rows
+constexpr int kUnitCost = 2;        // tiles' worth of work that starting and finishing a unit takes
+// Blocks per SM of the span kernel, and stages of a warp's ring (what fits beside them).
+constexpr int ctas_per_sm(int d, int nt) { return nt == 1 ? 4 : d == 64 ? 3 : 2; }
+constexpr int ring_stages(int d, int nt) { return d == 64 ? 5 : nt == 1 ? 3 : 5; }
+constexpr int kHoldTile = 64;       // keys per work item of hold_kernel
 constexpr int kMostTiles = 1 << 30; // of all units together
 constexpr int kTableInSmem = 256;   // requests whose tile offsets every CTA computes for itself
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.44269504088896341f;
@@ -42,7 +47,7 @@ constexpr float kLazy = 8.f;        // the running maximum is raised only past 2
 
 struct Params {
     Table tab;
-    int32_t batch, hq, hkv, g, t_shift, stages;
+    int32_t batch, hq, hkv, g, t_shift;
     float scale_log2;
     int64_t total_q, tile_stride, q_stride;
     const uint16_t *q;
@@ -120,7 +125,10 @@ __device__ __forceinline__ Req load_req(const Params &p, int b, bool report) {
     }
     return r;
 }
-__device__ __forceinline__ int unit_tiles(int L) { return max(1, (L + kTile - 1) / kTile); }
+// A unit enters the sequence as kUnitCost stand-in tiles and its real ones, so that a span
+// of many short units holds no more work than one inside a long unit.
+__device__ __forceinline__ int real_tiles(int L) { return max(1, (L + kTile - 1) / kTile); }
+__device__ __forceinline__ int unit_tiles(int L) { return kUnitCost + real_tiles(L); }
 template <int NT>
 __device__ __forceinline__ int row_blocks(const Params &p, int n) { return (n * p.g + 8 * NT - 1) / (8 * NT); }
 
@@ -170,10 +178,11 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Params p) {
 // The part of one unit that lies in one span.
 struct Segment {
     int64_t base;            // of the request's page list
-    int pos, end;            // its tiles in the sequence of all tiles
+    int end;                 // of its tiles in the sequence of all tiles
+    int first;               // the unit's first real tile there
     int b, kh, rb, L, n, qo0;
-    int t0, t1;              // its tiles within the unit
-    int tiles;               // of the unit
+    int t0, t1;              // its real tiles within the unit (t1 <= t0: none)
+    int tiles;               // real tiles of the unit
 };
 
 template <int NT>
@@ -190,15 +199,14 @@ __device__ __forceinline__ Segment segment_at(const Params &p, const int *off, i
     s.n = r.n;
     s.qo0 = r.qo0;
     s.base = r.base;
-    s.tiles = unit_tiles(r.L);
-    const int rem = pos - off[lo];
-    const int u = rem / s.tiles;
-    s.t0 = rem - u * s.tiles;
+    s.tiles = real_tiles(r.L);
+    const int all = s.tiles + kUnitCost, rem = pos - off[lo], u = rem / all, at = rem - u * all;
     s.rb = u / p.hkv;
     s.kh = u - s.rb * p.hkv;
-    s.t1 = min(s.tiles, s.t0 + span_end - pos);
-    s.pos = pos;
-    s.end = pos + (s.t1 - s.t0);
+    s.first = pos - at + kUnitCost;
+    s.end = min(pos - at + all, span_end);
+    s.t0 = max(at - kUnitCost, 0);
+    s.t1 = s.end - s.first;
     return s;
 }
 
@@ -211,76 +219,84 @@ __device__ __forceinline__ int unit_keys(const Params &p, const Segment &s) {
 }
 
 // Walks the tiles of a span that have keys, one call of fetch() per tile, and issues their
-// copies.  A tile is 64 / t pieces (pages, or a page's next 64 keys); the pool addresses of
-// 64 consecutive pieces (a window) are held by the lanes, two each, and each lane issues the
-// copies of its own pieces.  The next window's slots are looked up a window ahead.
-template <int D, int NT>
+// copies.  A piece is min(page size, 32) keys of one page; the pool addresses of 64
+// consecutive pieces (a window) are held by the lanes, two each, and each lane issues the
+// copies of its own: one, or four where the pool's tile is 64 slots (kT = 64) and the piece
+// a half of it.  The next window's slots are looked up a window ahead.
+template <int D, int NT, int kT>
 struct Fetcher {
-    Segment s;
-    int span_end;
-    int t, t_end, keys;      // next tile of the segment; end of those with keys; unit_keys
-    bool done;
+    int64_t base;            // of the request's page list
+    int span_end, next;      // tiles of all units: the span's end, the next segment's start
+    int kh, t, t_end, keys;  // next tile of the unit; end of those with keys; unit_keys
+    bool done, bad;          // no tile left; a piece of the window lies on a bad page
     const uint8_t *src[2];   // pieces 64 w + lane, + 32 of the window; nullptr: past the keys, or a bad page
-    bool bad;                // one of them is a bad page
     int nxt[2];              // slots of the next window's
 
+    // log2 of the keys of a piece
+    __device__ __forceinline__ static int shift(const Params &p) { return kT == 64 ? 5 : kT == 16 ? 4 : p.t_shift; }
     __device__ __forceinline__ void look_up(const Params &p, int window, int lane) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const int64_t key = static_cast<int64_t>(window * 64 + 32 * i + lane) << p.t_shift;
-            nxt[i] = key < keys && key < static_cast<int64_t>(t_end) * kTile 
-                         ? static_cast<int>(quant::slot_of(p.tab, s.base, static_cast<int>(key)))
+            const int64_t key = static_cast<int64_t>(window * 64 + 32 * i + lane) << shift(p);
+            nxt[i] = key < keys && key < static_cast<int64_t>(t_end) * kTile
+                         ? static_cast<int>(quant::slot_of(p.tab, base, static_cast<int>(key)))
                          : -3;
         }
     }
     // the looked-up window becomes the current one
     __device__ __forceinline__ void enter_window(const Params &p, int window, int lane) {
-        const int64_t head = static_cast<int64_t>(s.kh) * quant::tile_bytes(1 << p.t_shift, D);
+        const int64_t head = static_cast<int64_t>(kh) * quant::tile_bytes(1 << p.t_shift, D);
         int flags = 0;
-        bad = false;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             src[i] = nxt[i] >= 0 ? p.pool + static_cast<int64_t>(nxt[i] >> p.t_shift) * p.tile_stride + head : nullptr;
-            if (nxt[i] == -1 || nxt[i] == -2) {
-                bad = true;
-                flags |= nxt[i] == -1 ? PKV_DEVERR_RANGE : PKV_DEVERR_CONTIG;
-            }
+            if (nxt[i] == -1) flags |= PKV_DEVERR_RANGE;
+            if (nxt[i] == -2) flags |= PKV_DEVERR_CONTIG;
         }
         if (flags) raise_flag(p.err, flags);
-        bad = __any_sync(0xffffffffu, bad);
+        bad = __any_sync(0xffffffffu, flags);
         look_up(p, window + 1, lane);
     }
-    __device__ __forceinline__ void enter(const Params &p, const int *off, int pos, int lane) {
+    __device__ __forceinline__ void enter(const Params &p, const int *off, int lane) {
         for (;;) {
-            if (pos >= span_end) {
+            if (next >= span_end) {
                 done = true;
                 return;
             }
-            s = segment_at<NT>(p, off, pos, span_end);
+            const Segment s = segment_at<NT>(p, off, next, span_end);
+            next = s.end;
+            base = s.base;
+            kh = s.kh;
             keys = unit_keys<NT>(p, s);
             t = s.t0;
             t_end = min(s.t1, (keys + kTile - 1) / kTile);
             if (t < t_end) break;
-            pos = s.end;
         }
-        const int w = t >> p.t_shift;   // 64 pieces are t = 2^t_shift tiles
+        const int w = t >> (shift(p) + 1);   // 64 pieces are 2^(shift + 1) tiles
         look_up(p, w, lane);
         enter_window(p, w, lane);
     }
     __device__ __forceinline__ void start(const Params &p, const int *off, int begin, int end, int lane) {
         span_end = end;
+        next = begin;
         done = false;
-        enter(p, off, begin, lane);
+        enter(p, off, lane);
     }
     // Copies the next tile into `stage`, completing on `bar`, and moves on.
     __device__ __forceinline__ void fetch(const Params &p, const int *off, uint8_t *stage, uint64_t *bar, int lane) {
-        const int shift = 6 - p.t_shift;            // log2 of the pieces of a tile
-        const uint32_t bytes = quant::tile_bytes(1 << p.t_shift, D);
-        const int first = (t & ((1 << p.t_shift) - 1)) << shift;   // the tile's first piece within the window
-        const int n = min(1 << shift, (keys - t * kTile + (1 << p.t_shift) - 1) >> p.t_shift);
-        uint32_t live = n;
-        if (bad) {
-            live = 0;
+        const int ps = shift(p), in_window = (2 << ps) - 1;
+        const uint32_t bytes = quant::tile_bytes(1 << ps, D);
+        const int first = (t & in_window) << (5 - ps);   // the tile's first piece within the window
+        const int n = min(1 << (5 - ps), (keys - t * kTile + (1 << ps) - 1) >> ps);
+        if (!bad) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int j = 32 * i + lane - first;
+                if (j == 0) mbar_arrive_expect_tx(bar, n * bytes);
+            }
+            if (kT != 64) __syncwarp();   // (with one piece the same lane copies)
+        } else {
+            uint32_t live = 0;
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int j = 32 * i + lane - first;
@@ -291,34 +307,48 @@ struct Fetcher {
                     fence_proxy_async_smem();   // before later copies into this stage
                 }
             }
+            if (lane == 0) mbar_arrive_expect_tx(bar, live * bytes);
+            __syncwarp();
         }
-        if (lane == 0) mbar_arrive_expect_tx(bar, live * bytes);
-        __syncwarp();
+        if (kT == 64) {
+            // K and V codes, K and V scales of 32 of the tile's 64 slots
+            constexpr int C = 32 * D / 2, S = 32 * D / 16;
+            const uint8_t *a = first < 32 ? src[0] : src[1];
+            if (lane == (first & 31) && a) {
+                const uint8_t *codes = a + (t & 1) * C, *scales = a + 4 * C + (t & 1) * S;
+                bulk_load(stage, codes, C, bar);
+                bulk_load(stage + C, codes + 2 * C, C, bar);
+                bulk_load(stage + 2 * C, scales, S, bar);
+                bulk_load(stage + 2 * C + S, scales + 2 * S, S, bar);
+            }
+        } else {
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int j = 32 * i + lane - first;
-            if (j >= 0 && j < n && src[i]) bulk_load(stage + j * bytes, src[i], bytes, bar);
+            for (int i = 0; i < 2; ++i) {
+                const int j = 32 * i + lane - first;
+                if (j >= 0 && j < n && src[i]) bulk_load(stage + j * bytes, src[i], bytes, bar);
+            }
         }
-        __syncwarp();
+        if (bad) __syncwarp();
         if (++t >= t_end)
-            enter(p, off, s.end, lane);
-        else if ((t & ((1 << p.t_shift) - 1)) == 0)
-            enter_window(p, t >> p.t_shift, lane);
+            enter(p, off, lane);
+        else if ((t & in_window) == 0)
+            enter_window(p, t >> (ps + 1), lane);
     }
 };
 
-// Where key `k` (a lane's part) of the 16-key group `kt` lies in a stage.  kT is the tile of
-// the pool: with 64 or 16 slots known to the compiler every address is a lane's base and a
-// constant; kT = 0 works it out for any.
+// Where key `k` (a lane's part) of the 16-key group `kt` lies in a stage.  kT is the slots of a
+// pool tile: with 64 (pieces of 32) or 16 known to the compiler every address is a lane's base
+// and a constant; kT = 0 works it out for the others.
 template <int D, int kT>
 struct Rows {
     const uint8_t *stage;
     int t_shift;
     __device__ __forceinline__ const uint8_t *piece(int kt, int k, int &at, int &t) const {
-        if (kT >= 16) {
-            t = kT;
-            at = kt * 16 % kT + k;
-            return stage + kt * 16 / kT * quant::tile_bytes(kT ? kT : 1, D);
+        if (kT > 0) {
+            constexpr int P = kT == 64 ? 32 : 16;
+            t = P;
+            at = kt * 16 % P + k;
+            return stage + kt * 16 / P * quant::tile_bytes(P, D);
         }
         t = 1 << t_shift;
         at = (kt * 16 + k) & (t - 1);
@@ -350,7 +380,7 @@ struct State {
     float o[D / 16][NT][4];        // O^T
 };
 
-// One tile: keys 64 t ... of the unit.  With kMask some row's bound or the unit's last key
+// One tile: keys kTile t ... of the unit.  With kMask some row's bound or the unit's last key
 // lies inside the tile.
 template <int D, int NT, int kT, bool kMask>
 __device__ __forceinline__ void tile_step(const Params &p, State<D, NT> &st, const uint8_t *stage, int key0, int keys,
@@ -358,59 +388,61 @@ __device__ __forceinline__ void tile_step(const Params &p, State<D, NT> &st, con
     const int r = lane >> 2, c = lane & 3;
     constexpr int KS = D / 16;     // contraction steps of q.k, and 16-row blocks of O^T
     const Rows<D, kT> rows{stage, p.t_shift};
-    float s[4][NT][4];
+    float s[kGroups][NT][4];
+    // q.k a word (eight dims per lane) at a time over the groups of 16 keys: their MMAs
+    // are independent of one another
+    uint32_t w[kGroups][2][D / 32], sc[kGroups][2];
 #pragma unroll
-    for (int kt = 0; kt < 4; ++kt) {
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-            for (int i = 0; i < 4; ++i) s[kt][n][i] = 0.f;
-        uint32_t h[2][D / 8];      // fp16 pairs of this lane's D/4 dims of rows r and r + 8
+    for (int kt = 0; kt < kGroups; ++kt)
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int k = key_of(r) + 8 * u;
             const uint8_t *cp = rows.codes(0, kt, k) + c * (D / 8), *sp = rows.scales(0, kt, k) + c * (D / 64);
             if (D == 128) {
-                const uint4 w = *reinterpret_cast<const uint4 *>(cp);
-                const uint32_t sc = quant::scales_to_f16(*reinterpret_cast<const uint16_t *>(sp));
-                const uint32_t s0 = __byte_perm(sc, 0, 0x1010), s1 = __byte_perm(sc, 0, 0x3232);
-                const uint32_t ww[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    uint32_t x[4];
-                    quant::codes_to_f16(ww[i], x);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) h[u][i * 4 + e] = quant::mul_f16x2(x[e], i < 2 ? s0 : s1);
-                }
+                const uint4 x = *reinterpret_cast<const uint4 *>(cp);
+                w[kt][u][0] = x.x;
+                w[kt][u][1] = x.y;
+                w[kt][u][D / 64] = x.z;
+                w[kt][u][D / 32 - 1] = x.w;
+                sc[kt][u] = quant::scales_to_f16(*reinterpret_cast<const uint16_t *>(sp));
             } else {
-                const uint2 w = *reinterpret_cast<const uint2 *>(cp);
-                const uint32_t sc = quant::scales_to_f16(*sp);
-                const uint32_t s0 = __byte_perm(sc, 0, 0x1010);
-                const uint32_t ww[2] = {w.x, w.y};
-#pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    uint32_t x[4];
-                    quant::codes_to_f16(ww[i], x);
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) h[u][i * 4 + e] = quant::mul_f16x2(x[e], s0);
-                }
+                const uint2 x = *reinterpret_cast<const uint2 *>(cp);
+                w[kt][u][0] = x.x;
+                w[kt][u][1] = x.y;
+                sc[kt][u] = quant::scales_to_f16(*sp);
             }
+#pragma unroll
+            for (int n = 0; n < NT; ++n) s[kt][n][2 * u] = s[kt][n][2 * u + 1] = 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < KS; ++j)
+    for (int i = 0; i < D / 32; ++i)
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
-                mma_f16(s[kt][n], h[0][2 * j], h[1][2 * j], h[0][2 * j + 1], h[1][2 * j + 1], st.q[j][n][0], st.q[j][n][1]);
-    }
+        for (int kt = 0; kt < kGroups; ++kt) {
+            uint32_t h[2][4];
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                // D = 128: the lane's 32 dims are two blocks, two words each
+                const uint32_t sb = __byte_perm(sc[kt][u], 0, D == 64 || i < 2 ? 0x1010 : 0x3232);
+                quant::codes_to_f16(w[kt][u][i], h[u]);
+#pragma unroll
+                for (int e = 0; e < 4; ++e) h[u][e] = quant::mul_f16x2(h[u][e], sb);
+            }
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    mma_f16(s[kt][n], h[0][2 * j], h[1][2 * j], h[0][2 * j + 1], h[1][2 * j + 1], st.q[2 * i + j][n][0],
+                            st.q[2 * i + j][n][1]);
+        }
     // softmax: s[kt][n][2 u + w] is key kt * 16 + key_of(r) + 8 u of row 8 n + 2 c + w
-    uint32_t pt[4][NT][2];
+    uint32_t pt[kGroups][NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
             float top = -INFINITY;
 #pragma unroll
-            for (int kt = 0; kt < 4; ++kt)
+            for (int kt = 0; kt < kGroups; ++kt)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     float &x = s[kt][n][2 * u + w];
@@ -435,7 +467,7 @@ __device__ __forceinline__ void tile_step(const Params &p, State<D, NT> &st, con
             const float base = st.m[n][w] == -INFINITY ? 0.f : st.m[n][w];   // no key yet: every weight is 2^-inf
             float sum = 0.f;
 #pragma unroll
-            for (int kt = 0; kt < 4; ++kt)
+            for (int kt = 0; kt < kGroups; ++kt)
 #pragma unroll
                 for (int u = 0; u < 2; ++u) {
                     float &x = s[kt][n][2 * u + w];
@@ -445,13 +477,13 @@ __device__ __forceinline__ void tile_step(const Params &p, State<D, NT> &st, con
             st.l[n][w] += sum;
         }
 #pragma unroll
-        for (int kt = 0; kt < 4; ++kt)
+        for (int kt = 0; kt < kGroups; ++kt)
 #pragma unroll
             for (int u = 0; u < 2; ++u)
                 pt[kt][n][u] = transpose_8x8(pack_f16x2(s[kt][n][2 * u], s[kt][n][2 * u + 1]));
     }
 #pragma unroll
-    for (int kt = 0; kt < 4; ++kt) {
+    for (int kt = 0; kt < kGroups; ++kt) {
         uint32_t a[2][2][KS];      // [keys 2c.. / 2c + 8..][even / odd dim][16-row block]
         bool bad = false;
 #pragma unroll
@@ -618,16 +650,18 @@ __device__ __forceinline__ void finish_segment(const Params &p, const Segment &s
 }
 
 template <int D, int NT, int kT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attend_kernel(const Params p) {
+__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) attend_kernel(const Params p) {
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ __align__(8) uint64_t bars[kWarps * kMaxStages];
+    __shared__ __align__(8) uint64_t bars[kWarps * ring_stages(D, NT)];
     __shared__ long long scratch[kWarps];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t stage_bytes = (kTile >> p.t_shift) * quant::tile_bytes(1 << p.t_shift, D);
-    uint8_t *ring = smem + static_cast<uint32_t>(warp * p.stages) * stage_bytes;
-    uint64_t *bar = bars + warp * kMaxStages;
+    const int piece = min(1 << p.t_shift, kTile);
+    const uint32_t stage_bytes = kTile / piece * quant::tile_bytes(piece, D);
+    constexpr int S = ring_stages(D, NT);
+    uint8_t *ring = smem + static_cast<uint32_t>(warp * S) * stage_bytes;
+    uint64_t *bar = bars + warp * S;
     if (lane == 0) {
-        for (int i = 0; i < p.stages; ++i) mbar_init(&bar[i], 1);
+        for (int i = 0; i < S; ++i) mbar_init(&bar[i], 1);
         mbar_init_fence();
     }
     __syncwarp();
@@ -635,7 +669,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attend_kernel(const
     pdl_launch_next();
     const int *off = p.off;
     if (!p.off_ready) {
-        int *mine = reinterpret_cast<int *>(smem + static_cast<uint32_t>(kWarps * p.stages) * stage_bytes);
+        int *mine = reinterpret_cast<int *>(smem + static_cast<uint32_t>(kWarps * S) * stage_bytes);
         build_table<NT, kThreads>(p, mine, scratch, blockIdx.x == 0);
         off = mine;
     }
@@ -646,8 +680,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attend_kernel(const
     }
     const int total = off[p.batch], per = off[p.batch + 1];
     uint32_t issued = 0, used = 0;   // tiles whose copies were issued, and awaited
+    uint32_t put = 0, take = 0, phase = 0;   // stages of the next copy and of the next tile; its barrier's phase
     bool ok = true;
-    const uint32_t S = p.stages;
     State<D, NT> st;
     for (int sp = blockIdx.x * kWarps + warp; ok && sp < p.spans_max; sp += gridDim.x * kWarps) {
         // (sp * per stays below total + spans_max * per: checked to fit on the host)
@@ -656,23 +690,25 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attend_kernel(const
             if (lane == 0) p.cuts[sp] = make_int4(-1, 0, 0, 0);
             continue;
         }
-        Fetcher<D, NT> f;
+        Fetcher<D, NT, kT> f;
         f.start(p, off, begin, end, lane);
         auto fetch_next = [&]() {
             if (f.done) return;
-            const uint32_t b = issued % S;
-            f.fetch(p, off, ring + b * stage_bytes, &bar[b], lane);
+            f.fetch(p, off, ring + put * stage_bytes, &bar[put], lane);
+            put = put == S - 1 ? 0 : put + 1;
             ++issued;
         };
-        for (uint32_t i = 0; i < S; ++i) fetch_next();
+        for (int i = 0; i < S; ++i) fetch_next();
         for (int pos = begin; ok && pos < end;) {
             const Segment s = segment_at<NT>(p, off, pos, end);
             const int keys = unit_keys<NT>(p, s);
-            if (pos == begin && lane == 0) {
-                const int u0 = pos - s.t0, u1 = u0 + s.tiles - 1, s0 = u0 / per;
-                p.cuts[sp] = s.t0 ? make_int4(s.b, s.rb * p.hkv + s.kh, (sp - s0) * 2 + (u0 > s0 * per ? 1 : 0), u1 / per - sp)
+            if (pos == begin && lane == 0) {   // cut: the unit has real tiles on both sides of the boundary
+                const int s0 = s.first / per, s1 = (s.first + s.tiles - 1) / per;
+                p.cuts[sp] = s.t0 ? make_int4(s.b, s.rb * p.hkv + s.kh, (sp - s0) * 2 + (s.first > s0 * per ? 1 : 0), s1 - sp)
                                   : make_int4(-1, 0, 0, 0);
             }
+            pos = s.end;
+            if (s.t0 >= s.t1) continue;
             start_segment<D, NT>(p, s, st, lane);
             int low = s.L;   // every row sees the keys below it
 #pragma unroll
@@ -682,21 +718,24 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attend_kernel(const
             low = __reduce_min_sync(0xffffffffu, low);
             const int t_end = min(s.t1, (keys + kTile - 1) / kTile);
             for (int t = s.t0; t < t_end; ++t) {
-                const uint32_t b = used % S;
-                ok = wait_for(&bar[b], (used / S) & 1, p.wait_ns);
+                ok = wait_for(&bar[take], phase, p.wait_ns);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
+                const uint8_t *stage = ring + take * stage_bytes;
                 if ((t + 1) * kTile <= low)
-                    tile_step<D, NT, kT, false>(p, st, ring + b * stage_bytes, t * kTile, keys, lane);
+                    tile_step<D, NT, kT, false>(p, st, stage, t * kTile, keys, lane);
                 else
-                    tile_step<D, NT, kT, true>(p, st, ring + b * stage_bytes, t * kTile, keys, lane);
+                    tile_step<D, NT, kT, true>(p, st, stage, t * kTile, keys, lane);
                 ++used;
+                if (++take == S) {
+                    take = 0;
+                    phase ^= 1;
+                }
                 __syncwarp();
                 fetch_next();
             }
             if (!ok) break;
-            finish_segment<D, NT>(p, s, st, static_cast<int64_t>(sp) * 2 + (s.t0 == 0 && pos > begin ? 1 : 0), lane);
-            pos = s.end;
+            finish_segment<D, NT>(p, s, st, static_cast<int64_t>(sp) * 2 + (s.t0 == 0 && s.first > begin ? 1 : 0), lane);
         }
     }
     if (!ok) {   // a wait ran out: the copies in flight land before the block's memory is given back
@@ -802,7 +841,7 @@ __global__ void __launch_bounds__(kHoldThreads) hold_kernel(const Params p, cons
             if (static_cast<int64_t>(r.n) * p.g > h.min_rows) L = r.L;
         }
         // one scan of both sums: rows below, tiles above bit 36
-        long long v = L + (static_cast<long long>((L + kTile - 1) / kTile) << 36), incl = v;
+        long long v = L + (static_cast<long long>((L + kHoldTile - 1) / kHoldTile) << 36), incl = v;
         for (int o = 1; o < 32; o <<= 1) {
             const long long x = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += x;
@@ -849,10 +888,10 @@ __global__ void __launch_bounds__(kHoldThreads) hold_kernel(const Params p, cons
         const int L = first[lo + 1] - first[lo];
         int64_t base;
         quant::key_count(p.tab, lo, base, p.err, false);
-        const int key0 = (tl - tile0[lo]) * kTile;
+        const int key0 = (tl - tile0[lo]) * kHoldTile;
         uint16_t *dst = (is_v ? h.v : h.k) + ((static_cast<int64_t>(j / 4) * p.hkv + kh) * h.rows + first[lo]) * 64 + (j % 4) * 16;
 #pragma unroll
-        for (int i = 0; i < kTile / kRowsAtOnce; ++i) {
+        for (int i = 0; i < kHoldTile / kRowsAtOnce; ++i) {
             const int key = key0 + i * kRowsAtOnce + row_in;
             const bool in = key < L && first[lo] + key < h.rows;
             const int64_t slot = in ? quant::slot_of(p.tab, base, key) : -3;
@@ -937,7 +976,7 @@ constexpr int kHeldRows = 64;   // rows per request and kv head up to which the 
 
 struct Plan {
     bool spans, held, plan_launch;
-    int nt, grid, stages, spans_max, span_tiles;
+    int nt, grid, spans_max, span_tiles;
     size_t smem, part_o, part_ml, cuts, table;          // span kernel
     size_t hold_k, hold_first, ext;                     // held path: one of the two tensors, row table, extend.cu's own
     int64_t hold_rows;
@@ -978,16 +1017,15 @@ static bool make_plan(const pkv_quant_args *a, bool extend, Plan &pl) {
     if (pl.spans) {
         const int64_t few = pl.held ? kHeldRows : rows;
         pl.nt = few <= 8 ? 1 : 2;
-        const int t = std::min(a->page_size, quant::kMaxTile);
+        const int t = std::min(a->page_size, kTile);
         const size_t stage = static_cast<size_t>(kTile / t) * quant::tile_bytes(t, a->head_dim);
-        pl.stages = a->head_dim == 128 ? (pl.nt == 1 ? 2 : 3) : 4;
-        pl.grid = std::max(1, sm_count()) * (pl.nt == 1 ? 3 : 2);
+        pl.grid = std::max(1, sm_count()) * ctas_per_sm(a->head_dim, pl.nt);
         pl.plan_launch = a->batch > kTableInSmem;
-        pl.smem = kWarps * pl.stages * stage + (pl.plan_launch ? 0 : (static_cast<size_t>(a->batch) + 2) * 4);
+        pl.smem = kWarps * ring_stages(a->head_dim, pl.nt) * stage + (pl.plan_launch ? 0 : (static_cast<size_t>(a->batch) + 2) * 4);
         int64_t spans = static_cast<int64_t>(pl.grid) * kWarps;
         // all units' tiles, at most
         const int64_t blocks = (a->total_q * g + 8 * pl.nt - 1) / (8 * pl.nt) + a->batch;
-        const int64_t tiles = blocks * a->num_kv_heads * ((std::max(1, a->max_seq_len) + kTile - 1) / kTile);
+        const int64_t tiles = blocks * a->num_kv_heads * ((std::max(1, a->max_seq_len) + kTile - 1) / kTile + kUnitCost);
         if (a->kv_chunk > 0) {
             pl.span_tiles = a->kv_chunk / kTile;
             spans = (tiles + pl.span_tiles - 1) / pl.span_tiles;
@@ -1103,7 +1141,7 @@ static pkv_status launch_held(const pkv_quant_args *a, const Params &p, const Pl
         }
         set->store(1);
     }
-    const int64_t items = (pl.hold_rows / kTile + a->batch) * a->num_kv_heads;
+    const int64_t items = (pl.hold_rows / kHoldTile + a->batch) * a->num_kv_heads;
     const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(items, 8ll * std::max(1, sm_count())));
     const pkv_status st = launch_status(launch_chained(hold_kernel<D>, dim3(static_cast<unsigned>(grid)), dim3(kHoldThreads),
                                                        smem, s, p, h),
@@ -1136,7 +1174,6 @@ static pkv_status attend(const char *who, const pkv_quant_args *a, bool extend, 
         p.max_rows = kHeldRows;
         at += 2 * pl.hold_k + pl.hold_first + pl.ext;
     }
-    p.stages = pl.stages;
     p.span_tiles = pl.span_tiles;
     p.spans_max = pl.spans_max;
     p.part_o = reinterpret_cast<float *>(at);
