@@ -37,8 +37,8 @@ constexpr int kTile = 32;           // keys per stage
 constexpr int kGroups = kTile / 16; // of 16 keys: the MMAs' key rows
 constexpr int kUnitCost = 2;        // tiles' worth of work that starting and finishing a unit takes
 // Blocks per SM of the span kernel, and stages of a warp's ring (what fits beside them).
-constexpr int ctas_per_sm(int d, int nt) { return nt == 1 ? 4 : d == 64 ? 3 : 2; }
-constexpr int ring_stages(int d, int nt) { return d == 64 ? 5 : nt == 1 ? 3 : 5; }
+constexpr int ctas_per_sm(int d, int nt) { return nt == 1 ? 3 : d == 64 ? 3 : 2; }
+constexpr int ring_stages(int d, int nt) { return d == 64 ? 6 : nt == 1 ? 4 : 5; }
 constexpr int kHoldTile = 64;       // keys per work item of hold_kernel
 constexpr int kMostTiles = 1 << 30; // of all units together
 constexpr int kTableInSmem = 256;   // requests whose tile offsets every CTA computes for itself
@@ -74,6 +74,32 @@ __device__ __forceinline__ float ex2(float x) {
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
 }
+// Three-input maximum, and two fp32 in one 64-bit register with the paired FMA and add.
+__device__ __forceinline__ float fmax3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(a), "f"(b));
+    return d;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     uint32_t r;
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
@@ -92,12 +118,20 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                  "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
 }
+// Bounded wait; the polls suspend the warp for up to 2 us each, so that warps that wait
+// leave the issue slots to those that compute.
 __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
     if (mbar_try_wait(bar, parity)) return true;
     const uint64_t t0 = global_ns();
-    for (uint32_t i = 1;; ++i) {
-        if (mbar_try_wait(bar, parity)) return true;
-        if ((i & 63) == 1 && global_ns() - t0 > limit_ns) return false;
+    for (;;) {
+        uint32_t ok;
+        asm volatile(
+            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
+            : "=r"(ok)
+            : "r"(smem_u32(bar)), "r"(parity), "r"(2000)
+            : "memory");
+        if (ok) return true;
+        if (global_ns() - t0 > limit_ns) return false;
     }
 }
 
@@ -287,13 +321,9 @@ struct Fetcher {
         const int ps = shift(p), in_window = (2 << ps) - 1;
         const uint32_t bytes = quant::tile_bytes(1 << ps, D);
         const int first = (t & in_window) << (5 - ps);   // the tile's first piece within the window
-        const int n = min(1 << (5 - ps), (keys - t * kTile + (1 << ps) - 1) >> ps);
+        const int n = kT == 64 ? 1 : min(1 << (5 - ps), (keys - t * kTile + (1 << ps) - 1) >> ps);
         if (!bad) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int j = 32 * i + lane - first;
-                if (j == 0) mbar_arrive_expect_tx(bar, n * bytes);
-            }
+            if (lane == (first & 31)) mbar_arrive_expect_tx(bar, n * bytes);
             if (kT != 64) __syncwarp();   // (with one piece the same lane copies)
         } else {
             uint32_t live = 0;
@@ -376,7 +406,9 @@ struct State {
     uint32_t q[D / 16][NT][2];     // fp16 fragments of q
     float f[NT][2];                // score -> base-2 logit, per row of this lane's columns
     int end[NT][2];                // key bound of those rows
-    float m[NT][2], l[NT][2];      // running maximum; this lane's share of the sum
+    float nm[NT][2];               // minus the running maximum (0 before the first key)
+    float limit[NT][2];            // the maximum is raised past this: it + kLazy (-inf before the first key)
+    float l[NT][2];                // this lane's share of the sum
     float o[D / 16][NT][4];        // O^T
 };
 
@@ -438,49 +470,51 @@ __device__ __forceinline__ void tile_step(const Params &p, State<D, NT> &st, con
     uint32_t pt[kGroups][NT][2];
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
+        float top[2];   // of this lane's keys
 #pragma unroll
         for (int w = 0; w < 2; ++w) {
-            float top = -INFINITY;
 #pragma unroll
             for (int kt = 0; kt < kGroups; ++kt)
 #pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    float &x = s[kt][n][2 * u + w];
-                    if (kMask && key0 + kt * 16 + key_of(r) + 8 * u >= st.end[n][w]) x = -INFINITY;
-                    top = fmaxf(top, x);
-                }
+                for (int u = 0; u < 2; ++u)
+                    if (kMask && key0 + kt * 16 + key_of(r) + 8 * u >= st.end[n][w]) s[kt][n][2 * u + w] = -INFINITY;
+            top[w] = fmaxf(fmax3(s[0][n][w], s[0][n][2 + w], s[1][n][w]), s[1][n][2 + w]);
+        }
+        // the maximum is looked for across lanes only when some score passes it by 2^8
+        if (__any_sync(0xffffffffu, top[0] * st.f[n][0] > st.limit[n][0] || top[1] * st.f[n][1] > st.limit[n][1])) {
 #pragma unroll
-            for (int o = 4; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            const float mx = top * st.f[n][w];
-            const bool raise = mx > st.m[n][w] + kLazy || (st.m[n][w] == -INFINITY && mx != -INFINITY);
-            if (__any_sync(0xffffffffu, raise)) {   // rare: the sums so far are rescaled
-                const float mn = raise ? mx : st.m[n][w];
-                const float corr = mn == -INFINITY ? 1.f : ex2(st.m[n][w] - mn);
-                st.m[n][w] = mn;
-                st.l[n][w] *= corr;
+            for (int w = 0; w < 2; ++w) {
 #pragma unroll
-                for (int t = 0; t < KS; ++t) {
-                    st.o[t][n][w] *= corr;
-                    st.o[t][n][2 + w] *= corr;
+                for (int o = 4; o < 32; o <<= 1) top[w] = fmaxf(top[w], __shfl_xor_sync(0xffffffffu, top[w], o));
+                const float mx = top[w] * st.f[n][w];
+                if (mx > st.limit[n][w]) {
+                    const bool fresh = st.limit[n][w] == -INFINITY;
+                    const float corr = fresh ? 0.f : ex2(-st.nm[n][w] - mx);
+                    st.nm[n][w] = -mx;
+                    st.limit[n][w] = mx + kLazy;
+                    st.l[n][w] *= corr;
+#pragma unroll
+                    for (int t = 0; t < KS; ++t) {
+                        st.o[t][n][w] *= corr;
+                        st.o[t][n][2 + w] *= corr;
+                    }
                 }
             }
-            const float base = st.m[n][w] == -INFINITY ? 0.f : st.m[n][w];   // no key yet: every weight is 2^-inf
-            float sum = 0.f;
-#pragma unroll
-            for (int kt = 0; kt < kGroups; ++kt)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    float &x = s[kt][n][2 * u + w];
-                    x = ex2(fmaf(x, st.f[n][w], -base));
-                    sum += x;
-                }
-            st.l[n][w] += sum;
         }
+        const uint64_t f2 = pair(st.f[n][0], st.f[n][1]), nm2 = pair(st.nm[n][0], st.nm[n][1]);
+        uint64_t sum = pair(st.l[n][0], st.l[n][1]);
 #pragma unroll
         for (int kt = 0; kt < kGroups; ++kt)
 #pragma unroll
-            for (int u = 0; u < 2; ++u)
-                pt[kt][n][u] = transpose_8x8(pack_f16x2(s[kt][n][2 * u], s[kt][n][2 * u + 1]));
+            for (int u = 0; u < 2; ++u) {
+                const float2 y = unpair(fma2(pair(s[kt][n][2 * u], s[kt][n][2 * u + 1]), f2, nm2));
+                const float x0 = ex2(y.x), x1 = ex2(y.y);
+                sum = add2(sum, pair(x0, x1));
+                pt[kt][n][u] = transpose_8x8(pack_f16x2(x0, x1));
+            }
+        const float2 l = unpair(sum);
+        st.l[n][0] = l.x;
+        st.l[n][1] = l.y;
     }
 #pragma unroll
     for (int kt = 0; kt < kGroups; ++kt) {
@@ -602,7 +636,8 @@ __device__ __forceinline__ void start_segment(const Params &p, const Segment &s,
                 }
             }
             st.end[n][v] = end;
-            st.m[n][v] = -INFINITY;
+            st.nm[n][v] = 0.f;
+            st.limit[n][v] = -INFINITY;
             st.l[n][v] = 0.f;
         }
 #pragma unroll
@@ -638,13 +673,13 @@ __device__ __forceinline__ void finish_segment(const Params &p, const Segment &s
                 uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * D + r * W);
 #pragma unroll
                 for (int i = 0; i < W / 8; ++i) dst[i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
-                if (r == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (st.m[n][v] + log2f(l)) * kLn2;
+                if (r == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (log2f(l) - st.nm[n][v]) * kLn2;
             } else {
                 float4 *dst = reinterpret_cast<float4 *>(p.part_o + (slot * 8 * NT + lr) * D + r * W);
 #pragma unroll
                 for (int i = 0; i < W / 4; ++i)
                     dst[i] = make_float4(st.o[2 * i][n][v], st.o[2 * i][n][2 + v], st.o[2 * i + 1][n][v], st.o[2 * i + 1][n][2 + v]);
-                if (r == 0) reinterpret_cast<float2 *>(p.part_ml)[slot * 8 * NT + lr] = make_float2(st.m[n][v], l);
+                if (r == 0) reinterpret_cast<float2 *>(p.part_ml)[slot * 8 * NT + lr] = make_float2(l == 0.f ? -INFINITY : -st.nm[n][v], l);
             }
         }
 }
@@ -748,7 +783,7 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) attend_kernel(co
 // sum 2^(m_i - M) l_i.  A block per boundary; the P - 1 boundaries that cut a unit into P
 // partials share its tasks, a task being 32 dims of a row: a warp reads four partials at a
 // time, eight lanes of four dims each.
-constexpr int kMergeThreads = 256;
+constexpr int kMergeThreads = 128;
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
