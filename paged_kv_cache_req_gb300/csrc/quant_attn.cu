@@ -33,13 +33,13 @@ namespace qattn {
 using quant::Table;
 
 constexpr int kWarps = 4, kThreads = kWarps * 32;
-constexpr int kTile = 32;           // keys per stage
-constexpr int kGroups = kTile / 16; // of 16 keys: the MMAs' key rows
-constexpr int kUnitCost = 2;        // tiles' worth of work that starting and finishing a unit takes
+constexpr int kTile = 64;           // keys per stage of the copies
+constexpr int kStep = 32;           // keys per step of the math: what 128 to 168 registers hold
+constexpr int kGroups = kStep / 16; // of 16 keys: the MMAs' key rows
+constexpr int kUnitCost = 1;        // tiles' worth of work that starting and finishing a unit takes
 // Blocks per SM of the span kernel, and stages of a warp's ring (what fits beside them).
 constexpr int ctas_per_sm(int d, int nt) { return nt == 1 ? 3 : d == 64 ? 3 : 2; }
-constexpr int ring_stages(int d, int nt) { return d == 64 ? 6 : nt == 1 ? 4 : 5; }
-constexpr int kHoldTile = 64;       // keys per work item of hold_kernel
+constexpr int ring_stages(int d, int nt) { return d == 128 && nt == 1 ? 2 : 3; }
 constexpr int kMostTiles = 1 << 30; // of all units together
 constexpr int kTableInSmem = 256;   // requests whose tile offsets every CTA computes for itself
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.44269504088896341f;
@@ -112,6 +112,7 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+__device__ __forceinline__ void prefetch_l1(const void *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                      smem_u32(dst)),
@@ -252,22 +253,48 @@ __device__ __forceinline__ int unit_keys(const Params &p, const Segment &s) {
     return s.L - s.n + last;
 }
 
-// Walks the tiles of a span that have keys, one call of fetch() per tile, and issues their
-// copies.  A piece is min(page size, 32) keys of one page; the pool addresses of 64
-// consecutive pieces (a window) are held by the lanes, two each, and each lane issues the
-// copies of its own: one, or four where the pool's tile is 64 slots (kT = 64) and the piece
-// a half of it.  The next window's slots are looked up a window ahead.
+// What the math needs of a segment: a warp's queue of them lies in shared memory.
+struct Work {
+    int kh, rb, L, n, qo0;
+    int t, t_end, keys;      // tiles with keys that some row sees; unit_keys
+    int slot;                // of its partial; -1: the segment is the whole unit
+    int pad[3];
+};
+constexpr int kQueue = 8;    // segments that the copies may be ahead by (at most a ring's stages + 1)
+
+// A segment without keys: zeros and -inf where it is the whole unit, else an empty partial.
+template <int D, int NT>
+__device__ __forceinline__ void write_empty(const Params &p, const Segment &s, int slot, int lane) {
+    for (int lr = 0; lr < 8 * NT; ++lr) {
+        const int row = s.rb * 8 * NT + lr, tok = row / p.g;
+        if (tok >= s.n) return;
+        const int64_t at = static_cast<int64_t>(s.qo0 + tok) * p.hq + s.kh * p.g + (row - tok * p.g);
+        if (slot < 0) {
+            if (lane < D / 8) *reinterpret_cast<uint4 *>(p.out + at * D + lane * 8) = make_uint4(0, 0, 0, 0);
+            if (lane == 0 && p.lse) p.lse[at] = -INFINITY;
+        } else if (lane == 0) {
+            reinterpret_cast<float2 *>(p.part_ml)[static_cast<int64_t>(slot) * 8 * NT + lr] = make_float2(-INFINITY, 0.f);
+        }
+    }
+}
+
+// Walks the warp's spans and issues the copies of their tiles, one call of fetch() per tile,
+// and queues the segments for the math.  A piece is a pool tile (a page, or a page's next 64
+// keys); the pool addresses of 64 consecutive pieces (a window) are held by the lanes, two
+// each, and each lane issues the copies of its own.  Slots are looked up before they are
+// needed: the next window's with a window, a new segment's one tile ahead.
 template <int D, int NT, int kT>
 struct Fetcher {
     int64_t base;            // of the request's page list
-    int span_end, next;      // tiles of all units: the span's end, the next segment's start
+    int sp, span_end, next;  // the span; tiles of all units: its end, the next segment's start
     int kh, t, t_end, keys;  // next tile of the unit; end of those with keys; unit_keys
-    bool done, bad;          // no tile left; a piece of the window lies on a bad page
+    bool done, fresh, bad;   // no tile left; the window is not entered yet; a piece of it lies on a bad page
     const uint8_t *src[2];   // pieces 64 w + lane, + 32 of the window; nullptr: past the keys, or a bad page
     int nxt[2];              // slots of the next window's
+    uint32_t queued;         // segments so far
 
     // log2 of the keys of a piece
-    __device__ __forceinline__ static int shift(const Params &p) { return kT == 64 ? 5 : kT == 16 ? 4 : p.t_shift; }
+    __device__ __forceinline__ static int shift(const Params &p) { return kT == 64 ? 6 : kT == 16 ? 4 : p.t_shift; }
     __device__ __forceinline__ void look_up(const Params &p, int window, int lane) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -278,7 +305,7 @@ struct Fetcher {
         }
     }
     // the looked-up window becomes the current one
-    __device__ __forceinline__ void enter_window(const Params &p, int window, int lane) {
+    __device__ __forceinline__ void enter_window(const Params &p, int lane) {
         const int64_t head = static_cast<int64_t>(kh) * quant::tile_bytes(1 << p.t_shift, D);
         int flags = 0;
 #pragma unroll
@@ -289,39 +316,69 @@ struct Fetcher {
         }
         if (flags) raise_flag(p.err, flags);
         bad = __any_sync(0xffffffffu, flags);
-        look_up(p, window + 1, lane);
+        look_up(p, (t >> shift(p)) + 1, lane);   // 64 pieces are 2^shift tiles
+        fresh = false;
     }
-    __device__ __forceinline__ void enter(const Params &p, const int *off, int lane) {
+    // To the next segment that has keys.
+    __device__ __forceinline__ void advance(const Params &p, const int *off, Work *queue, int lane) {
+        const int total = off[p.batch], per = off[p.batch + 1];
         for (;;) {
-            if (next >= span_end) {
-                done = true;
-                return;
+            while (next >= span_end) {   // the warp's next span
+                sp += gridDim.x * kWarps;
+                if (sp >= p.spans_max) {
+                    done = true;
+                    return;
+                }
+                // (sp * per stays below total + spans_max * per: checked to fit on the host)
+                next = sp * per;
+                span_end = min(total, next + per);
+                if (next >= total && lane == 0) p.cuts[sp] = make_int4(-1, 0, 0, 0);
             }
             const Segment s = segment_at<NT>(p, off, next, span_end);
+            const int begin = sp * per;
+            if (next == begin && lane == 0) {   // cut: the unit has real tiles on both sides of the boundary
+                const int s0 = s.first / per, s1 = (s.first + s.tiles - 1) / per;
+                p.cuts[sp] = s.t0 ? make_int4(s.b, s.rb * p.hkv + s.kh, (sp - s0) * 2 + (s.first > s0 * per ? 1 : 0), s1 - sp)
+                                  : make_int4(-1, 0, 0, 0);
+            }
             next = s.end;
+            if (s.t0 >= s.t1) continue;
+            const int slot = s.t0 == 0 && s.t1 == s.tiles ? -1 : sp * 2 + (s.t0 == 0 && s.first > begin ? 1 : 0);
             base = s.base;
             kh = s.kh;
             keys = unit_keys<NT>(p, s);
             t = s.t0;
             t_end = min(s.t1, (keys + kTile - 1) / kTile);
-            if (t < t_end) break;
+            if (t >= t_end) {
+                write_empty<D, NT>(p, s, slot, lane);
+                continue;
+            }
+            look_up(p, t >> shift(p), lane);
+            if (lane == 0) queue[queued % kQueue] = Work{s.kh, s.rb, s.L, s.n, s.qo0, t, t_end, keys, slot, {0, 0, 0}};
+            ++queued;
+            fresh = true;
+            // q's rows on their way to L1
+            const int row = s.rb * 8 * NT + lane / (D / 64), tok = row / p.g;
+            if (lane < 8 * NT * (D / 64) && tok < s.n)
+                prefetch_l1(p.q + static_cast<int64_t>(s.qo0 + tok) * p.q_stride + (s.kh * p.g + row - tok * p.g) * D +
+                            lane % (D / 64) * 64);
+            return;
         }
-        const int w = t >> (shift(p) + 1);   // 64 pieces are 2^(shift + 1) tiles
-        look_up(p, w, lane);
-        enter_window(p, w, lane);
     }
-    __device__ __forceinline__ void start(const Params &p, const int *off, int begin, int end, int lane) {
-        span_end = end;
-        next = begin;
+    __device__ __forceinline__ void start(const Params &p, const int *off, Work *queue, int lane) {
+        sp = (static_cast<int>(blockIdx.x) - static_cast<int>(gridDim.x)) * kWarps + (threadIdx.x >> 5);
+        next = span_end = 0;
+        queued = 0;
         done = false;
-        enter(p, off, lane);
+        advance(p, off, queue, lane);
     }
     // Copies the next tile into `stage`, completing on `bar`, and moves on.
-    __device__ __forceinline__ void fetch(const Params &p, const int *off, uint8_t *stage, uint64_t *bar, int lane) {
-        const int ps = shift(p), in_window = (2 << ps) - 1;
+    __device__ __forceinline__ void fetch(const Params &p, const int *off, Work *queue, uint8_t *stage, uint64_t *bar, int lane) {
+        if (fresh) enter_window(p, lane);
+        const int ps = shift(p), in_window = (1 << ps) - 1;
         const uint32_t bytes = quant::tile_bytes(1 << ps, D);
-        const int first = (t & in_window) << (5 - ps);   // the tile's first piece within the window
-        const int n = kT == 64 ? 1 : min(1 << (5 - ps), (keys - t * kTile + (1 << ps) - 1) >> ps);
+        const int first = (t & in_window) << (6 - ps);   // the tile's first piece within the window
+        const int n = kT == 64 ? 1 : min(1 << (6 - ps), (keys - t * kTile + (1 << ps) - 1) >> ps);
         if (!bad) {
             if (lane == (first & 31)) mbar_arrive_expect_tx(bar, n * bytes);
             if (kT != 64) __syncwarp();   // (with one piece the same lane copies)
@@ -341,16 +398,8 @@ struct Fetcher {
             __syncwarp();
         }
         if (kT == 64) {
-            // K and V codes, K and V scales of 32 of the tile's 64 slots
-            constexpr int C = 32 * D / 2, S = 32 * D / 16;
             const uint8_t *a = first < 32 ? src[0] : src[1];
-            if (lane == (first & 31) && a) {
-                const uint8_t *codes = a + (t & 1) * C, *scales = a + 4 * C + (t & 1) * S;
-                bulk_load(stage, codes, C, bar);
-                bulk_load(stage + C, codes + 2 * C, C, bar);
-                bulk_load(stage + 2 * C, scales, S, bar);
-                bulk_load(stage + 2 * C + S, scales + 2 * S, S, bar);
-            }
+            if (lane == (first & 31) && a) bulk_load(stage, a, bytes, bar);
         } else {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -360,40 +409,50 @@ struct Fetcher {
         }
         if (bad) __syncwarp();
         if (++t >= t_end)
-            enter(p, off, lane);
+            advance(p, off, queue, lane);
         else if ((t & in_window) == 0)
-            enter_window(p, t >> (ps + 1), lane);
+            fresh = true;
     }
 };
 
-// Where key `k` (a lane's part) of the 16-key group `kt` lies in a stage.  kT is the slots of a
-// pool tile: with 64 (pieces of 32) or 16 known to the compiler every address is a lane's base
-// and a constant; kT = 0 works it out for the others.
+// Where key `k` (a lane's part) of the 16-key group `kt` of a step lies: relative to the step's
+// first codes and first scales.  kT is the slots of a pool tile: with 64 or 16 known to the
+// compiler every address is a lane's base and a constant; kT = 0 works it out for the others.
 template <int D, int kT>
 struct Rows {
-    const uint8_t *stage;
+    const uint8_t *codes_at, *scales_at;   // the step's first piece (64 slots: moved to the step's half of it)
     int t_shift;
-    __device__ __forceinline__ const uint8_t *piece(int kt, int k, int &at, int &t) const {
+    __device__ __forceinline__ Rows(const uint8_t *stage, int step, int shift) : t_shift(shift) {
+        codes_at = scales_at = stage;
+        if (kT == 64) {
+            codes_at += step * (kStep * D / 2);
+            scales_at += step * (kStep * D / 16);
+        } else {
+            codes_at += step * (kStep >> shift) * quant::tile_bytes(1 << shift, D);
+            scales_at = codes_at;
+        }
+    }
+    __device__ __forceinline__ int piece(int kt, int k, int &at, int &t) const {
+        const int key = kt * 16 + k;
         if (kT > 0) {
-            constexpr int P = kT == 64 ? 32 : 16;
-            t = P;
-            at = kt * 16 % P + k;
-            return stage + kt * 16 / P * quant::tile_bytes(P, D);
+            t = kT;
+            at = kT == 64 ? key : k;
+            return kT == 64 ? 0 : kt * quant::tile_bytes(16, D);
         }
         t = 1 << t_shift;
-        at = (kt * 16 + k) & (t - 1);
-        return stage + ((kt * 16 + k) >> t_shift) * quant::tile_bytes(t, D);
+        at = key & (t - 1);
+        return (key >> t_shift) * quant::tile_bytes(t, D);
     }
     // its codes (part 0 = K, 1 = V), and its scales
     __device__ __forceinline__ const uint8_t *codes(int part, int kt, int k) const {
         int at, t;
-        const uint8_t *b = piece(kt, k, at, t);
-        return b + part * t * (D / 2) + at * (D / 2);
+        const int b = piece(kt, k, at, t);
+        return codes_at + b + part * t * (D / 2) + at * (D / 2);
     }
     __device__ __forceinline__ const uint8_t *scales(int part, int kt, int k) const {
         int at, t;
-        const uint8_t *b = piece(kt, k, at, t);
-        return b + t * D + part * t * (D / 16) + at * (D / 16);
+        const int b = piece(kt, k, at, t);
+        return scales_at + b + t * D + part * t * (D / 16) + at * (D / 16);
     }
 };
 
@@ -412,14 +471,14 @@ struct State {
     float o[D / 16][NT][4];        // O^T
 };
 
-// One tile: keys kTile t ... of the unit.  With kMask some row's bound or the unit's last key
-// lies inside the tile.
+// One step: 32 keys, the unit's key0 ..., in half `step` of a stage.  With kMask some row's
+// bound or the unit's last key lies among them.
 template <int D, int NT, int kT, bool kMask>
-__device__ __forceinline__ void tile_step(const Params &p, State<D, NT> &st, const uint8_t *stage, int key0, int keys,
-                                          int lane) {
+__device__ __forceinline__ void tile_step(const Params &p, State<D, NT> &st, const uint8_t *stage, int step, int key0,
+                                          int keys, int lane) {
     const int r = lane >> 2, c = lane & 3;
     constexpr int KS = D / 16;     // contraction steps of q.k, and 16-row blocks of O^T
-    const Rows<D, kT> rows{stage, p.t_shift};
+    const Rows<D, kT> rows(stage, step, p.t_shift);
     float s[kGroups][NT][4];
     // q.k a word (eight dims per lane) at a time over the groups of 16 keys: their MMAs
     // are independent of one another
@@ -584,7 +643,7 @@ __device__ __forceinline__ void tile_step(const Params &p, State<D, NT> &st, con
 
 // q fragments, score factors and bounds of a segment's rows; a fresh softmax state.
 template <int D, int NT>
-__device__ __forceinline__ void start_segment(const Params &p, const Segment &s, State<D, NT> &st, int lane) {
+__device__ __forceinline__ void start_segment(const Params &p, const Work &s, State<D, NT> &st, int lane) {
     const int r = lane >> 2, c = lane & 3;
     const float gk = p.k_scale ? p.k_scale[s.kh] : 1.f;
 #pragma unroll
@@ -631,7 +690,7 @@ __device__ __forceinline__ void start_segment(const Params &p, const Segment &s,
             if (tv < s.n) {
                 end = !p.qo_indptr ? s.L : p.kv_end ? __ldg(p.kv_end + s.qo0 + tv) : s.L - s.n + tv + 1;
                 if (end < 0 || end > s.L) {
-                    if (r == 0 && s.kh == 0 && s.t0 == 0) raise_flag(p.err, PKV_DEVERR_RANGE);
+                    if (r == 0 && s.kh == 0 && s.t == 0) raise_flag(p.err, PKV_DEVERR_RANGE);
                     end = 0;
                 }
             }
@@ -650,10 +709,11 @@ __device__ __forceinline__ void start_segment(const Params &p, const Segment &s,
 // The segment's rows: normalised to the output when it is the whole unit, else the partial
 // of slot 0 of its span (a unit that began at or before it), or of slot 1.
 template <int D, int NT>
-__device__ __forceinline__ void finish_segment(const Params &p, const Segment &s, State<D, NT> &st, int64_t slot, int lane) {
+__device__ __forceinline__ void finish_segment(const Params &p, const Work &s, State<D, NT> &st, int lane) {
     const int r = lane >> 2, c = lane & 3;
     constexpr int W = D / 8;   // dims of a lane: D/8 r ...
-    const bool whole = s.t0 == 0 && s.t1 == s.tiles;
+    const int64_t slot = s.slot;
+    const bool whole = slot < 0;
     const float gv = p.v_scale ? p.v_scale[s.kh] : 1.f;
 #pragma unroll
     for (int n = 0; n < NT; ++n)
@@ -689,9 +749,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) attend_kernel(co
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[kWarps * ring_stages(D, NT)];
     __shared__ long long scratch[kWarps];
+    __shared__ __align__(16) Work queues[kWarps][kQueue];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int piece = min(1 << p.t_shift, kTile);
-    const uint32_t stage_bytes = kTile / piece * quant::tile_bytes(piece, D);
+    const uint32_t stage_bytes = (kTile >> p.t_shift) * quant::tile_bytes(1 << p.t_shift, D);
     constexpr int S = ring_stages(D, NT);
     uint8_t *ring = smem + static_cast<uint32_t>(warp * S) * stage_bytes;
     uint64_t *bar = bars + warp * S;
@@ -713,65 +773,56 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) attend_kernel(co
         for (int h = lane; g && h < p.hkv; h += 32)
             if (!quant::good_scale(g[h])) raise_flag(p.err, PKV_DEVERR_RANGE);
     }
-    const int total = off[p.batch], per = off[p.batch + 1];
     uint32_t issued = 0, used = 0;   // tiles whose copies were issued, and awaited
     uint32_t put = 0, take = 0, phase = 0;   // stages of the next copy and of the next tile; its barrier's phase
+    uint32_t seg = 0;                // segments whose math began
     bool ok = true;
     State<D, NT> st;
-    for (int sp = blockIdx.x * kWarps + warp; ok && sp < p.spans_max; sp += gridDim.x * kWarps) {
-        // (sp * per stays below total + spans_max * per: checked to fit on the host)
-        const int begin = sp * per, end = min(total, begin + per);
-        if (begin >= total) {
-            if (lane == 0) p.cuts[sp] = make_int4(-1, 0, 0, 0);
-            continue;
-        }
-        Fetcher<D, NT, kT> f;
-        f.start(p, off, begin, end, lane);
-        auto fetch_next = [&]() {
-            if (f.done) return;
-            f.fetch(p, off, ring + put * stage_bytes, &bar[put], lane);
+    Work w{};
+    int low = 0;                     // every row of the segment sees the keys below it
+    Fetcher<D, NT, kT> f;
+    Work *queue = queues[warp];
+    f.start(p, off, queue, lane);
+    for (;;) {
+        // (one place for the copies and one for the math: the instructions of a cold start come
+        // from memory too)
+        while (!f.done && issued - used < S) {
+            f.fetch(p, off, queue, ring + put * stage_bytes, &bar[put], lane);
             put = put == S - 1 ? 0 : put + 1;
             ++issued;
-        };
-        for (int i = 0; i < S; ++i) fetch_next();
-        for (int pos = begin; ok && pos < end;) {
-            const Segment s = segment_at<NT>(p, off, pos, end);
-            const int keys = unit_keys<NT>(p, s);
-            if (pos == begin && lane == 0) {   // cut: the unit has real tiles on both sides of the boundary
-                const int s0 = s.first / per, s1 = (s.first + s.tiles - 1) / per;
-                p.cuts[sp] = s.t0 ? make_int4(s.b, s.rb * p.hkv + s.kh, (sp - s0) * 2 + (s.first > s0 * per ? 1 : 0), s1 - sp)
-                                  : make_int4(-1, 0, 0, 0);
-            }
-            pos = s.end;
-            if (s.t0 >= s.t1) continue;
-            start_segment<D, NT>(p, s, st, lane);
-            int low = s.L;   // every row sees the keys below it
+        }
+        if (issued == used) break;
+        if (w.t >= w.t_end) {
+            __syncwarp();
+            w = queue[seg++ % kQueue];
+            start_segment<D, NT>(p, w, st, lane);
+            low = w.L;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
                 for (int v = 0; v < 2; ++v) low = min(low, st.end[n][v]);
             low = __reduce_min_sync(0xffffffffu, low);
-            const int t_end = min(s.t1, (keys + kTile - 1) / kTile);
-            for (int t = s.t0; t < t_end; ++t) {
-                ok = wait_for(&bar[take], phase, p.wait_ns);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                const uint8_t *stage = ring + take * stage_bytes;
-                if ((t + 1) * kTile <= low)
-                    tile_step<D, NT, kT, false>(p, st, stage, t * kTile, keys, lane);
-                else
-                    tile_step<D, NT, kT, true>(p, st, stage, t * kTile, keys, lane);
-                ++used;
-                if (++take == S) {
-                    take = 0;
-                    phase ^= 1;
-                }
-                __syncwarp();
-                fetch_next();
-            }
-            if (!ok) break;
-            finish_segment<D, NT>(p, s, st, static_cast<int64_t>(sp) * 2 + (s.t0 == 0 && s.first > begin ? 1 : 0), lane);
         }
+        ok = wait_for(&bar[take], phase, p.wait_ns);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) break;
+        const uint8_t *stage = ring + take * stage_bytes;
+        const int key0 = w.t * kTile;
+#pragma unroll 1
+        for (int h = 0; h < kTile / kStep; ++h) {
+            const int k = key0 + h * kStep;
+            if (k + kStep <= low)
+                tile_step<D, NT, kT, false>(p, st, stage, h, k, w.keys, lane);
+            else if (k < w.keys)
+                tile_step<D, NT, kT, true>(p, st, stage, h, k, w.keys, lane);
+        }
+        ++used;
+        if (++take == S) {
+            take = 0;
+            phase ^= 1;
+        }
+        if (++w.t >= w.t_end) finish_segment<D, NT>(p, w, st, lane);
+        __syncwarp();
     }
     if (!ok) {   // a wait ran out: the copies in flight land before the block's memory is given back
         if (lane == 0) raise_flag(p.err, PKV_DEVERR_TIMEOUT);
@@ -781,33 +832,39 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) attend_kernel(co
 
 // Combines the partials of the units that span boundaries cut: o = sum 2^(m_i - M) o_i /
 // sum 2^(m_i - M) l_i.  A block per boundary; the P - 1 boundaries that cut a unit into P
-// partials share its tasks, a task being 32 dims of a row: a warp reads four partials at a
-// time, eight lanes of four dims each.
+// partials share its outputs (four dims of a row each) evenly, and where that leaves
+// threads over, 2, 4 ... 32 of them share an output's partials.
 constexpr int kMergeThreads = 128;
 
 template <int D, int NT>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
     pdl_wait();          // inputs may come from the previous kernel of the stream
     pdl_launch_next();
-    const int64_t sp = blockIdx.x;
-    const int4 c = p.cuts[sp];
+    const int4 c = p.cuts[blockIdx.x];
     if (c.x < 0) return;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, sub = lane >> 3;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int back = c.z >> 1, parts = back + c.w + 1, rb = c.y / p.hkv, kh = c.y - rb * p.hkv;
-    const int64_t s0 = sp - back;
+    const int64_t s0 = static_cast<int>(blockIdx.x) - back;
     const int qo0 = p.qo_indptr ? p.qo_indptr[c.x] : c.x, n = p.qo_indptr ? p.qo_indptr[c.x + 1] - qo0 : 1;
-    constexpr int kTasks = 8 * NT * (D / 32);
-    for (int task = (back - 1) * (kMergeThreads / 32) + warp; task < kTasks; task += (parts - 1) * (kMergeThreads / 32)) {
-        const int lr = task / (D / 32), d0 = (task % (D / 32)) * 32 + (lane & 7) * 4;
-        const int row = rb * 8 * NT + lr, tok = row / p.g, hh = row - tok * p.g;
-        if (tok >= n) continue;
+    const float gv = p.v_scale ? p.v_scale[kh] : 1.f;
+    const int rows = min(8 * NT, n * p.g - rb * 8 * NT);
+    const int outs = rows * (D / 4), share = (outs + parts - 2) / (parts - 1);
+    int group = 1;   // outputs a warp works on at a time (the other lanes share their partials)
+    while (group < 32 && group * (kMergeThreads / 32) < share) group *= 2;
+    const int sub = lane / group, subs = 32 / group;
+    const int end = min(outs, back * share);
+    for (int o0 = (back - 1) * share; o0 < end; o0 += group * (kMergeThreads / 32)) {
+        const int out = o0 + warp * group + lane % group;
+        const bool live = out < end;
+        const int lr = live ? out / (D / 4) : 0, d0 = live ? out % (D / 4) * 4 : 0;
         float m = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-        for (int i = sub; i < parts; i += 4) {
+        for (int i = sub; i < parts; i += subs) {
             const int64_t at = ((s0 + i) * 2 + (i == 0 ? c.z & 1 : 0)) * 8 * NT + lr;
             const float2 ml = reinterpret_cast<const float2 *>(p.part_ml)[at];
             const float4 x = *reinterpret_cast<const float4 *>(p.part_o + at * D + d0);
+            if (ml.y == 0.f) continue;   // no key of the row in that span
             const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
             const float c0 = ex2(m - base), c1 = ex2(ml.x - base);
             m = mn;
@@ -817,8 +874,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
             o.z = o.z * c0 + x.z * c1;
             o.w = o.w * c0 + x.w * c1;
         }
-#pragma unroll
-        for (int off = 8; off < 32; off <<= 1) {
+        for (int off = group; off < 32; off <<= 1) {
             const float m2 = __shfl_xor_sync(0xffffffffu, m, off), l2 = __shfl_xor_sync(0xffffffffu, l, off);
             const float4 x = make_float4(__shfl_xor_sync(0xffffffffu, o.x, off), __shfl_xor_sync(0xffffffffu, o.y, off),
                                          __shfl_xor_sync(0xffffffffu, o.z, off), __shfl_xor_sync(0xffffffffu, o.w, off));
@@ -831,9 +887,10 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
             o.z = o.z * c0 + x.z * c1;
             o.w = o.w * c0 + x.w * c1;
         }
-        if (sub) continue;
-        const int64_t at = static_cast<int64_t>(qo0 + tok) * p.hq + kh * p.g + hh;
-        const float inv = l == 0.f ? 0.f : (p.v_scale ? p.v_scale[kh] : 1.f) / l;
+        if (sub || !live) continue;
+        const int row = rb * 8 * NT + lr, tok = row / p.g;
+        const int64_t at = static_cast<int64_t>(qo0 + tok) * p.hq + kh * p.g + (row - tok * p.g);
+        const float inv = l == 0.f ? 0.f : gv / l;
         *reinterpret_cast<uint2 *>(p.out + at * D + d0) =
             make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
         if (d0 == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
@@ -876,7 +933,7 @@ __global__ void __launch_bounds__(kHoldThreads) hold_kernel(const Params p, cons
             if (static_cast<int64_t>(r.n) * p.g > h.min_rows) L = r.L;
         }
         // one scan of both sums: rows below, tiles above bit 36
-        long long v = L + (static_cast<long long>((L + kHoldTile - 1) / kHoldTile) << 36), incl = v;
+        long long v = L + (static_cast<long long>((L + kTile - 1) / kTile) << 36), incl = v;
         for (int o = 1; o < 32; o <<= 1) {
             const long long x = __shfl_up_sync(0xffffffffu, incl, o);
             if (lane >= o) incl += x;
@@ -923,10 +980,10 @@ __global__ void __launch_bounds__(kHoldThreads) hold_kernel(const Params p, cons
         const int L = first[lo + 1] - first[lo];
         int64_t base;
         quant::key_count(p.tab, lo, base, p.err, false);
-        const int key0 = (tl - tile0[lo]) * kHoldTile;
+        const int key0 = (tl - tile0[lo]) * kTile;
         uint16_t *dst = (is_v ? h.v : h.k) + ((static_cast<int64_t>(j / 4) * p.hkv + kh) * h.rows + first[lo]) * 64 + (j % 4) * 16;
 #pragma unroll
-        for (int i = 0; i < kHoldTile / kRowsAtOnce; ++i) {
+        for (int i = 0; i < kTile / kRowsAtOnce; ++i) {
             const int key = key0 + i * kRowsAtOnce + row_in;
             const bool in = key < L && first[lo] + key < h.rows;
             const int64_t slot = in ? quant::slot_of(p.tab, base, key) : -3;
@@ -1052,7 +1109,7 @@ static bool make_plan(const pkv_quant_args *a, bool extend, Plan &pl) {
     if (pl.spans) {
         const int64_t few = pl.held ? kHeldRows : rows;
         pl.nt = few <= 8 ? 1 : 2;
-        const int t = std::min(a->page_size, kTile);
+        const int t = std::min(a->page_size, quant::kMaxTile);
         const size_t stage = static_cast<size_t>(kTile / t) * quant::tile_bytes(t, a->head_dim);
         pl.grid = std::max(1, sm_count()) * ctas_per_sm(a->head_dim, pl.nt);
         pl.plan_launch = a->batch > kTableInSmem;
@@ -1176,7 +1233,7 @@ static pkv_status launch_held(const pkv_quant_args *a, const Params &p, const Pl
         }
         set->store(1);
     }
-    const int64_t items = (pl.hold_rows / kHoldTile + a->batch) * a->num_kv_heads;
+    const int64_t items = (pl.hold_rows / kTile + a->batch) * a->num_kv_heads;
     const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(items, 8ll * std::max(1, sm_count())));
     const pkv_status st = launch_status(launch_chained(hold_kernel<D>, dim3(static_cast<unsigned>(grid)), dim3(kHoldThreads),
                                                        smem, s, p, h),
