@@ -32,16 +32,19 @@ namespace qattn {
 
 using quant::Table;
 
-constexpr int kWarps = 4, kThreads = kWarps * 32;
 constexpr int kTile = 64;           // keys per stage of the copies
 constexpr int kStep = 32;           // keys per step of the math: what 128 to 168 registers hold
 constexpr int kGroups = kStep / 16; // of 16 keys: the MMAs' key rows
 constexpr int kUnitCost = 1;        // tiles' worth of work that starting and finishing a unit takes
-// Blocks per SM of the span kernel, and stages of a warp's ring (what fits beside them).
-constexpr int ctas_per_sm(int d, int nt) { return nt == 1 ? 3 : d == 64 ? 3 : 2; }
+// The span kernel runs one block per SM, which holds all the shared memory: a second block of
+// a persistent grid could be left without room where the launch before still has a block,
+// and then starts when the others end.  Its warps (as many as their registers allow) and
+// the stages of a warp's ring.
+constexpr int warps_per_sm(int d, int nt) { return nt == 2 && d == 128 ? 8 : 12; }
 constexpr int ring_stages(int d, int nt) { return d == 128 && nt == 1 ? 2 : 3; }
 constexpr int kMostTiles = 1 << 30; // of all units together
-constexpr int kTableInSmem = 256;   // requests whose tile offsets every CTA computes for itself
+constexpr int kTableInSmem = 1024;  // requests whose tile offsets every block computes for itself
+constexpr int kReqInSmem = 128;     // requests whose lengths are kept beside them
 constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.44269504088896341f;
 constexpr float kLazy = 8.f;        // the running maximum is raised only past 2^8 (weights stay below 2^8 in fp16)
 
@@ -112,7 +115,6 @@ __device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1,
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
-__device__ __forceinline__ void prefetch_l1(const void *p) { asm volatile("prefetch.global.L1 [%0];" ::"l"(p)); }
 __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
     asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
                      smem_u32(dst)),
@@ -170,13 +172,20 @@ __device__ __forceinline__ int row_blocks(const Params &p, int n) { return (n * 
 // off[b] = first tile of request b's units, off[B] = all tiles, off[B + 1] = tiles per
 // span, by the block's threads.  The host has checked that the tiles of well-formed inputs
 // fit; row ranges that overlap could exceed that, and then no request has any.
+struct Table1 {
+    int *off;    // [B + 2]
+    Req *req;    // [B], or nullptr: read again where needed
+};
+
 template <int NT, int kBlock>
-__device__ __forceinline__ void build_table(const Params &p, int *off, long long *scratch, bool report) {
+__device__ __forceinline__ void build_table(const Params &p, const Table1 &tb, long long *scratch, bool report) {
+    int *off = tb.off;
     const int B = p.batch, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int seg = (B + kBlock - 1) / kBlock, lo = min(B, tid * seg), hi = min(B, lo + seg);
     long long local = 0;
     for (int b = lo; b < hi; ++b) {
         const Req r = load_req(p, b, report);
+        if (tb.req) tb.req[b] = r;
         local += static_cast<long long>(row_blocks<NT>(p, r.n)) * p.hkv * unit_tiles(r.L);
         off[b + 1] = static_cast<int>(local);
     }
@@ -207,7 +216,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Params p) {
     pdl_wait();          // inputs may come from the previous kernel of the stream
     pdl_launch_next();
     __shared__ long long scratch[32];
-    build_table<NT, 1024>(p, p.off, scratch, true);
+    build_table<NT, 1024>(p, Table1{p.off, nullptr}, scratch, true);
 }
 
 // The part of one unit that lies in one span.
@@ -221,14 +230,15 @@ struct Segment {
 };
 
 template <int NT>
-__device__ __forceinline__ Segment segment_at(const Params &p, const int *off, int pos, int span_end) {
+__device__ __forceinline__ Segment segment_at(const Params &p, const Table1 &tb, int pos, int span_end) {
+    const int *off = tb.off;
     int lo = 0, hi = p.batch;   // the last request with off[b] <= pos (those without rows have no tiles)
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (off[mid] <= pos) lo = mid; else hi = mid;
     }
     Segment s;
-    const Req r = load_req(p, lo, false);
+    const Req r = tb.req ? tb.req[lo] : load_req(p, lo, false);
     s.b = lo;
     s.L = r.L;
     s.n = r.n;
@@ -320,11 +330,11 @@ struct Fetcher {
         fresh = false;
     }
     // To the next segment that has keys.
-    __device__ __forceinline__ void advance(const Params &p, const int *off, Work *queue, int lane) {
-        const int total = off[p.batch], per = off[p.batch + 1];
+    __device__ __forceinline__ void advance(const Params &p, const Table1 &tb, Work *queue, int lane) {
+        const int total = tb.off[p.batch], per = tb.off[p.batch + 1];
         for (;;) {
             while (next >= span_end) {   // the warp's next span
-                sp += gridDim.x * kWarps;
+                sp += gridDim.x * warps_per_sm(D, NT);
                 if (sp >= p.spans_max) {
                     done = true;
                     return;
@@ -334,7 +344,7 @@ struct Fetcher {
                 span_end = min(total, next + per);
                 if (next >= total && lane == 0) p.cuts[sp] = make_int4(-1, 0, 0, 0);
             }
-            const Segment s = segment_at<NT>(p, off, next, span_end);
+            const Segment s = segment_at<NT>(p, tb, next, span_end);
             const int begin = sp * per;
             if (next == begin && lane == 0) {   // cut: the unit has real tiles on both sides of the boundary
                 const int s0 = s.first / per, s1 = (s.first + s.tiles - 1) / per;
@@ -357,23 +367,20 @@ struct Fetcher {
             if (lane == 0) queue[queued % kQueue] = Work{s.kh, s.rb, s.L, s.n, s.qo0, t, t_end, keys, slot, {0, 0, 0}};
             ++queued;
             fresh = true;
-            // q's rows on their way to L1
-            const int row = s.rb * 8 * NT + lane / (D / 64), tok = row / p.g;
-            if (lane < 8 * NT * (D / 64) && tok < s.n)
-                prefetch_l1(p.q + static_cast<int64_t>(s.qo0 + tok) * p.q_stride + (s.kh * p.g + row - tok * p.g) * D +
-                            lane % (D / 64) * 64);
             return;
         }
     }
-    __device__ __forceinline__ void start(const Params &p, const int *off, Work *queue, int lane) {
-        sp = (static_cast<int>(blockIdx.x) - static_cast<int>(gridDim.x)) * kWarps + (threadIdx.x >> 5);
+    __device__ __forceinline__ void start(const Params &p, const Table1 &tb, Work *queue, int lane) {
+        // the warps of a block take spans far apart: what short units really cost differs along
+        // the sequence, and so evens out over an SM
+        sp = static_cast<int>((threadIdx.x >> 5) * gridDim.x + blockIdx.x) - static_cast<int>(gridDim.x) * warps_per_sm(D, NT);
         next = span_end = 0;
         queued = 0;
         done = false;
-        advance(p, off, queue, lane);
+        advance(p, tb, queue, lane);
     }
     // Copies the next tile into `stage`, completing on `bar`, and moves on.
-    __device__ __forceinline__ void fetch(const Params &p, const int *off, Work *queue, uint8_t *stage, uint64_t *bar, int lane) {
+    __device__ __forceinline__ void fetch(const Params &p, const Table1 &tb, Work *queue, uint8_t *stage, uint64_t *bar, int lane) {
         if (fresh) enter_window(p, lane);
         const int ps = shift(p), in_window = (1 << ps) - 1;
         const uint32_t bytes = quant::tile_bytes(1 << ps, D);
@@ -409,7 +416,7 @@ struct Fetcher {
         }
         if (bad) __syncwarp();
         if (++t >= t_end)
-            advance(p, off, queue, lane);
+            advance(p, tb, queue, lane);
         else if ((t & in_window) == 0)
             fresh = true;
     }
@@ -641,16 +648,12 @@ __device__ __forceinline__ void tile_step(const Params &p, State<D, NT> &st, con
     }
 }
 
-// q fragments, score factors and bounds of a segment's rows; a fresh softmax state.
+// This lane's row of q as an MMA column (row 8 n + r of the unit, dims D/4 c ...), as it lies
+// in memory.
 template <int D, int NT>
-__device__ __forceinline__ void start_segment(const Params &p, const Work &s, State<D, NT> &st, int lane) {
+__device__ __forceinline__ void load_q(const Params &p, const Work &s, int n, uint32_t (&w)[D / 8], int lane) {
     const int r = lane >> 2, c = lane & 3;
-    const float gk = p.k_scale ? p.k_scale[s.kh] : 1.f;
-#pragma unroll
-    for (int n = 0; n < NT; ++n) {
-        // this lane's row as an MMA column of q: row 8 n + r, dims D/4 c ...
         const int row = s.rb * 8 * NT + n * 8 + r, tok = row / p.g, hh = row - tok * p.g;
-        uint32_t w[D / 8];
         if (tok < s.n) {
             const uint4 *src = reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(s.qo0 + tok) * p.q_stride +
                                                                (s.kh * p.g + hh) * D + c * (D / 4));
@@ -662,6 +665,24 @@ __device__ __forceinline__ void start_segment(const Params &p, const Work &s, St
         } else {
 #pragma unroll
             for (int i = 0; i < D / 8; ++i) w[i] = 0;
+        }
+}
+
+// q fragments, score factors and bounds of a segment's rows; a fresh softmax state.  At NT =
+// 1 the rows of q are in `ahead`, loaded a tile ago.
+template <int D, int NT>
+__device__ __forceinline__ void start_segment(const Params &p, const Work &s, State<D, NT> &st, const uint32_t (&ahead)[D / 8],
+                                              int lane) {
+    const int r = lane >> 2, c = lane & 3;
+    const float gk = p.k_scale ? p.k_scale[s.kh] : 1.f;
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        uint32_t w[D / 8];
+        if (NT == 1) {
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) w[i] = ahead[i];
+        } else {
+            load_q<D, NT>(p, s, n, w, lane);
         }
         uint32_t mx = 0;
 #pragma unroll
@@ -745,7 +766,8 @@ __device__ __forceinline__ void finish_segment(const Params &p, const Work &s, S
 }
 
 template <int D, int NT, int kT>
-__global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) attend_kernel(const Params p) {
+__global__ void __launch_bounds__(warps_per_sm(D, NT) * 32, 1) attend_kernel(const Params p) {
+    constexpr int kWarps = warps_per_sm(D, NT), kThreads = kWarps * 32;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ __align__(8) uint64_t bars[kWarps * ring_stages(D, NT)];
     __shared__ long long scratch[kWarps];
@@ -762,11 +784,15 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) attend_kernel(co
     __syncwarp();
     pdl_wait();          // inputs may come from the previous kernel of the stream
     pdl_launch_next();
-    const int *off = p.off;
+    Table1 tb{p.off, nullptr};
     if (!p.off_ready) {
-        int *mine = reinterpret_cast<int *>(smem + static_cast<uint32_t>(kWarps * S) * stage_bytes);
-        build_table<NT, kThreads>(p, mine, scratch, blockIdx.x == 0);
-        off = mine;
+        uint8_t *mine = smem + static_cast<uint32_t>(kWarps * S) * stage_bytes;
+        if (p.batch <= kReqInSmem) {
+            tb.req = reinterpret_cast<Req *>(mine);
+            mine += p.batch * sizeof(Req);
+        }
+        tb.off = reinterpret_cast<int *>(mine);
+        build_table<NT, kThreads>(p, tb, scratch, blockIdx.x == 0);
     }
     if (blockIdx.x == 0 && warp < 2) {   // unusable head scales
         const float *g = warp ? p.v_scale : p.k_scale;
@@ -782,12 +808,19 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) attend_kernel(co
     int low = 0;                     // every row of the segment sees the keys below it
     Fetcher<D, NT, kT> f;
     Work *queue = queues[warp];
-    f.start(p, off, queue, lane);
+    f.start(p, tb, queue, lane);
+    uint32_t q_raw[D / 8];           // the next segment's rows of q
+    bool q_ahead = false;
+    if (NT == 1 && f.queued > 0) {
+        __syncwarp();
+        load_q<D, NT>(p, queue[0], 0, q_raw, lane);
+        q_ahead = true;
+    }
     for (;;) {
         // (one place for the copies and one for the math: the instructions of a cold start come
         // from memory too)
         while (!f.done && issued - used < S) {
-            f.fetch(p, off, queue, ring + put * stage_bytes, &bar[put], lane);
+            f.fetch(p, tb, queue, ring + put * stage_bytes, &bar[put], lane);
             put = put == S - 1 ? 0 : put + 1;
             ++issued;
         }
@@ -795,7 +828,9 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) attend_kernel(co
         if (w.t >= w.t_end) {
             __syncwarp();
             w = queue[seg++ % kQueue];
-            start_segment<D, NT>(p, w, st, lane);
+            if (NT == 1 && !q_ahead) load_q<D, NT>(p, w, 0, q_raw, lane);
+            q_ahead = false;
+            start_segment<D, NT>(p, w, st, q_raw, lane);
             low = w.L;
 #pragma unroll
             for (int n = 0; n < NT; ++n)
@@ -807,6 +842,10 @@ __global__ void __launch_bounds__(kThreads, ctas_per_sm(D, NT)) attend_kernel(co
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
         const uint8_t *stage = ring + take * stage_bytes;
+        if (NT == 1 && w.t + 1 >= w.t_end && f.queued > seg) {   // the next segment's q on its way
+            load_q<D, NT>(p, queue[seg % kQueue], 0, q_raw, lane);
+            q_ahead = true;
+        }
         const int key0 = w.t * kTile;
 #pragma unroll 1
         for (int h = 0; h < kTile / kStep; ++h) {
@@ -1111,10 +1150,12 @@ static bool make_plan(const pkv_quant_args *a, bool extend, Plan &pl) {
         pl.nt = few <= 8 ? 1 : 2;
         const int t = std::min(a->page_size, quant::kMaxTile);
         const size_t stage = static_cast<size_t>(kTile / t) * quant::tile_bytes(t, a->head_dim);
-        pl.grid = std::max(1, sm_count()) * ctas_per_sm(a->head_dim, pl.nt);
+        const int warps = warps_per_sm(a->head_dim, pl.nt);
+        pl.grid = std::max(1, sm_count());
         pl.plan_launch = a->batch > kTableInSmem;
-        pl.smem = kWarps * ring_stages(a->head_dim, pl.nt) * stage + (pl.plan_launch ? 0 : (static_cast<size_t>(a->batch) + 2) * 4);
-        int64_t spans = static_cast<int64_t>(pl.grid) * kWarps;
+        pl.smem = warps * ring_stages(a->head_dim, pl.nt) * stage;
+        if (!pl.plan_launch) pl.smem += (static_cast<size_t>(a->batch) + 2) * 4 + (a->batch <= kReqInSmem ? a->batch * sizeof(Req) : 0);
+        int64_t spans = static_cast<int64_t>(pl.grid) * warps;
         // all units' tiles, at most
         const int64_t blocks = (a->total_q * g + 8 * pl.nt - 1) / (8 * pl.nt) + a->batch;
         const int64_t tiles = blocks * a->num_kv_heads * ((std::max(1, a->max_seq_len) + kTile - 1) / kTile + kUnitCost);
@@ -1207,7 +1248,7 @@ static pkv_status launch(const char *who, const Params &p, const Plan &pl, cudaS
         st = launch_status(launch_chained(plan_kernel<NT>, dim3(1), dim3(1024), 0, s, p), who);
         if (st != PKV_OK) return st;
     }
-    st = launch_status(launch_chained(kern, dim3(pl.grid), dim3(kThreads), pl.smem, s, p), who);
+    st = launch_status(launch_chained(kern, dim3(pl.grid), dim3(warps_per_sm(D, NT) * 32), pl.smem, s, p), who);
     if (st != PKV_OK) return st;
     return launch_status(launch_chained(merge_kernel<D, NT>, dim3(pl.spans_max), dim3(kMergeThreads), 0, s, p), who);
 }
