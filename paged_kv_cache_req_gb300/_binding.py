@@ -365,29 +365,44 @@ def pkv_span_plan(seg_indptr, seg_kind, seg_start, seg_end, qo_indptr, q_pos, kv
     _check(st, "pkv_span_plan")
 
 
-def _typed(t: Optional[torch.Tensor], name: str, dtype, shape=None, device=None):
-    """t, checked: its type, row-major order, shape where given, and (with `device`) its device."""
-    if t is not None:
-        if t.dtype != dtype or not t.is_contiguous() or (shape is not None and tuple(t.shape) != tuple(shape)):
-            raise ValueError("%s must be a contiguous %s tensor%s" % (
-                name, str(dtype).replace("torch.", ""), "" if shape is None else " of shape %s" % (tuple(shape),)))
-        if device is not None and t.device != device:
-            raise ValueError("%s is on %s, the pool on %s" % (name, t.device, device))
-    return t
+_U8, _I32T, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
+
+
+def _ptr(t: Optional[torch.Tensor], name: str, dtype, shape, dev: int):
+    """Address of t (0 for None), checked: its type, row-major order, shape (None: any) and device."""
+    if t is None:
+        return 0
+    if t.dtype is not dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
+        raise ValueError("%s must be a contiguous %s tensor%s" % (
+            name, str(dtype).replace("torch.", ""), "" if shape is None else " of shape %s" % (tuple(shape),)))
+    if t.get_device() != dev:
+        raise ValueError("%s is on %s, the pool on cuda:%d" % (name, t.device, dev))
+    return t.data_ptr()
 
 
 def _quant_pool(pool, page_size, head_dim):
-    """Checks a 4-bit pool [tiles, kv heads, tile bytes] against the page size and head_dim."""
-    nbytes = int(_lib.pkv_quant_tile_bytes(int(page_size), int(head_dim)))
+    """Checks a 4-bit pool [tiles, kv heads, tile bytes] against the page size and head_dim;
+    returns its device index, address and tile stride."""
+    nbytes = _lib.pkv_quant_tile_bytes(page_size, head_dim)
     if nbytes == 0:
         raise PkvError(PKV_ERR_UNSUPPORTED, "4-bit pool", "page_size a power of two in [1, 1024], head_dim 64 or 128")
-    if pool.dim() != 3 or pool.dtype != torch.uint8 or pool.shape[2] != nbytes or pool.stride(2) != 1 or \
-            (pool.shape[1] > 1 and pool.stride(1) != nbytes):
+    if pool.dtype is not _U8 or pool.dim() != 3:
         raise ValueError("the 4-bit pool must be uint8 [tiles, kv heads, %d] with contiguous tiles" % nbytes)
-    if pool.is_cuda and pool.device.index != torch.cuda.current_device():
+    tiles, hkv, last = pool.shape
+    ts, hs, es = pool.stride()
+    if last != nbytes or es != 1 or (hkv > 1 and hs != nbytes):
+        raise ValueError("the 4-bit pool must be uint8 [tiles, kv heads, %d] with contiguous tiles" % nbytes)
+    dev = pool.get_device()
+    if dev < 0:
+        raise ValueError("libpkv takes device tensors only (got a %s tensor)" % pool.device)
+    if dev != torch.cuda.current_device():
         raise ValueError("the pool is on %s, which is not the current device" % pool.device)
     # a pool of one tile may carry any stride
-    return pool.stride(0) if pool.shape[0] > 1 else pool.shape[1] * nbytes
+    return dev, pool.data_ptr(), ts if tiles > 1 else hkv * nbytes
+
+
+def _quant_stream(stream, dev: int) -> int:
+    return torch._C._cuda_getCurrentRawStream(dev) if stream is None else stream.cuda_stream
 
 
 def pkv_quant_tile_bytes(page_size: int, head_dim: int) -> int:
@@ -397,42 +412,45 @@ def pkv_quant_tile_bytes(page_size: int, head_dim: int) -> int:
 
 def pkv_quant_store(pool, k_new, v_new, slot_mapping, err_flags, *, page_size, k_scale=None, v_scale=None, stream=None):
     """pool uint8 [tiles, Hkv, tile bytes]; k_new, v_new bf16 [n, Hkv, D], tokens any stride apart; scales fp32 [Hkv]."""
-    n, hkv, d = k_new.shape
-    ts = _quant_pool(pool, page_size, d)
-    dev = pool.device
-    for name, t in (("k_new", k_new), ("v_new", v_new)):
-        if t.dtype != torch.bfloat16 or tuple(t.shape) != (n, pool.shape[1], d) or t.stride(2) != 1 or \
-                (hkv > 1 and t.stride(1) != d) or t.device != dev:
-            raise ValueError("%s must be bf16 [n, %d, %d] on the pool's device, its rows contiguous" % (name, pool.shape[1], d))
-    _typed(slot_mapping, "slot_mapping", torch.int32, (n,), dev)
-    _typed(k_scale, "k_scale", torch.float32, (hkv,), dev)
-    _typed(v_scale, "v_scale", torch.float32, (hkv,), dev)
+    shape = k_new.shape
+    n, hkv, d = shape
+    dev, pool_ptr, ts = _quant_pool(pool, page_size, d)
+    ks, vs = k_new.stride(), v_new.stride()
+    if k_new.dtype is not _BF16 or v_new.dtype is not _BF16 or v_new.shape != shape or pool.shape[1] != hkv or \
+            ks[2] != 1 or vs[2] != 1 or (hkv > 1 and (ks[1] != d or vs[1] != d)) or \
+            k_new.get_device() != dev or v_new.get_device() != dev:
+        raise ValueError("k_new and v_new must be bf16 [n, %d, %d] on the pool's device, a token's rows contiguous" % (
+            pool.shape[1], d))
     row = hkv * d
-    st = _lib.pkv_quant_store(_p(pool), pool.shape[0], ts, hkv, d, int(page_size), _p(k_scale), _p(v_scale), _p(k_new),
-                              _p(v_new), k_new.stride(0) if n > 1 else row, v_new.stride(0) if n > 1 else row,
-                              _p(slot_mapping), n, _p(err_flags), _stream(stream))
-    _check(st, "pkv_quant_store")
+    st = _lib.pkv_quant_store(
+        pool_ptr, pool.shape[0], ts, hkv, d, page_size, _ptr(k_scale, "k_scale", _F32, (hkv,), dev),
+        _ptr(v_scale, "v_scale", _F32, (hkv,), dev), k_new.data_ptr(), v_new.data_ptr(), ks[0] if n > 1 else row,
+        vs[0] if n > 1 else row, _ptr(slot_mapping, "slot_mapping", _I32T, (n,), dev), n,
+        _ptr(err_flags, "err_flags", _I32T, None, dev), _quant_stream(stream, dev))
+    if st != PKV_OK:
+        _check(st, "pkv_quant_store")
 
 
 def pkv_quant_gather(pool, req_to_token, req_pool_idx, seq_lens, max_seq_len, k_out, v_out, cu_seqlens, err_flags, *,
                      page_size, k_scale=None, v_scale=None, kv_start=None, stream=None):
     """k_out, v_out bf16 [rows, Hkv, D] receive the requests' rows in order (see pkv_ragged_gather)."""
-    rows, hkv, d = k_out.shape
-    ts = _quant_pool(pool, page_size, d)
-    dev, B = pool.device, seq_lens.numel()
-    _typed(k_out, "k_out", torch.bfloat16, (rows, pool.shape[1], d), dev)
-    _typed(v_out, "v_out", torch.bfloat16, (rows, pool.shape[1], d), dev)
-    _typed(cu_seqlens, "cu_seqlens", torch.int32, (B + 1,), dev)
-    for name, t in (("seq_lens", seq_lens), ("req_pool_idx", req_pool_idx), ("kv_start", kv_start)):
-        _typed(t, name, torch.int32, (B,), dev)
-    _typed(req_to_token, "req_to_token", torch.int32, None, dev)
-    _typed(k_scale, "k_scale", torch.float32, (hkv,), dev)
-    _typed(v_scale, "v_scale", torch.float32, (hkv,), dev)
-    st = _lib.pkv_quant_gather(_p(pool), pool.shape[0], ts, hkv, d, int(page_size), _p(k_scale), _p(v_scale),
-                               _p(req_to_token), req_to_token.shape[0], req_to_token.stride(0), req_to_token.shape[1],
-                               _p(req_pool_idx), _p(kv_start), _p(seq_lens), B, int(max_seq_len), _p(k_out), _p(v_out),
-                               rows, _p(cu_seqlens), _p(err_flags), _stream(stream))
-    _check(st, "pkv_quant_gather")
+    shape = k_out.shape
+    rows, hkv, d = shape
+    dev, pool_ptr, ts = _quant_pool(pool, page_size, d)
+    if pool.shape[1] != hkv:
+        raise ValueError("k_out must be bf16 [rows, %d, %d]" % (pool.shape[1], d))
+    batch = seq_lens.shape
+    r2t_rows, r2t_width = req_to_token.shape
+    st = _lib.pkv_quant_gather(
+        pool_ptr, pool.shape[0], ts, hkv, d, page_size, _ptr(k_scale, "k_scale", _F32, (hkv,), dev),
+        _ptr(v_scale, "v_scale", _F32, (hkv,), dev), _ptr(req_to_token, "req_to_token", _I32T, None, dev), r2t_rows,
+        req_to_token.stride(0), r2t_width, _ptr(req_pool_idx, "req_pool_idx", _I32T, batch, dev),
+        _ptr(kv_start, "kv_start", _I32T, batch, dev), _ptr(seq_lens, "seq_lens", _I32T, batch, dev), batch[0],
+        int(max_seq_len), _ptr(k_out, "k_out", _BF16, None, dev), _ptr(v_out, "v_out", _BF16, shape, dev), rows,
+        _ptr(cu_seqlens, "cu_seqlens", _I32T, (batch[0] + 1,), dev), _ptr(err_flags, "err_flags", _I32T, None, dev),
+        _quant_stream(stream, dev))
+    if st != PKV_OK:
+        _check(st, "pkv_quant_gather")
 
 
 def make_quant_args(layout, q, pool, out, *, page_size, sm_scale, max_seq_len, k_scale=None, v_scale=None, lse=None,
@@ -442,23 +460,20 @@ def make_quant_args(layout, q, pool, out, *, page_size, sm_scale, max_seq_len, k
     """Arguments of pkv_quant_decode (no qo_indptr) or pkv_quant_extend: q bf16 [rows, Hq, D], rows any
     stride apart; pool uint8 [tiles, Hkv, tile bytes]; out bf16 [rows, Hq, D]."""
     T, hq, d = q.shape
-    ts = _quant_pool(pool, page_size, d)
-    dev, hkv = pool.device, pool.shape[1]
-    if q.dtype != torch.bfloat16 or q.stride(2) != 1 or (hq > 1 and q.stride(1) != d) or q.device != dev:
-        raise ValueError("q must be bf16 [rows, Hq, D] on the pool's device, its rows contiguous")
+    dev, _, ts = _quant_pool(pool, page_size, d)
+    hkv = pool.shape[1]
+    if q.dtype is not _BF16 or q.stride(2) != 1 or (hq > 1 and q.stride(1) != d) or q.get_device() != dev:
+        raise ValueError("q must be bf16 [rows, Hq, D] on the pool's device, a row's heads contiguous")
     B = T if qo_indptr is None else qo_indptr.numel() - 1
-    _typed(out, "out", torch.bfloat16, (T, hq, d), dev)
-    _typed(lse, "lse", torch.float32, (T, hq), dev)
-    _typed(k_scale, "k_scale", torch.float32, (hkv,), dev)
-    _typed(v_scale, "v_scale", torch.float32, (hkv,), dev)
-    for name, t, n in (("qo_indptr", qo_indptr, B + 1), ("kv_end", kv_end, T), ("kv_indptr", kv_indptr, B + 1),
-                       ("kv_last_page_len", kv_last_page_len, B), ("seq_lens", seq_lens, B),
-                       ("req_pool_idx", req_pool_idx, B), ("kv_start", kv_start, B)):
-        _typed(t, name, torch.int32, (n,), dev)
-    _typed(kv_indices, "kv_indices", torch.int32, None, dev)
-    _typed(req_to_token, "req_to_token", torch.int32, None, dev)
-    if block_table is not None:
-        _typed(block_table, "block_table", torch.int32, (B, block_table.shape[1]), dev)
+    for name, t, dtype, shape in (
+            ("out", out, _BF16, (T, hq, d)), ("lse", lse, _F32, (T, hq)), ("k_scale", k_scale, _F32, (hkv,)),
+            ("v_scale", v_scale, _F32, (hkv,)), ("qo_indptr", qo_indptr, _I32T, (B + 1,)), ("kv_end", kv_end, _I32T, (T,)),
+            ("kv_indptr", kv_indptr, _I32T, (B + 1,)), ("kv_last_page_len", kv_last_page_len, _I32T, (B,)),
+            ("seq_lens", seq_lens, _I32T, (B,)), ("req_pool_idx", req_pool_idx, _I32T, (B,)),
+            ("kv_start", kv_start, _I32T, (B,)), ("kv_indices", kv_indices, _I32T, None),
+            ("req_to_token", req_to_token, _I32T, None),
+            ("block_table", block_table, _I32T, None if block_table is None else (B, block_table.shape[1]))):
+        _ptr(t, name, dtype, shape, dev)
     a = QuantArgs()
     a.layout, a.batch = layout, B
     a.num_q_heads, a.num_kv_heads, a.head_dim = hq, hkv, d
@@ -480,6 +495,7 @@ def make_quant_args(layout, q, pool, out, *, page_size, sm_scale, max_seq_len, k
         setattr(a, name, None if t is None else _p(t).value)
     # the struct holds raw pointers: keep the tensors alive as long as it lives
     a._keep = tuple(t for _, t in tensors if t is not None)
+    a._dev = dev
     return a
 
 
@@ -492,9 +508,12 @@ def pkv_quant_extend_workspace_size(args: QuantArgs) -> int:
 
 
 def _quant_attend(fn, who, args, workspace, err_flags, stream):
-    ws_ptr = _p(workspace) if workspace is not None else None
-    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(fn(ctypes.byref(args), ws_ptr, ws_bytes, _p(err_flags), _stream(stream)), who)
+    dev = args._dev
+    if dev != torch.cuda.current_device() or workspace.get_device() != dev or err_flags.get_device() != dev:
+        raise ValueError("%s: the workspace, err_flags and the current device must be the pool's (cuda:%d)" % (who, dev))
+    st = fn(ctypes.byref(args), workspace.data_ptr(), workspace.nbytes, err_flags.data_ptr(), _quant_stream(stream, dev))
+    if st != PKV_OK:
+        _check(st, who)
 
 
 def pkv_quant_decode(args: QuantArgs, workspace: torch.Tensor, err_flags, stream=None):

@@ -1,6 +1,7 @@
 // Rows of the 4-bit pool: pkv_quant_store (quantise new K/V rows into their slots) and
 // pkv_quant_gather (read a batch's rows back as bf16).
 #include <algorithm>
+#include <type_traits>
 
 #include "quant.cuh"
 
@@ -10,13 +11,23 @@ namespace {
 
 constexpr int kThreads = 256;
 
+// 32 bytes in one access (a whole sector per thread).
+__device__ __forceinline__ void load_32(const void *p, uint32_t (&w)[8]) {
+    asm volatile("ld.global.nc.L1::no_allocate.v8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]), "=r"(w[4]), "=r"(w[5]), "=r"(w[6]), "=r"(w[7])
+                 : "l"(p));
+}
+__device__ __forceinline__ void store_32(void *p, const uint32_t (&w)[8]) {
+    asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]),
+                 "r"(w[4]), "r"(w[5]), "r"(w[6]), "r"(w[7])
+                 : "memory");
+}
+
 // 16 bf16 elements at p as 8 packed words.
 template <bool kVec>
 __device__ __forceinline__ void load_block(const uint16_t *__restrict__ p, uint32_t (&w)[8]) {
     if (kVec) {
-        const uint4 a = ld_stream_16(p), b = ld_stream_16(p + 8);
-        w[0] = a.x; w[1] = a.y; w[2] = a.z; w[3] = a.w;
-        w[4] = b.x; w[5] = b.y; w[6] = b.z; w[7] = b.w;
+        load_32(p, w);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
@@ -24,10 +35,13 @@ __device__ __forceinline__ void load_block(const uint16_t *__restrict__ p, uint3
     }
 }
 
-// One block of 16 elements: s = e4m3(amax / (6 g)), codes e2m1(x / (s g)), in fp32 with
-// IEEE division, so that a quotient on a border between two codes is decided by the tie
-// rule and not by a reciprocal's rounding.  The largest magnitude is found on the bf16
-// bits (they order like the numbers, infinities and NaN last).
+// One block of 16 elements: s = e4m3(amax / (6 g)), codes e2m1(x / (s g)) with quotients
+// rounded to nearest in fp32, so that one on a border between two codes is decided by the
+// tie rule and not by a reciprocal's rounding.  With y = RN(1 / d), q = RN(x y) and the exact
+// remainder r = x - q d, RN(q + r y) is the correctly rounded x / d as long as nothing leaves
+// the normal range (Markstein 1990): two FMAs for an element instead of a division.  The
+// largest magnitude is found on the bf16 bits (they order like the numbers, infinities and
+// NaN last).
 __device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], float g, uint32_t &scale) {
     uint32_t m = 0;
 #pragma unroll
@@ -40,46 +54,74 @@ __device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], float g, uint3
     scale = float_to_scale(__fdiv_rn(__uint_as_float(top << 16), __fmul_rn(6.f, g)));
     const float den = __fmul_rn(f16x2_to_f32(scales_to_f16(scale)).x, g);
     if (!(den > 0.f)) return make_uint2(0, 0);
-    uint32_t c[2] = {0, 0};
+    uint32_t c[8];
+    if (den > 0x1p-90f && den < 0x1p90f) {
+        // (an element below 2^-30 den has code 0 whatever its quotient's last bit)
+        const float y = __frcp_rn(den);
+        auto quotient = [&](float x) {
+            const float q = __fmul_rn(x, y);
+            return __fmaf_rn(__fmaf_rn(-q, den, x), y, q);
+        };
 #pragma unroll
-    for (int i = 0; i < 8; ++i)
-        c[i >> 2] |= pair_to_codes(__fdiv_rn(bf16_lo(w[i]), den), __fdiv_rn(bf16_hi(w[i]), den)) << (8 * (i & 3));
-    return make_uint2(c[0], c[1]);
+        for (int i = 0; i < 8; ++i) c[i] = pair_to_codes(quotient(bf16_lo(w[i])), quotient(bf16_hi(w[i])));
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) c[i] = pair_to_codes(__fdiv_rn(bf16_lo(w[i]), den), __fdiv_rn(bf16_hi(w[i]), den));
+    }
+    return make_uint2(c[0] | (c[1] << 8) | (c[2] << 16) | (c[3] << 24), c[4] | (c[5] << 8) | (c[6] << 16) | (c[7] << 24));
 }
 
-// One thread per block of 16 dims of a K or V row.
+// Both kernels give a lane one block of 16 dims and a warp 32 neighbouring blocks of one token
+// (its K rows head by head, then its V rows): 1 KB of bf16 in one run, which is where most of
+// the bytes are.  (A warp that takes the same row of 4 or 8 tokens instead has the pool's
+// codes in one run and bf16 in pieces of 128 or 256 bytes: 3 to 7 % slower.)  A token is
+// `iters` such steps; few tokens are cut into `parts` of them so that every SM has some.
+__host__ __device__ inline int row_iters(int head_dim, int hkv) { return (2 * hkv * (head_dim / kBlock) + 31) / 32; }
+inline int64_t row_parts(int64_t tokens, int iters) {
+    const int64_t want = 48ll * std::max(1, sm_count());   // warps that the device holds
+    return std::max<int64_t>(1, std::min<int64_t>(iters, want / std::max<int64_t>(1, tokens)));
+}
+
 template <int D, bool kVec>
 __global__ void __launch_bounds__(kThreads)
 store_kernel(uint8_t *__restrict__ pool, int64_t num_slots, int64_t tile_stride, int t_shift, int32_t hkv,
              const float *__restrict__ k_scale, const float *__restrict__ v_scale,
              const uint16_t *__restrict__ k_new, const uint16_t *__restrict__ v_new, int64_t k_stride,
-             int64_t v_stride, const int32_t *__restrict__ slot_mapping, int64_t blocks, int32_t *__restrict__ err) {
+             int64_t v_stride, const int32_t *__restrict__ slot_mapping, uint32_t n, uint32_t parts,
+             int32_t *__restrict__ err) {
     pdl_wait();          // inputs may come from the previous kernel of the stream
     pdl_launch_next();
     constexpr int kPerRow = D / kBlock;
-    const int64_t e = static_cast<int64_t>(blockIdx.x) * kThreads + threadIdx.x;
-    if (e >= blocks) return;
-    const int j = static_cast<int>(e % kPerRow);
-    const int64_t r = e / kPerRow;
-    const int kh = static_cast<int>(r % hkv);
-    const bool is_v = (r / hkv) & 1;
-    const int64_t i = r / hkv / 2;
+    const uint32_t item = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), i = item / parts;
+    const int part = static_cast<int>(item - i * parts), lane = threadIdx.x & 31, j = lane % kPerRow;
+    if (i >= n) return;
     const int64_t slot = slot_mapping[i];
-    if (slot < 0) return;   // padded token
-    const float *scales = is_v ? v_scale : k_scale;
-    const float g = scales ? scales[kh] : 1.f;
-    if (slot >= num_slots || !good_scale(g)) {
-        if (j == 0) raise_flag(err, PKV_DEVERR_RANGE);
+    if (slot < 0) return;   // a padded token
+    if (slot >= num_slots) {
+        if (lane == 0 && part == 0) raise_flag(err, PKV_DEVERR_RANGE);
         return;
     }
-    uint32_t w[8];
-    load_block<kVec>((is_v ? v_new + i * v_stride : k_new + i * k_stride) + static_cast<int64_t>(kh) * D + j * kBlock, w);
-    uint32_t scale;
-    const uint2 codes = quantise(w, g, scale);
     const int t = 1 << t_shift, at = static_cast<int>(slot & (t - 1));
-    uint8_t *tile = pool + (slot >> t_shift) * tile_stride + static_cast<int64_t>(kh) * tile_bytes(t, D);
-    *reinterpret_cast<uint2 *>(tile + (is_v ? t * (D / 2) : 0) + at * (D / 2) + j * 8) = codes;
-    tile[t * D + (is_v ? t * (D / kBlock) : 0) + at * (D / kBlock) + j] = static_cast<uint8_t>(scale);
+    uint8_t *tile = pool + (slot >> t_shift) * tile_stride;
+    const int iters = (2 * hkv * kPerRow + 31) / 32, each = (iters + static_cast<int>(parts) - 1) / static_cast<int>(parts);
+    const int end = min(2 * hkv, (part + 1) * each * (32 / kPerRow));
+    for (int h = part * each * (32 / kPerRow) + lane / kPerRow; h < end; h += 32 / kPerRow) {
+        const bool is_v = h >= hkv;
+        const int kh = is_v ? h - hkv : h;
+        const float *scales = is_v ? v_scale : k_scale;
+        uint32_t w[8];
+        load_block<kVec>((is_v ? v_new + i * v_stride : k_new + i * k_stride) + static_cast<int64_t>(kh) * D + j * kBlock, w);
+        const float g = scales ? __ldg(scales + kh) : 1.f;
+        if (!good_scale(g)) {
+            if (j == 0) raise_flag(err, PKV_DEVERR_RANGE);
+            continue;
+        }
+        uint32_t scale;
+        const uint2 codes = quantise(w, g, scale);
+        uint8_t *piece = tile + static_cast<int64_t>(kh) * tile_bytes(t, D);
+        *reinterpret_cast<uint2 *>(piece + (is_v ? t * (D / 2) : 0) + at * (D / 2) + j * 8) = codes;
+        piece[t * D + (is_v ? t * kPerRow : 0) + at * kPerRow + j] = static_cast<uint8_t>(scale);
+    }
 }
 
 constexpr int kGatherChunk = kThreads * 8;   // requests per step of the offset scan
@@ -118,8 +160,7 @@ __device__ __forceinline__ void write_block(uint16_t *__restrict__ dst, uint2 co
         o[i] = pack_bf16x2(c.x * s, c.y * s);
     }
     if (kVec) {
-        st_stream_16(dst, make_uint4(o[0], o[1], o[2], o[3]));
-        st_stream_16(dst + 8, make_uint4(o[4], o[5], o[6], o[7]));
+        store_32(dst, o);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -136,87 +177,106 @@ struct GatherParams {
     int32_t hkv, batch;
     const float *k_scale, *v_scale;
     const int32_t *r2t, *req_pool_idx, *kv_start, *seq_lens;
-    int64_t r2t_rows, r2t_stride, r2t_width, splits, cap;
+    int64_t r2t_rows, r2t_stride, r2t_width, cap;
+    int32_t parts;
     uint16_t *k_out, *v_out;
     int32_t *cu_seqlens, *err;
 };
 
-// Work items (request, split), dealt to a persistent grid in request order; every CTA
-// scans the lengths once for its offsets (as pkv_ragged_gather does).  A warp takes a
-// token: its lanes the blocks of 16 dims of the token's K and V rows.
-template <int D, bool kVec>
-__global__ void __launch_bounds__(kThreads) gather_kernel(const GatherParams p) {
+// The batch's tokens (and parts), in order, are dealt to the warps of a persistent grid,
+// whatever the requests' lengths; every CTA scans the lengths for the offsets (2048 requests
+// at a time, as pkv_ragged_gather does) and a warp finds its token's request in them.  The
+// writes of bf16 bound it: 3.6 times the bytes that it reads.
+constexpr int kGatherCtas = 5;   // per SM
+
+// kWhole: a warp takes two whole tokens in turn (neighbours share the sectors of their scales);
+// else one part of one.
+template <int D, bool kVec, bool kWhole>
+__global__ void __launch_bounds__(kThreads, kGatherCtas) gather_kernel(const GatherParams p) {
     pdl_wait();          // inputs may come from the previous kernel of the stream
     pdl_launch_next();
     __shared__ long long warp_sums[kThreads / 32];
-    __shared__ long long off_s[kGatherChunk];
-    constexpr int W = kThreads / 32, kPerRow = D / kBlock;
-    if (blockIdx.x == 0 && threadIdx.x == 0) p.cu_seqlens[0] = 0;
-    if (blockIdx.x == 0 && threadIdx.x < 2) {   // unusable head scales
-        const float *g = threadIdx.x ? p.v_scale : p.k_scale;
-        for (int h = 0; g && h < p.hkv; ++h)
+    __shared__ long long off_s[kGatherChunk + 1];
+    __shared__ long long row_s[kGatherChunk];   // offset of the request's first column in the table; -1: malformed
+    constexpr int kPerRow = D / kBlock;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const bool first = blockIdx.x == 0;
+    if (first && threadIdx.x == 0) p.cu_seqlens[0] = 0;
+    if (first && warp < 2) {   // unusable head scales
+        const float *g = warp ? p.v_scale : p.k_scale;
+        for (int h = lane; g && h < p.hkv; h += 32)
             if (!good_scale(g[h])) raise_flag(p.err, PKV_DEVERR_RANGE);
     }
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int t = 1 << p.t_shift;
-    const int64_t items = static_cast<int64_t>(p.batch) * p.splits;
-    int64_t w = blockIdx.x;
     long long carry = 0;
-    for (int c0 = 0; c0 < p.batch && w < items; c0 += kGatherChunk) {
-        long long n8[8], mine = 0;
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            const int j = c0 + threadIdx.x * 8 + k;
-            n8[k] = j < p.batch ? max(p.seq_lens[j], 0) : 0;
-            mine += n8[k];
+    for (int c0 = 0; c0 < p.batch; c0 += kGatherChunk) {
+        const int nreq = min(kGatherChunk, p.batch - c0);
+        const int per = (nreq + kThreads - 1) / kThreads, j0 = min(nreq, static_cast<int>(threadIdx.x) * per);
+        const int j1 = min(nreq, j0 + per);
+        long long mine = 0;
+        for (int j = j0; j < j1; ++j) {
+            const int b = c0 + j;
+            const int64_t n = p.seq_lens[b], row = p.req_pool_idx[b], s = p.kv_start ? p.kv_start[b] : 0;
+            const bool ok = n >= 0 && row >= 0 && row < p.r2t_rows && s >= 0 && s + n <= p.r2t_width;
+            if (first && !ok) raise_flag(p.err, PKV_DEVERR_RANGE);
+            row_s[j] = ok ? row * p.r2t_stride + s : -1;
+            off_s[j + 1] = max(n, static_cast<int64_t>(0));
+            mine += off_s[j + 1];
         }
         long long total = 0;
-        long long run = carry + block_scan(mine, warp_sums, &total);
-#pragma unroll
-        for (int k = 0; k < 8; ++k) {
-            off_s[threadIdx.x * 8 + k] = run;
-            run += n8[k];
-        }
-        carry += total;
-        __syncthreads();
-        for (; w < items && w / p.splits < c0 + kGatherChunk; w += gridDim.x) {
-            const int b = static_cast<int>(w / p.splits);
-            const int64_t y = w % p.splits;
-            const long long before = off_s[b - c0];
-            const int64_t row = p.req_pool_idx[b], s = p.kv_start ? p.kv_start[b] : 0;
-            int64_t L = max(p.seq_lens[b], 0);
-            const bool valid = row >= 0 && row < p.r2t_rows && s >= 0 && s + L <= p.r2t_width && p.seq_lens[b] >= 0;
-            if (y == 0 && threadIdx.x == 0) {
-                p.cu_seqlens[b + 1] = static_cast<int32_t>(before + L);
-                if (before + L > p.cap) raise_flag(p.err, PKV_DEVERR_CAPACITY);
-                if (!valid) raise_flag(p.err, PKV_DEVERR_RANGE);
+        long long run = block_scan(mine, warp_sums, &total);
+        for (int j = j0; j < j1; ++j) {   // (entry j0 belongs to the thread before)
+            run += off_s[j + 1];
+            off_s[j + 1] = run;
+            if (first) {
+                p.cu_seqlens[c0 + j + 1] = static_cast<int32_t>(carry + run);
+                if (carry + run > p.cap) raise_flag(p.err, PKV_DEVERR_CAPACITY);
             }
-            if (before + L > p.cap) L = p.cap > before ? p.cap - before : 0;
-            for (int64_t i = y * W + warp; i < L; i += p.splits * W) {
-                const int64_t o = before + i;
-                int64_t slot = valid ? __ldg(p.r2t + row * p.r2t_stride + s + i) : -1;
+        }
+        if (threadIdx.x == 0) off_s[0] = 0;
+        __syncthreads();
+        // (row numbers fit cu_seqlens' int32)
+        const int tokens = static_cast<int>(min(min(total, max(p.cap - carry, 0ll)), static_cast<long long>(INT32_MAX)));
+        const int j = lane % kPerRow, each = (row_iters(D, p.hkv) + p.parts - 1) / p.parts * (32 / kPerRow);
+        const int mine0 = blockIdx.x * (kThreads / 32) + warp, warps = gridDim.x * (kThreads / 32);
+        for (int64_t w = mine0; w < (kWhole ? (static_cast<int64_t>(tokens) + 1) / 2 : static_cast<int64_t>(tokens) * p.parts); w += warps) {
+            const int g0 = static_cast<int>(kWhole ? 2 * w : w / p.parts);
+            const int h0 = kWhole ? 0 : static_cast<int>(w - static_cast<int64_t>(g0) * p.parts) * each;
+            const int h1 = kWhole ? 2 * p.hkv : min(2 * p.hkv, h0 + each);
+            int b = 0;
+            for (int hi = nreq; hi - b > 1;) {   // the last request that starts at or before the token
+                const int mid = (b + hi) >> 1;
+                if (off_s[mid] <= g0) b = mid; else hi = mid;
+            }
+            for (int g = g0; g < (kWhole ? min(tokens, g0 + 2) : g0 + 1); ++g) {
+                while (off_s[b + 1] <= g) ++b;
+                const int64_t row = row_s[b], o = carry + g;
+                int64_t slot = row >= 0 ? __ldg(p.r2t + row + (g - off_s[b])) : -1;
                 if (slot < 0 || slot >= p.num_slots) {
-                    if (valid && lane == 0) raise_flag(p.err, PKV_DEVERR_RANGE);
+                    if (row >= 0 && lane == 0) raise_flag(p.err, PKV_DEVERR_RANGE);
                     slot = -1;
                 }
                 const int at = static_cast<int>(slot & (t - 1));
                 const uint8_t *base = p.pool + (slot < 0 ? 0 : slot >> p.t_shift) * p.tile_stride;
-                for (int e = lane; e < 2 * p.hkv * kPerRow; e += 32) {
-                    const int j = e % kPerRow, kh = (e / kPerRow) % p.hkv;
-                    const bool is_v = e >= p.hkv * kPerRow;
+                const uint8_t *code_at = base + at * (D / 2) + j * 8, *scale_at = base + t * D + at * kPerRow + j;
+#pragma unroll 4
+                for (int h = h0 + lane / kPerRow; h < h1; h += 32 / kPerRow) {
+                    const bool is_v = h >= p.hkv;
+                    const int kh = is_v ? h - p.hkv : h;
                     const float *scales = is_v ? p.v_scale : p.k_scale;
+                    const int64_t piece = static_cast<int64_t>(kh) * tile_bytes(t, D);
                     uint2 codes = make_uint2(0, 0);
                     uint32_t scale = 0;
                     if (slot >= 0) {
-                        const uint8_t *tile = base + static_cast<int64_t>(kh) * tile_bytes(t, D);
-                        codes = __ldg(reinterpret_cast<const uint2 *>(tile + (is_v ? t * (D / 2) : 0) + at * (D / 2) + j * 8));
-                        scale = __ldg(tile + t * D + (is_v ? t * kPerRow : 0) + at * kPerRow + j);
+                        codes = __ldg(reinterpret_cast<const uint2 *>(code_at + piece + (is_v ? t * (D / 2) : 0)));
+                        scale = __ldg(scale_at + piece + (is_v ? t * kPerRow : 0));
                     }
                     uint16_t *dst = (is_v ? p.v_out : p.k_out) + (o * p.hkv + kh) * D + j * kBlock;
-                    write_block<kVec>(dst, codes, scale, scales ? scales[kh] : 1.f);
+                    write_block<kVec>(dst, codes, scale, scales ? __ldg(scales + kh) : 1.f);
                 }
             }
         }
+        carry += total;
         __syncthreads();   // off_s is rewritten by the next chunk
     }
 }
@@ -239,13 +299,14 @@ template <int D>
 pkv_status launch_store(uint8_t *pool, int64_t num_slots, int64_t tile_stride, int t_shift, int32_t hkv,
                         const float *ks, const float *vs, const uint16_t *kn, const uint16_t *vn, int64_t k_stride,
                         int64_t v_stride, const int32_t *slots, int32_t n, int32_t *err, cudaStream_t s) {
-    const bool vec = aligned(kn, 16) && aligned(vn, 16) && k_stride % 8 == 0 && v_stride % 8 == 0;
-    const int64_t blocks = static_cast<int64_t>(n) * 2 * hkv * (D / kBlock);
-    const int64_t grid = (blocks + kThreads - 1) / kThreads;
-    if (grid > INT32_MAX) return fail(PKV_ERR_UNSUPPORTED, "pkv_quant_store: too many rows for one call");
+    const bool vec = aligned(kn, 32) && aligned(vn, 32) && k_stride % 16 == 0 && v_stride % 16 == 0;
+    const int64_t parts = row_parts(n, row_iters(D, hkv)), items = n * parts;
+    if (items > INT32_MAX) return fail(PKV_ERR_UNSUPPORTED, "pkv_quant_store: too many rows for one call");
+    const int64_t grid = (items + kThreads / 32 - 1) / (kThreads / 32);
     auto kern = vec ? store_kernel<D, true> : store_kernel<D, false>;
     return launch_status(launch_chained(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, pool, num_slots,
-                                        tile_stride, t_shift, hkv, ks, vs, kn, vn, k_stride, v_stride, slots, blocks, err),
+                                        tile_stride, t_shift, hkv, ks, vs, kn, vn, k_stride, v_stride, slots,
+                                        static_cast<uint32_t>(n), static_cast<uint32_t>(parts), err),
                          "pkv_quant_store");
 }
 
@@ -319,17 +380,20 @@ extern "C" pkv_status pkv_quant_gather(const void *pool, int64_t num_tiles, int6
     p.v_out = static_cast<uint16_t *>(v_out);
     p.cu_seqlens = cu_seqlens;
     p.err = err_flags;
-    // enough items for two waves of the device even for a handful of long requests
-    const int64_t sms = std::max(1, sm_count()), W = kThreads / 32;
-    const int64_t want = 2 * sms * (2048 / kThreads);
-    p.splits = (static_cast<int64_t>(max_seq_len) + W * 4 - 1) / (W * 4);
-    if (batch > 0) p.splits = std::min<int64_t>(p.splits, std::max<int64_t>(1, (want + batch - 1) / batch));
-    p.splits = std::max<int64_t>(1, p.splits);
-    const int64_t items = static_cast<int64_t>(std::max(batch, 1)) * p.splits;
-    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(items, 8 * sms));
-    const bool vec = aligned(k_out, 16) && aligned(v_out, 16);
-    auto *kern = head_dim == 128 ? (vec ? gather_kernel<128, true> : gather_kernel<128, false>)
-                                 : (vec ? gather_kernel<64, true> : gather_kernel<64, false>);
+    // as many blocks as fit at once, or as the tokens (at most batch x max_seq_len) need
+    const int64_t most = static_cast<int64_t>(batch) * max_seq_len;
+    p.parts = static_cast<int32_t>(row_parts(most, row_iters(head_dim, kv_heads)));
+    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((most * p.parts + kThreads / 32 - 1) / (kThreads / 32),
+                                                                static_cast<int64_t>(kGatherCtas) * std::max(1, sm_count())));
+    const bool vec = aligned(k_out, 32) && aligned(v_out, 32);
+    auto pick = [&](auto d, auto v) {
+        return p.parts == 1 ? gather_kernel<decltype(d)::value, decltype(v)::value, true>
+                            : gather_kernel<decltype(d)::value, decltype(v)::value, false>;
+    };
+    using D128 = std::integral_constant<int, 128>;
+    using D64 = std::integral_constant<int, 64>;
+    auto *kern = head_dim == 128 ? (vec ? pick(D128{}, std::true_type{}) : pick(D128{}, std::false_type{}))
+                                 : (vec ? pick(D64{}, std::true_type{}) : pick(D64{}, std::false_type{}));
     return launch_status(launch_chained(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0,
                                         reinterpret_cast<cudaStream_t>(stream), p),
                          "pkv_quant_gather");
