@@ -602,7 +602,7 @@ size_t pkv_quant_decode_workspace_size(const pkv_quant_args *args);
  * below its bound (kv_end, or causal over the last positions); a row with bound 0 gives
  * out = 0, lse = -inf.  The new tokens must be in the pool already (pkv_quant_store).
  * Checks and flags are pkv_extend's; more than total_kv keys raise PKV_DEVERR_CAPACITY.
- * Requests with more than 64 (row, query head) pairs per kv head have their keys and
+ * Requests with more than 128 (row, query head) pairs per kv head have their keys and
  * values copied out of the pool into the workspace as 16-bit floats first (exactly), which
  * total_kv sizes; a step of which max_q_len, or without it the average, says that there is
  * no such request needs no room for that, and computes a larger request all the same.  A

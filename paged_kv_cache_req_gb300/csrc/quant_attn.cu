@@ -51,6 +51,7 @@ constexpr float kLazy = 8.f;        // the running maximum is raised only past 2
 struct Params {
     Table tab;
     int32_t batch, hq, hkv, g, t_shift;
+    uint32_t g_magic;        // ceil(2^32 / g), for g > 1
     float scale_log2;
     int64_t total_q, tile_stride, q_stride;
     const uint16_t *q;
@@ -172,6 +173,14 @@ __device__ __forceinline__ int row_blocks(const Params &p, int n) { return (n * 
 // off[b] = first tile of request b's units, off[B] = all tiles, off[B + 1] = tiles per
 // span, by the block's threads.  The host has checked that the tiles of well-formed inputs
 // fit; row ranges that overlap could exceed that, and then no request has any.
+// Token of row r of a request and kv head: r / g, by a multiplication (for r < 2^28, which
+// the host checks, the estimate is at most one off).
+__device__ __forceinline__ int token_of(const Params &p, int r) {
+    if (p.g == 1) return r;
+    const int q = static_cast<int>(__umulhi(static_cast<uint32_t>(r), p.g_magic));
+    return q - (q * p.g > r ? 1 : 0);
+}
+
 struct Table1 {
     int *off;    // [B + 2]
     Req *req;    // [B], or nullptr: read again where needed
@@ -219,48 +228,62 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Params p) {
     build_table<NT, 1024>(p, Table1{p.off, nullptr}, scratch, true);
 }
 
-// The part of one unit that lies in one span.
-struct Segment {
+// A unit and its place in the sequence of all units' tiles.
+struct Unit {
     int64_t base;            // of the request's page list
-    int end;                 // of its tiles in the sequence of all tiles
-    int first;               // the unit's first real tile there
-    int b, kh, rb, L, n, qo0;
-    int t0, t1;              // its real tiles within the unit (t1 <= t0: none)
-    int tiles;               // real tiles of the unit
+    int b, rb, kh;
+    int L, n, qo0;           // the request's keys, query rows and first query row
+    int first, tiles;        // first real tile in the sequence; real tiles
 };
 
-template <int NT>
-__device__ __forceinline__ Segment segment_at(const Params &p, const Table1 &tb, int pos, int span_end) {
+__device__ __forceinline__ Req get_req(const Params &p, const Table1 &tb, int b) {
+    return tb.req ? tb.req[b] : load_req(p, b, false);
+}
+__device__ __forceinline__ void set_req(Unit &u, const Req &r, int b) {
+    u.b = b;
+    u.L = r.L;
+    u.n = r.n;
+    u.qo0 = r.qo0;
+    u.base = r.base;
+    u.tiles = real_tiles(r.L);
+}
+// The unit that holds tile `pos` of the sequence.
+__device__ __forceinline__ Unit find_unit(const Params &p, const Table1 &tb, int pos) {
     const int *off = tb.off;
     int lo = 0, hi = p.batch;   // the last request with off[b] <= pos (those without rows have no tiles)
     while (hi - lo > 1) {
         const int mid = (lo + hi) >> 1;
         if (off[mid] <= pos) lo = mid; else hi = mid;
     }
-    Segment s;
-    const Req r = tb.req ? tb.req[lo] : load_req(p, lo, false);
-    s.b = lo;
-    s.L = r.L;
-    s.n = r.n;
-    s.qo0 = r.qo0;
-    s.base = r.base;
-    s.tiles = real_tiles(r.L);
-    const int all = s.tiles + kUnitCost, rem = pos - off[lo], u = rem / all, at = rem - u * all;
-    s.rb = u / p.hkv;
-    s.kh = u - s.rb * p.hkv;
-    s.first = pos - at + kUnitCost;
-    s.end = min(pos - at + all, span_end);
-    s.t0 = max(at - kUnitCost, 0);
-    s.t1 = s.end - s.first;
-    return s;
+    Unit u;
+    set_req(u, get_req(p, tb, lo), lo);
+    const int all = u.tiles + kUnitCost, rem = pos - off[lo], i = rem / all;
+    u.rb = i / p.hkv;
+    u.kh = i - u.rb * p.hkv;
+    u.first = pos - (rem - i * all) + kUnitCost;
+    return u;
+}
+// The unit after u (there is one): the next kv head, row block or request.
+__device__ __forceinline__ void next_unit(const Params &p, const Table1 &tb, Unit &u) {
+    const int end = u.first + u.tiles;
+    if (end == tb.off[u.b + 1]) {
+        int b = u.b + 1;
+        while (tb.off[b + 1] == end) ++b;   // requests without rows
+        set_req(u, get_req(p, tb, b), b);
+        u.rb = u.kh = 0;
+    } else if (++u.kh == p.hkv) {
+        u.kh = 0;
+        ++u.rb;
+    }
+    u.first = end + kUnitCost;
 }
 
 // Keys that some row of the unit may see: the causal bound of its last token, or all.
 template <int NT>
-__device__ __forceinline__ int unit_keys(const Params &p, const Segment &s) {
-    if (!p.qo_indptr || p.kv_end) return s.L;
-    const int last = min(s.n, ((s.rb + 1) * 8 * NT - 1) / p.g + 1);   // tokens up to the block's last row
-    return s.L - s.n + last;
+__device__ __forceinline__ int unit_keys(const Params &p, const Unit &u) {
+    if (!p.qo_indptr || p.kv_end) return u.L;
+    const int last = min(u.n, token_of(p, (u.rb + 1) * 8 * NT - 1) + 1);   // tokens up to the block's last row
+    return u.L - u.n + last;
 }
 
 // What the math needs of a segment: a warp's queue of them lies in shared memory.
@@ -274,9 +297,9 @@ constexpr int kQueue = 8;    // segments that the copies may be ahead by (at mos
 
 // A segment without keys: zeros and -inf where it is the whole unit, else an empty partial.
 template <int D, int NT>
-__device__ __forceinline__ void write_empty(const Params &p, const Segment &s, int slot, int lane) {
+__device__ __forceinline__ void write_empty(const Params &p, const Unit &s, int slot, int lane) {
     for (int lr = 0; lr < 8 * NT; ++lr) {
-        const int row = s.rb * 8 * NT + lr, tok = row / p.g;
+        const int row = s.rb * 8 * NT + lr, tok = token_of(p, row);
         if (tok >= s.n) return;
         const int64_t at = static_cast<int64_t>(s.qo0 + tok) * p.hq + s.kh * p.g + (row - tok * p.g);
         if (slot < 0) {
@@ -295,9 +318,9 @@ __device__ __forceinline__ void write_empty(const Params &p, const Segment &s, i
 // needed: the next window's with a window, a new segment's one tile ahead.
 template <int D, int NT, int kT>
 struct Fetcher {
-    int64_t base;            // of the request's page list
+    Unit u;
     int sp, span_end, next;  // the span; tiles of all units: its end, the next segment's start
-    int kh, t, t_end, keys;  // next tile of the unit; end of those with keys; unit_keys
+    int t, t_end, keys;      // next tile of the unit; end of those with keys; unit_keys
     bool done, fresh, bad;   // no tile left; the window is not entered yet; a piece of it lies on a bad page
     const uint8_t *src[2];   // pieces 64 w + lane, + 32 of the window; nullptr: past the keys, or a bad page
     int nxt[2];              // slots of the next window's
@@ -310,13 +333,13 @@ struct Fetcher {
         for (int i = 0; i < 2; ++i) {
             const int64_t key = static_cast<int64_t>(window * 64 + 32 * i + lane) << shift(p);
             nxt[i] = key < keys && key < static_cast<int64_t>(t_end) * kTile
-                         ? static_cast<int>(quant::slot_of(p.tab, base, static_cast<int>(key)))
+                         ? static_cast<int>(quant::slot_of(p.tab, u.base, static_cast<int>(key)))
                          : -3;
         }
     }
     // the looked-up window becomes the current one
     __device__ __forceinline__ void enter_window(const Params &p, int lane) {
-        const int64_t head = static_cast<int64_t>(kh) * quant::tile_bytes(1 << p.t_shift, D);
+        const int64_t head = static_cast<int64_t>(u.kh) * quant::tile_bytes(1 << p.t_shift, D);
         int flags = 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
@@ -331,40 +354,48 @@ struct Fetcher {
     }
     // To the next segment that has keys.
     __device__ __forceinline__ void advance(const Params &p, const Table1 &tb, Work *queue, int lane) {
-        const int total = tb.off[p.batch], per = tb.off[p.batch + 1];
         for (;;) {
-            while (next >= span_end) {   // the warp's next span
-                sp += gridDim.x * warps_per_sm(D, NT);
-                if (sp >= p.spans_max) {
-                    done = true;
-                    return;
+            if (next < span_end) {
+                next_unit(p, tb, u);
+            } else {   // the warp's next span
+                const int total = tb.off[p.batch], per = tb.off[p.batch + 1];
+                for (;;) {
+                    sp += gridDim.x * warps_per_sm(D, NT);
+                    if (sp >= p.spans_max) {
+                        done = true;
+                        return;
+                    }
+                    // (sp * per stays below total + spans_max * per: checked to fit on the host)
+                    next = sp * per;
+                    if (next < total) break;
+                    if (lane == 0) p.cuts[sp] = make_int4(-1, 0, 0, 0);
                 }
-                // (sp * per stays below total + spans_max * per: checked to fit on the host)
-                next = sp * per;
                 span_end = min(total, next + per);
-                if (next >= total && lane == 0) p.cuts[sp] = make_int4(-1, 0, 0, 0);
+                u = find_unit(p, tb, next);
+                if (lane == 0) {   // cut: the unit has real tiles on both sides of the boundary
+                    int4 cut = make_int4(-1, 0, 0, 0);
+                    if (u.first < next) {
+                        const int s0 = u.first / per, s1 = (u.first + u.tiles - 1) / per;
+                        cut = make_int4(u.b, u.rb * p.hkv + u.kh, (sp - s0) * 2 + (u.first > s0 * per ? 1 : 0), s1 - sp);
+                    }
+                    p.cuts[sp] = cut;
+                }
             }
-            const Segment s = segment_at<NT>(p, tb, next, span_end);
-            const int begin = sp * per;
-            if (next == begin && lane == 0) {   // cut: the unit has real tiles on both sides of the boundary
-                const int s0 = s.first / per, s1 = (s.first + s.tiles - 1) / per;
-                p.cuts[sp] = s.t0 ? make_int4(s.b, s.rb * p.hkv + s.kh, (sp - s0) * 2 + (s.first > s0 * per ? 1 : 0), s1 - sp)
-                                  : make_int4(-1, 0, 0, 0);
-            }
-            next = s.end;
-            if (s.t0 >= s.t1) continue;
-            const int slot = s.t0 == 0 && s.t1 == s.tiles ? -1 : sp * 2 + (s.t0 == 0 && s.first > begin ? 1 : 0);
-            base = s.base;
-            kh = s.kh;
-            keys = unit_keys<NT>(p, s);
-            t = s.t0;
-            t_end = min(s.t1, (keys + kTile - 1) / kTile);
+            const int begin = span_end - u.first;   // (tiles of the unit before the span's end)
+            const int t0 = max(next - u.first, 0), t1 = min(u.tiles, begin);
+            const bool starts_inside = t0 == 0 && next < u.first;
+            next = min(u.first + u.tiles, span_end);
+            if (t0 >= t1) continue;
+            const int slot = t0 == 0 && t1 == u.tiles ? -1 : sp * 2 + (starts_inside ? 1 : 0);
+            keys = unit_keys<NT>(p, u);
+            t = t0;
+            t_end = min(t1, (keys + kTile - 1) / kTile);
             if (t >= t_end) {
-                write_empty<D, NT>(p, s, slot, lane);
+                write_empty<D, NT>(p, u, slot, lane);
                 continue;
             }
             look_up(p, t >> shift(p), lane);
-            if (lane == 0) queue[queued % kQueue] = Work{s.kh, s.rb, s.L, s.n, s.qo0, t, t_end, keys, slot, {0, 0, 0}};
+            if (lane == 0) queue[queued % kQueue] = Work{u.kh, u.rb, u.L, u.n, u.qo0, t, t_end, keys, slot, {0, 0, 0}};
             ++queued;
             fresh = true;
             return;
@@ -653,7 +684,7 @@ __device__ __forceinline__ void tile_step(const Params &p, State<D, NT> &st, con
 template <int D, int NT>
 __device__ __forceinline__ void load_q(const Params &p, const Work &s, int n, uint32_t (&w)[D / 8], int lane) {
     const int r = lane >> 2, c = lane & 3;
-        const int row = s.rb * 8 * NT + n * 8 + r, tok = row / p.g, hh = row - tok * p.g;
+        const int row = s.rb * 8 * NT + n * 8 + r, tok = token_of(p, row), hh = row - tok * p.g;
         if (tok < s.n) {
             const uint4 *src = reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(s.qo0 + tok) * p.q_stride +
                                                                (s.kh * p.g + hh) * D + c * (D / 4));
@@ -706,7 +737,7 @@ __device__ __forceinline__ void start_segment(const Params &p, const Work &s, St
             const int ev = __shfl_sync(0xffffffffu, e, (2 * c + v) * 4);
             // kept normal and finite, so that -inf (a masked key) stays -inf and 0 stays 0
             st.f[n][v] = fminf(fmaxf(p.scale_log2 * gk * __int_as_float((127 - ev) << 23), 1.2e-38f), 3.4e38f);
-            const int rv = s.rb * 8 * NT + n * 8 + 2 * c + v, tv = rv / p.g;
+            const int rv = s.rb * 8 * NT + n * 8 + 2 * c + v, tv = token_of(p, rv);
             int end = s.L;   // rows past the last (zeros, never written) ask for no masking
             if (tv < s.n) {
                 end = !p.qo_indptr ? s.L : p.kv_end ? __ldg(p.kv_end + s.qo0 + tv) : s.L - s.n + tv + 1;
@@ -743,7 +774,7 @@ __device__ __forceinline__ void finish_segment(const Params &p, const Work &s, S
             float l = st.l[n][v];
 #pragma unroll
             for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            const int lr = n * 8 + 2 * c + v, row = s.rb * 8 * NT + lr, tok = row / p.g, hh = row - tok * p.g;
+            const int lr = n * 8 + 2 * c + v, row = s.rb * 8 * NT + lr, tok = token_of(p, row), hh = row - tok * p.g;
             if (tok >= s.n) continue;
             if (whole) {
                 const int64_t at = static_cast<int64_t>(s.qo0 + tok) * p.hq + s.kh * p.g + hh;
@@ -927,7 +958,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
             o.w = o.w * c0 + x.w * c1;
         }
         if (sub || !live) continue;
-        const int row = rb * 8 * NT + lr, tok = row / p.g;
+        const int row = rb * 8 * NT + lr, tok = token_of(p, row);
         const int64_t at = static_cast<int64_t>(qo0 + tok) * p.hq + kh * p.g + (row - tok * p.g);
         const float inv = l == 0.f ? 0.f : gv / l;
         *reinterpret_cast<uint2 *>(p.out + at * D + d0) =
@@ -1103,7 +1134,7 @@ static pkv_status validate(const char *who, const pkv_quant_args *a, bool extend
 
 // How a call runs: the span kernel (its rows per unit, grid, spans), and for requests with
 // many query rows the held path; with the workspace of each.
-constexpr int kHeldRows = 64;   // rows per request and kv head up to which the span kernel is used
+constexpr int kHeldRows = 128;   // rows per request and kv head up to which the span kernel is used
 
 struct Plan {
     bool spans, held, plan_launch;
@@ -1128,6 +1159,16 @@ static pkv_extend_args extend_args(const pkv_quant_args *a) {
     e.sm_scale = a->sm_scale;
     e.max_seq_len = a->max_seq_len;
     e.kv_chunk = a->kv_chunk;
+    if (e.kv_chunk == 0) {
+        // keys are split only when the blocks of 128 rows leave SMs idle: a split block writes
+        // and reads back its fp32 rows (8192 rows over 16384 keys: 2140 us in pieces of 4096 keys,
+        // 1170 us whole)
+        const int g = 1 << ilog2(a->num_q_heads / a->num_kv_heads);
+        const int64_t blocks = a->num_kv_heads * std::max<int64_t>(1, std::max<int64_t>(a->batch, a->total_q * g / 128));
+        const int64_t pieces = std::max<int64_t>(1, 2ll * std::max(1, sm_count()) / blocks), L = std::max(1, a->max_seq_len);
+        e.kv_chunk = static_cast<int32_t>(std::min<int64_t>((std::max<int64_t>(512, (L + pieces - 1) / pieces) + 127) / 128 * 128,
+                                                            INT32_MAX / 128 * 128));
+    }
     e.total_q = a->total_q;
     e.q = a->q;
     e.qo_indptr = a->qo_indptr;
@@ -1215,6 +1256,7 @@ static Params params(const pkv_quant_args *a, int32_t *err) {
     p.hq = a->num_q_heads;
     p.hkv = a->num_kv_heads;
     p.g = a->num_q_heads / a->num_kv_heads;
+    p.g_magic = static_cast<uint32_t>(((1ull << 32) + p.g - 1) / p.g);
     p.scale_log2 = a->sm_scale * kLog2e;
     p.total_q = a->total_q;
     p.tile_stride = a->tile_stride;
@@ -1297,7 +1339,7 @@ static pkv_status attend(const char *who, const pkv_quant_args *a, bool extend, 
     if (ws_bytes < need) return fail(PKV_ERR_CAPACITY, "%s: workspace of %zu bytes, %zu needed", who, ws_bytes, need);
     if (!ws || !aligned(ws, 256))
         return fail(PKV_ERR_INVALID_ARG, "%s: workspace must be non-null and 256-byte aligned", who);
-    if (a->total_q * a->num_q_heads > INT32_MAX) return fail(PKV_ERR_UNSUPPORTED, "%s: too many query rows", who);
+    if (a->total_q * a->num_q_heads >= 1 << 28) return fail(PKV_ERR_UNSUPPORTED, "%s: too many query rows", who);
     Params p = params(a, err);
     p.wait_ns = wait_limit_ns();
     char *at = static_cast<char *>(ws);
