@@ -122,20 +122,22 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                  "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
 }
-// Bounded wait; the polls suspend the warp for up to 2 us each, so that warps that wait
-// leave the issue slots to those that compute.
+// Bounded wait: false once `limit_ns` have passed.  The first poll returns at once, so that a
+// limit of some nanoseconds means what it says; the later ones suspend the warp for a
+// while (the time is looked at after the first of them and then after every 64).
 __device__ __forceinline__ bool wait_for(uint64_t *bar, uint32_t parity, uint64_t limit_ns) {
-    if (mbar_try_wait(bar, parity)) return true;
+    uint32_t ok;
+    asm volatile(
+        "{\n .reg .pred p;\n mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n selp.u32 %0, 1, 0, p;\n}\n"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    if (ok) return true;
+    if (limit_ns < 1000) return false;
     const uint64_t t0 = global_ns();
-    for (;;) {
-        uint32_t ok;
-        asm volatile(
-            "{\n .reg .pred p;\n mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n selp.u32 %0, 1, 0, p;\n}\n"
-            : "=r"(ok)
-            : "r"(smem_u32(bar)), "r"(parity), "r"(2000)
-            : "memory");
-        if (ok) return true;
-        if (global_ns() - t0 > limit_ns) return false;
+    for (uint32_t i = 1;; ++i) {
+        if (mbar_try_wait(bar, parity)) return true;
+        if ((i & 63) == 1 && global_ns() - t0 > limit_ns) return false;
     }
 }
 
@@ -895,7 +897,11 @@ __global__ void __launch_bounds__(warps_per_sm(D, NT) * 32, 1) attend_kernel(con
         __syncwarp();
     }
     if (!ok) {   // a wait ran out: the copies in flight land before the block's memory is given back
-        if (lane == 0) raise_flag(p.err, PKV_DEVERR_TIMEOUT);
+        if (lane == 0) {
+            raise_flag(p.err, PKV_DEVERR_TIMEOUT);
+            // merge_kernel reads the record of every span, this warp's later ones too
+            for (int sp = f.sp + gridDim.x * kWarps; sp < p.spans_max; sp += gridDim.x * kWarps) p.cuts[sp] = make_int4(-1, 0, 0, 0);
+        }
         for (; used < issued; ++used) mbar_wait(&bar[used % S], (used / S) & 1);
     }
 }

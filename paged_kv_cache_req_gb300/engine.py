@@ -28,6 +28,12 @@ runs either through its own page list ("paged": the page-aligned encoder of
 "Approach 1") or through pkv_ragged_gather into a contiguous varlen buffer
 followed by a varlen decode ("gather": "Approach 2").
 
+With ``quant=True`` (GQA) the K/V pool is held in 4 bits (see pkv_quant_store): the
+given bf16 pools are quantised once, and the step's calls are their 4-bit forms
+(pkv_quant_store, pkv_quant_decode or pkv_quant_extend, and pkv_quant_gather before a
+contiguous cross-attention).  ``scales`` are the heads' fp32 (k_scale, v_scale), by
+default each head's largest magnitude in the pools / 2688.
+
 Nothing here computes: every step runs in libpkv's kernels.
 """
 from __future__ import annotations
@@ -69,14 +75,45 @@ def _pack(owners, device):
     return buf
 
 
+class _QuantPool:
+    """A 4-bit pool with its head scales, filled from bf16 pools [slots, Hkv, D]."""
+
+    def __init__(self, k_pool, v_pool, page_size, err, scales=None):
+        slots, hkv, d = k_pool.shape
+        tile = min(page_size, 64)
+        if slots % tile:
+            raise ValueError("the pool's slots must be whole pages")
+        dev = k_pool.device
+        if scales is None:
+            # the largest code (6) x the largest block scale (448) is the head's largest magnitude
+            scales = [(p.abs().amax(dim=(0, 2)).float() / 2688.0).clamp_(min=1e-30) for p in (k_pool, v_pool)]
+        self.page_size = page_size
+        self.k_scale, self.v_scale = (x.to(dev) for x in scales)
+        self.pool = torch.zeros((slots // tile, hkv, B.pkv_quant_tile_bytes(page_size, d)), dtype=torch.uint8, device=dev)
+        step = 1 << 20
+        for i in range(0, slots, step):
+            n = min(step, slots - i)
+            self.store(k_pool[i:i + n], v_pool[i:i + n], torch.arange(i, i + n, dtype=torch.int32, device=dev), err)
+
+    def store(self, k_new, v_new, slot_mapping, err):
+        B.pkv_quant_store(self.pool, k_new, v_new, slot_mapping, err, page_size=self.page_size, k_scale=self.k_scale,
+                          v_scale=self.v_scale)
+
+    def args(self, layout, q, out, **kw):
+        return B.make_quant_args(layout, q, self.pool, out, page_size=self.page_size, k_scale=self.k_scale,
+                                 v_scale=self.v_scale, **kw)
+
+
 class DecodeStep:
     def __init__(self, wl: Workload, device="cuda", cross_mode: str = "paged", kv_chunk: int = 0,
                  pools=None, values: Optional[Dict[str, torch.Tensor]] = None, seed: Optional[int] = None,
-                 alloc: bool = False, fused: bool = False):
+                 alloc: bool = False, fused: bool = False, quant: bool = False, scales=None):
         if cross_mode not in ("paged", "gather"):
             raise ValueError(cross_mode)
         if fused and wl.kind != "gqa":
             raise ValueError("the token-table layout and the fused store are GQA only")
+        if quant and wl.kind != "gqa":
+            raise ValueError("the 4-bit pool is GQA only")
         self.fused = bool(fused)
         self.wl = wl
         self.device = torch.device(device)
@@ -91,6 +128,7 @@ class DecodeStep:
         self.k_pool, self.v_pool = pools
         vals = make_values(wl, seed=seed) if values is None else values
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.quant = _QuantPool(self.k_pool, self.v_pool, ps, self.err, scales) if quant else None
         Bn = wl.batch
         self.k_new = vals["k_new"].to(dev)
         self.v_new = vals["v_new"].to(dev) if vals["v_new"] is not None else None
@@ -132,6 +170,16 @@ class DecodeStep:
                 pb.args = B.make_decode_args(B.PKV_KIND_GQA, layout, pb.q, pb.k_rag, pb.v_rag, pb.out,
                                              sm_scale=wl.sm_scale, max_seq_len=pb.max_len,
                                              cu_seqlens=pb.cu, lse=pb.lse, kv_chunk=self.kv_chunk)
+            elif self.quant is not None:
+                kw = dict(sm_scale=wl.sm_scale, max_seq_len=pb.max_len, lse=pb.lse, kv_chunk=self.kv_chunk)
+                if self.fused:
+                    pb.args = self.quant.args(B.PKV_LAYOUT_REQ_TO_TOKEN, pb.q, pb.out, seq_lens=pb.seq_lens,
+                                              req_to_token=self.r2t, req_pool_idx=self.req_pool_idx,
+                                              kv_start=pb.kv_start, **kw)
+                else:
+                    self._page_lists(pb, max_pages)
+                    pb.args = self.quant.args(B.PKV_LAYOUT_CSR, pb.q, pb.out, kv_indptr=pb.kv_indptr,
+                                              kv_indices=pb.kv_indices, kv_last_page_len=pb.kv_last, **kw)
             elif self.fused:
                 # pages straight from req_to_token; the problem that stores writes its new rows itself
                 kn, vn = (self.k_new, self.v_new) if p.stores else (None, None)
@@ -148,16 +196,22 @@ class DecodeStep:
                                              head_dim_v=wl.head_dim_v, block_table=pb.block_table,
                                              seq_lens=pb.seq_lens, lse=pb.lse, kv_chunk=self.kv_chunk)
             else:
-                pb.kv_indptr = torch.empty(Bn + 1, dtype=torch.int32, device=dev)
-                pb.kv_indices = torch.empty(max(Bn * max_pages, 1), dtype=torch.int32, device=dev)
-                pb.kv_last = torch.empty(Bn, dtype=torch.int32, device=dev)
+                self._page_lists(pb, max_pages)
                 pb.args = B.make_decode_args(B.PKV_KIND_GQA, B.PKV_LAYOUT_CSR, pb.q, self.k_pool, self.v_pool,
                                              pb.out, page_size=ps, sm_scale=wl.sm_scale, max_seq_len=pb.max_len,
                                              kv_indptr=pb.kv_indptr, kv_indices=pb.kv_indices,
                                              kv_last_page_len=pb.kv_last, lse=pb.lse, kv_chunk=self.kv_chunk)
-            nbytes = B.pkv_decode_workspace_size(pb.args)
+            pb.quant = isinstance(pb.args, B.QuantArgs)
+            nbytes = (B.pkv_quant_decode_workspace_size if pb.quant else B.pkv_decode_workspace_size)(pb.args)
             pb.ws_bytes = nbytes
             pb.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
+
+    def _page_lists(self, pb, max_pages):
+        """Buffers of a problem's CSR page lists."""
+        dev, Bn = self.device, self.wl.batch
+        pb.kv_indptr = torch.empty(Bn + 1, dtype=torch.int32, device=dev)
+        pb.kv_indices = torch.empty(max(Bn * max_pages, 1), dtype=torch.int32, device=dev)
+        pb.kv_last = torch.empty(Bn, dtype=torch.int32, device=dev)
 
     def _setup_alloc(self, seed):
         """Free list = the pool pages no cached position uses (page 0 is padding), in a
@@ -221,18 +275,26 @@ class DecodeStep:
 
     def store(self, name: str = "self"):
         pb = self.problems[name]
+        if self.quant is not None:
+            self.quant.store(self.k_new, self.v_new, pb.slot_mapping, self.err)
+            return
         if self.fused and not pb.gather:
             return                                   # the decode call stores the new rows itself
         B.pkv_store(self.k_pool, self.v_pool, self.k_new, self.v_new, pb.slot_mapping, self.err)
 
     def gather(self, name: str):
         pb = self.problems[name]
+        if self.quant is not None:
+            B.pkv_quant_gather(self.quant.pool, self.r2t, self.req_pool_idx, pb.seq_lens, pb.max_len, pb.k_rag, pb.v_rag,
+                               pb.cu, self.err, page_size=self.quant.page_size, k_scale=self.quant.k_scale,
+                               v_scale=self.quant.v_scale, kv_start=pb.kv_start)
+            return
         B.pkv_ragged_gather(self.k_pool, self.v_pool, self.r2t, self.req_pool_idx, pb.seq_lens, pb.max_len,
                             pb.k_rag, pb.v_rag, pb.cu, self.err, kv_start=pb.kv_start)
 
     def decode(self, name: str):
         pb = self.problems[name]
-        B.pkv_decode(pb.args, pb.workspace, self.err)
+        (B.pkv_quant_decode if pb.quant else B.pkv_decode)(pb.args, pb.workspace, self.err)
 
     def run(self):
         """One decode step: (allocation), then for each problem page lists, (store), (gather), attention."""
@@ -253,8 +315,10 @@ class DecodeStep:
         for pb in self.problems.values():
             if not self.fused or pb.gather:
                 n += 1                               # gather or build_indices
+            if not self.fused or pb.gather or self.quant is not None:
                 n += 1 if pb.spec.stores else 0      # store
             n += 1 + (1 if pb.ws_bytes > 0 else 0)   # split kernel (+ merge when requests can split)
+            n += 1 if pb.quant and self.wl.batch > 1024 else 0   # (the tile table of a large batch)
         return n
 
     def check_errors(self) -> int:
@@ -287,10 +351,12 @@ class ExtendStep:
         pkv_extend          attention of every query row over its visible keys
 
     With ``token_table=True`` pkv_extend reads the pages straight from req_to_token
-    (PKV_LAYOUT_REQ_TO_TOKEN) and the step has no pkv_build_indices launch.
+    (PKV_LAYOUT_REQ_TO_TOKEN) and the step has no pkv_build_indices launch.  With
+    ``quant=True`` the pool is held in 4 bits (pkv_quant_store, pkv_quant_extend).
     """
 
-    def __init__(self, ew, device="cuda", kv_chunk: int = 0, seed: Optional[int] = None, token_table: bool = False):
+    def __init__(self, ew, device="cuda", kv_chunk: int = 0, seed: Optional[int] = None, token_table: bool = False,
+                 quant: bool = False, scales=None):
         self.token_table = bool(token_table)
         self.ew = ew
         dev = self.device = torch.device(device)
@@ -349,7 +415,18 @@ class ExtendStep:
         self.in_buf = _pack(ins, dev)
         if self.kv_end is not None:
             self.seg = [getattr(self._seg_holder, "s%d" % i) for i in range(len(self.seg))]
-        if self.token_table:
+        self.quant = _QuantPool(self.k_pool, self.v_pool, ps, self.err, scales) if quant else None
+        if self.quant is not None:
+            kw = dict(sm_scale=ew.sm_scale, max_seq_len=int(ew.seq_lens.max()), kv_end=self.kv_end, lse=self.lse,
+                      qo_indptr=self.qo_indptr, kv_chunk=kv_chunk, total_kv=int(ew.seq_lens.sum()),
+                      max_q_len=int(ew.qo_lens.max()))
+            if self.token_table:
+                self.args = self.quant.args(B.PKV_LAYOUT_REQ_TO_TOKEN, self.q, self.out, seq_lens=self.seq_lens,
+                                            req_to_token=self.r2t, req_pool_idx=self.req_pool_idx, **kw)
+            else:
+                self.args = self.quant.args(B.PKV_LAYOUT_CSR, self.q, self.out, kv_indptr=self.kv_indptr,
+                                            kv_indices=self.kv_indices, kv_last_page_len=self.kv_last, **kw)
+        elif self.token_table:
             self.args = B.make_extend_args(B.PKV_LAYOUT_REQ_TO_TOKEN, self.q, self.k_pool, self.v_pool, self.out,
                                            self.qo_indptr, page_size=ps, sm_scale=ew.sm_scale,
                                            max_seq_len=int(ew.seq_lens.max()), kv_end=self.kv_end,
@@ -360,7 +437,7 @@ class ExtendStep:
                                            page_size=ps, sm_scale=ew.sm_scale, max_seq_len=int(ew.seq_lens.max()),
                                            kv_end=self.kv_end, kv_indptr=self.kv_indptr, kv_indices=self.kv_indices,
                                            kv_last_page_len=self.kv_last, lse=self.lse, kv_chunk=kv_chunk)
-        self.ws_bytes = B.pkv_extend_workspace_size(self.args)
+        self.ws_bytes = (B.pkv_quant_extend_workspace_size if quant else B.pkv_extend_workspace_size)(self.args)
         self.workspace = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=dev)
 
     def build_indices(self):
@@ -371,6 +448,9 @@ class ExtendStep:
                             kv_indptr=self.kv_indptr, kv_indices=self.kv_indices, kv_last_page_len=self.kv_last)
 
     def store(self):
+        if self.quant is not None:
+            self.quant.store(self.k_new, self.v_new, self.slot_mapping, self.err)
+            return
         B.pkv_store(self.k_pool, self.v_pool, self.k_new, self.v_new, self.slot_mapping, self.err)
 
     def plan(self):
@@ -378,7 +458,7 @@ class ExtendStep:
             B.pkv_span_plan(*self.seg, self.plan_qo, self.q_pos, self.kv_end, self.err)
 
     def attend(self):
-        B.pkv_extend(self.args, self.workspace, self.err)
+        (B.pkv_extend if self.quant is None else B.pkv_quant_extend)(self.args, self.workspace, self.err)
 
     def run(self):
         self.build_indices()
@@ -387,6 +467,13 @@ class ExtendStep:
         self.attend()
 
     def launches_per_step(self) -> int:
+        if self.quant is not None:
+            # spans and their merge; with many rows the copy out of the pool and its attention besides
+            # (alone for one request)
+            held = int(self.ew.qo_lens.max()) * (self.ew.num_q_heads // self.ew.num_kv_heads) > 128
+            n = 2 if not held or self.ew.batch > 1 else 0
+            n += 2 if held else 0
+            return n + (1 if self.token_table else 2) + (1 if self.kv_end is not None else 0)
         return (2 if self.token_table else 3) + (1 if self.kv_end is not None else 0) + (1 if self.ws_bytes > 0 else 0)
 
     def check_errors(self) -> int:

@@ -253,8 +253,8 @@ def extend(B, cache, q, rows, layout="table", kv_end=None, **kw):
     out = torch.full(q.shape, 3.0, dtype=torch.bfloat16, device=DEV)
     lse = torch.full(q.shape[:2], 3.0, dtype=torch.float32, device=DEV)
     err = err_word()
-    a = cache.args(B, layout, q, out, lse=lse, qo_indptr=up(np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)),
-                   kv_end=None if kv_end is None else up(np.asarray(kv_end, dtype=np.int32)), **kw)
+    kw.setdefault("qo_indptr", up(np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)))
+    a = cache.args(B, layout, q, out, lse=lse, kv_end=None if kv_end is None else up(np.asarray(kv_end, dtype=np.int32)), **kw)
     ws = torch.full((B.pkv_quant_extend_workspace_size(a),), 0xFF, dtype=torch.uint8, device=DEV)
     B.pkv_quant_extend(a, ws, err)
     return out, lse, err.item()
