@@ -366,13 +366,15 @@ def pkv_span_plan(seg_indptr, seg_kind, seg_start, seg_end, qo_indptr, q_pos, kv
 
 
 _U8, _I32T, _F32, _BF16 = torch.uint8, torch.int32, torch.float32, torch.bfloat16
+_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+_TILE_BYTES = {}   # (page size, head_dim) -> bytes of one kv head's piece of a tile
 
 
 def _ptr(t: Optional[torch.Tensor], name: str, dtype, shape, dev: int):
     """Address of t (0 for None), checked: its type, row-major order, shape (None: any) and device."""
     if t is None:
         return 0
-    if t.dtype is not dtype or not t.is_contiguous() or (shape is not None and t.shape != shape):
+    if t.dtype is not dtype or (shape is not None and t.shape != shape) or not t.is_contiguous():
         raise ValueError("%s must be a contiguous %s tensor%s" % (
             name, str(dtype).replace("torch.", ""), "" if shape is None else " of shape %s" % (tuple(shape),)))
     if t.get_device() != dev:
@@ -382,23 +384,25 @@ def _ptr(t: Optional[torch.Tensor], name: str, dtype, shape, dev: int):
 
 def _quant_pool(pool, page_size, head_dim):
     """Checks a 4-bit pool [tiles, kv heads, tile bytes] against the page size and head_dim;
-    returns its device index, address and tile stride."""
-    nbytes = _lib.pkv_quant_tile_bytes(page_size, head_dim)
-    if nbytes == 0:
-        raise PkvError(PKV_ERR_UNSUPPORTED, "4-bit pool", "page_size a power of two in [1, 1024], head_dim 64 or 128")
-    if pool.dtype is not _U8 or pool.dim() != 3:
-        raise ValueError("the 4-bit pool must be uint8 [tiles, kv heads, %d] with contiguous tiles" % nbytes)
-    tiles, hkv, last = pool.shape
-    ts, hs, es = pool.stride()
-    if last != nbytes or es != 1 or (hkv > 1 and hs != nbytes):
+    returns its device index, address, tiles, kv heads and tile stride."""
+    nbytes = _TILE_BYTES.get((page_size, head_dim))
+    if nbytes is None:
+        nbytes = _lib.pkv_quant_tile_bytes(page_size, head_dim)
+        if nbytes == 0:
+            raise PkvError(PKV_ERR_UNSUPPORTED, "4-bit pool",
+                           "page_size a power of two in [1, 1024], head_dim 64 or 128")
+        _TILE_BYTES[page_size, head_dim] = nbytes
+    shape, stride = pool.shape, pool.stride()
+    if len(shape) != 3 or pool.dtype is not _U8 or shape[2] != nbytes or stride[2] != 1 or \
+            (shape[1] > 1 and stride[1] != nbytes):
         raise ValueError("the 4-bit pool must be uint8 [tiles, kv heads, %d] with contiguous tiles" % nbytes)
     dev = pool.get_device()
     if dev < 0:
         raise ValueError("libpkv takes device tensors only (got a %s tensor)" % pool.device)
-    if dev != torch.cuda.current_device():
+    if dev != _device():
         raise ValueError("the pool is on %s, which is not the current device" % pool.device)
     # a pool of one tile may carry any stride
-    return dev, pool.data_ptr(), ts if tiles > 1 else hkv * nbytes
+    return dev, pool.data_ptr(), shape[0], shape[1], stride[0] if shape[0] > 1 else shape[1] * nbytes
 
 
 def _quant_stream(stream, dev: int) -> int:
@@ -414,16 +418,15 @@ def pkv_quant_store(pool, k_new, v_new, slot_mapping, err_flags, *, page_size, k
     """pool uint8 [tiles, Hkv, tile bytes]; k_new, v_new bf16 [n, Hkv, D], tokens any stride apart; scales fp32 [Hkv]."""
     shape = k_new.shape
     n, hkv, d = shape
-    dev, pool_ptr, ts = _quant_pool(pool, page_size, d)
+    dev, pool_ptr, tiles, heads, ts = _quant_pool(pool, page_size, d)
     ks, vs = k_new.stride(), v_new.stride()
-    if k_new.dtype is not _BF16 or v_new.dtype is not _BF16 or v_new.shape != shape or pool.shape[1] != hkv or \
+    if k_new.dtype is not _BF16 or v_new.dtype is not _BF16 or v_new.shape != shape or heads != hkv or \
             ks[2] != 1 or vs[2] != 1 or (hkv > 1 and (ks[1] != d or vs[1] != d)) or \
             k_new.get_device() != dev or v_new.get_device() != dev:
-        raise ValueError("k_new and v_new must be bf16 [n, %d, %d] on the pool's device, a token's rows contiguous" % (
-            pool.shape[1], d))
+        raise ValueError("k_new and v_new must be bf16 [n, %d, %d] on the pool's device, a token's rows contiguous" % (heads, d))
     row = hkv * d
     st = _lib.pkv_quant_store(
-        pool_ptr, pool.shape[0], ts, hkv, d, page_size, _ptr(k_scale, "k_scale", _F32, (hkv,), dev),
+        pool_ptr, tiles, ts, hkv, d, page_size, _ptr(k_scale, "k_scale", _F32, (hkv,), dev),
         _ptr(v_scale, "v_scale", _F32, (hkv,), dev), k_new.data_ptr(), v_new.data_ptr(), ks[0] if n > 1 else row,
         vs[0] if n > 1 else row, _ptr(slot_mapping, "slot_mapping", _I32T, (n,), dev), n,
         _ptr(err_flags, "err_flags", _I32T, None, dev), _quant_stream(stream, dev))
@@ -436,15 +439,15 @@ def pkv_quant_gather(pool, req_to_token, req_pool_idx, seq_lens, max_seq_len, k_
     """k_out, v_out bf16 [rows, Hkv, D] receive the requests' rows in order (see pkv_ragged_gather)."""
     shape = k_out.shape
     rows, hkv, d = shape
-    dev, pool_ptr, ts = _quant_pool(pool, page_size, d)
-    if pool.shape[1] != hkv:
-        raise ValueError("k_out must be bf16 [rows, %d, %d]" % (pool.shape[1], d))
+    dev, pool_ptr, tiles, heads, ts = _quant_pool(pool, page_size, d)
+    if heads != hkv:
+        raise ValueError("k_out must be bf16 [rows, %d, %d]" % (heads, d))
     batch = seq_lens.shape
     r2t_rows, r2t_width = req_to_token.shape
     st = _lib.pkv_quant_gather(
-        pool_ptr, pool.shape[0], ts, hkv, d, page_size, _ptr(k_scale, "k_scale", _F32, (hkv,), dev),
+        pool_ptr, tiles, ts, hkv, d, page_size, _ptr(k_scale, "k_scale", _F32, (hkv,), dev),
         _ptr(v_scale, "v_scale", _F32, (hkv,), dev), _ptr(req_to_token, "req_to_token", _I32T, None, dev), r2t_rows,
-        req_to_token.stride(0), r2t_width, _ptr(req_pool_idx, "req_pool_idx", _I32T, batch, dev),
+        r2t_width, r2t_width, _ptr(req_pool_idx, "req_pool_idx", _I32T, batch, dev),
         _ptr(kv_start, "kv_start", _I32T, batch, dev), _ptr(seq_lens, "seq_lens", _I32T, batch, dev), batch[0],
         int(max_seq_len), _ptr(k_out, "k_out", _BF16, None, dev), _ptr(v_out, "v_out", _BF16, shape, dev), rows,
         _ptr(cu_seqlens, "cu_seqlens", _I32T, (batch[0] + 1,), dev), _ptr(err_flags, "err_flags", _I32T, None, dev),
@@ -460,8 +463,7 @@ def make_quant_args(layout, q, pool, out, *, page_size, sm_scale, max_seq_len, k
     """Arguments of pkv_quant_decode (no qo_indptr) or pkv_quant_extend: q bf16 [rows, Hq, D], rows any
     stride apart; pool uint8 [tiles, Hkv, tile bytes]; out bf16 [rows, Hq, D]."""
     T, hq, d = q.shape
-    dev, _, ts = _quant_pool(pool, page_size, d)
-    hkv = pool.shape[1]
+    dev, _, _, hkv, ts = _quant_pool(pool, page_size, d)
     if q.dtype is not _BF16 or q.stride(2) != 1 or (hq > 1 and q.stride(1) != d) or q.get_device() != dev:
         raise ValueError("q must be bf16 [rows, Hq, D] on the pool's device, a row's heads contiguous")
     B = T if qo_indptr is None else qo_indptr.numel() - 1
@@ -509,7 +511,7 @@ def pkv_quant_extend_workspace_size(args: QuantArgs) -> int:
 
 def _quant_attend(fn, who, args, workspace, err_flags, stream):
     dev = args._dev
-    if dev != torch.cuda.current_device() or workspace.get_device() != dev or err_flags.get_device() != dev:
+    if dev != _device() or workspace.get_device() != dev or err_flags.get_device() != dev:
         raise ValueError("%s: the workspace, err_flags and the current device must be the pool's (cuda:%d)" % (who, dev))
     st = fn(ctypes.byref(args), workspace.data_ptr(), workspace.nbytes, err_flags.data_ptr(), _quant_stream(stream, dev))
     if st != PKV_OK:
