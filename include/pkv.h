@@ -552,8 +552,8 @@ typedef struct pkv_quant_args {
     int32_t block_table_width;
     int32_t max_q_len;         /* pkv_quant_extend: host upper bound on a request's query rows; 0: unknown */
     int64_t total_q;           /* query rows: B for pkv_quant_decode, qo_indptr[B] for pkv_quant_extend */
-    int64_t total_kv;          /* pkv_quant_extend: host upper bound on the sum of the key counts (sizes the
-                                  workspace); 0: batch * max_seq_len */
+    int64_t total_kv;          /* host upper bound on the sum of the key counts (pkv_quant_extend: sizes the
+                                  workspace; pkv_quant_decode: a hint); 0: unknown, batch * max_seq_len */
     int64_t num_tiles;         /* the pool (see above) */
     int64_t tile_stride;
     int64_t q_row_stride;      /* elements between query rows (>= Hq * head_dim, a multiple of 8) */

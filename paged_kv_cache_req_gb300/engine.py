@@ -171,7 +171,8 @@ class DecodeStep:
                                              sm_scale=wl.sm_scale, max_seq_len=pb.max_len,
                                              cu_seqlens=pb.cu, lse=pb.lse, kv_chunk=self.kv_chunk)
             elif self.quant is not None:
-                kw = dict(sm_scale=wl.sm_scale, max_seq_len=pb.max_len, lse=pb.lse, kv_chunk=self.kv_chunk)
+                kw = dict(sm_scale=wl.sm_scale, max_seq_len=pb.max_len, lse=pb.lse, kv_chunk=self.kv_chunk,
+                          total_kv=int(p.seq_lens.sum()))
                 if self.fused:
                     pb.args = self.quant.args(B.PKV_LAYOUT_REQ_TO_TOKEN, pb.q, pb.out, seq_lens=pb.seq_lens,
                                               req_to_token=self.r2t, req_pool_idx=self.req_pool_idx,
