@@ -35,7 +35,8 @@ using quant::Table;
 constexpr int kTile = 64;           // keys per stage of the copies
 constexpr int kStep = 32;           // keys per step of the math: what 128 to 168 registers hold
 constexpr int kGroups = kStep / 16; // of 16 keys: the MMAs' key rows
-constexpr int kUnitCost = 1;        // tiles' worth of work that starting and finishing a unit takes
+// Tiles' worth of work that starting and finishing a unit takes (16 rows: q is loaded in place).
+constexpr int unit_cost(int nt) { return nt == 1 ? 1 : 2; }
 // The span kernel runs one block per SM, which holds all the shared memory: a second block of
 // a persistent grid could be left without room where the launch before still has a block,
 // and then starts when the others end.  Its warps (as many as their registers allow) and
@@ -165,10 +166,9 @@ __device__ __forceinline__ Req load_req(const Params &p, int b, bool report) {
     }
     return r;
 }
-// A unit enters the sequence as kUnitCost stand-in tiles and its real ones, so that a span
+// A unit enters the sequence as unit_cost stand-in tiles and its real ones, so that a span
 // of many short units holds no more work than one inside a long unit.
 __device__ __forceinline__ int real_tiles(int L) { return max(1, (L + kTile - 1) / kTile); }
-__device__ __forceinline__ int unit_tiles(int L) { return kUnitCost + real_tiles(L); }
 template <int NT>
 __device__ __forceinline__ int row_blocks(const Params &p, int n) { return (n * p.g + 8 * NT - 1) / (8 * NT); }
 
@@ -197,7 +197,7 @@ __device__ __forceinline__ void build_table(const Params &p, const Table1 &tb, l
     for (int b = lo; b < hi; ++b) {
         const Req r = load_req(p, b, report);
         if (tb.req) tb.req[b] = r;
-        local += static_cast<long long>(row_blocks<NT>(p, r.n)) * p.hkv * unit_tiles(r.L);
+        local += static_cast<long long>(row_blocks<NT>(p, r.n)) * p.hkv * (unit_cost(NT) + real_tiles(r.L));
         off[b + 1] = static_cast<int>(local);
     }
     long long incl = local;
@@ -250,6 +250,7 @@ __device__ __forceinline__ void set_req(Unit &u, const Req &r, int b) {
     u.tiles = real_tiles(r.L);
 }
 // The unit that holds tile `pos` of the sequence.
+template <int NT>
 __device__ __forceinline__ Unit find_unit(const Params &p, const Table1 &tb, int pos) {
     const int *off = tb.off;
     int lo = 0, hi = p.batch;   // the last request with off[b] <= pos (those without rows have no tiles)
@@ -259,13 +260,14 @@ __device__ __forceinline__ Unit find_unit(const Params &p, const Table1 &tb, int
     }
     Unit u;
     set_req(u, get_req(p, tb, lo), lo);
-    const int all = u.tiles + kUnitCost, rem = pos - off[lo], i = rem / all;
+    const int all = u.tiles + unit_cost(NT), rem = pos - off[lo], i = rem / all;
     u.rb = i / p.hkv;
     u.kh = i - u.rb * p.hkv;
-    u.first = pos - (rem - i * all) + kUnitCost;
+    u.first = pos - (rem - i * all) + unit_cost(NT);
     return u;
 }
 // The unit after u (there is one): the next kv head, row block or request.
+template <int NT>
 __device__ __forceinline__ void next_unit(const Params &p, const Table1 &tb, Unit &u) {
     const int end = u.first + u.tiles;
     if (end == tb.off[u.b + 1]) {
@@ -277,7 +279,7 @@ __device__ __forceinline__ void next_unit(const Params &p, const Table1 &tb, Uni
         u.kh = 0;
         ++u.rb;
     }
-    u.first = end + kUnitCost;
+    u.first = end + unit_cost(NT);
 }
 
 // Keys that some row of the unit may see: the causal bound of its last token, or all.
@@ -358,7 +360,7 @@ struct Fetcher {
     __device__ __forceinline__ void advance(const Params &p, const Table1 &tb, Work *queue, int lane) {
         for (;;) {
             if (next < span_end) {
-                next_unit(p, tb, u);
+                next_unit<NT>(p, tb, u);
             } else {   // the warp's next span
                 const int total = tb.off[p.batch], per = tb.off[p.batch + 1];
                 for (;;) {
@@ -373,7 +375,7 @@ struct Fetcher {
                     if (lane == 0) p.cuts[sp] = make_int4(-1, 0, 0, 0);
                 }
                 span_end = min(total, next + per);
-                u = find_unit(p, tb, next);
+                u = find_unit<NT>(p, tb, next);
                 if (lane == 0) {   // cut: the unit has real tiles on both sides of the boundary
                     int4 cut = make_int4(-1, 0, 0, 0);
                     if (u.first < next) {
@@ -1377,7 +1379,7 @@ static bool make_plan(const pkv_quant_args *a, bool extend, Plan &pl) {
         int64_t spans = static_cast<int64_t>(pl.grid) * warps;
         // all units' tiles, at most
         const int64_t blocks = (a->total_q * g + 8 * pl.nt - 1) / (8 * pl.nt) + a->batch;
-        const int64_t tiles = blocks * a->num_kv_heads * ((std::max(1, a->max_seq_len) + kTile - 1) / kTile + kUnitCost);
+        const int64_t tiles = blocks * a->num_kv_heads * ((std::max(1, a->max_seq_len) + kTile - 1) / kTile + unit_cost(pl.nt));
         if (a->kv_chunk > 0) {
             pl.span_tiles = a->kv_chunk / kTile;
             spans = (tiles + pl.span_tiles - 1) / pl.span_tiles;
