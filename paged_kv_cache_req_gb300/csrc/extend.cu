@@ -58,6 +58,7 @@ constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLazy = 8.f;
 constexpr int kRing = 8;                   // slots of the item queue
 constexpr int kItemReaders = 16;           // warps that read every queued item
+constexpr int kMostItems = 1 << 29;        // at which the item counts saturate
 constexpr int kLayoutHeld = 4;             // Params::layout: key t of request b is row kv_indptr[b] + t of the held tensors
 
 template <int D>
@@ -91,6 +92,7 @@ struct Cfg {
 struct Params {
     int32_t layout, batch, hq, hkv, g, g_shift, T;
     int32_t ps_shift, ps_mask, box_rows, bt_width, chunk, max_len;
+    int32_t items_max;         // that the workspace's partials hold (kMostItems: nothing is split)
     float scale_log2;
     int64_t num_pages, kv_indices_len, total_q;
     const int32_t *qo_indptr, *kv_end, *kv_indptr, *kv_indices, *kv_last, *block_table, *seq_lens;
@@ -112,6 +114,7 @@ struct Params {
     int64_t held_rows;                 // rows per head and 64-dim slab of the held tensors
     int32_t heads;                     // query heads per kv head (g is the next power of two)
     int32_t min_rows;                  // requests with at most this many rows per kv head are left out
+    const int32_t *order;              // [B] the requests in the order of their items: the longest first
 };
 
 // Keys of request b (0 and a flag for malformed inputs).
@@ -198,6 +201,7 @@ struct Req {
 // Request b from the inputs (flags raised only with `report`); causal rows need their keys.
 __device__ __forceinline__ Req load_req(const Params &p, int b, bool report) {
     Req r;
+    if (p.layout == kLayoutHeld) b = p.order[b];
     r.L = key_count(p, b, r.base, report);
     r.n = q_count(p, b, report);
     if (p.layout == kLayoutHeld && r.n * p.heads <= p.min_rows) r.n = 0;
@@ -270,7 +274,9 @@ __device__ __forceinline__ Item locate(const Params &p, const Tables &t, int64_t
     return it;
 }
 
-// Every CTA builds the same tables (CTA 0 reports malformed inputs).
+// Every CTA builds the same tables (CTA 0 reports malformed inputs).  Row ranges that overlap
+// could make more items than the workspace was sized for: then there are none.  (One
+// request's items are at most INT32_MAX / kRows, a thread's some dozen of those.)
 __device__ __forceinline__ void build_tables(const Params &p, const Tables &t, int *scratch) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int B = p.batch;
@@ -290,23 +296,31 @@ __device__ __forceinline__ void build_tables(const Params &p, const Tables &t, i
     int incl = local;
     for (int o = 1; o < 32; o <<= 1) {
         const int x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
+        if (lane >= o) incl = min(incl + x, kMostItems);
     }
     if (lane == 31) scratch[warp] = incl;
     __syncthreads();
-    int wbase = 0;
-    for (int w = 0; w < warp; ++w) wbase += scratch[w];
-    int run = wbase + incl - local;
+    int wbase = 0, total = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w == warp) wbase = total;
+        total = min(total + scratch[w], kMostItems);
+    }
+    const bool fits = total < kMostItems && total <= p.items_max;
+    int run = fits ? wbase + incl - local : 0;
     for (int b = lo; b < hi; ++b) {
         t.off[b] = run;
+        if (!fits) continue;
         const Req r = t.keys ? get_req(p, t, b) : load_req(p, b, false);
         run += p.hkv * per_head_items(p, r.L, r.n);
     }
-    if (tid == kThreads - 1) t.off[B] = wbase + incl;
+    if (tid == kThreads - 1) {
+        t.off[B] = fits ? total : 0;
+        if (!fits && blockIdx.x == 0) raise_flag(p.err, PKV_DEVERR_RANGE);
+    }
     __syncthreads();
     if (blockIdx.x == 0) {   // the merge kernel's tables: items and groups per request, as prefixes
         int gl = 0;
-        for (int b = lo; b < hi; ++b) {
+        for (int b = lo; fits && b < hi; ++b) {
             const Req r = t.keys ? get_req(p, t, b) : load_req(p, b, false);
             gl += p.hkv * ((r.n + p.T - 1) / p.T);
         }
@@ -323,6 +337,7 @@ __device__ __forceinline__ void build_tables(const Params &p, const Tables &t, i
         for (int b = lo; b < hi; ++b) {
             p.goff[b] = grun;
             p.ioff[b] = t.off[b];
+            if (!fits) continue;
             const Req r = t.keys ? get_req(p, t, b) : load_req(p, b, false);
             grun += p.hkv * ((r.n + p.T - 1) / p.T);
         }
@@ -1286,6 +1301,7 @@ static pkv_status launch_t(const pkv_extend_args *a, const Plan &pl, void *ws, i
     p.box_rows = std::min(a->page_size, kTile);
     p.bt_width = a->block_table_width;
     p.chunk = pl.chunk;
+    p.items_max = pl.nch_max > 1 ? static_cast<int>(pl.items_max) : kMostItems;
     p.max_len = a->max_seq_len;
     p.scale_log2 = a->sm_scale * kLog2e;
     p.num_pages = a->num_slots >> p.ps_shift;
@@ -1330,6 +1346,7 @@ static pkv_status launch_t(const pkv_extend_args *a, const Plan &pl, void *ws, i
         p.held_rows = held->rows;
         p.heads = a->num_q_heads / a->num_kv_heads;
         p.min_rows = held->min_rows;
+        p.order = held->order;
     }
     CUtensorMap tmq, tmk, tmv;
     {   // q [total_q, Hq, D]: boxes of 64 dims x g heads x T tokens = 128 rows of 128 bytes

@@ -11,6 +11,7 @@ struct Held {
     const void *k, *v;           // bf16 / fp16 [D/64][kv heads][rows][64]
     int64_t rows;
     const int32_t *first_row;    // device [B + 1]: request b's keys are rows first_row[b] .. first_row[b + 1] - 1
+    const int32_t *order;        // device [B]: the requests, the longest first (their items are handed out so)
     const float *k_scale, *v_scale;
     int64_t q_row_stride;
     int32_t min_rows;            // requests with at most this many (token, head) rows per kv head are left out

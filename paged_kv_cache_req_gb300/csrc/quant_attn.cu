@@ -172,9 +172,6 @@ __device__ __forceinline__ int real_tiles(int L) { return max(1, (L + kTile - 1)
 template <int NT>
 __device__ __forceinline__ int row_blocks(const Params &p, int n) { return (n * p.g + 8 * NT - 1) / (8 * NT); }
 
-// off[b] = first tile of request b's units, off[B] = all tiles, off[B + 1] = tiles per
-// span, by the block's threads.  The host has checked that the tiles of well-formed inputs
-// fit; row ranges that overlap could exceed that, and then no request has any.
 // Token of row r of a request and kv head: r / g, by a multiplication (for r < 2^28, which
 // the host checks, the estimate is at most one off).
 __device__ __forceinline__ int token_of(const Params &p, int r) {
@@ -188,6 +185,9 @@ struct Table1 {
     Req *req;    // [B], or nullptr: read again where needed
 };
 
+// off[b] = first tile of request b's units, off[B] = all tiles, off[B + 1] = tiles per
+// span, by the block's threads.  The host has checked that the tiles of well-formed inputs
+// fit the spans; row ranges that overlap could exceed that, and then no request has any.
 template <int NT, int kBlock>
 __device__ __forceinline__ void build_table(const Params &p, const Table1 &tb, long long *scratch, bool report) {
     int *off = tb.off;
@@ -212,7 +212,8 @@ __device__ __forceinline__ void build_table(const Params &p, const Table1 &tb, l
         if (w < warp) before += scratch[w];
         total += scratch[w];
     }
-    const bool fits = total <= kMostTiles;
+    const bool fits = total <= (p.span_tiles ? min(static_cast<long long>(kMostTiles), static_cast<long long>(p.span_tiles) * p.spans_max)
+                                             : static_cast<long long>(kMostTiles));
     for (int b = lo; b < hi; ++b) off[b + 1] = fits ? off[b + 1] + static_cast<int>(before) : 0;
     if (tid == 0) {
         if (!fits && report) raise_flag(p.err, PKV_DEVERR_RANGE);
@@ -300,11 +301,13 @@ struct Work {
 constexpr int kQueue = 8;    // segments that the copies may be ahead by (at most a ring's stages + 1)
 
 // A segment without keys: zeros and -inf where it is the whole unit, else an empty partial.
+// (Given bounds leave a unit without keys only where the request has none.)
 template <int D, int NT>
 __device__ __forceinline__ void write_empty(const Params &p, const Unit &s, int slot, int lane) {
     for (int lr = 0; lr < 8 * NT; ++lr) {
         const int row = s.rb * 8 * NT + lr, tok = token_of(p, row);
         if (tok >= s.n) return;
+        if (p.kv_end && s.kh == 0 && lane == 0 && p.kv_end[s.qo0 + tok] != 0) raise_flag(p.err, PKV_DEVERR_RANGE);
         const int64_t at = static_cast<int64_t>(s.qo0 + tok) * p.hq + s.kh * p.g + (row - tok * p.g);
         if (slot < 0) {
             if (lane < D / 8) *reinterpret_cast<uint4 *>(p.out + at * D + lane * 8) = make_uint4(0, 0, 0, 0);
@@ -688,19 +691,19 @@ __device__ __forceinline__ void tile_step(const Params &p, State<D, NT> &st, con
 template <int D, int NT>
 __device__ __forceinline__ void load_q(const Params &p, const Work &s, int n, uint32_t (&w)[D / 8], int lane) {
     const int r = lane >> 2, c = lane & 3;
-        const int row = s.rb * 8 * NT + n * 8 + r, tok = token_of(p, row), hh = row - tok * p.g;
-        if (tok < s.n) {
-            const uint4 *src = reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(s.qo0 + tok) * p.q_stride +
-                                                               (s.kh * p.g + hh) * D + c * (D / 4));
+    const int row = s.rb * 8 * NT + n * 8 + r, tok = token_of(p, row), hh = row - tok * p.g;
+    if (tok < s.n) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(s.qo0 + tok) * p.q_stride +
+                                                           (s.kh * p.g + hh) * D + c * (D / 4));
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                const uint4 x = __ldg(src + i);
-                w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) w[i] = 0;
+        for (int i = 0; i < D / 32; ++i) {
+            const uint4 x = __ldg(src + i);
+            w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
         }
+    } else {
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) w[i] = 0;
+    }
 }
 
 // q fragments, score factors and bounds of a segment's rows; a fresh softmax state.  At NT =
@@ -1132,17 +1135,18 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
 // many rows.  Layout [D/64][kv heads][rows][64], request after request.  A key whose V
 // holds a NaN block gets a NaN K and a zero V: a zero weight times NaN would reach rows that
 // do not see the key.
-constexpr int kHoldThreads = 256;
+constexpr int kHoldThreads = 256, kHoldCtas = 6;   // threads of a block, blocks per SM
 
 struct HoldParams {
     uint16_t *k, *v;
     int64_t rows;
-    int32_t *first_row, *counter;
+    int32_t *first_row, *counter, *order;
     int32_t min_rows;
 };
+constexpr int kSorted = 1024;   // requests up to which their items go longest first
 
 template <int D>
-__global__ void __launch_bounds__(kHoldThreads) hold_kernel(const Params p, const HoldParams h) {
+__global__ void __launch_bounds__(kHoldThreads, kHoldCtas) hold_kernel(const Params p, const HoldParams h) {
     extern __shared__ __align__(16) int32_t table[];   // [B + 1] first rows, [B + 1] first tiles
     __shared__ long long scratch[kHoldThreads / 32];
     __shared__ long long carry_s[2];
@@ -1181,6 +1185,18 @@ __global__ void __launch_bounds__(kHoldThreads) hold_kernel(const Params p, cons
     }
     if (blockIdx.x == 0) {
         for (int i = tid; i <= B; i += kHoldThreads) h.first_row[i] = first[i];
+        for (int b = tid; b < B; b += kHoldThreads) {
+            int place = b;
+            if (B <= kSorted) {
+                const int L = first[b + 1] - first[b];
+                place = 0;
+                for (int j = 0; j < B; ++j) {
+                    const int x = first[j + 1] - first[j];
+                    place += x > L || (x == L && j < b) ? 1 : 0;
+                }
+            }
+            h.order[place] = b;
+        }
         if (tid == 0) {
             *h.counter = 0;
             if (first[B] > h.rows) raise_flag(p.err, PKV_DEVERR_CAPACITY);
@@ -1241,9 +1257,7 @@ __global__ void __launch_bounds__(kHoldThreads) hold_kernel(const Params p, cons
                 }
             }
             if (in) {
-                uint4 *o = reinterpret_cast<uint4 *>(dst + static_cast<int64_t>(key) * 64);
-                o[0] = make_uint4(x[0], x[1], x[2], x[3]);
-                o[1] = make_uint4(x[4], x[5], x[6], x[7]);
+                quant::store_32(dst + static_cast<int64_t>(key) * 64, x);
             }
         }
     }
@@ -1272,8 +1286,10 @@ static pkv_status validate(const char *who, const pkv_quant_args *a, bool extend
         return fail(PKV_ERR_INVALID_ARG, "%s: the tile stride must hold all kv heads and be a multiple of 16 bytes", who);
     if (a->q_row_stride < static_cast<int64_t>(a->num_q_heads) * a->head_dim || a->q_row_stride % 8)
         return fail(PKV_ERR_INVALID_ARG, "%s: q_row_stride must hold Hq x head_dim and be 16-byte aligned", who);
-    if (a->total_q > INT32_MAX || a->num_tiles * t > INT32_MAX)
-        return fail(PKV_ERR_UNSUPPORTED, "%s: more than 2^31 pool slots or query rows", who);
+    if (a->num_tiles > INT32_MAX / t) return fail(PKV_ERR_UNSUPPORTED, "%s: more than 2^31 pool slots", who);
+    if (a->total_q > INT32_MAX || a->total_q * a->num_q_heads >= 1 << 28 ||
+        static_cast<int64_t>(a->batch) * a->num_kv_heads > INT32_MAX)
+        return fail(PKV_ERR_UNSUPPORTED, "%s: 2^28 (query row, head) pairs or more", who);
     if (a->batch == 0 || !check_ptrs) return PKV_OK;
     if (!a->q || !a->pool || !a->out) return fail(PKV_ERR_INVALID_ARG, "%s: null q/pool/out", who);
     if (extend ? !a->qo_indptr : (a->qo_indptr || a->kv_end || a->total_q != a->batch))
@@ -1292,7 +1308,8 @@ static pkv_status validate(const char *who, const pkv_quant_args *a, bool extend
 
 // How a call runs: the span kernel (its rows per unit, grid, spans), and for requests with
 // many query rows the held path; with the workspace of each.
-constexpr int kHeldRows = 128;   // rows per request and kv head up to which the span kernel is used
+constexpr int kHeldRows = 128;     // rows per request and kv head up to which the span kernel is used
+constexpr int kHeldBatch = 4096;   // requests whose tables fit the held path's shared memory
 
 struct Plan {
     bool unit, spans, held, plan_launch;
@@ -1342,7 +1359,11 @@ static bool make_plan(const pkv_quant_args *a, bool extend, Plan &pl) {
     const int64_t batch = std::max(a->batch, 1), total_q = std::max<int64_t>(a->total_q, 1);
     // rows of a request and kv head: at most max_q_len's, or what the average says
     const int64_t rows = (extend && a->max_q_len > 0 ? a->max_q_len : (total_q + batch - 1) / batch) * g;
-    pl.held = extend && rows > kHeldRows;
+    // (a batch too large for the held path's tables, or keys past its counters and coordinates, take
+    // the spans whatever their rows)
+    pl.hold_rows = std::max<int64_t>(1, a->total_kv > 0 ? a->total_kv : batch * a->max_seq_len);
+    pl.held = extend && rows > kHeldRows && a->batch <= kHeldBatch && batch * a->max_seq_len <= INT32_MAX &&
+              pl.hold_rows <= INT32_MAX / (static_cast<int64_t>(a->num_kv_heads) * (a->head_dim / 64));
     const int64_t sms = std::max(1, sm_count());
     if (!extend && a->kv_chunk == 0) {
         // What the two kernels take, in parts of about 0.75 us: a block per unit starts, then makes
@@ -1393,14 +1414,11 @@ static bool make_plan(const pkv_quant_args *a, bool extend, Plan &pl) {
         pl.table = up256((static_cast<size_t>(a->batch) + 2) * 4);
     }
     if (pl.held) {
-        pl.hold_rows = a->total_kv > 0 ? a->total_kv : batch * a->max_seq_len;
-        pl.hold_rows = std::max<int64_t>(pl.hold_rows, 1);
-        if (pl.hold_rows > INT32_MAX / (a->num_kv_heads * (a->head_dim / 64))) return false;
         pl.hold_k = up256(static_cast<size_t>(pl.hold_rows) * a->num_kv_heads * a->head_dim * 2);
-        pl.hold_first = up256((static_cast<size_t>(a->batch) + 1) * 4);
+        pl.hold_first = up256((static_cast<size_t>(a->batch) * 2 + 1) * 4);   // first rows, and the order
         const pkv_extend_args e = extend_args(a);
         pl.ext = up256(ext::held_workspace(&e));
-        if (pl.ext == 0 || (static_cast<size_t>(a->batch) + 1) * 8 > 64 * 1024) return false;
+        if (pl.ext == 0) return false;
     }
     return true;
 }
@@ -1485,6 +1503,7 @@ static pkv_status launch_held(const pkv_quant_args *a, const Params &p, const Pl
     h.v = reinterpret_cast<uint16_t *>(ws + pl.hold_k);
     h.rows = pl.hold_rows;
     h.first_row = reinterpret_cast<int32_t *>(ws + 2 * pl.hold_k);
+    h.order = h.first_row + a->batch + 1;
     h.counter = reinterpret_cast<int32_t *>(own + ext::held_counter_offset(&e));
     h.min_rows = pl.spans ? kHeldRows : 0;
     const size_t smem = (static_cast<size_t>(a->batch) + 1) * 8;
@@ -1498,12 +1517,12 @@ static pkv_status launch_held(const pkv_quant_args *a, const Params &p, const Pl
         set->store(1);
     }
     const int64_t items = (pl.hold_rows / kTile + a->batch) * a->num_kv_heads;
-    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(items, 8ll * std::max(1, sm_count())));
+    const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(items, static_cast<int64_t>(kHoldCtas) * std::max(1, sm_count())));
     const pkv_status st = launch_status(launch_chained(hold_kernel<D>, dim3(static_cast<unsigned>(grid)), dim3(kHoldThreads),
                                                        smem, s, p, h),
                                         "pkv_quant_extend (hold kernel)");
     if (st != PKV_OK) return st;
-    const ext::Held held{h.k, h.v, h.rows, h.first_row, a->k_scale, a->v_scale, a->q_row_stride, h.min_rows};
+    const ext::Held held{h.k, h.v, h.rows, h.first_row, h.order, a->k_scale, a->v_scale, a->q_row_stride, h.min_rows};
     return ext::held_launch(&e, held, own, p.err, s);
 }
 
@@ -1520,7 +1539,6 @@ static pkv_status attend(const char *who, const pkv_quant_args *a, bool extend, 
     if (ws_bytes < need) return fail(PKV_ERR_CAPACITY, "%s: workspace of %zu bytes, %zu needed", who, ws_bytes, need);
     if (!ws || !aligned(ws, 256))
         return fail(PKV_ERR_INVALID_ARG, "%s: workspace must be non-null and 256-byte aligned", who);
-    if (a->total_q * a->num_q_heads >= 1 << 28) return fail(PKV_ERR_UNSUPPORTED, "%s: too many query rows", who);
     Params p = params(a, err);
     p.wait_ns = wait_limit_ns();
     char *at = static_cast<char *>(ws);
