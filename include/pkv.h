@@ -585,7 +585,7 @@ typedef struct pkv_quant_args {
  * One query row per request over all its keys; the same formulas with K and V the
  * pool's values.  Page lists, checks and flags are pkv_decode's.  Arithmetic: K and V
  * enter the tensor cores as code * s, exact in 16 bits; scores, softmax and sums are
- * fp32, the weights fp16 or bf16, the output bf16 rounded to nearest even.  What the
+ * fp32, the weights fp16, the output bf16 rounded to nearest even.  What the
  * pool holds at slots past a request's keys does not matter, NaN patterns included.
  * workspace: at least pkv_quant_decode_workspace_size(args) bytes, 256-byte aligned, not
  * shared with a call that may run at the same time; it needs no initialisation.
@@ -627,7 +627,7 @@ int32_t pkv_abi_version(void);
  *
  * Failure detection without a hang, after the fail-loud checks of the AWS
  * Neuron encoder-cache doc ("Read Path"): the kernels that pipeline through
- * mbarriers (the TMA decode, MLA decode and pkv_extend kernels) wait on them
+ * mbarriers (the TMA decode, MLA decode, pkv_extend and 4-bit attention kernels) wait on them
  * for at most this many nanoseconds.  A wait that runs out raises
  * PKV_DEVERR_TIMEOUT in err_flags and makes its CTA give up: every CTA that
  * sees the flag stops waiting, lets the copies and MMAs it already issued

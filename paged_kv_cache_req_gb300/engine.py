@@ -318,7 +318,8 @@ class DecodeStep:
                 n += 1                               # gather or build_indices
             if not self.fused or pb.gather or self.quant is not None:
                 n += 1 if pb.spec.stores else 0      # store
-            n += 1 + (1 if pb.ws_bytes > 0 else 0)   # split kernel (+ merge when requests can split)
+            # attention (+ merge when requests can split; a 4-bit call without one takes the least workspace)
+            n += 1 + (1 if pb.ws_bytes > (256 if pb.quant else 0) else 0)
             n += 1 if pb.quant and self.wl.batch > 1024 else 0   # (the tile table of a large batch)
         return n
 
@@ -470,7 +471,7 @@ class ExtendStep:
     def launches_per_step(self) -> int:
         if self.quant is not None:
             # spans and their merge; with many rows the copy out of the pool and its attention besides
-            # (alone for one request)
+            # (alone for one request), not counting the join of the latter's pieces where it splits keys
             held = int(self.ew.qo_lens.max()) * (self.ew.num_q_heads // self.ew.num_kv_heads) > 128
             n = 2 if not held or self.ew.batch > 1 else 0
             n += 2 if held else 0

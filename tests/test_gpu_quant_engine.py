@@ -228,6 +228,49 @@ def test_malformed_row_offsets(B):
         assert e & B.PKV_DEVERR_RANGE
 
 
+@pytest.mark.parametrize("n,max_q", [(16, 0), (64, 0), (64, 64), (256, 256)])
+def test_row_ranges_that_overlap_stay_in_the_workspace(B, n, max_q):
+    """Every second request claims all rows (the others run backwards), with the keys split:
+    more pieces than the workspace was sized for."""
+    rng = np.random.default_rng(67)
+    batch = 33
+    cache = Cache(rng, [600] * batch, 16, 2, 128)
+    q = to_bf16(values(rng, (n, 8, 128)))
+    out, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], dtype=torch.float32, device=DEV)
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    a = cache.args(B, "table", q, out, lse=lse, kv_chunk=64, max_q_len=max_q,
+                   qo_indptr=up(np.array([0, n] * (batch // 2) + [0, n], dtype=np.int32)))
+    size = B.pkv_quant_extend_workspace_size(a)
+    ws = torch.full((4 * size + (64 << 20),), 0xA5, dtype=torch.uint8, device=DEV)
+    B.pkv_quant_extend(a, ws[:size], err)
+    assert err.item() & B.PKV_DEVERR_RANGE
+    assert (ws[size:] == 0xA5).all()
+
+
+def test_a_bound_without_keys_is_flagged(B):
+    """kv_end past the keys of a request that has none."""
+    rng = np.random.default_rng(68)
+    cache = Cache(rng, [0, 40], 16, 2, 64)
+    q = to_bf16(values(rng, (3, 4, 64)))
+    out, lse, e = extend(B, cache, q, [1, 2], kv_end=[1, 40, 7])
+    assert e == B.PKV_DEVERR_RANGE
+    assert (out[0] == 0).all() and torch.isinf(lse[0]).all()
+    check(cache, q, out, lse, [1, 2], kv_end=[0, 40, 7])
+
+
+def test_a_batch_past_the_held_tables(B):
+    """Many requests of many rows each: more than the tables of the copied keys hold."""
+    rng = np.random.default_rng(69)
+    batch = 4100
+    lens = (33 + rng.integers(0, 30, batch)).tolist()
+    cache = Cache(rng, lens, 16, 1, 64)
+    rows = [33] * batch
+    q = to_bf16(values(rng, (33 * batch, 4, 64)))
+    out, lse, e = extend(B, cache, q, rows, max_q_len=33)
+    assert e == 0
+    check(cache, q, out, lse, rows, only=[0, 1, 2050, batch - 1])
+
+
 def test_a_serving_batch_on_its_own_stream(B):
     """Calls on a stream that is not the current one, tensors made on another."""
     rng = np.random.default_rng(66)
