@@ -123,6 +123,102 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                  "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
 }
+__device__ __forceinline__ constexpr int ilog2_of(int x) { return x <= 1 ? 0 : 1 + ilog2_of(x / 2); }
+// The stage of a tile has the layout of a 64-slot pool tile, or of four 16-slot ones, whatever
+// the pool's: with constant addresses the math of a tile takes less time than with the pool's
+// tile size looked up.  kT is 64 or 16 for pools of such tiles, copied as they lie (a bulk
+// copy each); 0 for the others, copied part by part: K codes, V codes, K scales, V scales.
+// Of those, tiles of 32 slots are four bulk copies each, and those of up to 8 slots are copied
+// 16 bytes per lane: a bulk copy keeps the SM's copy unit busy for some 18 cycles whatever its
+// size.  Measured, in us, over bulk copies of whole pieces with their tile size looked up by
+// the math: 16 requests x 16384 keys x 8 kv heads of 128, page size 1: 129 / 114, 2: 101 / 91,
+// 4: 87 / 83, 8: 81 / 80, 32: 78 / 76; of 64: 105 / 79, 77 / 63, 62 / 55, 57 / 53, 54 / 51.
+constexpr int kGatherShift = 3;   // log2 of the slots
+template <int kT>
+__device__ __forceinline__ bool gathers(int t_shift) { return kT == 0 && t_shift <= kGatherShift; }
+template <int kBytes>
+__device__ __forceinline__ void cp_async_small(void *dst, const void *src) {   // 4 or 8 bytes
+    asm volatile("cp.async.ca.shared.global [%0], [%1], %2;" ::"r"(smem_u32(dst)), "l"(src), "n"(kBytes) : "memory");
+}
+__device__ __forceinline__ void arrive_with_copies(uint64_t *bar) {   // once this lane's copies so far have landed
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ const uint8_t *from_lane(const uint8_t *p, int lane) {
+    return reinterpret_cast<const uint8_t *>(__shfl_sync(0xffffffffu, reinterpret_cast<uint64_t>(p), lane));
+}
+// Copies the pieces of a tile (2^ps slots each) of 32 slots or fewer into the stage; piece i's
+// address is lane (first + i) % 32's src[(first + i) / 32], null for one that is not copied.
+// `bar` counts each lane's arrival where the warp copies itself, else the bytes.
+template <int D>
+__device__ __forceinline__ void copy_parts(const uint8_t *const (&src)[2], int first, int ps, uint8_t *stage, uint64_t *bar, int lane) {
+    const uint8_t *low = first < 32 ? src[0] : src[1];   // (only 64 pieces lie in both)
+    first &= 31;
+    const int t = 1 << ps;
+    if (!gathers<0>(ps)) {
+        const int pieces = 64 >> ps, j = lane & (pieces - 1), part = lane >> (6 - ps);
+        const uint8_t *a = from_lane(low, first + j);
+        if (part < 4 && a) {
+            const int size = part < 2 ? t * (D / 2) : t * (D / 16);
+            const int before = part < 2 ? part * (D / 2) : D + (part - 2) * (D / 16);   // bytes per slot of the parts before
+            bulk_load(stage + before * 64 + j * size, a + before * t, size, bar);
+        }
+        return;
+    }
+    // codes: 16 bytes per lane, whole pieces at a time, each K then V
+    constexpr int kHalf = 64 * D / 16 / 32 / 2;          // rounds for 32 slots
+    if (D == 128 && ps == 3) {                           // two rounds for a piece
+#pragma unroll
+        for (int i = 0; i < kHalf; ++i) {
+            const uint8_t *a = from_lane(low, first + i);
+            if (!a) continue;
+            cp_async_16(stage + i * 512 + lane * 16, a + lane * 16, 16);
+            cp_async_16(stage + 32 * D + i * 512 + lane * 16, a + 512 + lane * 16, 16);
+        }
+    } else {
+        const int per = ilog2_of(D / 16) + ps;           // log2 of a piece's 16 bytes, at most 5
+        const int in = lane & ((1 << per) - 1), part = in >> (per - 1), c = in & ((1 << (per - 1)) - 1);
+        uint8_t *dst = stage + part * (32 * D) + (lane >> per) * (t * (D / 2)) + c * 16;
+        const int step = 32 >> per;
+        int j = first + (lane >> per);
+#pragma unroll
+        for (int i = 0; i < 2 * kHalf; ++i, j += step, dst += 512 / 2) {
+            const uint8_t *a = from_lane(ps == 0 && i >= kHalf ? src[1] : low, j & 31);
+            if (a) cp_async_16(dst, a + in * 16, 16);
+        }
+    }
+    // scales: 4, 8 or 16 bytes per lane
+    const int unit = min(4, ps + ilog2_of(D / 16));      // log2 of the bytes
+    const int per = ps + ilog2_of(D / 8) - unit;         // log2 of a piece's
+    const int in = lane & ((1 << per) - 1), part = in >> (per - 1), c = in & ((1 << (per - 1)) - 1);
+    uint8_t *dst = stage + 64 * D + part * (4 * D) + (lane >> per) * (t * (D / 16)) + (c << unit);
+    const int step = 32 >> per, rounds = (64 * D / 8 >> unit) / 32;
+    int j = first + (lane >> per);
+    for (int i = 0; i < rounds; ++i, j += step, dst += 16 << unit) {
+        const uint8_t *a = from_lane(ps == 0 && i >= rounds / 2 ? src[1] : low, j & 31);
+        if (!a) continue;
+        a += t * D + (in << unit);
+        if (unit == 4) cp_async_16(dst, a, 16);
+        else if (unit == 3) cp_async_small<8>(dst, a);
+        else cp_async_small<4>(dst, a);
+    }
+    arrive_with_copies(bar);
+}
+// Zeros in place of piece j.
+template <int D, int kT>
+__device__ __forceinline__ void zero_piece(uint8_t *stage, int j, int ps) {
+    const int t = 1 << ps;
+    if (kT != 0) {
+        uint32_t *w = reinterpret_cast<uint32_t *>(stage + j * quant::tile_bytes(kT, D));
+        for (int o = 0; o < quant::tile_bytes(kT, D) / 4; ++o) w[o] = 0;
+        return;
+    }
+    for (int part = 0; part < 2; ++part) {
+        uint32_t *codes = reinterpret_cast<uint32_t *>(stage + part * (32 * D) + j * t * (D / 2));
+        uint32_t *scales = reinterpret_cast<uint32_t *>(stage + 64 * D + part * (4 * D) + j * t * (D / 16));
+        for (int o = 0; o < t * (D / 8); ++o) codes[o] = 0;
+        for (int o = 0; o < t * (D / 64); ++o) scales[o] = 0;
+    }
+}
 // Bounded wait: false once `limit_ns` have passed.  The first poll returns at once, so that a
 // limit of some nanoseconds means what it says; the later ones suspend the warp for a
 // while (the time is looked at after the first of them and then after every 64).
@@ -424,35 +520,42 @@ struct Fetcher {
         const uint32_t bytes = quant::tile_bytes(1 << ps, D);
         const int first = (t & in_window) << (6 - ps);   // the tile's first piece within the window
         const int n = kT == 64 ? 1 : min(1 << (6 - ps), (keys - t * kTile + (1 << ps) - 1) >> ps);
-        if (!bad) {
-            if (lane == (first & 31)) mbar_arrive_expect_tx(bar, n * bytes);
-            if (kT != 64) __syncwarp();   // (with one piece the same lane copies)
-        } else {
-            uint32_t live = 0;
+        if (bad) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int j = 32 * i + lane - first;
-                const bool mine = j >= 0 && j < n;
-                live += __popc(__ballot_sync(0xffffffffu, mine && src[i]));
-                if (mine && !src[i]) {   // a bad page reads as zeros
-                    for (uint32_t o = 0; o < bytes; o += 16) *reinterpret_cast<uint4 *>(stage + j * bytes + o) = make_uint4(0, 0, 0, 0);
-                    fence_proxy_async_smem();   // before later copies into this stage
+                if (j >= 0 && j < n && !src[i]) {   // a bad page reads as zeros
+                    zero_piece<D, kT>(stage, j, ps);
+                    fence_proxy_async_smem();       // before later copies into this stage
                 }
             }
-            if (lane == 0) mbar_arrive_expect_tx(bar, live * bytes);
             __syncwarp();
+        }
+        if (!gathers<kT>(ps)) {
+            uint32_t live = n;
+            if (bad) {
+                live = 0;
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    const int j = 32 * i + lane - first;
+                    live += __popc(__ballot_sync(0xffffffffu, j >= 0 && j < n && src[i]));
+                }
+            }
+            if (lane == (first & 31)) mbar_arrive_expect_tx(bar, live * bytes);
+            if (kT != 64) __syncwarp();   // (with one piece the same lane copies)
         }
         if (kT == 64) {
             const uint8_t *a = first < 32 ? src[0] : src[1];
             if (lane == (first & 31) && a) bulk_load(stage, a, bytes, bar);
-        } else {
+        } else if (kT == 16) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int j = 32 * i + lane - first;
                 if (j >= 0 && j < n && src[i]) bulk_load(stage + j * bytes, src[i], bytes, bar);
             }
+        } else {
+            copy_parts<D>(src, first, ps, stage, bar, lane);
         }
-        if (bad) __syncwarp();
         if (++t >= t_end)
             advance(p, tb, queue, lane);
         else if ((t & in_window) == 0)
@@ -460,44 +563,30 @@ struct Fetcher {
     }
 };
 
-// Where key `k` (a lane's part) of the 16-key group `kt` of a step lies: relative to the step's
-// first codes and first scales.  kT is the slots of a pool tile: with 64 or 16 known to the
-// compiler every address is a lane's base and a constant; kT = 0 works it out for the others.
+// Where key `k` (a lane's part) of the 16-key group `kt` of a step lies: every address is a
+// lane's base and a constant.
 template <int D, int kT>
 struct Rows {
-    const uint8_t *codes_at, *scales_at;   // the step's first piece (64 slots: moved to the step's half of it)
-    int t_shift;
-    __device__ __forceinline__ Rows(const uint8_t *stage, int step, int shift) : t_shift(shift) {
+    const uint8_t *codes_at, *scales_at;   // the step's first 16-slot tile, or its half of the 64-slot one
+    __device__ __forceinline__ Rows(const uint8_t *stage, int step) {
         codes_at = scales_at = stage;
-        if (kT == 64) {
+        if (kT != 16) {
             codes_at += step * (kStep * D / 2);
             scales_at += step * (kStep * D / 16);
         } else {
-            codes_at += step * (kStep >> shift) * quant::tile_bytes(1 << shift, D);
+            codes_at += step * (kStep / 16) * quant::tile_bytes(16, D);
             scales_at = codes_at;
         }
     }
-    __device__ __forceinline__ int piece(int kt, int k, int &at, int &t) const {
-        const int key = kt * 16 + k;
-        if (kT > 0) {
-            t = kT;
-            at = kT == 64 ? key : k;
-            return kT == 64 ? 0 : kt * quant::tile_bytes(16, D);
-        }
-        t = 1 << t_shift;
-        at = key & (t - 1);
-        return (key >> t_shift) * quant::tile_bytes(t, D);
-    }
+    static constexpr int kSlots = kT == 16 ? 16 : 64;
+    __device__ __forceinline__ static int piece(int kt) { return kT == 16 ? kt * quant::tile_bytes(16, D) : 0; }
+    __device__ __forceinline__ static int slot(int kt, int k) { return kT == 16 ? k : kt * 16 + k; }
     // its codes (part 0 = K, 1 = V), and its scales
     __device__ __forceinline__ const uint8_t *codes(int part, int kt, int k) const {
-        int at, t;
-        const int b = piece(kt, k, at, t);
-        return codes_at + b + part * t * (D / 2) + at * (D / 2);
+        return codes_at + piece(kt) + part * kSlots * (D / 2) + slot(kt, k) * (D / 2);
     }
     __device__ __forceinline__ const uint8_t *scales(int part, int kt, int k) const {
-        int at, t;
-        const int b = piece(kt, k, at, t);
-        return scales_at + b + t * D + part * t * (D / 16) + at * (D / 16);
+        return scales_at + piece(kt) + kSlots * D + part * kSlots * (D / 16) + slot(kt, k) * (D / 16);
     }
 };
 
@@ -523,7 +612,7 @@ __device__ __forceinline__ void tile_step(const Params &p, State<D, NT> &st, con
                                           int keys, int lane) {
     const int r = lane >> 2, c = lane & 3;
     constexpr int KS = D / 16;     // contraction steps of q.k, and 16-row blocks of O^T
-    const Rows<D, kT> rows(stage, step, p.t_shift);
+    const Rows<D, kT> rows(stage, step);
     float s[kGroups][NT][4];
     // q.k a word (eight dims per lane) at a time over the groups of 16 keys: their MMAs
     // are independent of one another
@@ -811,12 +900,12 @@ __global__ void __launch_bounds__(warps_per_sm(D, NT) * 32, 1) attend_kernel(con
     __shared__ long long scratch[kWarps];
     __shared__ __align__(16) Work queues[kWarps][kQueue];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const uint32_t stage_bytes = (kTile >> p.t_shift) * quant::tile_bytes(1 << p.t_shift, D);
+    constexpr uint32_t stage_bytes = quant::tile_bytes(kTile, D);
     constexpr int S = ring_stages(D, NT);
     uint8_t *ring = smem + static_cast<uint32_t>(warp * S) * stage_bytes;
     uint64_t *bar = bars + warp * S;
     if (lane == 0) {
-        for (int i = 0; i < S; ++i) mbar_init(&bar[i], 1);
+        for (int i = 0; i < S; ++i) mbar_init(&bar[i], gathers<kT>(p.t_shift) ? 32 : 1);
         mbar_init_fence();
     }
     __syncwarp();
@@ -924,11 +1013,12 @@ __global__ void __launch_bounds__(warps_per_sm(D, NT) * 32, 1) unit_kernel(const
     __shared__ float2 ml[kWarps][8 * NT];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const int shift = kT == 64 ? 6 : kT == 16 ? 4 : p.t_shift, pieces = 64 >> shift;
-    const uint32_t bytes = quant::tile_bytes(1 << shift, D), stage_bytes = pieces * bytes;
+    const uint32_t bytes = quant::tile_bytes(1 << shift, D);
+    constexpr uint32_t stage_bytes = quant::tile_bytes(kTile, D);
     uint8_t *ring = smem + static_cast<uint32_t>(warp * S) * stage_bytes;
     uint64_t *bar = bars + warp * S;
     if (lane == 0) {
-        for (int i = 0; i < S; ++i) mbar_init(&bar[i], 1);
+        for (int i = 0; i < S; ++i) mbar_init(&bar[i], gathers<kT>(p.t_shift) ? 32 : 1);
         mbar_init_fence();
     }
     __syncwarp();
@@ -956,25 +1046,30 @@ __global__ void __launch_bounds__(warps_per_sm(D, NT) * 32, 1) unit_kernel(const
     };
     auto fetch = [&](const int (&slot)[2], int stage) {
         uint8_t *dst = ring + stage * stage_bytes;
+        const uint8_t *src[2];
         uint32_t live = 0;
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
+            src[i] = slot[i] >= 0 ? p.pool + static_cast<int64_t>(slot[i] >> shift) * p.tile_stride + static_cast<int64_t>(kh) * bytes
+                                  : nullptr;
             live += __popc(__ballot_sync(0xffffffffu, slot[i] >= 0));
             if (slot[i] == -1 || slot[i] == -2) {   // a bad page reads as zeros
                 raise_flag(p.err, slot[i] == -1 ? PKV_DEVERR_RANGE : PKV_DEVERR_CONTIG);
-                for (uint32_t o = 0; o < bytes; o += 16)
-                    *reinterpret_cast<uint4 *>(dst + (32 * i + lane) * bytes + o) = make_uint4(0, 0, 0, 0);
+                zero_piece<D, kT>(dst, 32 * i + lane, shift);
                 fence_proxy_async_smem();   // before later copies into this stage
             }
         }
-        if (lane == 0) mbar_arrive_expect_tx(&bar[stage], live * bytes);
-        __syncwarp();
+        if (!gathers<kT>(shift)) {
+            if (lane == 0) mbar_arrive_expect_tx(&bar[stage], live * bytes);
+            __syncwarp();
+        }
+        if (kT != 0) {
 #pragma unroll
-        for (int i = 0; i < 2; ++i)
-            if (slot[i] >= 0)
-                bulk_load(dst + (32 * i + lane) * bytes,
-                          p.pool + static_cast<int64_t>(slot[i] >> shift) * p.tile_stride + static_cast<int64_t>(kh) * bytes, bytes,
-                          &bar[stage]);
+            for (int i = 0; i < 2; ++i)
+                if (src[i]) bulk_load(dst + (32 * i + lane) * bytes, src[i], bytes, &bar[stage]);
+        } else {
+            copy_parts<D>(src, 0, shift, dst, &bar[stage], lane);
+        }
         __syncwarp();
     };
     int slots[S][2];
@@ -1382,16 +1477,14 @@ static bool make_plan(const pkv_quant_args *a, bool extend, Plan &pl) {
     pl.spans = !pl.unit && (!pl.held || batch > 1);
     if (pl.unit) {
         pl.nt = g <= 8 ? 1 : 2;
-        const int t = std::min(a->page_size, quant::kMaxTile);
         pl.grid = static_cast<int>(batch * a->num_kv_heads);
-        pl.smem = static_cast<size_t>(warps_per_sm(a->head_dim, pl.nt) * ring_stages(a->head_dim, pl.nt)) * (kTile / t) *
-                  quant::tile_bytes(t, a->head_dim);
+        pl.smem = static_cast<size_t>(warps_per_sm(a->head_dim, pl.nt) * ring_stages(a->head_dim, pl.nt)) *
+                  quant::tile_bytes(kTile, a->head_dim);
     }
     if (pl.spans) {
         const int64_t few = pl.held ? kHeldRows : rows;
         pl.nt = few <= 8 ? 1 : 2;
-        const int t = std::min(a->page_size, quant::kMaxTile);
-        const size_t stage = static_cast<size_t>(kTile / t) * quant::tile_bytes(t, a->head_dim);
+        const size_t stage = quant::tile_bytes(kTile, a->head_dim);
         const int warps = warps_per_sm(a->head_dim, pl.nt);
         pl.grid = static_cast<int>(sms);
         pl.plan_launch = a->batch > kTableInSmem;
