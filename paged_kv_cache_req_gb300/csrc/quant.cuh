@@ -23,6 +23,7 @@ namespace quant {
 
 constexpr int kBlock = 16;      // head dims that share a scale
 constexpr int kMaxTile = 64;    // slots per tile at most
+constexpr uint8_t kMostScale = 0x7e;  // e4m3 448: the largest, and what larger ones saturate to
 constexpr uint8_t kNanScale = 0x7f;   // e4m3 NaN: a block that held an infinity or a NaN
 
 constexpr int tile_bytes(int t, int d) { return (t * d * 9 / 8 + 15) / 16 * 16; }

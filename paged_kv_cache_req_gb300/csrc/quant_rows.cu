@@ -43,8 +43,9 @@ __device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], float g, uint3
     const float den = __fmul_rn(f16x2_to_f32(scales_to_f16(scale)).x, g);
     if (!(den > 0.f)) return make_uint2(0, 0);
     uint32_t c[8];
-    if (den > 0x1p-90f && den < 0x1p90f) {
-        // (an element below 2^-30 den has code 0 whatever its quotient's last bit)
+    if (scale != kMostScale && den > 0x1p-90f && den < 0x1p90f) {
+        // (no quotient is above 9 where the scale did not saturate, and an element below 2^-30 den
+        // has code 0 whatever its quotient's last bit)
         const float y = __frcp_rn(den);
         auto quotient = [&](float x) {
             const float q = __fmul_rn(x, y);

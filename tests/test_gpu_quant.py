@@ -94,6 +94,26 @@ def test_store_bytes(B, D, ps, H, n, form):
     assert not store[:, H:].any()
 
 
+@pytest.mark.parametrize("e", [-126, -100, -85, -60, -20, 20, 100, 125])
+def test_store_with_any_head_scale(B, e):
+    """g = 2^e against magnitudes from 2^-120 to 2^127: saturated, vanishing and far quotients."""
+    rng = np.random.default_rng(300 + e)
+    n, H, D, ps = 64, 1, 64, 16
+    x = values(rng, (n, H, D))
+    x = R.bf16(np.clip(x, -3, 3) * np.float32(2.0) ** np.linspace(-120, 126, n).astype(np.int64)[:, None, None])
+    x[::5, :, ::7] = 0.0
+    g = np.array([2.0 ** e], dtype=np.float32)
+    pool = torch.zeros((n // ps, H, R.tile_bytes(ps, D)), dtype=torch.uint8, device=DEV)
+    want = pool.cpu().numpy()
+    for part in (0, 1):
+        R.write(want, ps, np.arange(n), part, *R.quantise(x, g))
+    err = err_word()
+    B.pkv_quant_store(pool, to_bf16(x), to_bf16(x), up(np.arange(n, dtype=np.int32)), err, page_size=ps, k_scale=up(g), v_scale=up(g))
+    assert err.item() == 0
+    got = pool.cpu().numpy()
+    assert (got == want).all(), "%d bytes differ" % (got != want).sum()
+
+
 def test_store_flags(B):
     rng = np.random.default_rng(3)
     k = values(rng, (4, 2, 128))
