@@ -1,26 +1,40 @@
-// pkv_quant_decode / pkv_quant_extend: attention over a 4-bit K/V pool.
+// pkv_quant_decode / pkv_quant_extend: attention over a 4-bit K/V pool, in three ways.
 //
-// Work: a unit is (request, block of 8 NT query rows, kv head); its rows are the (token,
-// query head) pairs of the heads that share the kv head, its keys tiles of 64.  All units'
-// tiles in order (request, row block, kv head) form one sequence that is cut into equal
-// spans, one per warp of a persistent grid, whatever the requests' lengths.  A warp works
-// alone: it fetches the tiles of its span into its own ring of stages with bulk copies
-// (one per page of at most 64 keys: the pool keeps all that attention reads of it in one
-// piece), and no warp waits for another.  A unit inside one span is written by its warp; one
-// that a span boundary cuts leaves an fp32 partial per span for merge_kernel.
+// Spans (attend_kernel, merge_kernel).  A unit is (request, block of 8 NT query rows, kv
+// head); its rows are the (token, query head) pairs of the heads that share the kv head, its
+// keys tiles of 64.  All units' tiles in order (request, row block, kv head) form one sequence
+// that is cut into equal spans, one per warp of a grid of one block per SM, whatever the
+// requests' lengths.  A warp works alone: it copies the tiles of its span into its own ring
+// of stages, and no warp waits for another.  A unit inside one span is written by its warp;
+// one that a span boundary cuts leaves an fp32 partial per span for merge_kernel.
+// One block per unit (unit_kernel): small decodes, whose time is latency.
+// Held keys (hold_kernel, then the tcgen05 kernel of extend.cu): requests with many query rows.
 //
-// Math per tile, in the warp's registers, keys as MMA rows so that 8 query rows fill an
+// Math per 32 keys, in the warp's registers, keys as MMA rows so that 8 query rows fill an
 // n = 8 tile: S^T = K q^T, then P^T through movmatrix, O^T += V^T P^T, all m16n8k16 with
-// fp16 operands and fp32 sums.  A code times its block scale is exact in fp16; q (bf16) is
-// taken into fp16 exactly too, after a power of two per row that brings its largest
-// magnitude to [64, 128) (elements 2^-30 below the largest lose bits).  The dims are
-// assigned to the MMA's contraction (and output row) indices so that a lane reads
+// fp16 operands and fp32 sums.  (A decode has 1 to 16 rows per kv head: the 128 rows of a
+// tcgen05 tile would be mostly padding, and K and V would first have to be written out to
+// shared memory as 16-bit values, 3.6 times what is read.)  A code times its block scale is exact in fp16; q
+// (bf16) is taken into fp16 exactly too, after a power of two per row that brings its
+// largest magnitude to [64, 128) (elements 2^-30 below the largest lose bits).  The
+// dims are assigned to the MMA's contraction (and output row) indices so that a lane reads
 // contiguous codes: lane (r, c) = (lane / 4, lane % 4) holds dims D/4 c ... of key row r for
 // K, and dims D/8 r ... of keys of column c for V.  Softmax in base 2 with a running
-// maximum per row that is raised only past 2^8.  The instructions, not the copies, are what
-// a tile costs most (a conversion of two codes issues every second cycle), so V's codes of
-// two keys are interleaved before they are converted: a conversion then gives the pair
-// of keys that the MMA wants (half the permutes).
+// maximum per row that is raised only past 2^8; P is rounded to fp16 (by at most 2^-11 of a
+// weight, where the bf16 kernels' P has 2^-8).
+//
+// What bounds it: instructions as much as bytes.  At D = 128 a tile of 64 keys has 256
+// conversions of two codes, which issue every second cycle, and 256 fp16 products at the
+// same rate; an SM makes a tile in 174 ns, and its share of the copy rate is one in 206.
+// Hence V's codes of two keys are interleaved before they are converted (a conversion then
+// gives the pair of keys that the MMA wants, for half the permutes), the maximum is looked
+// for across lanes only when some score passes it, and a step is 32 keys: 16 need fewer
+// registers and less code but took 71 us where 32 take 66 (16 requests x 16384 keys x 8 kv
+// heads), 64 gained 4 % on long requests of 64 dims and lost as much on short ones.
+// Measured at 8 kv heads of 128, 32 query heads, page size 64: 128 requests of 128 to 16384
+// keys 98 us, 5.1 TB/s, fixed costs included; 90 % of the copy rate per further request.
+// Some 19 us of a call do not depend on the keys: start and tile table 6, first copies and
+// last tiles, merge 5.
 #include <algorithm>
 #include <cmath>
 
@@ -1159,7 +1173,8 @@ __global__ void __launch_bounds__(warps_per_sm(D, NT) * 32, 1) unit_kernel(const
 // Combines the partials of the units that span boundaries cut: o = sum 2^(m_i - M) o_i /
 // sum 2^(m_i - M) l_i.  A block per boundary; the P - 1 boundaries that cut a unit into P
 // partials share its outputs (four dims of a row each) evenly, and where that leaves
-// threads over, 2, 4 ... 32 of them share an output's partials.
+// threads over, 2, 4 ... 32 of them share an output's partials.  Its time (5 us alone, 11 us with
+// a cold cache) is the latency of the records and then of the partials.
 constexpr int kMergeThreads = 128;
 
 template <int D, int NT>
@@ -1229,7 +1244,9 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
 // extend.cu: per key and head that moves 4.6 D bytes once, against 4 D flops for each of the
 // many rows.  Layout [D/64][kv heads][rows][64], request after request.  A key whose V
 // holds a NaN block gets a NaN K and a zero V: a zero weight times NaN would reach rows that
-// do not see the key.
+// do not see the key.  A thread takes 16 dims of a key and writes 32 bytes, a whole sector; six
+// blocks of 256 threads fill an SM.  Bound by the writes: 20325 keys of 8 requests x 8 kv heads of
+// 128 (83 MB written, 23 MB read) 27 us with a cold cache.
 constexpr int kHoldThreads = 256, kHoldCtas = 6;   // threads of a block, blocks per SM
 
 struct HoldParams {
