@@ -271,6 +271,62 @@ def test_a_batch_past_the_held_tables(B):
     check(cache, q, out, lse, rows, only=[0, 1, 2050, batch - 1])
 
 
+def test_many_rows_of_a_request_without_keys(B):
+    """The copied-keys path where one request has no key at all, and where none has."""
+    rng = np.random.default_rng(70)
+    for lens in ([0, 300], [0, 0]):
+        cache = Cache(rng, lens, 16, 2, 64)
+        q = to_bf16(values(rng, (400, 4, 64)))
+        ends = np.concatenate([np.zeros(200), rng.integers(0, lens[1] + 1, 200)]).astype(np.int32)
+        out, lse, e = extend(B, cache, q, [200, 200], kv_end=ends)
+        assert e == 0
+        assert (out[:200] == 0).all() and (lse[:200] == -float("inf")).all()
+        check(cache, q, out, lse, [200, 200], kv_end=ends)
+
+
+def test_equal_rows_for_one_slot(B):
+    """A slot named twice with the same row holds that row."""
+    rng = np.random.default_rng(71)
+    ps, H, D = 16, 2, 64
+    x = values(rng, (40, H, D))
+    slots = rng.permutation(48)[:20].astype(np.int32)
+    x[20:] = x[:20]
+    pool = torch.zeros((3, H, R.tile_bytes(ps, D)), dtype=torch.uint8, device=DEV)
+    want = pool.cpu().numpy()
+    g = np.array([0.5, 0.02], dtype=np.float32)
+    for part in (0, 1):
+        R.write(want, ps, slots, part, *R.quantise(x[:20], g))
+    err = torch.zeros(1, dtype=torch.int32, device=DEV)
+    B.pkv_quant_store(pool, to_bf16(x), to_bf16(x), up(np.concatenate([slots, slots])), err, page_size=ps, k_scale=up(g),
+                      v_scale=up(g))
+    assert err.item() == 0 and (pool.cpu().numpy() == want).all()
+
+
+def test_two_calls_at_once(B):
+    """Two streams, each with its own workspace: decodes beside many-row steps, again and again."""
+    rng = np.random.default_rng(72)
+    cache = Cache(rng, [900, 30, 400, 2000], 16, 2, 128)
+    rows = [200, 3, 100, 64]
+    qd, qe = to_bf16(values(rng, (4, 8, 128))), to_bf16(values(rng, (sum(rows), 8, 128)))
+    calls = []
+    for q, extra, size, call in (
+            (qd, {}, B.pkv_quant_decode_workspace_size, B.pkv_quant_decode),
+            (qe, dict(qo_indptr=up(np.concatenate([[0], np.cumsum(rows)]).astype(np.int32))),
+             B.pkv_quant_extend_workspace_size, B.pkv_quant_extend)):
+        out, lse = torch.zeros_like(q), torch.zeros(q.shape[:2], dtype=torch.float32, device=DEV)
+        a = cache.args(B, "table", q, out, lse=lse, **extra)
+        calls.append((call, a, torch.empty(size(a), dtype=torch.uint8, device=DEV),
+                      torch.zeros(1, dtype=torch.int32, device=DEV), out, lse, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    for _ in range(30):
+        for call, a, ws, err, _, _, stream in calls:
+            call(a, ws, err, stream=stream)
+    torch.cuda.synchronize()
+    for i, (_, _, _, err, out, lse, _) in enumerate(calls):
+        assert err.item() == 0
+        check(cache, qe if i else qd, out, lse, rows if i else None)
+
+
 def test_a_serving_batch_on_its_own_stream(B):
     """Calls on a stream that is not the current one, tensors made on another."""
     rng = np.random.default_rng(66)
