@@ -7,7 +7,7 @@
 // requests' lengths.  A warp works alone: it copies the tiles of its span into its own ring
 // of stages, and no warp waits for another.  A unit inside one span is written by its warp;
 // one that a span boundary cuts leaves an fp32 partial per span for merge_kernel.
-// One block per unit (unit_kernel): small decodes, whose time is latency.
+// One block per unit (unit_kernel): small calls, whose time is latency.
 // Held keys (hold_kernel, then the tcgen05 kernel of extend.cu): requests with many query rows.
 //
 // Math per 32 keys, in the warp's registers, keys as MMA rows so that 8 query rows fill an
@@ -1014,12 +1014,14 @@ __global__ void __launch_bounds__(warps_per_sm(D, NT) * 32, 1) attend_kernel(con
     }
 }
 
-// ---------------------------------------------------------------- small decodes
-// One block per unit (request and kv head; one query row each): its warps take the tiles in
-// turn and combine their states in shared memory, in one launch with no table of tiles before
-// and no merge after it.  For calls whose time is latency: 4 requests of up to 255 keys x 8
-// kv heads take 7 us so and 12 us with spans; with more work the spans' even shares win.
-template <int D, int NT, int kT>
+// ---------------------------------------------------------------- small calls
+// One block per unit: its warps take the tiles in turn and combine their states in shared
+// memory, in one launch with no table of tiles before and no merge after it (a request of more
+// row blocks than the host expects: each block takes several in turn).  For calls whose time
+// is latency: 4 requests of up to 255 keys x 8 kv heads take 7 us so and 12 us with spans;
+// with more work the spans' even shares win.
+// kRows: query rows by qo_indptr; else one per request (known to the compiler, 0.4 us of 7).
+template <int D, int NT, int kT, bool kRows>
 __global__ void __launch_bounds__(warps_per_sm(D, NT) * 32, 1) unit_kernel(const Params p) {
     constexpr int kWarps = warps_per_sm(D, NT), S = ring_stages(D, NT);
     extern __shared__ __align__(128) uint8_t smem[];
@@ -1038,135 +1040,168 @@ __global__ void __launch_bounds__(warps_per_sm(D, NT) * 32, 1) unit_kernel(const
     __syncwarp();
     pdl_wait();          // inputs may come from the previous kernel of the stream
     pdl_launch_next();
-    const int b = blockIdx.x / p.hkv, kh = blockIdx.x - b * p.hkv;
-    if (blockIdx.x == 0 && warp < 2) {   // unusable head scales
+    const int b = blockIdx.x, kh = blockIdx.y;
+    const int rb0 = kRows ? blockIdx.z : 0;
+    const bool first = kh == 0 && rb0 == 0;
+    if (first && b == 0 && warp < 2) {   // unusable head scales
         const float *g = warp ? p.v_scale : p.k_scale;
         for (int h = lane; g && h < p.hkv; h += 32)
             if (!quant::good_scale(g[h])) raise_flag(p.err, PKV_DEVERR_RANGE);
     }
-    int64_t base;
-    const int L = quant::key_count(p.tab, b, base, p.err, kh == 0 && threadIdx.x == 0);
-    const int tiles = (L + kTile - 1) / kTile;
-    const Work w{kh, 0, L, 1, b, 0, tiles, L, -1, {0, 0, 0}};
-    uint32_t q_raw[D / 8];
-    if (NT == 1) load_q<D, NT>(p, w, 0, q_raw, lane);
-    // slots of the pieces of tile t: piece lane, + 32
-    auto look_up = [&](int t, int (&slot)[2]) {
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int64_t key = (static_cast<int64_t>(t) << 6) + (static_cast<int64_t>(32 * i + lane) << shift);
-            slot[i] = 32 * i + lane < pieces && key < L ? static_cast<int>(quant::slot_of(p.tab, base, static_cast<int>(key))) : -3;
-        }
-    };
-    auto fetch = [&](const int (&slot)[2], int stage) {
-        uint8_t *dst = ring + stage * stage_bytes;
-        const uint8_t *src[2];
-        uint32_t live = 0;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            src[i] = slot[i] >= 0 ? p.pool + static_cast<int64_t>(slot[i] >> shift) * p.tile_stride + static_cast<int64_t>(kh) * bytes
-                                  : nullptr;
-            live += __popc(__ballot_sync(0xffffffffu, slot[i] >= 0));
-            if (slot[i] == -1 || slot[i] == -2) {   // a bad page reads as zeros
-                raise_flag(p.err, slot[i] == -1 ? PKV_DEVERR_RANGE : PKV_DEVERR_CONTIG);
-                zero_piece<D, kT>(dst, 32 * i + lane, shift);
-                fence_proxy_async_smem();   // before later copies into this stage
-            }
-        }
-        if (!gathers<kT>(shift)) {
-            if (lane == 0) mbar_arrive_expect_tx(&bar[stage], live * bytes);
-            __syncwarp();
-        }
-        if (kT != 0) {
-#pragma unroll
-            for (int i = 0; i < 2; ++i)
-                if (src[i]) bulk_load(dst + (32 * i + lane) * bytes, src[i], bytes, &bar[stage]);
-        } else {
-            copy_parts<D>(src, 0, shift, dst, &bar[stage], lane);
-        }
-        __syncwarp();
-    };
-    int slots[S][2];
-#pragma unroll
-    for (int i = 0; i < S; ++i) look_up(warp + i * kWarps, slots[i]);
-#pragma unroll
-    for (int i = 0; i < S; ++i)
-        if (warp + i * kWarps < tiles) fetch(slots[i], i);
-    State<D, NT> st;
-    start_segment<D, NT>(p, w, st, q_raw, lane);
-    bool ok = true;
-    int stage = 0, phase = 0, t = warp;
-    for (; t < tiles; t += kWarps) {
-        int next[2];
-        look_up(t + S * kWarps, next);
-        ok = __all_sync(0xffffffffu, wait_for(&bar[stage], phase, p.wait_ns));
-        if (!ok) break;
-#pragma unroll 1
-        for (int h = 0; h < kTile / kStep; ++h) {
-            const int k = t * kTile + h * kStep;
-            if (k + kStep <= L)
-                tile_step<D, NT, kT, false>(p, st, ring + stage * stage_bytes, h, k, L, lane);
-            else if (k < L)
-                tile_step<D, NT, kT, true>(p, st, ring + stage * stage_bytes, h, k, L, lane);
-        }
-        __syncwarp();
-        if (t + S * kWarps < tiles) fetch(next, stage);
-        if (++stage == S) {
-            stage = 0;
-            phase ^= 1;
-        }
+    Req req;
+    if (kRows) {
+        req = load_req(p, b, first && threadIdx.x == 0);
+    } else {
+        req.L = quant::key_count(p.tab, b, req.base, p.err, first && threadIdx.x == 0);
+        req.n = 1;
+        req.qo0 = b;
     }
-    if (!ok) {   // a wait ran out: the copies in flight land before the block's memory is given back
-        if (lane == 0) raise_flag(p.err, PKV_DEVERR_TIMEOUT);
-        for (int i = 0; i < S && t < tiles; ++i, t += kWarps) {
-            mbar_wait(&bar[stage], phase);
+    const int64_t base = req.base;
+    const int rows = kRows ? req.n * p.g : p.g;
+    bool ok = true;
+    int stage = 0, phase = 0;
+    for (int rb = rb0; !kRows || rb * 8 * NT < rows; rb += gridDim.z) {
+        Unit u{};
+        u.rb = rb;
+        u.L = req.L;
+        u.n = req.n;
+        const int keys = kRows ? unit_keys<NT>(p, u) : req.L, tiles = (keys + kTile - 1) / kTile;
+        const Work w{kh, rb, req.L, req.n, req.qo0, 0, tiles, keys, -1, {0, 0, 0}};
+        uint32_t q_raw[D / 8];
+        if (NT == 1) load_q<D, NT>(p, w, 0, q_raw, lane);
+        // slots of the pieces of tile t: piece lane, + 32
+        auto look_up = [&](int t, int (&slot)[2]) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int64_t key = (static_cast<int64_t>(t) << 6) + (static_cast<int64_t>(32 * i + lane) << shift);
+                slot[i] = 32 * i + lane < pieces && key < keys ? static_cast<int>(quant::slot_of(p.tab, base, static_cast<int>(key))) : -3;
+            }
+        };
+        auto fetch = [&](const int (&slot)[2], int stage) {
+            uint8_t *dst = ring + stage * stage_bytes;
+            const uint8_t *src[2];
+            uint32_t live = 0;
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                src[i] = slot[i] >= 0 ? p.pool + static_cast<int64_t>(slot[i] >> shift) * p.tile_stride + static_cast<int64_t>(kh) * bytes
+                                      : nullptr;
+                live += __popc(__ballot_sync(0xffffffffu, slot[i] >= 0));
+                if (slot[i] == -1 || slot[i] == -2) {   // a bad page reads as zeros
+                    raise_flag(p.err, slot[i] == -1 ? PKV_DEVERR_RANGE : PKV_DEVERR_CONTIG);
+                    zero_piece<D, kT>(dst, 32 * i + lane, shift);
+                    fence_proxy_async_smem();   // before later copies into this stage
+                }
+            }
+            if (!gathers<kT>(shift)) {
+                if (lane == 0) mbar_arrive_expect_tx(&bar[stage], live * bytes);
+                __syncwarp();
+            }
+            if (kT != 0) {
+#pragma unroll
+                for (int i = 0; i < 2; ++i)
+                    if (src[i]) bulk_load(dst + (32 * i + lane) * bytes, src[i], bytes, &bar[stage]);
+            } else {
+                copy_parts<D>(src, 0, shift, dst, &bar[stage], lane);
+            }
+            __syncwarp();
+        };
+        int slots[S][2];
+#pragma unroll
+        for (int i = 0; i < S; ++i) look_up(warp + i * kWarps, slots[i]);
+#pragma unroll
+        for (int i = 0; i < S; ++i)
+            if (ok && warp + i * kWarps < tiles) fetch(slots[i], (stage + i) % S);
+        State<D, NT> st;
+        start_segment<D, NT>(p, w, st, q_raw, lane);
+        int low = req.L;   // every row sees the keys below it
+        if (kRows) {
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int v = 0; v < 2; ++v) low = min(low, st.end[n][v]);
+            low = __reduce_min_sync(0xffffffffu, low);
+        }
+        const bool was_ok = ok;
+        int t = warp;
+        for (; ok && t < tiles; t += kWarps) {
+            int next[2];
+            look_up(t + S * kWarps, next);
+            ok = __all_sync(0xffffffffu, wait_for(&bar[stage], phase, p.wait_ns));
+            if (!ok) break;
+#pragma unroll 1
+            for (int h = 0; h < kTile / kStep; ++h) {
+                const int k = t * kTile + h * kStep;
+                if (k + kStep <= low)
+                    tile_step<D, NT, kT, false>(p, st, ring + stage * stage_bytes, h, k, keys, lane);
+                else if (k < keys)
+                    tile_step<D, NT, kT, true>(p, st, ring + stage * stage_bytes, h, k, keys, lane);
+            }
+            __syncwarp();
+            if (t + S * kWarps < tiles) fetch(next, stage);
             if (++stage == S) {
                 stage = 0;
                 phase ^= 1;
             }
         }
-    }
-    // the warps' states, each over its own (drained) ring
-    float *red = reinterpret_cast<float *>(ring);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int v = 0; v < 2; ++v) {
-            float l = st.l[n][v];
-#pragma unroll
-            for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-            const int row = n * 8 + 2 * c + v;
-            if (r == 0) ml[warp][row] = make_float2(l == 0.f ? -INFINITY : -st.nm[n][v], l);
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i)
-                *reinterpret_cast<float2 *>(red + row * D + r * (D / 8) + 2 * i) = make_float2(st.o[i][n][v], st.o[i][n][2 + v]);
+        if (was_ok && !ok) {   // a wait ran out: the copies in flight land before the block's memory is given back
+            if (lane == 0) raise_flag(p.err, PKV_DEVERR_TIMEOUT);
+            for (int i = 0; i < S && t < tiles; ++i, t += kWarps) {
+                mbar_wait(&bar[stage], phase);
+                if (++stage == S) {
+                    stage = 0;
+                    phase ^= 1;
+                }
+            }
         }
-    __syncthreads();
-    const float gv = p.v_scale ? p.v_scale[kh] : 1.f;
-    for (int e = threadIdx.x; e < p.g * (D / 4); e += kWarps * 32) {
-        const int row = e / (D / 4), d0 = e % (D / 4) * 4;
-        float m = -INFINITY, l = 0.f;
+        // the warps' states, each over its own (drained) ring
+        float *red = reinterpret_cast<float *>(ring);
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) m = fmaxf(m, ml[i][row].x);
-        const float base_m = m == -INFINITY ? 0.f : m;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int n = 0; n < NT; ++n)
 #pragma unroll
-        for (int i = 0; i < kWarps; ++i) {
-            const float2 x = ml[i][row];
-            if (x.y == 0.f) continue;   // no key of the row
-            const float wgt = ex2(x.x - base_m);
-            const float4 y = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem + static_cast<uint32_t>(i * S) * stage_bytes) + row * D + d0);
-            l = fmaf(x.y, wgt, l);
-            o.x = fmaf(y.x, wgt, o.x);
-            o.y = fmaf(y.y, wgt, o.y);
-            o.z = fmaf(y.z, wgt, o.z);
-            o.w = fmaf(y.w, wgt, o.w);
+            for (int v = 0; v < 2; ++v) {
+                float l = st.l[n][v];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                const int row = n * 8 + 2 * c + v;
+                if (r == 0) ml[warp][row] = make_float2(l == 0.f ? -INFINITY : -st.nm[n][v], l);
+#pragma unroll
+                for (int i = 0; i < D / 16; ++i)
+                    *reinterpret_cast<float2 *>(red + row * D + r * (D / 8) + 2 * i) = make_float2(st.o[i][n][v], st.o[i][n][2 + v]);
+            }
+        __syncthreads();
+        const float gv = p.v_scale ? p.v_scale[kh] : 1.f;
+        const int live = min(8 * NT, rows - rb * 8 * NT);
+        for (int e = threadIdx.x; e < live * (D / 4); e += kWarps * 32) {
+            const int row = e / (D / 4), d0 = e % (D / 4) * 4;
+            float m = -INFINITY, l = 0.f;
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) m = fmaxf(m, ml[i][row].x);
+            const float base_m = m == -INFINITY ? 0.f : m;
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kWarps; ++i) {
+                const float2 x = ml[i][row];
+                if (x.y == 0.f) continue;   // no key of the row
+                const float wgt = ex2(x.x - base_m);
+                const float4 y = *reinterpret_cast<const float4 *>(reinterpret_cast<const float *>(smem + static_cast<uint32_t>(i * S) * stage_bytes) + row * D + d0);
+                l = fmaf(x.y, wgt, l);
+                o.x = fmaf(y.x, wgt, o.x);
+                o.y = fmaf(y.y, wgt, o.y);
+                o.z = fmaf(y.z, wgt, o.z);
+                o.w = fmaf(y.w, wgt, o.w);
+            }
+            const int r0 = rb * 8 * NT + row, tok = kRows ? token_of(p, r0) : 0;
+            const int64_t at = static_cast<int64_t>(req.qo0 + tok) * p.hq + kh * p.g + (r0 - tok * p.g);
+            const float inv = l == 0.f ? 0.f : gv / l;
+            *reinterpret_cast<uint2 *>(p.out + at * D + d0) =
+                make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+            if (d0 == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
-        const int64_t at = static_cast<int64_t>(b) * p.hq + kh * p.g + row;
-        const float inv = l == 0.f ? 0.f : gv / l;
-        *reinterpret_cast<uint2 *>(p.out + at * D + d0) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (d0 == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
+        if (!kRows) break;
+        if ((rb + static_cast<int>(gridDim.z)) * 8 * NT < rows) {
+            fence_proxy_async_smem();   // the states, before the next rows' copies over them
+            __syncthreads();
+        }
     }
 }
 
@@ -1418,14 +1453,15 @@ static pkv_status validate(const char *who, const pkv_quant_args *a, bool extend
     return PKV_OK;
 }
 
-// How a call runs: the span kernel (its rows per unit, grid, spans), and for requests with
-// many query rows the held path; with the workspace of each.
+// How a call runs: a block per unit, or the span kernel (its rows per unit, grid, spans), and
+// for requests with many query rows the held path; with the workspace of each.
 constexpr int kHeldRows = 128;     // rows per request and kv head up to which the span kernel is used
 constexpr int kHeldBatch = 4096;   // requests whose tables fit the held path's shared memory
 
 struct Plan {
     bool unit, spans, held, plan_launch;
-    int nt, grid, spans_max, span_tiles;
+    int nt, spans_max, span_tiles;
+    dim3 grid;
     size_t smem, part_o, part_ml, cuts, table;          // span kernel
     size_t hold_k, hold_first, ext;                     // held path: one of the two tensors, row table, extend.cu's own
     int64_t hold_rows;
@@ -1477,24 +1513,28 @@ static bool make_plan(const pkv_quant_args *a, bool extend, Plan &pl) {
     pl.held = extend && rows > kHeldRows && a->batch <= kHeldBatch && batch * a->max_seq_len <= INT32_MAX &&
               pl.hold_rows <= INT32_MAX / (static_cast<int64_t>(a->num_kv_heads) * (a->head_dim / 64));
     const int64_t sms = std::max(1, sm_count());
-    if (!extend && a->kv_chunk == 0) {
+    if (!pl.held && a->kv_chunk == 0) {
         // What the two kernels take, in parts of about 0.75 us: a block per unit starts, then makes
-        // `rounds` of its warps over the unit's tiles, unit after unit where there are more than
-        // SMs; spans start more slowly, share the tiles evenly and are merged.  The longest request
+        // `rounds` of its warps over the unit's tiles, unit after unit where there are more than SMs;
+        // spans start more slowly, share the tiles evenly and are merged.  The longest request
         // counts for the first, the sum for the second (total_kv, or half of what max_seq_len
-        // allows: lengths are rarely equal).  Measured (8 kv
-        // heads of 128, us; unit / spans): 16 x 768 keys 7.0 / 12.9, 16 x 3000 17.7 / 24.8, 32 x 700
-        // 12.7 / 15.8, 4 x 2048 11.5 / 12.5, but 64 x 256 18.3 / 15.0 and 64 x 64 17.5 / 10.3.
-        const int warps = warps_per_sm(a->head_dim, g <= 8 ? 1 : 2);
-        const int64_t units = batch * a->num_kv_heads, tiles = (std::max(1, a->max_seq_len) + kTile - 1) / kTile;
+        // allows: lengths are rarely equal).  Measured (8 kv heads of 128, us; unit / spans): decodes of
+        // 16 x 768 keys 7.0 / 12.9, 16 x 3000 17.7 / 24.8, 32 x 700 12.7 / 15.8, 4 x 2048 11.5 / 12.5, but
+        // 64 x 256 18.3 / 15.0 and 64 x 64 17.5 / 10.3; 16 rows per head, 4 x 512 keys 9.0 / 15.1, 16 x 2000
+        // 17.4 / 25.8, 32 x 256 15.0 / 19.4; 48 rows, 4 x 1000 11.9 / 18.6.
+        const int nt = rows <= 8 ? 1 : 2, warps = warps_per_sm(a->head_dim, nt);
+        const int64_t blocks = (rows + 8 * nt - 1) / (8 * nt), units = batch * a->num_kv_heads * blocks;
+        const int64_t tiles = (std::max(1, a->max_seq_len) + kTile - 1) / kTile;
         const int64_t rounds = (tiles + warps - 1) / warps, waves = (units + sms - 1) / sms;
-        const int64_t all = (a->total_kv > 0 ? a->total_kv / kTile : batch * tiles / 2) * a->num_kv_heads + units;
-        pl.unit = 5 + waves * (2 + 3 * rounds) <= 13 + 3 * ((all + sms * warps - 1) / (sms * warps));
+        const int64_t all = (a->total_kv > 0 ? std::min(a->total_kv / kTile, batch * tiles) : batch * tiles / 2) * a->num_kv_heads * blocks + units;
+        pl.unit = 5 + waves * (2 + 3 * rounds) <= 13 + 3 * ((all + sms * warps - 1) / (sms * warps)) &&
+                  a->num_kv_heads <= 65535 && blocks <= 65535;   // (sides of the grid)
     }
     pl.spans = !pl.unit && (!pl.held || batch > 1);
     if (pl.unit) {
-        pl.nt = g <= 8 ? 1 : 2;
-        pl.grid = static_cast<int>(batch * a->num_kv_heads);
+        pl.nt = rows <= 8 ? 1 : 2;
+        pl.grid = dim3(static_cast<unsigned>(batch), static_cast<unsigned>(a->num_kv_heads),
+                       static_cast<unsigned>((rows + 8 * pl.nt - 1) / (8 * pl.nt)));
         pl.smem = static_cast<size_t>(warps_per_sm(a->head_dim, pl.nt) * ring_stages(a->head_dim, pl.nt)) *
                   quant::tile_bytes(kTile, a->head_dim);
     }
@@ -1503,11 +1543,11 @@ static bool make_plan(const pkv_quant_args *a, bool extend, Plan &pl) {
         pl.nt = few <= 8 ? 1 : 2;
         const size_t stage = quant::tile_bytes(kTile, a->head_dim);
         const int warps = warps_per_sm(a->head_dim, pl.nt);
-        pl.grid = static_cast<int>(sms);
+        pl.grid = dim3(static_cast<unsigned>(sms));
         pl.plan_launch = a->batch > kTableInSmem;
         pl.smem = warps * ring_stages(a->head_dim, pl.nt) * stage;
         if (!pl.plan_launch) pl.smem += (static_cast<size_t>(a->batch) + 2) * 4 + (a->batch <= kReqInSmem ? a->batch * sizeof(Req) : 0);
-        int64_t spans = static_cast<int64_t>(pl.grid) * warps;
+        int64_t spans = sms * warps;
         // all units' tiles, at most
         const int64_t blocks = (a->total_q * g + 8 * pl.nt - 1) / (8 * pl.nt) + a->batch;
         const int64_t tiles = blocks * a->num_kv_heads * ((std::max(1, a->max_seq_len) + kTile - 1) / kTile + unit_cost(pl.nt));
@@ -1584,7 +1624,10 @@ static Params params(const pkv_quant_args *a, int32_t *err) {
 template <int D, int NT>
 static pkv_status launch(const char *who, const Params &p, const Plan &pl, cudaStream_t s) {
     auto *kern = p.t_shift == 6 ? attend_kernel<D, NT, 64> : p.t_shift == 4 ? attend_kernel<D, NT, 16> : attend_kernel<D, NT, 0>;
-    if (pl.unit) kern = p.t_shift == 6 ? unit_kernel<D, NT, 64> : p.t_shift == 4 ? unit_kernel<D, NT, 16> : unit_kernel<D, NT, 0>;
+    if (pl.unit && p.qo_indptr)
+        kern = p.t_shift == 6 ? unit_kernel<D, NT, 64, true> : p.t_shift == 4 ? unit_kernel<D, NT, 16, true> : unit_kernel<D, NT, 0, true>;
+    else if (pl.unit)
+        kern = p.t_shift == 6 ? unit_kernel<D, NT, 64, false> : p.t_shift == 4 ? unit_kernel<D, NT, 16, false> : unit_kernel<D, NT, 0, false>;
     std::atomic<int64_t> *set = device_memo(reinterpret_cast<const void *>(kern));
     if (!set) return fail(PKV_ERR_CUDA, "%s: cannot query the current device", who);
     if (set->load() < static_cast<int64_t>(pl.smem)) {   // kernel attributes are per device
@@ -1599,7 +1642,7 @@ static pkv_status launch(const char *who, const Params &p, const Plan &pl, cudaS
         st = launch_status(launch_chained(plan_kernel<NT>, dim3(1), dim3(1024), 0, s, p), who);
         if (st != PKV_OK) return st;
     }
-    st = launch_status(launch_chained(kern, dim3(pl.grid), dim3(warps_per_sm(D, NT) * 32), pl.smem, s, p), who);
+    st = launch_status(launch_chained(kern, pl.grid, dim3(warps_per_sm(D, NT) * 32), pl.smem, s, p), who);
     if (st != PKV_OK || pl.unit) return st;
     return launch_status(launch_chained(merge_kernel<D, NT>, dim3(pl.spans_max), dim3(kMergeThreads), 0, s, p), who);
 }

@@ -470,10 +470,10 @@ class ExtendStep:
 
     def launches_per_step(self) -> int:
         if self.quant is not None:
-            # spans and their merge; with many rows the copy out of the pool and its attention besides
+            # spans and their merge (small calls: one launch and the least workspace); with many rows the copy out of the pool and its attention besides
             # (alone for one request), not counting the join of the latter's pieces where it splits keys
             held = int(self.ew.qo_lens.max()) * (self.ew.num_q_heads // self.ew.num_kv_heads) > 128
-            n = 2 if not held or self.ew.batch > 1 else 0
+            n = (2 if self.ws_bytes > 256 else 1) if not held or self.ew.batch > 1 else 0
             n += 2 if held else 0
             return n + (1 if self.token_table else 2) + (1 if self.kv_end is not None else 0)
         return (2 if self.token_table else 3) + (1 if self.kv_end is not None else 0) + (1 if self.ws_bytes > 0 else 0)

@@ -6,7 +6,7 @@ import pytest
 import torch
 
 import _quant_ref as R
-from test_gpu_quant import DEV, Cache, check, decode, extend, host, to_bf16, up, values
+from test_gpu_quant import DECODE, DEV, EXTEND, Cache, check, decode, extend, host, to_bf16, up, values
 
 pytestmark = pytest.mark.gpu
 
@@ -269,6 +269,53 @@ def test_a_batch_past_the_held_tables(B):
     out, lse, e = extend(B, cache, q, rows, max_q_len=33)
     assert e == 0
     check(cache, q, out, lse, rows, only=[0, 1, 2050, batch - 1])
+
+
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("max_q", [0, 1])
+@pytest.mark.parametrize("D,ps,H,g,lens,rows", [
+    (128, 16, 8, 4, [300, 40, 5, 1000], [4, 1, 3, 8]), (64, 1, 2, 1, [70, 9, 0], [1, 9, 0]), (128, 1, 4, 8, [200], [5]),
+    (64, 64, 20, 2, [130, 64, 65], [4, 4, 4]), (128, 32, 2, 7, [33, 900], [2, 2]), (64, 8, 1, 16, [2000], [7]),
+    (128, 2, 3, 3, [1, 2, 3, 100], [1, 2, 3, 4]), (64, 4, 8, 5, [17], [3]), (128, 128, 1, 4, [400, 0, 129], [16, 0, 2])])
+def test_small_multi_row_calls(B, D, ps, H, g, lens, rows, max_q, given):
+    """One launch, a block per request and kv head; max_q = 1 makes it go over the rows 8 or 16 at a time."""
+    rng = np.random.default_rng(73 + D + ps + H)
+    cache = Cache(rng, lens, ps, H, D)
+    q = to_bf16(values(rng, (sum(rows), H * g, D)))
+    ends = None
+    if given:
+        ends = np.concatenate([rng.integers(0, n + 1, r) for n, r in zip(lens, rows)]).astype(np.int32)
+        ends[::3] = 0
+    probe = cache.args(B, "table", q, torch.zeros_like(q), max_q_len=max_q,
+                       qo_indptr=up(np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)))
+    if max_q == 1:   # (with more rows announced, the spans may be the better choice)
+        assert B.pkv_quant_extend_workspace_size(probe) == 256
+    out, lse, e = extend(B, cache, q, rows, "table", ends, max_q_len=max_q)
+    assert e == 0
+    check(cache, q, out, lse, rows, ends)
+
+
+@pytest.mark.parametrize("case", [c[:-1] for c in DECODE if c[-1] == 0])
+def test_decode_in_spans(B, case):
+    D, ps, H, g, lens, layout = case
+    rng = np.random.default_rng(74 + D + ps + H)
+    cache = Cache(rng, lens, ps, H, D)
+    q = to_bf16(values(rng, (len(lens), H * g, D)))
+    out, lse, e = decode(B, cache, q, layout, kv_chunk=128)
+    assert e == 0
+    check(cache, q, out, lse)
+
+
+@pytest.mark.parametrize("case", [c[:-1] for c in EXTEND if c[-1] == 0 and max(c[5]) * c[3] <= 128])
+def test_extend_in_spans(B, case):
+    D, ps, H, g, lens, rows, layout = case
+    rng = np.random.default_rng(75 + D + ps + H)
+    cache = Cache(rng, lens, ps, H, D)
+    q = to_bf16(values(rng, (sum(rows), H * g, D)))
+    for chunk in (64, 256):
+        out, lse, e = extend(B, cache, q, rows, layout, kv_chunk=chunk)
+        assert e == 0
+        check(cache, q, out, lse, rows)
 
 
 def test_many_rows_of_a_request_without_keys(B):
