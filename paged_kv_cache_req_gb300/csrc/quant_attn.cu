@@ -1506,7 +1506,7 @@ static bool make_plan(const pkv_quant_args *a, bool extend, Plan &pl) {
     const int g = a->num_q_heads / a->num_kv_heads;
     const int64_t batch = std::max(a->batch, 1), total_q = std::max<int64_t>(a->total_q, 1);
     // rows of a request and kv head: at most max_q_len's, or what the average says
-    const int64_t rows = (extend && a->max_q_len > 0 ? a->max_q_len : (total_q + batch - 1) / batch) * g;
+    const int64_t rows = (extend && a->max_q_len > 0 ? std::min<int64_t>(a->max_q_len, total_q) : (total_q + batch - 1) / batch) * g;
     // (a batch too large for the held path's tables, or keys past its counters and coordinates, take
     // the spans whatever their rows)
     pl.hold_rows = std::max<int64_t>(1, a->total_kv > 0 ? a->total_kv : batch * a->max_seq_len);
@@ -1522,13 +1522,16 @@ static bool make_plan(const pkv_quant_args *a, bool extend, Plan &pl) {
         // 16 x 768 keys 7.0 / 12.9, 16 x 3000 17.7 / 24.8, 32 x 700 12.7 / 15.8, 4 x 2048 11.5 / 12.5, but
         // 64 x 256 18.3 / 15.0 and 64 x 64 17.5 / 10.3; 16 rows per head, 4 x 512 keys 9.0 / 15.1, 16 x 2000
         // 17.4 / 25.8, 32 x 256 15.0 / 19.4; 48 rows, 4 x 1000 11.9 / 18.6.
+        // (Calls of more units than a grid's side take the spans in any case.)
         const int nt = rows <= 8 ? 1 : 2, warps = warps_per_sm(a->head_dim, nt);
         const int64_t blocks = (rows + 8 * nt - 1) / (8 * nt), units = batch * a->num_kv_heads * blocks;
-        const int64_t tiles = (std::max(1, a->max_seq_len) + kTile - 1) / kTile;
-        const int64_t rounds = (tiles + warps - 1) / warps, waves = (units + sms - 1) / sms;
-        const int64_t all = (a->total_kv > 0 ? std::min(a->total_kv / kTile, batch * tiles) : batch * tiles / 2) * a->num_kv_heads * blocks + units;
-        pl.unit = 5 + waves * (2 + 3 * rounds) <= 13 + 3 * ((all + sms * warps - 1) / (sms * warps)) &&
-                  a->num_kv_heads <= 65535 && blocks <= 65535;   // (sides of the grid)
+        if (units <= 65535) {
+            const int64_t tiles = (std::max(1, a->max_seq_len) + kTile - 1) / kTile;
+            const int64_t rounds = (tiles + warps - 1) / warps, waves = (units + sms - 1) / sms;
+            const int64_t of_all = a->total_kv > 0 ? std::min(a->total_kv / kTile, batch * tiles) : batch * tiles / 2;
+            const int64_t all = of_all * a->num_kv_heads * blocks + units;
+            pl.unit = 5 + waves * (2 + 3 * rounds) <= 13 + 3 * ((all + sms * warps - 1) / (sms * warps));
+        }
     }
     pl.spans = !pl.unit && (!pl.held || batch > 1);
     if (pl.unit) {

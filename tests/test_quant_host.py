@@ -186,3 +186,17 @@ def test_binding_refuses_wrong_tensors(B):
             B.make_quant_args(B.PKV_LAYOUT_BLOCK_TABLE, qq, pool, oo, **ok)
     with pytest.raises(ValueError):      # device tensors only
         B.pkv_quant_store(pool, kv, kv, slots, err, page_size=16)
+
+
+def test_sizes_with_far_hints(B):
+    """Upper bounds far above the real sizes plan as the real sizes do, or for the spans; sizes past the limits are refused."""
+    big = 2 ** 31 - 1
+    size = B.pkv_quant_extend_workspace_size
+    base = dict(qo_indptr=256, total_q=40, max_q_len=40)
+    assert size(_args(B, **dict(base, max_q_len=big))) == size(_args(B, **base)) > 256
+    assert size(_args(B, **dict(base, total_kv=2 ** 62))) > 0            # (keys past the copies' coordinates: spans)
+    assert size(_args(B, **dict(base, total_kv=2 ** 62, max_q_len=1))) >= 256
+    assert B.pkv_quant_decode_workspace_size(_args(B, total_kv=2 ** 62)) >= 256
+    # 2^28 (row, head) pairs, or 2^31 (request, kv head) pairs
+    assert size(_args(B, qo_indptr=256, total_q=2 ** 25)) == 0
+    assert size(_args(B, qo_indptr=256, batch=2 ** 30, total_q=2)) == 0
