@@ -69,6 +69,13 @@ __device__ __forceinline__ uint2 quantise(const uint32_t (&w)[8], float g, uint3
 // Both are bound by memory, the conversions next (ALU half busy).  Stored and read back: 86,000
 // tokens x 20 heads of 64 (1.13 GB in all) 210 us, 5.4 TB/s; 8192 x 8 heads of 128 (86 MB) 24 us.
 __host__ __device__ inline int row_iters(int head_dim, int hkv) { return (2 * hkv * (head_dim / kBlock) + 31) / 32; }
+// log2 of the tokens that share a warp, where a token has half a warp's blocks or fewer (one kv
+// head, or two of 64 dims): 262,144 tokens of one head of 128 read back 77 us with one to a
+// warp, 44 with two; of 64, 77 and 24 us with four.
+inline int row_pack(int head_dim, int hkv) {
+    const int blocks = 2 * hkv * (head_dim / kBlock);
+    return blocks < 32 && is_pow2(blocks) ? 5 - ilog2(blocks) : 0;
+}
 inline int64_t row_parts(int64_t tokens, int iters) {
     const int64_t want = 48ll * std::max(1, sm_count());   // warps that the device holds
     return std::max<int64_t>(1, std::min<int64_t>(iters, want / std::max<int64_t>(1, tokens)));
@@ -79,13 +86,14 @@ __global__ void __launch_bounds__(kThreads)
 store_kernel(uint8_t *__restrict__ pool, int64_t num_slots, int64_t tile_stride, int t_shift, int32_t hkv,
              const float *__restrict__ k_scale, const float *__restrict__ v_scale,
              const uint16_t *__restrict__ k_new, const uint16_t *__restrict__ v_new, int64_t k_stride,
-             int64_t v_stride, const int32_t *__restrict__ slot_mapping, uint32_t n, uint32_t parts,
+             int64_t v_stride, const int32_t *__restrict__ slot_mapping, uint32_t n, uint32_t parts, int pack,
              int32_t *__restrict__ err) {
     pdl_wait();          // inputs may come from the previous kernel of the stream
     pdl_launch_next();
     constexpr int kPerRow = D / kBlock;
-    const uint32_t item = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), i = item / parts;
-    const int part = static_cast<int>(item - i * parts), lane = threadIdx.x & 31, j = lane % kPerRow;
+    const uint32_t item = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5), token = item / parts;
+    const int part = static_cast<int>(item - token * parts), lane = threadIdx.x & (31 >> pack), j = lane % kPerRow;
+    const uint32_t i = (token << pack) + ((threadIdx.x & 31) >> (5 - pack));
     if (i >= n) return;
     const int64_t slot = slot_mapping[i];
     if (slot < 0) return;   // a padded token
@@ -170,7 +178,7 @@ struct GatherParams {
     const float *k_scale, *v_scale;
     const int32_t *r2t, *req_pool_idx, *kv_start, *seq_lens;
     int64_t r2t_rows, r2t_stride, r2t_width, cap;
-    int32_t parts;
+    int32_t parts, pack;
     uint16_t *k_out, *v_out;
     int32_t *cu_seqlens, *err;
 };
@@ -183,9 +191,10 @@ struct GatherParams {
 // writes; 15,700 x 8 heads of 128 (65 MB of 82) 21 us.
 constexpr int kGatherCtas = 5;   // per SM
 
-// kWhole: a warp takes two whole tokens in turn (neighbours share the sectors of their scales);
-// else one part of one.
-template <int D, bool kVec, bool kWhole>
+// kTokens: a warp takes two whole tokens in turn (neighbours share the sectors of their scales);
+// kPacked: so do the lanes of it that a small token needs; kParts: one part of one token.
+enum { kParts, kTokens, kPacked };
+template <int D, bool kVec, int kMode>
 __global__ void __launch_bounds__(kThreads, kGatherCtas) gather_kernel(const GatherParams p) {
     pdl_wait();          // inputs may come from the previous kernel of the stream
     pdl_launch_next();
@@ -193,12 +202,14 @@ __global__ void __launch_bounds__(kThreads, kGatherCtas) gather_kernel(const Gat
     __shared__ long long off_s[kGatherChunk + 1];
     __shared__ long long row_s[kGatherChunk];   // offset of the request's first column in the table; -1: malformed
     constexpr int kPerRow = D / kBlock;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    constexpr bool kWhole = kMode != kParts;
+    const int pack = kMode == kPacked ? p.pack : 0;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & (31 >> pack);   // (of those that share a token)
     const bool first = blockIdx.x == 0;
     if (first && threadIdx.x == 0) p.cu_seqlens[0] = 0;
     if (first && warp < 2) {   // unusable head scales
         const float *g = warp ? p.v_scale : p.k_scale;
-        for (int h = lane; g && h < p.hkv; h += 32)
+        for (int h = threadIdx.x & 31; g && h < p.hkv; h += 32)
             if (!good_scale(g[h])) raise_flag(p.err, PKV_DEVERR_RANGE);
     }
     const int t = 1 << p.t_shift;
@@ -232,9 +243,11 @@ __global__ void __launch_bounds__(kThreads, kGatherCtas) gather_kernel(const Gat
         // (row numbers fit cu_seqlens' int32)
         const int tokens = static_cast<int>(min(min(total, max(p.cap - carry, 0ll)), static_cast<long long>(INT32_MAX)));
         const int j = lane % kPerRow, each = (row_iters(D, p.hkv) + p.parts - 1) / p.parts * (32 / kPerRow);
+        const int sub = (threadIdx.x & 31) >> (5 - pack);
         const int mine0 = blockIdx.x * (kThreads / 32) + warp, warps = gridDim.x * (kThreads / 32);
-        for (int64_t w = mine0; w < (kWhole ? (static_cast<int64_t>(tokens) + 1) / 2 : static_cast<int64_t>(tokens) * p.parts); w += warps) {
-            const int g0 = static_cast<int>(kWhole ? 2 * w : w / p.parts);
+        for (int64_t w = mine0; w < (kWhole ? ((static_cast<int64_t>(tokens) + 1) / 2 + (1 << pack) - 1) >> pack : static_cast<int64_t>(tokens) * p.parts);
+             w += warps) {
+            const int g0 = static_cast<int>(kWhole ? 2 * ((w << pack) + sub) : w / p.parts);
             const int h0 = kWhole ? 0 : static_cast<int>(w - static_cast<int64_t>(g0) * p.parts) * each;
             const int h1 = kWhole ? 2 * p.hkv : min(2 * p.hkv, h0 + each);
             int b = 0;
@@ -294,13 +307,14 @@ pkv_status launch_store(uint8_t *pool, int64_t num_slots, int64_t tile_stride, i
                         const float *ks, const float *vs, const uint16_t *kn, const uint16_t *vn, int64_t k_stride,
                         int64_t v_stride, const int32_t *slots, int32_t n, int32_t *err, cudaStream_t s) {
     const bool vec = aligned(kn, 32) && aligned(vn, 32) && k_stride % 16 == 0 && v_stride % 16 == 0;
-    const int64_t parts = row_parts(n, row_iters(D, hkv)), items = n * parts;
+    const int pack = row_pack(D, hkv);
+    const int64_t parts = row_parts(n, row_iters(D, hkv)), items = ((n + (int64_t{1} << pack) - 1) >> pack) * parts;
     if (items > INT32_MAX) return fail(PKV_ERR_UNSUPPORTED, "pkv_quant_store: too many rows for one call");
     const int64_t grid = (items + kThreads / 32 - 1) / (kThreads / 32);
     auto kern = vec ? store_kernel<D, true> : store_kernel<D, false>;
     return launch_status(launch_chained(kern, dim3(static_cast<unsigned>(grid)), dim3(kThreads), 0, s, pool, num_slots,
                                         tile_stride, t_shift, hkv, ks, vs, kn, vn, k_stride, v_stride, slots,
-                                        static_cast<uint32_t>(n), static_cast<uint32_t>(parts), err),
+                                        static_cast<uint32_t>(n), static_cast<uint32_t>(parts), pack, err),
                          "pkv_quant_store");
 }
 
@@ -377,12 +391,14 @@ extern "C" pkv_status pkv_quant_gather(const void *pool, int64_t num_tiles, int6
     // as many blocks as fit at once, or as the tokens (at most batch x max_seq_len) need
     const int64_t most = static_cast<int64_t>(batch) * max_seq_len;
     p.parts = static_cast<int32_t>(row_parts(most, row_iters(head_dim, kv_heads)));
+    p.pack = row_pack(head_dim, kv_heads);   // (then a token is one step, and parts 1)
     const int64_t grid = std::max<int64_t>(1, std::min<int64_t>((most * p.parts + kThreads / 32 - 1) / (kThreads / 32),
                                                                 static_cast<int64_t>(kGatherCtas) * std::max(1, sm_count())));
     const bool vec = aligned(k_out, 32) && aligned(v_out, 32);
     auto pick = [&](auto d, auto v) {
-        return p.parts == 1 ? gather_kernel<decltype(d)::value, decltype(v)::value, true>
-                            : gather_kernel<decltype(d)::value, decltype(v)::value, false>;
+        constexpr int D = decltype(d)::value;
+        constexpr bool V = decltype(v)::value;
+        return p.pack ? gather_kernel<D, V, kPacked> : p.parts == 1 ? gather_kernel<D, V, kTokens> : gather_kernel<D, V, kParts>;
     };
     using D128 = std::integral_constant<int, 128>;
     using D64 = std::integral_constant<int, 64>;
