@@ -349,6 +349,51 @@ def test_equal_rows_for_one_slot(B):
     assert err.item() == 0 and (pool.cpu().numpy() == want).all()
 
 
+@pytest.mark.parametrize("D,H,n", [(64, 1, 1), (64, 1, 7), (64, 1, 1001), (64, 2, 5), (64, 2, 333), (128, 1, 3), (128, 1, 1001)])
+def test_tokens_that_share_a_warp(B, D, H, n):
+    """Rows of half a warp or less: padded tokens and slots past the pool among them, then read back
+    with a bad page, an empty request and rows past the capacity."""
+    rng = np.random.default_rng(76 + D + H + n)
+    ps, slots = 4, 4 * (n // 4 + 3)
+    x = values(rng, (n, H, D))
+    mapping = rng.permutation(slots)[:n].astype(np.int32)
+    where = rng.random(n)
+    where[0] = 0.5
+    mapping[where < 0.1] = -1
+    mapping[where > 0.9] += slots
+    kept = (where >= 0.1) & (where <= 0.9)
+    g = np.array([0.5, 0.125], dtype=np.float32)[:H]   # (products with it are exact)
+    before = rng.integers(0, 100, (slots // ps, H, R.tile_bytes(ps, D))).astype(np.uint8)
+    want = before.copy()
+    for part in (0, 1):
+        R.write(want, ps, mapping[kept], part, *R.quantise(x[kept], g))
+    pool, err = up(before), torch.zeros(1, dtype=torch.int32, device=DEV)
+    kw = dict(page_size=ps, k_scale=up(g), v_scale=up(g))
+    B.pkv_quant_store(pool, to_bf16(x), to_bf16(x), up(mapping), err, **kw)
+    assert err.item() == (B.PKV_DEVERR_RANGE if (where > 0.9).any() else 0)
+    assert (pool.cpu().numpy() == want).all()
+    lens = np.array([n // 2, 0, n - n // 2], dtype=np.int32)
+    table = np.zeros((3, n + 4), dtype=np.int32)
+    for b, m in enumerate(lens):
+        table[b, :m] = rng.integers(0, slots, m)
+    cap = n - n // 10
+    out = [torch.full((cap, H, D), 9.0, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    cu = torch.zeros(4, dtype=torch.int32, device=DEV)
+    flat = np.concatenate([table[b, :m] for b, m in enumerate(lens)])[:cap].astype(np.int64)
+    bad = n // 3
+    if n > 100:
+        table[0, bad], flat[bad] = slots, 0
+    err.zero_()
+    B.pkv_quant_gather(pool, up(table), up(np.arange(3, dtype=np.int32)), up(lens), n, out[0], out[1], cu, err, **kw)
+    assert err.item() == (B.PKV_DEVERR_RANGE if n > 100 else 0) | (B.PKV_DEVERR_CAPACITY if cap < n else 0)
+    assert cu.tolist() == [0] + np.cumsum(lens).tolist()
+    for part, o in enumerate(out):
+        ref = R.bf16(R.read(want, ps, D, flat, part, g).astype(np.float32))
+        if n > 100:
+            ref[bad] = 0
+        assert (host(o) == ref).all()
+
+
 def test_two_calls_at_once(B):
     """Two streams, each with its own workspace: decodes beside many-row steps, again and again."""
     rng = np.random.default_rng(72)
