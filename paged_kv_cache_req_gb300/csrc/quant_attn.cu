@@ -1235,14 +1235,19 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
         const int lr = live ? out / (D / 4) : 0, d0 = live ? out % (D / 4) * 4 : 0;
         float m = -INFINITY, l = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+        // (no branch in the loop: the loads of several partials are in flight at a time)
+#pragma unroll 8
         for (int i = sub; i < parts; i += subs) {
             const int64_t at = ((s0 + i) * 2 + (i == 0 ? c.z & 1 : 0)) * 8 * NT + lr;
             const float2 ml = reinterpret_cast<const float2 *>(p.part_ml)[at];
-            const float4 x = *reinterpret_cast<const float4 *>(p.part_o + at * D + d0);
-            if (ml.y == 0.f) continue;   // no key of the row in that span
-            const float mn = fmaxf(m, ml.x), base = mn == -INFINITY ? 0.f : mn;
-            const float c0 = ex2(m - base), c1 = ex2(ml.x - base);
+            float4 x = *reinterpret_cast<const float4 *>(p.part_o + at * D + d0);
+            const bool some = ml.y != 0.f;   // else no key of the row in that span, and x was not written
+            x.x = some ? x.x : 0.f;
+            x.y = some ? x.y : 0.f;
+            x.z = some ? x.z : 0.f;
+            x.w = some ? x.w : 0.f;
+            const float mn = some ? fmaxf(m, ml.x) : m, base = mn == -INFINITY ? 0.f : mn;
+            const float c0 = ex2(m - base), c1 = some ? ex2(ml.x - base) : 0.f;
             m = mn;
             l = l * c0 + ml.y * c1;
             o.x = o.x * c0 + x.x * c1;
