@@ -77,6 +77,25 @@ std::atomic<int64_t> *device_memo(const void *key, int tag) {
     return &memo[std::make_tuple(dev, key, tag)];   // map nodes never move
 }
 
+size_t raise_smem_limit(const void *kernel) {
+    std::atomic<int64_t> *memo = device_memo(kernel);
+    if (!memo) return 0;
+    if (memo->load() == 0) {
+        int optin = 0, dev = 0;
+        cudaFuncAttributes fa{};
+        if (cudaGetDevice(&dev) != cudaSuccess ||
+            cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
+            cudaFuncGetAttributes(&fa, kernel) != cudaSuccess ||
+            cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 optin - static_cast<int>(fa.sharedSizeBytes)) != cudaSuccess) {
+            (void)cudaGetLastError();
+            return 0;
+        }
+        memo->store(optin - static_cast<int64_t>(fa.sharedSizeBytes));
+    }
+    return static_cast<size_t>(memo->load());
+}
+
 namespace {
 constexpr uint64_t kDefaultWaitNs = 2000000000ull;
 std::atomic<uint64_t> g_wait_limit_ns{kDefaultWaitNs};

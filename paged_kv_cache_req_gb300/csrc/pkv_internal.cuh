@@ -28,6 +28,11 @@ uint64_t wait_limit_ns();
 // raised shared-memory limit are per device, so they are set and cached per device.
 // Starts at 0; nullptr if the current device cannot be queried.  Thread-safe.
 std::atomic<int64_t> *device_memo(const void *key, int tag = 0);
+// Gives `kernel` on the current device all the dynamic shared memory that a block may have, once
+// per device, and returns its bytes (0 if CUDA refuses).  The limit of a kernel is one value
+// that every thread of the process shares: callers that set it to what their own launch needs
+// take from one another what they have just set, and so all of them set this one.
+size_t raise_smem_limit(const void *kernel);
 
 // Launches `kernel` on stream `s` as a programmatic dependent of the kernel before it
 // in the stream: it may be scheduled while that kernel drains.  Every kernel of this

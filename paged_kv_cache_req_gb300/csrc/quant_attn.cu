@@ -1637,15 +1637,8 @@ static pkv_status launch(const char *who, const Params &p, const Plan &pl, cudaS
         kern = p.t_shift == 6 ? unit_kernel<D, NT, 64, true> : p.t_shift == 4 ? unit_kernel<D, NT, 16, true> : unit_kernel<D, NT, 0, true>;
     else if (pl.unit)
         kern = p.t_shift == 6 ? unit_kernel<D, NT, 64, false> : p.t_shift == 4 ? unit_kernel<D, NT, 16, false> : unit_kernel<D, NT, 0, false>;
-    std::atomic<int64_t> *set = device_memo(reinterpret_cast<const void *>(kern));
-    if (!set) return fail(PKV_ERR_CUDA, "%s: cannot query the current device", who);
-    if (set->load() < static_cast<int64_t>(pl.smem)) {   // kernel attributes are per device
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(pl.smem)) != cudaSuccess) {
-            (void)cudaGetLastError();
-            return fail(PKV_ERR_CUDA, "%s: cannot raise the shared-memory limit", who);
-        }
-        set->store(static_cast<int64_t>(pl.smem));
-    }
+    if (raise_smem_limit(reinterpret_cast<const void *>(kern)) < pl.smem)
+        return fail(PKV_ERR_CUDA, "%s: cannot raise the shared-memory limit", who);
     pkv_status st = PKV_OK;
     if (pl.plan_launch) {
         st = launch_status(launch_chained(plan_kernel<NT>, dim3(1), dim3(1024), 0, s, p), who);
@@ -1669,15 +1662,8 @@ static pkv_status launch_held(const pkv_quant_args *a, const Params &p, const Pl
     h.counter = reinterpret_cast<int32_t *>(own + ext::held_counter_offset(&e));
     h.min_rows = pl.spans ? kHeldRows : 0;
     const size_t smem = (static_cast<size_t>(a->batch) + 1) * 8;
-    std::atomic<int64_t> *set = device_memo(reinterpret_cast<const void *>(hold_kernel<D>));
-    if (!set) return fail(PKV_ERR_CUDA, "pkv_quant_extend: cannot query the current device");
-    if (set->load() == 0) {
-        if (cudaFuncSetAttribute(hold_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, 64 * 1024) != cudaSuccess) {
-            (void)cudaGetLastError();
-            return fail(PKV_ERR_CUDA, "pkv_quant_extend: cannot raise the shared-memory limit");
-        }
-        set->store(1);
-    }
+    if (raise_smem_limit(reinterpret_cast<const void *>(hold_kernel<D>)) < smem)
+        return fail(PKV_ERR_CUDA, "pkv_quant_extend: cannot raise the shared-memory limit");
     const int64_t items = (pl.hold_rows / kTile + a->batch) * a->num_kv_heads;
     const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(items, static_cast<int64_t>(kHoldCtas) * std::max(1, sm_count())));
     const pkv_status st = launch_status(launch_chained(hold_kernel<D>, dim3(static_cast<unsigned>(grid)), dim3(kHoldThreads),

@@ -1,5 +1,9 @@
 """The 4-bit attention calls at the ends of what they allow: many short segments per warp, weights
 and scales far apart, first calls from several threads, large batches."""
+import os
+import subprocess
+import sys
+
 import numpy as np
 import pytest
 import torch
@@ -8,6 +12,7 @@ import _quant_ref as R
 from test_gpu_quant import DEV, Cache, check, decode, extend, host, to_bf16, up, values  # noqa: F401
 
 pytestmark = pytest.mark.gpu
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
 
 
 @pytest.fixture(scope="module")
@@ -32,3 +37,54 @@ def test_short_segments_follow_one_another(B, D, H, g):
     for _ in range(10):
         o2, l2, e = decode(B, cache, q, kv_chunk=256)
         assert e == 0 and torch.equal(out, o2) and torch.equal(lse, l2)
+
+
+FIRST_CALLS = """
+import sys, threading
+import torch
+from paged_kv_cache_req_gb300 import _binding as B
+
+dev = "cuda"
+failed = []
+barrier = threading.Barrier(2)
+
+
+def make(D, Hq, ps, batch):
+    # one key per request, all on page 0
+    pool = torch.zeros((16, 1, B.pkv_quant_tile_bytes(ps, D)), dtype=torch.uint8, device=dev)
+    q = torch.ones((batch, Hq, D), dtype=torch.bfloat16, device=dev)
+    ones = torch.ones(batch, dtype=torch.int32, device=dev)
+    out = torch.empty_like(q)
+    a = B.make_quant_args(B.PKV_LAYOUT_BLOCK_TABLE, q, pool, out, page_size=ps, sm_scale=1.0, max_seq_len=64, kv_chunk=64,
+                          block_table=torch.zeros((batch, 64), dtype=torch.int32, device=dev), seq_lens=ones)
+    ws = torch.empty(B.pkv_quant_decode_workspace_size(a), dtype=torch.uint8, device=dev)
+    return a, ws, torch.zeros(1, dtype=torch.int32, device=dev), torch.cuda.Stream()
+
+
+def work(batch):
+    for a, ws, err, stream in calls[batch]:
+        barrier.wait()
+        for _ in range(3):
+            try:
+                B.pkv_quant_decode(a, ws, err, stream=stream)
+            except B.PkvError as e:
+                failed.append("batch %d, head_dim %d: %s" % (batch, a.head_dim, e))
+
+
+calls = {n: [make(D, Hq, ps, n) for D in (64, 128) for Hq in (4, 16) for ps in (1, 16, 64)] for n in (2, 1000)}
+torch.cuda.synchronize()
+threads = [threading.Thread(target=work, args=(n,)) for n in calls]
+[t.start() for t in threads]
+[t.join() for t in threads]
+torch.cuda.synchronize()
+assert all(err.item() == 0 for n in calls for _, _, err, _ in calls[n])
+sys.exit("\\n".join(failed) if failed else 0)
+"""
+
+
+def test_first_calls_from_two_threads(B):
+    """A small and a large batch of each kernel, called for the first time in a process by two threads
+    at once: neither takes back the shared memory that the other needs."""
+    for _ in range(3):
+        r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=ROOT, capture_output=True, text=True, timeout=300)
+        assert r.returncode == 0, r.stderr
