@@ -194,8 +194,7 @@ extern "C" pkv_status pkv_alloc_extend(const int32_t *prefix_lens, const int32_t
     if (num_pool_pages > INT32_MAX / page_size) return fail(PKV_ERR_UNSUPPORTED, "pkv_alloc_extend: pool above 2^31 slots");
     if (batch == 0) return ok();
     const size_t smem = static_cast<size_t>(batch + 1) * 4 * sizeof(int32_t);
-    if (smem > 48 * 1024 && cudaFuncSetAttribute(alloc_extend_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                                 static_cast<int>(smem)) != cudaSuccess)
+    if (smem > 48 * 1024 && raise_smem_limit(reinterpret_cast<const void *>(alloc_extend_kernel)) < smem)
         return fail(PKV_ERR_CUDA, "pkv_alloc_extend: cannot raise the shared-memory limit");
     return launch_status(
         launch_chained(alloc_extend_kernel, dim3(1), dim3(kAllocThreads), smem, reinterpret_cast<cudaStream_t>(stream),

@@ -1522,19 +1522,8 @@ static pkv_status launch_merge(const Params &p, cudaStream_t s) {
     if (p.n_chunks_max == 1) return PKV_OK;
     const size_t msmem = static_cast<size_t>(GC) * p.n_chunks_max * 4;
     if (msmem > 200 * 1024) return fail(PKV_ERR_UNSUPPORTED, "pkv_decode: too many splits for the merge");
-    if (msmem > 48 * 1024) {
-        // the raised limit is per device: remember the largest one set on this device
-        std::atomic<int64_t> *m = device_memo(reinterpret_cast<const void *>(merge_kernel<D, GC>));
-        if (!m) return fail(PKV_ERR_CUDA, "pkv_decode: cannot query the current device");
-        if (m->load() < static_cast<int64_t>(msmem)) {
-            if (cudaFuncSetAttribute(merge_kernel<D, GC>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     static_cast<int>(msmem)) != cudaSuccess)
-                return fail(PKV_ERR_CUDA, "pkv_decode: cannot raise the merge shared-memory limit");
-            int64_t cur = m->load();
-            while (cur < static_cast<int64_t>(msmem) && !m->compare_exchange_weak(cur, static_cast<int64_t>(msmem))) {
-            }
-        }
-    }
+    if (msmem > 48 * 1024 && raise_smem_limit(reinterpret_cast<const void *>(merge_kernel<D, GC>)) < msmem)
+        return fail(PKV_ERR_CUDA, "pkv_decode: cannot raise the merge shared-memory limit");
     return launch_status(launch_chained(merge_kernel<D, GC>, dim3(p.batch * p.hkv * p.hsplit), dim3(kThreads), msmem, s, p),
                          "pkv_decode(GQA merge kernel)");
 }

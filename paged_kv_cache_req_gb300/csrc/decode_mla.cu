@@ -1193,9 +1193,7 @@ pkv_status launch(const pkv_decode_args *a, void *ws, size_t ws_bytes, int32_t *
                                                tmkv, tmrope),
                        "pkv_decode(MLA split kernel)");
     if (st != PKV_OK) return st;
-    if (msmem > 48 * 1024 &&
-        cudaFuncSetAttribute(mla_merge_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(msmem)) !=
-            cudaSuccess)
+    if (msmem > 48 * 1024 && raise_smem_limit(reinterpret_cast<const void *>(mla_merge_kernel)) < msmem)
         return fail(PKV_ERR_CUDA, "pkv_decode(MLA): cannot raise the merge shared-memory limit");
     return launch_status(launch_chained(mla_merge_kernel, dim3(a->batch * pl.hgroups, kHeads / 16), dim3(256), msmem, s, p,
                                         pl.max_splits),
