@@ -1557,8 +1557,9 @@ static bool make_plan(const pkv_quant_args *a, bool extend, Plan &pl) {
         pl.smem = warps * ring_stages(a->head_dim, pl.nt) * stage;
         if (!pl.plan_launch) pl.smem += (static_cast<size_t>(a->batch) + 2) * 4 + (a->batch <= kReqInSmem ? a->batch * sizeof(Req) : 0);
         int64_t spans = sms * warps;
-        // all units' tiles, at most
-        const int64_t blocks = (a->total_q * g + 8 * pl.nt - 1) / (8 * pl.nt) + a->batch;
+        // all units' tiles, at most (beside held keys the requests with few rows only)
+        const int64_t all_rows = pl.held ? std::min<int64_t>(a->total_q * g, batch * kHeldRows) : a->total_q * g;
+        const int64_t blocks = (all_rows + 8 * pl.nt - 1) / (8 * pl.nt) + a->batch;
         const int64_t tiles = blocks * a->num_kv_heads * ((std::max(1, a->max_seq_len) + kTile - 1) / kTile + unit_cost(pl.nt));
         if (a->kv_chunk > 0) {
             pl.span_tiles = a->kv_chunk / kTile;

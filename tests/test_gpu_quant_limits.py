@@ -88,3 +88,22 @@ def test_first_calls_from_two_threads(B):
     for _ in range(3):
         r = subprocess.run([sys.executable, "-c", FIRST_CALLS], cwd=ROOT, capture_output=True, text=True, timeout=300)
         assert r.returncode == 0, r.stderr
+
+
+def test_many_rows_under_far_bounds(B):
+    """More rows and a higher bound on the keys than the span kernel's sequence of tiles could count."""
+    rng = np.random.default_rng(92)
+    lens, rows = [500, 33, 70], [65000, 3, 2000]
+    cache = Cache(rng, lens, 16, 8, 64)
+    q = to_bf16(values(rng, (sum(rows), 16, 64)))
+    ends = np.concatenate([rng.integers(0, n + 1, r) for n, r in zip(lens, rows)]).astype(np.int32)
+    out, lse, e = extend(B, cache, q, rows, kv_end=ends, max_seq_len=1 << 20, total_kv=sum(lens))
+    assert e == 0
+    some = np.concatenate([[0, 1, 64999, 65000, 65001, 65002, 65003, 67002], rng.integers(0, sum(rows), 60)])
+    req = np.searchsorted(np.cumsum(rows), some, side="right")
+    for b in range(3):
+        at = some[req == b]
+        k, v = cache.kv(b)
+        ref, rl, tol, lt = R.attention(host(q[up(at)]).astype(np.float64), k, v, ends[at], 64 ** -0.5)
+        R.assert_within(host(out[up(at)]), ref, tol, "request %d out" % b)
+        R.assert_within(host(lse[up(at)]), rl, lt, "request %d lse" % b)
