@@ -585,7 +585,9 @@ typedef struct pkv_quant_args {
  * One query row per request over all its keys; the same formulas with K and V the
  * pool's values.  Page lists, checks and flags are pkv_decode's.  Arithmetic: K and V
  * enter the tensor cores as code * s, exact in 16 bits; scores, softmax and sums are
- * fp32, the weights fp16, the output bf16 rounded to nearest even.  What the
+ * fp32, the output bf16 rounded to nearest even.  The weights are fp16 in the product
+ * with V: 2^-11 relative down to 2^-25 of the row's largest, 2^-36 of the largest below
+ * that (a key's that is smaller still counts in the sum, but its V does not).  What the
  * pool holds at slots past a request's keys does not matter, NaN patterns included.
  * workspace: at least pkv_quant_decode_workspace_size(args) bytes, 256-byte aligned, not
  * shared with a call that may run at the same time; it needs no initialisation.
@@ -605,7 +607,8 @@ size_t pkv_quant_decode_workspace_size(const pkv_quant_args *args);
  * Requests with more than 128 (row, query head) pairs per kv head have their keys and
  * values copied out of the pool into the workspace as 16-bit floats first (exactly), which
  * total_kv sizes; a step of which max_q_len, or without it the average, says that there is
- * no such request needs no room for that, and computes a larger request all the same.  A
+ * no such request needs no room for that, and computes a larger request all the same.  Their
+ * weights are 2^-11 relative down to 2^-21 of the row's largest and 2^-32 of it below that.  A
  * row that sees a key whose V holds a NaN block may be NaN in all its dims there.
  * workspace as for pkv_quant_decode, of pkv_quant_extend_workspace_size(args) bytes.
  */

@@ -38,8 +38,12 @@
 // kHeld: the same kernel for pkv_quant_extend, over keys and values that quant_attn.cu has
 // taken out of the 4-bit pool: K bf16 and V fp16 (both exact) in workspace tensors
 // [D/64][kv heads][rows][64], so that a box is 128 consecutive rows, 16 KB in one piece.  The
-// heads' fp32 scales go into the score scale and the epilogue, P is rounded to fp16 instead
-// of bf16 (three more bits), and a NaN key makes the rows that see it NaN.
+// heads' fp32 scales go into the score scale and the epilogue, and a NaN key makes the rows that
+// see it NaN.  P is rounded to fp16 instead of bf16: three more bits down to 2^-21 of the row's
+// largest weight, but an absolute 2^-32 of the largest below that (and 0 below 2^-32), where bf16
+// keeps its bits: weights are held times 2^7 for that, as high as 2^15 with a maximum that is
+// raised past 2^8 only (one raised past 2^4, with a lift of 11, costs 8 %: 1,195 -> 1,293 us at 8192 rows
+// over 16384 keys).
 #include <algorithm>
 
 #include "extend_held.cuh"
@@ -56,6 +60,7 @@ constexpr int kProducerWarp = 8, kQkWarp = 9, kPvWarp = 10, kEpiWarp0 = 11, kVPr
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLazy = 8.f;
+constexpr float kLift = 7.f;               // kHeld: log2 of what the fp16 weights are held times
 constexpr int kRing = 8;                   // slots of the item queue
 constexpr int kItemReaders = 16;           // warps that read every queued item
 constexpr int kMostItems = 1 << 29;        // at which the item counts saturate
@@ -1018,7 +1023,7 @@ ext_kernel(const Params p, const __grid_constant__ CUtensorMap tmq, const __grid
 #pragma unroll
                     for (int j = 0; j < 64; ++j) x[j] = j < vis ? x[j] : -INFINITY;
                 }
-                float mx;
+                float mx, top;   // the largest score, as a logit and as it is
                 {   // a tree of three-input maxima: 64 -> 22 -> 8 -> 3 -> 1
                     float t[22];
 #pragma unroll
@@ -1028,10 +1033,16 @@ ext_kernel(const Params p, const __grid_constant__ CUtensorMap tmq, const __grid
 #pragma unroll
                     for (int j = 0; j < 7; ++j) u[j] = fmax3(t[3 * j], t[3 * j + 1], t[3 * j + 2]);
                     u[7] = t[21];
-                    mx = fmax3(fmax3(u[0], u[1], u[2]), fmax3(u[3], u[4], u[5]), fmaxf(u[6], u[7])) *
-                         scale;   // scores are unscaled up to here (the scale is positive)
+                    top = fmax3(fmax3(u[0], u[1], u[2]), fmax3(u[3], u[4], u[5]), fmaxf(u[6], u[7]));
+                    mx = top * scale;   // scores are unscaled up to here (the scale is positive)
                 }
-                const bool raise = mx > m + kLazy || (m == -INFINITY && mx != -INFINITY);
+                bool raise = m == -INFINITY && mx != -INFINITY;
+                if (kHeld) {   // m is kLift below the maximum; raised by the exponent that a weight would have
+                    raise |= fmaf(top, scale, -m) > kLift + kLazy;
+                    mx -= kLift;
+                } else {
+                    raise |= mx > m + kLazy;
+                }
                 const float corr = raise ? ex2(m - mx) : 1.f;
                 if (__any_sync(0xffffffffu, raise && m != -INFINITY) && ok) {
                     // the group's accumulator is final for tile n - 1 (of this item: m is

@@ -107,3 +107,60 @@ def test_many_rows_under_far_bounds(B):
         ref, rl, tol, lt = R.attention(host(q[up(at)]).astype(np.float64), k, v, ends[at], 64 ** -0.5)
         R.assert_within(host(out[up(at)]), ref, tol, "request %d out" % b)
         R.assert_within(host(lse[up(at)]), rl, lt, "request %d lse" % b)
+
+
+def sink_bound(q, k, v, ends, sm_scale):
+    """q [n, D], k / v [L, D] fp64 of one head -> (out, lse, bounds of both).
+
+    As _quant_ref.attention (the sum that lse is the logarithm of has L terms in fp32, so L 2^-23
+    relative: the largest weight is 2^7 there, and each of 16384 weights of 2^-14.6 is added to it
+    with up to half of 128's last place, 2^-18, lost), but for the weights: one is rounded by 2^-11 relative, or, where it is
+    subnormal in fp16, by 2^-25; the largest is held as 2^7 or more, so that is 2^-32 of it."""
+    s = q @ k.T * sm_scale
+    s[np.arange(k.shape[0])[None] >= np.asarray(ends)[:, None]] = -np.inf
+    m = s.max(1, keepdims=True)
+    p = np.exp(s - m)
+    den = p.sum(1, keepdims=True)
+    out = p @ v / den
+    ds = (np.abs(q) @ np.abs(k).T).max(1, keepdims=True) * sm_scale * k.shape[1] * 2.0 ** -23
+    rel = 2.0 ** -11 + 2 * (ds + 2.0 ** -21 + k.shape[0] * 2.0 ** -23)
+    tol = 2.0 ** -8 * np.abs(out) + (1 + 2.0 ** -8) * (rel * (p @ np.abs(v) / den) +
+                                                       2.0 ** -32 * (np.isfinite(s) @ np.abs(v)) / den)
+    lse = m + np.log(den)
+    ltol = ds + 2.0 ** -21 + k.shape[0] * 2.0 ** -23 + 2.0 ** -22 * (np.abs(m) + np.abs(lse) + 1)
+    return out, lse[:, 0], tol, ltol[:, 0]
+
+
+@pytest.mark.parametrize("spread", [0.0, 0.5])
+@pytest.mark.parametrize("D,rows,chunk", [(128, 1, 1 << 20), (64, 1, 1 << 20), (128, 1, 0), (64, 9, 1 << 20), (128, 14, 1 << 20),
+                                          (128, 200, 1 << 20), (64, 200, 1 << 20), (128, 200, 2048)])
+def test_a_key_far_above_the_others(B, D, rows, chunk, spread):
+    """One key 15 to 18 nats above 16384 others, with a value of 0: the output is what the others give."""
+    rng = np.random.default_rng(94)
+    L, nats = 16385, np.array([15.0, 17.0, 18.0])
+    cache = Cache(rng, [L] * 3, 64, 1, D)
+    cache.ks[:], cache.vs[:] = 1.0, 0.25
+    for b in range(3):
+        k = np.tile(spread * rng.standard_normal((L, 1, 1)), (1, 1, D)) * np.where(np.arange(D) % 2 == 0, 1, -1) / 8
+        v = np.abs(values(rng, (L, 1, D), 0.3))
+        k[:], v[5 * b] = R.bf16(k), 0.0
+        k[5 * b, 0] = 6.0
+        for part, x, g in ((0, k, cache.ks), (1, v, cache.vs)):
+            R.write(cache.pool, 64, cache.slots[b], part, *R.quantise(x.astype(np.float32), g))
+    q = np.repeat(nats / (6.0 * D * D ** -0.5), rows)[:, None, None] + np.zeros((1, 1, D))
+    if spread:   # the even and odd dims' difference gives the other keys scores of some 0.5 nats
+        q = q + np.where(np.arange(D) % 2 == 0, 1, -1) * (8 * D ** -0.5 / D) * D
+    q = to_bf16(R.bf16(q))
+    if rows == 1:
+        out, lse, e = decode(B, cache, q, kv_chunk=chunk)
+    else:
+        out, lse, e = extend(B, cache, q, [rows] * 3, kv_chunk=chunk)
+    assert e == 0
+    for b in range(3):
+        k, v = cache.kv(b)
+        at = slice(b * rows, (b + 1) * rows)
+        ref, rl, tol, lt = sink_bound(host(q)[at, 0].astype(np.float64), k[:, 0], v[:, 0], np.arange(L - rows + 1, L + 1),
+                                      D ** -0.5)
+        assert (tol < 0.06 * ref + 1e-9).all()
+        R.assert_within(host(out)[at, 0], ref, tol, "%g nats" % nats[b])
+        R.assert_within(host(lse)[at, 0], rl, lt, "lse")
