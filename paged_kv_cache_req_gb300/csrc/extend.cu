@@ -988,7 +988,9 @@ ext_kernel(const Params p, const __grid_constant__ CUtensorMap tmq, const __grid
             const bool valid = tq < it.n && (!kHeld || hh < p.heads);
             const int64_t qrow = static_cast<int64_t>(it.qo0) + tq;
             const int head = it.kh * (kHeld ? p.heads : p.g) + hh;
-            const float scale = kHeld && p.k_scale ? p.scale_log2 * __ldg(p.k_scale + it.kh) : p.scale_log2;
+            // (held: kept normal and finite, so that -inf, a masked key, stays -inf and 0 stays 0)
+            const float scale = kHeld ? fminf(fmaxf(p.scale_log2 * (p.k_scale ? __ldg(p.k_scale + it.kh) : 1.f), 1.2e-38f), 3.4e38f)
+                                      : p.scale_log2;
             float m = -INFINITY, l = 0.f;
             if (it.n_tiles == 0) {   // no keys: out = 0, lse = -inf
                 if (grp == 0 && valid && it.nch == 1) {

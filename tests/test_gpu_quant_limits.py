@@ -164,3 +164,18 @@ def test_a_key_far_above_the_others(B, D, rows, chunk, spread):
         assert (tol < 0.06 * ref + 1e-9).all()
         R.assert_within(host(out)[at, 0], ref, tol, "%g nats" % nats[b])
         R.assert_within(host(lse)[at, 0], rl, lt, "lse")
+
+
+@pytest.mark.parametrize("rows,chunk", [(1, 0), (1, 128), (7, 128), (200, 0), (200, 256)])
+def test_a_vanishing_score_scale(B, rows, chunk):
+    """sm_scale times K's head scale below fp32's range: equal weights, also beside masked keys."""
+    rng = np.random.default_rng(95)
+    cache = Cache(rng, [333, 260], 16, 2, 128)
+    cache.ks[:] = 1e-20
+    q = to_bf16(values(rng, (2 * rows, 8, 128)))
+    if rows == 1:
+        out, lse, e = decode(B, cache, q, sm_scale=5e-32, kv_chunk=chunk)
+    else:
+        out, lse, e = extend(B, cache, q, [rows] * 2, sm_scale=5e-32, kv_chunk=chunk)
+    assert e == 0
+    check(cache, q, out, lse, None if rows == 1 else [rows] * 2, sm_scale=5e-32)
