@@ -895,10 +895,11 @@ ext_kernel(const Params p, const __grid_constant__ CUtensorMap tmq, const __grid
             }
             const float den = sa.y * wa + sb2.y * wb;
             if (kHeld)
-                inv = den == 0.f ? 0.f : (p.v_scale ? __ldg(p.v_scale + it.kh) : 1.f) / den;
+                inv = den == 0.f ? 0.f : 1.f / den;
             else
                 inv = den > 0.f ? 1.f / den : 0.f;
             const float ca = wa * inv, cb2 = wb * inv;
+            const float gv = kHeld && p.v_scale ? __ldg(p.v_scale + it.kh) : 1.f;   // (last: gv / den may be subnormal)
             const int tq = it.qblk * p.T + tok;
             const bool valid = tq < it.n && (!kHeld || hh < p.heads);
             const int64_t qrow = static_cast<int64_t>(it.qo0) + tq;
@@ -925,7 +926,7 @@ ext_kernel(const Params p, const __grid_constant__ CUtensorMap tmq, const __grid
                             // selects, not products: an accumulator left out may hold anything
                             const float xa = ok && wa != 0.f ? oa[q2][e] * ca : 0.f;
                             const float xb = ok && wb != 0.f ? ob[q2][e] * cb2 : 0.f;
-                            ov[e] = xa + xb;
+                            ov[e] = kHeld ? (xa + xb) * gv : xa + xb;
                         }
                         const int col = (cb + q2) * 16;
                         if (single) {

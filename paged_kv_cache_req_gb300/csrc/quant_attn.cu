@@ -94,6 +94,11 @@ struct Params {
     int32_t max_rows;        // > 0: requests with more rows per kv head are left to the held path
 };
 
+__device__ __forceinline__ float rcp(float x) {
+    float y;
+    asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -896,10 +901,10 @@ __device__ __forceinline__ void finish_segment(const Params &p, const Work &s, S
             if (tok >= s.n) continue;
             if (whole) {
                 const int64_t at = static_cast<int64_t>(s.qo0 + tok) * p.hq + s.kh * p.g + hh;
-                const float inv = l == 0.f ? 0.f : gv / l;
+                const float inv = l == 0.f ? 0.f : rcp(l);   // (gv / l may be below fp32's normal numbers)
                 uint32_t h[W / 2];
 #pragma unroll
-                for (int t = 0; t < D / 16; ++t) h[t] = pack_bf16x2(st.o[t][n][v] * inv, st.o[t][n][2 + v] * inv);
+                for (int t = 0; t < D / 16; ++t) h[t] = pack_bf16x2(st.o[t][n][v] * inv * gv, st.o[t][n][2 + v] * inv * gv);
                 uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * D + r * W);
 #pragma unroll
                 for (int i = 0; i < W / 8; ++i) dst[i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
@@ -1201,9 +1206,9 @@ __global__ void __launch_bounds__(warps_per_sm(D, NT) * 32, 1) unit_kernel(const
             }
             const int r0 = rb * 8 * NT + row, tok = kRows ? token_of(p, r0) : 0;
             const int64_t at = static_cast<int64_t>(req.qo0 + tok) * p.hq + kh * p.g + (r0 - tok * p.g);
-            const float inv = l == 0.f ? 0.f : gv / l;
+            const float inv = l == 0.f ? 0.f : rcp(l);
             *reinterpret_cast<uint2 *>(p.out + at * D + d0) =
-                make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+                make_uint2(pack_bf16x2(o.x * inv * gv, o.y * inv * gv), pack_bf16x2(o.z * inv * gv, o.w * inv * gv));
             if (d0 == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
         if (!kRows) break;
@@ -1280,9 +1285,9 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
         if (sub || !live) continue;
         const int row = rb * 8 * NT + lr, tok = token_of(p, row);
         const int64_t at = static_cast<int64_t>(qo0 + tok) * p.hq + kh * p.g + (row - tok * p.g);
-        const float inv = l == 0.f ? 0.f : gv / l;
+        const float inv = l == 0.f ? 0.f : rcp(l);
         *reinterpret_cast<uint2 *>(p.out + at * D + d0) =
-            make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
+            make_uint2(pack_bf16x2(o.x * inv * gv, o.y * inv * gv), pack_bf16x2(o.z * inv * gv, o.w * inv * gv));
         if (d0 == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
 }

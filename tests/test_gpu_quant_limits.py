@@ -179,3 +179,23 @@ def test_a_vanishing_score_scale(B, rows, chunk):
         out, lse, e = extend(B, cache, q, [rows] * 2, sm_scale=5e-32, kv_chunk=chunk)
     assert e == 0
     check(cache, q, out, lse, None if rows == 1 else [rows] * 2, sm_scale=5e-32)
+
+
+@pytest.mark.parametrize("e", [-121, 100])
+@pytest.mark.parametrize("rows,chunk", [(1, 0), (1, 1 << 20), (1, 256), (6, 1 << 20), (6, 256), (300, 1 << 20), (300, 1024)])
+def test_far_head_scales_of_v(B, rows, chunk, e):
+    """V's head scale near both ends of fp32 over thousands of equal keys: the output keeps its bits."""
+    rng = np.random.default_rng(96)
+    cache = Cache(rng, [4000, 700], 64, 1, 64, spread=0.1)
+    cache.vs[:] = 2.0 ** e
+    for b, L in enumerate(cache.lens):      # values of one sign: their mean is as large as they are
+        R.write(cache.pool, 64, cache.slots[b], 1, *R.quantise(np.abs(values(rng, (L, 1, 64))), np.ones(1, np.float32)))
+    q = to_bf16(values(rng, (2 * rows, 4, 64)))
+    if rows == 1:
+        out, lse, err = decode(B, cache, q, kv_chunk=chunk)
+    else:
+        out, lse, err = extend(B, cache, q, [rows] * 2, kv_chunk=chunk)
+    assert err == 0
+    out = torch.ldexp(out.double(), torch.tensor(-e))          # (exact: compared at a scale of 1)
+    cache.vs[:] = 1.0
+    check(cache, q, out, lse, None if rows == 1 else [rows] * 2)
