@@ -829,6 +829,7 @@ __device__ __forceinline__ void start_segment(const Params &p, const Work &s, St
                                               int lane) {
     const int r = lane >> 2, c = lane & 3;
     const float gk = p.k_scale ? p.k_scale[s.kh] : 1.f;
+    const float small = fminf(p.scale_log2, gk), large = fmaxf(p.scale_log2, gk);
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         uint32_t w[D / 8];
@@ -859,7 +860,9 @@ __device__ __forceinline__ void start_segment(const Params &p, const Work &s, St
         for (int v = 0; v < 2; ++v) {   // this lane's rows as columns of S^T: 8 n + 2 c + v
             const int ev = __shfl_sync(0xffffffffu, e, (2 * c + v) * 4);
             // kept normal and finite, so that -inf (a masked key) stays -inf and 0 stays 0
-            st.f[n][v] = fminf(fmaxf(p.scale_log2 * gk * __int_as_float((127 - ev) << 23), 1.2e-38f), 3.4e38f);
+            // (the power of two joins the factor that it brings nearer to 1: scale x g alone may be 0)
+            const float down = __int_as_float((127 - ev) << 23);
+            st.f[n][v] = fminf(fmaxf(ev < 0 ? small * down * large : large * down * small, 1.2e-38f), 3.4e38f);
             const int rv = s.rb * 8 * NT + n * 8 + 2 * c + v, tv = token_of(p, rv);
             int end = s.L;   // rows past the last (zeros, never written) ask for no masking
             if (tv < s.n) {

@@ -199,3 +199,26 @@ def test_far_head_scales_of_v(B, rows, chunk, e):
     out = torch.ldexp(out.double(), torch.tensor(-e))          # (exact: compared at a scale of 1)
     cache.vs[:] = 1.0
     check(cache, q, out, lse, None if rows == 1 else [rows] * 2)
+
+
+@pytest.mark.parametrize("rows,chunk", [(1, 0), (1, 64), (3, 64)])
+def test_far_queries_over_vanishing_scales(B, rows, chunk):
+    """Queries near bf16's largest value, sm_scale and K's head scale so small that their product alone
+    is 0 in fp32: the logits are not."""
+    rng = np.random.default_rng(97)
+    D, L = 128, 2 * rows
+    cache = Cache(rng, [L], 16, 1, D)
+    for part, x in ((0, 1.0), (1, 1.0)):      # every second key 6 x 448 in all dims, the others 0; values of both signs
+        rowsx = np.full((L, 1, D), x, dtype=np.float32) * (np.arange(L) % 2 == 0 if part == 0 else 1 - 2 * (np.arange(L) % 2))[:, None, None]
+        c, s = R.quantise(rowsx.astype(np.float32), np.array([1.0 / 2688], dtype=np.float32))
+        R.write(cache.pool, 16, cache.slots[0], part, c, s)
+    cache.ks[:], cache.vs[:] = 2.0 ** -75, 2.0 ** -11
+    sm = 2.0 ** -76
+    q = torch.full((rows, 1, D), 2.0 ** 127, dtype=torch.bfloat16, device=DEV)
+    if rows == 1:
+        out, lse, e = decode(B, cache, q, sm_scale=sm, kv_chunk=chunk)
+    else:
+        out, lse, e = extend(B, cache, q, [rows], sm_scale=sm, kv_chunk=chunk, kv_end=[L] * rows)
+    assert e == 0
+    assert (np.abs(host(out)) > 0.005).all()
+    check(cache, q, out, lse, None if rows == 1 else [rows], kv_end=None if rows == 1 else [L] * rows, sm_scale=sm)
