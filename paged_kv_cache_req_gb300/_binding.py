@@ -511,9 +511,12 @@ def pkv_quant_extend_workspace_size(args: QuantArgs) -> int:
 
 def _quant_attend(fn, who, args, workspace, err_flags, stream):
     dev = args._dev
-    if dev != _device() or workspace.get_device() != dev or err_flags.get_device() != dev:
-        raise ValueError("%s: the workspace, err_flags and the current device must be the pool's (cuda:%d)" % (who, dev))
-    st = fn(ctypes.byref(args), workspace.data_ptr(), workspace.nbytes, err_flags.data_ptr(), _quant_stream(stream, dev))
+    if dev != _device() or workspace.get_device() != dev:
+        raise ValueError("%s: the workspace and the current device must be the pool's (cuda:%d)" % (who, dev))
+    if not workspace.is_contiguous():
+        raise ValueError("%s: the workspace must be contiguous" % who)
+    st = fn(ctypes.byref(args), workspace.data_ptr(), workspace.nbytes, _ptr(err_flags, "err_flags", _I32T, None, dev),
+            _quant_stream(stream, dev))
     if st != PKV_OK:
         _check(st, who)
 
