@@ -29,9 +29,9 @@ runs either through its own page list ("paged": the page-aligned encoder of
 followed by a varlen decode ("gather": "Approach 2").
 
 With ``quant=True`` (GQA) the K/V pool is held in 4 bits (see pkv_quant_store): the
-given bf16 pools are quantised once, and the step's calls are their 4-bit forms
-(pkv_quant_store, pkv_quant_decode or pkv_quant_extend, and pkv_quant_gather before a
-contiguous cross-attention).  ``scales`` are the heads' fp32 (k_scale, v_scale), by
+given bf16 pools are quantised once and not kept (k_pool and v_pool are None then), and the
+step's calls are their 4-bit forms (pkv_quant_store, pkv_quant_decode or pkv_quant_extend,
+and pkv_quant_gather before a contiguous cross-attention).  ``scales`` are the heads' fp32 (k_scale, v_scale), by
 default each head's largest magnitude in the pools / 2688.
 
 Nothing here computes: every step runs in libpkv's kernels.
@@ -129,6 +129,9 @@ class DecodeStep:
         vals = make_values(wl, seed=seed) if values is None else values
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
         self.quant = _QuantPool(self.k_pool, self.v_pool, ps, self.err, scales) if quant else None
+        if quant:
+            del pools
+            self.k_pool = self.v_pool = None   # nothing reads the bf16 rows again
         Bn = wl.batch
         self.k_new = vals["k_new"].to(dev)
         self.v_new = vals["v_new"].to(dev) if vals["v_new"] is not None else None
@@ -163,7 +166,7 @@ class DecodeStep:
             max_pages = -(-pb.max_len // ps) if pb.max_len else 0
             if pb.gather:
                 rows = int(p.seq_lens.sum())
-                pb.k_rag = torch.empty((max(rows, 1),) + tuple(self.k_pool.shape[1:]), dtype=torch.bfloat16, device=dev)
+                pb.k_rag = torch.empty((max(rows, 1),) + tuple(self.k_new.shape[1:]), dtype=torch.bfloat16, device=dev)
                 pb.v_rag = torch.empty_like(pb.k_rag)
                 pb.cu = torch.empty(Bn + 1, dtype=torch.int32, device=dev)
                 layout = B.PKV_LAYOUT_VARLEN
@@ -419,6 +422,7 @@ class ExtendStep:
             self.seg = [getattr(self._seg_holder, "s%d" % i) for i in range(len(self.seg))]
         self.quant = _QuantPool(self.k_pool, self.v_pool, ps, self.err, scales) if quant else None
         if self.quant is not None:
+            self.k_pool = self.v_pool = None   # nothing reads the bf16 rows again
             kw = dict(sm_scale=ew.sm_scale, max_seq_len=int(ew.seq_lens.max()), kv_end=self.kv_end, lse=self.lse,
                       qo_indptr=self.qo_indptr, kv_chunk=kv_chunk, total_kv=int(ew.seq_lens.sum()),
                       max_q_len=int(ew.qo_lens.max()))
