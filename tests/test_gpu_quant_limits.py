@@ -222,3 +222,38 @@ def test_far_queries_over_vanishing_scales(B, rows, chunk):
     assert e == 0
     assert (np.abs(host(out)) > 0.005).all()
     check(cache, q, out, lse, None if rows == 1 else [rows], kv_end=None if rows == 1 else [L] * rows, sm_scale=sm)
+
+
+@pytest.mark.parametrize("D,H", [(128, 1), (64, 2), (128, 8), (64, 3)])
+@pytest.mark.parametrize("batch", [2047, 2048, 2049, 5000])
+def test_gather_of_thousands_of_requests(B, batch, D, H):
+    """Requests past the 2048 whose offsets are scanned at a time: empty ones at the border, tokens of
+    half a warp and whole ones; a capacity that ends inside the second part."""
+    rng = np.random.default_rng(98 + batch + D + H)
+    ps, slots, lens = 16, 640, rng.integers(0, 6, batch).astype(np.int32)
+    lens[2040:2052] = 0
+    lens[2050:2051] = 9
+    lens[-1] = 4
+    total = int(lens.sum())
+    x = values(rng, (slots, H, D))
+    g = (2.0 ** -rng.integers(0, 4, H)).astype(np.float32)      # (products with it are exact)
+    pool = np.zeros((slots // ps, H, R.tile_bytes(ps, D)), dtype=np.uint8)
+    for part in (0, 1):
+        R.write(pool, ps, np.arange(slots), part, *R.quantise(x * (1 + part), g))
+    table = rng.integers(0, slots, (batch + 3, 12)).astype(np.int32)
+    rows = rng.permutation(batch + 3)[:batch].astype(np.int32)
+    flat = np.concatenate([table[r, :n] for r, n in zip(rows, lens)]).astype(np.int64)
+    want = [R.bf16(R.read(pool, ps, D, flat, part, g).astype(np.float32)) for part in (0, 1)]
+    cu_want = np.concatenate([[0], np.cumsum(lens)])
+    caps = [total + 7] + ([int(cu_want[2048]) + 1, int(cu_want[3000]) + 1] if batch == 5000 else [])
+    for cap in caps:
+        out = [torch.full((cap, H, D), 9.0, dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+        cu = torch.zeros(batch + 1, dtype=torch.int32, device=DEV)
+        err = torch.zeros(1, dtype=torch.int32, device=DEV)
+        B.pkv_quant_gather(up(pool), up(table), up(rows), up(lens), int(lens.max()), out[0], out[1], cu, err, page_size=ps,
+                           k_scale=up(g), v_scale=up(g))
+        assert err.item() == (0 if cap >= total else B.PKV_DEVERR_CAPACITY)
+        assert cu.tolist() == cu_want.tolist()
+        n = min(cap, total)
+        for o, w in zip(out, want):
+            assert (host(o[:n]) == w[:n]).all() and (o[n:] == 9).all()
