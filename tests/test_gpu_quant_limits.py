@@ -257,3 +257,68 @@ def test_gather_of_thousands_of_requests(B, batch, D, H):
         n = min(cap, total)
         for o, w in zip(out, want):
             assert (host(o[:n]) == w[:n]).all() and (o[n:] == 9).all()
+
+
+PATHS = [([1, 1, 1], dict(kv_chunk=0)), ([1, 1, 1], dict(kv_chunk=128)), ([6, 3, 0], dict(kv_chunk=0)), ([6, 3, 5], dict(kv_chunk=128)),
+         ([200, 150, 140], dict(kv_chunk=0)), ([200, 1, 140], dict(kv_chunk=256, max_q_len=200))]
+
+
+def call(B, cache, q, rows, **kw):
+    if rows == [1, 1, 1]:
+        return decode(B, cache, q, **kw)
+    return extend(B, cache, q, rows, **kw)
+
+
+@pytest.mark.parametrize("rows,kw", PATHS)
+@pytest.mark.parametrize("D,ps", [(128, 16), (64, 64), (128, 4)])
+def test_a_poisoned_value_reaches_only_who_sees_it(B, D, ps, rows, kw):
+    """A NaN in a stored value: the rows that see its key are NaN in that block, the others as without it."""
+    rng = np.random.default_rng(99)
+    cache = Cache(rng, [333, 200, 150], ps, 2, D)
+    c, s = R.quantise(values(rng, (1, 2, D)), cache.vs)
+    s[0, 1, 2] = 0x7f
+    at = 331
+    R.write(cache.pool, ps, cache.slots[0][at:at + 1], 1, c, s)
+    q = to_bf16(values(rng, (sum(rows), 8, D)))
+    out, lse, e = call(B, cache, q, rows, **kw)
+    assert e == 0
+    o = host(out)
+    seen = np.zeros(o.shape[:2], dtype=bool)
+    first = max(0, at + 1 - (333 - rows[0] + 1)) if rows != [1, 1, 1] else 0
+    seen[first:rows[0], 4:] = True
+    assert np.isnan(o[seen][:, 32:48]).all() and np.isfinite(o[~seen]).all()
+    clean = c.copy(), s.copy()
+    clean[1][0, 1, 2] = 0
+    R.write(cache.pool, ps, cache.slots[0][at:at + 1], 1, *clean)
+    o2, l2, e = call(B, cache, q, rows, **kw)
+    assert e == 0 and (host(o2)[~seen] == o[~seen]).all()
+    check(cache, q, o2, l2, None if rows == [1, 1, 1] else rows)
+
+
+@pytest.mark.parametrize("rows,kw", PATHS)
+def test_strided_queries_and_tiles(B, rows, kw):
+    """Query rows as slices of wider rows, tiles further apart than they are long, rows past the last
+    request's (left as they were), and a call without lse."""
+    rng = np.random.default_rng(100)
+    D, H, g = 64, 3, 4
+    cache = Cache(rng, [333, 200, 150], 16, H, D)
+    one, n = rows == [1, 1, 1], sum(rows)
+    q = to_bf16(values(rng, (n, H * g, D)))
+    out, lse, e = call(B, cache, q, rows, **kw)
+    assert e == 0
+    check(cache, q, out, lse, None if one else rows)
+    offsets = {} if one else dict(qo_indptr=up(np.concatenate([[0], np.cumsum(rows)]).astype(np.int32)))
+    o2, err = torch.zeros_like(q), torch.zeros(1, dtype=torch.int32, device=DEV)
+    a = cache.args(B, "table", q, o2, **dict(kw, **offsets))
+    size, fn = ((B.pkv_quant_decode_workspace_size, B.pkv_quant_decode) if one else
+                (B.pkv_quant_extend_workspace_size, B.pkv_quant_extend))
+    fn(a, torch.empty(size(a), dtype=torch.uint8, device=DEV), err)
+    assert err.item() == 0 and torch.equal(o2, out)
+    wide = torch.full((n + 5, H * g * D + 2 * H * D + 8), float("nan"), dtype=torch.bfloat16, device=DEV)
+    wide[:n, 8:8 + H * g * D] = q.view(n, -1)
+    sliced = wide[:n if one else n + 5, 8:8 + H * g * D].unflatten(1, (H * g, D))
+    tiles = torch.full((cache.pool.shape[0], H + 2, cache.pool.shape[2]), 0xFF, dtype=torch.uint8, device=DEV)
+    tiles[:, :H] = up(cache.pool)
+    o2, l2, e = call(B, cache, sliced, rows, **dict(kw, pool=tiles[:, :H], **offsets))
+    assert e == 0 and (o2[n:] == 3).all() and (l2[n:] == 3).all()
+    check(cache, q, o2[:n], l2[:n], None if one else rows)
