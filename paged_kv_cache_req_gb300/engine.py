@@ -31,8 +31,8 @@ followed by a varlen decode ("gather": "Approach 2").
 With ``quant=True`` (GQA) the K/V pool is held in 4 bits (see pkv_quant_store): the
 given bf16 pools are quantised once and not kept (k_pool and v_pool are None then), and the
 step's calls are their 4-bit forms (pkv_quant_store, pkv_quant_decode or pkv_quant_extend,
-and pkv_quant_gather before a contiguous cross-attention).  ``scales`` are the heads' fp32 (k_scale, v_scale), by
-default each head's largest magnitude in the pools / 2688.
+and pkv_quant_gather before a contiguous cross-attention).  ``scales`` are the heads' fp32
+(k_scale, v_scale), by default each head's largest finite magnitude in the pools / 2688.
 
 Nothing here computes: every step runs in libpkv's kernels.
 """
@@ -84,13 +84,16 @@ class _QuantPool:
         if slots % tile:
             raise ValueError("the pool's slots must be whole pages")
         dev = k_pool.device
+        step = 1 << 20
         if scales is None:
             # the largest code (6) x the largest block scale (448) is the head's largest magnitude
-            scales = [(p.abs().amax(dim=(0, 2)).float() / 2688.0).clamp_(min=1e-30) for p in (k_pool, v_pool)]
+            # (of its finite values: a block that holds another is NaN whatever the scale)
+            tops = [torch.stack([p[i:i + step].abs().nan_to_num_(0.0, 0.0, 0.0).amax(dim=(0, 2)) for i in range(0, slots, step)])
+                    for p in (k_pool, v_pool)]
+            scales = [(t.amax(0).float() / 2688.0).clamp_(min=1e-30) for t in tops]
         self.page_size = page_size
         self.k_scale, self.v_scale = (x.to(dev) for x in scales)
         self.pool = torch.zeros((slots // tile, hkv, B.pkv_quant_tile_bytes(page_size, d)), dtype=torch.uint8, device=dev)
-        step = 1 << 20
         for i in range(0, slots, step):
             n = min(step, slots - i)
             self.store(k_pool[i:i + n], v_pool[i:i + n], torch.arange(i, i + n, dtype=torch.int32, device=dev), err)

@@ -1,4 +1,5 @@
-"""A 4-bit step holds no bf16 pool."""
+"""A 4-bit step and the bf16 pools it is made from: they are let go, and what is not a number in them
+costs its own block alone."""
 import gc
 
 import pytest
@@ -52,3 +53,21 @@ def test_given_pools_stay_the_callers(engine):
     step = engine.DecodeStep(wl, pools=pools, quant=True)
     step.run()
     assert step.check_errors() == 0 and all(torch.equal(p, w) for p, w in zip(pools, want))
+
+
+def test_a_value_that_is_no_number_leaves_the_head_its_scale(engine):
+    from paged_kv_cache_req_gb300.workloads import make_workload
+    wl = make_workload("tiny_gqa", batch=4)
+    clean = engine.fill_pool(wl, device="cuda")
+    want = engine.DecodeStep(wl, pools=clean, quant=True)
+    pools = [p.clone() for p in clean]
+    # (slot 0 is padding: no request reads it)
+    pools[0][0, 0, 3], pools[1][0, 1, 5], pools[1][0, 0, 40] = float("inf"), float("nan"), float("-inf")
+    step = engine.DecodeStep(wl, pools=pools, quant=True)
+    assert step.check_errors() == 0
+    assert torch.equal(step.quant.k_scale, want.quant.k_scale) and torch.equal(step.quant.v_scale, want.quant.v_scale)
+    want.run()
+    step.run()
+    assert step.check_errors() == 0
+    for name, pb in step.problems.items():
+        assert torch.equal(pb.out, want.problems[name].out)
