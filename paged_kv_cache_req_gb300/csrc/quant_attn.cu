@@ -1288,7 +1288,9 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const Params p) {
         if (sub || !live) continue;
         const int row = rb * 8 * NT + lr, tok = token_of(p, row);
         const int64_t at = static_cast<int64_t>(qo0 + tok) * p.hq + kh * p.g + (row - tok * p.g);
-        const float inv = l == 0.f ? 0.f : rcp(l);
+        // (a division, not rcp(): with that the compiler orders the loop's loads otherwise, 77 us for 69 at
+        // 1 request x 131072 keys x 1 kv head)
+        const float inv = l == 0.f ? 0.f : 1.f / l;
         *reinterpret_cast<uint2 *>(p.out + at * D + d0) =
             make_uint2(pack_bf16x2(o.x * inv * gv, o.y * inv * gv), pack_bf16x2(o.z * inv * gv, o.w * inv * gv));
         if (d0 == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
