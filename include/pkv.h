@@ -603,12 +603,15 @@ size_t pkv_quant_decode_workspace_size(const pkv_quant_args *args);
  * The query rows of request b are qo_indptr[b] .. qo_indptr[b+1]-1, each over the keys
  * below its bound (kv_end, or causal over the last positions); a row with bound 0 gives
  * out = 0, lse = -inf.  The new tokens must be in the pool already (pkv_quant_store).
- * Checks and flags are pkv_extend's; more than total_kv keys raise PKV_DEVERR_CAPACITY.
+ * Checks and flags are pkv_extend's.  Given bounds say what counts, not what is read: a
+ * request's keys are read to the last one whatever kv_end.
  * Requests with more than 128 (row, query head) pairs per kv head have their keys and
  * values copied out of the pool into the workspace as 16-bit floats first (exactly), which
- * total_kv sizes; a step of which max_q_len, or without it the average, says that there is
+ * total_kv sizes (for all requests of the step; more keys to copy than it says raise
+ * PKV_DEVERR_CAPACITY); a step of which max_q_len, or without it the average, says that there is
  * no such request needs no room for that, and computes a larger request all the same.  Their
- * weights are 2^-11 relative down to 2^-21 of the row's largest and 2^-32 of it below that.  A
+ * weights are 2^-11 relative down to 2^-21 of the row's largest and 2^-32 of it below that, and
+ * their scores before k_scale and sm_scale (sums of q times code * s) have to fit fp32.  A
  * row that sees a key whose V holds a NaN block may be NaN in all its dims there.
  * workspace as for pkv_quant_decode, of pkv_quant_extend_workspace_size(args) bytes.
  */

@@ -16,7 +16,8 @@
 // tcgen05 tile would be mostly padding, and K and V would first have to be written out to
 // shared memory as 16-bit values, 3.6 times what is read.)  A code times its block scale is exact in fp16; q
 // (bf16) is taken into fp16 exactly too, after a power of two per row that brings its
-// largest magnitude to [64, 128) (elements 2^-30 below the largest lose bits).  The
+// largest magnitude to [64, 128) (elements more than 2^23 below the largest lose bits: 2^-31
+// of it at most).  The
 // dims are assigned to the MMA's contraction (and output row) indices so that a lane reads
 // contiguous codes: lane (r, c) = (lane / 4, lane % 4) holds dims D/4 c ... of key row r for
 // K, and dims D/8 r ... of keys of column c for V.  Softmax in base 2 with a running
@@ -34,7 +35,7 @@
 // registers and less code but took 71 us where 32 take 66 (16 requests x 16384 keys x 8 kv
 // heads), 64 gained 4 % on long requests of 64 dims and lost as much on short ones.
 // Measured at 8 kv heads of 128, 32 query heads, page size 64: 128 requests of 128 to 16384
-// keys 98 us, 5.1 TB/s, fixed costs included; 90 % of the copy rate per further request.
+// keys 99 us, 5.0 TB/s, fixed costs included; 90 % of the copy rate per further request.
 // Some 19 us of a call do not depend on the keys: start and tile table 6, first copies and
 // last tiles, merge 5.
 #include <algorithm>
@@ -1545,7 +1546,8 @@ static bool make_plan(const pkv_quant_args *a, bool extend, Plan &pl) {
         // allows: lengths are rarely equal).  Measured (8 kv heads of 128, us; unit / spans): decodes of
         // 16 x 768 keys 7.0 / 12.9, 16 x 3000 17.7 / 24.8, 32 x 700 12.7 / 15.8, 4 x 2048 11.5 / 12.5, but
         // 64 x 256 18.3 / 15.0 and 64 x 64 17.5 / 10.3; 16 rows per head, 4 x 512 keys 9.0 / 15.1, 16 x 2000
-        // 17.4 / 25.8, 32 x 256 15.0 / 19.4; 48 rows, 4 x 1000 11.9 / 18.6.
+        // 17.4 / 25.8, 32 x 256 15.0 / 19.4; 48 rows, 4 x 1000 11.9 / 18.6.  (The same rule at 64 dims,
+        // whose tiles are half the bytes and take some two thirds of the time.)
         // (Calls of more units than a grid's side take the spans in any case.)
         const int nt = rows <= 8 ? 1 : 2, warps = warps_per_sm(a->head_dim, nt);
         const int64_t blocks = (rows + 8 * nt - 1) / (8 * nt), units = batch * a->num_kv_heads * blocks;
