@@ -1001,7 +1001,7 @@ __global__ void __launch_bounds__(warps_per_sm(D, NT) * 32, 1) attend_kernel(con
         if (!ok) break;
         const uint8_t *stage = ring + take * stage_bytes;
         if (NT == 1 && w.t + 1 >= w.t_end && f.queued > seg) {   // the next segment's q on its way
-            __syncwarp();   // lane 0 wrote the entry, maybe in this round's fetch(); a vote orders no memory
+            __syncwarp();   // lane 0 wrote the entry, maybe in the fetch() just above; a vote orders no memory
             load_q<D, NT>(p, queue[seg % kQueue], 0, q_raw, lane);
             q_ahead = true;
         }

@@ -322,3 +322,17 @@ def test_strided_queries_and_tiles(B, rows, kw):
     o2, l2, e = call(B, cache, sliced, rows, **dict(kw, pool=tiles[:, :H], **offsets))
     assert e == 0 and (o2[n:] == 3).all() and (l2[n:] == 3).all()
     check(cache, q, o2[:n], l2[:n], None if one else rows)
+
+
+@pytest.mark.parametrize("batch,chunk", [(300, 0), (1100, 0), (300, 128)])
+def test_copied_keys_of_hundreds_of_requests(B, batch, chunk):
+    """Many requests of just more rows than the spans take, others of few rows or none between them."""
+    rng = np.random.default_rng(101 + batch)
+    rows = rng.choice([0, 1, 5, 32, 33, 40], batch, p=[0.1, 0.1, 0.1, 0.1, 0.4, 0.2])
+    rows[[0, -1]] = 33, 40
+    lens = np.maximum(rows, rng.integers(0, 200, batch)).tolist()
+    cache = Cache(rng, lens, 16, 2, 64)
+    q = to_bf16(values(rng, (int(rows.sum()), 8, 64)))
+    out, lse, e = extend(B, cache, q, rows.tolist(), max_q_len=40, total_kv=sum(lens), kv_chunk=chunk)
+    assert e == 0
+    check(cache, q, out, lse, rows.tolist(), only=[0, 1, 255, 256, 257, batch - 2, batch - 1] + list(range(0, batch, batch // 20)))
