@@ -43,7 +43,8 @@
 // largest weight, but an absolute 2^-32 of the largest below that (and 0 below 2^-32), where bf16
 // keeps its bits: weights are held times 2^7 for that, as high as 2^15 with a maximum that is
 // raised past 2^8 only (one raised past 2^4, with a lift of 11, costs 8 %: 1,195 -> 1,293 us at 8192 rows
-// over 16384 keys).
+// over 16384 keys).  kBf16V (the 8-bit pool, whose scales need bf16's range): V and P bf16, as for
+// the bf16 pool.
 #include <algorithm>
 
 #include "extend_held.cuh"
@@ -455,7 +456,7 @@ __device__ __forceinline__ Item ring_read(const Item *ring, uint64_t *bars, uint
 
 // Sixteen warps: four of them on one SM sub-partition share its 16K registers, so
 // at most 128 registers a thread.
-template <int D, bool kHeld>
+template <int D, bool kHeld, bool kBf16V>
 __global__ void __maxnreg__(128)
 ext_kernel(const Params p, const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
            const __grid_constant__ CUtensorMap tmv) {
@@ -808,7 +809,7 @@ ext_kernel(const Params p, const __grid_constant__ CUtensorMap tmq, const __grid
         // Group g's half of tile n (keys 64 g ... 64 g + 63) into its accumulator.  An
         // item's first tile starts both accumulators afresh, once the epilogue has read
         // the previous item's.
-        const uint32_t idesc = kHeld ? tc05::idesc_f16_f32(kRows, D, false, true) : tc05::idesc_bf16_f32(kRows, D, false, true);
+        const uint32_t idesc = kBf16V ? tc05::idesc_bf16_f32(kRows, D, false, true) : tc05::idesc_f16_f32(kRows, D, false, true);
         uint32_t n = 0, io = 0;
         bool ok = true;
         for (uint32_t k = 0; ok; ++k) {
@@ -1082,8 +1083,8 @@ ext_kernel(const Params p, const __grid_constant__ CUtensorMap tmq, const __grid
                     const float a0 = ex2(ya.x), a1 = ex2(ya.y), b0 = ex2(yb.x), b1 = ex2(yb.y);
                     acc = add2(acc, pair(a0, a1));
                     acc = add2(acc, pair(b0, b1));
-                    h0[j] = kHeld ? pack_f16x2(a0, a1) : pack_bf16x2(a0, a1);
-                    h1[j] = kHeld ? pack_f16x2(b0, b1) : pack_bf16x2(b0, b1);
+                    h0[j] = kBf16V ? pack_bf16x2(a0, a1) : pack_f16x2(a0, a1);
+                    h1[j] = kBf16V ? pack_bf16x2(b0, b1) : pack_f16x2(b0, b1);
                 }
                 const float2 ls = unpair(acc);
                 l += ls.x + ls.y;
@@ -1298,7 +1299,7 @@ static pkv_status validate(const pkv_extend_args *a, bool check_ptrs) {
     return PKV_OK;
 }
 
-template <int D, bool kHeld>
+template <int D, bool kHeld, bool kBf16V>
 static pkv_status launch_t(const pkv_extend_args *a, const Plan &pl, void *ws, int32_t *err, cudaStream_t s,
                            const Held *held = nullptr) {
     using C = Cfg<D>;
@@ -1378,7 +1379,7 @@ static pkv_status launch_t(const pkv_extend_args *a, const Plan &pl, void *ws, i
         const uint32_t bk[2] = {64, kTile};
         // (the copies move 16-bit words: V's are fp16)
         if (!encode_tmap_bf16(&tmk, held->k, 2, dk, sk, bk) || !encode_tmap_bf16(&tmv, held->v, 2, dk, sk, bk))
-            return fail(PKV_ERR_CUDA, "pkv_quant_extend: cuTensorMapEncodeTiled rejected the workspace");
+            return fail(PKV_ERR_CUDA, "%s: cuTensorMapEncodeTiled rejected the workspace", held->who);
     } else {
         // pool rows as a 2-D tensor (kv heads x head_dim wide): a box is 64 dims of one
         // kv head over a page's rows
@@ -1389,17 +1390,17 @@ static pkv_status launch_t(const pkv_extend_args *a, const Plan &pl, void *ws, i
         if (!encode_tmap_bf16(&tmk, a->k_pool, 2, dk, sk, bk) || !encode_tmap_bf16(&tmv, a->v_pool, 2, dk, sv, bk))
             return fail(PKV_ERR_CUDA, "pkv_extend: cuTensorMapEncodeTiled rejected the pools");
     }
-    std::atomic<int64_t> *m_lim = device_memo(reinterpret_cast<const void *>(ext_kernel<D, kHeld>));
+    std::atomic<int64_t> *m_lim = device_memo(reinterpret_cast<const void *>(ext_kernel<D, kHeld, kBf16V>));
     if (!m_lim) return fail(PKV_ERR_CUDA, "pkv_extend: cannot query the current device");
     if (m_lim->load() == 0) {   // kernel attributes are per device
         int optin = 0, dev = 0;
         cudaFuncAttributes fa{};
         if (cudaGetDevice(&dev) != cudaSuccess ||
             cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev) != cudaSuccess ||
-            cudaFuncGetAttributes(&fa, ext_kernel<D, kHeld>) != cudaSuccess)
+            cudaFuncGetAttributes(&fa, ext_kernel<D, kHeld, kBf16V>) != cudaSuccess)
             return fail(PKV_ERR_CUDA, "pkv_extend: cannot query shared-memory limits");
         const size_t l = static_cast<size_t>(optin) - fa.sharedSizeBytes;
-        if (cudaFuncSetAttribute(ext_kernel<D, kHeld>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(l)) !=
+        if (cudaFuncSetAttribute(ext_kernel<D, kHeld, kBf16V>, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(l)) !=
             cudaSuccess)
             return fail(PKV_ERR_CUDA, "pkv_extend: cannot raise the shared-memory limit");
         m_lim->store(static_cast<int64_t>(l));
@@ -1416,13 +1417,13 @@ static pkv_status launch_t(const pkv_extend_args *a, const Plan &pl, void *ws, i
     const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(pl.items_max, sm_count()));
     pkv_status st;
     if (kHeld) {   // the kernel before it zeroed the item counter
-        st = launch_status(launch_chained(ext_kernel<D, kHeld>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, s, p,
+        st = launch_status(launch_chained(ext_kernel<D, kHeld, kBf16V>, dim3(static_cast<unsigned>(grid)), dim3(kThreads), smem, s, p,
                                           tmq, tmk, tmv),
-                           "pkv_quant_extend (attention kernel)");
+                           held->who);
     } else {
         if (cudaMemsetAsync(p.counter, 0, sizeof(int32_t), s) != cudaSuccess)
             return fail(PKV_ERR_CUDA, "pkv_extend: cannot reset the item counter");
-        ext_kernel<D, kHeld><<<static_cast<unsigned>(grid), kThreads, smem, s>>>(p, tmq, tmk, tmv);
+        ext_kernel<D, kHeld, kBf16V><<<static_cast<unsigned>(grid), kThreads, smem, s>>>(p, tmq, tmk, tmv);
         st = check_launch("pkv_extend (attention kernel)");
     }
     if (st != PKV_OK || pl.nch_max <= 1) return st;
@@ -1445,9 +1446,10 @@ size_t held_counter_offset(const pkv_extend_args *a) {
 
 pkv_status held_launch(const pkv_extend_args *a, const Held &held, void *workspace, int32_t *err, cudaStream_t s) {
     Plan pl;
-    if (!make_plan(a, pl)) return fail(PKV_ERR_UNSUPPORTED, "pkv_quant_extend: too many work items");
-    return a->head_dim == 128 ? launch_t<128, true>(a, pl, workspace, err, s, &held)
-                              : launch_t<64, true>(a, pl, workspace, err, s, &held);
+    if (!make_plan(a, pl)) return fail(PKV_ERR_UNSUPPORTED, "%s: too many work items", held.who);
+    auto *launch = held.bf16_v ? (a->head_dim == 128 ? launch_t<128, true, true> : launch_t<64, true, true>)
+                               : (a->head_dim == 128 ? launch_t<128, true, false> : launch_t<64, true, false>);
+    return launch(a, pl, workspace, err, s, &held);
 }
 
 }  // namespace ext
@@ -1478,8 +1480,8 @@ extern "C" pkv_status pkv_extend(const pkv_extend_args *args, void *workspace, s
     if (!workspace || !aligned(workspace, 256))
         return fail(PKV_ERR_INVALID_ARG, "pkv_extend: workspace must be non-null and 256-byte aligned");
     auto s = reinterpret_cast<cudaStream_t>(stream);
-    return args->head_dim == 128 ? launch_t<128, false>(args, pl, workspace, err_flags, s)
-                                 : launch_t<64, false>(args, pl, workspace, err_flags, s);
+    return args->head_dim == 128 ? launch_t<128, false, true>(args, pl, workspace, err_flags, s)
+                                 : launch_t<64, false, true>(args, pl, workspace, err_flags, s);
 }
 
 extern "C" pkv_status pkv_span_plan(int32_t batch, const int32_t *seg_indptr, const int32_t *seg_kind,

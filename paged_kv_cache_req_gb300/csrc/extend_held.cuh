@@ -1,5 +1,5 @@
-// What quant_attn.cu hands to the multi-query kernel of extend.cu: keys and values taken out
-// of the 4-bit pool into workspace tensors.
+// What the quantised pools' attention hands to the multi-query kernel of extend.cu: keys and
+// values taken out of the pool into workspace tensors.
 #pragma once
 
 #include "pkv_internal.cuh"
@@ -8,13 +8,15 @@ namespace pkv {
 namespace ext {
 
 struct Held {
-    const void *k, *v;           // bf16 / fp16 [D/64][kv heads][rows][64]
+    const void *k, *v;           // bf16, and fp16 or bf16 (bf16_v) [D/64][kv heads][rows][64]
     int64_t rows;
     const int32_t *first_row;    // device [B + 1]: request b's keys are rows first_row[b] .. first_row[b + 1] - 1
     const int32_t *order;        // device [B]: the requests, the longest first (their items are handed out so)
     const float *k_scale, *v_scale;
     int64_t q_row_stride;
     int32_t min_rows;            // requests with at most this many (token, head) rows per kv head are left out
+    bool bf16_v;                 // V, and so the weights that multiply it, in bf16
+    const char *who;             // the call, for its errors
 };
 
 // Bytes of the kernel's own workspace, the place of its item counter there (int32, to be
