@@ -619,6 +619,213 @@ pkv_status pkv_quant_extend(const pkv_quant_args *args, void *workspace, size_t 
                             int32_t *err_flags, pkv_stream_t stream);
 size_t pkv_quant_extend_workspace_size(const pkv_quant_args *args);
 
+/*
+ * The 8-bit K/V pool: pkv_byte_store, pkv_byte_gather, pkv_byte_decode, pkv_byte_extend and
+ * pkv_byte_weights.
+ *
+ * One byte per element: half of bf16's memory and traffic, at four significant bits.  Slots
+ * lie in tiles of t = min(page_size, 64) consecutive ones, as in the 4-bit pool; a tile's K
+ * rows of one kv head are a block with one scale, and its V rows another.  A scale is a
+ * power of two s = 2^(E - 127), held as the byte E; an element is an e4m3 float:
+ *     E = the least number >= 1 with max |x_i| <= 448 s,   code_i = e4m3(x_i / s),   value_i = code_i s
+ * (to nearest, ties to even; E is at most 247).  An infinity or a NaN reads back as NaN and does
+ * not count in the maximum.  Values are fp32: those that round to 2^128 are infinite.
+ *
+ * The pool is uint8: tiles tile_stride bytes apart (a multiple of 16; the pool is 16-byte
+ * aligned), each of pkv_byte_tile_bytes(page_size, head_dim, kv_heads) bytes:
+ *     for each kv head: K codes [t][head_dim], V codes [t][head_dim];
+ *     then for each kv head two bytes: E of K, E of V;
+ * rounded up to 32 bytes, from t = 16 on to 128.  Slots, pages and req_to_token are those of
+ * the other pools.  page_size is a power of two in [1, 1024], head_dim 64 or 128 (K and V
+ * alike).  A pool needs no initialisation.
+ */
+
+/* Bytes of a tile (0 for an unsupported page_size or head_dim, or kv_heads < 1). */
+size_t pkv_byte_tile_bytes(int32_t page_size, int32_t head_dim, int32_t kv_heads);
+
+/*
+ * pkv_byte_store -- pkv_store into an 8-bit pool: quantise this step's K/V rows.
+ *
+ * k_new, v_new and slot_mapping as for pkv_quant_store.  For each tile and kv head, K and V
+ * apart, let E be what the call's rows in the tile need.  Where they hold the tile's first
+ * slot the tile begins anew: its scale becomes E, and what its other slots held is lost
+ * (slots of a page are filled in order; to write a tile's rows again, write all of them
+ * from the first one on in one call).  Else the scale becomes the larger of E and the tile's,
+ * and where it grows the codes of the other slots follow: e4m3(code 2^(E_old - E_new)), exact
+ * for what stays normal.  Of rows that name one slot twice one is stored, the others count for
+ * nothing.  Nothing else of the pool is written.
+ * workspace: at least pkv_byte_store_workspace_size(num_tiles, page_size) bytes, 256-byte
+ * aligned, not shared with a call that may run at the same time; it needs no initialisation.
+ */
+pkv_status pkv_byte_store(void *pool, int64_t num_tiles, int64_t tile_stride, int32_t kv_heads, int32_t head_dim,
+                        int32_t page_size, const void *k_new, const void *v_new, int64_t k_token_stride,
+                        int64_t v_token_stride, const int32_t *slot_mapping, int32_t n_tokens, void *workspace,
+                        size_t workspace_bytes, int32_t *err_flags, pkv_stream_t stream);
+/* Workspace bytes pkv_byte_store needs for such a pool, whatever the call (at least 256; 0 on invalid arguments). */
+size_t pkv_byte_store_workspace_size(int64_t num_tiles, int32_t page_size);
+
+/*
+ * pkv_byte_gather -- pkv_ragged_gather from an 8-bit pool: rows read back as bf16.
+ *
+ * As pkv_quant_gather, without head scales; value_i rounded to bf16 (nearest even).
+ */
+pkv_status pkv_byte_gather(const void *pool, int64_t num_tiles, int64_t tile_stride, int32_t kv_heads, int32_t head_dim,
+                         int32_t page_size, const int32_t *req_to_token, int64_t r2t_rows, int64_t r2t_row_stride,
+                         int64_t r2t_width, const int32_t *req_pool_idx, const int32_t *kv_start,
+                         const int32_t *seq_lens, int32_t batch, int32_t max_seq_len, void *k_out, void *v_out,
+                         int64_t out_rows_cap, int32_t *cu_seqlens, int32_t *err_flags, pkv_stream_t stream);
+
+/* Arguments of pkv_byte_decode, pkv_byte_extend and pkv_byte_weights. */
+typedef struct pkv_byte_args {
+    int32_t layout;            /* PKV_LAYOUT_CSR, PKV_LAYOUT_BLOCK_TABLE or PKV_LAYOUT_REQ_TO_TOKEN */
+    int32_t batch;             /* B >= 0 */
+    int32_t num_q_heads;       /* Hq */
+    int32_t num_kv_heads;      /* Hkv; Hq / Hkv any whole number in [1, 16] */
+    int32_t head_dim;          /* 64 or 128 */
+    int32_t page_size;
+    float sm_scale;            /* softmax scale, positive and finite */
+    int32_t max_seq_len;       /* host upper bound on every request's key count */
+    int32_t kv_chunk;          /* keys per split, a multiple of 64; 0 lets the library choose */
+    int32_t block_table_width;
+    int32_t max_q_len;         /* with qo_indptr: host upper bound on a request's query rows; 0: unknown */
+    int64_t total_q;           /* query rows: B without qo_indptr, else qo_indptr[B] */
+    int64_t total_kv;          /* host upper bound on the sum of the key counts, as in pkv_quant_args */
+    int64_t num_tiles;         /* the pool (see above) */
+    int64_t tile_stride;
+    int64_t q_row_stride;      /* elements between query rows (>= Hq * head_dim, a multiple of 8) */
+    int64_t kv_indices_len;    /* CSR: entries of kv_indices */
+    const void *q;             /* bf16 [total_q, Hq, head_dim], rows q_row_stride apart */
+    const void *pool;
+    const int32_t *qo_indptr;  /* pkv_byte_extend, pkv_byte_weights [B+1]; NULL for pkv_byte_decode */
+    const int32_t *kv_end;     /* with qo_indptr: [total_q] or NULL (causal), as for pkv_extend */
+    const int32_t *kv_indptr;        /* CSR [B+1] */
+    const int32_t *kv_indices;       /* CSR pages */
+    const int32_t *kv_last_page_len; /* CSR [B] */
+    const int32_t *block_table;      /* BLOCK_TABLE [B, block_table_width] */
+    const int32_t *seq_lens;         /* BLOCK_TABLE and REQ_TO_TOKEN [B] */
+    const int32_t *req_to_token;     /* REQ_TO_TOKEN: as in pkv_decode_args */
+    int64_t r2t_rows;
+    int64_t r2t_row_stride;
+    int64_t r2t_width;
+    const int32_t *req_pool_idx;
+    const int32_t *kv_start;
+    void *out;                 /* bf16 [total_q, Hq, head_dim]; not used by pkv_byte_weights */
+    float *lse;                /* fp32 [total_q, Hq], natural log; nullable (pkv_byte_weights: an input) */
+    const float *acc_in;       /* weights received so far: fp32 [r2t_rows, acc_row_stride], or NULL for zeros */
+    float *acc_out;            /* the same with this call's (may be acc_in); NULL: not asked for */
+    int64_t acc_row_stride;    /* elements between rows of acc_in and acc_out, >= r2t_width */
+} pkv_byte_args;
+
+/*
+ * pkv_byte_decode -- pkv_decode (GQA / MHA) over an 8-bit pool.
+ *
+ * One query row per request over all its keys; the same formulas with K and V the pool's
+ * values.  Page lists, checks and flags are pkv_decode's.  Arithmetic: codes are exact in
+ * fp16; scores, softmax and sums are fp32, the output bf16 rounded to nearest even.  In the
+ * product with V a weight times its block's scale is fp16: 2^-11 relative down to 2^-25, 2^-36
+ * absolute below that, of the row's largest weight times the largest of the scales.  What the
+ * pool holds at slots past a request's keys does not matter, NaN included.
+ * acc_out (PKV_LAYOUT_REQ_TO_TOKEN only): the call also adds up what each key receives,
+ *     acc_out[row, s + t] = acc_in[row, s + t] + sum over query heads h of exp(sm_scale q[b,h] . K[t] - lse[b,h])
+ * for the keys t < L of request b (row = req_pool_idx[b], s = kv_start[b] or 0): the columns
+ * of req_to_token.  Other columns are left as they were.  Requests that share a row get
+ * unspecified sums.
+ * workspace: at least pkv_byte_decode_workspace_size(args) bytes, 256-byte aligned, not
+ * shared with a call that may run at the same time; it needs no initialisation.
+ */
+pkv_status pkv_byte_decode(const pkv_byte_args *args, void *workspace, size_t workspace_bytes, int32_t *err_flags,
+                         pkv_stream_t stream);
+/* Workspace bytes pkv_byte_decode needs for these arguments (at least 256; 0 on invalid arguments). */
+size_t pkv_byte_decode_workspace_size(const pkv_byte_args *args);
+
+/*
+ * pkv_byte_extend -- pkv_extend over an 8-bit pool.
+ *
+ * As pkv_quant_extend, with the pool's values for K and V; acc_in and acc_out must be NULL
+ * (pkv_byte_weights gives the weights of its rows).  Requests with more than 128 (row, query
+ * head) pairs per kv head have their keys and values copied out of the pool into the workspace
+ * as bf16 (exactly), which total_kv sizes; their weights are bf16 in the product with V (2^-9
+ * relative), and a row that sees a key whose V holds a NaN may be NaN in all its dims there.
+ */
+pkv_status pkv_byte_extend(const pkv_byte_args *args, void *workspace, size_t workspace_bytes, int32_t *err_flags,
+                         pkv_stream_t stream);
+size_t pkv_byte_extend_workspace_size(const pkv_byte_args *args);
+
+/*
+ * pkv_byte_weights -- what each key receives from given query rows.
+ *
+ * The query rows of pkv_byte_extend (all of a step's, or some: the last rows of a prompt), with
+ * the lse that it gave for them:
+ *     acc_out[row, s + t] = acc_in[row, s + t] + sum over the request's rows j with t < kv_end[j], heads h of
+ *                           exp(sm_scale q[j,h] . K[t] - lse[j,h])
+ * for all keys t < L of request b.  PKV_LAYOUT_REQ_TO_TOKEN only; qo_indptr, lse and acc_out are
+ * required.  A row whose bound is 0 or outside [0, L], or whose lse is -inf, gives nothing.
+ * V is not read.  Checks, flags and columns as for pkv_byte_decode and pkv_byte_extend.
+ */
+pkv_status pkv_byte_weights(const pkv_byte_args *args, void *workspace, size_t workspace_bytes, int32_t *err_flags,
+                          pkv_stream_t stream);
+size_t pkv_byte_weights_workspace_size(const pkv_byte_args *args);
+
+/* Arguments of pkv_evict. */
+typedef struct pkv_evict_args {
+    int32_t batch;                 /* B in [0, 8192] */
+    int32_t page_size;             /* a power of two in [1, 1024] */
+    int32_t max_seq_len;           /* host upper bound on every request's token count */
+    int64_t num_pool_pages;
+    const int32_t *req_to_token;   /* int32 [r2t_rows, r2t_row_stride], as in pkv_decode_args */
+    int32_t *req_to_token_out;     /* the same shape; may be req_to_token */
+    int64_t r2t_rows;
+    int64_t r2t_row_stride;
+    int64_t r2t_width;
+    const float *acc;              /* fp32 [r2t_rows, acc_row_stride] (see pkv_byte_args) */
+    float *acc_out;                /* the same shape; may be acc */
+    int64_t acc_row_stride;        /* >= r2t_width */
+    const int32_t *req_pool_idx;   /* [B] */
+    const int32_t *kv_start;       /* [B] (multiples of page_size), or NULL for 0 */
+    const int32_t *seq_lens;       /* [B] */
+    int32_t *seq_lens_out;         /* [B]; may be seq_lens */
+    const int32_t *budget;         /* [B] tokens that request b may keep, >= 0 */
+    const int32_t *keep_first;     /* [B] first tokens that stay in any case, or NULL for 0 */
+    const int32_t *keep_last;      /* [B] last tokens that stay in any case, or NULL for 0 */
+    int32_t *free_pages;           /* [free_pages_len], as in pkv_alloc_extend */
+    int64_t free_pages_len;
+    const int32_t *free_state;     /* [2] = {head, count} */
+    int32_t *free_state_out;       /* [2]; may be free_state */
+} pkv_evict_args;
+
+/*
+ * pkv_evict -- give back the pages whose tokens received least attention.
+ *
+ * Request b has n = ceil(L / page_size) pages.  It keeps max(1, budget[b] / page_size) of them,
+ * or all if it has no more: its last page, those that hold one of its first keep_first[b] or
+ * last keep_last[b] tokens (these stay even where they are more), and of the others those
+ * with the highest sums of acc over their tokens.  A sum is in fp64, rounded to fp32 once;
+ * of equal ones the earlier page stays; NaN counts as more than any number.
+ * The kept columns of its row of req_to_token and of acc move together, in order;
+ * seq_lens_out[b] is the number that is left.  Columns of acc_out that fall free become 0 (a new
+ * token starts with none); those of req_to_token_out are left as they were, as is all else
+ * behind L.
+ * Evicted pages go to the front of the free list, free_pages[head - n' .. head), requests in
+ * order, pages in the order of their columns, and free_state_out = {head - n', count + n'}.
+ * Positions that were rotated into the keys stay what they were: a caller counts on.
+ * A page that another request reads too (a shared prefix) must lie within keep_first.
+ *
+ * A row or region outside the table, a negative length, budget, keep_first or keep_last, a
+ * kv_start that is no multiple of page_size, and two requests with one row raise
+ * PKV_DEVERR_RANGE, more than max_seq_len tokens PKV_DEVERR_CAPACITY: that request is left as it
+ * is, with seq_lens_out[b] = seq_lens[b] and nothing copied where the outputs are others.  Where a
+ * request that has to lose pages has one outside the pool (PKV_DEVERR_RANGE) or one whose first slot is not a
+ * multiple of page_size (PKV_DEVERR_CONTIG) among those that may go, it loses none.  Where the
+ * free list has no room before head for all evicted pages, PKV_DEVERR_CAPACITY is raised and no
+ * request loses any.
+ * workspace: at least pkv_evict_workspace_size(batch, max_seq_len, page_size) bytes, 256-byte
+ * aligned, not shared with a call that may run at the same time; it needs no initialisation.
+ */
+pkv_status pkv_evict(const pkv_evict_args *args, void *workspace, size_t workspace_bytes, int32_t *err_flags,
+                     pkv_stream_t stream);
+/* Workspace bytes of pkv_evict (at least 256; 0 on invalid arguments). */
+size_t pkv_evict_workspace_size(int32_t batch, int32_t max_seq_len, int32_t page_size);
+
 /* Static description of a status code. */
 const char *pkv_status_string(pkv_status status);
 

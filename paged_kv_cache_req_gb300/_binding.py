@@ -27,7 +27,10 @@ EXPORTED_SYMBOLS = ("pkv_build_indices", "pkv_store", "pkv_decode", "pkv_decode_
                     "pkv_status_string", "pkv_last_error", "pkv_abi_version", "pkv_set_wait_limit",
                     "pkv_wait_limit", "pkv_quant_tile_bytes", "pkv_quant_store", "pkv_quant_gather",
                     "pkv_quant_decode", "pkv_quant_decode_workspace_size", "pkv_quant_extend",
-                    "pkv_quant_extend_workspace_size")
+                    "pkv_quant_extend_workspace_size", "pkv_byte_tile_bytes", "pkv_byte_store", "pkv_byte_store_workspace_size",
+                    "pkv_byte_gather", "pkv_byte_decode", "pkv_byte_decode_workspace_size", "pkv_byte_extend",
+                    "pkv_byte_extend_workspace_size", "pkv_byte_weights", "pkv_byte_weights_workspace_size", "pkv_evict",
+                    "pkv_evict_workspace_size")
 
 
 class PkvError(RuntimeError):
@@ -100,6 +103,41 @@ class QuantArgs(ctypes.Structure):
     ]
 
 
+class ByteArgs(ctypes.Structure):
+    """Mirror of ``pkv_byte_args`` (field order and types must match include/pkv.h)."""
+    _fields_ = [
+        ("layout", ctypes.c_int32), ("batch", ctypes.c_int32), ("num_q_heads", ctypes.c_int32),
+        ("num_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+        ("sm_scale", ctypes.c_float), ("max_seq_len", ctypes.c_int32), ("kv_chunk", ctypes.c_int32),
+        ("block_table_width", ctypes.c_int32), ("max_q_len", ctypes.c_int32), ("total_q", ctypes.c_int64),
+        ("total_kv", ctypes.c_int64),
+        ("num_tiles", ctypes.c_int64), ("tile_stride", ctypes.c_int64), ("q_row_stride", ctypes.c_int64),
+        ("kv_indices_len", ctypes.c_int64),
+        ("q", ctypes.c_void_p), ("pool", ctypes.c_void_p),
+        ("qo_indptr", ctypes.c_void_p), ("kv_end", ctypes.c_void_p),
+        ("kv_indptr", ctypes.c_void_p), ("kv_indices", ctypes.c_void_p), ("kv_last_page_len", ctypes.c_void_p),
+        ("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+        ("req_to_token", ctypes.c_void_p), ("r2t_rows", ctypes.c_int64), ("r2t_row_stride", ctypes.c_int64),
+        ("r2t_width", ctypes.c_int64), ("req_pool_idx", ctypes.c_void_p), ("kv_start", ctypes.c_void_p),
+        ("out", ctypes.c_void_p), ("lse", ctypes.c_void_p), ("acc_in", ctypes.c_void_p), ("acc_out", ctypes.c_void_p),
+        ("acc_row_stride", ctypes.c_int64),
+    ]
+
+
+class EvictArgs(ctypes.Structure):
+    """Mirror of ``pkv_evict_args`` (field order and types must match include/pkv.h)."""
+    _fields_ = [
+        ("batch", ctypes.c_int32), ("page_size", ctypes.c_int32), ("max_seq_len", ctypes.c_int32),
+        ("num_pool_pages", ctypes.c_int64), ("req_to_token", ctypes.c_void_p), ("req_to_token_out", ctypes.c_void_p),
+        ("r2t_rows", ctypes.c_int64), ("r2t_row_stride", ctypes.c_int64), ("r2t_width", ctypes.c_int64),
+        ("acc", ctypes.c_void_p), ("acc_out", ctypes.c_void_p), ("acc_row_stride", ctypes.c_int64),
+        ("req_pool_idx", ctypes.c_void_p), ("kv_start", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p),
+        ("seq_lens_out", ctypes.c_void_p), ("budget", ctypes.c_void_p), ("keep_first", ctypes.c_void_p),
+        ("keep_last", ctypes.c_void_p), ("free_pages", ctypes.c_void_p), ("free_pages_len", ctypes.c_int64),
+        ("free_state", ctypes.c_void_p), ("free_state_out", ctypes.c_void_p),
+    ]
+
+
 def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
     if not os.path.exists(path):
         raise ImportError("libpkv.so is not built (%s); run `python -m paged_kv_cache_req_gb300.build`" % path)
@@ -131,6 +169,22 @@ def load_library(path: str = _LIB_PATH) -> ctypes.CDLL:
         fn.argtypes = [ctypes.POINTER(QuantArgs)]
     for fn in (lib.pkv_quant_tile_bytes, lib.pkv_quant_decode_workspace_size, lib.pkv_quant_extend_workspace_size):
         fn.restype = SZ
+    lib.pkv_byte_tile_bytes.argtypes = [I32, I32, I32]
+    lib.pkv_byte_store.argtypes = [P, I64, I64, I32, I32, I32, P, P, I64, I64, P, I32, P, SZ, P, P]
+    lib.pkv_byte_store_workspace_size.argtypes = [I64, I32]
+    lib.pkv_byte_gather.argtypes = [P, I64, I64, I32, I32, I32, P, I64, I64, I64, P, P, P, I32, I32, P, P, I64, P, P, P]
+    lib.pkv_evict.argtypes = [ctypes.POINTER(EvictArgs), P, SZ, P, P]
+    lib.pkv_evict_workspace_size.argtypes = [I32, I32, I32]
+    for fn in (lib.pkv_byte_decode, lib.pkv_byte_extend, lib.pkv_byte_weights):
+        fn.argtypes = [ctypes.POINTER(ByteArgs), P, SZ, P, P]
+    for fn in (lib.pkv_byte_decode_workspace_size, lib.pkv_byte_extend_workspace_size, lib.pkv_byte_weights_workspace_size):
+        fn.argtypes = [ctypes.POINTER(ByteArgs)]
+    for fn in (lib.pkv_byte_tile_bytes, lib.pkv_byte_store_workspace_size, lib.pkv_byte_decode_workspace_size,
+               lib.pkv_byte_extend_workspace_size, lib.pkv_byte_weights_workspace_size, lib.pkv_evict_workspace_size):
+        fn.restype = SZ
+    for fn in (lib.pkv_byte_store, lib.pkv_byte_gather, lib.pkv_byte_decode, lib.pkv_byte_extend, lib.pkv_byte_weights,
+               lib.pkv_evict):
+        fn.restype = ctypes.c_int
     for fn in (lib.pkv_quant_store, lib.pkv_quant_gather, lib.pkv_quant_decode, lib.pkv_quant_extend):
         fn.restype = ctypes.c_int
     for fn in (lib.pkv_alloc_extend, lib.pkv_write_req_to_token, lib.pkv_encoder_merge, lib.pkv_extend,
@@ -527,6 +581,199 @@ def pkv_quant_decode(args: QuantArgs, workspace: torch.Tensor, err_flags, stream
 
 def pkv_quant_extend(args: QuantArgs, workspace: torch.Tensor, err_flags, stream=None):
     _quant_attend(_lib.pkv_quant_extend, "pkv_quant_extend", args, workspace, err_flags, stream)
+
+
+_TILE8_BYTES = {}   # (page size, head_dim, kv heads) -> bytes of a tile
+
+
+def _byte_pool(pool, page_size, head_dim, hkv):
+    """Checks an 8-bit pool [tiles, tile bytes] against the page size, head_dim and kv heads;
+    returns its device index, address, tiles and tile stride."""
+    nbytes = _TILE8_BYTES.get((page_size, head_dim, hkv))
+    if nbytes is None:
+        nbytes = _lib.pkv_byte_tile_bytes(page_size, head_dim, hkv)
+        if nbytes == 0:
+            raise PkvError(PKV_ERR_UNSUPPORTED, "8-bit pool",
+                           "page_size a power of two in [1, 1024], head_dim 64 or 128")
+        _TILE8_BYTES[page_size, head_dim, hkv] = nbytes
+    shape, stride = pool.shape, pool.stride()
+    if len(shape) != 2 or pool.dtype is not _U8 or shape[1] != nbytes or stride[1] != 1:
+        raise ValueError("the 8-bit pool must be uint8 [tiles, %d] with contiguous tiles" % nbytes)
+    dev = pool.get_device()
+    if dev < 0:
+        raise ValueError("libpkv takes device tensors only (got a %s tensor)" % pool.device)
+    if dev != _device():
+        raise ValueError("the pool is on %s, which is not the current device" % pool.device)
+    # a pool of one tile may carry any stride
+    return dev, pool.data_ptr(), shape[0], stride[0] if shape[0] > 1 else nbytes
+
+
+def _workspace(workspace, who: str, dev: int):
+    if workspace.get_device() != dev:
+        raise ValueError("%s: the workspace must be on cuda:%d" % (who, dev))
+    if not workspace.is_contiguous():
+        raise ValueError("%s: the workspace must be contiguous" % who)
+    return workspace.data_ptr(), workspace.nbytes
+
+
+def pkv_byte_tile_bytes(page_size: int, head_dim: int, kv_heads: int) -> int:
+    """Bytes of a tile of min(page_size, 64) slots of an 8-bit pool."""
+    return int(_lib.pkv_byte_tile_bytes(int(page_size), int(head_dim), int(kv_heads)))
+
+
+def pkv_byte_store_workspace_size(num_tiles: int, page_size: int) -> int:
+    return int(_lib.pkv_byte_store_workspace_size(int(num_tiles), int(page_size)))
+
+
+def pkv_byte_store(pool, k_new, v_new, slot_mapping, workspace, err_flags, *, page_size, stream=None):
+    """pool uint8 [tiles, tile bytes]; k_new, v_new bf16 [n, Hkv, D], tokens any stride apart."""
+    shape = k_new.shape
+    n, hkv, d = shape
+    dev, pool_ptr, tiles, ts = _byte_pool(pool, page_size, d, hkv)
+    ks, vs = k_new.stride(), v_new.stride()
+    if k_new.dtype is not _BF16 or v_new.dtype is not _BF16 or v_new.shape != shape or ks[2] != 1 or vs[2] != 1 or \
+            (hkv > 1 and (ks[1] != d or vs[1] != d)) or k_new.get_device() != dev or v_new.get_device() != dev:
+        raise ValueError("k_new and v_new must be bf16 [n, Hkv, D] on the pool's device, a token's rows contiguous")
+    row = hkv * d
+    ws, ws_bytes = _workspace(workspace, "pkv_byte_store", dev)
+    st = _lib.pkv_byte_store(
+        pool_ptr, tiles, ts, hkv, d, page_size, k_new.data_ptr(), v_new.data_ptr(), ks[0] if n > 1 else row,
+        vs[0] if n > 1 else row, _ptr(slot_mapping, "slot_mapping", _I32T, (n,), dev), n, ws, ws_bytes,
+        _ptr(err_flags, "err_flags", _I32T, None, dev), _quant_stream(stream, dev))
+    if st != PKV_OK:
+        _check(st, "pkv_byte_store")
+
+
+def pkv_byte_gather(pool, req_to_token, req_pool_idx, seq_lens, max_seq_len, k_out, v_out, cu_seqlens, err_flags, *,
+                  page_size, kv_start=None, stream=None):
+    """k_out, v_out bf16 [rows, Hkv, D] receive the requests' rows in order (see pkv_ragged_gather)."""
+    shape = k_out.shape
+    rows, hkv, d = shape
+    dev, pool_ptr, tiles, ts = _byte_pool(pool, page_size, d, hkv)
+    batch = seq_lens.shape
+    r2t_rows, r2t_width = req_to_token.shape
+    st = _lib.pkv_byte_gather(
+        pool_ptr, tiles, ts, hkv, d, page_size, _ptr(req_to_token, "req_to_token", _I32T, None, dev), r2t_rows,
+        r2t_width, r2t_width, _ptr(req_pool_idx, "req_pool_idx", _I32T, batch, dev),
+        _ptr(kv_start, "kv_start", _I32T, batch, dev), _ptr(seq_lens, "seq_lens", _I32T, batch, dev), batch[0],
+        int(max_seq_len), _ptr(k_out, "k_out", _BF16, None, dev), _ptr(v_out, "v_out", _BF16, shape, dev), rows,
+        _ptr(cu_seqlens, "cu_seqlens", _I32T, (batch[0] + 1,), dev), _ptr(err_flags, "err_flags", _I32T, None, dev),
+        _quant_stream(stream, dev))
+    if st != PKV_OK:
+        _check(st, "pkv_byte_gather")
+
+
+def make_byte_args(layout, q, pool, out, *, page_size, num_kv_heads, sm_scale, max_seq_len, lse=None, qo_indptr=None,
+                 kv_end=None, kv_indptr=None, kv_indices=None, kv_last_page_len=None, block_table=None, seq_lens=None,
+                 req_to_token=None, req_pool_idx=None, kv_start=None, acc_in=None, acc_out=None, total_kv=0, max_q_len=0,
+                 kv_chunk=0) -> ByteArgs:
+    """Arguments of pkv_byte_decode (no qo_indptr), pkv_byte_extend or pkv_byte_weights: q bf16 [rows, Hq, D], rows
+    any stride apart; pool uint8 [tiles, tile bytes]; out bf16 [rows, Hq, D] (None for pkv_byte_weights);
+    acc_in, acc_out fp32 of req_to_token's shape."""
+    T, hq, d = q.shape
+    hkv = int(num_kv_heads)
+    dev, _, _, ts = _byte_pool(pool, page_size, d, hkv)
+    if q.dtype is not _BF16 or q.stride(2) != 1 or (hq > 1 and q.stride(1) != d) or q.get_device() != dev:
+        raise ValueError("q must be bf16 [rows, Hq, D] on the pool's device, a row's heads contiguous")
+    B = T if qo_indptr is None else qo_indptr.numel() - 1
+    table = None if req_to_token is None else req_to_token.shape
+    if table is None and (acc_in is not None or acc_out is not None):
+        raise ValueError("acc_in and acc_out need req_to_token, whose columns they have")
+    for name, t, dtype, shape in (
+            ("out", out, _BF16, (T, hq, d)), ("lse", lse, _F32, (T, hq)), ("qo_indptr", qo_indptr, _I32T, (B + 1,)),
+            ("kv_end", kv_end, _I32T, (T,)), ("kv_indptr", kv_indptr, _I32T, (B + 1,)),
+            ("kv_last_page_len", kv_last_page_len, _I32T, (B,)), ("seq_lens", seq_lens, _I32T, (B,)),
+            ("req_pool_idx", req_pool_idx, _I32T, (B,)), ("kv_start", kv_start, _I32T, (B,)),
+            ("kv_indices", kv_indices, _I32T, None), ("req_to_token", req_to_token, _I32T, None),
+            ("acc_in", acc_in, _F32, table), ("acc_out", acc_out, _F32, table),
+            ("block_table", block_table, _I32T, None if block_table is None else (B, block_table.shape[1]))):
+        _ptr(t, name, dtype, shape, dev)
+    a = ByteArgs()
+    a.layout, a.batch = layout, B
+    a.num_q_heads, a.num_kv_heads, a.head_dim = hq, hkv, d
+    a.page_size, a.sm_scale, a.max_seq_len, a.kv_chunk = int(page_size), float(sm_scale), int(max_seq_len), int(kv_chunk)
+    a.block_table_width = block_table.shape[1] if block_table is not None else 0
+    a.total_q, a.total_kv, a.max_q_len = T, int(total_kv), int(max_q_len)
+    a.num_tiles, a.tile_stride = pool.shape[0], ts
+    a.q_row_stride = q.stride(0) if T > 1 else hq * d
+    a.kv_indices_len = kv_indices.numel() if kv_indices is not None else 0
+    if table is not None:
+        a.r2t_rows, a.r2t_width = table
+        a.r2t_row_stride = a.acc_row_stride = req_to_token.stride(0)
+    tensors = (("q", q), ("pool", pool), ("qo_indptr", qo_indptr), ("kv_end", kv_end), ("kv_indptr", kv_indptr),
+               ("kv_indices", kv_indices), ("kv_last_page_len", kv_last_page_len), ("block_table", block_table),
+               ("seq_lens", seq_lens), ("req_to_token", req_to_token), ("req_pool_idx", req_pool_idx),
+               ("kv_start", kv_start), ("out", out), ("lse", lse), ("acc_in", acc_in), ("acc_out", acc_out))
+    for name, t in tensors:
+        setattr(a, name, None if t is None else _p(t).value)
+    # the struct holds raw pointers: keep the tensors alive as long as it lives
+    a._keep = tuple(t for _, t in tensors if t is not None)
+    a._dev = dev
+    return a
+
+
+def pkv_byte_decode_workspace_size(args: ByteArgs) -> int:
+    return int(_lib.pkv_byte_decode_workspace_size(ctypes.byref(args)))
+
+
+def pkv_byte_extend_workspace_size(args: ByteArgs) -> int:
+    return int(_lib.pkv_byte_extend_workspace_size(ctypes.byref(args)))
+
+
+def pkv_byte_weights_workspace_size(args: ByteArgs) -> int:
+    return int(_lib.pkv_byte_weights_workspace_size(ctypes.byref(args)))
+
+
+def pkv_byte_decode(args: ByteArgs, workspace: torch.Tensor, err_flags, stream=None):
+    _quant_attend(_lib.pkv_byte_decode, "pkv_byte_decode", args, workspace, err_flags, stream)
+
+
+def pkv_byte_extend(args: ByteArgs, workspace: torch.Tensor, err_flags, stream=None):
+    _quant_attend(_lib.pkv_byte_extend, "pkv_byte_extend", args, workspace, err_flags, stream)
+
+
+def pkv_byte_weights(args: ByteArgs, workspace: torch.Tensor, err_flags, stream=None):
+    _quant_attend(_lib.pkv_byte_weights, "pkv_byte_weights", args, workspace, err_flags, stream)
+
+
+def pkv_evict_workspace_size(batch: int, max_seq_len: int, page_size: int) -> int:
+    return int(_lib.pkv_evict_workspace_size(int(batch), int(max_seq_len), int(page_size)))
+
+
+def pkv_evict(req_to_token, req_pool_idx, seq_lens, acc, budget, free_pages, free_state, workspace, err_flags, *,
+              page_size, num_pool_pages, max_seq_len, kv_start=None, keep_first=None, keep_last=None,
+              req_to_token_out=None, acc_out=None, seq_lens_out=None, free_state_out=None, stream=None):
+    """acc fp32 of req_to_token's shape; budget, keep_first, keep_last int32 [B]; free_state int32 [2] = {head, count}.
+    Outputs that are not given are the inputs."""
+    dev = req_to_token.get_device()
+    if dev < 0:
+        raise ValueError("libpkv takes device tensors only (got a %s tensor)" % req_to_token.device)
+    if dev != _device():
+        raise ValueError("pkv_evict: req_to_token is on %s, which is not the current device" % req_to_token.device)
+    table, batch = req_to_token.shape, seq_lens.shape
+    if len(table) != 2 or len(batch) != 1:
+        raise ValueError("pkv_evict: req_to_token must be [rows, width], seq_lens [B]")
+    a = EvictArgs()
+    a.batch, a.page_size, a.max_seq_len, a.num_pool_pages = batch[0], int(page_size), int(max_seq_len), int(num_pool_pages)
+    a.r2t_rows, a.r2t_width = table
+    a.r2t_row_stride = a.acc_row_stride = table[1]
+    a.free_pages_len = free_pages.numel()
+    for name, t, dtype, shape in (
+            ("req_to_token", req_to_token, _I32T, table),
+            ("req_to_token_out", req_to_token if req_to_token_out is None else req_to_token_out, _I32T, table),
+            ("acc", acc, _F32, table), ("acc_out", acc if acc_out is None else acc_out, _F32, table),
+            ("req_pool_idx", req_pool_idx, _I32T, batch), ("kv_start", kv_start, _I32T, batch),
+            ("seq_lens", seq_lens, _I32T, batch),
+            ("seq_lens_out", seq_lens if seq_lens_out is None else seq_lens_out, _I32T, batch),
+            ("budget", budget, _I32T, batch), ("keep_first", keep_first, _I32T, batch),
+            ("keep_last", keep_last, _I32T, batch), ("free_pages", free_pages, _I32T, None),
+            ("free_state", free_state, _I32T, (2,)),
+            ("free_state_out", free_state if free_state_out is None else free_state_out, _I32T, (2,))):
+        setattr(a, name, _ptr(t, name, dtype, shape, dev) or None)
+    ws, ws_bytes = _workspace(workspace, "pkv_evict", dev)
+    st = _lib.pkv_evict(ctypes.byref(a), ws, ws_bytes, _ptr(err_flags, "err_flags", _I32T, None, dev), _quant_stream(stream, dev))
+    if st != PKV_OK:
+        _check(st, "pkv_evict")
 
 
 def pkv_status_string(status: int) -> str:

@@ -1,0 +1,640 @@
+// pkv_byte_decode / pkv_byte_extend / pkv_byte_weights: attention over an 8-bit K/V pool.
+//
+// Work is cut and handed out as for the 4-bit pool (spans.cuh: spans of tiles, one per warp; a block
+// per unit for small calls; held keys for requests with many rows).
+//
+// Math per 32 keys, in a warp's registers: S^T = K q^T and O^T += V^T P^T, all m16n8k16 with
+// fp16 operands and fp32 sums, keys as MMA rows.  An e4m3 code is exact in fp16; q (bf16) is
+// taken into fp16 after a power of two per row.  K's scale multiplies the scores.  V's cannot
+// wait for the end, as it differs from tile to tile: a weight takes 2^(E - M) before it is rounded
+// to fp16, M being the largest E of the warp's tiles so far (`unit`), and the sums are in units of
+// 2^M; where M grows they are multiplied by 2^(M_old - M).  So nothing is past fp16 (weights
+// are at most 2^15), and a weight is 2^-11 relative down to 2^(M - E - 25) of the row's largest.
+//
+// Lane (r, c) = (lane / 4, lane % 4) holds dims D/4 c ... of key row r for K, and dims D/8 r
+// ... of keys of column c for V, as the 4-bit kernel's do; codes of two keys are interleaved before
+// V's conversion, so that one gives the pair of keys that the MMA wants.
+#include "byte.cuh"
+#include "spans.cuh"
+
+namespace pkv {
+namespace qattn {
+namespace {
+
+template <int D, int NT>
+struct State8 : qattn::State<D, NT> {
+    float unit;   // M - 127: the sums are in units of 2^unit (kNoUnit: no key yet)
+};
+
+// 2^d of an integer d <= 0 (0 below the normal numbers).
+__device__ __forceinline__ float down_by(float d) { return __int_as_float(max(0, static_cast<int>(d) + 127) << 23); }
+
+template <int D, int kT_>
+struct Quant8 {
+    static constexpr int kDim = D, kT = kT_;
+    static constexpr bool kUnits = true, kHeldBf16V = true;
+    static constexpr const char *kExtend = "pkv_byte_extend";
+    // A stage: the codes of a 64-slot tile, or of four 16-slot ones (kT = 16), as they lie; kT = 0 (other
+    // tiles): K codes [64][D], V codes [64][D].  Behind them the scales: 16 bytes of a piece with
+    // its own two among them, 4 where kT is 0.
+    static constexpr int kCodes = 128 * D;
+    static constexpr uint32_t kStageBytes = kCodes + 256;
+    static constexpr int warps(int) { return D == 128 ? 6 : 12; }
+    static constexpr int stages(int) { return 2; }
+    template <int NT>
+    using State = State8<D, NT>;
+
+    // (copied 16 bytes per lane)
+    __device__ __forceinline__ static bool gathers(int) { return kT == 0; }
+    __device__ __forceinline__ static const uint8_t *piece(const Params &p, int slot, int kh) {
+        return p.pool + static_cast<int64_t>(slot >> p.t_shift) * p.tile_stride + (static_cast<int64_t>(kh) * 2 * D << p.t_shift);
+    }
+    // The scale bytes of the tile whose piece of kv head kh is at `a`, in whole units of kUnit bytes.
+    template <int kUnit>
+    __device__ __forceinline__ static const uint8_t *scales(const Params &p, const uint8_t *a, int kh) {
+        return a + (static_cast<int64_t>(p.hkv - kh) * 2 * D << p.t_shift) + (2 * kh & ~(kUnit - 1));
+    }
+    __device__ __forceinline__ static void zero_piece(uint8_t *stage, int j, int ps) {
+        const int t = 1 << ps;
+        if (kT != 0) {
+            uint32_t *w = reinterpret_cast<uint32_t *>(stage + j * 2 * kT * D);
+            for (int o = 0; o < kT * D / 2; ++o) w[o] = 0;
+            for (int o = 0; o < 4; ++o) reinterpret_cast<uint32_t *>(stage + kCodes + j * 16)[o] = 0x01010101u;
+            return;
+        }
+        for (int part = 0; part < 2; ++part) {
+            uint32_t *w = reinterpret_cast<uint32_t *>(stage + part * 64 * D + j * t * D);
+            for (int o = 0; o < t * D / 4; ++o) w[o] = 0;
+        }
+        reinterpret_cast<uint32_t *>(stage + kCodes)[j] = 0x01010101u;
+    }
+    // Copies a tile's n pieces, `live` of them on good pages; piece i of the window is lane i % 32's src[i / 32].
+    __device__ __forceinline__ static void copy(const Params &p, int kh, const uint8_t *const (&src)[2], int first, int n,
+                                                uint32_t live, int ps, uint8_t *stage, uint64_t *bar, int lane) {
+        if (kT != 0) {
+            constexpr uint32_t bytes = 2 * kT * D;
+            if (lane == (first & 31)) mbar_arrive_expect_tx(bar, live * (bytes + 16));
+            if (kT != 64) __syncwarp();   // (with one piece the same lane copies)
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int j = 32 * i + lane - first;
+                if (j >= 0 && j < n && src[i]) {
+                    bulk_load(stage + j * bytes, src[i], bytes, bar);
+                    bulk_load(stage + kCodes + j * 16, scales<16>(p, src[i], kh), 16, bar);
+                }
+            }
+            return;
+        }
+        constexpr int kRow = D / 16, kRounds = 64 * kRow / 32;   // 16 bytes per lane; rounds for K (and V)
+        const uint8_t *low = first < 32 ? src[0] : src[1];       // (only 64 pieces lie in both)
+        const int at = first & 31, c = lane % kRow;
+#pragma unroll 8
+        for (int i = 0; i < kRounds; ++i) {
+            const int row = i * (32 / kRow) + lane / kRow, j = row >> ps;
+            const uint8_t *a = from_lane(ps == 0 && i >= kRounds / 2 ? src[1] : low, (at + j) & 31);
+            if (!a) continue;
+            a += (row & ((1 << ps) - 1)) * D + c * 16;
+            cp_async_16(stage + row * D + c * 16, a, 16);
+            cp_async_16(stage + 64 * D + row * D + c * 16, a + (D << ps), 16);
+        }
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int j = 32 * i + lane - first;
+            if (j >= 0 && j < (64 >> ps) && src[i]) cp_async_small<4>(stage + kCodes + j * 4, scales<4>(p, src[i], kh));
+        }
+        arrive_with_copies(bar);
+    }
+
+    // Where key k of the 16-key group kt of half `step` lies: its codes (part 0 = K, 1 = V) and its two scale bytes.
+    __device__ __forceinline__ static const uint8_t *codes(const uint8_t *stage, int step, int part, int kt, int k) {
+        if (kT == 16) return stage + (step * kGroups + kt) * (32 * D) + part * (16 * D) + k * D;
+        return stage + part * (64 * D) + (step * kStep + kt * 16 + k) * D;
+    }
+    __device__ __forceinline__ static uint32_t scale_bytes(const Params &p, const uint8_t *stage, int step, int kt, int k, int kh) {
+        const int at = kT == 64 ? (2 * kh & 15) : kT == 16 ? (step * kGroups + kt) * 16 + (2 * kh & 15)
+                                : ((step * kStep + kt * 16 + k) >> p.t_shift) * 4 + (2 * kh & 3);
+        return *reinterpret_cast<const uint16_t *>(stage + kCodes + at);
+    }
+
+    // One step: 32 keys, the unit's key0 ..., in half `step` of a stage.  With kMask some row's
+    // bound or the unit's last key lies among them.
+    template <int NT, bool kMask>
+    __device__ __forceinline__ static void step(const Params &p, State<NT> &st, const uint8_t *stage, int step, int key0, int keys,
+                                                int kh, int lane) {
+        const int r = lane >> 2, c = lane & 3;
+        constexpr int KS = D / 16;     // contraction steps of q.k, and 16-row blocks of O^T
+        float s[kGroups][NT][4];
+        uint32_t w[kGroups][2][D / 16];
+        float ks[kGroups][2], ve[kGroups][2];   // K's scale and log2 of V's, of keys kt * 16 + r + 8 u
+#pragma unroll
+        for (int kt = 0; kt < kGroups; ++kt)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const uint4 *cp = reinterpret_cast<const uint4 *>(codes(stage, step, 0, kt, r + 8 * u) + c * (D / 4));
+#pragma unroll
+                for (int i = 0; i < D / 64; ++i) {
+                    const uint4 x = cp[i];
+                    w[kt][u][4 * i] = x.x; w[kt][u][4 * i + 1] = x.y; w[kt][u][4 * i + 2] = x.z; w[kt][u][4 * i + 3] = x.w;
+                }
+                const uint32_t e = scale_bytes(p, stage, step, kt, r + 8 * u, kh);
+                ks[kt][u] = byte::scale_value(e & 0xff);
+                ve[kt][u] = static_cast<float>(e >> 8) - 127.f;
+                // (pieces past the last key were not copied)
+                if (kMask && kT != 64 && key0 + kt * 16 + (kT == 16 ? 0 : r + 8 * u) >= keys) ve[kt][u] = kNoUnit;
+#pragma unroll
+                for (int n = 0; n < NT; ++n) s[kt][n][2 * u] = s[kt][n][2 * u + 1] = 0.f;
+            }
+#pragma unroll
+        for (int i = 0; i < KS; ++i)
+#pragma unroll
+            for (int kt = 0; kt < kGroups; ++kt) {
+                const uint32_t a0 = byte::lo_to_f16(w[kt][0][i]), a1 = byte::lo_to_f16(w[kt][1][i]);
+                const uint32_t a2 = byte::hi_to_f16(w[kt][0][i]), a3 = byte::hi_to_f16(w[kt][1][i]);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) mma_f16(s[kt][n], a0, a1, a2, a3, st.q[i][n][0], st.q[i][n][1]);
+            }
+        {   // the unit of the sums
+            float most = ve[0][0];
+            if (kT != 64) {
+                most = fmaxf(fmaxf(ve[0][0], ve[0][1]), fmaxf(ve[1][0], ve[1][1]));
+                if (kT == 0) most = static_cast<float>(__reduce_max_sync(0xffffffffu, static_cast<int>(most)));
+            }
+            if (most > st.unit) {
+                const float corr = down_by(st.unit - most);
+                st.unit = most;
+#pragma unroll
+                for (int t = 0; t < KS; ++t)
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) st.o[t][n][i] *= corr;
+            }
+#pragma unroll
+            for (int kt = 0; kt < kGroups; ++kt)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) ve[kt][u] = down_by(ve[kt][u] - st.unit);
+        }
+        // softmax: s[kt][n][2 u + w] is key kt * 16 + r + 8 u of row 8 n + 2 c + w, from here on a base-2 logit
+        uint32_t pt[kGroups][NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+            float top[2];   // of this lane's keys
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+#pragma unroll
+                for (int kt = 0; kt < kGroups; ++kt)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        float &x = s[kt][n][2 * u + v];
+                        // (the factor stays normal and finite, so that 0 stays 0)
+                        x *= fminf(fmaxf(st.f[n][v] * ks[kt][u], 1.2e-38f), 3.4e38f);
+                        if (kMask && key0 + kt * 16 + r + 8 * u >= st.end[n][v]) x = -INFINITY;
+                    }
+                top[v] = fmaxf(fmax3(s[0][n][v], s[0][n][2 + v], s[1][n][v]), s[1][n][2 + v]);
+            }
+            // the maximum is looked for across lanes only when some logit passes it by kLazy
+            if (__any_sync(0xffffffffu, top[0] + st.nm[n][0] > st.limit[n][0] || top[1] + st.nm[n][1] > st.limit[n][1])) {
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+#pragma unroll
+                    for (int o = 4; o < 32; o <<= 1) top[v] = fmaxf(top[v], __shfl_xor_sync(0xffffffffu, top[v], o));
+                    if (top[v] + st.nm[n][v] > st.limit[n][v]) {
+                        const bool fresh = st.limit[n][v] == -INFINITY;
+                        const float nm = kLift - top[v];
+                        const float corr = fresh ? 0.f : ex2(nm - st.nm[n][v]);
+                        st.nm[n][v] = nm;
+                        st.limit[n][v] = kLift + kLazy;
+                        st.l[n][v] *= corr;
+#pragma unroll
+                        for (int t = 0; t < KS; ++t) {
+                            st.o[t][n][v] *= corr;
+                            st.o[t][n][2 + v] *= corr;
+                        }
+                    }
+                }
+            }
+            const uint64_t nm2 = pair(st.nm[n][0], st.nm[n][1]);
+            uint64_t sum = pair(st.l[n][0], st.l[n][1]);
+#pragma unroll
+            for (int kt = 0; kt < kGroups; ++kt)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const float2 y = unpair(add2(pair(s[kt][n][2 * u], s[kt][n][2 * u + 1]), nm2));
+                    const float x0 = ex2(y.x), x1 = ex2(y.y);
+                    sum = add2(sum, pair(x0, x1));
+                    pt[kt][n][u] = transpose_8x8(pack_f16x2(x0 * ve[kt][u], x1 * ve[kt][u]));
+                }
+            const float2 l = unpair(sum);
+            st.l[n][0] = l.x;
+            st.l[n][1] = l.y;
+        }
+#pragma unroll
+        for (int kt = 0; kt < kGroups; ++kt) {
+            uint32_t a[2][2][KS];      // [keys 2c.. / 2c + 8..][even / odd dim][16-row block]
+            bool bad = false;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                uint32_t x[2][D / 32];   // codes of the two keys, D/8 dims each
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int k = 2 * c + e + 8 * u;
+                    const uint8_t *cp = codes(stage, step, 1, kt, k) + r * (D / 8);
+                    if (D == 128) {
+                        const uint4 y = *reinterpret_cast<const uint4 *>(cp);
+                        x[e][0] = y.x; x[e][1] = y.y; x[e][D / 32 - 2] = y.z; x[e][D / 32 - 1] = y.w;
+                    } else {
+                        const uint2 y = *reinterpret_cast<const uint2 *>(cp);
+                        x[e][0] = y.x; x[e][1] = y.y;
+                    }
+                    if (kMask) {
+                        // nothing of a key past the unit's last, and no NaN that only some rows may see
+                        const bool in = key0 + kt * 16 + k < keys;
+#pragma unroll
+                        for (int i = 0; i < D / 32; ++i) {
+                            const uint32_t nan = byte::nan_bytes(x[e][i]);
+                            bad |= in && nan;
+                            x[e][i] = in ? x[e][i] & ~nan : 0;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) {
+                    const uint32_t lo = __byte_perm(x[0][i], x[1][i], 0x5140), hi = __byte_perm(x[0][i], x[1][i], 0x7362);
+                    a[u][0][2 * i] = byte::lo_to_f16(lo);
+                    a[u][1][2 * i] = byte::hi_to_f16(lo);
+                    a[u][0][2 * i + 1] = byte::lo_to_f16(hi);
+                    a[u][1][2 * i + 1] = byte::hi_to_f16(hi);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < KS; ++t)
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+                    mma_f16(st.o[t][n], a[0][0][t], a[0][1][t], a[1][0][t], a[1][1][t], pt[kt][n][0], pt[kt][n][1]);
+            if (kMask && __any_sync(0xffffffffu, bad)) {
+                // the rows that see a key with a NaN in V get it in that dim
+                for (int k = 0; k < 16; ++k) {
+                    const int key = key0 + kt * 16 + k;
+                    if (key >= keys) continue;
+                    const uint8_t *cp = codes(stage, step, 1, kt, k) + r * (D / 8);
+#pragma unroll
+                    for (int t = 0; t < KS; ++t)
+#pragma unroll
+                        for (int odd = 0; odd < 2; ++odd) {
+                            if ((cp[2 * t + odd] & 0x7f) != 0x7f) continue;
+#pragma unroll
+                            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                                for (int v = 0; v < 2; ++v)
+                                    if (key < st.end[n][v]) st.o[t][n][2 * odd + v] = __int_as_float(0x7fffffff);
+                        }
+                }
+            }
+        }
+    }
+
+    template <int NT>
+    __device__ __forceinline__ static void start(const Params &p, const Work &w, State<NT> &st, const uint32_t (&ahead)[D / 8], int lane) {
+        start_segment<D, NT>(p, w, st, ahead, lane);
+        st.unit = kNoUnit;
+    }
+
+    // The segment's rows: normalised to the output when it is the whole unit, else a partial
+    // (see Work::slot).
+    template <int NT>
+    __device__ __forceinline__ static void finish(const Params &p, const Work &s, State<NT> &st, int lane) {
+        const int r = lane >> 2, c = lane & 3;
+        constexpr int W = D / 8;   // dims of a lane: D/8 r ...
+        const int64_t slot = s.slot;
+        const float one = power_of_two(st.unit);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int v = 0; v < 2; ++v) {
+                float l = st.l[n][v];
+#pragma unroll
+                for (int o = 4; o < 32; o <<= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+                const int lr = n * 8 + 2 * c + v, row = s.rb * 8 * NT + lr, tok = token_of(p, row), hh = row - tok * p.g;
+                if (tok >= s.n) continue;
+                if (slot < 0) {
+                    const int64_t at = static_cast<int64_t>(s.qo0 + tok) * p.hq + s.kh * p.g + hh;
+                    const float inv = l == 0.f ? 0.f : rcp(l);   // (one / l may be outside fp32's normal numbers)
+                    uint32_t h[W / 2];
+#pragma unroll
+                    for (int t = 0; t < D / 16; ++t) h[t] = pack_bf16x2(st.o[t][n][v] * inv * one, st.o[t][n][2 + v] * inv * one);
+                    uint4 *dst = reinterpret_cast<uint4 *>(p.out + at * D + r * W);
+#pragma unroll
+                    for (int i = 0; i < W / 8; ++i) dst[i] = make_uint4(h[4 * i], h[4 * i + 1], h[4 * i + 2], h[4 * i + 3]);
+                    if (r == 0 && p.lse) p.lse[at] = l == 0.f ? -INFINITY : (log2f(l) - st.nm[n][v]) * kLn2;
+                } else {
+                    float4 *dst = reinterpret_cast<float4 *>(p.part_o + (slot * 8 * NT + lr) * D + r * W);
+#pragma unroll
+                    for (int i = 0; i < W / 4; ++i)
+                        dst[i] = make_float4(st.o[2 * i][n][v], st.o[2 * i][n][2 + v], st.o[2 * i + 1][n][v], st.o[2 * i + 1][n][2 + v]);
+                    if (r == 0) {
+                        reinterpret_cast<float2 *>(p.part_ml)[slot * 8 * NT + lr] = make_float2(l == 0.f ? -INFINITY : -st.nm[n][v], l);
+                        p.part_unit[slot * 8 * NT + lr] = st.unit;
+                    }
+                }
+            }
+    }
+
+    // Sixteen dims of a held row: both as bf16, which has the range for any scale.
+    struct Block {
+        uint4 codes;
+        uint32_t scale;
+    };
+    __device__ __forceinline__ static Block load_block(const Params &p, int64_t slot, int kh, bool is_v, int j) {
+        const int t = 1 << p.t_shift, at = static_cast<int>(slot & (t - 1));
+        const uint8_t *a = piece(p, static_cast<int>(slot), kh);
+        Block b;
+        b.codes = __ldg(reinterpret_cast<const uint4 *>(a + (is_v ? t * D : 0) + at * D + j * 16));
+        b.scale = __ldg(a + (static_cast<int64_t>(p.hkv - kh) * 2 * D << p.t_shift) + 2 * kh + is_v);
+        return b;
+    }
+    __device__ __forceinline__ static bool has_nan(const Block &b) {
+        return (byte::nan_bytes(b.codes.x) | byte::nan_bytes(b.codes.y) | byte::nan_bytes(b.codes.z) | byte::nan_bytes(b.codes.w)) != 0;
+    }
+    // `any`: V holds a NaN for the key
+    __device__ __forceinline__ static void hold(const Block &b, bool is_v, bool any, uint32_t (&x)[8]) {
+        const uint32_t w[4] = {b.codes.x, b.codes.y, b.codes.z, b.codes.w};
+        const float s = byte::scale_value(b.scale);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 f = quant::f16x2_to_f32(i % 2 ? byte::hi_to_f16(w[i / 2]) : byte::lo_to_f16(w[i / 2]));
+            x[i] = any ? (is_v ? 0u : 0x7fff7fffu) : pack_bf16x2(f.x * s, f.y * s);
+        }
+    }
+};
+
+// ---------------------------------------------------------------- weights
+// What keys receive: a block takes 512 keys of one request and kv head, its warps 64 each, over
+// all the request's rows, 64 at a time in shared memory as fp16.  With lse known a weight is one
+// exponential: w = 2^(logit - lse2).  Partial sums, one per kv head, are added up by add_kernel
+// in a fixed order.
+constexpr int kWeighWarps = 8, kWeighKeys = 64 * kWeighWarps, kWeighRows = 64;
+
+struct WeighParams {
+    const float *lse;
+    float *part;             // [Hkv][B][max_len]
+    const float *acc_in;
+    float *acc_out;
+    int64_t acc_stride;
+};
+
+template <int D>
+__global__ void __launch_bounds__(kWeighWarps * 32) weigh_kernel(const Params p, const WeighParams wp) {
+    __shared__ __align__(16) uint32_t q_s[kWeighRows * D / 2];   // fp16 pairs
+    __shared__ float f_s[kWeighRows], lse_s[kWeighRows];
+    __shared__ int end_s[kWeighRows];
+    pdl_wait();          // inputs may come from the previous kernel of the stream
+    pdl_launch_next();
+    const int b = blockIdx.z, kh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
+    const Req req = load_req(p, b, blockIdx.x == 0 && kh == 0 && threadIdx.x == 0);
+    const int k0 = blockIdx.x * kWeighKeys + warp * 64;
+    if (static_cast<int>(blockIdx.x) * kWeighKeys >= req.L) return;
+    const int rows = req.n * p.g;
+    constexpr int KS = D / 16;
+    float sum[2][2][2] = {};   // [half][16-key group][u] of keys k0 + 32 h + 16 kt + r + 8 u
+    for (int r0 = 0; r0 < rows; r0 += kWeighRows) {
+        __syncthreads();
+        // eight lanes per row
+        for (int row = threadIdx.x >> 3; row < kWeighRows; row += kWeighWarps * 4) {
+            const int rr = r0 + row, tok = token_of(p, rr), j = threadIdx.x & 7;
+            uint32_t w[D / 16];
+            uint32_t top = 0;
+            const bool live = rr < rows;
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                uint4 x = make_uint4(0, 0, 0, 0);
+                if (live) x = __ldg(reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(req.qo0 + tok) * p.q_stride +
+                                                                    (kh * p.g + rr - tok * p.g) * D + j * (D / 8)) + i);
+                w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
+            }
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
+            top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+            for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+            int e = min(126, 6 + 127 - static_cast<int>(top >> 7));   // (see start_segment)
+            if (top == 0 || top >= 0x7f80u) e = 0;
+            const float up = __int_as_float((e + 127) << 23), down = __int_as_float((127 - e) << 23);
+#pragma unroll
+            for (int i = 0; i < D / 16; ++i) q_s[row * (D / 2) + j * (D / 16) + i] = pack_f16x2(bf16_lo(w[i]) * up, bf16_hi(w[i]) * up);
+            if (j == 0) {
+                int end = 0;
+                float lse = 0.f;
+                if (live) {
+                    lse = wp.lse[static_cast<int64_t>(req.qo0 + tok) * p.hq + kh * p.g + rr - tok * p.g] * kLog2e;
+                    end = !p.qo_indptr ? req.L : p.kv_end ? p.kv_end[req.qo0 + tok] : req.L - req.n + tok + 1;
+                    if (end < 0 || end > req.L) {
+                        if (blockIdx.x == 0 && kh == 0) raise_flag(p.err, PKV_DEVERR_RANGE);
+                        end = 0;
+                    }
+                    if (lse == -INFINITY) end = 0;
+                }
+                f_s[row] = fminf(fmaxf(p.scale_log2 * down, 1.2e-38f), 3.4e38f);
+                lse_s[row] = lse;
+                end_s[row] = end;
+            }
+        }
+        __syncthreads();
+        const int blocks = min(kWeighRows, rows - r0 + 7) / 8;
+#pragma unroll 1
+        for (int h = 0; h < 2; ++h) {
+            const int key0 = k0 + h * 32;
+            if (key0 >= req.L) break;
+            uint32_t a[2][2][KS][2];   // [16-key group][u][step][lo / hi]
+            float ks[2][2];
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                for (int u = 0; u < 2; ++u) {
+                    const int key = key0 + kt * 16 + r + 8 * u;
+                    const int64_t slot = key < req.L ? quant::slot_of(p.tab, req.base, key) : -3;
+                    if (slot == -1 || slot == -2) raise_flag(p.err, slot == -1 ? PKV_DEVERR_RANGE : PKV_DEVERR_CONTIG);
+                    uint32_t w[KS];
+                    uint32_t e = 1;
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) w[i] = 0;
+                    if (slot >= 0) {
+                        const int t = 1 << p.t_shift;
+                        const uint8_t *base = Quant8<D, 0>::piece(p, static_cast<int>(slot), kh);
+                        const uint4 *cp = reinterpret_cast<const uint4 *>(base + (slot & (t - 1)) * D + c * (D / 4));
+#pragma unroll
+                        for (int i = 0; i < D / 64; ++i) {
+                            const uint4 x = ld_stream_16(cp + i);
+                            w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
+                        }
+                        e = __ldg(base + (static_cast<int64_t>(p.hkv - kh) * 2 * D << p.t_shift) + 2 * kh);
+                    }
+                    ks[kt][u] = byte::scale_value(e);
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) {
+                        a[kt][u][i][0] = byte::lo_to_f16(w[i]);
+                        a[kt][u][i][1] = byte::hi_to_f16(w[i]);
+                    }
+                }
+            float part[2][2] = {};
+#pragma unroll 1
+            for (int n = 0; n < blocks; ++n) {
+                float s[2][4] = {};
+                const uint32_t *qp = q_s + (n * 8 + r) * (D / 2) + c * (D / 8);
+#pragma unroll
+                for (int i = 0; i < KS; i += 2) {
+                    const uint4 x = *reinterpret_cast<const uint4 *>(qp + 2 * i);
+#pragma unroll
+                    for (int kt = 0; kt < 2; ++kt) {
+                        mma_f16(s[kt], a[kt][0][i][0], a[kt][1][i][0], a[kt][0][i][1], a[kt][1][i][1], x.x, x.y);
+                        mma_f16(s[kt], a[kt][0][i + 1][0], a[kt][1][i + 1][0], a[kt][0][i + 1][1], a[kt][1][i + 1][1], x.z, x.w);
+                    }
+                }
+#pragma unroll
+                for (int v = 0; v < 2; ++v) {
+                    const int row = n * 8 + 2 * c + v;
+                    const float f = f_s[row], lse = lse_s[row];
+                    const int end = end_s[row];
+#pragma unroll
+                    for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                        for (int u = 0; u < 2; ++u) {
+                            const float y = s[kt][2 * u + v] * fminf(fmaxf(f * ks[kt][u], 1.2e-38f), 3.4e38f) - lse;
+                            part[kt][u] += key0 + kt * 16 + r + 8 * u < end ? ex2(y) : 0.f;
+                        }
+                }
+            }
+#pragma unroll
+            for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                for (int u = 0; u < 2; ++u)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i) sum[i][kt][u] += h == i ? part[kt][u] : 0.f;
+        }
+    }
+    float *part = wp.part + (static_cast<int64_t>(kh) * p.batch + b) * p.tab.max_len;
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+#pragma unroll
+        for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                float x = sum[h][kt][u];
+                x += __shfl_xor_sync(0xffffffffu, x, 1);
+                x += __shfl_xor_sync(0xffffffffu, x, 2);
+                const int key = k0 + h * 32 + kt * 16 + r + 8 * u;
+                if (c == 0 && key < req.L) part[key] = x;
+            }
+}
+
+__global__ void __launch_bounds__(256) add_kernel(const Params p, const WeighParams wp) {
+    pdl_wait();          // inputs may come from the previous kernel of the stream
+    pdl_launch_next();
+    const int b = blockIdx.y, key = blockIdx.x * 256 + threadIdx.x;
+    int64_t base;
+    const int L = quant::key_count(p.tab, b, base, p.err, false);
+    if (key >= L) return;
+    const int64_t row = p.tab.req_pool_idx[b], at = row * wp.acc_stride + (p.tab.kv_start ? p.tab.kv_start[b] : 0) + key;
+    float x = 0.f;
+    for (int kh = 0; kh < p.hkv; ++kh) x += wp.part[(static_cast<int64_t>(kh) * p.batch + b) * p.tab.max_len + key];
+    wp.acc_out[at] = wp.acc_in ? wp.acc_in[at] + x : x;
+}
+
+// ---------------------------------------------------------------- host side
+int64_t tile_of(const pkv_byte_args *a) {
+    return byte::tile_bytes(std::min(a->page_size, quant::kMaxTile), a->head_dim, a->num_kv_heads);
+}
+Shape shape_of(const pkv_byte_args *a) { return a->head_dim == 128 ? shape<Quant8<128, 0>>(tile_of(a)) : shape<Quant8<64, 0>>(tile_of(a)); }
+
+enum Call { kDecode, kExtend, kWeights };
+const char *const kNames[] = {"pkv_byte_decode", "pkv_byte_extend", "pkv_byte_weights"};
+
+pkv_status check(const pkv_byte_args *a, Call call, bool check_ptrs) {
+    const char *who = kNames[call];
+    const pkv_status st = validate(who, a, call != kDecode, check_ptrs, tile_of, call != kWeights);
+    if (st != PKV_OK) return st;
+    if (call == kExtend && (a->acc_out || a->acc_in))
+        return fail(PKV_ERR_INVALID_ARG, "%s: acc_in and acc_out must be NULL (pkv_byte_weights takes the rows)", who);
+    if (!a->acc_out && a->acc_in) return fail(PKV_ERR_INVALID_ARG, "%s: acc_in without acc_out", who);
+    if (call == kWeights || a->acc_out) {
+        if (a->layout != PKV_LAYOUT_REQ_TO_TOKEN) return fail(PKV_ERR_UNSUPPORTED, "%s: weights need the token-table layout", who);
+        if (a->acc_row_stride < a->r2t_width) return fail(PKV_ERR_INVALID_ARG, "%s: acc_row_stride smaller than the table's width", who);
+        if (a->batch > 65535 || a->num_kv_heads > 65535) return fail(PKV_ERR_UNSUPPORTED, "%s: weights of more than 65535 requests", who);
+    }
+    if (call == kWeights && check_ptrs && a->batch > 0 && (!a->lse || !a->acc_out))
+        return fail(PKV_ERR_INVALID_ARG, "%s: null lse/acc_out", who);
+    return PKV_OK;
+}
+
+// Workspace of the weights: partial sums, and lse where the caller wants none.
+struct WeighPlan {
+    size_t part, lse;
+};
+WeighPlan weigh_plan(const pkv_byte_args *a) {
+    return {up256(static_cast<size_t>(a->num_kv_heads) * a->batch * a->max_seq_len * 4),
+            a->lse ? 0 : up256(static_cast<size_t>(a->total_q) * a->num_q_heads * 4)};
+}
+
+pkv_status weigh(const char *who, const pkv_byte_args *a, const Params &p, const float *lse, float *part, cudaStream_t s) {
+    if (a->max_seq_len == 0) return ok();
+    const WeighParams wp{lse, part, a->acc_in, a->acc_out, a->acc_row_stride};
+    const unsigned L = static_cast<unsigned>(a->max_seq_len), B = static_cast<unsigned>(a->batch);
+    auto *kern = a->head_dim == 128 ? weigh_kernel<128> : weigh_kernel<64>;
+    const pkv_status st = launch_status(launch_chained(kern, dim3((L + kWeighKeys - 1) / kWeighKeys, static_cast<unsigned>(a->num_kv_heads), B),
+                                                       dim3(kWeighWarps * 32), 0, s, p, wp), who);
+    if (st != PKV_OK) return st;
+    return launch_status(launch_chained(add_kernel, dim3((L + 255) / 256, B), dim3(256), 0, s, p, wp), who);
+}
+
+size_t size_of(const pkv_byte_args *a, Call call) {
+    if (!a || check(a, call, false) != PKV_OK) return 0;
+    if (call == kWeights) return std::max<size_t>(weigh_plan(a).part, 256);
+    const size_t n = workspace_size(a, call == kExtend, shape_of(a));
+    if (n == 0 || call == kExtend || !a->acc_out) return n;
+    const WeighPlan w = weigh_plan(a);
+    return n + w.part + w.lse;
+}
+
+pkv_status run(const pkv_byte_args *a, Call call, void *ws, size_t ws_bytes, int32_t *err, cudaStream_t s) {
+    const char *who = kNames[call];
+    if (!a) return fail(PKV_ERR_INVALID_ARG, "%s: null args", who);
+    if (!err) return fail(PKV_ERR_INVALID_ARG, "%s: err_flags is required", who);
+    pkv_status st = check(a, call, true);
+    if (st != PKV_OK) return st;
+    if (a->batch == 0 || (a->total_q == 0 && call != kWeights)) return ok();
+    Params p = params(a, err);
+    const size_t need = size_of(a, call);
+    if (need == 0) return fail(PKV_ERR_UNSUPPORTED, "%s: too many splits, keys or requests", who);
+    st = check_workspace(who, ws, ws_bytes, need);
+    if (st != PKV_OK) return st;
+    char *at = static_cast<char *>(ws);
+    if (call == kWeights) return weigh(who, a, p, a->lse, reinterpret_cast<float *>(at), s);
+    Plan pl;
+    if (!make_plan(a, call == kExtend, shape_of(a), pl)) return fail(PKV_ERR_UNSUPPORTED, "%s: too many splits, keys or requests", who);
+    if (!a->acc_out) return attend<Quant8>(who, a, pl, p, at, s);
+    const WeighPlan w = weigh_plan(a);
+    float *part = reinterpret_cast<float *>(at);
+    if (!p.lse) p.lse = reinterpret_cast<float *>(at + w.part);
+    const Params weighed = p;
+    st = attend<Quant8>(who, a, pl, p, at + w.part + w.lse, s);
+    return st != PKV_OK ? st : weigh(who, a, weighed, weighed.lse, part, s);
+}
+
+}  // namespace
+}  // namespace qattn
+}  // namespace pkv
+
+extern "C" size_t pkv_byte_decode_workspace_size(const pkv_byte_args *args) { return pkv::qattn::size_of(args, pkv::qattn::kDecode); }
+extern "C" size_t pkv_byte_extend_workspace_size(const pkv_byte_args *args) { return pkv::qattn::size_of(args, pkv::qattn::kExtend); }
+extern "C" size_t pkv_byte_weights_workspace_size(const pkv_byte_args *args) { return pkv::qattn::size_of(args, pkv::qattn::kWeights); }
+extern "C" pkv_status pkv_byte_decode(const pkv_byte_args *args, void *workspace, size_t workspace_bytes, int32_t *err_flags,
+                                    pkv_stream_t stream) {
+    return pkv::qattn::run(args, pkv::qattn::kDecode, workspace, workspace_bytes, err_flags, reinterpret_cast<cudaStream_t>(stream));
+}
+extern "C" pkv_status pkv_byte_extend(const pkv_byte_args *args, void *workspace, size_t workspace_bytes, int32_t *err_flags,
+                                    pkv_stream_t stream) {
+    return pkv::qattn::run(args, pkv::qattn::kExtend, workspace, workspace_bytes, err_flags, reinterpret_cast<cudaStream_t>(stream));
+}
+extern "C" pkv_status pkv_byte_weights(const pkv_byte_args *args, void *workspace, size_t workspace_bytes, int32_t *err_flags,
+                                     pkv_stream_t stream) {
+    return pkv::qattn::run(args, pkv::qattn::kWeights, workspace, workspace_bytes, err_flags, reinterpret_cast<cudaStream_t>(stream));
+}

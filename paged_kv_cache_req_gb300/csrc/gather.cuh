@@ -1,4 +1,4 @@
-// Reading the rows of a quantised pool back as bf16: what pkv_quant_gather and pkv_q8_gather share.
+// Reading the rows of a quantised pool back as bf16: what pkv_quant_gather and pkv_byte_gather share.
 //
 // A format F gives kDim, the place of a token's blocks of 16 dims in its tile (place), the
 // read of one (load) and its bf16 values (write).
