@@ -23,7 +23,9 @@ namespace {
 
 template <int D, int NT>
 struct State8 : qattn::State<D, NT> {
-    float unit;   // M - 127: the sums are in units of 2^unit (kNoUnit: no key yet)
+    float unit;       // M - 127: the sums are in units of 2^unit (kNoUnit: no key yet)
+    float *logits;    // row 2 c of the unit's logits, where they are asked for
+    int rows;         // rows of the unit from there on
 };
 
 // 2^d of an integer d <= 0 (0 below the normal numbers).
@@ -192,6 +194,18 @@ struct Quant8 {
                     }
                 top[v] = fmaxf(fmax3(s[0][n][v], s[0][n][2 + v], s[1][n][v]), s[1][n][2 + v]);
             }
+            if (p.logits) {   // (base 2; a key that no row sees is not among them)
+#pragma unroll
+                for (int v = 0; v < 2; ++v)
+                    if (8 * n + v < st.rows)
+#pragma unroll
+                        for (int kt = 0; kt < kGroups; ++kt)
+#pragma unroll
+                            for (int u = 0; u < 2; ++u) {
+                                const int key = key0 + kt * 16 + r + 8 * u;
+                                if (!kMask || key < keys) st.logits[(8 * n + v) * p.logit_stride + key] = s[kt][n][2 * u + v];
+                            }
+            }
             // the maximum is looked for across lanes only when some logit passes it by kLazy
             if (__any_sync(0xffffffffu, top[0] + st.nm[n][0] > st.limit[n][0] || top[1] + st.nm[n][1] > st.limit[n][1])) {
 #pragma unroll
@@ -297,6 +311,11 @@ struct Quant8 {
     __device__ __forceinline__ static void start(const Params &p, const Work &w, State<NT> &st, const uint32_t (&ahead)[D / 8], int lane) {
         start_segment<D, NT>(p, w, st, ahead, lane);
         st.unit = kNoUnit;
+        if (p.logits) {   // (one query row per request)
+            const int row = w.rb * 8 * NT + 2 * (lane & 3);
+            st.logits = p.logits + (static_cast<int64_t>(w.qo0) * p.hq + w.kh * p.g + row) * p.logit_stride;
+            st.rows = p.g - row;
+        }
     }
 
     // The segment's rows: normalised to the output when it is the whole unit, else a partial
@@ -368,11 +387,11 @@ struct Quant8 {
 };
 
 // ---------------------------------------------------------------- weights
-// What keys receive: a block takes 512 keys of one request and kv head, its warps 64 each, over
-// all the request's rows, 64 at a time in shared memory as fp16.  With lse known a weight is one
-// exponential: w = 2^(logit - lse2).  Partial sums, one per kv head, are added up by add_kernel
-// in a fixed order.
-constexpr int kWeighWarps = 8, kWeighKeys = 64 * kWeighWarps, kWeighRows = 64;
+// What keys receive from given rows: a block takes 512 keys of one request and kv head, its warps 64
+// each, over all the request's rows, 128 at a time in shared memory as fp16.  With lse known a
+// weight is one exponential: w = 2^(logit - lse2).  Partial sums, one per kv head, are added up
+// by add_kernel in a fixed order.
+constexpr int kWeighWarps = 8, kWeighKeys = 64 * kWeighWarps, kWeighRows = 128;
 
 struct WeighParams {
     const float *lse;
@@ -382,11 +401,22 @@ struct WeighParams {
     int64_t acc_stride;
 };
 
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
 template <int D>
-__global__ void __launch_bounds__(kWeighWarps * 32) weigh_kernel(const Params p, const WeighParams wp) {
-    __shared__ __align__(16) uint32_t q_s[kWeighRows * D / 2];   // fp16 pairs
-    __shared__ float f_s[kWeighRows], lse_s[kWeighRows];
-    __shared__ int end_s[kWeighRows];
+struct WeighSmem {
+    uint32_t q[kWeighRows * D / 2];                     // fp16 pairs, a row's words as they lie
+    float f[kWeighRows], minus_lse[kWeighRows];         // score -> base-2 logit without K's scale; -lse2
+    int end[kWeighRows], low[kWeighRows / 8];           // key bounds; the least of each eight
+};
+
+template <int D>
+__global__ void __launch_bounds__(kWeighWarps * 32, 2) weigh_kernel(const Params p, const WeighParams wp) {
+    __shared__ __align__(16) WeighSmem<D> sm;
     pdl_wait();          // inputs may come from the previous kernel of the stream
     pdl_launch_next();
     const int b = blockIdx.z, kh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
@@ -397,18 +427,19 @@ __global__ void __launch_bounds__(kWeighWarps * 32) weigh_kernel(const Params p,
     constexpr int KS = D / 16;
     float sum[2][2][2] = {};   // [half][16-key group][u] of keys k0 + 32 h + 16 kt + r + 8 u
     for (int r0 = 0; r0 < rows; r0 += kWeighRows) {
+        const int live = min(kWeighRows, rows - r0), blocks = (live + 7) / 8;
         __syncthreads();
         // eight lanes per row
-        for (int row = threadIdx.x >> 3; row < kWeighRows; row += kWeighWarps * 4) {
+        for (int row = threadIdx.x >> 3; row < blocks * 8; row += kWeighWarps * 4) {
             const int rr = r0 + row, tok = token_of(p, rr), j = threadIdx.x & 7;
             uint32_t w[D / 16];
             uint32_t top = 0;
-            const bool live = rr < rows;
+            const bool in = row < live;
 #pragma unroll
             for (int i = 0; i < D / 64; ++i) {
                 uint4 x = make_uint4(0, 0, 0, 0);
-                if (live) x = __ldg(reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(req.qo0 + tok) * p.q_stride +
-                                                                    (kh * p.g + rr - tok * p.g) * D + j * (D / 8)) + i);
+                if (in) x = __ldg(reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(req.qo0 + tok) * p.q_stride +
+                                                                  (kh * p.g + rr - tok * p.g) * D + j * (D / 8)) + i);
                 w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
             }
 #pragma unroll
@@ -420,32 +451,39 @@ __global__ void __launch_bounds__(kWeighWarps * 32) weigh_kernel(const Params p,
             if (top == 0 || top >= 0x7f80u) e = 0;
             const float up = __int_as_float((e + 127) << 23), down = __int_as_float((127 - e) << 23);
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) q_s[row * (D / 2) + j * (D / 16) + i] = pack_f16x2(bf16_lo(w[i]) * up, bf16_hi(w[i]) * up);
-            if (j == 0) {
-                int end = 0;
-                float lse = 0.f;
-                if (live) {
-                    lse = wp.lse[static_cast<int64_t>(req.qo0 + tok) * p.hq + kh * p.g + rr - tok * p.g] * kLog2e;
-                    end = !p.qo_indptr ? req.L : p.kv_end ? p.kv_end[req.qo0 + tok] : req.L - req.n + tok + 1;
-                    if (end < 0 || end > req.L) {
-                        if (blockIdx.x == 0 && kh == 0) raise_flag(p.err, PKV_DEVERR_RANGE);
-                        end = 0;
-                    }
-                    if (lse == -INFINITY) end = 0;
+            for (int i = 0; i < D / 16; ++i) sm.q[row * (D / 2) + j * (D / 16) + i] = pack_f16x2(bf16_lo(w[i]) * up, bf16_hi(w[i]) * up);
+            int end = 0;
+            float minus_lse = 0.f;
+            if (in && j == 0) {
+                const float lse = wp.lse[static_cast<int64_t>(req.qo0 + tok) * p.hq + kh * p.g + rr - tok * p.g] * kLog2e;
+                end = !p.qo_indptr ? req.L : p.kv_end ? p.kv_end[req.qo0 + tok] : req.L - req.n + tok + 1;
+                if (end < 0 || end > req.L) {
+                    if (blockIdx.x == 0 && kh == 0) raise_flag(p.err, PKV_DEVERR_RANGE);
+                    end = 0;
                 }
-                f_s[row] = fminf(fmaxf(p.scale_log2 * down, 1.2e-38f), 3.4e38f);
-                lse_s[row] = lse;
-                end_s[row] = end;
+                if (lse == -INFINITY) end = 0;
+                minus_lse = -lse;
+            }
+            if (j == 0) {   // (rows past the last have bound 0: nothing of them counts)
+                sm.f[row] = p.scale_log2 * down;
+                sm.minus_lse[row] = minus_lse;
+                sm.end[row] = end;
             }
         }
         __syncthreads();
-        const int blocks = min(kWeighRows, rows - r0 + 7) / 8;
+        if (threadIdx.x < blocks) {
+            int low = INT32_MAX;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) low = min(low, sm.end[threadIdx.x * 8 + i]);
+            sm.low[threadIdx.x] = low;
+        }
+        __syncthreads();
 #pragma unroll 1
         for (int h = 0; h < 2; ++h) {
             const int key0 = k0 + h * 32;
             if (key0 >= req.L) break;
             uint32_t a[2][2][KS][2];   // [16-key group][u][step][lo / hi]
-            float ks[2][2];
+            uint64_t ks[2][2];
 #pragma unroll
             for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
@@ -468,47 +506,54 @@ __global__ void __launch_bounds__(kWeighWarps * 32) weigh_kernel(const Params p,
                         }
                         e = __ldg(base + (static_cast<int64_t>(p.hkv - kh) * 2 * D << p.t_shift) + 2 * kh);
                     }
-                    ks[kt][u] = byte::scale_value(e);
+                    ks[kt][u] = pair(byte::scale_value(e), byte::scale_value(e));
 #pragma unroll
                     for (int i = 0; i < KS; ++i) {
                         a[kt][u][i][0] = byte::lo_to_f16(w[i]);
                         a[kt][u][i][1] = byte::hi_to_f16(w[i]);
                     }
                 }
-            float part[2][2] = {};
+            uint64_t part[2][2] = {};   // of rows 2 c and 2 c + 1
 #pragma unroll 1
             for (int n = 0; n < blocks; ++n) {
                 float s[2][4] = {};
-                const uint32_t *qp = q_s + (n * 8 + r) * (D / 2) + c * (D / 8);
+                const uint32_t *qp = sm.q + (n * 8 + r) * (D / 2) + c * (D / 8);
 #pragma unroll
                 for (int i = 0; i < KS; i += 2) {
                     const uint4 x = *reinterpret_cast<const uint4 *>(qp + 2 * i);
 #pragma unroll
-                    for (int kt = 0; kt < 2; ++kt) {
-                        mma_f16(s[kt], a[kt][0][i][0], a[kt][1][i][0], a[kt][0][i][1], a[kt][1][i][1], x.x, x.y);
-                        mma_f16(s[kt], a[kt][0][i + 1][0], a[kt][1][i + 1][0], a[kt][0][i + 1][1], a[kt][1][i + 1][1], x.z, x.w);
-                    }
-                }
-#pragma unroll
-                for (int v = 0; v < 2; ++v) {
-                    const int row = n * 8 + 2 * c + v;
-                    const float f = f_s[row], lse = lse_s[row];
-                    const int end = end_s[row];
+                    for (int kt = 0; kt < 2; ++kt) mma_f16(s[kt], a[kt][0][i][0], a[kt][1][i][0], a[kt][0][i][1], a[kt][1][i][1], x.x, x.y);
 #pragma unroll
                     for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-                        for (int u = 0; u < 2; ++u) {
-                            const float y = s[kt][2 * u + v] * fminf(fmaxf(f * ks[kt][u], 1.2e-38f), 3.4e38f) - lse;
-                            part[kt][u] += key0 + kt * 16 + r + 8 * u < end ? ex2(y) : 0.f;
-                        }
+                        mma_f16(s[kt], a[kt][0][i + 1][0], a[kt][1][i + 1][0], a[kt][0][i + 1][1], a[kt][1][i + 1][1], x.z, x.w);
                 }
+                const int row = n * 8 + 2 * c;
+                const uint64_t f = *reinterpret_cast<const uint64_t *>(&sm.f[row]), lse = *reinterpret_cast<const uint64_t *>(&sm.minus_lse[row]);
+                const bool whole = key0 + 32 <= sm.low[n];
+                int2 end = make_int2(0, 0);
+                if (!whole) end = *reinterpret_cast<const int2 *>(&sm.end[row]);
+#pragma unroll
+                for (int kt = 0; kt < 2; ++kt)
+#pragma unroll
+                    for (int u = 0; u < 2; ++u) {
+                        const float2 y = unpair(fma2(mul2(pair(s[kt][2 * u], s[kt][2 * u + 1]), f), ks[kt][u], lse));
+                        float x0 = ex2(y.x), x1 = ex2(y.y);
+                        if (!whole) {
+                            const int key = key0 + kt * 16 + r + 8 * u;
+                            x0 = key < end.x ? x0 : 0.f;
+                            x1 = key < end.y ? x1 : 0.f;
+                        }
+                        part[kt][u] = add2(part[kt][u], pair(x0, x1));
+                    }
             }
 #pragma unroll
             for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
-                for (int u = 0; u < 2; ++u)
+                for (int u = 0; u < 2; ++u) {
+                    const float2 x = unpair(part[kt][u]);
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) sum[i][kt][u] += h == i ? part[kt][u] : 0.f;
+                    for (int i = 0; i < 2; ++i) sum[i][kt][u] += h == i ? x.x + x.y : 0.f;
+                }
         }
     }
     float *part = wp.part + (static_cast<int64_t>(kh) * p.batch + b) * p.tab.max_len;
@@ -539,6 +584,26 @@ __global__ void __launch_bounds__(256) add_kernel(const Params p, const WeighPar
     wp.acc_out[at] = wp.acc_in ? wp.acc_in[at] + x : x;
 }
 
+// The same from a decode's logits: acc_out = acc_in + sum over heads of 2^(logit - lse2).
+__global__ void __launch_bounds__(256) finish_kernel(const Params p, const WeighParams wp) {
+    extern __shared__ float lse_s[];
+    pdl_wait();          // the logits
+    pdl_launch_next();
+    const int b = blockIdx.y, key = blockIdx.x * 256 + threadIdx.x;
+    int64_t base;
+    const int L = quant::key_count(p.tab, b, base, p.err, false);
+    if (static_cast<int>(blockIdx.x) * 256 >= L) return;
+    for (int h = threadIdx.x; h < p.hq; h += 256) lse_s[h] = wp.lse[static_cast<int64_t>(b) * p.hq + h] * kLog2e;
+    __syncthreads();
+    if (key >= L) return;
+    const int64_t row = p.tab.req_pool_idx[b], at = row * wp.acc_stride + (p.tab.kv_start ? p.tab.kv_start[b] : 0) + key;
+    const float *y = p.logits + static_cast<int64_t>(b) * p.hq * p.logit_stride + key;
+    float x = 0.f;
+#pragma unroll 16
+    for (int h = 0; h < p.hq; ++h) x += ex2(__ldcs(y + h * p.logit_stride) - lse_s[h]);
+    wp.acc_out[at] = wp.acc_in ? wp.acc_in[at] + x : x;
+}
+
 // ---------------------------------------------------------------- host side
 int64_t tile_of(const pkv_byte_args *a) {
     return byte::tile_bytes(std::min(a->page_size, quant::kMaxTile), a->head_dim, a->num_kv_heads);
@@ -558,20 +623,28 @@ pkv_status check(const pkv_byte_args *a, Call call, bool check_ptrs) {
     if (call == kWeights || a->acc_out) {
         if (a->layout != PKV_LAYOUT_REQ_TO_TOKEN) return fail(PKV_ERR_UNSUPPORTED, "%s: weights need the token-table layout", who);
         if (a->acc_row_stride < a->r2t_width) return fail(PKV_ERR_INVALID_ARG, "%s: acc_row_stride smaller than the table's width", who);
-        if (a->batch > 65535 || a->num_kv_heads > 65535) return fail(PKV_ERR_UNSUPPORTED, "%s: weights of more than 65535 requests", who);
+        if (a->batch > 65535 || a->num_q_heads > 8192) return fail(PKV_ERR_UNSUPPORTED, "%s: weights of more than 65535 requests or 8192 query heads", who);
     }
     if (call == kWeights && check_ptrs && a->batch > 0 && (!a->lse || !a->acc_out))
         return fail(PKV_ERR_INVALID_ARG, "%s: null lse/acc_out", who);
     return PKV_OK;
 }
 
-// Workspace of the weights: partial sums, and lse where the caller wants none.
+// Workspace of the weights: partial sums of given rows, or a decode's logits (and its lse where the
+// caller wants none).  Logits move 8 bytes per key and query head, where reading K again moves
+// head_dim per kv head (and takes the scores a second time): 32 requests of 128 to 8192 keys, 32
+// heads over 8 of 128.
 struct WeighPlan {
     size_t part, lse;
+    int64_t stride;          // floats of a row of logits
 };
-WeighPlan weigh_plan(const pkv_byte_args *a) {
-    return {up256(static_cast<size_t>(a->num_kv_heads) * a->batch * a->max_seq_len * 4),
-            a->lse ? 0 : up256(static_cast<size_t>(a->total_q) * a->num_q_heads * 4)};
+WeighPlan weigh_plan(const pkv_byte_args *a, Call call) {
+    WeighPlan w{};
+    w.stride = (static_cast<int64_t>(a->max_seq_len) + 7) / 8 * 8;
+    const size_t rows = static_cast<size_t>(call == kDecode ? a->num_q_heads : a->num_kv_heads) * a->batch;
+    w.part = up256(rows * static_cast<size_t>(call == kDecode ? w.stride : a->max_seq_len) * 4);
+    w.lse = call == kWeights || a->lse ? 0 : up256(static_cast<size_t>(a->total_q) * a->num_q_heads * 4);
+    return w;
 }
 
 pkv_status weigh(const char *who, const pkv_byte_args *a, const Params &p, const float *lse, float *part, cudaStream_t s) {
@@ -587,10 +660,10 @@ pkv_status weigh(const char *who, const pkv_byte_args *a, const Params &p, const
 
 size_t size_of(const pkv_byte_args *a, Call call) {
     if (!a || check(a, call, false) != PKV_OK) return 0;
-    if (call == kWeights) return std::max<size_t>(weigh_plan(a).part, 256);
+    if (call == kWeights) return std::max<size_t>(weigh_plan(a, call).part, 256);
     const size_t n = workspace_size(a, call == kExtend, shape_of(a));
     if (n == 0 || call == kExtend || !a->acc_out) return n;
-    const WeighPlan w = weigh_plan(a);
+    const WeighPlan w = weigh_plan(a, call);
     return n + w.part + w.lse;
 }
 
@@ -611,12 +684,17 @@ pkv_status run(const pkv_byte_args *a, Call call, void *ws, size_t ws_bytes, int
     Plan pl;
     if (!make_plan(a, call == kExtend, shape_of(a), pl)) return fail(PKV_ERR_UNSUPPORTED, "%s: too many splits, keys or requests", who);
     if (!a->acc_out) return attend<Quant8>(who, a, pl, p, at, s);
-    const WeighPlan w = weigh_plan(a);
-    float *part = reinterpret_cast<float *>(at);
+    if (a->max_seq_len == 0) return attend<Quant8>(who, a, pl, p, at, s);
+    const WeighPlan w = weigh_plan(a, call);
+    p.logits = reinterpret_cast<float *>(at);
+    p.logit_stride = w.stride;
     if (!p.lse) p.lse = reinterpret_cast<float *>(at + w.part);
-    const Params weighed = p;
+    const Params q = p;
     st = attend<Quant8>(who, a, pl, p, at + w.part + w.lse, s);
-    return st != PKV_OK ? st : weigh(who, a, weighed, weighed.lse, part, s);
+    if (st != PKV_OK) return st;
+    const WeighParams wp{q.lse, nullptr, a->acc_in, a->acc_out, a->acc_row_stride};
+    return launch_status(launch_chained(finish_kernel, dim3((static_cast<unsigned>(a->max_seq_len) + 255) / 256, static_cast<unsigned>(a->batch)),
+                                        dim3(256), static_cast<size_t>(a->num_q_heads) * 4, s, q, wp), who);
 }
 
 }  // namespace

@@ -1,11 +1,12 @@
 // pkv_evict: the pages whose tokens received least attention go back to the free list.
 //
-// Two kernels, a cluster of blocks per request in each.  The first checks the requests, counts
-// what each loses, and writes each page's score as a 32-bit key whose unsigned order is
-// theirs.  The second finds the border key by digits (11, 11 and 10 bits: a histogram of the
-// pages that share the digits so far, summed over the cluster), numbers the pages that stay and
-// those that go, and moves the columns: chunk after chunk, each read by the whole
-// cluster before any of it is written, so that a row may be compacted in place.
+// Two kernels, a cluster of blocks per request in each.  The first checks the requests and
+// their pages and counts what each loses.  The second takes each page's score as a 32-bit key
+// whose unsigned order is theirs (kept in shared memory where they fit), finds the border key by
+// digits (11, 11 and 10 bits: a histogram of the pages that share the digits so far, summed over the
+// cluster), numbers the pages that stay and those that go, and moves the columns: chunk after
+// chunk, each read by the whole cluster before any of it is written, so that a row may be
+// compacted in place.
 #include <algorithm>
 
 #include "pkv_internal.cuh"
@@ -14,10 +15,10 @@ namespace pkv {
 namespace evict {
 namespace {
 
-constexpr int kThreads = 1024;
 constexpr int kMaxBatch = 8192, kMaxCluster = 8;
 constexpr int kBins = 2048;
-constexpr int kEach = 4;          // columns of a thread per chunk
+constexpr int kEach = 8;          // columns of a thread per chunk
+constexpr int kKeysInSmem = 16384;   // pages of a block up to which its keys are kept in shared memory
 
 struct Info {                     // a request, as the first kernel found it
     int64_t r2t, acc;             // its first column in the table and in acc
@@ -29,55 +30,59 @@ enum { kBad, kKeep, kEvict };
 struct Params {
     pkv_evict_args a;
     int32_t *err;
-    uint32_t *keys;               // [B][pages_max]; then each page's new place, or -1
+    uint32_t *places;             // [B][pages_max]: each page's new place, or -1 (before that its key, where keys are many)
     Info *info;                   // [B]
     int32_t *free_state;          // head and count as they were
     int64_t pages_max;
-    int32_t ps_shift;
+    int32_t ps_shift, cluster, smem_keys;
 };
 
-__device__ __forceinline__ int cluster_size() {
-    uint32_t n;
-    asm volatile("mov.u32 %0, %%cluster_nctaid.x;\n" : "=r"(n));
-    return static_cast<int>(n);
-}
-__device__ __forceinline__ int block_sum_int(int v, int *scratch) {   // kThreads threads; every thread gets the sum
+template <int T>
+__device__ __forceinline__ int block_sum_int(int v, int *scratch) {   // every thread gets the sum
     v = __reduce_add_sync(0xffffffffu, v);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __syncthreads();
     if (lane == 0) scratch[warp] = v;
     __syncthreads();
-    return __reduce_add_sync(0xffffffffu, scratch[lane]);
+    return __reduce_add_sync(0xffffffffu, lane < T / 32 ? scratch[lane] : 0);
 }
-// Exclusive prefix over the block's threads; *total gets the sum.
-__device__ __forceinline__ int block_scan(int v, int *scratch, int *total) {
+// Exclusive prefix over the block's warps of a value per warp; *total gets the sum.
+template <int T>
+__device__ __forceinline__ int warps_scan(int v, int *scratch, int *total) {
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    int incl = v;
-    for (int o = 1; o < 32; o <<= 1) {
-        const int x = __shfl_up_sync(0xffffffffu, incl, o);
-        if (lane >= o) incl += x;
-    }
     __syncthreads();
-    if (lane == 31) scratch[warp] = incl;
+    if (lane == 0) scratch[warp] = v;
     __syncthreads();
-    int x = scratch[lane], s = x;
+    const int x = lane < T / 32 ? scratch[lane] : 0;
+    int s = x;
     for (int o = 1; o < 32; o <<= 1) {
         const int y = __shfl_up_sync(0xffffffffu, s, o);
         if (lane >= o) s += y;
     }
     *total = __shfl_sync(0xffffffffu, s, 31);
-    return __shfl_sync(0xffffffffu, s - x, warp) + incl - v;
+    return __shfl_sync(0xffffffffu, s - x, warp);
 }
-// Sum of the values that the cluster's blocks hold in `mine`, and of those before this block.
-__device__ __forceinline__ int cluster_sum(int *mine, int rank, int size, int *before) {
-    int all = 0, low = 0;
-    for (int i = 0; i < size; ++i) {
-        const int x = ld_cluster_s32(mapa(smem_u32(mine), i));
-        if (i < rank) low += x;
-        all += x;
+// The same over its threads.
+template <int T>
+__device__ __forceinline__ int block_scan(int v, int *scratch, int *total) {
+    const int lane = threadIdx.x & 31;
+    int incl = v;
+    for (int o = 1; o < 32; o <<= 1) {
+        const int x = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += x;
     }
-    *before = low;
-    return all;
+    return warps_scan<T>(__shfl_sync(0xffffffffu, incl, 31), scratch, total) + incl - v;
+}
+// Makes shared and global writes of the cluster's blocks visible to all of them.
+__device__ __forceinline__ void sync_all(int size) {
+    __syncthreads();
+    if (size > 1) cluster_sync_all();
+}
+// Sum of the values that the blocks before this one hold in `mine`.
+__device__ __forceinline__ int sum_before(int *mine, int rank) {
+    int low = 0;
+    for (int i = 0; i < rank; ++i) low += ld_cluster_s32(mapa(smem_u32(mine), i));
+    return low;
 }
 
 // Unsigned keys in the order of the scores; NaN above all.
@@ -87,30 +92,30 @@ __device__ __forceinline__ uint32_t key_of(float score) {
     return u & 0x80000000u ? ~u : u | 0x80000000u;
 }
 
-__global__ void __launch_bounds__(kThreads) score_kernel(const Params p) {
+template <int T>
+__global__ void __launch_bounds__(T) check_kernel(const Params p) {
     __shared__ int scratch[32];
     __shared__ int flags_s;
     pdl_wait();          // inputs may come from the previous kernel of the stream
     pdl_launch_next();
     const pkv_evict_args &a = p.a;
-    const int size = cluster_size(), rank = cluster_rank(), b = blockIdx.x / size, tid = threadIdx.x;
+    const int size = p.cluster, rank = size > 1 ? cluster_rank() : 0, b = blockIdx.x / size, tid = threadIdx.x;
     if (blockIdx.x == 0 && tid < 2) p.free_state[tid] = a.free_state[tid];
     const int64_t row = a.req_pool_idx[b], s = a.kv_start ? a.kv_start[b] : 0, L = a.seq_lens[b];
     const int64_t budget = a.budget[b], first = a.keep_first ? a.keep_first[b] : 0, last = a.keep_last ? a.keep_last[b] : 0;
     const int mask = a.page_size - 1;
     bool bad = row < 0 || row >= a.r2t_rows || s < 0 || (s & mask) || L < 0 || s + L > a.r2t_width || budget < 0 || first < 0 || last < 0;
     int same = 0;
-    for (int i = tid; i < a.batch; i += kThreads) same += i != b && a.req_pool_idx[i] == row;
-    bad |= block_sum_int(same, scratch) != 0;
-    const bool long_ = !bad && L > a.max_seq_len;
+    for (int i = tid; i < a.batch; i += T) same |= i != b && a.req_pool_idx[i] == row;
+    bad |= __syncthreads_or(same) != 0;
+    const bool too_long = !bad && L > a.max_seq_len;
     Info f{};
     f.L = static_cast<int>(L);
-    f.state = bad || long_ ? kBad : kKeep;
-    int n = 0;
+    f.state = bad || too_long ? kBad : kKeep;
     if (f.state == kKeep) {
         f.r2t = row * a.r2t_row_stride + s;
         f.acc = row * a.acc_row_stride + s;
-        n = static_cast<int>((L + mask) >> p.ps_shift);
+        const int n = static_cast<int>((L + mask) >> p.ps_shift);
         const int64_t head = (first + mask) >> p.ps_shift, tail = max(L - last, static_cast<int64_t>(0)) >> p.ps_shift;
         f.head = static_cast<int>(min(head, static_cast<int64_t>(n)));
         f.tail = static_cast<int>(max(static_cast<int64_t>(f.head), min(tail, static_cast<int64_t>(n - 1))));
@@ -118,69 +123,97 @@ __global__ void __launch_bounds__(kThreads) score_kernel(const Params p) {
                                       max(static_cast<int64_t>(0), n - max(static_cast<int64_t>(1), budget >> p.ps_shift))));
         if (f.gone > 0) f.state = kEvict;
     }
-    int flags = bad ? PKV_DEVERR_RANGE : long_ ? PKV_DEVERR_CAPACITY : 0;
+    int flags = bad ? PKV_DEVERR_RANGE : too_long ? PKV_DEVERR_CAPACITY : 0;
     if (f.state == kEvict) {
-        // the pages in [head, tail) are whole
-        const int lanes = min(a.page_size, 32), shift = min(p.ps_shift, 5), sub = tid & (lanes - 1), each = a.page_size >> shift;
-        const int groups = kThreads >> shift;   // pages at a time
-        for (int64_t p0 = f.head + static_cast<int64_t>(rank) * groups; p0 < f.tail; p0 += static_cast<int64_t>(size) * groups) {
-            const int64_t page = p0 + (tid >> shift);
-            const bool in = page < f.tail;
-            double sum = 0;
-            if (in) {
-                const float *x = a.acc + f.acc + (page << p.ps_shift) + sub;
-                for (int i = 0; i < each; ++i) sum += x[i * lanes];
-            }
-            for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-            if (in && sub == 0) {
-                p.keys[b * p.pages_max + page] = key_of(static_cast<float>(sum));
-                const int64_t slot = a.req_to_token[f.r2t + (page << p.ps_shift)];
-                if (slot < 0 || (slot >> p.ps_shift) >= a.num_pool_pages) flags |= PKV_DEVERR_RANGE;
-                else if (slot & mask) flags |= PKV_DEVERR_CONTIG;
+        const int32_t *table = a.req_to_token + f.r2t;
+        const int step = size * T;
+        for (int p0 = f.head + rank * T + tid; p0 < f.tail; p0 += step * 8) {
+            int64_t slot[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) slot[i] = p0 + i * step < f.tail ? table[static_cast<int64_t>(p0 + i * step) << p.ps_shift] : 0;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                if (slot[i] < 0 || (slot[i] >> p.ps_shift) >= a.num_pool_pages) flags |= PKV_DEVERR_RANGE;
+                else if (slot[i] & mask) flags |= PKV_DEVERR_CONTIG;
             }
         }
     }
     flags = __reduce_or_sync(0xffffffffu, flags);
-    if (tid == 0) flags_s = 0;
+    if ((tid & 31) == 0) scratch[tid >> 5] = flags;
     __syncthreads();
-    if ((tid & 31) == 0 && flags) atomicOr(&flags_s, flags);
-    __syncthreads();
-    cluster_sync_all();
-    if (rank == 0) {
-        flags = 0;
-        for (int i = 0; i < size; ++i) flags |= ld_cluster_s32(mapa(smem_u32(&flags_s), i));
-        if (tid == 0) {
-            if (flags) raise_flag(p.err, flags);
-            if (flags && f.state == kEvict) {   // a bad page
-                f.state = kKeep;
-                f.gone = 0;
-            }
-            p.info[b] = f;
+    flags = 0;
+    for (int i = 0; i < T / 32; ++i) flags |= scratch[i];
+    if (tid == 0) flags_s = flags;
+    sync_all(size);
+    if (rank == 0 && tid == 0) {
+        for (int i = 1; i < size; ++i) flags |= ld_cluster_s32(mapa(smem_u32(&flags_s), i));
+        if (flags) raise_flag(p.err, flags);
+        if (flags && f.state == kEvict) {   // a bad page
+            f.state = kKeep;
+            f.gone = 0;
         }
+        p.info[b] = f;
     }
-    __syncthreads();
-    cluster_sync_all();   // (no block leaves while its shared memory is read)
+    sync_all(size);   // (no block leaves while its shared memory is read)
 }
 
-__global__ void __launch_bounds__(kThreads) move_kernel(const Params p) {
+// Keys of the pages [lo, hi) of a request: `keys[i - lo]` is page i's.
+template <int T>
+__device__ __forceinline__ void load_keys(const Params &p, const float *__restrict__ acc, int lo, int hi, uint32_t *keys) {
+    const int tid = threadIdx.x;
+    if (p.ps_shift == 0) {
+        for (int i0 = lo + tid; i0 < hi; i0 += 8 * T) {
+            float x[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = i0 + i * T < hi ? acc[i0 + i * T] : 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                if (i0 + i * T < hi) keys[i0 + i * T - lo] = key_of(x[i]);
+        }
+        return;
+    }
+    // 4 columns to a lane (2 where a page has no more), a page to up to 32 lanes; these pages are whole
+    const int cols = p.ps_shift == 1 ? 2 : 4, lane_shift = min(p.ps_shift - (cols == 4 ? 2 : 1), 5), lanes = 1 << lane_shift;
+    const int sub = tid & (lanes - 1), each = (1 << p.ps_shift) / (cols * lanes);
+    for (int i0 = lo; i0 < hi; i0 += T >> lane_shift) {
+        const int page = i0 + (tid >> lane_shift);
+        double sum = 0;
+        if (page < hi) {
+            const float *x = acc + (static_cast<int64_t>(page) << p.ps_shift) + sub * cols;
+            for (int e = 0; e < each; ++e, x += lanes * cols)
+                for (int c = 0; c < cols; ++c) sum += x[c];
+        }
+        for (int o = 1; o < lanes; o <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+        if (page < hi && sub == 0) keys[page - lo] = key_of(static_cast<float>(sum));
+    }
+}
+
+template <int T>
+__global__ void __launch_bounds__(T) move_kernel(const Params p) {
+    extern __shared__ uint32_t keys_s[];
     __shared__ int hist[3][kBins];
     __shared__ int scratch[32];
-    __shared__ int found[2];
+    __shared__ int found[3];
     __shared__ int ties_s, gone_s;
-    pdl_wait();          // the first kernel's keys
+    pdl_wait();          // the first kernel's findings
     pdl_launch_next();
     const pkv_evict_args &a = p.a;
-    const int size = cluster_size(), rank = cluster_rank(), b = blockIdx.x / size, tid = threadIdx.x;
+    const int size = p.cluster, rank = size > 1 ? cluster_rank() : 0, b = blockIdx.x / size, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     Info f = p.info[b];
     // pages that the requests before this one lose, and all of them
     int low = 0, all = 0;
-    for (int i = tid; i < a.batch; i += kThreads) {
+    for (int i = tid; i < a.batch; i += T) {
         const int g = p.info[i].gone;
         all += g;
         if (i < b) low += g;
     }
-    all = block_sum_int(all, scratch);
-    low = block_sum_int(low, scratch);
+    for (int i = tid; i < 3 * kBins; i += T) (&hist[0][0])[i] = 0;
+    const int n = f.tail - f.head, seg = (n + size - 1) / size;
+    const int lo = f.head + min(n, rank * seg), hi = f.head + min(n, (rank + 1) * seg);
+    uint32_t *places = p.places + b * p.pages_max, *keys = p.smem_keys ? keys_s : places + lo;
+    if (f.gone > 0) load_keys<T>(p, a.acc + f.acc, lo, hi, keys);
+    all = block_sum_int<T>(all, scratch);
+    low = block_sum_int<T>(low, scratch);
     const int64_t head = p.free_state[0], count = p.free_state[1];
     const bool room = all == 0 || (head >= all && head <= a.free_pages_len);
     if (blockIdx.x == 0 && tid == 0) {
@@ -194,108 +227,110 @@ __global__ void __launch_bounds__(kThreads) move_kernel(const Params p) {
     }
     const int left = f.L - (f.gone << p.ps_shift);
     if (rank == 0 && tid == 0) a.seq_lens_out[b] = left;
-    const bool move_table = a.req_to_token_out != a.req_to_token, move_acc = a.acc_out != a.acc;
-    if (f.state == kBad || (f.gone == 0 && !move_table && !move_acc)) return;   // (the whole cluster)
-    uint32_t *keys = p.keys + b * p.pages_max;
+    const bool elsewhere = a.req_to_token_out != a.req_to_token || a.acc_out != a.acc;
+    if (f.state == kBad || (f.gone == 0 && !elsewhere)) return;   // (the whole cluster)
     if (f.gone > 0) {
         // ---- the border: the key of the best page that goes, and how many of that key go
-        const int n = f.tail - f.head, seg = (n + size - 1) / size;
-        const int lo = f.head + min(n, rank * seg), hi = f.head + min(n, (rank + 1) * seg);
-        for (int i = tid; i < 3 * kBins; i += kThreads) (&hist[0][0])[i] = 0;
-        __syncthreads();
         uint32_t border = 0, known = 0;   // its digits so far, and their mask
         int want = f.gone, ties = 0;      // pages to find among those that share them; pages that do
+        __syncthreads();
 #pragma unroll 1
         for (int d = 0; d < 3; ++d) {
             const int shift = d == 0 ? 21 : d == 1 ? 10 : 0, bins = d == 2 ? 1024 : kBins;
-            for (int i = lo + tid; i < hi; i += kThreads) {
+#pragma unroll 4
+            for (int i = tid; i < hi - lo; i += T) {
                 const uint32_t k = keys[i];
                 if ((k & known) == border) atomicAdd(&hist[d][(k >> shift) & (bins - 1)], 1);
             }
-            __syncthreads();
-            cluster_sync_all();
-            int x[2] = {0, 0};
-            for (int r = 0; r < size; ++r)
+            sync_all(size);
+            constexpr int kOwn = kBins / T;   // bins of a thread
+            int x[kOwn], sum = 0;
 #pragma unroll
-                for (int i = 0; i < 2; ++i) x[i] += ld_cluster_s32(mapa(smem_u32(&hist[d][2 * tid + i]), r));
-            int total;
-            const int before = block_scan(x[0] + x[1], scratch, &total);
-            if (before < want && want <= before + x[0]) {
-                found[0] = 2 * tid;
-                found[1] = before;
-                ties_s = x[0];
-            } else if (before + x[0] < want && want <= before + x[0] + x[1]) {
-                found[0] = 2 * tid + 1;
-                found[1] = before + x[0];
-                ties_s = x[1];
+            for (int i = 0; i < kOwn; ++i) {
+                x[i] = hist[d][kOwn * tid + i];
+                for (int r = 1; r < size; ++r) x[i] += ld_cluster_s32(mapa(smem_u32(&hist[d][kOwn * tid + i]), (rank + r) % size));
+                sum += x[i];
+            }
+            int total, before = block_scan<T>(sum, scratch, &total);
+            if (before < want && want <= before + sum) {
+#pragma unroll
+                for (int i = 0; i < kOwn; ++i) {
+                    if (before < want && want <= before + x[i]) {
+                        found[0] = kOwn * tid + i;
+                        found[1] = before;
+                        found[2] = x[i];
+                    }
+                    before += x[i];
+                }
             }
             __syncthreads();
             border |= static_cast<uint32_t>(found[0]) << shift;
             known |= static_cast<uint32_t>(bins - 1) << shift;
             want -= found[1];
-            ties = ties_s;
-            __syncthreads();
+            ties = found[2];
         }
-        // ---- of the pages at the border the last `want` go: places of this thread's pages in order
-        const int per = (hi - lo + kThreads - 1) / kThreads, i0 = min(hi, lo + tid * per), i1 = min(hi, i0 + per);
-        int t = 0;
-        for (int i = i0; i < i1; ++i) t += keys[i] == border;
-        int sum, before;
-        int tie = block_scan(t, scratch, &sum);
-        if (tid == 0) ties_s = sum;
-        __syncthreads();
-        cluster_sync_all();
-        cluster_sum(&ties_s, rank, size, &before);
-        tie += before;
+        // ---- of the pages at the border the last `want` go.  Each warp has a run of pages, 32 at a time.
+        const int per = ((hi - lo + T / 32 - 1) / (T / 32) + 31) / 32 * 32, i0 = min(hi - lo, warp * per), i1 = min(hi - lo, i0 + per);
         const int stay = ties - want;
-        int go = 0;
-        {
-            int x = tie;
-            for (int i = i0; i < i1; ++i) {
-                const uint32_t k = keys[i];
-                go += k < border || (k == border && x++ >= stay);
+        const uint32_t lower = (1u << lane) - 1;
+        int tie = 0, sum;
+        if (ties > want) {   // else all of them go
+            for (int i = i0 + lane; i < i1 + lane; i += 32) tie += __popc(__ballot_sync(0xffffffffu, i < i1 && keys[i] == border));
+            tie = warps_scan<T>(tie, scratch, &sum);
+            if (size > 1) {
+                if (tid == 0) ties_s = sum;
+                sync_all(size);
+                tie += sum_before(&ties_s, rank);
             }
         }
-        int gone = block_scan(go, scratch, &sum);
-        if (tid == 0) gone_s = sum;
-        __syncthreads();
-        cluster_sync_all();
-        cluster_sum(&gone_s, rank, size, &before);
-        gone += before;
-        int32_t *out = a.free_pages + head - all + low;
-        for (int i = i0; i < i1; ++i) {
-            const uint32_t k = keys[i];
-            const bool goes = k < border || (k == border && tie++ >= stay);
-            if (goes) out[gone] = a.req_to_token[f.r2t + (static_cast<int64_t>(i) << p.ps_shift)] >> p.ps_shift;
-            keys[i] = goes ? 0xffffffffu : static_cast<uint32_t>(i - gone);
-            gone += goes;
+        int gone = 0;
+        for (int i = i0 + lane, x = tie; i < i1 + lane; i += 32) {
+            const uint32_t k = i < i1 ? keys[i] : 0xffffffffu;
+            const uint32_t eq = __ballot_sync(0xffffffffu, i < i1 && k == border);
+            gone += __popc(__ballot_sync(0xffffffffu, i < i1 && (k < border || (k == border && (ties <= want || x + __popc(eq & lower) >= stay)))));
+            x += __popc(eq);
         }
-        __syncthreads();
-        cluster_sync_all();   // all places are known to the cluster
+        gone = warps_scan<T>(gone, scratch, &sum);
+        if (size > 1) {
+            if (tid == 0) gone_s = sum;
+            sync_all(size);
+            gone += sum_before(&gone_s, rank);
+        }
+        int32_t *out = a.free_pages + head - all + low;
+        for (int i = i0 + lane; i < i1 + lane; i += 32) {
+            const uint32_t k = i < i1 ? keys[i] : 0xffffffffu;
+            const uint32_t eq = __ballot_sync(0xffffffffu, i < i1 && k == border);
+            const bool goes = i < i1 && (k < border || (k == border && (ties <= want || tie + __popc(eq & lower) >= stay)));
+            const uint32_t g = __ballot_sync(0xffffffffu, goes);
+            const int at = gone + __popc(g & lower);
+            if (goes) out[at] = a.req_to_token[f.r2t + (static_cast<int64_t>(lo + i) << p.ps_shift)] >> p.ps_shift;
+            if (i < i1) places[lo + i] = goes ? 0xffffffffu : static_cast<uint32_t>(lo + i - at);
+            gone += __popc(g);
+            tie += __popc(eq);
+        }
+        sync_all(size);   // all places are known to the cluster
     }
     // ---- the columns
     const int mask = a.page_size - 1;
-    const int from = move_table || move_acc ? 0 : f.head << p.ps_shift;   // (columns before head stay where they are)
-    const int step = size * kThreads * kEach;
+    const int from = elsewhere ? 0 : f.head << p.ps_shift;   // (columns before head stay where they are)
+    const int step = size * T * kEach;
     for (int c0 = from; c0 < f.L; c0 += step) {
         int32_t slot[kEach];
         float w[kEach];
         int to[kEach];
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
-            const int c = c0 + (rank * kEach + e) * kThreads + tid;
-            to[e] = -1;
-            if (c >= f.L) continue;
-            const int page = c >> p.ps_shift;
+            const int c = c0 + (rank * kEach + e) * T + tid, page = c >> p.ps_shift;
             int q = page;
-            if (f.gone > 0 && page >= f.head) q = page < f.tail ? static_cast<int>(__ldcg(keys + page)) : page - f.gone;
-            if (q < 0) continue;
-            to[e] = (q << p.ps_shift) + (c & mask);
-            slot[e] = a.req_to_token[f.r2t + c];
-            w[e] = a.acc[f.acc + c];
+            if (c >= f.L) q = -1;
+            else if (f.gone > 0 && page >= f.head) q = page < f.tail ? static_cast<int>(__ldcg(places + page)) : page - f.gone;
+            to[e] = q < 0 ? -1 : (q << p.ps_shift) + (c & mask);
+            if (c < f.L) {   // (read whether it stays or not: the place is on its way)
+                slot[e] = a.req_to_token[f.r2t + c];
+                w[e] = a.acc[f.acc + c];
+            }
         }
-        __syncthreads();
-        cluster_sync_all();   // the chunk has been read
+        sync_all(size);   // the chunk has been read
 #pragma unroll
         for (int e = 0; e < kEach; ++e) {
             if (to[e] < 0) continue;
@@ -304,27 +339,35 @@ __global__ void __launch_bounds__(kThreads) move_kernel(const Params p) {
         }
     }
     // (a column behind the last kept one is nobody's target, and all of them have been read)
-    for (int c = left + rank * kThreads + tid; c < f.L; c += size * kThreads) a.acc_out[f.acc + c] = 0.f;
-    __syncthreads();
-    cluster_sync_all();   // (no block leaves while its shared memory is read)
+    for (int c = left + rank * T + tid; c < f.L; c += size * T) a.acc_out[f.acc + c] = 0.f;
+    sync_all(size);   // (no block leaves while its shared memory is read)
 }
 
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-pkv_status launch(void (*kern)(Params), const Params &p, int batch, int cluster, cudaStream_t s) {
+pkv_status launch(void (*kern)(Params), const Params &p, int threads, size_t smem, cudaStream_t s) {
     cudaLaunchConfig_t cfg{};
-    cfg.gridDim = dim3(static_cast<unsigned>(batch * cluster));
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3(static_cast<unsigned>(p.a.batch * p.cluster));
+    cfg.blockDim = dim3(static_cast<unsigned>(threads));
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = s;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = static_cast<unsigned>(cluster);
+    attr[1].val.clusterDim.x = static_cast<unsigned>(p.cluster);
     attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = 2;
+    cfg.numAttrs = p.cluster > 1 ? 2 : 1;
     return launch_status(cudaLaunchKernelEx(&cfg, kern, p), "pkv_evict");
+}
+template <int T>
+pkv_status run(const Params &p, cudaStream_t s) {
+    const size_t smem = p.smem_keys ? (static_cast<size_t>(p.pages_max) + p.cluster - 1) / p.cluster * 4 : 0;
+    if (raise_smem_limit(reinterpret_cast<const void *>(move_kernel<T>)) < smem)
+        return fail(PKV_ERR_CUDA, "pkv_evict: cannot raise the shared-memory limit");
+    const pkv_status st = launch(check_kernel<T>, p, T, 0, s);
+    return st != PKV_OK ? st : launch(move_kernel<T>, p, T, smem, s);
 }
 
 }  // namespace
@@ -380,10 +423,11 @@ extern "C" pkv_status pkv_evict(const pkv_evict_args *args, void *workspace, siz
     char *at = static_cast<char *>(workspace);
     p.free_state = reinterpret_cast<int32_t *>(at);
     p.info = reinterpret_cast<Info *>(at + 256);
-    p.keys = reinterpret_cast<uint32_t *>(at + 256 + up256(a.batch * sizeof(Info)));
+    p.places = reinterpret_cast<uint32_t *>(at + 256 + up256(a.batch * sizeof(Info)));
     // more blocks to a request while there are SMs for them and columns to share
     int cluster = 1;
-    while (cluster < kMaxCluster && static_cast<int64_t>(longest) > 2048ll * cluster && 2ll * a.batch * cluster <= sm_count()) cluster *= 2;
-    const pkv_status st = launch(score_kernel, p, a.batch, cluster, s);
-    return st != PKV_OK ? st : launch(move_kernel, p, a.batch, cluster, s);
+    while (cluster < kMaxCluster && static_cast<int64_t>(longest) > 4096ll * cluster && 2ll * a.batch * cluster <= sm_count()) cluster *= 2;
+    p.cluster = cluster;
+    p.smem_keys = (p.pages_max + cluster - 1) / cluster <= kKeysInSmem;
+    return longest > 2048 ? run<1024>(p, s) : run<256>(p, s);
 }

@@ -63,6 +63,8 @@ struct Params {
     // per span: the unit that its first tile continues, {request (-1: none), row block * Hkv + kv
     // head, 2 x spans back to its first + (1 if it began inside that span), spans on to its last}
     int4 *cuts;
+    float *logits;           // formats that keep them: base-2 logits [B][Hq][logit_stride], or null
+    int64_t logit_stride;
     int32_t max_rows;        // > 0: requests with more rows per kv head are left to the held path
 };
 
