@@ -407,9 +407,11 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return d;
 }
 
+// Place in its row of the k-th 16 bytes of lane (r, c)'s dims: the four c of two rows lie in eight bank groups.
+__device__ __forceinline__ int q_chunk(int row, int c, int k) { return (4 * k + c) ^ ((row & 1) << 2); }
 template <int D>
 struct WeighSmem {
-    uint32_t q[kWeighRows * D / 2];                     // fp16 pairs, a row's words as they lie
+    uint4 q[kWeighRows * D / 8];                        // fp16, 16 bytes of a row at a time (see q_chunk)
     float f[kWeighRows], minus_lse[kWeighRows];         // score -> base-2 logit without K's scale; -lse2
     int end[kWeighRows], low[kWeighRows / 8];           // key bounds; the least of each eight
 };
@@ -451,7 +453,12 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 2) weigh_kernel(const Params
             if (top == 0 || top >= 0x7f80u) e = 0;
             const float up = __int_as_float((e + 127) << 23), down = __int_as_float((127 - e) << 23);
 #pragma unroll
-            for (int i = 0; i < D / 16; ++i) sm.q[row * (D / 2) + j * (D / 16) + i] = pack_f16x2(bf16_lo(w[i]) * up, bf16_hi(w[i]) * up);
+            for (int i = 0; i < D / 16; ++i) w[i] = pack_f16x2(bf16_lo(w[i]) * up, bf16_hi(w[i]) * up);
+#pragma unroll
+            for (int i = 0; i < D / 64; ++i) {
+                const int chunk = j * (D / 64) + i;
+                sm.q[row * (D / 8) + q_chunk(row, chunk / (D / 32), chunk % (D / 32))] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
+            }
             int end = 0;
             float minus_lse = 0.f;
             if (in && j == 0) {
@@ -517,10 +524,10 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 2) weigh_kernel(const Params
 #pragma unroll 1
             for (int n = 0; n < blocks; ++n) {
                 float s[2][4] = {};
-                const uint32_t *qp = sm.q + (n * 8 + r) * (D / 2) + c * (D / 8);
+                const uint4 *qp = sm.q + (n * 8 + r) * (D / 8);
 #pragma unroll
                 for (int i = 0; i < KS; i += 2) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(qp + 2 * i);
+                    const uint4 x = qp[q_chunk(r, c, i / 2)];
 #pragma unroll
                     for (int kt = 0; kt < 2; ++kt) mma_f16(s[kt], a[kt][0][i][0], a[kt][1][i][0], a[kt][0][i][1], a[kt][1][i][1], x.x, x.y);
 #pragma unroll
