@@ -33,6 +33,11 @@ given bf16 pools are quantised once and not kept (k_pool and v_pool are None the
 step's calls are their 4-bit forms (pkv_quant_store, pkv_quant_decode or pkv_quant_extend,
 and pkv_quant_gather before a contiguous cross-attention).  ``scales`` are the heads' fp32
 (k_scale, v_scale), by default each head's largest finite magnitude in the pools / 2688.
+With ``quant=8`` it is held in 8 bits, with a scale per tile and head (see pkv_byte_store), which
+takes no ``scales``.
+
+``BudgetedDecode`` is a serving loop of its own: prefills and decode steps over an 8-bit pool,
+which count what each key receives, and evictions that keep every request within a budget.
 
 Nothing here computes: every step runs in libpkv's kernels.
 """
@@ -46,7 +51,7 @@ import torch
 from . import _binding as B
 from .workloads import Workload, fill_pool, make_values
 
-__all__ = ["DecodeStep", "ExtendStep"]
+__all__ = ["DecodeStep", "ExtendStep", "BudgetedDecode"]
 
 
 class _ProblemBuffers:
@@ -106,17 +111,72 @@ class _QuantPool:
         return B.make_quant_args(layout, q, self.pool, out, page_size=self.page_size, k_scale=self.k_scale,
                                  v_scale=self.v_scale, **kw)
 
+    def gather(self, r2t, req_pool_idx, seq_lens, max_len, k_out, v_out, cu, err, kv_start):
+        B.pkv_quant_gather(self.pool, r2t, req_pool_idx, seq_lens, max_len, k_out, v_out, cu, err, page_size=self.page_size,
+                           k_scale=self.k_scale, v_scale=self.v_scale, kv_start=kv_start)
+
+    decode_size, extend_size = staticmethod(B.pkv_quant_decode_workspace_size), staticmethod(B.pkv_quant_extend_workspace_size)
+    decode, extend = staticmethod(B.pkv_quant_decode), staticmethod(B.pkv_quant_extend)
+    store_launches = 1
+
+
+class _BytePool:
+    """An 8-bit pool of `slots` slots, empty or filled from bf16 pools [slots, Hkv, D]."""
+
+    def __init__(self, slots, hkv, d, page_size, device):
+        tile = min(page_size, 64)
+        if slots % tile:
+            raise ValueError("the pool's slots must be whole pages")
+        self.page_size, self.kv_heads = page_size, hkv
+        self.pool = torch.zeros((slots // tile, B.pkv_byte_tile_bytes(page_size, d, hkv)), dtype=torch.uint8, device=device)
+        self.workspace = torch.empty(B.pkv_byte_store_workspace_size(slots // tile, page_size), dtype=torch.uint8, device=device)
+
+    @classmethod
+    def of(cls, k_pool, v_pool, page_size, err, scales=None):
+        if scales is not None:
+            raise ValueError("an 8-bit pool has its own scales")
+        slots, hkv, d = k_pool.shape
+        self = cls(slots, hkv, d, page_size, k_pool.device)
+        step = 1 << 20                                # (whole pages)
+        for i in range(0, slots, step):
+            n = min(step, slots - i)
+            self.store(k_pool[i:i + n], v_pool[i:i + n], torch.arange(i, i + n, dtype=torch.int32, device=k_pool.device), err)
+        return self
+
+    def store(self, k_new, v_new, slot_mapping, err):
+        B.pkv_byte_store(self.pool, k_new, v_new, slot_mapping, self.workspace, err, page_size=self.page_size)
+
+    def args(self, layout, q, out, **kw):
+        return B.make_byte_args(layout, q, self.pool, out, page_size=self.page_size, num_kv_heads=self.kv_heads, **kw)
+
+    def gather(self, r2t, req_pool_idx, seq_lens, max_len, k_out, v_out, cu, err, kv_start):
+        B.pkv_byte_gather(self.pool, r2t, req_pool_idx, seq_lens, max_len, k_out, v_out, cu, err, page_size=self.page_size,
+                          kv_start=kv_start)
+
+    decode_size, extend_size = staticmethod(B.pkv_byte_decode_workspace_size), staticmethod(B.pkv_byte_extend_workspace_size)
+    decode, extend = staticmethod(B.pkv_byte_decode), staticmethod(B.pkv_byte_extend)
+    store_launches = 2
+
+
+def _quantised(quant, k_pool, v_pool, page_size, err, scales):
+    """The pool that ``quant`` names, filled from the bf16 ones: None, 4 bits (True or 4) or 8."""
+    if quant not in (False, True, 4, 8):
+        raise ValueError("quant must be False, True, 4 or 8")
+    if not quant:
+        return None
+    return (_BytePool.of if quant == 8 else _QuantPool)(k_pool, v_pool, page_size, err, scales)
+
 
 class DecodeStep:
     def __init__(self, wl: Workload, device="cuda", cross_mode: str = "paged", kv_chunk: int = 0,
                  pools=None, values: Optional[Dict[str, torch.Tensor]] = None, seed: Optional[int] = None,
-                 alloc: bool = False, fused: bool = False, quant: bool = False, scales=None):
+                 alloc: bool = False, fused: bool = False, quant=False, scales=None):
         if cross_mode not in ("paged", "gather"):
             raise ValueError(cross_mode)
         if fused and wl.kind != "gqa":
             raise ValueError("the token-table layout and the fused store are GQA only")
         if quant and wl.kind != "gqa":
-            raise ValueError("the 4-bit pool is GQA only")
+            raise ValueError("a quantised pool is GQA only")
         self.fused = bool(fused)
         self.wl = wl
         self.device = torch.device(device)
@@ -131,7 +191,7 @@ class DecodeStep:
         self.k_pool, self.v_pool = pools
         vals = make_values(wl, seed=seed) if values is None else values
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.quant = _QuantPool(self.k_pool, self.v_pool, ps, self.err, scales) if quant else None
+        self.quant = _quantised(quant, self.k_pool, self.v_pool, ps, self.err, scales)
         if quant:
             del pools
             self.k_pool = self.v_pool = None   # nothing reads the bf16 rows again
@@ -208,8 +268,8 @@ class DecodeStep:
                                              pb.out, page_size=ps, sm_scale=wl.sm_scale, max_seq_len=pb.max_len,
                                              kv_indptr=pb.kv_indptr, kv_indices=pb.kv_indices,
                                              kv_last_page_len=pb.kv_last, lse=pb.lse, kv_chunk=self.kv_chunk)
-            pb.quant = isinstance(pb.args, B.QuantArgs)
-            nbytes = (B.pkv_quant_decode_workspace_size if pb.quant else B.pkv_decode_workspace_size)(pb.args)
+            pb.quant = isinstance(pb.args, (B.QuantArgs, B.ByteArgs))
+            nbytes = (self.quant.decode_size if pb.quant else B.pkv_decode_workspace_size)(pb.args)
             pb.ws_bytes = nbytes
             pb.workspace = torch.empty(max(nbytes, 256), dtype=torch.uint8, device=dev)
 
@@ -292,16 +352,15 @@ class DecodeStep:
     def gather(self, name: str):
         pb = self.problems[name]
         if self.quant is not None:
-            B.pkv_quant_gather(self.quant.pool, self.r2t, self.req_pool_idx, pb.seq_lens, pb.max_len, pb.k_rag, pb.v_rag,
-                               pb.cu, self.err, page_size=self.quant.page_size, k_scale=self.quant.k_scale,
-                               v_scale=self.quant.v_scale, kv_start=pb.kv_start)
+            self.quant.gather(self.r2t, self.req_pool_idx, pb.seq_lens, pb.max_len, pb.k_rag, pb.v_rag, pb.cu, self.err,
+                              pb.kv_start)
             return
         B.pkv_ragged_gather(self.k_pool, self.v_pool, self.r2t, self.req_pool_idx, pb.seq_lens, pb.max_len,
                             pb.k_rag, pb.v_rag, pb.cu, self.err, kv_start=pb.kv_start)
 
     def decode(self, name: str):
         pb = self.problems[name]
-        (B.pkv_quant_decode if pb.quant else B.pkv_decode)(pb.args, pb.workspace, self.err)
+        (self.quant.decode if pb.quant else B.pkv_decode)(pb.args, pb.workspace, self.err)
 
     def run(self):
         """One decode step: (allocation), then for each problem page lists, (store), (gather), attention."""
@@ -323,7 +382,7 @@ class DecodeStep:
             if not self.fused or pb.gather:
                 n += 1                               # gather or build_indices
             if not self.fused or pb.gather or self.quant is not None:
-                n += 1 if pb.spec.stores else 0      # store
+                n += (1 if self.quant is None else self.quant.store_launches) if pb.spec.stores else 0
             # attention (+ merge when requests can split; a 4-bit call without one takes the least workspace)
             n += 1 + (1 if pb.ws_bytes > (256 if pb.quant else 0) else 0)
             n += 1 if pb.quant and self.wl.batch > 1024 else 0   # (the tile table of a large batch)
@@ -360,11 +419,12 @@ class ExtendStep:
 
     With ``token_table=True`` pkv_extend reads the pages straight from req_to_token
     (PKV_LAYOUT_REQ_TO_TOKEN) and the step has no pkv_build_indices launch.  With
-    ``quant=True`` the pool is held in 4 bits (pkv_quant_store, pkv_quant_extend).
+    ``quant=True`` the pool is held in 4 bits (pkv_quant_store, pkv_quant_extend), with
+    ``quant=8`` in 8 (pkv_byte_store, pkv_byte_extend).
     """
 
     def __init__(self, ew, device="cuda", kv_chunk: int = 0, seed: Optional[int] = None, token_table: bool = False,
-                 quant: bool = False, scales=None):
+                 quant=False, scales=None):
         self.token_table = bool(token_table)
         self.ew = ew
         dev = self.device = torch.device(device)
@@ -423,7 +483,7 @@ class ExtendStep:
         self.in_buf = _pack(ins, dev)
         if self.kv_end is not None:
             self.seg = [getattr(self._seg_holder, "s%d" % i) for i in range(len(self.seg))]
-        self.quant = _QuantPool(self.k_pool, self.v_pool, ps, self.err, scales) if quant else None
+        self.quant = _quantised(quant, self.k_pool, self.v_pool, ps, self.err, scales)
         if self.quant is not None:
             self.k_pool = self.v_pool = None   # nothing reads the bf16 rows again
             kw = dict(sm_scale=ew.sm_scale, max_seq_len=int(ew.seq_lens.max()), kv_end=self.kv_end, lse=self.lse,
@@ -446,7 +506,7 @@ class ExtendStep:
                                            page_size=ps, sm_scale=ew.sm_scale, max_seq_len=int(ew.seq_lens.max()),
                                            kv_end=self.kv_end, kv_indptr=self.kv_indptr, kv_indices=self.kv_indices,
                                            kv_last_page_len=self.kv_last, lse=self.lse, kv_chunk=kv_chunk)
-        self.ws_bytes = (B.pkv_quant_extend_workspace_size if quant else B.pkv_extend_workspace_size)(self.args)
+        self.ws_bytes = (self.quant.extend_size if quant else B.pkv_extend_workspace_size)(self.args)
         self.workspace = torch.empty(max(self.ws_bytes, 256), dtype=torch.uint8, device=dev)
 
     def build_indices(self):
@@ -467,7 +527,7 @@ class ExtendStep:
             B.pkv_span_plan(*self.seg, self.plan_qo, self.q_pos, self.kv_end, self.err)
 
     def attend(self):
-        (B.pkv_extend if self.quant is None else B.pkv_quant_extend)(self.args, self.workspace, self.err)
+        (B.pkv_extend if self.quant is None else self.quant.extend)(self.args, self.workspace, self.err)
 
     def run(self):
         self.build_indices()
@@ -482,7 +542,7 @@ class ExtendStep:
             held = int(self.ew.qo_lens.max()) * (self.ew.num_q_heads // self.ew.num_kv_heads) > 128
             n = (2 if self.ws_bytes > 256 else 1) if not held or self.ew.batch > 1 else 0
             n += 2 if held else 0
-            return n + (1 if self.token_table else 2) + (1 if self.kv_end is not None else 0)
+            return n + self.quant.store_launches + (0 if self.token_table else 1) + (1 if self.kv_end is not None else 0)
         return (2 if self.token_table else 3) + (1 if self.kv_end is not None else 0) + (1 if self.ws_bytes > 0 else 0)
 
     def check_errors(self) -> int:
@@ -498,3 +558,91 @@ class ExtendStep:
         self.in_buf.copy_(h_in["inputs"], non_blocking=True)
         self.run()
         h_out["out"].copy_(self.out, non_blocking=True)
+
+
+class BudgetedDecode:
+    """A batch's serving loop over an 8-bit pool, each request within a budget of tokens:
+
+        prefill()  pkv_alloc_extend, pkv_write_req_to_token, pkv_byte_store, pkv_byte_extend, and
+                   pkv_byte_weights of each request's last ``window`` rows
+        step()     the same for one token per request, with pkv_byte_decode, which adds up what
+                   each key receives
+        evict()    pkv_evict: requests above the budget lose the pages that received least, but
+                   none of the first ``keep_first`` and last ``keep_last`` tokens
+
+    Request b has row b of the table ``r2t`` and of ``acc`` (what its keys received so far).  Pages
+    come from one free list and go back to it.  ``width`` bounds a request's tokens between two
+    evictions; positions that are rotated into q and k are the caller's to count, as an eviction
+    makes ``seq_lens`` smaller.  Every buffer stays where it is, so step() and evict() can be captured.
+    """
+
+    def __init__(self, batch, num_q_heads, num_kv_heads, head_dim, page_size, num_pages, width, budget, keep_first=4,
+                 keep_last=64, window=32, sm_scale=None, device="cuda"):
+        dev = self.device = torch.device(device)
+        i32 = lambda v: torch.full((batch,), v, dtype=torch.int32, device=dev)  # noqa: E731
+        self.batch, self.num_q_heads, self.head_dim = batch, num_q_heads, head_dim
+        self.page_size, self.num_pages, self.width, self.window = page_size, num_pages, width, window
+        self.sm_scale = head_dim ** -0.5 if sm_scale is None else sm_scale
+        self.pool = _BytePool(num_pages * page_size, num_kv_heads, head_dim, page_size, dev)
+        self.r2t = torch.zeros((batch, width), dtype=torch.int32, device=dev)
+        self.acc = torch.zeros((batch, width), dtype=torch.float32, device=dev)
+        self.rows = torch.arange(batch, dtype=torch.int32, device=dev)
+        self.seq_lens, self.prefix_lens, self.last_loc = i32(0), i32(0), i32(0)
+        self.budget, self.keep_first, self.keep_last = i32(budget), i32(keep_first), i32(keep_last)
+        self.free_pages = torch.arange(num_pages, dtype=torch.int32, device=dev)
+        self.free_state = torch.tensor([0, num_pages], dtype=torch.int32, device=dev)
+        self.err = torch.zeros(1, dtype=torch.int32, device=dev)
+        self.new_loc = i32(0)
+        self.q = torch.zeros((batch, num_q_heads, head_dim), dtype=torch.bfloat16, device=dev)
+        self.k_new = torch.zeros((batch, num_kv_heads, head_dim), dtype=torch.bfloat16, device=dev)
+        self.v_new = torch.zeros_like(self.k_new)
+        self.out = torch.zeros_like(self.q)
+        self.lse = torch.zeros((batch, num_q_heads), dtype=torch.float32, device=dev)
+        self.args = self._args(self.q, self.out, self.lse, acc_in=self.acc, acc_out=self.acc)
+        self.workspace = torch.empty(B.pkv_byte_decode_workspace_size(self.args), dtype=torch.uint8, device=dev)
+        self.evict_workspace = torch.empty(B.pkv_evict_workspace_size(batch, width, page_size), dtype=torch.uint8, device=dev)
+
+    def _args(self, q, out, lse, **kw):
+        return self.pool.args(B.PKV_LAYOUT_REQ_TO_TOKEN, q, out, sm_scale=self.sm_scale, max_seq_len=self.width, lse=lse,
+                              seq_lens=self.seq_lens, req_to_token=self.r2t, req_pool_idx=self.rows, **kw)
+
+    def _grow(self, new_lens, new_loc, k_new, v_new):
+        """Each request by new_lens [B] tokens: slots, table columns, rows."""
+        self.prefix_lens.copy_(self.seq_lens)
+        self.seq_lens.add_(new_lens)
+        last = (self.prefix_lens - 1).clamp_(min=0).long()
+        self.last_loc.copy_(self.r2t.gather(1, last[:, None])[:, 0])
+        B.pkv_alloc_extend(self.prefix_lens, self.seq_lens, self.last_loc, self.page_size, self.num_pages, self.free_pages,
+                           self.free_state, new_loc, self.err)
+        B.pkv_write_req_to_token(self.r2t, self.rows, self.prefix_lens, self.seq_lens, new_loc, self.err)
+        self.pool.store(k_new, v_new, new_loc, self.err)
+
+    def prefill(self, q, k_new, v_new, new_lens):
+        """new_lens: each request's new tokens (host integers), whose rows q, k_new, v_new hold in order -> out."""
+        total = sum(new_lens)
+        at = np.concatenate([[0], np.cumsum(new_lens)]).astype(np.int32)
+        up = lambda x: torch.from_numpy(np.ascontiguousarray(x)).to(self.device)  # noqa: E731
+        self._grow(up(np.asarray(new_lens, dtype=np.int32)), torch.full((total,), -1, dtype=torch.int32, device=self.device), k_new, v_new)
+        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], dtype=torch.float32, device=self.device)
+        args = self._args(q, out, lse, qo_indptr=up(at), max_q_len=max(new_lens))
+        B.pkv_byte_extend(args, torch.empty(B.pkv_byte_extend_workspace_size(args), dtype=torch.uint8, device=self.device), self.err)
+        seen = [min(n, self.window) for n in new_lens]
+        rows = up(np.concatenate([np.arange(e - n, e) for e, n in zip(at[1:], seen)]))
+        args = self._args(q[rows], None, lse[rows], qo_indptr=up(np.concatenate([[0], np.cumsum(seen)]).astype(np.int32)),
+                          acc_in=self.acc, acc_out=self.acc)
+        B.pkv_byte_weights(args, torch.empty(B.pkv_byte_weights_workspace_size(args), dtype=torch.uint8, device=self.device), self.err)
+        return out
+
+    def step(self):
+        """One token per request, of q, k_new and v_new -> out."""
+        self._grow(1, self.new_loc, self.k_new, self.v_new)
+        B.pkv_byte_decode(self.args, self.workspace, self.err)
+        return self.out
+
+    def evict(self):
+        B.pkv_evict(self.r2t, self.rows, self.seq_lens, self.acc, self.budget, self.free_pages, self.free_state,
+                    self.evict_workspace, self.err, page_size=self.page_size, num_pool_pages=self.num_pages,
+                    max_seq_len=self.width, keep_first=self.keep_first, keep_last=self.keep_last)
+
+    def check_errors(self) -> int:
+        return int(self.err.item())
