@@ -37,24 +37,23 @@ struct Quant8 {
     static constexpr bool kUnits = true, kHeldBf16V = true;
     static constexpr const char *kExtend = "pkv_byte_extend";
     // A stage: the codes of a 64-slot tile, or of four 16-slot ones (kT = 16), as they lie; kT = 0 (other
-    // tiles): K codes [64][D], V codes [64][D].  Behind them the scales: 16 bytes of a piece with
-    // its own two among them, 4 where kT is 0.
-    static constexpr int kCodes = 128 * D;
-    static constexpr uint32_t kStageBytes = kCodes + 256;
-    static constexpr int warps(int) { return D == 128 ? 6 : 12; }
+    // tiles): K codes [64][D], V codes [64][D].  In each line of 128 bytes the eight 16-byte chunks
+    // are swapped about, chunk x ^ (line % 8), by the tensor copies or by the lanes that copy: the keys that eight
+    // lanes read at a time lie a line apart or more, and so in different banks.  Behind them the
+    // scales: 16 bytes of a piece with its own two among them, 4 where kT is 0.
+    static constexpr int kCodes = 128 * D, kAlign = 1024;
+    static constexpr uint32_t kStageBytes = kCodes + 1024;
+    static constexpr int warps(int) { return D == 128 ? 6 : 11; }
     static constexpr int stages(int) { return 2; }
     template <int NT>
     using State = State8<D, NT>;
 
     // (copied 16 bytes per lane)
     __device__ __forceinline__ static bool gathers(int) { return kT == 0; }
+    // A piece: its address, or where it is copied as a box (kT != 0) its tile, counted from 1.
     __device__ __forceinline__ static const uint8_t *piece(const Params &p, int slot, int kh) {
+        if (kT != 0) return reinterpret_cast<const uint8_t *>(static_cast<uintptr_t>((slot >> p.t_shift) + 1));
         return p.pool + static_cast<int64_t>(slot >> p.t_shift) * p.tile_stride + (static_cast<int64_t>(kh) * 2 * D << p.t_shift);
-    }
-    // The scale bytes of the tile whose piece of kv head kh is at `a`, in whole units of kUnit bytes.
-    template <int kUnit>
-    __device__ __forceinline__ static const uint8_t *scales(const Params &p, const uint8_t *a, int kh) {
-        return a + (static_cast<int64_t>(p.hkv - kh) * 2 * D << p.t_shift) + (2 * kh & ~(kUnit - 1));
     }
     __device__ __forceinline__ static void zero_piece(uint8_t *stage, int j, int ps) {
         const int t = 1 << ps;
@@ -64,10 +63,9 @@ struct Quant8 {
             for (int o = 0; o < 4; ++o) reinterpret_cast<uint32_t *>(stage + kCodes + j * 16)[o] = 0x01010101u;
             return;
         }
-        for (int part = 0; part < 2; ++part) {
-            uint32_t *w = reinterpret_cast<uint32_t *>(stage + part * 64 * D + j * t * D);
-            for (int o = 0; o < t * D / 4; ++o) w[o] = 0;
-        }
+        for (int part = 0; part < 2; ++part)
+            for (int o = 0; o < t * D; o += 16)
+                *reinterpret_cast<uint4 *>(stage + part * 64 * D + swapped(j * t * D + o)) = make_uint4(0, 0, 0, 0);
         reinterpret_cast<uint32_t *>(stage + kCodes)[j] = 0x01010101u;
     }
     // Copies a tile's n pieces, `live` of them on good pages; piece i of the window is lane i % 32's src[i / 32].
@@ -81,8 +79,9 @@ struct Quant8 {
             for (int i = 0; i < 2; ++i) {
                 const int j = 32 * i + lane - first;
                 if (j >= 0 && j < n && src[i]) {
-                    bulk_load(stage + j * bytes, src[i], bytes, bar);
-                    bulk_load(stage + kCodes + j * 16, scales<16>(p, src[i], kh), 16, bar);
+                    const int tile = static_cast<int>(reinterpret_cast<uintptr_t>(src[i])) - 1;
+                    tma_load_3d(stage + j * bytes, &p.map, 0, kh * (2 * kT * D / 128), tile, bar);
+                    bulk_load(stage + kCodes + j * 16, p.pool + tile * p.tile_stride + static_cast<int64_t>(p.hkv) * bytes + (2 * kh & ~15), 16, bar);
                 }
             }
             return;
@@ -96,22 +95,31 @@ struct Quant8 {
             const uint8_t *a = from_lane(ps == 0 && i >= kRounds / 2 ? src[1] : low, (at + j) & 31);
             if (!a) continue;
             a += (row & ((1 << ps) - 1)) * D + c * 16;
-            cp_async_16(stage + row * D + c * 16, a, 16);
-            cp_async_16(stage + 64 * D + row * D + c * 16, a + (D << ps), 16);
+            uint8_t *dst = stage + swapped(row * D + c * 16);
+            cp_async_16(dst, a, 16);
+            cp_async_16(dst + 64 * D, a + (D << ps), 16);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int j = 32 * i + lane - first;
-            if (j >= 0 && j < (64 >> ps) && src[i]) cp_async_small<4>(stage + kCodes + j * 4, scales<4>(p, src[i], kh));
+            if (j >= 0 && j < (64 >> ps) && src[i]) {
+                const uint8_t *a = src[i] + (static_cast<int64_t>(p.hkv - kh) * 2 * D << ps) + (2 * kh & ~3);
+                cp_async_small<4>(stage + kCodes + j * 4, a);
+            }
         }
         arrive_with_copies(bar);
     }
 
-    // Where key k of the 16-key group kt of half `step` lies: its codes (part 0 = K, 1 = V) and its two scale bytes.
-    __device__ __forceinline__ static const uint8_t *codes(const uint8_t *stage, int step, int part, int kt, int k) {
-        if (kT == 16) return stage + (step * kGroups + kt) * (32 * D) + part * (16 * D) + k * D;
-        return stage + part * (64 * D) + (step * kStep + kt * 16 + k) * D;
+    // Where byte `at` of a run of lines that begins on a multiple of 1024 is.
+    __device__ __forceinline__ static int swapped(int at) { return at ^ ((at >> 3) & 0x70); }
+    // Byte `at` of the codes (part 0 = K, 1 = V) of key k of the 16-key group kt of half `step`.  (The
+    // groups begin on multiples of 1024, so the swap is a lane's own.)
+    __device__ __forceinline__ static const uint8_t *codes(const uint8_t *stage, int step, int part, int kt, int k, int at) {
+        const uint8_t *group = kT == 16 ? stage + (step * kGroups + kt) * (32 * D) + part * (16 * D)
+                                        : stage + part * (64 * D) + (step * kStep + kt * 16) * D;
+        return group + swapped(k * D + at);
     }
+    // Its two scale bytes.
     __device__ __forceinline__ static uint32_t scale_bytes(const Params &p, const uint8_t *stage, int step, int kt, int k, int kh) {
         const int at = kT == 64 ? (2 * kh & 15) : kT == 16 ? (step * kGroups + kt) * 16 + (2 * kh & 15)
                                 : ((step * kStep + kt * 16 + k) >> p.t_shift) * 4 + (2 * kh & 3);
@@ -132,10 +140,9 @@ struct Quant8 {
         for (int kt = 0; kt < kGroups; ++kt)
 #pragma unroll
             for (int u = 0; u < 2; ++u) {
-                const uint4 *cp = reinterpret_cast<const uint4 *>(codes(stage, step, 0, kt, r + 8 * u) + c * (D / 4));
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i) {
-                    const uint4 x = cp[i];
+                    const uint4 x = *reinterpret_cast<const uint4 *>(codes(stage, step, 0, kt, r + 8 * u, c * (D / 4) + 16 * i));
                     w[kt][u][4 * i] = x.x; w[kt][u][4 * i + 1] = x.y; w[kt][u][4 * i + 2] = x.z; w[kt][u][4 * i + 3] = x.w;
                 }
                 const uint32_t e = scale_bytes(p, stage, step, kt, r + 8 * u, kh);
@@ -252,7 +259,7 @@ struct Quant8 {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int k = 2 * c + e + 8 * u;
-                    const uint8_t *cp = codes(stage, step, 1, kt, k) + r * (D / 8);
+                    const uint8_t *cp = codes(stage, step, 1, kt, k, r * (D / 8));
                     if (D == 128) {
                         const uint4 y = *reinterpret_cast<const uint4 *>(cp);
                         x[e][0] = y.x; x[e][1] = y.y; x[e][D / 32 - 2] = y.z; x[e][D / 32 - 1] = y.w;
@@ -290,7 +297,7 @@ struct Quant8 {
                 for (int k = 0; k < 16; ++k) {
                     const int key = key0 + kt * 16 + k;
                     if (key >= keys) continue;
-                    const uint8_t *cp = codes(stage, step, 1, kt, k) + r * (D / 8);
+                    const uint8_t *cp = codes(stage, step, 1, kt, k, r * (D / 8));
 #pragma unroll
                     for (int t = 0; t < KS; ++t)
 #pragma unroll
@@ -591,24 +598,52 @@ __global__ void __launch_bounds__(256) add_kernel(const Params p, const WeighPar
     wp.acc_out[at] = wp.acc_in ? wp.acc_in[at] + x : x;
 }
 
-// The same from a decode's logits: acc_out = acc_in + sum over heads of 2^(logit - lse2).
+// The same from a decode's logits: acc_out = acc_in + sum over heads of 2^(logit - lse2).  A thread
+// has four keys and every fourth head, whose loads are all on their way before the first is used.
+constexpr int kFinishKeys = 256;
 __global__ void __launch_bounds__(256) finish_kernel(const Params p, const WeighParams wp) {
-    extern __shared__ float lse_s[];
+    __shared__ float4 sums[4][kFinishKeys / 4];
     pdl_wait();          // the logits
     pdl_launch_next();
-    const int b = blockIdx.y, key = blockIdx.x * 256 + threadIdx.x;
+    const int b = blockIdx.y, quad = threadIdx.x & 63, group = threadIdx.x >> 6, key0 = blockIdx.x * kFinishKeys;
     int64_t base;
     const int L = quant::key_count(p.tab, b, base, p.err, false);
-    if (static_cast<int>(blockIdx.x) * 256 >= L) return;
-    for (int h = threadIdx.x; h < p.hq; h += 256) lse_s[h] = wp.lse[static_cast<int64_t>(b) * p.hq + h] * kLog2e;
+    if (key0 >= L) return;
+    const int64_t row = p.tab.req_pool_idx[b], first = row * wp.acc_stride + (p.tab.kv_start ? p.tab.kv_start[b] : 0);
+    const int mine = key0 + threadIdx.x;
+    const float before = wp.acc_in && mine < L ? wp.acc_in[first + mine] : 0.f;
+    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (key0 + 4 * quad < L) {   // (a row of logits is whole 8 floats; what lies behind L is dropped below)
+        const float *y = p.logits + static_cast<int64_t>(b) * p.hq * p.logit_stride + key0 + 4 * quad;
+        const float *lse = wp.lse + static_cast<int64_t>(b) * p.hq;
+        for (int h0 = group; h0 < p.hq; h0 += 32) {
+            float4 v[8];
+            float l[8];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int h = h0 + 4 * i;
+                v[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+                l[i] = 0.f;
+                if (h < p.hq) {
+                    v[i] = __ldcs(reinterpret_cast<const float4 *>(y + h * p.logit_stride));
+                    l[i] = __ldg(lse + h);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float m = l[i] * kLog2e;
+                x.x += ex2(v[i].x - m);
+                x.y += ex2(v[i].y - m);
+                x.z += ex2(v[i].z - m);
+                x.w += ex2(v[i].w - m);
+            }
+        }
+    }
+    sums[group][quad] = x;
     __syncthreads();
-    if (key >= L) return;
-    const int64_t row = p.tab.req_pool_idx[b], at = row * wp.acc_stride + (p.tab.kv_start ? p.tab.kv_start[b] : 0) + key;
-    const float *y = p.logits + static_cast<int64_t>(b) * p.hq * p.logit_stride + key;
-    float x = 0.f;
-#pragma unroll 16
-    for (int h = 0; h < p.hq; ++h) x += ex2(__ldcs(y + h * p.logit_stride) - lse_s[h]);
-    wp.acc_out[at] = wp.acc_in ? wp.acc_in[at] + x : x;
+    if (mine >= L) return;
+    const float *s = reinterpret_cast<const float *>(sums) + threadIdx.x;
+    wp.acc_out[first + mine] = before + ((s[0] + s[kFinishKeys]) + (s[2 * kFinishKeys] + s[3 * kFinishKeys]));
 }
 
 // ---------------------------------------------------------------- host side
@@ -630,7 +665,7 @@ pkv_status check(const pkv_byte_args *a, Call call, bool check_ptrs) {
     if (call == kWeights || a->acc_out) {
         if (a->layout != PKV_LAYOUT_REQ_TO_TOKEN) return fail(PKV_ERR_UNSUPPORTED, "%s: weights need the token-table layout", who);
         if (a->acc_row_stride < a->r2t_width) return fail(PKV_ERR_INVALID_ARG, "%s: acc_row_stride smaller than the table's width", who);
-        if (a->batch > 65535 || a->num_q_heads > 8192) return fail(PKV_ERR_UNSUPPORTED, "%s: weights of more than 65535 requests or 8192 query heads", who);
+        if (a->batch > 65535 || a->num_kv_heads > 65535) return fail(PKV_ERR_UNSUPPORTED, "%s: weights of more than 65535 requests or kv heads", who);
     }
     if (call == kWeights && check_ptrs && a->batch > 0 && (!a->lse || !a->acc_out))
         return fail(PKV_ERR_INVALID_ARG, "%s: null lse/acc_out", who);
@@ -674,6 +709,16 @@ size_t size_of(const pkv_byte_args *a, Call call) {
     return n + w.part + w.lse;
 }
 
+// The map of a pool whose pieces are copied as boxes.
+bool encode_pool(const pkv_byte_args *a, Params &p) {
+    if (p.t_shift != 6 && p.t_shift != 4) return true;
+    const uint32_t lines = static_cast<uint32_t>((2 * a->head_dim << p.t_shift) / 128);
+    const uint64_t dims[3] = {64, static_cast<uint64_t>(a->num_kv_heads) * lines, static_cast<uint64_t>(std::max<int64_t>(1, a->num_tiles))};
+    const uint64_t strides[2] = {128, static_cast<uint64_t>(a->tile_stride)};
+    const uint32_t box[3] = {64, lines, 1};
+    return encode_tmap_bf16(&p.map, a->pool, 3, dims, strides, box);   // (pairs of bytes)
+}
+
 pkv_status run(const pkv_byte_args *a, Call call, void *ws, size_t ws_bytes, int32_t *err, cudaStream_t s) {
     const char *who = kNames[call];
     if (!a) return fail(PKV_ERR_INVALID_ARG, "%s: null args", who);
@@ -690,6 +735,7 @@ pkv_status run(const pkv_byte_args *a, Call call, void *ws, size_t ws_bytes, int
     if (call == kWeights) return weigh(who, a, p, a->lse, reinterpret_cast<float *>(at), s);
     Plan pl;
     if (!make_plan(a, call == kExtend, shape_of(a), pl)) return fail(PKV_ERR_UNSUPPORTED, "%s: too many splits, keys or requests", who);
+    if ((pl.unit || pl.spans) && !encode_pool(a, p)) return fail(PKV_ERR_CUDA, "%s: cuTensorMapEncodeTiled rejected the pool", who);
     if (!a->acc_out) return attend<Quant8>(who, a, pl, p, at, s);
     if (a->max_seq_len == 0) return attend<Quant8>(who, a, pl, p, at, s);
     const WeighPlan w = weigh_plan(a, call);
@@ -700,8 +746,8 @@ pkv_status run(const pkv_byte_args *a, Call call, void *ws, size_t ws_bytes, int
     st = attend<Quant8>(who, a, pl, p, at + w.part + w.lse, s);
     if (st != PKV_OK) return st;
     const WeighParams wp{q.lse, nullptr, a->acc_in, a->acc_out, a->acc_row_stride};
-    return launch_status(launch_chained(finish_kernel, dim3((static_cast<unsigned>(a->max_seq_len) + 255) / 256, static_cast<unsigned>(a->batch)),
-                                        dim3(256), static_cast<size_t>(a->num_q_heads) * 4, s, q, wp), who);
+    return launch_status(launch_chained(finish_kernel, dim3((static_cast<unsigned>(a->max_seq_len) + kFinishKeys - 1) / kFinishKeys,
+                                                            static_cast<unsigned>(a->batch)), dim3(256), 0, s, q, wp), who);
 }
 
 }  // namespace

@@ -297,16 +297,28 @@ __global__ void __launch_bounds__(T) move_kernel(const Params p) {
             gone += sum_before(&gone_s, rank);
         }
         int32_t *out = a.free_pages + head - all + low;
-        for (int i = i0 + lane; i < i1 + lane; i += 32) {
-            const uint32_t k = i < i1 ? keys[i] : 0xffffffffu;
-            const uint32_t eq = __ballot_sync(0xffffffffu, i < i1 && k == border);
-            const bool goes = i < i1 && (k < border || (k == border && (ties <= want || tie + __popc(eq & lower) >= stay)));
-            const uint32_t g = __ballot_sync(0xffffffffu, goes);
-            const int at = gone + __popc(g & lower);
-            if (goes) out[at] = a.req_to_token[f.r2t + (static_cast<int64_t>(lo + i) << p.ps_shift)] >> p.ps_shift;
-            if (i < i1) places[lo + i] = goes ? 0xffffffffu : static_cast<uint32_t>(lo + i - at);
-            gone += __popc(g);
-            tie += __popc(eq);
+        const int32_t *table = a.req_to_token + f.r2t + (static_cast<int64_t>(lo) << p.ps_shift);
+        constexpr int kAhead = 8;   // table entries on their way before any place is written
+        for (int j0 = i0; j0 < i1; j0 += 32 * kAhead) {
+            int32_t slot[kAhead];
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int i = j0 + 32 * j + lane;
+                slot[j] = i < i1 ? table[static_cast<int64_t>(i) << p.ps_shift] : 0;
+            }
+#pragma unroll
+            for (int j = 0; j < kAhead; ++j) {
+                const int i = j0 + 32 * j + lane;
+                const uint32_t k = i < i1 ? keys[i] : 0xffffffffu;
+                const uint32_t eq = __ballot_sync(0xffffffffu, i < i1 && k == border);
+                const bool goes = i < i1 && (k < border || (k == border && (ties <= want || tie + __popc(eq & lower) >= stay)));
+                const uint32_t g = __ballot_sync(0xffffffffu, goes);
+                const int at = gone + __popc(g & lower);
+                if (goes) out[at] = slot[j] >> p.ps_shift;
+                if (i < i1) places[lo + i] = goes ? 0xffffffffu : static_cast<uint32_t>(lo + i - at);
+                gone += __popc(g);
+                tie += __popc(eq);
+            }
         }
         sync_all(size);   // all places are known to the cluster
     }

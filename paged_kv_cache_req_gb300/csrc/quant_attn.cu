@@ -380,6 +380,7 @@ template <int D, int kT_>
 struct Quant4 {
     static constexpr int kDim = D, kT = kT_;
     static constexpr bool kUnits = false, kHeldBf16V = false;
+    static constexpr int kAlign = 128;
     static constexpr const char *kExtend = "pkv_quant_extend";
     static constexpr uint32_t kStageBytes = quant::tile_bytes(kTile, D);
     static constexpr int warps(int nt) { return warps_per_sm(D, nt); }

@@ -34,6 +34,12 @@ constexpr float kLn2 = 0.69314718055994531f, kLog2e = 1.44269504088896341f;
 // past 2^8 only, with a lift of 7: 76.5 us for 77.1 at 64 requests x 4 rows x up to 16384 keys, 79.3 for 81.4
 // with scores four times as far apart; one row per request the same.)
 constexpr float kLazy = 4.f, kLift = 11.f;
+// Dynamic shared memory from the next multiple of kAlign on (formats that need more than 128 get the room).
+template <int kAlign>
+__device__ __forceinline__ uint8_t *aligned_smem(uint8_t *raw) {
+    return kAlign <= 128 ? raw : raw + (kAlign - (smem_u32(raw) & (kAlign - 1)) & (kAlign - 1));
+}
+
 constexpr float kNoUnit = -1000.f;   // log2 of the unit of a sum that holds nothing yet
 // 2^e of an integer e >= -126 as a float (0 below, infinity above 127).
 __device__ __forceinline__ float power_of_two(float e) {
@@ -41,6 +47,7 @@ __device__ __forceinline__ float power_of_two(float e) {
 }
 
 struct Params {
+    CUtensorMap map;         // formats that copy pieces as tensor boxes: the pool as [tiles][lines of 128 bytes]
     Table tab;
     int32_t batch, hq, hkv, g, t_shift;
     uint32_t g_magic;        // ceil(2^32 / g), for g > 1
@@ -555,15 +562,16 @@ __device__ __forceinline__ void start_segment(const Params &p, const Work &s, St
 }
 
 template <class F, int NT>
-__global__ void __launch_bounds__(F::warps(NT) * 32, 1) attend_kernel(const Params p) {
+__global__ void __launch_bounds__(F::warps(NT) * 32, 1) attend_kernel(const __grid_constant__ Params p) {
     constexpr int D = F::kDim, kWarps = F::warps(NT), kThreads = kWarps * 32;
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[kWarps * F::stages(NT)];
     __shared__ long long scratch[kWarps];
     __shared__ __align__(16) Work queues[kWarps][kQueue];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     constexpr uint32_t stage_bytes = F::kStageBytes;
     constexpr int S = F::stages(NT);
+    uint8_t *smem = aligned_smem<F::kAlign>(smem_raw);
     uint8_t *ring = smem + static_cast<uint32_t>(warp * S) * stage_bytes;
     uint64_t *bar = bars + warp * S;
     if (lane == 0) {
@@ -671,15 +679,16 @@ __global__ void __launch_bounds__(F::warps(NT) * 32, 1) attend_kernel(const Para
 // with more work the spans' even shares win.
 // kRows: query rows by qo_indptr; else one per request (known to the compiler, 0.4 us of 7).
 template <class F, int NT, bool kRows>
-__global__ void __launch_bounds__(F::warps(NT) * 32, 1) unit_kernel(const Params p) {
+__global__ void __launch_bounds__(F::warps(NT) * 32, 1) unit_kernel(const __grid_constant__ Params p) {
     constexpr int D = F::kDim, kWarps = F::warps(NT), S = F::stages(NT);
-    extern __shared__ __align__(128) uint8_t smem[];
+    extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[kWarps * S];
     __shared__ float2 ml[kWarps][8 * NT];
     __shared__ float unit_of[kWarps];   // log2 of the unit of a warp's sums (formats with one)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const int shift = F::kT == 64 ? 6 : F::kT == 16 ? 4 : p.t_shift, pieces = 64 >> shift;
     constexpr uint32_t stage_bytes = F::kStageBytes;
+    uint8_t *smem = aligned_smem<F::kAlign>(smem_raw);
     uint8_t *ring = smem + static_cast<uint32_t>(warp * S) * stage_bytes;
     uint64_t *bar = bars + warp * S;
     if (lane == 0) {
@@ -1069,13 +1078,13 @@ __global__ void __launch_bounds__(kHoldThreads, kHoldCtas) hold_kernel(const Par
 // What the plan has to know of a format at a head_dim and page size.
 struct Shape {
     int warps[2], stages[2];   // at NT = 1 and 2
-    size_t stage;              // bytes of a stage
+    size_t stage, slack;       // bytes of a stage; for the alignment of the first one
     bool units;                // sums have a unit
     int64_t tile;              // bytes of a pool tile
 };
 template <class F>
 static Shape shape(int64_t tile) {
-    return Shape{{F::warps(1), F::warps(2)}, {F::stages(1), F::stages(2)}, F::kStageBytes, F::kUnits, tile};
+    return Shape{{F::warps(1), F::warps(2)}, {F::stages(1), F::stages(2)}, F::kStageBytes, F::kAlign > 128 ? F::kAlign : 0, F::kUnits, tile};
 }
 
 // (`needs_out`: the call writes the attention's output)
@@ -1210,7 +1219,7 @@ static bool make_plan(const A *a, bool extend, const Shape &f, Plan &pl) {
         pl.nt = rows <= 8 ? 1 : 2;
         pl.grid = dim3(static_cast<unsigned>(batch), static_cast<unsigned>(a->num_kv_heads),
                        static_cast<unsigned>((rows + 8 * pl.nt - 1) / (8 * pl.nt)));
-        pl.smem = static_cast<size_t>(f.warps[pl.nt - 1] * f.stages[pl.nt - 1]) * f.stage;
+        pl.smem = static_cast<size_t>(f.warps[pl.nt - 1] * f.stages[pl.nt - 1]) * f.stage + f.slack;
     }
     if (pl.spans) {
         const int64_t few = pl.held ? kHeldRows : rows;
@@ -1218,7 +1227,7 @@ static bool make_plan(const A *a, bool extend, const Shape &f, Plan &pl) {
         const int warps = f.warps[pl.nt - 1];
         pl.grid = dim3(static_cast<unsigned>(sms));
         pl.plan_launch = a->batch > kTableInSmem;
-        pl.smem = static_cast<size_t>(warps * f.stages[pl.nt - 1]) * f.stage;
+        pl.smem = static_cast<size_t>(warps * f.stages[pl.nt - 1]) * f.stage + f.slack;
         if (!pl.plan_launch) pl.smem += (static_cast<size_t>(a->batch) + 2) * 4 + (a->batch <= kReqInSmem ? a->batch * sizeof(Req) : 0);
         int64_t spans = sms * warps;
         // all units' tiles, at most (beside held keys the requests with few rows only)
