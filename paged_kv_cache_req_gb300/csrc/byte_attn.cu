@@ -31,20 +31,22 @@ struct State8 : qattn::State<D, NT> {
 // 2^d of an integer d <= 0 (0 below the normal numbers).
 __device__ __forceinline__ float down_by(float d) { return __int_as_float(max(0, static_cast<int>(d) + 127) << 23); }
 
-template <int D, int kT_>
+template <int D, int kT_, int kNT>
 struct Quant8 {
     static constexpr int kDim = D, kT = kT_;
     static constexpr bool kUnits = true, kHeldBf16V = true;
     static constexpr const char *kExtend = "pkv_byte_extend";
-    // A stage: the codes of a 64-slot tile, or of four 16-slot ones (kT = 16), as they lie; kT = 0 (other
-    // tiles): K codes [64][D], V codes [64][D].  In each line of 128 bytes the eight 16-byte chunks
-    // are swapped about, chunk x ^ (line % 8), by the tensor copies or by the lanes that copy: the keys that eight
-    // lanes read at a time lie a line apart or more, and so in different banks.  Behind them the
-    // scales: 16 bytes of a piece with its own two among them, 4 where kT is 0.
-    static constexpr int kCodes = 128 * D, kAlign = 1024;
-    static constexpr uint32_t kStageBytes = kCodes + 1024;
-    static constexpr int warps(int) { return D == 128 ? 6 : 11; }
-    static constexpr int stages(int) { return 2; }
+    // A stage is a tile of 64 keys, or of 32 (D = 128 and 16 rows, whose math takes so long that 8 warps are
+    // needed): K codes [keys][D], V codes [keys][D], or of pools of 16-slot tiles (kT = 16) those as they
+    // lie.  In each line of 128 bytes the eight 16-byte chunks are swapped about, chunk x ^ (line %
+    // 8), by the tensor copies or by the lanes that copy: the keys that eight lanes read at a time lie a
+    // line apart or more, and so in different banks.  Beside it the scales: 16 bytes of a piece with its
+    // own two among them, 4 where kT is 0.
+    static constexpr int kKeys = D == 128 && kNT == 2 ? 32 : 64, kAlign = 1024, kAux = 256;
+    static constexpr uint32_t kStageBytes = 2 * kKeys * D;
+    static constexpr int kLines = kT == 64 && kKeys == 64 ? D : D / 4;   // of the box that one tensor copy brings
+    static constexpr int warps(int nt) { return D == 64 ? 12 : nt == 2 ? 8 : 6; }
+    static constexpr int stages(int nt) { return D == 128 && nt == 2 ? 3 : 2; }
     template <int NT>
     using State = State8<D, NT>;
 
@@ -55,56 +57,64 @@ struct Quant8 {
         if (kT != 0) return reinterpret_cast<const uint8_t *>(static_cast<uintptr_t>((slot >> p.t_shift) + 1));
         return p.pool + static_cast<int64_t>(slot >> p.t_shift) * p.tile_stride + (static_cast<int64_t>(kh) * 2 * D << p.t_shift);
     }
-    __device__ __forceinline__ static void zero_piece(uint8_t *stage, int j, int ps) {
+    __device__ __forceinline__ static void zero_piece(const Stage &stage, int j, int ps) {
         const int t = 1 << ps;
         if (kT != 0) {
-            uint32_t *w = reinterpret_cast<uint32_t *>(stage + j * 2 * kT * D);
-            for (int o = 0; o < kT * D / 2; ++o) w[o] = 0;
-            for (int o = 0; o < 4; ++o) reinterpret_cast<uint32_t *>(stage + kCodes + j * 16)[o] = 0x01010101u;
+            constexpr int kBytes = 2 * (kT > kKeys ? kKeys : kT) * D;
+            uint32_t *w = reinterpret_cast<uint32_t *>(stage.codes + j * kBytes);
+            for (int o = 0; o < kBytes / 4; ++o) w[o] = 0;
+            for (int o = 0; o < 4; ++o) reinterpret_cast<uint32_t *>(stage.aux + j * 16)[o] = 0x01010101u;
             return;
         }
         for (int part = 0; part < 2; ++part)
             for (int o = 0; o < t * D; o += 16)
-                *reinterpret_cast<uint4 *>(stage + part * 64 * D + swapped(j * t * D + o)) = make_uint4(0, 0, 0, 0);
-        reinterpret_cast<uint32_t *>(stage + kCodes)[j] = 0x01010101u;
+                *reinterpret_cast<uint4 *>(stage.codes + part * kKeys * D + swapped(j * t * D + o)) = make_uint4(0, 0, 0, 0);
+        reinterpret_cast<uint32_t *>(stage.aux)[j] = 0x01010101u;
     }
-    // Copies a tile's n pieces, `live` of them on good pages; piece i of the window is lane i % 32's src[i / 32].
+    // Copies a tile's n pieces (from key `half` of a larger one on), `live` of them on good pages; piece i of
+    // the window is lane i % 32's src[i / 32].
     __device__ __forceinline__ static void copy(const Params &p, int kh, const uint8_t *const (&src)[2], int first, int n,
-                                                uint32_t live, int ps, uint8_t *stage, uint64_t *bar, int lane) {
-        if (kT != 0) {
-            constexpr uint32_t bytes = 2 * kT * D;
-            if (lane == (first & 31)) mbar_arrive_expect_tx(bar, live * (bytes + 16));
+                                                uint32_t live, int ps, int half, const Stage &stage, uint64_t *bar, int lane) {
+        if constexpr (kT != 0) {
+            constexpr uint32_t kBytes = 2 * (kT > kKeys ? kKeys : kT) * D;
+            if (lane == (first & 31)) mbar_arrive_expect_tx(bar, live * (kBytes + 16));
             if (kT != 64) __syncwarp();   // (with one piece the same lane copies)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int j = 32 * i + lane - first;
                 if (j >= 0 && j < n && src[i]) {
-                    const int tile = static_cast<int>(reinterpret_cast<uintptr_t>(src[i])) - 1;
-                    tma_load_3d(stage + j * bytes, &p.map, 0, kh * (2 * kT * D / 128), tile, bar);
-                    bulk_load(stage + kCodes + j * 16, p.pool + tile * p.tile_stride + static_cast<int64_t>(p.hkv) * bytes + (2 * kh & ~15), 16, bar);
+                    const int tile = static_cast<int>(reinterpret_cast<uintptr_t>(src[i])) - 1, line = kh * (2 * kT * D / 128);
+                    if (kT > kKeys) {   // K's half of the tile, and V's
+                        tma_load_3d(stage.codes, &p.map, 0, line + half * D / 128, tile, bar);
+                        tma_load_3d(stage.codes + kKeys * D, &p.map, 0, line + (kT + half) * D / 128, tile, bar);
+                    } else {
+                        tma_load_3d(stage.codes + j * kBytes, &p.map, 0, line, tile, bar);
+                    }
+                    static_assert(kLines * 128 == (kT > kKeys ? kBytes / 2 : kBytes), "a box is what one copy brings");
+                    bulk_load(stage.aux + j * 16, p.pool + tile * p.tile_stride + static_cast<int64_t>(p.hkv) * 2 * kT * D + (2 * kh & ~15), 16, bar);
                 }
             }
             return;
         }
-        constexpr int kRow = D / 16, kRounds = 64 * kRow / 32;   // 16 bytes per lane; rounds for K (and V)
-        const uint8_t *low = first < 32 ? src[0] : src[1];       // (only 64 pieces lie in both)
+        constexpr int kRow = D / 16, kRounds = kKeys * kRow / 32;   // 16 bytes per lane; rounds for K (and V)
+        const uint8_t *low = first < 32 ? src[0] : src[1];          // (only 64 pieces lie in both)
         const int at = first & 31, c = lane % kRow;
 #pragma unroll 8
         for (int i = 0; i < kRounds; ++i) {
             const int row = i * (32 / kRow) + lane / kRow, j = row >> ps;
-            const uint8_t *a = from_lane(ps == 0 && i >= kRounds / 2 ? src[1] : low, (at + j) & 31);
+            const uint8_t *a = from_lane(kKeys == 64 && ps == 0 && i >= kRounds / 2 ? src[1] : low, (at + j) & 31);
             if (!a) continue;
             a += (row & ((1 << ps) - 1)) * D + c * 16;
-            uint8_t *dst = stage + swapped(row * D + c * 16);
+            uint8_t *dst = stage.codes + swapped(row * D + c * 16);
             cp_async_16(dst, a, 16);
-            cp_async_16(dst + 64 * D, a + (D << ps), 16);
+            cp_async_16(dst + kKeys * D, a + (D << ps), 16);
         }
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int j = 32 * i + lane - first;
-            if (j >= 0 && j < (64 >> ps) && src[i]) {
+            if (j >= 0 && j < (kKeys >> ps) && src[i]) {
                 const uint8_t *a = src[i] + (static_cast<int64_t>(p.hkv - kh) * 2 * D << ps) + (2 * kh & ~3);
-                cp_async_small<4>(stage + kCodes + j * 4, a);
+                cp_async_small<4>(stage.aux + j * 4, a);
             }
         }
         arrive_with_copies(bar);
@@ -112,25 +122,24 @@ struct Quant8 {
 
     // Where byte `at` of a run of lines that begins on a multiple of 1024 is.
     __device__ __forceinline__ static int swapped(int at) { return at ^ ((at >> 3) & 0x70); }
-    // Byte `at` of the codes (part 0 = K, 1 = V) of key k of the 16-key group kt of half `step`.  (The
-    // groups begin on multiples of 1024, so the swap is a lane's own.)
-    __device__ __forceinline__ static const uint8_t *codes(const uint8_t *stage, int step, int part, int kt, int k, int at) {
-        const uint8_t *group = kT == 16 ? stage + (step * kGroups + kt) * (32 * D) + part * (16 * D)
-                                        : stage + part * (64 * D) + (step * kStep + kt * 16) * D;
-        return group + swapped(k * D + at);
+    // Byte `at` of the codes (part 0 = K, 1 = V) of key k of the 16-key group kt of the stage's `step`-th 32 keys.
+    // (The groups begin on multiples of 1024, so the swap is a lane's own.)
+    __device__ __forceinline__ static const uint8_t *codes(const Stage &stage, int step, int part, int kt, int k, int at) {
+        const int group = step * kGroups + kt;
+        return stage.codes + (kT == 16 ? group * (32 * D) + part * (16 * D) : part * (kKeys * D) + group * (16 * D)) + swapped(k * D + at);
     }
     // Its two scale bytes.
-    __device__ __forceinline__ static uint32_t scale_bytes(const Params &p, const uint8_t *stage, int step, int kt, int k, int kh) {
-        const int at = kT == 64 ? (2 * kh & 15) : kT == 16 ? (step * kGroups + kt) * 16 + (2 * kh & 15)
-                                : ((step * kStep + kt * 16 + k) >> p.t_shift) * 4 + (2 * kh & 3);
-        return *reinterpret_cast<const uint16_t *>(stage + kCodes + at);
+    __device__ __forceinline__ static uint32_t scale_bytes(const Params &p, const Stage &stage, int step, int kt, int k, int kh) {
+        const int group = step * kGroups + kt;
+        const int at = kT == 64 ? (2 * kh & 15) : kT == 16 ? group * 16 + (2 * kh & 15) : ((group * 16 + k) >> p.t_shift) * 4 + (2 * kh & 3);
+        return *reinterpret_cast<const uint16_t *>(stage.aux + at);
     }
 
-    // One step: 32 keys, the unit's key0 ..., in half `step` of a stage.  With kMask some row's
-    // bound or the unit's last key lies among them.
+    // One step: a stage's `step`-th 32 keys, the unit's key0 ....  With kMask some row's bound or the unit's
+    // last key lies among them.
     template <int NT, bool kMask>
-    __device__ __forceinline__ static void step(const Params &p, State<NT> &st, const uint8_t *stage, int step, int key0, int keys,
-                                                int kh, int lane) {
+    __device__ __forceinline__ static void step(const Params &p, State<NT> &st, const Stage &stage, int step, int key0, int keys, int kh,
+                                                int lane) {
         const int r = lane >> 2, c = lane & 3;
         constexpr int KS = D / 16;     // contraction steps of q.k, and 16-row blocks of O^T
         float s[kGroups][NT][4];
@@ -511,7 +520,7 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 2) weigh_kernel(const Params
                     for (int i = 0; i < KS; ++i) w[i] = 0;
                     if (slot >= 0) {
                         const int t = 1 << p.t_shift;
-                        const uint8_t *base = Quant8<D, 0>::piece(p, static_cast<int>(slot), kh);
+                        const uint8_t *base = Quant8<D, 0, 1>::piece(p, static_cast<int>(slot), kh);
                         const uint4 *cp = reinterpret_cast<const uint4 *>(base + (slot & (t - 1)) * D + c * (D / 4));
 #pragma unroll
                         for (int i = 0; i < D / 64; ++i) {
@@ -650,7 +659,7 @@ __global__ void __launch_bounds__(256) finish_kernel(const Params p, const Weigh
 int64_t tile_of(const pkv_byte_args *a) {
     return byte::tile_bytes(std::min(a->page_size, quant::kMaxTile), a->head_dim, a->num_kv_heads);
 }
-Shape shape_of(const pkv_byte_args *a) { return a->head_dim == 128 ? shape<Quant8<128, 0>>(tile_of(a)) : shape<Quant8<64, 0>>(tile_of(a)); }
+Shape shape_of(const pkv_byte_args *a) { return a->head_dim == 128 ? shape<Quant8<128, 0, 1>, Quant8<128, 0, 2>>(tile_of(a)) : shape<Quant8<64, 0, 1>, Quant8<64, 0, 2>>(tile_of(a)); }
 
 enum Call { kDecode, kExtend, kWeights };
 const char *const kNames[] = {"pkv_byte_decode", "pkv_byte_extend", "pkv_byte_weights"};
@@ -710,12 +719,18 @@ size_t size_of(const pkv_byte_args *a, Call call) {
 }
 
 // The map of a pool whose pieces are copied as boxes.
-bool encode_pool(const pkv_byte_args *a, Params &p) {
+bool encode_pool(const pkv_byte_args *a, int nt, Params &p) {
     if (p.t_shift != 6 && p.t_shift != 4) return true;
     const uint32_t lines = static_cast<uint32_t>((2 * a->head_dim << p.t_shift) / 128);
     const uint64_t dims[3] = {64, static_cast<uint64_t>(a->num_kv_heads) * lines, static_cast<uint64_t>(std::max<int64_t>(1, a->num_tiles))};
     const uint64_t strides[2] = {128, static_cast<uint64_t>(a->tile_stride)};
-    const uint32_t box[3] = {64, lines, 1};
+    auto box_lines = [&](auto kt) {
+        constexpr int kT = decltype(kt)::value;
+        if (a->head_dim == 128) return nt == 1 ? Quant8<128, kT, 1>::kLines : Quant8<128, kT, 2>::kLines;
+        return nt == 1 ? Quant8<64, kT, 1>::kLines : Quant8<64, kT, 2>::kLines;
+    };
+    const int height = p.t_shift == 6 ? box_lines(std::integral_constant<int, 64>{}) : box_lines(std::integral_constant<int, 16>{});
+    const uint32_t box[3] = {64, static_cast<uint32_t>(height), 1};
     return encode_tmap_bf16(&p.map, a->pool, 3, dims, strides, box);   // (pairs of bytes)
 }
 
@@ -735,7 +750,7 @@ pkv_status run(const pkv_byte_args *a, Call call, void *ws, size_t ws_bytes, int
     if (call == kWeights) return weigh(who, a, p, a->lse, reinterpret_cast<float *>(at), s);
     Plan pl;
     if (!make_plan(a, call == kExtend, shape_of(a), pl)) return fail(PKV_ERR_UNSUPPORTED, "%s: too many splits, keys or requests", who);
-    if ((pl.unit || pl.spans) && !encode_pool(a, p)) return fail(PKV_ERR_CUDA, "%s: cuTensorMapEncodeTiled rejected the pool", who);
+    if ((pl.unit || pl.spans) && !encode_pool(a, pl.nt, p)) return fail(PKV_ERR_CUDA, "%s: cuTensorMapEncodeTiled rejected the pool", who);
     if (!a->acc_out) return attend<Quant8>(who, a, pl, p, at, s);
     if (a->max_seq_len == 0) return attend<Quant8>(who, a, pl, p, at, s);
     const WeighPlan w = weigh_plan(a, call);

@@ -376,13 +376,13 @@ __device__ __forceinline__ void finish_segment(const Params &p, const Work &s, S
         }
 }
 
-template <int D, int kT_>
+template <int D, int kT_, int>
 struct Quant4 {
     static constexpr int kDim = D, kT = kT_;
     static constexpr bool kUnits = false, kHeldBf16V = false;
-    static constexpr int kAlign = 128;
+    static constexpr int kAlign = 128, kKeys = 64, kAux = 0;
     static constexpr const char *kExtend = "pkv_quant_extend";
-    static constexpr uint32_t kStageBytes = quant::tile_bytes(kTile, D);
+    static constexpr uint32_t kStageBytes = quant::tile_bytes(kKeys, D);
     static constexpr int warps(int nt) { return warps_per_sm(D, nt); }
     static constexpr int stages(int nt) { return ring_stages(D, nt); }
     template <int NT>
@@ -392,10 +392,11 @@ struct Quant4 {
     __device__ __forceinline__ static const uint8_t *piece(const Params &p, int slot, int kh) {
         return p.pool + static_cast<int64_t>(slot >> p.t_shift) * p.tile_stride + static_cast<int64_t>(kh) * quant::tile_bytes(1 << p.t_shift, D);
     }
-    __device__ __forceinline__ static void zero_piece(uint8_t *stage, int j, int ps) { qattn::zero_piece<D, kT>(stage, j, ps); }
+    __device__ __forceinline__ static void zero_piece(const Stage &stage, int j, int ps) { qattn::zero_piece<D, kT>(stage.codes, j, ps); }
     // Copies a tile's n pieces, `live` of them on good pages; piece i of the window is lane i % 32's src[i / 32].
     __device__ __forceinline__ static void copy(const Params &, int, const uint8_t *const (&src)[2], int first, int n, uint32_t live,
-                                                int ps, uint8_t *stage, uint64_t *bar, int lane) {
+                                                int ps, int, const Stage &to, uint64_t *bar, int lane) {
+        uint8_t *stage = to.codes;
         const uint32_t bytes = quant::tile_bytes(1 << ps, D);
         if (!gathers(ps)) {
             if (lane == (first & 31)) mbar_arrive_expect_tx(bar, live * bytes);
@@ -415,9 +416,9 @@ struct Quant4 {
         }
     }
     template <int NT, bool kMask>
-    __device__ __forceinline__ static void step(const Params &p, State<NT> &st, const uint8_t *stage, int step, int key0, int keys, int,
+    __device__ __forceinline__ static void step(const Params &p, State<NT> &st, const Stage &stage, int step, int key0, int keys, int,
                                                 int lane) {
-        tile_step<D, NT, kT, kMask>(p, st, stage, step, key0, keys, lane);
+        tile_step<D, NT, kT, kMask>(p, st, stage.codes, step, key0, keys, lane);
     }
     template <int NT>
     __device__ __forceinline__ static void start(const Params &p, const Work &w, State<NT> &st, const uint32_t (&ahead)[D / 8], int lane) {
@@ -463,7 +464,7 @@ struct Quant4 {
 int64_t tile_of(const pkv_quant_args *a) {
     return static_cast<int64_t>(a->num_kv_heads) * quant::tile_bytes(std::min(a->page_size, quant::kMaxTile), a->head_dim);
 }
-Shape shape_of(const pkv_quant_args *a) { return a->head_dim == 128 ? shape<Quant4<128, 0>>(tile_of(a)) : shape<Quant4<64, 0>>(tile_of(a)); }
+Shape shape_of(const pkv_quant_args *a) { return a->head_dim == 128 ? shape<Quant4<128, 0, 1>, Quant4<128, 0, 2>>(tile_of(a)) : shape<Quant4<64, 0, 1>, Quant4<64, 0, 2>>(tile_of(a)); }
 
 size_t size_of(const char *who, const pkv_quant_args *a, bool extend) {
     if (!a || validate(who, a, extend, false, tile_of) != PKV_OK) return 0;

@@ -19,11 +19,13 @@ namespace qattn {
 
 using quant::Table;
 
-constexpr int kTile = 64;           // keys per stage of the copies
+constexpr int kTile = 64;           // keys that a block of the copy of held keys takes at a time
 constexpr int kStep = 32;           // keys per step of the math: what 128 to 168 registers hold
 constexpr int kGroups = kStep / 16; // of 16 keys: the MMAs' key rows
+// A tile is F::kKeys keys: what a stage of the copies holds.
 // Tiles' worth of work that starting and finishing a unit takes (16 rows: q is loaded in place).
-constexpr int unit_cost(int nt) { return nt == 1 ? 1 : 2; }
+template <class F>
+__host__ __device__ constexpr int unit_cost(int nt) { return (nt == 1 ? 1 : 2) * 64 / F::kKeys; }
 constexpr int kMostTiles = 1 << 30; // of all units together
 constexpr int kTableInSmem = 1024;  // requests whose tile offsets every block computes for itself
 constexpr int kReqInSmem = 128;     // requests whose lengths are kept beside them
@@ -185,7 +187,8 @@ __device__ __forceinline__ Req load_req(const Params &p, int b, bool report) {
 }
 // A unit enters the sequence as unit_cost stand-in tiles and its real ones, so that a span
 // of many short units holds no more work than one inside a long unit.
-__device__ __forceinline__ int real_tiles(int L) { return max(1, (L + kTile - 1) / kTile); }
+template <class F>
+__device__ __forceinline__ int real_tiles(int L) { return max(1, (L + F::kKeys - 1) / F::kKeys); }
 template <int NT>
 __device__ __forceinline__ int row_blocks(const Params &p, int n) { return (n * p.g + 8 * NT - 1) / (8 * NT); }
 
@@ -205,7 +208,7 @@ struct Table1 {
 // off[b] = first tile of request b's units, off[B] = all tiles, off[B + 1] = tiles per
 // span, by the block's threads.  The host has checked that the tiles of well-formed inputs
 // fit the spans; row ranges that overlap could exceed that, and then no request has any.
-template <int NT, int kBlock>
+template <class F, int NT, int kBlock>
 __device__ __forceinline__ void build_table(const Params &p, const Table1 &tb, long long *scratch, bool report) {
     int *off = tb.off;
     const int B = p.batch, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -214,7 +217,7 @@ __device__ __forceinline__ void build_table(const Params &p, const Table1 &tb, l
     for (int b = lo; b < hi; ++b) {
         const Req r = load_req(p, b, report);
         if (tb.req) tb.req[b] = r;
-        local += static_cast<long long>(row_blocks<NT>(p, r.n)) * p.hkv * (unit_cost(NT) + real_tiles(r.L));
+        local += static_cast<long long>(row_blocks<NT>(p, r.n)) * p.hkv * (unit_cost<F>(NT) + real_tiles<F>(r.L));
         off[b + 1] = static_cast<int>(local);
     }
     long long incl = local;
@@ -245,7 +248,7 @@ __global__ void __launch_bounds__(1024) plan_kernel(const Params p) {
     pdl_wait();          // inputs may come from the previous kernel of the stream
     pdl_launch_next();
     __shared__ long long scratch[32];
-    build_table<NT, 1024>(p, Table1{p.off, nullptr}, scratch, true);
+    build_table<F, NT, 1024>(p, Table1{p.off, nullptr}, scratch, true);
 }
 
 // A unit and its place in the sequence of all units' tiles.
@@ -259,16 +262,17 @@ struct Unit {
 __device__ __forceinline__ Req get_req(const Params &p, const Table1 &tb, int b) {
     return tb.req ? tb.req[b] : load_req(p, b, false);
 }
+template <class F>
 __device__ __forceinline__ void set_req(Unit &u, const Req &r, int b) {
     u.b = b;
     u.L = r.L;
     u.n = r.n;
     u.qo0 = r.qo0;
     u.base = r.base;
-    u.tiles = real_tiles(r.L);
+    u.tiles = real_tiles<F>(r.L);
 }
 // The unit that holds tile `pos` of the sequence.
-template <int NT>
+template <class F, int NT>
 __device__ __forceinline__ Unit find_unit(const Params &p, const Table1 &tb, int pos) {
     const int *off = tb.off;
     int lo = 0, hi = p.batch;   // the last request with off[b] <= pos (those without rows have no tiles)
@@ -277,27 +281,27 @@ __device__ __forceinline__ Unit find_unit(const Params &p, const Table1 &tb, int
         if (off[mid] <= pos) lo = mid; else hi = mid;
     }
     Unit u;
-    set_req(u, get_req(p, tb, lo), lo);
-    const int all = u.tiles + unit_cost(NT), rem = pos - off[lo], i = rem / all;
+    set_req<F>(u, get_req(p, tb, lo), lo);
+    const int all = u.tiles + unit_cost<F>(NT), rem = pos - off[lo], i = rem / all;
     u.rb = i / p.hkv;
     u.kh = i - u.rb * p.hkv;
-    u.first = pos - (rem - i * all) + unit_cost(NT);
+    u.first = pos - (rem - i * all) + unit_cost<F>(NT);
     return u;
 }
 // The unit after u (there is one): the next kv head, row block or request.
-template <int NT>
+template <class F, int NT>
 __device__ __forceinline__ void next_unit(const Params &p, const Table1 &tb, Unit &u) {
     const int end = u.first + u.tiles;
     if (end == tb.off[u.b + 1]) {
         int b = u.b + 1;
         while (tb.off[b + 1] == end) ++b;   // requests without rows
-        set_req(u, get_req(p, tb, b), b);
+        set_req<F>(u, get_req(p, tb, b), b);
         u.rb = u.kh = 0;
     } else if (++u.kh == p.hkv) {
         u.kh = 0;
         ++u.rb;
     }
-    u.first = end + unit_cost(NT);
+    u.first = end + unit_cost<F>(NT);
 }
 
 // Keys that some row of the unit may see: the causal bound of its last token, or all.
@@ -335,6 +339,11 @@ __device__ __forceinline__ void write_empty(const Params &p, const Unit &s, int 
     }
 }
 
+// A stage of a warp's ring: what the copies fill, and the format's few bytes beside it.
+struct Stage {
+    uint8_t *codes, *aux;
+};
+
 // Walks the warp's spans and issues the copies of their tiles, one call of fetch() per tile,
 // and queues the segments for the math.  A piece is a pool tile (a page, or a page's next 64
 // keys); the pool addresses of 64 consecutive pieces (a window) are held by the lanes, two
@@ -352,11 +361,13 @@ struct Fetcher {
 
     // log2 of the keys of a piece
     __device__ __forceinline__ static int shift(const Params &p) { return F::kT == 64 ? 6 : F::kT == 16 ? 4 : p.t_shift; }
+    // and of the tiles that 64 pieces are
+    __device__ __forceinline__ static int window_shift(const Params &p) { return shift(p) + 6 - ilog2_of(F::kKeys); }
     __device__ __forceinline__ void look_up(const Params &p, int window, int lane) {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int64_t key = static_cast<int64_t>(window * 64 + 32 * i + lane) << shift(p);
-            nxt[i] = key < keys && key < static_cast<int64_t>(t_end) * kTile
+            nxt[i] = key < keys && key < static_cast<int64_t>(t_end) * F::kKeys
                          ? static_cast<int>(quant::slot_of(p.tab, u.base, static_cast<int>(key)))
                          : -3;
         }
@@ -372,14 +383,14 @@ struct Fetcher {
         }
         if (flags) raise_flag(p.err, flags);
         bad = __any_sync(0xffffffffu, flags);
-        look_up(p, (t >> shift(p)) + 1, lane);   // 64 pieces are 2^shift tiles
+        look_up(p, (t >> window_shift(p)) + 1, lane);
         fresh = false;
     }
     // To the next segment that has keys.
     __device__ __forceinline__ void advance(const Params &p, const Table1 &tb, Work *queue, int lane) {
         for (;;) {
             if (next < span_end) {
-                next_unit<NT>(p, tb, u);
+                next_unit<F, NT>(p, tb, u);
             } else {   // the warp's next span
                 const int total = tb.off[p.batch], per = tb.off[p.batch + 1];
                 for (;;) {
@@ -394,7 +405,7 @@ struct Fetcher {
                     if (lane == 0) p.cuts[sp] = make_int4(-1, 0, 0, 0);
                 }
                 span_end = min(total, next + per);
-                u = find_unit<NT>(p, tb, next);
+                u = find_unit<F, NT>(p, tb, next);
                 if (lane == 0) {   // cut: the unit has real tiles on both sides of the boundary
                     int4 cut = make_int4(-1, 0, 0, 0);
                     if (u.first < next) {
@@ -412,12 +423,12 @@ struct Fetcher {
             const int slot = t0 == 0 && t1 == u.tiles ? -1 : sp * 2 + (starts_inside ? 1 : 0);
             keys = unit_keys<NT>(p, u);
             t = t0;
-            t_end = min(t1, (keys + kTile - 1) / kTile);
+            t_end = min(t1, (keys + F::kKeys - 1) / F::kKeys);
             if (t >= t_end) {
                 write_empty<F::kDim, NT>(p, u, slot, lane);
                 continue;
             }
-            look_up(p, t >> shift(p), lane);
+            look_up(p, t >> window_shift(p), lane);
             if (lane == 0) queue[queued % kQueue] = Work{u.kh, u.rb, u.L, u.n, u.qo0, t, t_end, keys, slot, {0, 0, 0}};
             ++queued;
             fresh = true;
@@ -434,11 +445,12 @@ struct Fetcher {
         advance(p, tb, queue, lane);
     }
     // Copies the next tile into `stage`, completing on `bar`, and moves on.
-    __device__ __forceinline__ void fetch(const Params &p, const Table1 &tb, Work *queue, uint8_t *stage, uint64_t *bar, int lane) {
+    __device__ __forceinline__ void fetch(const Params &p, const Table1 &tb, Work *queue, const Stage &stage, uint64_t *bar, int lane) {
         if (fresh) enter_window(p, lane);
-        const int ps = shift(p), in_window = (1 << ps) - 1;
-        const int first = (t & in_window) << (6 - ps);   // the tile's first piece within the window
-        const int n = F::kT == 64 ? 1 : min(1 << (6 - ps), (keys - t * kTile + (1 << ps) - 1) >> ps);
+        constexpr int kShift = ilog2_of(F::kKeys);
+        const int ps = shift(p), in_window = (1 << window_shift(p)) - 1;
+        const int first = ((t & in_window) << kShift) >> ps;   // the tile's first piece within the window
+        const int n = ps >= kShift ? 1 : min(1 << (kShift - ps), (keys - t * F::kKeys + (1 << ps) - 1) >> ps);
         if (bad) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
@@ -459,7 +471,7 @@ struct Fetcher {
                 live += __popc(__ballot_sync(0xffffffffu, j >= 0 && j < n && src[i]));
             }
         }
-        F::copy(p, u.kh, src, first, n, live, ps, stage, bar, lane);
+        F::copy(p, u.kh, src, first, n, live, ps, (t << kShift) & ((1 << ps) - 1), stage, bar, lane);
         if (++t >= t_end)
             advance(p, tb, queue, lane);
         else if ((t & in_window) == 0)
@@ -573,6 +585,7 @@ __global__ void __launch_bounds__(F::warps(NT) * 32, 1) attend_kernel(const __gr
     constexpr int S = F::stages(NT);
     uint8_t *smem = aligned_smem<F::kAlign>(smem_raw);
     uint8_t *ring = smem + static_cast<uint32_t>(warp * S) * stage_bytes;
+    uint8_t *aux = smem + static_cast<uint32_t>(kWarps * S) * stage_bytes + warp * S * F::kAux;
     uint64_t *bar = bars + warp * S;
     if (lane == 0) {
         for (int i = 0; i < S; ++i) mbar_init(&bar[i], F::gathers(p.t_shift) ? 32 : 1);
@@ -583,13 +596,13 @@ __global__ void __launch_bounds__(F::warps(NT) * 32, 1) attend_kernel(const __gr
     pdl_launch_next();
     Table1 tb{p.off, nullptr};
     if (!p.off_ready) {
-        uint8_t *mine = smem + static_cast<uint32_t>(kWarps * S) * stage_bytes;
+        uint8_t *mine = smem + static_cast<uint32_t>(kWarps * S) * (stage_bytes + F::kAux);
         if (p.batch <= kReqInSmem) {
             tb.req = reinterpret_cast<Req *>(mine);
             mine += p.batch * sizeof(Req);
         }
         tb.off = reinterpret_cast<int *>(mine);
-        build_table<NT, kThreads>(p, tb, scratch, blockIdx.x == 0);
+        build_table<F, NT, kThreads>(p, tb, scratch, blockIdx.x == 0);
     }
     if (blockIdx.x == 0 && warp < 2) {   // unusable head scales
         const float *g = warp ? p.v_scale : p.k_scale;
@@ -617,7 +630,7 @@ __global__ void __launch_bounds__(F::warps(NT) * 32, 1) attend_kernel(const __gr
         // (one place for the copies and one for the math: the instructions of a cold start come
         // from memory too)
         while (!f.done && issued - used < S) {
-            f.fetch(p, tb, queue, ring + put * stage_bytes, &bar[put], lane);
+            f.fetch(p, tb, queue, Stage{ring + put * stage_bytes, aux + put * F::kAux}, &bar[put], lane);
             put = put == S - 1 ? 0 : put + 1;
             ++issued;
         }
@@ -638,15 +651,15 @@ __global__ void __launch_bounds__(F::warps(NT) * 32, 1) attend_kernel(const __gr
         ok = wait_for(&bar[take], phase, p.wait_ns);
         ok = __all_sync(0xffffffffu, ok);
         if (!ok) break;
-        const uint8_t *stage = ring + take * stage_bytes;
+        const Stage stage{ring + take * stage_bytes, aux + take * F::kAux};
         if (NT == 1 && w.t + 1 >= w.t_end && f.queued > seg) {   // the next segment's q on its way
             __syncwarp();   // lane 0 wrote the entry, maybe in the fetch() just above; a vote orders no memory
             load_q<D, NT>(p, queue[seg % kQueue], 0, q_raw, lane);
             q_ahead = true;
         }
-        const int key0 = w.t * kTile;
+        const int key0 = w.t * F::kKeys;
 #pragma unroll 1
-        for (int h = 0; h < kTile / kStep; ++h) {
+        for (int h = 0; h < F::kKeys / kStep; ++h) {
             const int k = key0 + h * kStep;
             if (k + kStep <= low)
                 F::template step<NT, false>(p, st, stage, h, k, w.keys, w.kh, lane);
@@ -686,10 +699,11 @@ __global__ void __launch_bounds__(F::warps(NT) * 32, 1) unit_kernel(const __grid
     __shared__ float2 ml[kWarps][8 * NT];
     __shared__ float unit_of[kWarps];   // log2 of the unit of a warp's sums (formats with one)
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const int shift = F::kT == 64 ? 6 : F::kT == 16 ? 4 : p.t_shift, pieces = 64 >> shift;
+    const int shift = F::kT == 64 ? 6 : F::kT == 16 ? 4 : p.t_shift, pieces = max(1, F::kKeys >> shift);
     constexpr uint32_t stage_bytes = F::kStageBytes;
     uint8_t *smem = aligned_smem<F::kAlign>(smem_raw);
     uint8_t *ring = smem + static_cast<uint32_t>(warp * S) * stage_bytes;
+    uint8_t *aux = smem + static_cast<uint32_t>(kWarps * S) * stage_bytes + warp * S * F::kAux;
     uint64_t *bar = bars + warp * S;
     if (lane == 0) {
         for (int i = 0; i < S; ++i) mbar_init(&bar[i], F::gathers(p.t_shift) ? 32 : 1);
@@ -723,7 +737,7 @@ __global__ void __launch_bounds__(F::warps(NT) * 32, 1) unit_kernel(const __grid
         u.rb = rb;
         u.L = req.L;
         u.n = req.n;
-        const int keys = kRows ? unit_keys<NT>(p, u) : req.L, tiles = (keys + kTile - 1) / kTile;
+        const int keys = kRows ? unit_keys<NT>(p, u) : req.L, tiles = (keys + F::kKeys - 1) / F::kKeys;
         const Work w{kh, rb, req.L, req.n, req.qo0, 0, tiles, keys, -1, {0, 0, 0}};
         uint32_t q_raw[D / 8];
         if (NT == 1) load_q<D, NT>(p, w, 0, q_raw, lane);
@@ -731,12 +745,12 @@ __global__ void __launch_bounds__(F::warps(NT) * 32, 1) unit_kernel(const __grid
         auto look_up = [&](int t, int (&slot)[2]) {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-                const int64_t key = (static_cast<int64_t>(t) << 6) + (static_cast<int64_t>(32 * i + lane) << shift);
+                const int64_t key = static_cast<int64_t>(t) * F::kKeys + (static_cast<int64_t>(32 * i + lane) << shift);
                 slot[i] = 32 * i + lane < pieces && key < keys ? static_cast<int>(quant::slot_of(p.tab, base, static_cast<int>(key))) : -3;
             }
         };
-        auto fetch = [&](const int (&slot)[2], int stage) {
-            uint8_t *dst = ring + stage * stage_bytes;
+        auto fetch = [&](const int (&slot)[2], int t, int stage) {
+            const Stage dst{ring + stage * stage_bytes, aux + stage * F::kAux};
             const uint8_t *src[2];
             uint32_t live = 0;
 #pragma unroll
@@ -749,7 +763,7 @@ __global__ void __launch_bounds__(F::warps(NT) * 32, 1) unit_kernel(const __grid
                     fence_proxy_async_smem();   // before later copies into this stage
                 }
             }
-            F::copy(p, kh, src, 0, pieces, live, shift, dst, &bar[stage], lane);
+            F::copy(p, kh, src, 0, pieces, live, shift, (t * F::kKeys) & ((1 << shift) - 1), dst, &bar[stage], lane);
             __syncwarp();
         };
         int slots[S][2];
@@ -757,7 +771,7 @@ __global__ void __launch_bounds__(F::warps(NT) * 32, 1) unit_kernel(const __grid
         for (int i = 0; i < S; ++i) look_up(warp + i * kWarps, slots[i]);
 #pragma unroll
         for (int i = 0; i < S; ++i)
-            if (ok && warp + i * kWarps < tiles) fetch(slots[i], (stage + i) % S);
+            if (ok && warp + i * kWarps < tiles) fetch(slots[i], warp + i * kWarps, (stage + i) % S);
         typename F::template State<NT> st;
         F::template start<NT>(p, w, st, q_raw, lane);
         int low = req.L;   // every row sees the keys below it
@@ -776,15 +790,15 @@ __global__ void __launch_bounds__(F::warps(NT) * 32, 1) unit_kernel(const __grid
             ok = __all_sync(0xffffffffu, wait_for(&bar[stage], phase, p.wait_ns));
             if (!ok) break;
 #pragma unroll 1
-            for (int h = 0; h < kTile / kStep; ++h) {
-                const int k = t * kTile + h * kStep;
+            for (int h = 0; h < F::kKeys / kStep; ++h) {
+                const int k = t * F::kKeys + h * kStep;
                 if (k + kStep <= low)
-                    F::template step<NT, false>(p, st, ring + stage * stage_bytes, h, k, keys, kh, lane);
+                    F::template step<NT, false>(p, st, Stage{ring + stage * stage_bytes, aux + stage * F::kAux}, h, k, keys, kh, lane);
                 else if (k < keys)
-                    F::template step<NT, true>(p, st, ring + stage * stage_bytes, h, k, keys, kh, lane);
+                    F::template step<NT, true>(p, st, Stage{ring + stage * stage_bytes, aux + stage * F::kAux}, h, k, keys, kh, lane);
             }
             __syncwarp();
-            if (t + S * kWarps < tiles) fetch(next, stage);
+            if (t + S * kWarps < tiles) fetch(next, t + S * kWarps, stage);
             if (++stage == S) {
                 stage = 0;
                 phase ^= 1;
@@ -1077,14 +1091,17 @@ __global__ void __launch_bounds__(kHoldThreads, kHoldCtas) hold_kernel(const Par
 // ------------------------------------------------------------------ host side
 // What the plan has to know of a format at a head_dim and page size.
 struct Shape {
-    int warps[2], stages[2];   // at NT = 1 and 2
-    size_t stage, slack;       // bytes of a stage; for the alignment of the first one
+    // at NT = 1 and 2: warps, stages of each, unit_cost, keys of a tile, bytes of a stage
+    int warps[2], stages[2], cost[2], keys[2];
+    size_t stage[2];
+    size_t slack;              // bytes for the alignment of the first stage
     bool units;                // sums have a unit
     int64_t tile;              // bytes of a pool tile
 };
-template <class F>
+template <class F1, class F2>
 static Shape shape(int64_t tile) {
-    return Shape{{F::warps(1), F::warps(2)}, {F::stages(1), F::stages(2)}, F::kStageBytes, F::kAlign > 128 ? F::kAlign : 0, F::kUnits, tile};
+    return Shape{{F1::warps(1), F2::warps(2)}, {F1::stages(1), F2::stages(2)}, {unit_cost<F1>(1), unit_cost<F2>(2)}, {F1::kKeys, F2::kKeys},
+                 {F1::kStageBytes + F1::kAux, F2::kStageBytes + F2::kAux}, F1::kAlign > 128 ? F1::kAlign : 0, F1::kUnits, tile};
 }
 
 // (`needs_out`: the call writes the attention's output)
@@ -1204,14 +1221,14 @@ static bool make_plan(const A *a, bool extend, const Shape &f, Plan &pl) {
         // 17.4 / 25.8, 32 x 256 15.0 / 19.4; 48 rows, 4 x 1000 11.9 / 18.6.  (The same rule at 64 dims,
         // whose tiles are half the bytes and take some two thirds of the time.)
         // (Calls of more units than a grid's side take the spans in any case.)
-        const int nt = rows <= 8 ? 1 : 2, warps = f.warps[nt - 1];
+        const int nt = rows <= 8 ? 1 : 2, warps = f.warps[nt - 1], keys = f.keys[nt - 1];
         const int64_t blocks = (rows + 8 * nt - 1) / (8 * nt), units = batch * a->num_kv_heads * blocks;
         if (units <= 65535) {
-            const int64_t tiles = (std::max(1, a->max_seq_len) + kTile - 1) / kTile;
+            const int64_t tiles = (std::max(1, a->max_seq_len) + keys - 1) / keys;
             const int64_t rounds = (tiles + warps - 1) / warps, waves = (units + sms - 1) / sms;
-            const int64_t of_all = a->total_kv > 0 ? std::min(a->total_kv / kTile, batch * tiles) : batch * tiles / 2;
+            const int64_t of_all = a->total_kv > 0 ? std::min(a->total_kv / keys, batch * tiles) : batch * tiles / 2;
             const int64_t all = of_all * a->num_kv_heads * blocks + units;
-            pl.unit = 5 + waves * (2 + 3 * rounds) <= 13 + 3 * ((all + sms * warps - 1) / (sms * warps));
+            pl.unit = 5 + waves * (2 + 3 * rounds * keys / 64) <= 13 + 3 * ((all + sms * warps - 1) / (sms * warps)) * keys / 64;
         }
     }
     pl.spans = !pl.unit && (!pl.held || batch > 1);
@@ -1219,7 +1236,7 @@ static bool make_plan(const A *a, bool extend, const Shape &f, Plan &pl) {
         pl.nt = rows <= 8 ? 1 : 2;
         pl.grid = dim3(static_cast<unsigned>(batch), static_cast<unsigned>(a->num_kv_heads),
                        static_cast<unsigned>((rows + 8 * pl.nt - 1) / (8 * pl.nt)));
-        pl.smem = static_cast<size_t>(f.warps[pl.nt - 1] * f.stages[pl.nt - 1]) * f.stage + f.slack;
+        pl.smem = static_cast<size_t>(f.warps[pl.nt - 1] * f.stages[pl.nt - 1]) * f.stage[pl.nt - 1] + f.slack;
     }
     if (pl.spans) {
         const int64_t few = pl.held ? kHeldRows : rows;
@@ -1227,15 +1244,15 @@ static bool make_plan(const A *a, bool extend, const Shape &f, Plan &pl) {
         const int warps = f.warps[pl.nt - 1];
         pl.grid = dim3(static_cast<unsigned>(sms));
         pl.plan_launch = a->batch > kTableInSmem;
-        pl.smem = static_cast<size_t>(warps * f.stages[pl.nt - 1]) * f.stage + f.slack;
+        pl.smem = static_cast<size_t>(warps * f.stages[pl.nt - 1]) * f.stage[pl.nt - 1] + f.slack;
         if (!pl.plan_launch) pl.smem += (static_cast<size_t>(a->batch) + 2) * 4 + (a->batch <= kReqInSmem ? a->batch * sizeof(Req) : 0);
         int64_t spans = sms * warps;
         // all units' tiles, at most (beside held keys the requests with few rows only)
         const int64_t all_rows = pl.held ? std::min<int64_t>(a->total_q * g, batch * kHeldRows) : a->total_q * g;
         const int64_t blocks = (all_rows + 8 * pl.nt - 1) / (8 * pl.nt) + a->batch;
-        const int64_t tiles = blocks * a->num_kv_heads * ((std::max(1, a->max_seq_len) + kTile - 1) / kTile + unit_cost(pl.nt));
+        const int64_t tiles = blocks * a->num_kv_heads * ((std::max(1, a->max_seq_len) + f.keys[pl.nt - 1] - 1) / f.keys[pl.nt - 1] + f.cost[pl.nt - 1]);
         if (a->kv_chunk > 0) {
-            pl.span_tiles = a->kv_chunk / kTile;
+            pl.span_tiles = a->kv_chunk / f.keys[pl.nt - 1];
             spans = (tiles + pl.span_tiles - 1) / pl.span_tiles;
         }
         if (spans > INT32_MAX / 64 || tiles > kMostTiles) return false;
@@ -1305,27 +1322,27 @@ static Params params(const A *a, int32_t *err) {
     return p;
 }
 
-// Fm<D, kT>: the format at a head_dim, for pools of tiles of kT slots (0: others).
-template <template <int, int> class Fm, int D, int NT>
+// Fm<D, kT, NT>: the format at a head_dim, for pools of tiles of kT slots (0: others) and 8 NT rows.
+template <template <int, int, int> class Fm, int D, int NT>
 static pkv_status launch(const char *who, const Params &p, const Plan &pl, cudaStream_t s) {
     auto pick = [&](auto f) {
         using F = decltype(f);
         return !pl.unit ? attend_kernel<F, NT> : p.qo_indptr ? unit_kernel<F, NT, true> : unit_kernel<F, NT, false>;
     };
-    auto *kern = p.t_shift == 6 ? pick(Fm<D, 64>{}) : p.t_shift == 4 ? pick(Fm<D, 16>{}) : pick(Fm<D, 0>{});
+    auto *kern = p.t_shift == 6 ? pick(Fm<D, 64, NT>{}) : p.t_shift == 4 ? pick(Fm<D, 16, NT>{}) : pick(Fm<D, 0, NT>{});
     if (raise_smem_limit(reinterpret_cast<const void *>(kern)) < pl.smem)
         return fail(PKV_ERR_CUDA, "%s: cannot raise the shared-memory limit", who);
     pkv_status st = PKV_OK;
     if (pl.plan_launch) {
-        st = launch_status(launch_chained(plan_kernel<Fm<D, 0>, NT>, dim3(1), dim3(1024), 0, s, p), who);
+        st = launch_status(launch_chained(plan_kernel<Fm<D, 0, NT>, NT>, dim3(1), dim3(1024), 0, s, p), who);
         if (st != PKV_OK) return st;
     }
-    st = launch_status(launch_chained(kern, pl.grid, dim3(Fm<D, 0>::warps(NT) * 32), pl.smem, s, p), who);
+    st = launch_status(launch_chained(kern, pl.grid, dim3(Fm<D, 0, NT>::warps(NT) * 32), pl.smem, s, p), who);
     if (st != PKV_OK || pl.unit) return st;
-    return launch_status(launch_chained(merge_kernel<Fm<D, 0>, NT>, dim3(pl.spans_max), dim3(kMergeThreads), 0, s, p), who);
+    return launch_status(launch_chained(merge_kernel<Fm<D, 0, NT>, NT>, dim3(pl.spans_max), dim3(kMergeThreads), 0, s, p), who);
 }
 
-template <template <int, int> class Fm, int D, class A>
+template <template <int, int, int> class Fm, int D, class A>
 static pkv_status launch_held(const A *a, const Params &p, const Plan &pl, char *ws, cudaStream_t s) {
     const pkv_extend_args e = extend_args(a);
     char *own = ws + 2 * pl.hold_k + pl.hold_first;
@@ -1337,22 +1354,22 @@ static pkv_status launch_held(const A *a, const Params &p, const Plan &pl, char 
     h.order = h.first_row + a->batch + 1;
     h.counter = reinterpret_cast<int32_t *>(own + ext::held_counter_offset(&e));
     h.min_rows = pl.spans ? kHeldRows : 0;
-    auto *kern = hold_kernel<Fm<D, 0>>;
+    auto *kern = hold_kernel<Fm<D, 0, 1>>;
     const size_t smem = (static_cast<size_t>(a->batch) + 1) * 8;
     if (raise_smem_limit(reinterpret_cast<const void *>(kern)) < smem)
-        return fail(PKV_ERR_CUDA, "%s: cannot raise the shared-memory limit", Fm<D, 0>::kExtend);
+        return fail(PKV_ERR_CUDA, "%s: cannot raise the shared-memory limit", Fm<D, 0, 1>::kExtend);
     const int64_t items = (pl.hold_rows / kTile + a->batch) * a->num_kv_heads;
     const int64_t grid = std::max<int64_t>(1, std::min<int64_t>(items, static_cast<int64_t>(kHoldCtas) * std::max(1, sm_count())));
     const pkv_status st = launch_status(launch_chained(kern, dim3(static_cast<unsigned>(grid)), dim3(kHoldThreads), smem, s, p, h),
-                                        Fm<D, 0>::kExtend);
+                                        Fm<D, 0, 1>::kExtend);
     if (st != PKV_OK) return st;
-    const ext::Held held{h.k, h.v, h.rows, h.first_row, h.order, p.k_scale, p.v_scale, a->q_row_stride, h.min_rows, Fm<D, 0>::kHeldBf16V,
-                         Fm<D, 0>::kExtend};
+    const ext::Held held{h.k, h.v, h.rows, h.first_row, h.order, p.k_scale, p.v_scale, a->q_row_stride, h.min_rows, Fm<D, 0, 1>::kHeldBf16V,
+                         Fm<D, 0, 1>::kExtend};
     return ext::held_launch(&e, held, own, p.err, s);
 }
 
 // Checked arguments: the plan `pl`, parameters `p` but for the workspace's parts.
-template <template <int, int> class Fm, class A>
+template <template <int, int, int> class Fm, class A>
 static pkv_status attend(const char *who, const A *a, const Plan &pl, Params &p, char *at, cudaStream_t s) {
     p.wait_ns = wait_limit_ns();
     if (pl.held) {
