@@ -14,8 +14,7 @@
 // Lane (r, c) = (lane / 4, lane % 4) holds dims D/4 c ... of key row r for K, and dims D/8 r
 // ... of keys of column c for V, as the 4-bit kernel's do; codes of two keys are interleaved before
 // V's conversion, so that one gives the pair of keys that the MMA wants.
-#include "byte.cuh"
-#include "spans.cuh"
+#include "byte_weigh.cuh"
 
 namespace pkv {
 namespace qattn {
@@ -55,7 +54,7 @@ struct Quant8 {
     // A piece: its address, or where it is copied as a box (kT != 0) its tile, counted from 1.
     __device__ __forceinline__ static const uint8_t *piece(const Params &p, int slot, int kh) {
         if (kT != 0) return reinterpret_cast<const uint8_t *>(static_cast<uintptr_t>((slot >> p.t_shift) + 1));
-        return p.pool + static_cast<int64_t>(slot >> p.t_shift) * p.tile_stride + (static_cast<int64_t>(kh) * 2 * D << p.t_shift);
+        return piece_at<D>(p, slot, kh);
     }
     __device__ __forceinline__ static void zero_piece(const Stage &stage, int j, int ps) {
         const int t = 1 << ps;
@@ -381,10 +380,10 @@ struct Quant8 {
     };
     __device__ __forceinline__ static Block load_block(const Params &p, int64_t slot, int kh, bool is_v, int j) {
         const int t = 1 << p.t_shift, at = static_cast<int>(slot & (t - 1));
-        const uint8_t *a = piece(p, static_cast<int>(slot), kh);
+        const uint8_t *a = piece_at<D>(p, slot, kh);
         Block b;
         b.codes = __ldg(reinterpret_cast<const uint4 *>(a + (is_v ? t * D : 0) + at * D + j * 16));
-        b.scale = __ldg(a + (static_cast<int64_t>(p.hkv - kh) * 2 * D << p.t_shift) + 2 * kh + is_v);
+        b.scale = __ldg(scales_at<D>(p, a, kh) + is_v);
         return b;
     }
     __device__ __forceinline__ static bool has_nan(const Block &b) {
@@ -401,259 +400,6 @@ struct Quant8 {
         }
     }
 };
-
-// ---------------------------------------------------------------- weights
-// What keys receive from given rows: a block takes 512 keys of one request and kv head, its warps 64
-// each, over all the request's rows, 128 at a time in shared memory as fp16.  With lse known a
-// weight is one exponential: w = 2^(logit - lse2).  Partial sums, one per kv head, are added up
-// by add_kernel in a fixed order.
-constexpr int kWeighWarps = 8, kWeighKeys = 64 * kWeighWarps, kWeighRows = 128;
-
-struct WeighParams {
-    const float *lse;
-    float *part;             // [Hkv][B][max_len]
-    const float *acc_in;
-    float *acc_out;
-    int64_t acc_stride;
-};
-
-__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
-    uint64_t d;
-    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-    return d;
-}
-
-// Place in its row of the k-th 16 bytes of lane (r, c)'s dims: the four c of two rows lie in eight bank groups.
-__device__ __forceinline__ int q_chunk(int row, int c, int k) { return (4 * k + c) ^ ((row & 1) << 2); }
-template <int D>
-struct WeighSmem {
-    uint4 q[kWeighRows * D / 8];                        // fp16, 16 bytes of a row at a time (see q_chunk)
-    float f[kWeighRows], minus_lse[kWeighRows];         // score -> base-2 logit without K's scale; -lse2
-    int end[kWeighRows], low[kWeighRows / 8];           // key bounds; the least of each eight
-};
-
-template <int D>
-__global__ void __launch_bounds__(kWeighWarps * 32, 2) weigh_kernel(const Params p, const WeighParams wp) {
-    __shared__ __align__(16) WeighSmem<D> sm;
-    pdl_wait();          // inputs may come from the previous kernel of the stream
-    pdl_launch_next();
-    const int b = blockIdx.z, kh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
-    const Req req = load_req(p, b, blockIdx.x == 0 && kh == 0 && threadIdx.x == 0);
-    const int k0 = blockIdx.x * kWeighKeys + warp * 64;
-    if (static_cast<int>(blockIdx.x) * kWeighKeys >= req.L) return;
-    const int rows = req.n * p.g;
-    constexpr int KS = D / 16;
-    float sum[2][2][2] = {};   // [half][16-key group][u] of keys k0 + 32 h + 16 kt + r + 8 u
-    for (int r0 = 0; r0 < rows; r0 += kWeighRows) {
-        const int live = min(kWeighRows, rows - r0), blocks = (live + 7) / 8;
-        __syncthreads();
-        // eight lanes per row
-        for (int row = threadIdx.x >> 3; row < blocks * 8; row += kWeighWarps * 4) {
-            const int rr = r0 + row, tok = token_of(p, rr), j = threadIdx.x & 7;
-            uint32_t w[D / 16];
-            uint32_t top = 0;
-            const bool in = row < live;
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                uint4 x = make_uint4(0, 0, 0, 0);
-                if (in) x = __ldg(reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(req.qo0 + tok) * p.q_stride +
-                                                                  (kh * p.g + rr - tok * p.g) * D + j * (D / 8)) + i);
-                w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
-            }
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) top = __vmaxu2(top, w[i] & 0x7fff7fffu);
-            top = max(top & 0xffffu, top >> 16);
-#pragma unroll
-            for (int o = 1; o < 8; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-            int e = min(126, 6 + 127 - static_cast<int>(top >> 7));   // (see start_segment)
-            if (top == 0 || top >= 0x7f80u) e = 0;
-            const float up = __int_as_float((e + 127) << 23), down = __int_as_float((127 - e) << 23);
-#pragma unroll
-            for (int i = 0; i < D / 16; ++i) w[i] = pack_f16x2(bf16_lo(w[i]) * up, bf16_hi(w[i]) * up);
-#pragma unroll
-            for (int i = 0; i < D / 64; ++i) {
-                const int chunk = j * (D / 64) + i;
-                sm.q[row * (D / 8) + q_chunk(row, chunk / (D / 32), chunk % (D / 32))] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
-            }
-            int end = 0;
-            float minus_lse = 0.f;
-            if (in && j == 0) {
-                const float lse = wp.lse[static_cast<int64_t>(req.qo0 + tok) * p.hq + kh * p.g + rr - tok * p.g] * kLog2e;
-                end = !p.qo_indptr ? req.L : p.kv_end ? p.kv_end[req.qo0 + tok] : req.L - req.n + tok + 1;
-                if (end < 0 || end > req.L) {
-                    if (blockIdx.x == 0 && kh == 0) raise_flag(p.err, PKV_DEVERR_RANGE);
-                    end = 0;
-                }
-                if (lse == -INFINITY) end = 0;
-                minus_lse = -lse;
-            }
-            if (j == 0) {   // (rows past the last have bound 0: nothing of them counts)
-                sm.f[row] = p.scale_log2 * down;
-                sm.minus_lse[row] = minus_lse;
-                sm.end[row] = end;
-            }
-        }
-        __syncthreads();
-        if (threadIdx.x < blocks) {
-            int low = INT32_MAX;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) low = min(low, sm.end[threadIdx.x * 8 + i]);
-            sm.low[threadIdx.x] = low;
-        }
-        __syncthreads();
-#pragma unroll 1
-        for (int h = 0; h < 2; ++h) {
-            const int key0 = k0 + h * 32;
-            if (key0 >= req.L) break;
-            uint32_t a[2][2][KS][2];   // [16-key group][u][step][lo / hi]
-            uint64_t ks[2][2];
-#pragma unroll
-            for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const int key = key0 + kt * 16 + r + 8 * u;
-                    const int64_t slot = key < req.L ? quant::slot_of(p.tab, req.base, key) : -3;
-                    if (slot == -1 || slot == -2) raise_flag(p.err, slot == -1 ? PKV_DEVERR_RANGE : PKV_DEVERR_CONTIG);
-                    uint32_t w[KS];
-                    uint32_t e = 1;
-#pragma unroll
-                    for (int i = 0; i < KS; ++i) w[i] = 0;
-                    if (slot >= 0) {
-                        const int t = 1 << p.t_shift;
-                        const uint8_t *base = Quant8<D, 0, 1>::piece(p, static_cast<int>(slot), kh);
-                        const uint4 *cp = reinterpret_cast<const uint4 *>(base + (slot & (t - 1)) * D + c * (D / 4));
-#pragma unroll
-                        for (int i = 0; i < D / 64; ++i) {
-                            const uint4 x = ld_stream_16(cp + i);
-                            w[4 * i] = x.x; w[4 * i + 1] = x.y; w[4 * i + 2] = x.z; w[4 * i + 3] = x.w;
-                        }
-                        e = __ldg(base + (static_cast<int64_t>(p.hkv - kh) * 2 * D << p.t_shift) + 2 * kh);
-                    }
-                    ks[kt][u] = pair(byte::scale_value(e), byte::scale_value(e));
-#pragma unroll
-                    for (int i = 0; i < KS; ++i) {
-                        a[kt][u][i][0] = byte::lo_to_f16(w[i]);
-                        a[kt][u][i][1] = byte::hi_to_f16(w[i]);
-                    }
-                }
-            uint64_t part[2][2] = {};   // of rows 2 c and 2 c + 1
-#pragma unroll 1
-            for (int n = 0; n < blocks; ++n) {
-                float s[2][4] = {};
-                const uint4 *qp = sm.q + (n * 8 + r) * (D / 8);
-#pragma unroll
-                for (int i = 0; i < KS; i += 2) {
-                    const uint4 x = qp[q_chunk(r, c, i / 2)];
-#pragma unroll
-                    for (int kt = 0; kt < 2; ++kt) mma_f16(s[kt], a[kt][0][i][0], a[kt][1][i][0], a[kt][0][i][1], a[kt][1][i][1], x.x, x.y);
-#pragma unroll
-                    for (int kt = 0; kt < 2; ++kt)
-                        mma_f16(s[kt], a[kt][0][i + 1][0], a[kt][1][i + 1][0], a[kt][0][i + 1][1], a[kt][1][i + 1][1], x.z, x.w);
-                }
-                const int row = n * 8 + 2 * c;
-                const uint64_t f = *reinterpret_cast<const uint64_t *>(&sm.f[row]), lse = *reinterpret_cast<const uint64_t *>(&sm.minus_lse[row]);
-                const bool whole = key0 + 32 <= sm.low[n];
-                int2 end = make_int2(0, 0);
-                if (!whole) end = *reinterpret_cast<const int2 *>(&sm.end[row]);
-#pragma unroll
-                for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-                    for (int u = 0; u < 2; ++u) {
-                        const float2 y = unpair(fma2(mul2(pair(s[kt][2 * u], s[kt][2 * u + 1]), f), ks[kt][u], lse));
-                        float x0 = ex2(y.x), x1 = ex2(y.y);
-                        if (!whole) {
-                            const int key = key0 + kt * 16 + r + 8 * u;
-                            x0 = key < end.x ? x0 : 0.f;
-                            x1 = key < end.y ? x1 : 0.f;
-                        }
-                        part[kt][u] = add2(part[kt][u], pair(x0, x1));
-                    }
-            }
-#pragma unroll
-            for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-                for (int u = 0; u < 2; ++u) {
-                    const float2 x = unpair(part[kt][u]);
-#pragma unroll
-                    for (int i = 0; i < 2; ++i) sum[i][kt][u] += h == i ? x.x + x.y : 0.f;
-                }
-        }
-    }
-    float *part = wp.part + (static_cast<int64_t>(kh) * p.batch + b) * p.tab.max_len;
-#pragma unroll
-    for (int h = 0; h < 2; ++h)
-#pragma unroll
-        for (int kt = 0; kt < 2; ++kt)
-#pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                float x = sum[h][kt][u];
-                x += __shfl_xor_sync(0xffffffffu, x, 1);
-                x += __shfl_xor_sync(0xffffffffu, x, 2);
-                const int key = k0 + h * 32 + kt * 16 + r + 8 * u;
-                if (c == 0 && key < req.L) part[key] = x;
-            }
-}
-
-__global__ void __launch_bounds__(256) add_kernel(const Params p, const WeighParams wp) {
-    pdl_wait();          // inputs may come from the previous kernel of the stream
-    pdl_launch_next();
-    const int b = blockIdx.y, key = blockIdx.x * 256 + threadIdx.x;
-    int64_t base;
-    const int L = quant::key_count(p.tab, b, base, p.err, false);
-    if (key >= L) return;
-    const int64_t row = p.tab.req_pool_idx[b], at = row * wp.acc_stride + (p.tab.kv_start ? p.tab.kv_start[b] : 0) + key;
-    float x = 0.f;
-    for (int kh = 0; kh < p.hkv; ++kh) x += wp.part[(static_cast<int64_t>(kh) * p.batch + b) * p.tab.max_len + key];
-    wp.acc_out[at] = wp.acc_in ? wp.acc_in[at] + x : x;
-}
-
-// The same from a decode's logits: acc_out = acc_in + sum over heads of 2^(logit - lse2).  A thread
-// has four keys and every fourth head, whose loads are all on their way before the first is used.
-constexpr int kFinishKeys = 256;
-__global__ void __launch_bounds__(256) finish_kernel(const Params p, const WeighParams wp) {
-    __shared__ float4 sums[4][kFinishKeys / 4];
-    pdl_wait();          // the logits
-    pdl_launch_next();
-    const int b = blockIdx.y, quad = threadIdx.x & 63, group = threadIdx.x >> 6, key0 = blockIdx.x * kFinishKeys;
-    int64_t base;
-    const int L = quant::key_count(p.tab, b, base, p.err, false);
-    if (key0 >= L) return;
-    const int64_t row = p.tab.req_pool_idx[b], first = row * wp.acc_stride + (p.tab.kv_start ? p.tab.kv_start[b] : 0);
-    const int mine = key0 + threadIdx.x;
-    const float before = wp.acc_in && mine < L ? wp.acc_in[first + mine] : 0.f;
-    float4 x = make_float4(0.f, 0.f, 0.f, 0.f);
-    if (key0 + 4 * quad < L) {   // (a row of logits is whole 8 floats; what lies behind L is dropped below)
-        const float *y = p.logits + static_cast<int64_t>(b) * p.hq * p.logit_stride + key0 + 4 * quad;
-        const float *lse = wp.lse + static_cast<int64_t>(b) * p.hq;
-        for (int h0 = group; h0 < p.hq; h0 += 32) {
-            float4 v[8];
-            float l[8];
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int h = h0 + 4 * i;
-                v[i] = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-                l[i] = 0.f;
-                if (h < p.hq) {
-                    v[i] = __ldcs(reinterpret_cast<const float4 *>(y + h * p.logit_stride));
-                    l[i] = __ldg(lse + h);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float m = l[i] * kLog2e;
-                x.x += ex2(v[i].x - m);
-                x.y += ex2(v[i].y - m);
-                x.z += ex2(v[i].z - m);
-                x.w += ex2(v[i].w - m);
-            }
-        }
-    }
-    sums[group][quad] = x;
-    __syncthreads();
-    if (mine >= L) return;
-    const float *s = reinterpret_cast<const float *>(sums) + threadIdx.x;
-    wp.acc_out[first + mine] = before + ((s[0] + s[kFinishKeys]) + (s[2 * kFinishKeys] + s[3 * kFinishKeys]));
-}
 
 // ---------------------------------------------------------------- host side
 int64_t tile_of(const pkv_byte_args *a) {
@@ -698,17 +444,6 @@ WeighPlan weigh_plan(const pkv_byte_args *a, Call call) {
     return w;
 }
 
-pkv_status weigh(const char *who, const pkv_byte_args *a, const Params &p, const float *lse, float *part, cudaStream_t s) {
-    if (a->max_seq_len == 0) return ok();
-    const WeighParams wp{lse, part, a->acc_in, a->acc_out, a->acc_row_stride};
-    const unsigned L = static_cast<unsigned>(a->max_seq_len), B = static_cast<unsigned>(a->batch);
-    auto *kern = a->head_dim == 128 ? weigh_kernel<128> : weigh_kernel<64>;
-    const pkv_status st = launch_status(launch_chained(kern, dim3((L + kWeighKeys - 1) / kWeighKeys, static_cast<unsigned>(a->num_kv_heads), B),
-                                                       dim3(kWeighWarps * 32), 0, s, p, wp), who);
-    if (st != PKV_OK) return st;
-    return launch_status(launch_chained(add_kernel, dim3((L + 255) / 256, B), dim3(256), 0, s, p, wp), who);
-}
-
 size_t size_of(const pkv_byte_args *a, Call call) {
     if (!a || check(a, call, false) != PKV_OK) return 0;
     if (call == kWeights) return std::max<size_t>(weigh_plan(a, call).part, 256);
@@ -747,7 +482,13 @@ pkv_status run(const pkv_byte_args *a, Call call, void *ws, size_t ws_bytes, int
     st = check_workspace(who, ws, ws_bytes, need);
     if (st != PKV_OK) return st;
     char *at = static_cast<char *>(ws);
-    if (call == kWeights) return weigh(who, a, p, a->lse, reinterpret_cast<float *>(at), s);
+    if (call == kWeights) {
+        p.wait_ns = wait_limit_ns();
+        // rows of a request and kv head: at most max_q_len's, or what the average says
+        const int64_t most = a->max_q_len > 0 ? a->max_q_len : (a->total_q + a->batch - 1) / a->batch;
+        const WeighParams wp{a->lse, reinterpret_cast<float *>(at), a->acc_in, a->acc_out, a->acc_row_stride};
+        return launch_weigh(who, p, wp, a->head_dim, most * p.g, s);
+    }
     Plan pl;
     if (!make_plan(a, call == kExtend, shape_of(a), pl)) return fail(PKV_ERR_UNSUPPORTED, "%s: too many splits, keys or requests", who);
     if ((pl.unit || pl.spans) && !encode_pool(a, pl.nt, p)) return fail(PKV_ERR_CUDA, "%s: cuTensorMapEncodeTiled rejected the pool", who);
@@ -760,9 +501,7 @@ pkv_status run(const pkv_byte_args *a, Call call, void *ws, size_t ws_bytes, int
     const Params q = p;
     st = attend<Quant8>(who, a, pl, p, at + w.part + w.lse, s);
     if (st != PKV_OK) return st;
-    const WeighParams wp{q.lse, nullptr, a->acc_in, a->acc_out, a->acc_row_stride};
-    return launch_status(launch_chained(finish_kernel, dim3((static_cast<unsigned>(a->max_seq_len) + kFinishKeys - 1) / kFinishKeys,
-                                                            static_cast<unsigned>(a->batch)), dim3(256), 0, s, q, wp), who);
+    return launch_finish(who, q, WeighParams{q.lse, nullptr, a->acc_in, a->acc_out, a->acc_row_stride}, s);
 }
 
 }  // namespace
