@@ -193,23 +193,30 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 2) weigh_kernel(const Params
 
 // ---------------------------------------------------------------- many rows
 // The same on the 5th-generation tensor cores: S = K q^T with 128 keys as MMA rows and up to 128 query
-// rows as columns, fp16 in shared memory, fp32 in tensor memory.  Four warps take codes out of the
-// pool into fp16 lines (a tile of 128 keys ahead of its use), one thread issues the MMAs, and four warps have a
-// key per thread: its row of scores becomes weights and their sum.  Per score that is one
-// exponential, which bounds it: 16 of them per cycle and SM.
-constexpr int kTcKeys = 128, kTcTiles = 8, kTcRows = 128;   // keys of a tile, tiles of a block, query rows at a time
-constexpr int kTcThreads = 288;                             // warps 0-3 copy, 4-7 weigh, 8 issues
+// rows as columns, q as fp16 in shared memory, K as fp16 and S as fp32 in tensor memory.  The tiles of 128
+// keys of all requests and kv heads form one sequence that is cut into equal spans, one per SM.
+// Two groups of four warps copy the tiles in turn, a key per thread: its codes become fp16 in its
+// lane of tensor memory.  (Through shared memory instead, the fence before the tensor cores read it waits
+// for the next tiles' loads too: 107 us at 8 x 32 rows of 32 heads over up to 32768 keys.)  One thread issues the
+// MMAs, and two more groups take the tiles' scores in turn, a key per thread: its row becomes weights
+// and their sum.  Per score that is one exponential, which bounds it: 16 of them per cycle and SM.
+constexpr int kTcKeys = 128, kTcRows = 128;   // keys of a tile, query rows at a time
+constexpr int kTcThreads = 544;               // warps 0-7 copy, 8-15 weigh, 16 issues
+constexpr int kTcBatch = 1024;                // requests whose tiles are numbered in shared memory
+constexpr int kTcK = 4, kTcS = 2;             // tiles of keys, and of scores, in tensor memory
 
 template <int D>
 struct TcSmem {
-    static constexpr int kSlab = 128 * 128;                 // 128 rows of 64 dims
-    static constexpr int kQ = 0, kK = D / 64 * kSlab;       // q, then two tiles of keys
-    static constexpr int kBytes = 3 * (D / 64) * kSlab;
+    static constexpr int kSlab = 128 * 128;   // q: 128 rows of 64 dims
+    static constexpr int kOff = D / 64 * kSlab;             // [B + 1] first tile of each request
+    static constexpr int kBytes = kOff + (kTcBatch + 1) * 4;
+    static constexpr int kColS = kTcK * D / 2;              // tensor memory: keys, then scores
 };
 
 // Bounded wait; once one ran out, all of the block's later ones give up at once.
 __device__ __forceinline__ bool wait_or_leave(uint64_t *bar, uint32_t parity, volatile int *left, int32_t *err, uint64_t limit_ns) {
     if (*left) return false;
+    if (limit_ns >= 1000 && mbar_try_wait(bar, parity)) return true;   // (mostly; the clock is slow to read)
     if (wait_for(bar, parity, limit_ns)) return true;
     *left = 1;
     raise_flag(err, PKV_DEVERR_TIMEOUT);
@@ -223,233 +230,296 @@ __device__ __forceinline__ void put_16(uint8_t *slab, int row, int at, const uin
 }
 
 template <int D>
-__global__ void __launch_bounds__(kTcThreads, 2) weigh_many_kernel(const Params p, const WeighParams wp) {
+__global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const Params p, const WeighParams wp) {
     using C = TcSmem<D>;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ __align__(16) float f_s[kTcRows], minus_lse_s[kTcRows];   // score -> base-2 logit without K's scale; -lse2
     __shared__ __align__(16) int end_s[kTcRows];
-    __shared__ float scale_s[2][kTcKeys], acc_s[kTcTiles * kTcKeys];
-    __shared__ __align__(8) uint64_t bars[6];                // full, scored, free: two each
+    __shared__ __align__(8) uint64_t bars[2 * kTcK + 2 * kTcS + 1];
+    __shared__ int scan_s[kTcThreads / 32];
     __shared__ uint32_t tmem_slot;
     __shared__ int left_s, low_s;
     uint8_t *smem = aligned_smem<1024>(smem_raw);
-    uint64_t *full = bars, *scored = bars + 2, *freed = bars + 4;
+    int *off = reinterpret_cast<int *>(smem + C::kOff);
+    uint64_t *full = bars, *used = bars + kTcK, *scored = used + kTcK, *freed = scored + kTcS, *last = freed + kTcS;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    const int b = blockIdx.z, kh = blockIdx.y, k0 = blockIdx.x * (kTcTiles * kTcKeys);
-    pdl_wait();          // inputs may come from the previous kernel of the stream
-    const Req req = load_req(p, b, blockIdx.x == 0 && kh == 0 && threadIdx.x == 0);
-    if (k0 >= req.L) return;
-    const int tiles = min(kTcTiles, (req.L - k0 + kTcKeys - 1) / kTcKeys), rows = req.n * p.g;
     if (threadIdx.x == 0) {
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kTcK; ++i) {
             mbar_init(&full[i], 128);
+            mbar_init(&used[i], 1);
+        }
+        for (int i = 0; i < kTcS; ++i) {
             mbar_init(&scored[i], 1);
             mbar_init(&freed[i], 4);
         }
+        mbar_init(last, 1);
         mbar_init_fence();
         left_s = 0;
+        off[0] = 0;
     }
-    if (warp == 8) {
-        tc05::tmem_alloc(&tmem_slot, 256);
+    pdl_wait();          // inputs may come from the previous kernel of the stream
+    if (warp == 16) {
+        tc05::tmem_alloc(&tmem_slot, 512);
         tc05::tmem_relinquish();
     }
-    for (int i = threadIdx.x; i < kTcTiles * kTcKeys; i += kTcThreads) acc_s[i] = 0.f;
+    // ---- the sequence: off[b] = tiles of one kv head before request b
+    for (int b0 = 0, before = 0; b0 < p.batch; b0 += kTcThreads) {
+        const int b = b0 + threadIdx.x;
+        int v = 0;
+        if (b < p.batch) v = (load_req(p, b, blockIdx.x == 0).L + kTcKeys - 1) / kTcKeys;
+        int incl = v;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int x = __shfl_up_sync(0xffffffffu, incl, o);
+            if (lane >= o) incl += x;
+        }
+        __syncthreads();
+        if (lane == 31) scan_s[warp] = incl;
+        __syncthreads();
+        int all = 0;
+        for (int w = 0; w < kTcThreads / 32; ++w) {
+            if (w == warp) incl += all;
+            all += scan_s[w];
+        }
+        if (b < p.batch) off[b + 1] = before + incl;
+        before += all;
+    }
     tc05::fence_before_sync();
     __syncthreads();
     tc05::fence_after_sync();
     pdl_launch_next();   // (no sooner: a kernel that takes tensor memory must not come between)
     const uint32_t tbase = tmem_slot;
     volatile int *left = &left_s;
+    const int64_t all = static_cast<int64_t>(off[p.batch]) * p.hkv, per = (all + gridDim.x - 1) / gridDim.x;
+    int64_t pos = blockIdx.x * per;
+    const int64_t pos_end = min(all, pos + per);
+    constexpr int kPerRow = D / 16;   // lanes of a row of q
+    const int kj = lane % kPerRow;
+    const bool wide = ((reinterpret_cast<uintptr_t>(p.pool) | static_cast<uintptr_t>(p.tile_stride)) & 31) == 0;   // (pools are 16-byte aligned)
     uint32_t n = 0;          // tiles so far
-    for (int r0 = 0; r0 < rows; r0 += kTcRows) {
-        const int live = min(kTcRows, rows - r0), cols = (live + 15) / 16 * 16;
-        // ---- the rows of q, D/16 lanes each
-        if (threadIdx.x == 0) low_s = INT32_MAX;
-        __syncthreads();
-        if (warp < 8) {
-            constexpr int kPer = D / 16, kRows = 256 / kPer;
-            const int j = threadIdx.x % kPer;
-            int low = INT32_MAX;
+    int b = 0;
+    while (pos < pos_end) {
+        // ---- the next run of tiles of one request and kv head
+        for (int hi = p.batch; hi - b > 1;) {
+            const int mid = (b + hi) >> 1;
+            if (static_cast<int64_t>(off[mid]) * p.hkv <= pos) b = mid; else hi = mid;
+        }
+        const Req req = load_req(p, b, false);
+        const int of_b = off[b + 1] - off[b], in_b = static_cast<int>(pos - static_cast<int64_t>(off[b]) * p.hkv);
+        const int kh = in_b / of_b, t0 = in_b - kh * of_b;
+        const int tiles = static_cast<int>(min(static_cast<int64_t>(of_b - t0), pos_end - pos)), k0 = t0 * kTcKeys;
+        const int rows = req.n * p.g;
+        const bool report = kh == 0;
+        float *part = wp.part + (static_cast<int64_t>(kh) * p.batch + b) * p.tab.max_len;
+        if (rows == 0)
+            for (int i = threadIdx.x; i < min(tiles * kTcKeys, req.L - k0); i += kTcThreads) part[k0 + i] = 0.f;
+        // a copying or weighing warp's key of tile t, of those that its group takes (t % 2 = turn)
+        const int turn = static_cast<int>(((warp >> 2) ^ n) & 1), mine = (warp & 3) * 32 + lane;
+        auto look_up = [&](int t) -> int32_t {
+            const int key = k0 + t * kTcKeys + mine;
+            return t < tiles && key < req.L ? static_cast<int32_t>(quant::slot_of(p.tab, req.base, key)) : -3;
+        };
+        uint32_t code[D / 4];    // copying: the next tile's codes
+        int32_t slot = -3;       // and the slot of the one after it
+        auto load = [&](int32_t from) {
+            if (report && (from == -1 || from == -2)) raise_flag(p.err, from == -1 ? PKV_DEVERR_RANGE : PKV_DEVERR_CONTIG);
+            const uint8_t *a = from >= 0 ? piece_at<D>(p, from, kh) + (from & ((1 << p.t_shift) - 1)) * D : nullptr;
 #pragma unroll
-            for (int i = 0; i < kTcRows / kRows; ++i) {
-                const int row = i * kRows + threadIdx.x / kPer, rr = r0 + row, tok = token_of(p, rr);
-                if (row >= cols) break;              // (a warp's rows are whole sixteens or none, or it has one row group)
-                const bool in = row < live;
-                uint32_t w[8];
+            for (int i = 0; i < D / 32; ++i) {
+                if (a && wide) {
+                    quant::load_32(a + 32 * i, *reinterpret_cast<uint32_t(*)[8]>(code + 8 * i));
+                } else if (a) {
 #pragma unroll
-                for (int e = 0; e < 8; ++e) w[e] = 0;
-                if (in) {
-                    const uint4 *src = reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(req.qo0 + tok) * p.q_stride +
-                                                                       (kh * p.g + rr - tok * p.g) * D + j * 16);
-                    const uint4 x = __ldg(src), y = __ldg(src + 1);
-                    w[0] = x.x; w[1] = x.y; w[2] = x.z; w[3] = x.w;
-                    w[4] = y.x; w[5] = y.y; w[6] = y.z; w[7] = y.w;
-                }
-                uint32_t top = 0;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) top = __vmaxu2(top, w[e] & 0x7fff7fffu);
-                top = max(top & 0xffffu, top >> 16);
-#pragma unroll
-                for (int o = 1; o < kPer; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                int e2 = min(126, 6 + 127 - static_cast<int>(top >> 7));   // (see start_segment)
-                if (top == 0 || top >= 0x7f80u) e2 = 0;
-                const float up = __int_as_float((e2 + 127) << 23), down = __int_as_float((127 - e2) << 23);
-                uint32_t h[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) h[e] = pack_f16x2(bf16_lo(w[e]) * up, bf16_hi(w[e]) * up);
-                put_16(smem + C::kQ + j / 4 * C::kSlab, row, j % 4, h);
-                if (j == 0) {
-                    int end = 0;                     // (rows past the last have bound 0: nothing of them counts)
-                    float lse = 0.f;
-                    if (in) {
-                        lse = wp.lse[static_cast<int64_t>(req.qo0 + tok) * p.hq + kh * p.g + rr - tok * p.g] * kLog2e;
-                        end = !p.qo_indptr ? req.L : p.kv_end ? p.kv_end[req.qo0 + tok] : req.L - req.n + tok + 1;
-                        if (end < 0 || end > req.L) {
-                            if (blockIdx.x == 0 && kh == 0) raise_flag(p.err, PKV_DEVERR_RANGE);
-                            end = 0;
-                        }
-                        if (lse == -INFINITY) end = 0;
+                    for (int e = 0; e < 8; e += 4) {
+                        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(a + 32 * i + 4 * e));
+                        code[8 * i + e] = x.x; code[8 * i + e + 1] = x.y; code[8 * i + e + 2] = x.z; code[8 * i + e + 3] = x.w;
                     }
-                    f_s[row] = p.scale_log2 * down;
-                    minus_lse_s[row] = -lse;
-                    end_s[row] = end;
-                    low = min(low, end);
+                } else {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) code[8 * i + e] = 0;
                 }
             }
-            low = __reduce_min_sync(0xffffffffu, low);
-            if (lane == 0) atomicMin(&low_s, low);
-            fence_proxy_async_smem();                // before the tensor cores read it
-        }
-        __syncthreads();
-        const int low = low_s;
-        if (warp < 4) {
-            // ------------------------------------------------------------ keys: 32 of a tile to a warp
-            constexpr int kPer = D / 16, kAtOnce = 32 / kPer, kRounds = 32 / kAtOnce;   // lanes of a key, keys at a time
-            const int j = lane % kPer;
-            bool ok = true;
-            uint4 code[kRounds];
-            float scale;
-            auto load = [&](int t) {
-                const int key = k0 + t * kTcKeys + warp * 32 + lane;
-                const int64_t slot = key < req.L ? quant::slot_of(p.tab, req.base, key) : -3;
-                if (r0 == 0 && kh == 0 && (slot == -1 || slot == -2)) raise_flag(p.err, slot == -1 ? PKV_DEVERR_RANGE : PKV_DEVERR_CONTIG);
-                const uint8_t *piece = slot >= 0 ? piece_at<D>(p, slot, kh) : nullptr;
-                const uint8_t *row = piece ? piece + (slot & ((1 << p.t_shift) - 1)) * D : nullptr;
-                scale = piece ? byte::scale_value(__ldg(scales_at<D>(p, piece, kh))) : 1.f;
+        };
+        auto scale_of_key = [&](int32_t from) { return from >= 0 ? byte::scale_value(__ldg(scales_at<D>(p, piece_at<D>(p, from, kh), kh))) : 1.f; };
+        for (int r0 = 0; r0 < rows; r0 += kTcRows) {
+            const int live = min(kTcRows, rows - r0), cols = (live + 31) / 32 * 32;
+            if (threadIdx.x == 0) low_s = INT32_MAX;
+            float scale = 1.f;   // weighing: K's scale of the next tile's key
+            if (warp < 8) {      // (their latency passes under that of q)
+                load(look_up(turn));
+                slot = look_up(turn + 2);
+            }
+            __syncthreads();
+            if (warp >= 8 && warp < 16) {
+                // ---- the rows of q, D/16 lanes each
+                constexpr int kRows = 256 / kPerRow;
+                const int tid = threadIdx.x - 256;
+                int low = INT32_MAX;
+                uint32_t w[kTcRows / kRows][8];
 #pragma unroll
-                for (int i = 0; i < kRounds; ++i) {
-                    const uint8_t *a = from_lane(row, i * kAtOnce + lane / kPer);
-                    code[i] = a ? ld_stream_16(a + j * 16) : make_uint4(0, 0, 0, 0);
+                for (int i = 0; i < kTcRows / kRows; ++i) {
+                    const int row = i * kRows + tid / kPerRow, rr = r0 + row, tok = token_of(p, rr);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) w[i][e] = 0;
+                    if (row < live) {
+                        const uint4 *src = reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(req.qo0 + tok) * p.q_stride +
+                                                                           (kh * p.g + rr - tok * p.g) * D + kj * 16);
+                        const uint4 x = __ldg(src), y = __ldg(src + 1);
+                        w[i][0] = x.x; w[i][1] = x.y; w[i][2] = x.z; w[i][3] = x.w;
+                        w[i][4] = y.x; w[i][5] = y.y; w[i][6] = y.z; w[i][7] = y.w;
+                    }
                 }
-            };
-            load(0);
-            for (int t = 0; t < tiles; ++t) {
-                const uint32_t m = n + t, s = m & 1;
-                if (m >= 2) ok = __all_sync(0xffffffffu, ok && wait_or_leave(&freed[s], ((m >> 1) & 1) ^ 1, left, p.err, p.wait_ns));
-                if (!ok) break;
-                uint8_t *tile = smem + C::kK + s * (D / 64) * C::kSlab;
 #pragma unroll
-                for (int i = 0; i < kRounds; ++i) {
-                    const uint32_t w[4] = {code[i].x, code[i].y, code[i].z, code[i].w};
+                for (int i = 0; i < kTcRows / kRows; ++i) {
+                    const int row = i * kRows + tid / kPerRow, rr = r0 + row, tok = token_of(p, rr);
+                    uint32_t top = 0;
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) top = __vmaxu2(top, w[i][e] & 0x7fff7fffu);
+                    top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+                    for (int o = 1; o < kPerRow; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
+                    int e2 = min(126, 6 + 127 - static_cast<int>(top >> 7));   // (see start_segment)
+                    if (top == 0 || top >= 0x7f80u) e2 = 0;
+                    const float up = __int_as_float((e2 + 127) << 23), down = __int_as_float((127 - e2) << 23);
                     uint32_t h[8];
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) h[e] = e % 2 ? byte::hi_to_f16(w[e / 2]) : byte::lo_to_f16(w[e / 2]);
-                    put_16(tile + j / 4 * C::kSlab, warp * 32 + i * kAtOnce + lane / kPer, j % 4, h);
-                }
-                scale_s[s][warp * 32 + lane] = scale;
-                fence_proxy_async_smem();
-                mbar_arrive(&full[s]);
-                if (t + 1 < tiles) load(t + 1);
-            }
-        } else if (warp == 8) {
-            // ------------------------------------------------------------ S = K q^T
-            const uint32_t idesc = tc05::idesc_f16_f32(kTcKeys, cols, false, false);
-            bool ok = true;
-            for (int t = 0; t < tiles; ++t) {
-                const uint32_t m = n + t, s = m & 1;
-                ok = __all_sync(0xffffffffu, ok && wait_or_leave(&full[s], (m >> 1) & 1, left, p.err, p.wait_ns));
-                if (!ok) break;
-                tc05::fence_after_sync();
-                if (lane == 0) {
-                    const uint64_t kd = tc05::smem_desc(smem + C::kK + s * (D / 64) * C::kSlab, 16, 1024);
-                    const uint64_t qd = tc05::smem_desc(smem + C::kQ, 16, 1024);
-#pragma unroll
-                    for (int sl = 0; sl < D / 64; ++sl)
-#pragma unroll
-                        for (int k = 0; k < 4; ++k)   // 16 dims: +32 bytes
-                            tc05::mma_ss(tbase + s * kTcRows, kd + static_cast<uint64_t>((sl * C::kSlab + k * 32) >> 4),
-                                         qd + static_cast<uint64_t>((sl * C::kSlab + k * 32) >> 4), idesc, (sl | k) ? 1u : 0u);
-                    tc05::commit(&scored[s]);
-                }
-                __syncwarp();
-            }
-        } else {
-            // ------------------------------------------------------------ weights: a key per thread
-            const int quarter = warp & 3, row = quarter * 32 + lane;
-            bool ok = true;
-            for (int t = 0; t < tiles; ++t) {
-                const uint32_t m = n + t, s = m & 1;
-                // (full: the scales; it stays in this phase until `freed` says that they were read)
-                ok = __all_sync(0xffffffffu, ok && wait_or_leave(&full[s], (m >> 1) & 1, left, p.err, p.wait_ns) &&
-                                                 wait_or_leave(&scored[s], (m >> 1) & 1, left, p.err, p.wait_ns));
-                if (!ok) break;
-                tc05::fence_after_sync();
-                const float ks1 = scale_s[s][row];
-                const uint64_t ks = pair(ks1, ks1);
-                const int key = k0 + t * kTcKeys + row;
-                const bool whole = k0 + (t + 1) * kTcKeys <= low;
-                const uint32_t from = tc05::taddr(tbase, quarter * 32, s * kTcRows);
-                uint64_t sum0 = 0, sum1 = 0;
-                for (int c0 = 0; c0 < cols; c0 += 16) {
-                    float x[16];
-                    tc05::ld_x16(from + c0, x);
-                    tc05::wait_ld();
-#pragma unroll
-                    for (int e = 0; e < 16; e += 4) {
-                        const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(&f_s[c0 + e]);
-                        const ulonglong2 l = *reinterpret_cast<const ulonglong2 *>(&minus_lse_s[c0 + e]);
-                        const float2 y0 = unpair(fma2(mul2(pair(x[e], x[e + 1]), f.x), ks, l.x));
-                        const float2 y1 = unpair(fma2(mul2(pair(x[e + 2], x[e + 3]), f.y), ks, l.y));
-                        float w0 = ex2(y0.x), w1 = ex2(y0.y), w2 = ex2(y1.x), w3 = ex2(y1.y);
-                        if (!whole) {
-                            const int4 end = *reinterpret_cast<const int4 *>(&end_s[c0 + e]);
-                            w0 = key < end.x ? w0 : 0.f;
-                            w1 = key < end.y ? w1 : 0.f;
-                            w2 = key < end.z ? w2 : 0.f;
-                            w3 = key < end.w ? w3 : 0.f;
+                    for (int e = 0; e < 8; ++e) h[e] = pack_f16x2(bf16_lo(w[i][e]) * up, bf16_hi(w[i][e]) * up);
+                    put_16(smem + kj / 4 * C::kSlab, row, kj % 4, h);
+                    if (kj == 0 && row < cols) {
+                        int end = 0;                 // (rows past the last have bound 0: nothing of them counts)
+                        float lse = 0.f;
+                        if (row < live) {
+                            lse = wp.lse[static_cast<int64_t>(req.qo0 + tok) * p.hq + kh * p.g + rr - tok * p.g] * kLog2e;
+                            end = !p.qo_indptr ? req.L : p.kv_end ? p.kv_end[req.qo0 + tok] : req.L - req.n + tok + 1;
+                            if (end < 0 || end > req.L) {
+                                if (report) raise_flag(p.err, PKV_DEVERR_RANGE);
+                                end = 0;
+                            }
+                            if (lse == -INFINITY) end = 0;
                         }
-                        sum0 = add2(sum0, pair(w0, w1));
-                        sum1 = add2(sum1, pair(w2, w3));
+                        f_s[row] = p.scale_log2 * down;
+                        minus_lse_s[row] = -lse;
+                        end_s[row] = end;
+                        low = min(low, end);
                     }
                 }
-                const float2 a = unpair(add2(sum0, sum1));
-                acc_s[t * kTcKeys + row] += a.x + a.y;
-                tc05::fence_before_sync();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&freed[s]);
+                low = __reduce_min_sync(0xffffffffu, low);
+                if (lane == 0) atomicMin(&low_s, low);
+                fence_proxy_async_smem();            // before the tensor cores read it
             }
+            __syncthreads();
+            const int low = low_s;
+            if (warp < 8) {
+                // -------------------------------------------------------- keys
+                bool ok = true;
+                for (int t = turn; t < tiles; t += 2) {
+                    const uint32_t m = n + t, a = m % kTcK;
+                    if (m >= kTcK) ok = __all_sync(0xffffffffu, ok && wait_or_leave(&used[a], ((m / kTcK) & 1) ^ 1, left, p.err, p.wait_ns));
+                    if (!ok) break;
+                    tc05::fence_after_sync();
+                    const uint32_t to = tc05::taddr(tbase, (warp & 3) * 32, a * (D / 2));
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) {
+                        uint32_t h[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) h[e] = e % 2 ? byte::hi_to_f16(code[8 * i + e / 2]) : byte::lo_to_f16(code[8 * i + e / 2]);
+                        tc05::st_x16_u32(to + 16 * i, h);
+                    }
+                    load(slot);
+                    slot = look_up(t + 4);
+                    tc05::wait_st();
+                    tc05::fence_before_sync();
+                    mbar_arrive(&full[a]);
+                }
+            } else if (warp == 16) {
+                // -------------------------------------------------------- S = K q^T
+                const uint32_t idesc = tc05::idesc_f16_f32(kTcKeys, cols, false, false);
+                bool ok = true;
+                for (int t = 0; t < tiles; ++t) {
+                    const uint32_t m = n + t, a = m % kTcK, s = m % kTcS;
+                    ok = __all_sync(0xffffffffu, ok && wait_or_leave(&full[a], (m / kTcK) & 1, left, p.err, p.wait_ns) &&
+                                                     (m < kTcS || wait_or_leave(&freed[s], ((m / kTcS) & 1) ^ 1, left, p.err, p.wait_ns)));
+                    if (!ok) break;
+                    tc05::fence_after_sync();
+                    if (lane == 0) {
+                        const uint64_t qd = tc05::smem_desc(smem, 16, 1024);
+#pragma unroll
+                        for (int sl = 0; sl < D / 64; ++sl)
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)   // 16 dims: 8 columns of K, 32 bytes of q
+                                tc05::mma_ts(tbase + C::kColS + s * kTcRows, tbase + a * (D / 2) + (sl * 4 + k) * 8,
+                                             qd + static_cast<uint64_t>((sl * C::kSlab + k * 32) >> 4), idesc, (sl | k) ? 1u : 0u);
+                        tc05::commit(&scored[s]);
+                        tc05::commit(&used[a]);
+                    }
+                    __syncwarp();
+                }
+            } else {
+                // -------------------------------------------------------- weights: a key per thread
+                bool ok = true;
+                scale = scale_of_key(look_up(turn));
+                slot = look_up(turn + 2);
+                for (int t = turn; t < tiles; t += 2) {
+                    const uint32_t m = n + t, s = m % kTcS;
+                    const uint64_t ks = pair(scale, scale);
+                    scale = scale_of_key(slot);
+                    slot = look_up(t + 4);
+                    ok = __all_sync(0xffffffffu, ok && wait_or_leave(&scored[s], (m / kTcS) & 1, left, p.err, p.wait_ns));
+                    if (!ok) break;
+                    tc05::fence_after_sync();
+                    const int key = k0 + t * kTcKeys + mine;
+                    const bool whole = k0 + (t + 1) * kTcKeys <= low;
+                    const uint32_t from = tc05::taddr(tbase, (warp & 3) * 32, C::kColS + s * kTcRows);
+                    uint64_t sum0 = 0, sum1 = 0;
+                    for (int c0 = 0; c0 < cols; c0 += 32) {
+                        float x[32];
+                        tc05::ld_x16(from + c0, *reinterpret_cast<float(*)[16]>(x));
+                        tc05::ld_x16(from + c0 + 16, *reinterpret_cast<float(*)[16]>(x + 16));
+                        tc05::wait_ld();
+#pragma unroll
+                        for (int e = 0; e < 32; e += 4) {
+                            const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(&f_s[c0 + e]);
+                            const ulonglong2 l = *reinterpret_cast<const ulonglong2 *>(&minus_lse_s[c0 + e]);
+                            const float2 y0 = unpair(fma2(mul2(pair(x[e], x[e + 1]), f.x), ks, l.x));
+                            const float2 y1 = unpair(fma2(mul2(pair(x[e + 2], x[e + 3]), f.y), ks, l.y));
+                            float w0 = ex2(y0.x), w1 = ex2(y0.y), w2 = ex2(y1.x), w3 = ex2(y1.y);
+                            if (!whole) {
+                                const int4 end = *reinterpret_cast<const int4 *>(&end_s[c0 + e]);
+                                w0 = key < end.x ? w0 : 0.f;
+                                w1 = key < end.y ? w1 : 0.f;
+                                w2 = key < end.z ? w2 : 0.f;
+                                w3 = key < end.w ? w3 : 0.f;
+                            }
+                            sum0 = add2(sum0, pair(w0, w1));
+                            sum1 = add2(sum1, pair(w2, w3));
+                        }
+                    }
+                    tc05::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&freed[s]);
+                    const float2 a = unpair(add2(sum0, sum1));
+                    if (key < req.L) part[key] = r0 == 0 ? a.x + a.y : part[key] + (a.x + a.y);
+                }
+            }
+            n += tiles;
+            tc05::fence_before_sync();
+            __syncthreads();
+            tc05::fence_after_sync();
+            if (*left) break;
         }
-        n += tiles;
-        tc05::fence_before_sync();
-        __syncthreads();
-        tc05::fence_after_sync();
         if (*left) break;
+        pos += tiles;
     }
-    if (warp == 8) {
+    __syncthreads();
+    if (warp == 16) {
         if (*left) {   // MMAs that nobody waited for end before their memory is given back
-            __shared__ uint64_t last;
             if (lane == 0) {
-                mbar_init(&last, 1);
-                mbar_init_fence();
-                tc05::commit(&last);
-                mbar_wait(&last, 0);
+                tc05::commit(last);
+                mbar_wait(last, 0);
             }
             __syncwarp();
         }
-        tc05::tmem_dealloc(tbase, 256);
+        tc05::tmem_dealloc(tbase, 512);
     }
-    float *part = wp.part + (static_cast<int64_t>(kh) * p.batch + b) * p.tab.max_len;
-    for (int i = threadIdx.x; i < min(kTcTiles * kTcKeys, req.L - k0); i += kTcThreads) part[k0 + i] = acc_s[i];
 }
 
 __global__ void __launch_bounds__(256) add_kernel(const Params p, const WeighParams wp) {
@@ -522,12 +592,12 @@ pkv_status launch_weigh(const char *who, const Params &p, const WeighParams &wp,
     const unsigned L = static_cast<unsigned>(p.tab.max_len), B = static_cast<unsigned>(p.batch), H = static_cast<unsigned>(p.hkv);
     if (L == 0) return ok();
     pkv_status st;
-    if (rows >= kManyRows) {
+    if (rows >= kManyRows && p.batch <= kTcBatch) {
         auto *kern = head_dim == 128 ? weigh_many_kernel<128> : weigh_many_kernel<64>;
         const size_t smem = (head_dim == 128 ? TcSmem<128>::kBytes : TcSmem<64>::kBytes) + 1024;
         if (raise_smem_limit(reinterpret_cast<const void *>(kern)) < smem)
             return fail(PKV_ERR_CUDA, "%s: cannot raise the shared-memory limit", who);
-        st = launch_status(launch_chained(kern, dim3((L + kTcTiles * kTcKeys - 1) / (kTcTiles * kTcKeys), H, B), dim3(kTcThreads), smem, s, p, wp), who);
+        st = launch_status(launch_chained(kern, dim3(static_cast<unsigned>(std::max(1, sm_count()))), dim3(kTcThreads), smem, s, p, wp), who);
     } else {
         auto *kern = head_dim == 128 ? weigh_kernel<128> : weigh_kernel<64>;
         st = launch_status(launch_chained(kern, dim3((L + kWeighKeys - 1) / kWeighKeys, H, B), dim3(kWeighWarps * 32), 0, s, p, wp), who);

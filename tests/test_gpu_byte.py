@@ -588,6 +588,23 @@ def test_weights_of_extreme_rows(B):
     check(cache, q, out, lse, [5], ends, acc=acc)
 
 
+@pytest.mark.parametrize("D,rows", [(128, 5), (128, 40), (64, 40)])
+def test_weights_over_strided_tiles(B, D, rows):
+    """Tiles a multiple of 16 bytes apart, and of no more; more rows than one pass takes."""
+    rng = np.random.default_rng(32 + D + rows)
+    cache = Cache(rng, [300, 129], 64, 2, D)
+    q = to_bf16(values(rng, (2 * rows, 8, D)))
+    out, lse, e = extend(B, cache, q, [rows, rows])
+    nbytes = cache.pool.data.shape[1]
+    pool = torch.zeros((len(cache.pool.data), nbytes + 16), dtype=torch.uint8, device=DEV)[:, :nbytes]
+    pool.copy_(up(cache.pool.data))
+    acc, err = table_of(cache, rng, 0.0), err_word()
+    a = cache.args(B, "table", q, None, lse=lse, qo_indptr=i32([0, rows, 2 * rows]), acc_out=acc, pool=pool)
+    B.pkv_byte_weights(a, torch.empty(B.pkv_byte_weights_workspace_size(a), dtype=torch.uint8, device=DEV), err)
+    assert err.item() == 0
+    check(cache, q, out, lse, [rows, rows], acc=acc, held=rows * 4 > 128)
+
+
 def test_weights_flags(B):
     rng = np.random.default_rng(31)
     cache = Cache(rng, [40, 50], 16, 1, 64)
