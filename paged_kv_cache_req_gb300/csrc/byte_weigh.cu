@@ -195,15 +195,15 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 2) weigh_kernel(const Params
 // The same on the 5th-generation tensor cores: S = K q^T with 128 keys as MMA rows and up to 128 query
 // rows as columns, q as fp16 in shared memory, K as fp16 and S as fp32 in tensor memory.  The tiles of 128
 // keys of all requests and kv heads form one sequence that is cut into equal spans, one per SM.
-// Two groups of four warps copy the tiles in turn, a key per thread: its codes become fp16 in its
+// Four warps copy the tiles, a key per thread: its codes, loaded two tiles ahead, become fp16 in its
 // lane of tensor memory.  (Through shared memory instead, the fence before the tensor cores read it waits
 // for the next tiles' loads too: 107 us at 8 x 32 rows of 32 heads over up to 32768 keys.)  One thread issues the
-// MMAs, and two more groups take the tiles' scores in turn, a key per thread: its row becomes weights
+// MMAs, and two groups of four warps take the tiles' scores in turn, a key per thread: its row becomes weights
 // and their sum.  Per score that is one exponential, which bounds it: 16 of them per cycle and SM.
 constexpr int kTcKeys = 128, kTcRows = 128;   // keys of a tile, query rows at a time
-constexpr int kTcThreads = 544;               // warps 0-7 copy, 8-15 weigh, 16 issues
+constexpr int kTcThreads = 416;               // warps 0-3 copy, 4-11 weigh, 12 issues
 constexpr int kTcBatch = 1024;                // requests whose tiles are numbered in shared memory
-constexpr int kTcK = 4, kTcS = 2;             // tiles of keys, and of scores, in tensor memory
+constexpr int kTcK = 2, kTcS = 3;             // tiles of keys, and of scores, in tensor memory
 
 template <int D>
 struct TcSmem {
@@ -258,7 +258,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const Params 
         off[0] = 0;
     }
     pdl_wait();          // inputs may come from the previous kernel of the stream
-    if (warp == 16) {
+    if (warp == 12) {
         tc05::tmem_alloc(&tmem_slot, 512);
         tc05::tmem_relinquish();
     }
@@ -312,47 +312,54 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const Params 
         float *part = wp.part + (static_cast<int64_t>(kh) * p.batch + b) * p.tab.max_len;
         if (rows == 0)
             for (int i = threadIdx.x; i < min(tiles * kTcKeys, req.L - k0); i += kTcThreads) part[k0 + i] = 0.f;
-        // a copying or weighing warp's key of tile t, of those that its group takes (t % 2 = turn)
-        const int turn = static_cast<int>(((warp >> 2) ^ n) & 1), mine = (warp & 3) * 32 + lane;
-        auto look_up = [&](int t) -> int32_t {
+        // a copying or weighing thread's key in each tile
+        const int mine = (warp & 3) * 32 + lane;
+        // (a warp stops where it first uses what it loaded: an entry of the table is looked at, and a scale
+        // converted, a tile after their loads)
+        auto entry = [&](int t) {
             const int key = k0 + t * kTcKeys + mine;
-            return t < tiles && key < req.L ? static_cast<int32_t>(quant::slot_of(p.tab, req.base, key)) : -3;
+            int32_t first = -4;
+            if (t < tiles && key < req.L) first = __ldg(p.tab.r2t + req.base + (key & ~p.tab.ps_mask));
+            return first;
         };
-        uint32_t code[D / 4];    // copying: the next tile's codes
-        int32_t slot = -3;       // and the slot of the one after it
-        auto load = [&](int32_t from) {
+        auto slot_at = [&](int32_t first, int t) -> int32_t {   // (see slot_of; -3: no key)
+            if (first == -4 && !(t < tiles && k0 + t * kTcKeys + mine < req.L)) return -3;
+            if (first < 0 || first >= (p.tab.num_pages << p.tab.ps_shift)) return -1;
+            if (first & p.tab.ps_mask) return -2;
+            return first + ((k0 + t * kTcKeys + mine) & p.tab.ps_mask);
+        };
+        auto load = [&](int32_t from, uint32_t (&c)[D / 4]) {
             if (report && (from == -1 || from == -2)) raise_flag(p.err, from == -1 ? PKV_DEVERR_RANGE : PKV_DEVERR_CONTIG);
             const uint8_t *a = from >= 0 ? piece_at<D>(p, from, kh) + (from & ((1 << p.t_shift) - 1)) * D : nullptr;
 #pragma unroll
             for (int i = 0; i < D / 32; ++i) {
                 if (a && wide) {
-                    quant::load_32(a + 32 * i, *reinterpret_cast<uint32_t(*)[8]>(code + 8 * i));
+                    quant::load_32(a + 32 * i, *reinterpret_cast<uint32_t(*)[8]>(c + 8 * i));
                 } else if (a) {
 #pragma unroll
                     for (int e = 0; e < 8; e += 4) {
                         const uint4 x = __ldg(reinterpret_cast<const uint4 *>(a + 32 * i + 4 * e));
-                        code[8 * i + e] = x.x; code[8 * i + e + 1] = x.y; code[8 * i + e + 2] = x.z; code[8 * i + e + 3] = x.w;
+                        c[8 * i + e] = x.x; c[8 * i + e + 1] = x.y; c[8 * i + e + 2] = x.z; c[8 * i + e + 3] = x.w;
                     }
                 } else {
 #pragma unroll
-                    for (int e = 0; e < 8; ++e) code[8 * i + e] = 0;
+                    for (int e = 0; e < 8; ++e) c[8 * i + e] = 0;
                 }
             }
         };
-        auto scale_of_key = [&](int32_t from) { return from >= 0 ? byte::scale_value(__ldg(scales_at<D>(p, piece_at<D>(p, from, kh), kh))) : 1.f; };
+        auto scale_byte = [&](int32_t from) {
+            uint32_t e = 1;
+            if (from >= 0) e = __ldg(scales_at<D>(p, piece_at<D>(p, from, kh), kh));
+            return e;
+        };
         for (int r0 = 0; r0 < rows; r0 += kTcRows) {
             const int live = min(kTcRows, rows - r0), cols = (live + 31) / 32 * 32;
             if (threadIdx.x == 0) low_s = INT32_MAX;
-            float scale = 1.f;   // weighing: K's scale of the next tile's key
-            if (warp < 8) {      // (their latency passes under that of q)
-                load(look_up(turn));
-                slot = look_up(turn + 2);
-            }
             __syncthreads();
-            if (warp >= 8 && warp < 16) {
+            if (warp >= 4 && warp < 12) {
                 // ---- the rows of q, D/16 lanes each
                 constexpr int kRows = 256 / kPerRow;
-                const int tid = threadIdx.x - 256;
+                const int tid = threadIdx.x - 128;
                 int low = INT32_MAX;
                 uint32_t w[kTcRows / kRows][8];
 #pragma unroll
@@ -406,31 +413,42 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const Params 
                 if (lane == 0) atomicMin(&low_s, low);
                 fence_proxy_async_smem();            // before the tensor cores read it
             }
-            __syncthreads();
-            const int low = low_s;
-            if (warp < 8) {
+            if (warp >= 4) named_bar_sync(1, kTcThreads - 128);   // (the copying warps go ahead)
+            if (warp < 4) {
                 // -------------------------------------------------------- keys
                 bool ok = true;
-                for (int t = turn; t < tiles; t += 2) {
+                uint32_t code[2][D / 4];   // the next two tiles' codes
+                int32_t next[2];           // the table's entries of the two after them
+                next[0] = entry(0);
+                next[1] = entry(1);
+                load(slot_at(next[0], 0), code[0]);
+                load(slot_at(next[1], 1), code[1]);
+                next[0] = entry(2);
+                next[1] = entry(3);
+                auto put = [&](int t, uint32_t (&c)[D / 4], int32_t &ahead) {
                     const uint32_t m = n + t, a = m % kTcK;
                     if (m >= kTcK) ok = __all_sync(0xffffffffu, ok && wait_or_leave(&used[a], ((m / kTcK) & 1) ^ 1, left, p.err, p.wait_ns));
-                    if (!ok) break;
+                    if (!ok) return;
                     tc05::fence_after_sync();
-                    const uint32_t to = tc05::taddr(tbase, (warp & 3) * 32, a * (D / 2));
+                    const uint32_t to = tc05::taddr(tbase, warp * 32, a * (D / 2));
 #pragma unroll
                     for (int i = 0; i < D / 32; ++i) {
                         uint32_t h[16];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) h[e] = e % 2 ? byte::hi_to_f16(code[8 * i + e / 2]) : byte::lo_to_f16(code[8 * i + e / 2]);
+                        for (int e = 0; e < 16; ++e) h[e] = e % 2 ? byte::hi_to_f16(c[8 * i + e / 2]) : byte::lo_to_f16(c[8 * i + e / 2]);
                         tc05::st_x16_u32(to + 16 * i, h);
                     }
-                    load(slot);
-                    slot = look_up(t + 4);
+                    load(slot_at(ahead, t + 2), c);
+                    ahead = entry(t + 4);
                     tc05::wait_st();
                     tc05::fence_before_sync();
                     mbar_arrive(&full[a]);
+                };
+                for (int t = 0; t < tiles && ok; t += 2) {
+                    put(t, code[0], next[0]);
+                    if (t + 1 < tiles && ok) put(t + 1, code[1], next[1]);
                 }
-            } else if (warp == 16) {
+            } else if (warp == 12) {
                 // -------------------------------------------------------- S = K q^T
                 const uint32_t idesc = tc05::idesc_f16_f32(kTcKeys, cols, false, false);
                 bool ok = true;
@@ -456,13 +474,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const Params 
             } else {
                 // -------------------------------------------------------- weights: a key per thread
                 bool ok = true;
-                scale = scale_of_key(look_up(turn));
-                slot = look_up(turn + 2);
+                const int turn = static_cast<int>(((warp >> 2) + 1 + n) & 1);   // the group's tiles: t % 2 = turn
+                const int low = low_s;
+                const int32_t first = entry(turn);
+                int32_t next = entry(turn + 2);
+                uint32_t e_next = scale_byte(slot_at(first, turn));   // K's scale of the next tile's key
                 for (int t = turn; t < tiles; t += 2) {
                     const uint32_t m = n + t, s = m % kTcS;
+                    const float scale = byte::scale_value(e_next);
                     const uint64_t ks = pair(scale, scale);
-                    scale = scale_of_key(slot);
-                    slot = look_up(t + 4);
+                    e_next = scale_byte(slot_at(next, t + 2));
+                    next = entry(t + 4);
                     ok = __all_sync(0xffffffffu, ok && wait_or_leave(&scored[s], (m / kTcS) & 1, left, p.err, p.wait_ns));
                     if (!ok) break;
                     tc05::fence_after_sync();
@@ -470,27 +492,29 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const Params 
                     const bool whole = k0 + (t + 1) * kTcKeys <= low;
                     const uint32_t from = tc05::taddr(tbase, (warp & 3) * 32, C::kColS + s * kTcRows);
                     uint64_t sum0 = 0, sum1 = 0;
-                    for (int c0 = 0; c0 < cols; c0 += 32) {
-                        float x[32];
-                        tc05::ld_x16(from + c0, *reinterpret_cast<float(*)[16]>(x));
-                        tc05::ld_x16(from + c0 + 16, *reinterpret_cast<float(*)[16]>(x + 16));
-                        tc05::wait_ld();
+                    for (int c0 = 0; c0 < cols; c0 += 64) {
+                        float x[64];         // (columns behind `cols` may hold anything: they are not looked at)
+                        tc05::ld_x64(from + c0, x);
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(&f_s[c0 + e]);
-                            const ulonglong2 l = *reinterpret_cast<const ulonglong2 *>(&minus_lse_s[c0 + e]);
-                            const float2 y0 = unpair(fma2(mul2(pair(x[e], x[e + 1]), f.x), ks, l.x));
-                            const float2 y1 = unpair(fma2(mul2(pair(x[e + 2], x[e + 3]), f.y), ks, l.y));
-                            float w0 = ex2(y0.x), w1 = ex2(y0.y), w2 = ex2(y1.x), w3 = ex2(y1.y);
-                            if (!whole) {
-                                const int4 end = *reinterpret_cast<const int4 *>(&end_s[c0 + e]);
-                                w0 = key < end.x ? w0 : 0.f;
-                                w1 = key < end.y ? w1 : 0.f;
-                                w2 = key < end.z ? w2 : 0.f;
-                                w3 = key < end.w ? w3 : 0.f;
+                        for (int h = 0; h < 64; h += 32) {
+                            if (c0 + h >= cols) break;
+#pragma unroll
+                            for (int e = h; e < h + 32; e += 4) {
+                                const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(&f_s[c0 + e]);
+                                const ulonglong2 l = *reinterpret_cast<const ulonglong2 *>(&minus_lse_s[c0 + e]);
+                                const float2 y0 = unpair(fma2(mul2(pair(x[e], x[e + 1]), f.x), ks, l.x));
+                                const float2 y1 = unpair(fma2(mul2(pair(x[e + 2], x[e + 3]), f.y), ks, l.y));
+                                float w0 = ex2(y0.x), w1 = ex2(y0.y), w2 = ex2(y1.x), w3 = ex2(y1.y);
+                                if (!whole) {
+                                    const int4 end = *reinterpret_cast<const int4 *>(&end_s[c0 + e]);
+                                    w0 = key < end.x ? w0 : 0.f;
+                                    w1 = key < end.y ? w1 : 0.f;
+                                    w2 = key < end.z ? w2 : 0.f;
+                                    w3 = key < end.w ? w3 : 0.f;
+                                }
+                                sum0 = add2(sum0, pair(w0, w1));
+                                sum1 = add2(sum1, pair(w2, w3));
                             }
-                            sum0 = add2(sum0, pair(w0, w1));
-                            sum1 = add2(sum1, pair(w2, w3));
                         }
                     }
                     tc05::fence_before_sync();
@@ -510,7 +534,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const Params 
         pos += tiles;
     }
     __syncthreads();
-    if (warp == 16) {
+    if (warp == 12) {
         if (*left) {   // MMAs that nobody waited for end before their memory is given back
             if (lane == 0) {
                 tc05::commit(last);
