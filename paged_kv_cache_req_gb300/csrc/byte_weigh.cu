@@ -194,21 +194,26 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 2) weigh_kernel(const Params
 // ---------------------------------------------------------------- many rows
 // The same on the 5th-generation tensor cores: S = K q^T with 128 keys as MMA rows and up to 128 query
 // rows as columns, q as fp16 in shared memory, K as fp16 and S as fp32 in tensor memory.  The tiles of 128
-// keys of all requests and kv heads form one sequence that is cut into equal spans, one per SM.
-// Four warps copy the tiles, a key per thread: its codes, loaded two tiles ahead, become fp16 in its
-// lane of tensor memory.  (Through shared memory instead, the fence before the tensor cores read it waits
-// for the next tiles' loads too: 107 us at 8 x 32 rows of 32 heads over up to 32768 keys.)  One thread issues the
-// MMAs, and two groups of four warps take the tiles' scores in turn, a key per thread: its row becomes weights
-// and their sum.  Per score that is one exponential, which bounds it: 16 of them per cycle and SM.
+// keys of all requests and kv heads form one sequence that is cut into equal spans, one per SM.  One
+// warp brings the codes of a tile into shared memory (tensor boxes of whole pool tiles, or 16 bytes per lane
+// for small ones); four warps make them fp16, a key per thread, in its lane of tensor memory.
+// (Loaded a key per thread, without the detour: 64 us at 8 x 32 rows of 32 heads over up to 32768 keys.  As
+// fp16 in shared memory, with the fence that the tensor cores then need and that waits for the next
+// tiles' loads too: 107.)  One thread issues the MMAs, and two groups of four warps take the tiles' scores in
+// turn, a key per thread: its row becomes weights and their sum.
 constexpr int kTcKeys = 128, kTcRows = 128;   // keys of a tile, query rows at a time
-constexpr int kTcThreads = 416;               // warps 0-3 copy, 4-11 weigh, 12 issues
+constexpr int kTcThreads = 448;               // warps 0-3 convert, 4-11 weigh, 12 issues, 13 copies
 constexpr int kTcBatch = 1024;                // requests whose tiles are numbered in shared memory
-constexpr int kTcK = 2, kTcS = 3;             // tiles of keys, and of scores, in tensor memory
+constexpr int kTcRaw = 4, kTcK = 2, kTcS = 3; // tiles of codes in shared memory; of keys, and of scores, in tensor memory
+
+// Pools whose tiles' K rows of a head are 1 KB or more are copied as boxes.
+__host__ __device__ constexpr bool boxes(int t_shift, int d) { return (d << t_shift) >= 1024; }
 
 template <int D>
 struct TcSmem {
     static constexpr int kSlab = 128 * 128;   // q: 128 rows of 64 dims
-    static constexpr int kOff = D / 64 * kSlab;             // [B + 1] first tile of each request
+    static constexpr int kRaw = D / 64 * kSlab, kRawBytes = kTcKeys * D;
+    static constexpr int kOff = kRaw + kTcRaw * kRawBytes;  // [B + 1] first tile of each request
     static constexpr int kBytes = kOff + (kTcBatch + 1) * 4;
     static constexpr int kColS = kTcK * D / 2;              // tensor memory: keys, then scores
 };
@@ -230,18 +235,19 @@ __device__ __forceinline__ void put_16(uint8_t *slab, int row, int at, const uin
 }
 
 template <int D>
-__global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const Params p, const WeighParams wp) {
+__global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_constant__ Params p, const WeighParams wp) {
     using C = TcSmem<D>;
     extern __shared__ __align__(128) uint8_t smem_raw[];
     __shared__ __align__(16) float f_s[kTcRows], minus_lse_s[kTcRows];   // score -> base-2 logit without K's scale; -lse2
     __shared__ __align__(16) int end_s[kTcRows];
-    __shared__ __align__(8) uint64_t bars[2 * kTcK + 2 * kTcS + 1];
+    __shared__ __align__(8) uint64_t bars[2 * kTcRaw + 2 * kTcK + 2 * kTcS + 1];
     __shared__ int scan_s[kTcThreads / 32];
     __shared__ uint32_t tmem_slot;
     __shared__ int left_s, low_s;
     uint8_t *smem = aligned_smem<1024>(smem_raw);
     int *off = reinterpret_cast<int *>(smem + C::kOff);
-    uint64_t *full = bars, *used = bars + kTcK, *scored = used + kTcK, *freed = scored + kTcS, *last = freed + kTcS;
+    uint64_t *full = bars, *used = bars + kTcK, *scored = used + kTcK, *freed = scored + kTcS, *brought = freed + kTcS,
+             *taken = brought + kTcRaw, *last = taken + kTcRaw;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     if (threadIdx.x == 0) {
         for (int i = 0; i < kTcK; ++i) {
@@ -251,6 +257,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const Params 
         for (int i = 0; i < kTcS; ++i) {
             mbar_init(&scored[i], 1);
             mbar_init(&freed[i], 4);
+        }
+        for (int i = 0; i < kTcRaw; ++i) {
+            mbar_init(&brought[i], boxes(p.t_shift, D) ? 1 : 32);
+            mbar_init(&taken[i], 4);
         }
         mbar_init(last, 1);
         mbar_init_fence();
@@ -294,8 +304,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const Params 
     const int64_t pos_end = min(all, pos + per);
     constexpr int kPerRow = D / 16;   // lanes of a row of q
     const int kj = lane % kPerRow;
-    const bool wide = ((reinterpret_cast<uintptr_t>(p.pool) | static_cast<uintptr_t>(p.tile_stride)) & 31) == 0;   // (pools are 16-byte aligned)
-    uint32_t n = 0;          // tiles so far
+    uint32_t n = 0, issued = 0;   // tiles so far; of which the copies were issued
     int b = 0;
     while (pos < pos_end) {
         // ---- the next run of tiles of one request and kv head
@@ -312,7 +321,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const Params 
         float *part = wp.part + (static_cast<int64_t>(kh) * p.batch + b) * p.tab.max_len;
         if (rows == 0)
             for (int i = threadIdx.x; i < min(tiles * kTcKeys, req.L - k0); i += kTcThreads) part[k0 + i] = 0.f;
-        // a copying or weighing thread's key in each tile
+        // a converting or weighing thread's key in each tile
         const int mine = (warp & 3) * 32 + lane;
         // (a warp stops where it first uses what it loaded: an entry of the table is looked at, and a scale
         // converted, a tile after their loads)
@@ -327,25 +336,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const Params 
             if (first < 0 || first >= (p.tab.num_pages << p.tab.ps_shift)) return -1;
             if (first & p.tab.ps_mask) return -2;
             return first + ((k0 + t * kTcKeys + mine) & p.tab.ps_mask);
-        };
-        auto load = [&](int32_t from, uint32_t (&c)[D / 4]) {
-            if (report && (from == -1 || from == -2)) raise_flag(p.err, from == -1 ? PKV_DEVERR_RANGE : PKV_DEVERR_CONTIG);
-            const uint8_t *a = from >= 0 ? piece_at<D>(p, from, kh) + (from & ((1 << p.t_shift) - 1)) * D : nullptr;
-#pragma unroll
-            for (int i = 0; i < D / 32; ++i) {
-                if (a && wide) {
-                    quant::load_32(a + 32 * i, *reinterpret_cast<uint32_t(*)[8]>(c + 8 * i));
-                } else if (a) {
-#pragma unroll
-                    for (int e = 0; e < 8; e += 4) {
-                        const uint4 x = __ldg(reinterpret_cast<const uint4 *>(a + 32 * i + 4 * e));
-                        c[8 * i + e] = x.x; c[8 * i + e + 1] = x.y; c[8 * i + e + 2] = x.z; c[8 * i + e + 3] = x.w;
-                    }
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) c[8 * i + e] = 0;
-                }
-            }
         };
         auto scale_byte = [&](int32_t from) {
             uint32_t e = 1;
@@ -413,22 +403,26 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const Params 
                 if (lane == 0) atomicMin(&low_s, low);
                 fence_proxy_async_smem();            // before the tensor cores read it
             }
-            if (warp >= 4) named_bar_sync(1, kTcThreads - 128);   // (the copying warps go ahead)
+            if (warp >= 4 && warp < 13) named_bar_sync(1, 288);   // (the others go ahead)
             if (warp < 4) {
-                // -------------------------------------------------------- keys
+                // -------------------------------------------------------- codes to fp16
                 bool ok = true;
-                uint32_t code[2][D / 4];   // the next two tiles' codes
-                int32_t next[2];           // the table's entries of the two after them
-                next[0] = entry(0);
-                next[1] = entry(1);
-                load(slot_at(next[0], 0), code[0]);
-                load(slot_at(next[1], 1), code[1]);
-                next[0] = entry(2);
-                next[1] = entry(3);
-                auto put = [&](int t, uint32_t (&c)[D / 4], int32_t &ahead) {
-                    const uint32_t m = n + t, a = m % kTcK;
+                for (int t = 0; t < tiles; ++t) {
+                    const uint32_t m = n + t, a = m % kTcK, raw = m % kTcRaw;
+                    ok = __all_sync(0xffffffffu, ok && wait_or_leave(&brought[raw], (m / kTcRaw) & 1, left, p.err, p.wait_ns));
+                    if (!ok) break;
+                    const uint8_t *from = smem + C::kRaw + raw * C::kRawBytes;
+                    uint32_t c[D / 4];
+#pragma unroll
+                    for (int i = 0; i < D / 16; ++i) {
+                        const int at = mine * D + 16 * i;
+                        const uint4 x = *reinterpret_cast<const uint4 *>(from + (at ^ ((at >> 3) & 0x70)));
+                        c[4 * i] = x.x; c[4 * i + 1] = x.y; c[4 * i + 2] = x.z; c[4 * i + 3] = x.w;
+                    }
                     if (m >= kTcK) ok = __all_sync(0xffffffffu, ok && wait_or_leave(&used[a], ((m / kTcK) & 1) ^ 1, left, p.err, p.wait_ns));
-                    if (!ok) return;
+                    if (!ok) break;
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&taken[raw]);
                     tc05::fence_after_sync();
                     const uint32_t to = tc05::taddr(tbase, warp * 32, a * (D / 2));
 #pragma unroll
@@ -438,15 +432,78 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const Params 
                         for (int e = 0; e < 16; ++e) h[e] = e % 2 ? byte::hi_to_f16(c[8 * i + e / 2]) : byte::lo_to_f16(c[8 * i + e / 2]);
                         tc05::st_x16_u32(to + 16 * i, h);
                     }
-                    load(slot_at(ahead, t + 2), c);
-                    ahead = entry(t + 4);
                     tc05::wait_st();
                     tc05::fence_before_sync();
                     mbar_arrive(&full[a]);
+                }
+            } else if (warp == 13) {
+                // -------------------------------------------------------- the tiles' codes
+                // lane j: the table's entry of the tile's piece j (boxes), or of its keys j, + 32 ...
+                const bool box = boxes(p.t_shift, D);
+                const int pieces = kTcKeys >> p.t_shift;   // (boxes: at most 16)
+                auto entry_of = [&](int key) {
+                    int32_t first = -4;
+                    if (key < req.L) first = __ldg(p.tab.r2t + req.base + (key & ~p.tab.ps_mask));
+                    return first;
                 };
+                auto slot_of_key = [&](int32_t first, int key) -> int32_t {   // (see slot_of; -3: no key)
+                    if (key >= req.L) return -3;
+                    if (first < 0 || first >= (p.tab.num_pages << p.tab.ps_shift)) return -1;
+                    if (first & p.tab.ps_mask) return -2;
+                    return first + (key & p.tab.ps_mask);
+                };
+                const int past = max(1, static_cast<int>(p.tab.num_pages << p.tab.ps_shift >> p.t_shift));   // the map's tiles
+                int32_t ahead[2][4];                       // of this tile and the next
+                auto look_up = [&](int t, int32_t (&e)[4]) {
+                    const int key0 = k0 + t * kTcKeys;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        if (box && i > 0) break;
+                        const int key = key0 + (box ? lane << p.t_shift : 32 * i + lane);
+                        e[i] = t < tiles && (!box || lane < pieces) ? entry_of(key) : -4;
+                    }
+                };
+                bool ok = true;
+                auto bring = [&](int t, int32_t (&e)[4]) {
+                    const uint32_t m = n + t, raw = m % kTcRaw;
+                    if (m >= kTcRaw) ok = __all_sync(0xffffffffu, ok && wait_or_leave(&taken[raw], ((m / kTcRaw) & 1) ^ 1, left, p.err, p.wait_ns));
+                    if (!ok) return;
+                    issued = m + 1;
+                    const int key0 = k0 + t * kTcKeys;
+                    uint8_t *to = smem + C::kRaw + raw * C::kRawBytes;
+                    int flags = 0;
+                    if (box) {
+                        if (lane == 0) mbar_arrive_expect_tx(&brought[raw], C::kRawBytes);
+                        __syncwarp();
+                        if (lane < pieces) {               // (a bad page, or none: a box past the pool's last tile, zeros)
+                            const int32_t slot = slot_of_key(e[0], key0 + (lane << p.t_shift));
+                            if (slot == -1 || slot == -2) flags = slot == -1 ? PKV_DEVERR_RANGE : PKV_DEVERR_CONTIG;
+                            const int tile = slot >= 0 ? slot >> p.t_shift : past;
+                            tma_load_3d(to + (lane << p.t_shift) * D, &p.map, 0, kh * ((2 * D << p.t_shift) / 128), tile, &brought[raw]);
+                        }
+                    } else {
+                        constexpr int kRow = D / 16;       // lanes of a key
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int32_t slot = slot_of_key(e[i], key0 + 32 * i + lane);
+                            if (slot == -1 || slot == -2) flags |= slot == -1 ? PKV_DEVERR_RANGE : PKV_DEVERR_CONTIG;
+                            const uint8_t *row = slot >= 0 ? piece_at<D>(p, slot, kh) + (slot & ((1 << p.t_shift) - 1)) * D : nullptr;
+                            for (int k = 0; k < kRow; ++k) {
+                                const int key = k * (32 / kRow) + lane / kRow, at = (32 * i + key) * D + lane % kRow * 16;
+                                const uint8_t *a = from_lane(row, key);
+                                cp_async_16(to + (at ^ ((at >> 3) & 0x70)), a ? a + lane % kRow * 16 : p.pool, a ? 16 : 0);
+                            }
+                        }
+                        arrive_with_copies(&brought[raw]);
+                    }
+                    if (report && r0 == 0 && flags) raise_flag(p.err, flags);
+                    look_up(t + 2, e);
+                };
+                look_up(0, ahead[0]);
+                look_up(1, ahead[1]);
                 for (int t = 0; t < tiles && ok; t += 2) {
-                    put(t, code[0], next[0]);
-                    if (t + 1 < tiles && ok) put(t + 1, code[1], next[1]);
+                    bring(t, ahead[0]);
+                    if (t + 1 < tiles && ok) bring(t + 1, ahead[1]);
                 }
             } else if (warp == 12) {
                 // -------------------------------------------------------- S = K q^T
@@ -534,6 +591,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const Params 
         pos += tiles;
     }
     __syncthreads();
+    if (warp == 13 && *left)   // copies that nobody waited for land before the block's memory is given back
+        for (uint32_t m = issued > kTcRaw ? issued - kTcRaw : 0; m < issued; ++m) mbar_wait(&brought[m % kTcRaw], (m / kTcRaw) & 1);
     if (warp == 12) {
         if (*left) {   // MMAs that nobody waited for end before their memory is given back
             if (lane == 0) {
@@ -617,11 +676,21 @@ pkv_status launch_weigh(const char *who, const Params &p, const WeighParams &wp,
     if (L == 0) return ok();
     pkv_status st;
     if (rows >= kManyRows && p.batch <= kTcBatch) {
+        Params q = p;
+        if (boxes(p.t_shift, head_dim)) {   // the pool as lines of 128 bytes; a box is K's of a tile and head
+            const uint32_t lines = static_cast<uint32_t>((head_dim << p.t_shift) / 128);
+            const uint64_t dims[3] = {64, static_cast<uint64_t>(p.hkv) * 2 * lines,
+                                      static_cast<uint64_t>(std::max<int64_t>(1, p.tab.num_pages << p.tab.ps_shift >> p.t_shift))};
+            const uint64_t strides[2] = {128, static_cast<uint64_t>(p.tile_stride)};
+            const uint32_t box[3] = {64, lines, 1};
+            if (!encode_tmap_bf16(&q.map, p.pool, 3, dims, strides, box))   // (pairs of bytes)
+                return fail(PKV_ERR_CUDA, "%s: cuTensorMapEncodeTiled rejected the pool", who);
+        }
         auto *kern = head_dim == 128 ? weigh_many_kernel<128> : weigh_many_kernel<64>;
         const size_t smem = (head_dim == 128 ? TcSmem<128>::kBytes : TcSmem<64>::kBytes) + 1024;
         if (raise_smem_limit(reinterpret_cast<const void *>(kern)) < smem)
             return fail(PKV_ERR_CUDA, "%s: cannot raise the shared-memory limit", who);
-        st = launch_status(launch_chained(kern, dim3(static_cast<unsigned>(std::max(1, sm_count()))), dim3(kTcThreads), smem, s, p, wp), who);
+        st = launch_status(launch_chained(kern, dim3(static_cast<unsigned>(std::max(1, sm_count()))), dim3(kTcThreads), smem, s, q, wp), who);
     } else {
         auto *kern = head_dim == 128 ? weigh_kernel<128> : weigh_kernel<64>;
         st = launch_status(launch_chained(kern, dim3((L + kWeighKeys - 1) / kWeighKeys, H, B), dim3(kWeighWarps * 32), 0, s, p, wp), who);

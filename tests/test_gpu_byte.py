@@ -665,6 +665,53 @@ def test_two_calls_at_once_and_a_replayed_graph(B):
         check(c, q, out, None if out is None else a._keep and w[1], acc=acc)
 
 
+@pytest.mark.parametrize("D,ps,rows", [(128, 64, 40), (64, 4, 300)])
+def test_weights_whose_wait_runs_out(B, D, ps, rows):
+    """With a limit of 1 ns the call gives up, says so, and the next one is right."""
+    rng = np.random.default_rng(42)
+    cache = Cache(rng, [2000, 700], ps, 2, D)
+    q = to_bf16(values(rng, (2 * rows, 4, D)))
+    out, lse, e = extend(B, cache, q, [rows, rows])
+    acc, err = table_of(cache, rng, 0.0), err_word()
+    a = cache.args(B, "table", q, None, lse=lse, qo_indptr=i32([0, rows, 2 * rows]), acc_out=acc)
+    ws = torch.empty(B.pkv_byte_weights_workspace_size(a), dtype=torch.uint8, device=DEV)
+    B.pkv_set_wait_limit(1)
+    try:
+        B.pkv_byte_weights(a, ws, err)
+        assert err.item() in (0, 8)
+    finally:
+        B.pkv_set_wait_limit(0)
+    err.zero_()
+    B.pkv_byte_weights(a, ws, err)
+    assert err.item() == 0
+    check(cache, q, out, lse, [rows, rows], acc=acc, held=True)
+
+
+@pytest.mark.parametrize("ps", [64, 16, 4, 1])
+def test_weights_bad_pages(B, ps):
+    """A page outside the pool, and one that is not aligned, in a call of many rows."""
+    rng = np.random.default_rng(43)
+    cache = Cache(rng, [300, 200], ps, 1, 128)
+    q = to_bf16(values(rng, (100, 2, 128)))
+    out, lse, e = extend(B, cache, q, [50, 50])
+    table = cache.r2t.copy()
+    for bad, bit in ((cache.pages * ps + 5 * ps, 1), (-1, 1)) + (((table[cache.rpi[0], 64] + 1), 2),) * (ps > 1):
+        cache.r2t = table.copy()
+        cache.r2t[cache.rpi[0], 64] = bad
+        acc, err = table_of(cache, rng, 0.0), err_word()
+        a = cache.args(B, "table", q, None, lse=lse, qo_indptr=i32([0, 50, 100]), acc_out=acc)
+        B.pkv_byte_weights(a, torch.empty(B.pkv_byte_weights_workspace_size(a), dtype=torch.uint8, device=DEV), err)
+        assert err.item() == bit
+        got = host(acc)
+        cache.r2t = table
+        n = host(q).astype(np.float64)[50:]
+        k, v = cache.pool.read(cache.slots[1], 0), cache.pool.read(cache.slots[1], 1)
+        w, wt = R.attention(n, k, v, np.arange(151, 201), 128 ** -0.5, cache.pool.largest(cache.slots[1]))[2::3]
+        want = w.sum((0, 1))
+        R.assert_within(got[cache.rpi[1], :200], want, wt.sum((0, 1)) + 101 * 2.0 ** -23 * want, "the other request")
+        assert np.isfinite(got[cache.rpi[0], :300]).all()
+
+
 @pytest.mark.parametrize("batch,hi", [(3, 200), (40, 3000)])
 def test_a_wait_that_runs_out(B, batch, hi):
     """With a limit of 1 ns the call gives up, says so, and the next one is right."""
