@@ -243,7 +243,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
     __shared__ __align__(8) uint64_t bars[2 * kTcRaw + 2 * kTcK + 2 * kTcS + 1];
     __shared__ int scan_s[kTcThreads / 32];
     __shared__ uint32_t tmem_slot;
-    __shared__ int left_s, low_s;
+    __shared__ int left_s, low_s, exp_lo_s, exp_hi_s;
     uint8_t *smem = aligned_smem<1024>(smem_raw);
     int *off = reinterpret_cast<int *>(smem + C::kOff);
     uint64_t *full = bars, *used = bars + kTcK, *scored = used + kTcK, *freed = scored + kTcS, *brought = freed + kTcS,
@@ -344,7 +344,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
         };
         for (int r0 = 0; r0 < rows; r0 += kTcRows) {
             const int live = min(kTcRows, rows - r0), cols = (live + 31) / 32 * 32;
-            if (threadIdx.x == 0) low_s = INT32_MAX;
+            if (threadIdx.x == 0) {
+                low_s = exp_lo_s = INT32_MAX;
+                exp_hi_s = INT32_MIN;
+            }
             __syncthreads();
             if (warp >= 4 && warp < 12) {
                 // ---- the rows of q, D/16 lanes each
@@ -365,17 +368,35 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
                         w[i][4] = y.x; w[i][5] = y.y; w[i][6] = y.z; w[i][7] = y.w;
                     }
                 }
+                int up_by[kTcRows / kRows], lo = INT32_MAX, hi = INT32_MIN;
 #pragma unroll
                 for (int i = 0; i < kTcRows / kRows; ++i) {
-                    const int row = i * kRows + tid / kPerRow, rr = r0 + row, tok = token_of(p, rr);
                     uint32_t top = 0;
 #pragma unroll
                     for (int e = 0; e < 8; ++e) top = __vmaxu2(top, w[i][e] & 0x7fff7fffu);
                     top = max(top & 0xffffu, top >> 16);
 #pragma unroll
                     for (int o = 1; o < kPerRow; o <<= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, o));
-                    int e2 = min(126, 6 + 127 - static_cast<int>(top >> 7));   // (see start_segment)
-                    if (top == 0 || top >= 0x7f80u) e2 = 0;
+                    up_by[i] = min(126, 6 + 127 - static_cast<int>(top >> 7));   // (see start_segment)
+                    if (top >= 0x7f80u) up_by[i] = 0;
+                    if (top != 0) {
+                        lo = min(lo, up_by[i]);
+                        hi = max(hi, up_by[i]);
+                    }
+                }
+                lo = __reduce_min_sync(0xffffffffu, lo);
+                hi = __reduce_max_sync(0xffffffffu, hi);
+                if (lane == 0) {
+                    atomicMin(&exp_lo_s, lo);
+                    atomicMax(&exp_hi_s, hi);
+                }
+                named_bar_sync(2, 256);
+                // one power of two for all rows, the largest's, where it is at most 2^8 from the others'
+                const bool same = exp_hi_s - exp_lo_s <= 8;
+#pragma unroll
+                for (int i = 0; i < kTcRows / kRows; ++i) {
+                    const int row = i * kRows + tid / kPerRow, rr = r0 + row, tok = token_of(p, rr);
+                    const int e2 = exp_hi_s == INT32_MIN ? 0 : same ? exp_lo_s : up_by[i];   // (no row but zeros: any)
                     const float up = __int_as_float((e2 + 127) << 23), down = __int_as_float((127 - e2) << 23);
                     uint32_t h[8];
 #pragma unroll
@@ -533,6 +554,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
                 bool ok = true;
                 const int turn = static_cast<int>(((warp >> 2) + 1 + n) & 1);   // the group's tiles: t % 2 = turn
                 const int low = low_s;
+                const bool same = exp_hi_s - exp_lo_s <= 8;
                 const int32_t first = entry(turn);
                 int32_t next = entry(turn + 2);
                 uint32_t e_next = scale_byte(slot_at(first, turn));   // K's scale of the next tile's key
@@ -549,28 +571,34 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
                     const bool whole = k0 + (t + 1) * kTcKeys <= low;
                     const uint32_t from = tc05::taddr(tbase, (warp & 3) * 32, C::kColS + s * kTcRows);
                     uint64_t sum0 = 0, sum1 = 0;
+                    const float one = fminf(f_s[0] * scale, 3.4e38f);   // (where the rows share a factor; finite, so that 0 stays 0)
+                    const uint64_t fks = pair(one, one);
                     for (int c0 = 0; c0 < cols; c0 += 64) {
                         float x[64];         // (columns behind `cols` may hold anything: they are not looked at)
                         tc05::ld_x64(from + c0, x);
 #pragma unroll
                         for (int h = 0; h < 64; h += 32) {
                             if (c0 + h >= cols) break;
+                            if (whole && same) {
+#pragma unroll
+                                for (int e = h; e < h + 32; e += 4) {
+                                    const ulonglong2 l = *reinterpret_cast<const ulonglong2 *>(&minus_lse_s[c0 + e]);
+                                    const float2 y0 = unpair(fma2(pair(x[e], x[e + 1]), fks, l.x));
+                                    const float2 y1 = unpair(fma2(pair(x[e + 2], x[e + 3]), fks, l.y));
+                                    sum0 = add2(sum0, pair(ex2(y0.x), ex2(y0.y)));
+                                    sum1 = add2(sum1, pair(ex2(y1.x), ex2(y1.y)));
+                                }
+                                continue;
+                            }
 #pragma unroll
                             for (int e = h; e < h + 32; e += 4) {
                                 const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(&f_s[c0 + e]);
                                 const ulonglong2 l = *reinterpret_cast<const ulonglong2 *>(&minus_lse_s[c0 + e]);
+                                const int4 end = *reinterpret_cast<const int4 *>(&end_s[c0 + e]);
                                 const float2 y0 = unpair(fma2(mul2(pair(x[e], x[e + 1]), f.x), ks, l.x));
                                 const float2 y1 = unpair(fma2(mul2(pair(x[e + 2], x[e + 3]), f.y), ks, l.y));
-                                float w0 = ex2(y0.x), w1 = ex2(y0.y), w2 = ex2(y1.x), w3 = ex2(y1.y);
-                                if (!whole) {
-                                    const int4 end = *reinterpret_cast<const int4 *>(&end_s[c0 + e]);
-                                    w0 = key < end.x ? w0 : 0.f;
-                                    w1 = key < end.y ? w1 : 0.f;
-                                    w2 = key < end.z ? w2 : 0.f;
-                                    w3 = key < end.w ? w3 : 0.f;
-                                }
-                                sum0 = add2(sum0, pair(w0, w1));
-                                sum1 = add2(sum1, pair(w2, w3));
+                                sum0 = add2(sum0, pair(key < end.x ? ex2(y0.x) : 0.f, key < end.y ? ex2(y0.y) : 0.f));
+                                sum1 = add2(sum1, pair(key < end.z ? ex2(y1.x) : 0.f, key < end.w ? ex2(y1.y) : 0.f));
                             }
                         }
                     }

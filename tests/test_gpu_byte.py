@@ -570,22 +570,25 @@ def test_weights_of_rows(B, D, ps, H, g, lens, rows, bounds):
     assert torch.equal(acc, again)
 
 
-def test_weights_of_extreme_rows(B):
-    """Rows without keys, rows of zeros, a row of large and one of tiny values."""
+@pytest.mark.parametrize("more", [0, 60])
+@pytest.mark.parametrize("tiny", [2.0 ** -4, 2.0 ** -100])
+def test_weights_of_extreme_rows(B, more, tiny):
+    """Rows without keys, rows of zeros, a row of large and one of tiny values; alone and among many."""
     rng = np.random.default_rng(30)
-    cache = Cache(rng, [200], 16, 1, 64)
-    x = values(rng, (5, 2, 64))
+    cache = Cache(rng, [700], 16, 1, 64)
+    n = 5 + more
+    x = values(rng, (n, 2, 64))
     x[1] = 0
-    x[2] *= np.float32(2.0 ** -100)
+    x[2] *= np.float32(tiny)
     x[3] *= 16
     q = to_bf16(x)
-    ends = [0, 200, 150, 199, 1]
-    out, lse, e = extend(B, cache, q, [5], "table", ends)
+    ends = [0, 200, 150, 199, 1] + [700 - i for i in range(more)]
+    out, lse, e = extend(B, cache, q, [n], "table", ends)
     acc, err = table_of(cache, rng, 0.0), err_word()
-    a = cache.args(B, "table", q, None, lse=lse, qo_indptr=i32([0, 5]), kv_end=i32(ends), acc_out=acc)
+    a = cache.args(B, "table", q, None, lse=lse, qo_indptr=i32([0, n]), kv_end=i32(ends), acc_out=acc)
     B.pkv_byte_weights(a, torch.empty(B.pkv_byte_weights_workspace_size(a), dtype=torch.uint8, device=DEV), err)
     assert err.item() == 0
-    check(cache, q, out, lse, [5], ends, acc=acc)
+    check(cache, q, out, lse, [n], ends, acc=acc, held=n * 2 > 128)
 
 
 @pytest.mark.parametrize("D,rows", [(128, 5), (128, 40), (64, 40)])
