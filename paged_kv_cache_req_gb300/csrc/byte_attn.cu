@@ -36,63 +36,75 @@ struct Quant8 {
     static constexpr bool kUnits = true, kHeldBf16V = true;
     static constexpr const char *kExtend = "pkv_byte_extend";
     // A stage is a tile of 64 keys, or of 32 (D = 128 and 16 rows, whose math takes so long that 8 warps are
-    // needed): K codes [keys][D], V codes [keys][D], or of pools of 16-slot tiles (kT = 16) those as they
-    // lie.  In each line of 128 bytes the eight 16-byte chunks are swapped about, chunk x ^ (line %
+    // needed): K codes [keys][D], V codes [keys][D], or where pieces are smaller but 1 KB or more (kT = 16, or 0: of
+    // the pool's t slots) those as they lie.  In each line of 128 bytes the eight 16-byte chunks are swapped about, chunk x ^ (line %
     // 8), by the tensor copies or by the lanes that copy: the keys that eight lanes read at a time lie a
     // line apart or more, and so in different banks.  Beside it the scales: 16 bytes of a piece with its
-    // own two among them, 4 where kT is 0.
+    // own two among them, 4 where kT is 0 or 1.
     static constexpr int kKeys = D == 128 && kNT == 2 ? 32 : 64, kAlign = 1024, kAux = 256;
     static constexpr uint32_t kStageBytes = 2 * kKeys * D;
-    static constexpr int kLines = kT == 64 && kKeys == 64 ? D : D / 4;   // of the box that one tensor copy brings
+    static constexpr int kLines = kKeys == 64 ? D : D / 4;   // of the box that one tensor copy of a 64-slot tile brings
     static constexpr int warps(int nt) { return D == 64 ? 12 : nt == 2 ? 8 : 6; }
     static constexpr int stages(int nt) { return D == 128 && nt == 2 ? 3 : 2; }
     template <int NT>
     using State = State8<D, NT>;
 
-    // (copied 16 bytes per lane)
-    __device__ __forceinline__ static bool gathers(int) { return kT == 0; }
-    // A piece: its address, or where it is copied as a box (kT != 0) its tile, counted from 1.
+    // Pieces of 1 KB or more are copied as boxes, smaller ones (kT = 1) 16 bytes per lane; where kT is 0 or 1 the
+    // lanes copy the scales.  (In us, per lane / as boxes: 64 requests x 4096 keys x 8 kv heads of 128, page size 32: @32L@
+    // / @32B@, 4: @4L@ / @4B@.)
+    static constexpr int kSmall = 512 / D;
+    __host__ __device__ static constexpr bool gathers(int) { return kT == 1; }
+    __device__ __forceinline__ static int arrivals(int) { return kT >= 16 ? 1 : kT == 1 ? 32 : 33; }   // at a stage's barrier
+    // A piece: its address, or where it is copied as a box its tile, counted from 1.
     __device__ __forceinline__ static const uint8_t *piece(const Params &p, int slot, int kh) {
-        if (kT != 0) return reinterpret_cast<const uint8_t *>(static_cast<uintptr_t>((slot >> p.t_shift) + 1));
+        if (!gathers(p.t_shift)) return reinterpret_cast<const uint8_t *>(static_cast<uintptr_t>((slot >> p.t_shift) + 1));
         return piece_at<D>(p, slot, kh);
     }
     __device__ __forceinline__ static void zero_piece(const Stage &stage, int j, int ps) {
-        const int t = 1 << ps;
-        if (kT != 0) {
-            constexpr int kBytes = 2 * (kT > kKeys ? kKeys : kT) * D;
-            uint32_t *w = reinterpret_cast<uint32_t *>(stage.codes + j * kBytes);
-            for (int o = 0; o < kBytes / 4; ++o) w[o] = 0;
-            for (int o = 0; o < 4; ++o) reinterpret_cast<uint32_t *>(stage.aux + j * 16)[o] = 0x01010101u;
-            return;
+        const int bytes = kT > kKeys ? 2 * kKeys * D : 2 * D << ps;
+        if (gathers(ps)) {
+            for (int part = 0; part < 2; ++part)
+                for (int o = 0; o < bytes / 2; o += 16)
+                    *reinterpret_cast<uint4 *>(stage.codes + part * kKeys * D + swapped(j * (bytes / 2) + o)) = make_uint4(0, 0, 0, 0);
+        } else {   // (whole lines)
+            for (int o = 0; o < bytes; o += 16) *reinterpret_cast<uint4 *>(stage.codes + j * bytes + o) = make_uint4(0, 0, 0, 0);
         }
-        for (int part = 0; part < 2; ++part)
-            for (int o = 0; o < t * D; o += 16)
-                *reinterpret_cast<uint4 *>(stage.codes + part * kKeys * D + swapped(j * t * D + o)) = make_uint4(0, 0, 0, 0);
-        reinterpret_cast<uint32_t *>(stage.aux)[j] = 0x01010101u;
+        if (kT < 16)
+            reinterpret_cast<uint32_t *>(stage.aux)[j] = 0x01010101u;
+        else
+            reinterpret_cast<uint4 *>(stage.aux)[j] = make_uint4(0x01010101u, 0x01010101u, 0x01010101u, 0x01010101u);
     }
     // Copies a tile's n pieces (from key `half` of a larger one on), `live` of them on good pages; piece i of
     // the window is lane i % 32's src[i / 32].
     __device__ __forceinline__ static void copy(const Params &p, int kh, const uint8_t *const (&src)[2], int first, int n,
                                                 uint32_t live, int ps, int half, const Stage &stage, uint64_t *bar, int lane) {
-        if constexpr (kT != 0) {
-            constexpr uint32_t kBytes = 2 * (kT > kKeys ? kKeys : kT) * D;
-            if (lane == (first & 31)) mbar_arrive_expect_tx(bar, live * (kBytes + 16));
+        // the scale bytes of a tile, in whole units of `unit`
+        auto scales = [&](int64_t tile, int unit) {
+            return p.pool + tile * p.tile_stride + (static_cast<int64_t>(p.hkv) * 2 * D << p.t_shift) + (2 * kh & ~(unit - 1));
+        };
+        if constexpr (kT != 1) {
+            const uint32_t bytes = kT > kKeys ? 2 * kKeys * D : 2 * D << ps;
+            if (lane == (first & 31)) mbar_arrive_expect_tx(bar, live * (bytes + (kT == 0 ? 0 : 16)));
             if (kT != 64) __syncwarp();   // (with one piece the same lane copies)
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int j = 32 * i + lane - first;
                 if (j >= 0 && j < n && src[i]) {
-                    const int tile = static_cast<int>(reinterpret_cast<uintptr_t>(src[i])) - 1, line = kh * (2 * kT * D / 128);
+                    const int tile = static_cast<int>(reinterpret_cast<uintptr_t>(src[i])) - 1;
+                    const int line = kh * ((2 * D << p.t_shift) / 128);
                     if (kT > kKeys) {   // K's half of the tile, and V's
                         tma_load_3d(stage.codes, &p.map, 0, line + half * D / 128, tile, bar);
                         tma_load_3d(stage.codes + kKeys * D, &p.map, 0, line + (kT + half) * D / 128, tile, bar);
                     } else {
-                        tma_load_3d(stage.codes + j * kBytes, &p.map, 0, line, tile, bar);
+                        tma_load_3d(stage.codes + j * bytes, &p.map, 0, line, tile, bar);
                     }
-                    static_assert(kLines * 128 == (kT > kKeys ? kBytes / 2 : kBytes), "a box is what one copy brings");
-                    bulk_load(stage.aux + j * 16, p.pool + tile * p.tile_stride + static_cast<int64_t>(p.hkv) * 2 * kT * D + (2 * kh & ~15), 16, bar);
+                    if (kT == 0)
+                        cp_async_small<4>(stage.aux + j * 4, scales(tile, 4));
+                    else
+                        bulk_load(stage.aux + j * 16, scales(tile, 16), 16, bar);
                 }
             }
+            if (kT == 0) arrive_with_copies(bar);
             return;
         }
         constexpr int kRow = D / 16, kRounds = kKeys * kRow / 32;   // 16 bytes per lane; rounds for K (and V)
@@ -111,10 +123,8 @@ struct Quant8 {
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
             const int j = 32 * i + lane - first;
-            if (j >= 0 && j < (kKeys >> ps) && src[i]) {
-                const uint8_t *a = src[i] + (static_cast<int64_t>(p.hkv - kh) * 2 * D << ps) + (2 * kh & ~3);
-                cp_async_small<4>(stage.aux + j * 4, a);
-            }
+            if (j >= 0 && j < (kKeys >> ps) && src[i])
+                cp_async_small<4>(stage.aux + j * 4, src[i] + (static_cast<int64_t>(p.hkv - kh) * 2 * D << ps) + (2 * kh & ~3));
         }
         arrive_with_copies(bar);
     }
@@ -122,15 +132,20 @@ struct Quant8 {
     // Where byte `at` of a run of lines that begins on a multiple of 1024 is.
     __device__ __forceinline__ static int swapped(int at) { return at ^ ((at >> 3) & 0x70); }
     // Byte `at` of the codes (part 0 = K, 1 = V) of key k of the 16-key group kt of the stage's `step`-th 32 keys.
-    // (The groups begin on multiples of 1024, so the swap is a lane's own.)
-    __device__ __forceinline__ static const uint8_t *codes(const Stage &stage, int step, int part, int kt, int k, int at) {
+    // (Where the group's place does not depend on t it begins on a multiple of 1024, so the swap is a lane's own.)
+    __device__ __forceinline__ static const uint8_t *codes(const Params &p, const Stage &stage, int step, int part, int kt, int k, int at) {
         const int group = step * kGroups + kt;
+        if (kT == 0) {
+            const int key = group * 16 + k, in = key & ((1 << p.t_shift) - 1);
+            return stage.codes + swapped(((key - in) * 2 + in + (part << p.t_shift)) * D + at);
+        }
         return stage.codes + (kT == 16 ? group * (32 * D) + part * (16 * D) : part * (kKeys * D) + group * (16 * D)) + swapped(k * D + at);
     }
     // Its two scale bytes.
     __device__ __forceinline__ static uint32_t scale_bytes(const Params &p, const Stage &stage, int step, int kt, int k, int kh) {
         const int group = step * kGroups + kt;
-        const int at = kT == 64 ? (2 * kh & 15) : kT == 16 ? group * 16 + (2 * kh & 15) : ((group * 16 + k) >> p.t_shift) * 4 + (2 * kh & 3);
+        int at = kT == 64 ? (2 * kh & 15) : group * 16 + (2 * kh & 15);
+        if (kT < 16) at = ((group * 16 + k) >> p.t_shift) * 4 + (2 * kh & 3);
         return *reinterpret_cast<const uint16_t *>(stage.aux + at);
     }
 
@@ -150,7 +165,7 @@ struct Quant8 {
             for (int u = 0; u < 2; ++u) {
 #pragma unroll
                 for (int i = 0; i < D / 64; ++i) {
-                    const uint4 x = *reinterpret_cast<const uint4 *>(codes(stage, step, 0, kt, r + 8 * u, c * (D / 4) + 16 * i));
+                    const uint4 x = *reinterpret_cast<const uint4 *>(codes(p, stage, step, 0, kt, r + 8 * u, c * (D / 4) + 16 * i));
                     w[kt][u][4 * i] = x.x; w[kt][u][4 * i + 1] = x.y; w[kt][u][4 * i + 2] = x.z; w[kt][u][4 * i + 3] = x.w;
                 }
                 const uint32_t e = scale_bytes(p, stage, step, kt, r + 8 * u, kh);
@@ -174,7 +189,7 @@ struct Quant8 {
             float most = ve[0][0];
             if (kT != 64) {
                 most = fmaxf(fmaxf(ve[0][0], ve[0][1]), fmaxf(ve[1][0], ve[1][1]));
-                if (kT == 0) most = static_cast<float>(__reduce_max_sync(0xffffffffu, static_cast<int>(most)));
+                if (kT < 16) most = static_cast<float>(__reduce_max_sync(0xffffffffu, static_cast<int>(most)));
             }
             if (most > st.unit) {
                 const float corr = down_by(st.unit - most);
@@ -267,7 +282,7 @@ struct Quant8 {
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
                     const int k = 2 * c + e + 8 * u;
-                    const uint8_t *cp = codes(stage, step, 1, kt, k, r * (D / 8));
+                    const uint8_t *cp = codes(p, stage, step, 1, kt, k, r * (D / 8));
                     if (D == 128) {
                         const uint4 y = *reinterpret_cast<const uint4 *>(cp);
                         x[e][0] = y.x; x[e][1] = y.y; x[e][D / 32 - 2] = y.z; x[e][D / 32 - 1] = y.w;
@@ -305,7 +320,7 @@ struct Quant8 {
                 for (int k = 0; k < 16; ++k) {
                     const int key = key0 + kt * 16 + k;
                     if (key >= keys) continue;
-                    const uint8_t *cp = codes(stage, step, 1, kt, k, r * (D / 8));
+                    const uint8_t *cp = codes(p, stage, step, 1, kt, k, r * (D / 8));
 #pragma unroll
                     for (int t = 0; t < KS; ++t)
 #pragma unroll
@@ -455,7 +470,7 @@ size_t size_of(const pkv_byte_args *a, Call call) {
 
 // The map of a pool whose pieces are copied as boxes.
 bool encode_pool(const pkv_byte_args *a, int nt, Params &p) {
-    if (p.t_shift != 6 && p.t_shift != 4) return true;
+    if (1 << p.t_shift < (a->head_dim == 128 ? Quant8<128, 0, 1>::kSmall : Quant8<64, 0, 1>::kSmall)) return true;
     const uint32_t lines = static_cast<uint32_t>((2 * a->head_dim << p.t_shift) / 128);
     const uint64_t dims[3] = {64, static_cast<uint64_t>(a->num_kv_heads) * lines, static_cast<uint64_t>(std::max<int64_t>(1, a->num_tiles))};
     const uint64_t strides[2] = {128, static_cast<uint64_t>(a->tile_stride)};
@@ -464,7 +479,7 @@ bool encode_pool(const pkv_byte_args *a, int nt, Params &p) {
         if (a->head_dim == 128) return nt == 1 ? Quant8<128, kT, 1>::kLines : Quant8<128, kT, 2>::kLines;
         return nt == 1 ? Quant8<64, kT, 1>::kLines : Quant8<64, kT, 2>::kLines;
     };
-    const int height = p.t_shift == 6 ? box_lines(std::integral_constant<int, 64>{}) : box_lines(std::integral_constant<int, 16>{});
+    const int height = p.t_shift == 6 ? box_lines(std::integral_constant<int, 64>{}) : static_cast<int>(lines);
     const uint32_t box[3] = {64, static_cast<uint32_t>(height), 1};
     return encode_tmap_bf16(&p.map, a->pool, 3, dims, strides, box);   // (pairs of bytes)
 }

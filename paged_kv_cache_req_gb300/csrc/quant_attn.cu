@@ -380,7 +380,7 @@ template <int D, int kT_, int>
 struct Quant4 {
     static constexpr int kDim = D, kT = kT_;
     static constexpr bool kUnits = false, kHeldBf16V = false;
-    static constexpr int kAlign = 128, kKeys = 64, kAux = 0;
+    static constexpr int kAlign = 128, kKeys = 64, kAux = 0, kSmall = 0;
     static constexpr const char *kExtend = "pkv_quant_extend";
     static constexpr uint32_t kStageBytes = quant::tile_bytes(kKeys, D);
     static constexpr int warps(int nt) { return warps_per_sm(D, nt); }
@@ -389,6 +389,7 @@ struct Quant4 {
     using State = qattn::State<D, NT>;
 
     __device__ __forceinline__ static bool gathers(int t_shift) { return qattn::gathers<kT>(t_shift); }
+    __device__ __forceinline__ static int arrivals(int t_shift) { return gathers(t_shift) ? 32 : 1; }   // at a stage's barrier
     __device__ __forceinline__ static const uint8_t *piece(const Params &p, int slot, int kh) {
         return p.pool + static_cast<int64_t>(slot >> p.t_shift) * p.tile_stride + static_cast<int64_t>(kh) * quant::tile_bytes(1 << p.t_shift, D);
     }

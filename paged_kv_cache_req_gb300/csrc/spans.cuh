@@ -588,7 +588,7 @@ __global__ void __launch_bounds__(F::warps(NT) * 32, 1) attend_kernel(const __gr
     uint8_t *aux = smem + static_cast<uint32_t>(kWarps * S) * stage_bytes + warp * S * F::kAux;
     uint64_t *bar = bars + warp * S;
     if (lane == 0) {
-        for (int i = 0; i < S; ++i) mbar_init(&bar[i], F::gathers(p.t_shift) ? 32 : 1);
+        for (int i = 0; i < S; ++i) mbar_init(&bar[i], F::arrivals(p.t_shift));
         mbar_init_fence();
     }
     __syncwarp();
@@ -706,7 +706,7 @@ __global__ void __launch_bounds__(F::warps(NT) * 32, 1) unit_kernel(const __grid
     uint8_t *aux = smem + static_cast<uint32_t>(kWarps * S) * stage_bytes + warp * S * F::kAux;
     uint64_t *bar = bars + warp * S;
     if (lane == 0) {
-        for (int i = 0; i < S; ++i) mbar_init(&bar[i], F::gathers(p.t_shift) ? 32 : 1);
+        for (int i = 0; i < S; ++i) mbar_init(&bar[i], F::arrivals(p.t_shift));
         mbar_init_fence();
     }
     __syncwarp();
@@ -1322,7 +1322,7 @@ static Params params(const A *a, int32_t *err) {
     return p;
 }
 
-// Fm<D, kT, NT>: the format at a head_dim, for pools of tiles of kT slots (0: others) and 8 NT rows.
+// Fm<D, kT, NT>: the format at a head_dim, for pools of tiles of kT slots (0: others; 1: fewer than kSmall) and 8 NT rows.
 template <template <int, int, int> class Fm, int D, int NT>
 static pkv_status launch(const char *who, const Params &p, const Plan &pl, cudaStream_t s) {
     auto pick = [&](auto f) {
@@ -1330,6 +1330,8 @@ static pkv_status launch(const char *who, const Params &p, const Plan &pl, cudaS
         return !pl.unit ? attend_kernel<F, NT> : p.qo_indptr ? unit_kernel<F, NT, true> : unit_kernel<F, NT, false>;
     };
     auto *kern = p.t_shift == 6 ? pick(Fm<D, 64, NT>{}) : p.t_shift == 4 ? pick(Fm<D, 16, NT>{}) : pick(Fm<D, 0, NT>{});
+    if constexpr (Fm<D, 0, NT>::kSmall > 0)   // formats that take small pieces another way
+        if (1 << p.t_shift < Fm<D, 0, NT>::kSmall) kern = pick(Fm<D, 1, NT>{});
     if (raise_smem_limit(reinterpret_cast<const void *>(kern)) < pl.smem)
         return fail(PKV_ERR_CUDA, "%s: cannot raise the shared-memory limit", who);
     pkv_status st = PKV_OK;
