@@ -36,7 +36,7 @@ struct Quant8 {
     static constexpr bool kUnits = true, kHeldBf16V = true;
     static constexpr const char *kExtend = "pkv_byte_extend";
     // A stage is a tile of 64 keys, or of 32 (D = 128 and 16 rows, whose math takes so long that 8 warps are
-    // needed): K codes [keys][D], V codes [keys][D], or where pieces are smaller but 1 KB or more (kT = 16, or 0: of
+    // needed): K codes [keys][D], V codes [keys][D], or where pieces are smaller but 2 KB or more (kT = 16, or 0: of
     // the pool's t slots) those as they lie.  In each line of 128 bytes the eight 16-byte chunks are swapped about, chunk x ^ (line %
     // 8), by the tensor copies or by the lanes that copy: the keys that eight lanes read at a time lie a
     // line apart or more, and so in different banks.  Beside it the scales: 16 bytes of a piece with its
@@ -49,10 +49,10 @@ struct Quant8 {
     template <int NT>
     using State = State8<D, NT>;
 
-    // Pieces of 1 KB or more are copied as boxes, smaller ones (kT = 1) 16 bytes per lane; where kT is 0 or 1 the
-    // lanes copy the scales.  (In us, per lane / as boxes: 64 requests x 4096 keys x 8 kv heads of 128, page size 32: @32L@
-    // / @32B@, 4: @4L@ / @4B@.)
-    static constexpr int kSmall = 512 / D;
+    // Pieces of 2 KB or more are copied as boxes, smaller ones (kT = 1) 16 bytes per lane; where kT is 0 or 1 the
+    // lanes copy the scales.  (One row of 64 requests x 4096 keys x 8 kv heads, per lane / as boxes: 128 dims, pages of 32
+    // 111.2 / 103.4 us, 16 110.9 / 100.8, 8 113.3 / 111.8, 4 118.2 / 125.7; 64 dims, pages of 32 61.7 / 59.7, 8 63.1 / 64.3.)
+    static constexpr int kSmall = 1024 / D;
     __host__ __device__ static constexpr bool gathers(int) { return kT == 1; }
     __device__ __forceinline__ static int arrivals(int) { return kT >= 16 ? 1 : kT == 1 ? 32 : 33; }   // at a stage's barrier
     // A piece: its address, or where it is copied as a box its tile, counted from 1.

@@ -5,7 +5,8 @@
 // first kernel writes each token's number to who[slot].  Nothing clears that array: an entry
 // counts when the token that it names is one of the call's and has that slot.  The second
 // kernel gives each tile to one owner, the token of the tile's first named slot, which finds
-// the others in who, takes the maximum over all of them, and writes scales and codes.
+// the others in who, takes the maximum over all of them, and writes scales and codes.  For few tokens (a
+// decode step) one kernel does both: each of its blocks looks at all of the call's slots.
 #include "gather.cuh"
 #include "byte.cuh"
 
@@ -42,12 +43,6 @@ __global__ void __launch_bounds__(kThreads) claim_kernel(const StoreParams p) {
         return;
     }
     p.who[slot] = i;
-}
-
-// The token that the call stores at `slot`, or -1.
-__device__ __forceinline__ int owner(const StoreParams &p, int64_t slot) {
-    const int w = p.who[slot];
-    return w >= 0 && w < p.n && p.slots[w] == slot ? w : -1;
 }
 
 template <bool kVec>
@@ -140,26 +135,87 @@ __device__ __forceinline__ void store_tile(const StoreParams &p, int64_t tile, i
     }
 }
 
+// Tokens up to which every block looks at all of them.  (Stores of one token per tile, 8 kv heads of 128, one after
+// another: 32 tokens 1.9 us so and 3.8 with two kernels, 128 3.2 and 5.9, 256 5.1 and 5.8.)
+constexpr int kFewTokens = kThreads;
+
+// A block per token and kv head: the tile, if the token owns it.
+template <int D, bool kVec>
+__global__ void __launch_bounds__(kThreads) store_few_kernel(const StoreParams p) {
+    __shared__ Members mem;
+    __shared__ int who[kMaxTile];
+    __shared__ uint32_t red[kWarps][2];
+    pdl_wait();          // inputs may come from the previous kernel of the stream
+    pdl_launch_next();
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, i = blockIdx.x, kh = blockIdx.y, t = 1 << p.t_shift;
+    const int64_t mine = tid < p.n ? p.slots[tid] : -1, slot = p.slots[i];
+    if (slot < 0) return;   // a padded token
+    if (slot >= p.num_slots) {
+        if (tid == 0 && kh == 0) raise_flag(p.err, PKV_DEVERR_RANGE);
+        return;
+    }
+    if (tid < kMaxTile) who[tid] = -1;
+    __syncthreads();
+    if (mine >= 0 && mine >> p.t_shift == slot >> p.t_shift) atomicMax(&who[mine & (t - 1)], tid);   // (the last of equal ones)
+    __syncthreads();
+    // every warp for itself: the named slots of the tile, which of them is the first, and the list
+    const int w0 = who[lane], w1 = who[lane + 32];
+    const uint32_t h0 = __ballot_sync(0xffffffffu, w0 >= 0), h1 = __ballot_sync(0xffffffffu, w1 >= 0);
+    const uint64_t mask = h0 | (static_cast<uint64_t>(h1) << 32);
+    const int first = __ffsll(static_cast<long long>(mask)) - 1;
+    if (who[first] != i) return;   // another token owns the tile
+    if (warp == 0 && w0 >= 0) {
+        const int at = __popc(h0 & ((1u << lane) - 1));
+        mem.ent[at] = lane;
+        mem.tok[at] = w0;
+    }
+    if (warp == 1 && w1 >= 0) {
+        const int at = __popc(h0) + __popc(h1 & ((1u << lane) - 1));
+        mem.ent[at] = lane + 32;
+        mem.tok[at] = w1;
+    }
+    __syncthreads();
+    const int m = __popcll(mask);
+    constexpr int kFew = 2 * (32 / (2 * D / 16));
+    if (m > kFew)
+        store_tile<D, kVec, kThreads>(p, slot >> p.t_shift, kh, mem, mask, m, red);
+    else if (warp == 0)
+        store_tile<D, kVec, 32>(p, slot >> p.t_shift, kh, mem, mask, m, red);
+}
+
 // A block looks at a chunk of tokens and stores the tiles that they own, of one kv head: tiles
 // of few rows a warp each, the others by all its threads.
+constexpr int kLists = 4;   // tiles of many rows whose members are listed where they are found
 template <int D, bool kVec>
-__global__ void __launch_bounds__(kThreads) store_kernel(const StoreParams p) {
-    __shared__ Members many, few[kWarps];
+__global__ void __launch_bounds__(kThreads, 3) store_kernel(const StoreParams p) {
+    __shared__ Members many[kLists], few[kWarps];
     __shared__ int64_t seen[kMaxChunk], big[kMaxChunk];
     __shared__ uint32_t red[kWarps][2];
-    __shared__ int n_seen, n_big, n_many;
+    __shared__ int n_seen, n_big;
     __shared__ uint32_t mask_s[2];
+    __shared__ uint64_t masks[kLists];
+    __shared__ int32_t chunk_s[kMaxChunk];
     pdl_wait();          // who comes from the kernel before
     pdl_launch_next();
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31, kh = blockIdx.y, t = 1 << p.t_shift;
     if (tid == 0) n_seen = n_big = 0;
+    const int i0 = static_cast<int>(blockIdx.x) * p.chunk, i = i0 + tid;
+    if (tid < p.chunk) chunk_s[tid] = tid < p.n - i0 ? p.slots[i] : -1;
     __syncthreads();
-    const int64_t i = static_cast<int64_t>(blockIdx.x) * p.chunk + tid;
-    if (tid < p.chunk && i < p.n) {
-        const int64_t slot = p.slots[i];
+    // The token that the call stores at `slot`, or -1 (one of the chunk is not looked at in memory again).
+    auto owner_of = [&](int64_t slot) {
+        const int w = p.who[slot];
+        if (w < 0 || w >= p.n) return -1;
+        return (w >= i0 && w - i0 < p.chunk ? chunk_s[w - i0] : p.slots[w]) == slot ? w : -1;
+    };
+    if (tid < p.chunk) {
+        const int64_t slot = chunk_s[tid];
         // (the slot before it is mostly the token before it: then that, or one further back, owns the tile)
-        if (slot >= 0 && slot < p.num_slots && p.who[slot] == i && (!(slot & (t - 1)) || owner(p, slot - 1) < 0))
-            seen[atomicAdd(&n_seen, 1)] = slot;
+        if (slot >= 0 && slot < p.num_slots) {
+            const bool head = !(slot & (t - 1));
+            const int w = p.who[slot], before = head ? -1 : owner_of(slot - 1);
+            if (w == i && before < 0) seen[atomicAdd(&n_seen, 1)] = slot;
+        }
     }
     __syncthreads();
     constexpr int kFew = 2 * (32 / (2 * D / 16));
@@ -170,47 +226,58 @@ __global__ void __launch_bounds__(kThreads) store_kernel(const StoreParams p) {
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
             const int e = 32 * h + lane;
-            w[h] = e < t ? owner(p, (tile << p.t_shift) + e) : -1;
+            w[h] = e < t ? owner_of((tile << p.t_shift) + e) : -1;
             have[h] = __ballot_sync(0xffffffffu, w[h] >= 0);
         }
         const uint64_t mask = have[0] | (static_cast<uint64_t>(have[1]) << 32);
         if (mask & ((1ull << (slot & (t - 1))) - 1)) continue;   // an earlier slot's token owns the tile
         const int m = __popcll(mask);
+        int place = -1;
         if (m > kFew) {
-            if (lane == 0) big[atomicAdd(&n_big, 1)] = tile;
-            continue;
+            if (lane == 0) {
+                place = atomicAdd(&n_big, 1);
+                big[place] = tile;
+                if (place < kLists) masks[place] = mask;
+            }
+            place = __shfl_sync(0xffffffffu, place, 0);
+            if (place >= kLists) continue;
         }
+        Members &list = place >= 0 ? many[place] : few[warp];
         __syncwarp();
 #pragma unroll
         for (int h = 0; h < 2; ++h)
             if (w[h] >= 0) {
                 const int at = (h ? __popc(have[0]) : 0) + __popc(have[h] & ((1u << lane) - 1));
-                few[warp].ent[at] = 32 * h + lane;
-                few[warp].tok[at] = w[h];
+                list.ent[at] = 32 * h + lane;
+                list.tok[at] = w[h];
             }
         __syncwarp();
+        if (place >= 0) continue;
         store_tile<D, kVec, 32>(p, tile, kh, few[warp], mask, m, red);
     }
     __syncthreads();
     const int all = n_big;
     for (int s = 0; s < all; ++s) {
-        const int64_t tile = big[s];
-        int w = -1;
-        uint32_t have = 0;
-        if (warp < 2) {
-            w = tid < t ? owner(p, (tile << p.t_shift) + tid) : -1;
-            have = __ballot_sync(0xffffffffu, w >= 0);
-            if (lane == 0) mask_s[warp] = have;
+        if (s >= kLists) {   // (rows in no order: the list again, over the last one)
+            int w = -1;
+            uint32_t have = 0;
+            Members &list = many[kLists - 1];
+            if (warp < 2) {
+                w = tid < t ? owner_of((big[s] << p.t_shift) + tid) : -1;
+                have = __ballot_sync(0xffffffffu, w >= 0);
+                if (lane == 0) mask_s[warp] = have;
+            }
+            __syncthreads();
+            if (w >= 0) {
+                const int at = (warp ? __popc(mask_s[0]) : 0) + __popc(have & ((1u << lane) - 1));
+                list.ent[at] = tid;
+                list.tok[at] = w;
+            }
+            if (tid == 0) masks[kLists - 1] = mask_s[0] | (static_cast<uint64_t>(mask_s[1]) << 32);
+            __syncthreads();
         }
-        __syncthreads();
-        if (w >= 0) {
-            const int at = (warp ? __popc(mask_s[0]) : 0) + __popc(have & ((1u << lane) - 1));
-            many.ent[at] = tid;
-            many.tok[at] = w;
-        }
-        if (tid == 0) n_many = __popc(mask_s[0]) + __popc(mask_s[1]);
-        __syncthreads();
-        store_tile<D, kVec, kThreads>(p, tile, kh, many, mask_s[0] | (static_cast<uint64_t>(mask_s[1]) << 32), n_many, red);
+        const int at = min(s, kLists - 1);
+        store_tile<D, kVec, kThreads>(p, big[s], kh, many[at], masks[at], __popcll(masks[at]), red);
         __syncthreads();
     }
 }
@@ -323,15 +390,21 @@ extern "C" pkv_status pkv_byte_store(void *pool, int64_t num_tiles, int64_t tile
     p.slots = slot_mapping;
     p.who = static_cast<int32_t *>(workspace);
     p.err = err_flags;
+    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+    const bool vec = aligned(k_new, 32) && aligned(v_new, 32) && k_token_stride % 16 == 0 && v_token_stride % 16 == 0;
+    if (n_tokens <= kFewTokens) {
+        auto *few = head_dim == 128 ? (vec ? store_few_kernel<128, true> : store_few_kernel<128, false>)
+                                    : (vec ? store_few_kernel<64, true> : store_few_kernel<64, false>);
+        return launch_status(launch_chained(few, dim3(static_cast<unsigned>(n_tokens), static_cast<unsigned>(kv_heads)), dim3(kThreads), 0, s, p),
+                             "pkv_byte_store");
+    }
     // as many tokens to a block as leave two blocks for each SM
     const int64_t blocks = 2ll * std::max(1, sm_count());
     p.chunk = 1;
     while (p.chunk < kMaxChunk && static_cast<int64_t>(n_tokens) * kv_heads / (2 * p.chunk) >= blocks) p.chunk *= 2;
-    cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
     const pkv_status c = launch_status(launch_chained(claim_kernel, dim3((static_cast<unsigned>(n_tokens) + kThreads - 1) / kThreads),
                                                       dim3(kThreads), 0, s, p), "pkv_byte_store");
     if (c != PKV_OK) return c;
-    const bool vec = aligned(k_new, 32) && aligned(v_new, 32) && k_token_stride % 16 == 0 && v_token_stride % 16 == 0;
     auto *kern = head_dim == 128 ? (vec ? store_kernel<128, true> : store_kernel<128, false>)
                                  : (vec ? store_kernel<64, true> : store_kernel<64, false>);
     return launch_status(launch_chained(kern, dim3((static_cast<unsigned>(n_tokens) + p.chunk - 1) / p.chunk, static_cast<unsigned>(kv_heads)),

@@ -117,7 +117,10 @@ class _QuantPool:
 
     decode_size, extend_size = staticmethod(B.pkv_quant_decode_workspace_size), staticmethod(B.pkv_quant_extend_workspace_size)
     decode, extend = staticmethod(B.pkv_quant_decode), staticmethod(B.pkv_quant_extend)
-    store_launches = 1
+
+    @staticmethod
+    def store_launches(n):
+        return 1
 
 
 class _BytePool:
@@ -155,7 +158,10 @@ class _BytePool:
 
     decode_size, extend_size = staticmethod(B.pkv_byte_decode_workspace_size), staticmethod(B.pkv_byte_extend_workspace_size)
     decode, extend = staticmethod(B.pkv_byte_decode), staticmethod(B.pkv_byte_extend)
-    store_launches = 2
+
+    @staticmethod
+    def store_launches(n):
+        return 1 if n <= 256 else 2
 
 
 def _quantised(quant, k_pool, v_pool, page_size, err, scales):
@@ -382,7 +388,7 @@ class DecodeStep:
             if not self.fused or pb.gather:
                 n += 1                               # gather or build_indices
             if not self.fused or pb.gather or self.quant is not None:
-                n += (1 if self.quant is None else self.quant.store_launches) if pb.spec.stores else 0
+                n += (1 if self.quant is None else self.quant.store_launches(self.wl.batch)) if pb.spec.stores else 0
             # attention (+ merge when requests can split; a 4-bit call without one takes the least workspace)
             n += 1 + (1 if pb.ws_bytes > (256 if pb.quant else 0) else 0)
             n += 1 if pb.quant and self.wl.batch > 1024 else 0   # (the tile table of a large batch)
@@ -542,7 +548,7 @@ class ExtendStep:
             held = int(self.ew.qo_lens.max()) * (self.ew.num_q_heads // self.ew.num_kv_heads) > 128
             n = (2 if self.ws_bytes > 256 else 1) if not held or self.ew.batch > 1 else 0
             n += 2 if held else 0
-            return n + self.quant.store_launches + (0 if self.token_table else 1) + (1 if self.kv_end is not None else 0)
+            return n + self.quant.store_launches(int(self.ew.qo_lens.sum())) + (0 if self.token_table else 1) + (1 if self.kv_end is not None else 0)
         return (2 if self.token_table else 3) + (1 if self.kv_end is not None else 0) + (1 if self.ws_bytes > 0 else 0)
 
     def check_errors(self) -> int:
