@@ -444,8 +444,8 @@ pkv_status check(const pkv_byte_args *a, Call call, bool check_ptrs) {
 
 // Workspace of the weights: partial sums of given rows, or a decode's logits (and its lse where the
 // caller wants none).  Logits move 8 bytes per key and query head, where reading K again moves
-// head_dim per kv head (and takes the scores a second time): 32 requests of 128 to 8192 keys, 32
-// heads over 8 of 128.
+// head_dim per kv head and takes the scores a second time: for 32 requests of 128 to 8192 keys, 32
+// heads over 8 of 128, decode and weights took 42 us together so, and 87 with a second pass over K.
 struct WeighPlan {
     size_t part, lse;
     int64_t stride;          // floats of a row of logits
@@ -502,7 +502,9 @@ pkv_status run(const pkv_byte_args *a, Call call, void *ws, size_t ws_bytes, int
         // rows of a request and kv head: at most max_q_len's, or what the average says
         const int64_t most = a->max_q_len > 0 ? a->max_q_len : (a->total_q + a->batch - 1) / a->batch;
         const WeighParams wp{a->lse, reinterpret_cast<float *>(at), a->acc_in, a->acc_out, a->acc_row_stride};
-        return launch_weigh(who, p, wp, a->head_dim, most * p.g, s);
+        // keys: total_kv, or half of what max_seq_len allows
+        const int64_t keys = a->total_kv > 0 ? a->total_kv : static_cast<int64_t>(a->batch) * a->max_seq_len / 2;
+        return launch_weigh(who, p, wp, a->head_dim, most * p.g, keys, s);
     }
     Plan pl;
     if (!make_plan(a, call == kExtend, shape_of(a), pl)) return fail(PKV_ERR_UNSUPPORTED, "%s: too many splits, keys or requests", who);

@@ -694,16 +694,22 @@ __global__ void __launch_bounds__(256) finish_kernel(const Params p, const Weigh
     wp.acc_out[first + mine] = before + ((s[0] + s[kFinishKeys]) + (s[2 * kFinishKeys] + s[3 * kFinishKeys]));
 }
 
-// Rows of a request and kv head from which the tensor cores' tiles of 128 keys pay.
-constexpr int kManyRows = 32;
+// The tensor cores' tiles cost the same for few rows as for many, and a span that starts inside a request starts
+// slowly; the other kernel's blocks are short, but take each row's time.  So the first is taken for many rows, or
+// where an SM has many tiles.  Measured (8 kv heads of 128, us; tensor cores / not): 16 requests x 4096 keys (27 tiles
+// per SM), 4 rows per kv head 36.9 / 39.0, 32 rows 36.9 / 47.1, 128 rows 41 / 84; 8 x 16384 (54 tiles), 4 rows 58 / 70; 16 x
+// 2048 (13 tiles), 4 rows 27.6 / 20.6, 32 rows 26.9 / 24.6, 64 rows 28.7 / 32.7; 64 x 512, 32 rows 36.9 / 24.9, 128 rows
+// 45 / 47; 4 x 4096, 32 rows 22.6 / 14.4, 64 rows 22.6 / 18.5, 128 rows 24.7 / 26.6; 1 x 4096, 64 rows 14.5 / 16.5.
+constexpr int kManyRows = 64, kManyTiles = 20;
 
 }  // namespace
 
-pkv_status launch_weigh(const char *who, const Params &p, const WeighParams &wp, int head_dim, int64_t rows, cudaStream_t s) {
+pkv_status launch_weigh(const char *who, const Params &p, const WeighParams &wp, int head_dim, int64_t rows, int64_t keys, cudaStream_t s) {
     const unsigned L = static_cast<unsigned>(p.tab.max_len), B = static_cast<unsigned>(p.batch), H = static_cast<unsigned>(p.hkv);
     if (L == 0) return ok();
     pkv_status st;
-    if (rows >= kManyRows && p.batch <= kTcBatch) {
+    const bool many = rows >= kManyRows || keys * p.hkv / kTcKeys >= static_cast<int64_t>(kManyTiles) * std::max(1, sm_count());
+    if (many && p.batch <= kTcBatch) {
         Params q = p;
         if (boxes(p.t_shift, head_dim)) {   // the pool as lines of 128 bytes; a box is K's of a tile and head
             const uint32_t lines = static_cast<uint32_t>((head_dim << p.t_shift) / 128);

@@ -25,8 +25,9 @@ __device__ __forceinline__ const uint8_t *scales_at(const Params &p, const uint8
     return piece + (static_cast<int64_t>(p.hkv - kh) * 2 * D << p.t_shift) + 2 * kh;
 }
 
-// acc_out = acc_in + the weights of the given rows (`rows`: what the host expects of a request and kv head).
-pkv_status launch_weigh(const char *who, const Params &p, const WeighParams &wp, int head_dim, int64_t rows, cudaStream_t s);
+// acc_out = acc_in + the weights of the given rows (`rows`: what the host expects of a request and kv head, `keys`: of all requests).
+pkv_status launch_weigh(const char *who, const Params &p, const WeighParams &wp, int head_dim, int64_t rows, int64_t keys,
+                        cudaStream_t s);
 // acc_out = acc_in + the weights of a decode whose logits are in p.logits.
 pkv_status launch_finish(const char *who, const Params &p, const WeighParams &wp, cudaStream_t s);
 

@@ -570,6 +570,27 @@ def test_weights_of_rows(B, D, ps, H, g, lens, rows, bounds):
     assert torch.equal(acc, again)
 
 
+@pytest.mark.parametrize("total", [0, 1 << 22])
+@pytest.mark.parametrize("D,ps,H,g,lens,rows", [
+    (128, 64, 2, 1, [300, 1, 0, 129], [1, 1, 1, 1]),
+    (64, 16, 1, 4, [128, 127, 700], [0, 0, 3]),
+    (128, 1, 1, 2, [260], [2]),
+    (64, 4, 3, 5, [90, 513, 64], [9, 1, 4]),
+    (128, 256, 1, 8, [2000, 31], [7, 7]),
+])
+def test_weights_of_few_rows_of_many_keys(B, D, ps, H, g, lens, rows, total):
+    """The bound on the keys decides which kernel runs, not what comes out."""
+    rng = np.random.default_rng(33 + D + ps + sum(lens))
+    cache = Cache(rng, lens, ps, H, D)
+    q = to_bf16(values(rng, (sum(rows), H * g, D)))
+    out, lse, e = extend(B, cache, q, rows)
+    acc, err = table_of(cache, rng, 0.0), err_word()
+    a = cache.args(B, "table", q, None, lse=lse, qo_indptr=i32(np.concatenate([[0], np.cumsum(rows)])), acc_out=acc, total_kv=total)
+    B.pkv_byte_weights(a, torch.empty(B.pkv_byte_weights_workspace_size(a), dtype=torch.uint8, device=DEV), err)
+    assert err.item() == any(n > L for n, L in zip(rows, lens))   # (causal rows of a request without keys are flagged)
+    check(cache, q, None, None, rows, acc=acc)
+
+
 @pytest.mark.parametrize("more", [0, 60])
 @pytest.mark.parametrize("tiny", [2.0 ** -4, 2.0 ** -100])
 def test_weights_of_extreme_rows(B, more, tiny):
