@@ -729,7 +729,8 @@ typedef struct pkv_byte_args {
  *     acc_out[row, s + t] = acc_in[row, s + t] + sum over query heads h of exp(sm_scale q[b,h] . K[t] - lse[b,h])
  * for the keys t < L of request b (row = req_pool_idx[b], s = kv_start[b] or 0): the columns
  * of req_to_token.  Other columns are left as they were.  Requests that share a row get
- * unspecified sums.
+ * unspecified sums.  The workspace then holds the call's logits as well, 4 bytes for each of
+ * batch x Hq x max_seq_len.
  * workspace: at least pkv_byte_decode_workspace_size(args) bytes, 256-byte aligned, not
  * shared with a call that may run at the same time; it needs no initialisation.
  */
@@ -840,8 +841,8 @@ int32_t pkv_abi_version(void);
  *
  * Failure detection without a hang, after the fail-loud checks of the AWS
  * Neuron encoder-cache doc ("Read Path"): the kernels that pipeline through
- * mbarriers (the TMA decode, MLA decode, pkv_extend and 4-bit attention kernels) wait on them
- * for at most this many nanoseconds.  A wait that runs out raises
+ * mbarriers (the TMA decode, MLA decode and pkv_extend kernels, and those over 4- and 8-bit
+ * pools) wait on them for at most this many nanoseconds.  A wait that runs out raises
  * PKV_DEVERR_TIMEOUT in err_flags and makes its CTA give up: every CTA that
  * sees the flag stops waiting, lets the copies and MMAs it already issued
  * complete, frees its tensor memory and returns, so the launch ends and the
