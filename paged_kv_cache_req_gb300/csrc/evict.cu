@@ -268,13 +268,18 @@ __global__ void __launch_bounds__(T) move_kernel(const Params p) {
             known |= static_cast<uint32_t>(bins - 1) << shift;
             want -= found[1];
             ties = found[2];
+            if (ties == want) {   // all of them go, whatever their further digits
+                border |= ~known;
+                break;
+            }
         }
         // ---- of the pages at the border the last `want` go.  Each warp has a run of pages, 32 at a time.
         const int per = ((hi - lo + T / 32 - 1) / (T / 32) + 31) / 32 * 32, i0 = min(hi - lo, warp * per), i1 = min(hi - lo, i0 + per);
         const int stay = ties - want;
         const uint32_t lower = (1u << lane) - 1;
         int tie = 0, sum;
-        if (ties > want) {   // else all of them go
+        const bool all_go = ties == want;
+        if (!all_go) {
             for (int i = i0 + lane; i < i1 + lane; i += 32) tie += __popc(__ballot_sync(0xffffffffu, i < i1 && keys[i] == border));
             tie = warps_scan<T>(tie, scratch, &sum);
             if (size > 1) {
@@ -284,11 +289,17 @@ __global__ void __launch_bounds__(T) move_kernel(const Params p) {
             }
         }
         int gone = 0;
-        for (int i = i0 + lane, x = tie; i < i1 + lane; i += 32) {
-            const uint32_t k = i < i1 ? keys[i] : 0xffffffffu;
-            const uint32_t eq = __ballot_sync(0xffffffffu, i < i1 && k == border);
-            gone += __popc(__ballot_sync(0xffffffffu, i < i1 && (k < border || (k == border && (ties <= want || x + __popc(eq & lower) >= stay)))));
-            x += __popc(eq);
+        if (all_go) {
+#pragma unroll 4
+            for (int i = i0 + lane; i < i1; i += 32) gone += keys[i] <= border;
+            gone = __reduce_add_sync(0xffffffffu, gone);
+        } else {
+            for (int i = i0 + lane, x = tie; i < i1 + lane; i += 32) {
+                const uint32_t k = i < i1 ? keys[i] : 0xffffffffu;
+                const uint32_t eq = __ballot_sync(0xffffffffu, i < i1 && k == border);
+                gone += __popc(__ballot_sync(0xffffffffu, i < i1 && (k < border || (k == border && x + __popc(eq & lower) >= stay))));
+                x += __popc(eq);
+            }
         }
         gone = warps_scan<T>(gone, scratch, &sum);
         if (size > 1) {
@@ -310,14 +321,17 @@ __global__ void __launch_bounds__(T) move_kernel(const Params p) {
             for (int j = 0; j < kAhead; ++j) {
                 const int i = j0 + 32 * j + lane;
                 const uint32_t k = i < i1 ? keys[i] : 0xffffffffu;
-                const uint32_t eq = __ballot_sync(0xffffffffu, i < i1 && k == border);
-                const bool goes = i < i1 && (k < border || (k == border && (ties <= want || tie + __popc(eq & lower) >= stay)));
+                bool goes = i < i1 && k <= border;
+                if (!all_go) {
+                    const uint32_t eq = __ballot_sync(0xffffffffu, i < i1 && k == border);
+                    goes = i < i1 && (k < border || (k == border && tie + __popc(eq & lower) >= stay));
+                    tie += __popc(eq);
+                }
                 const uint32_t g = __ballot_sync(0xffffffffu, goes);
                 const int at = gone + __popc(g & lower);
                 if (goes) out[at] = slot[j] >> p.ps_shift;
                 if (i < i1) places[lo + i] = goes ? 0xffffffffu : static_cast<uint32_t>(lo + i - at);
                 gone += __popc(g);
-                tie += __popc(eq);
             }
         }
         sync_all(size);   // all places are known to the cluster
