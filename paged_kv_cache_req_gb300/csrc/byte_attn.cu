@@ -14,6 +14,11 @@
 // Lane (r, c) = (lane / 4, lane % 4) holds dims D/4 c ... of key row r for K, and dims D/8 r
 // ... of keys of column c for V, as the 4-bit kernel's do; codes of two keys are interleaved before
 // V's conversion, so that one gives the pair of keys that the MMA wants.
+//
+// What bounds it: with one row per head a large call reads the pool at 6.3 TB/s (64 requests x 16384 keys, 8 heads of
+// 128: 340 us; 4096 keys: 101 us, of which 16 are the table, first copies, uneven ends and the merge).  With 9 to 16
+// rows, 16 x 16384 keys take 105 us for 302 MB: 32 % of the tensor pipe, warps waiting for their own last instruction
+// (8 warps of 250 registers).  With heads of 64 dims instructions bound it: 64 x 1500 keys x 20 heads in 52 us, 48 % of the ALU.
 #include "byte_weigh.cuh"
 
 namespace pkv {
@@ -35,8 +40,8 @@ struct Quant8 {
     static constexpr int kDim = D, kT = kT_;
     static constexpr bool kUnits = true, kHeldBf16V = true;
     static constexpr const char *kExtend = "pkv_byte_extend";
-    // A stage is a tile of 64 keys, or of 32 (D = 128 and 16 rows, whose math takes so long that 8 warps are
-    // needed): K codes [keys][D], V codes [keys][D], or where pieces are smaller but 2 KB or more (kT = 16, or 0: of
+    // A stage is a tile of 64 keys, or of 32 (D = 128 and 16 rows, for 8 warps in place of 6: 64 requests x 4
+    // rows over up to 16384 keys 98 us for 101): K codes [keys][D], V codes [keys][D], or where pieces are smaller but 2 KB or more (kT = 16, or 0: of
     // the pool's t slots) those as they lie.  In each line of 128 bytes the eight 16-byte chunks are swapped about, chunk x ^ (line %
     // 8), by the tensor copies or by the lanes that copy: the keys that eight lanes read at a time lie a
     // line apart or more, and so in different banks.  Beside it the scales: 16 bytes of a piece with its
@@ -445,7 +450,7 @@ pkv_status check(const pkv_byte_args *a, Call call, bool check_ptrs) {
 // Workspace of the weights: partial sums of given rows, or a decode's logits (and its lse where the
 // caller wants none).  Logits move 8 bytes per key and query head, where reading K again moves
 // head_dim per kv head and takes the scores a second time: for 32 requests of 128 to 8192 keys, 32
-// heads over 8 of 128, decode and weights took 42 us together so, and 87 with a second pass over K.
+// heads over 8 of 128, decode and weights took 52 us together so (42 now), and 87 with a second pass over K.
 struct WeighPlan {
     size_t part, lse;
     int64_t stride;          // floats of a row of logits

@@ -11,7 +11,8 @@ namespace {
 // What keys receive from given rows: a block takes 512 keys of one request and kv head, its warps 64
 // each, over all the request's rows, 128 at a time in shared memory as fp16.  With lse known a
 // weight is one exponential: w = 2^(logit - lse2).  Partial sums, one per kv head, are added up
-// by add_kernel in a fixed order.
+// by add_kernel in a fixed order.  Up to 16 rows the loads' latency bounds it (8 requests x 16384 keys, 8 heads of
+// 128: 70 us for 134 MB of K), above that the MMAs and exponentials (128 rows: 154).
 constexpr int kWeighWarps = 8, kWeighKeys = 64 * kWeighWarps, kWeighRows = 128;
 
 __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
@@ -201,6 +202,9 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 2) weigh_kernel(const Params
 // fp16 in shared memory, with the fence that the tensor cores then need and that waits for the next
 // tiles' loads too: 107.)  One thread issues the MMAs, and two groups of four warps take the tiles' scores in
 // turn, a key per thread: its row becomes weights and their sum.
+// 8 requests x 32 rows of 32 heads over up to 32768 keys take 57 us with add_kernel's 5: 24 % of the tensor
+// pipe, 26 % of the ALU.  A tile of 128 keys takes an SM 0.85 us, the converting warps' chain from codes to tensor memory, and
+// a span's start inside a request some 6 us.
 constexpr int kTcKeys = 128, kTcRows = 128;   // keys of a tile, query rows at a time
 constexpr int kTcThreads = 448;               // warps 0-3 convert, 4-11 weigh, 12 issues, 13 copies
 constexpr int kTcBatch = 1024;                // requests whose tiles are numbered in shared memory
@@ -647,7 +651,8 @@ __global__ void __launch_bounds__(256) add_kernel(const Params p, const WeighPar
 }
 
 // The same from a decode's logits: acc_out = acc_in + sum over heads of 2^(logit - lse2).  A thread
-// has four keys and every fourth head, whose loads are all on their way before the first is used.
+// has four keys and every fourth head, whose loads are all on their way before the first is used: the logits are
+// still in L2 (32 requests of up to 8192 keys, 32 heads: 12 MB in 7.9 us cold), and latency bounds it.
 constexpr int kFinishKeys = 256;
 __global__ void __launch_bounds__(256) finish_kernel(const Params p, const WeighParams wp) {
     __shared__ float4 sums[4][kFinishKeys / 4];

@@ -14,14 +14,15 @@ namespace quant {
 
 constexpr int kThreads = 256;
 
-// Both kernels give a lane one block of 16 dims and a warp 32 neighbouring blocks of one token
+// Reading back, and the 4-bit store, give a lane one block of 16 dims and a warp 32 neighbouring blocks of one token
 // (its K rows head by head, then its V rows): 1 KB of bf16 in one run, which is where most of
 // the bytes are.  (A warp that takes the same row of 4 or 8 tokens instead has the pool's
 // codes in one run and bf16 in pieces of 128 or 256 bytes: 3 to 7 % slower.)  A token is
 // `iters` such steps; few tokens are cut into `parts` of them so that every SM has some.
 //
-// Both are bound by memory, the conversions next (ALU half busy).  Stored and read back: 86,000
-// tokens x 20 heads of 64 (1.13 GB in all) 210 us, 5.4 TB/s; 8192 x 8 heads of 128 (86 MB) 24 us.
+// Both are bound by memory, the conversions next (ALU half busy).  Stored in 4 bits and read back: 86,000
+// tokens x 20 heads of 64 (1.13 GB in all) 210 us, 5.4 TB/s; 8192 x 8 heads of 128 (86 MB) 24 us.  (From the
+// 8-bit pool the latter are read back in 13.5 us, 50 MB.)
 __host__ __device__ inline int row_iters(int head_dim, int hkv) { return (2 * hkv * (head_dim / kBlock) + 31) / 32; }
 // log2 of the tokens that share a warp, where a token has half a warp's blocks or fewer (one kv
 // head, or two of 64 dims): 262,144 tokens of one head of 128 read back 77 us with one to a

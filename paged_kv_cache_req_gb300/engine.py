@@ -633,6 +633,8 @@ class BudgetedDecode:
         args = self._args(q, out, lse, qo_indptr=up(at), max_q_len=max(new_lens))
         B.pkv_byte_extend(args, torch.empty(B.pkv_byte_extend_workspace_size(args), dtype=torch.uint8, device=self.device), self.err)
         seen = [min(n, self.window) for n in new_lens]
+        if not sum(seen):
+            return out
         rows = up(np.concatenate([np.arange(e - n, e) for e, n in zip(at[1:], seen)]))
         args = self._args(q[rows], None, lse[rows], qo_indptr=up(np.concatenate([[0], np.cumsum(seen)]).astype(np.int32)),
                           acc_in=self.acc, acc_out=self.acc)

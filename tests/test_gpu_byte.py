@@ -140,6 +140,81 @@ def test_store_same_slot_twice(B):
         assert any((got == w).all() for w in wants)
 
 
+@pytest.mark.parametrize("n", [256, 257, 2500])
+@pytest.mark.parametrize("D,ps,H,order", [(128, 8, 8, "rising"), (64, 16, 8, "any"), (128, 64, 8, "falling"), (64, 1, 8, "any"),
+                                          (128, 4, 1, "rising")])
+def test_store_around_the_sizes_that_change_the_kernel(B, D, ps, H, order, n):
+    """Whole tiles and parts of them, slots named twice (by rows that hold the same), padding, slots outside."""
+    rng = np.random.default_rng(D + ps + n)
+    t = R.tile_of(ps)
+    tiles = -(-n // t) + 3
+    k, v = values(rng, (n, H, D)), values(rng, (n, H, D), 3.0)
+    slots = 3 + np.arange(n, dtype=np.int32) if order == "rising" else rng.permutation(n).astype(np.int32) + t
+    if order == "falling":
+        slots = np.sort(slots)[::-1].copy()
+    for a, b in ((5, 200), (0, n - 1), (n // 2, 17)):
+        slots[b], k[b], v[b] = slots[a], k[a], v[a]
+    alone = slots.copy()
+    alone[[200, n - 1, 17]] = -1
+    for where, what in ((40, -1), (41, -7), (n - 2, tiles * t), (90, 2 ** 31 - 1)):
+        slots[where], alone[where] = what, -1
+    want = random_pool(rng, tiles, ps, D, H)
+    pool = up(want.data)
+    want.store(k, v, alone)
+    assert store(B, pool, to_bf16(k), to_bf16(v), slots, ps) == 1
+    got = pool.cpu().numpy()
+    assert (got == want.data).all(), "%d bytes differ" % (got != want.data).sum()
+
+
+def test_pool_of_more_than_4_gb(B):
+    """Rows stored, read, attended and weighed at both ends of a large pool."""
+    rng = np.random.default_rng(8)
+    H, D, ps, L = 8, 128, 64, 200
+    tiles = 2 ** 32 // R.tile_bytes(ps, D, H) + 40
+    pool = torch.empty((tiles, R.tile_bytes(ps, D, H)), dtype=torch.uint8, device=DEV)
+    pages = np.concatenate([np.arange(4), tiles - 1 - np.arange(4)]).reshape(2, 4)
+    table = (pages[:, :, None] * ps + np.arange(ps)).reshape(2, -1)[:, :L].astype(np.int32)
+    k, v = values(rng, (2 * L, H, D)), values(rng, (2 * L, H, D))
+    assert store(B, pool, to_bf16(k), to_bf16(v), table.reshape(-1), ps) == 0
+    small = R.Pool(np.zeros((8, R.tile_bytes(ps, D, H)), dtype=np.uint8), ps, D, H)
+    near = (np.arange(8).reshape(2, 4, 1) * ps + np.arange(ps)).reshape(2, -1)[:, :L]
+    small.store(k, v, near.reshape(-1))
+    assert (pool[torch.from_numpy(pages.reshape(-1)).to(DEV)].cpu().numpy()[:, :2 * ps * D * H].reshape(8, H, 2, ps, D)[[0, 1, 2, 4, 5, 6]] ==
+            small.codes[[0, 1, 2, 4, 5, 6]]).all()
+    rows, lens, err = i32([0, 1]), i32([L, L]), err_word()
+    ko, vo = [torch.empty((2 * L, H, D), dtype=torch.bfloat16, device=DEV) for _ in range(2)]
+    B.pkv_byte_gather(pool, up(table), rows, lens, L, ko, vo, i32([0, 0, 0]), err, page_size=ps)
+    assert (host(ko) == small.read(near.reshape(-1), 0)).all() and (host(vo) == small.read(near.reshape(-1), 1)).all()
+    n = 40
+    q = to_bf16(values(rng, (2 * n, H, D)))
+    acc = torch.zeros((2, L), device=DEV)
+    for one in (True, False):       # a decode that counts, and rows whose weights follow
+        x = q[:2] if one else q
+        out, lse = torch.empty_like(x), torch.empty(x.shape[:2], device=DEV)
+        kw = dict(page_size=ps, num_kv_heads=H, sm_scale=D ** -0.5, max_seq_len=L, lse=lse, req_to_token=up(table), req_pool_idx=rows,
+                  seq_lens=lens, qo_indptr=None if one else i32([0, n, 2 * n]))
+        acc.zero_()
+        a = B.make_byte_args(B.PKV_LAYOUT_REQ_TO_TOKEN, x, pool, out, acc_out=acc if one else None, **kw)
+        size, call = ((B.pkv_byte_decode_workspace_size, B.pkv_byte_decode) if one else
+                      (B.pkv_byte_extend_workspace_size, B.pkv_byte_extend))
+        call(a, torch.empty(size(a), dtype=torch.uint8, device=DEV), err)
+        if not one:
+            for total in (0, 1 << 22):
+                acc.zero_()
+                a = B.make_byte_args(B.PKV_LAYOUT_REQ_TO_TOKEN, x, pool, None, acc_out=acc, total_kv=total, **kw)
+                B.pkv_byte_weights(a, torch.empty(B.pkv_byte_weights_workspace_size(a), dtype=torch.uint8, device=DEV), err)
+                assert err.item() == 0
+        for b in range(2):
+            sl = slice(b, b + 1) if one else slice(b * n, (b + 1) * n)
+            ref, rl, w, tol, lt, wt = R.attention(host(x)[sl].astype(np.float64), small.read(near[b], 0), small.read(near[b], 1),
+                                                  [L] if one else np.arange(L - n + 1, L + 1), D ** -0.5, small.largest(near[b]))
+            R.assert_within(host(out)[sl], ref, tol, "out")
+            R.assert_within(host(lse)[sl], rl, lt, "lse")
+            want = w.sum((0, 1))
+            R.assert_within(host(acc)[b], want, wt.sum((0, 1)) + (len(ref) * H + 1) * 2.0 ** -23 * want, "weights")
+    assert err.item() == 0
+
+
 def test_store_flags_and_small_calls(B):
     rng = np.random.default_rng(3)
     k = values(rng, (4, 2, 128))
