@@ -217,7 +217,8 @@ template <int D>
 struct TcSmem {
     static constexpr int kSlab = 128 * 128;   // q: 128 rows of 64 dims
     static constexpr int kRaw = D / 64 * kSlab, kRawBytes = kTcKeys * D;
-    static constexpr int kOff = kRaw + kTcRaw * kRawBytes;  // [B + 1] first tile of each request
+    static constexpr int kReq = kRaw + kTcRaw * kRawBytes;  // [B] the requests
+    static constexpr int kOff = kReq + kTcBatch * static_cast<int>(sizeof(Req));   // [B + 1] first tile of each
     static constexpr int kBytes = kOff + (kTcBatch + 1) * 4;
     static constexpr int kColS = kTcK * D / 2;              // tensor memory: keys, then scores
 };
@@ -247,9 +248,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
     __shared__ __align__(8) uint64_t bars[2 * kTcRaw + 2 * kTcK + 2 * kTcS + 1];
     __shared__ int scan_s[kTcThreads / 32];
     __shared__ uint32_t tmem_slot;
-    __shared__ int left_s, low_s, exp_lo_s, exp_hi_s;
+    __shared__ int left_s, low_s, exp_lo_s, exp_hi_s, stop_s[2];
     uint8_t *smem = aligned_smem<1024>(smem_raw);
     int *off = reinterpret_cast<int *>(smem + C::kOff);
+    Req *reqs = reinterpret_cast<Req *>(smem + C::kReq);
     uint64_t *full = bars, *used = bars + kTcK, *scored = used + kTcK, *freed = scored + kTcS, *brought = freed + kTcS,
              *taken = brought + kTcRaw, *last = taken + kTcRaw;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -280,7 +282,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
     for (int b0 = 0, before = 0; b0 < p.batch; b0 += kTcThreads) {
         const int b = b0 + threadIdx.x;
         int v = 0;
-        if (b < p.batch) v = (load_req(p, b, blockIdx.x == 0).L + kTcKeys - 1) / kTcKeys;
+        if (b < p.batch) {
+            const Req r = load_req(p, b, blockIdx.x == 0);
+            reqs[b] = r;
+            v = (r.L + kTcKeys - 1) / kTcKeys;
+        }
         int incl = v;
         for (int o = 1; o < 32; o <<= 1) {
             const int x = __shfl_up_sync(0xffffffffu, incl, o);
@@ -309,22 +315,28 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
     constexpr int kPerRow = D / 16;   // lanes of a row of q
     const int kj = lane % kPerRow;
     uint32_t n = 0, issued = 0;   // tiles so far; of which the copies were issued
+    uint32_t pass = 0;
     int b = 0;
-    while (pos < pos_end) {
+    // The roles go through the same runs and passes, each as far ahead as the barriers of the tiles let it: a run's
+    // first keys are in tensor memory before the last one's weights are done.  The warps that weigh stage the rows and
+    // meet the issuing one before each pass; those leave together, the others by themselves.
+    const bool weighs = warp >= 4 && warp < 12;
+    bool ok = true, stop = false;
+    while (pos < pos_end && ok && !stop) {
         // ---- the next run of tiles of one request and kv head
         for (int hi = p.batch; hi - b > 1;) {
             const int mid = (b + hi) >> 1;
             if (static_cast<int64_t>(off[mid]) * p.hkv <= pos) b = mid; else hi = mid;
         }
-        const Req req = load_req(p, b, false);
+        const Req req = reqs[b];
         const int of_b = off[b + 1] - off[b], in_b = static_cast<int>(pos - static_cast<int64_t>(off[b]) * p.hkv);
         const int kh = in_b / of_b, t0 = in_b - kh * of_b;
         const int tiles = static_cast<int>(min(static_cast<int64_t>(of_b - t0), pos_end - pos)), k0 = t0 * kTcKeys;
         const int rows = req.n * p.g;
         const bool report = kh == 0;
         float *part = wp.part + (static_cast<int64_t>(kh) * p.batch + b) * p.tab.max_len;
-        if (rows == 0)
-            for (int i = threadIdx.x; i < min(tiles * kTcKeys, req.L - k0); i += kTcThreads) part[k0 + i] = 0.f;
+        if (rows == 0 && weighs)
+            for (int i = threadIdx.x - 128; i < min(tiles * kTcKeys, req.L - k0); i += 256) part[k0 + i] = 0.f;
         // a converting or weighing thread's key in each tile
         const int mine = (warp & 3) * 32 + lane;
         // (a warp stops where it first uses what it loaded: an entry of the table is looked at, and a scale
@@ -348,23 +360,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
         };
         for (int r0 = 0; r0 < rows; r0 += kTcRows) {
             const int live = min(kTcRows, rows - r0), cols = (live + 31) / 32 * 32;
-            if (threadIdx.x == 0) {
-                low_s = exp_lo_s = INT32_MAX;
-                exp_hi_s = INT32_MIN;
-            }
-            __syncthreads();
-            if (warp >= 4 && warp < 12) {
+            if (weighs) {
+                named_bar_sync(2, 256);              // the last pass is done: its rows may be overwritten
+                if (threadIdx.x == 128) {
+                    low_s = exp_lo_s = INT32_MAX;
+                    exp_hi_s = INT32_MIN;
+                    stop_s[pass & 1] = *left;        // (two in turn: the issuing warp may still look at the one before)
+                }
+                named_bar_sync(2, 256);
                 // ---- the rows of q, D/16 lanes each
                 constexpr int kRows = 256 / kPerRow;
                 const int tid = threadIdx.x - 128;
                 int low = INT32_MAX;
                 uint32_t w[kTcRows / kRows][8];
+                float lse_of[kTcRows / kRows];       // with the rows: all loads are on their way at once
+                int end_of[kTcRows / kRows];
 #pragma unroll
                 for (int i = 0; i < kTcRows / kRows; ++i) {
                     const int row = i * kRows + tid / kPerRow, rr = r0 + row, tok = token_of(p, rr);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) w[i][e] = 0;
+                    lse_of[i] = 0.f;
+                    end_of[i] = 0;                   // (rows past the last have bound 0: nothing of them counts)
                     if (row < live) {
+                        if (kj == 0) {
+                            lse_of[i] = __ldg(wp.lse + static_cast<int64_t>(req.qo0 + tok) * p.hq + kh * p.g + rr - tok * p.g);
+                            end_of[i] = !p.qo_indptr ? req.L : p.kv_end ? __ldg(p.kv_end + req.qo0 + tok) : req.L - req.n + tok + 1;
+                        }
                         const uint4 *src = reinterpret_cast<const uint4 *>(p.q + static_cast<int64_t>(req.qo0 + tok) * p.q_stride +
                                                                            (kh * p.g + rr - tok * p.g) * D + kj * 16);
                         const uint4 x = __ldg(src), y = __ldg(src + 1);
@@ -399,7 +421,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
                 const bool same = exp_hi_s - exp_lo_s <= 8;
 #pragma unroll
                 for (int i = 0; i < kTcRows / kRows; ++i) {
-                    const int row = i * kRows + tid / kPerRow, rr = r0 + row, tok = token_of(p, rr);
+                    const int row = i * kRows + tid / kPerRow;
                     const int e2 = exp_hi_s == INT32_MIN ? 0 : same ? exp_lo_s : up_by[i];   // (no row but zeros: any)
                     const float up = __int_as_float((e2 + 127) << 23), down = __int_as_float((127 - e2) << 23);
                     uint32_t h[8];
@@ -407,17 +429,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
                     for (int e = 0; e < 8; ++e) h[e] = pack_f16x2(bf16_lo(w[i][e]) * up, bf16_hi(w[i][e]) * up);
                     put_16(smem + kj / 4 * C::kSlab, row, kj % 4, h);
                     if (kj == 0 && row < cols) {
-                        int end = 0;                 // (rows past the last have bound 0: nothing of them counts)
-                        float lse = 0.f;
-                        if (row < live) {
-                            lse = wp.lse[static_cast<int64_t>(req.qo0 + tok) * p.hq + kh * p.g + rr - tok * p.g] * kLog2e;
-                            end = !p.qo_indptr ? req.L : p.kv_end ? p.kv_end[req.qo0 + tok] : req.L - req.n + tok + 1;
-                            if (end < 0 || end > req.L) {
-                                if (report) raise_flag(p.err, PKV_DEVERR_RANGE);
-                                end = 0;
-                            }
-                            if (lse == -INFINITY) end = 0;
+                        const float lse = lse_of[i] * kLog2e;
+                        int end = end_of[i];
+                        if (end < 0 || end > req.L) {
+                            if (report) raise_flag(p.err, PKV_DEVERR_RANGE);
+                            end = 0;
                         }
+                        if (lse == -INFINITY) end = 0;
                         f_s[row] = p.scale_log2 * down;
                         minus_lse_s[row] = -lse;
                         end_s[row] = end;
@@ -428,10 +446,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
                 if (lane == 0) atomicMin(&low_s, low);
                 fence_proxy_async_smem();            // before the tensor cores read it
             }
-            if (warp >= 4 && warp < 13) named_bar_sync(1, 288);   // (the others go ahead)
+            if (weighs || warp == 12) {
+                named_bar_sync(1, 288);              // (the others go ahead)
+                stop = stop_s[pass & 1] != 0;
+                if (stop) break;
+            }
+            ++pass;
             if (warp < 4) {
                 // -------------------------------------------------------- codes to fp16
-                bool ok = true;
+                // (the warps that weigh load the rows when they have done the last pass: these are ahead of them)
+                for (int i = threadIdx.x; i < live * (D / 64); i += 128) {   // lines of 128 bytes
+                    const int rr = r0 + i / (D / 64), tok = token_of(p, rr);
+                    prefetch_l2(p.q + static_cast<int64_t>(req.qo0 + tok) * p.q_stride + (kh * p.g + rr - tok * p.g) * D + i % (D / 64) * 64);
+                }
                 for (int t = 0; t < tiles; ++t) {
                     const uint32_t m = n + t, a = m % kTcK, raw = m % kTcRaw;
                     ok = __all_sync(0xffffffffu, ok && wait_or_leave(&brought[raw], (m / kTcRaw) & 1, left, p.err, p.wait_ns));
@@ -488,7 +515,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
                         e[i] = t < tiles && (!box || lane < pieces) ? entry_of(key) : -4;
                     }
                 };
-                bool ok = true;
                 auto bring = [&](int t, int32_t (&e)[4]) {
                     const uint32_t m = n + t, raw = m % kTcRaw;
                     if (m >= kTcRaw) ok = __all_sync(0xffffffffu, ok && wait_or_leave(&taken[raw], ((m / kTcRaw) & 1) ^ 1, left, p.err, p.wait_ns));
@@ -533,12 +559,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
             } else if (warp == 12) {
                 // -------------------------------------------------------- S = K q^T
                 const uint32_t idesc = tc05::idesc_f16_f32(kTcKeys, cols, false, false);
-                bool ok = true;
+                bool on = true;
                 for (int t = 0; t < tiles; ++t) {
                     const uint32_t m = n + t, a = m % kTcK, s = m % kTcS;
-                    ok = __all_sync(0xffffffffu, ok && wait_or_leave(&full[a], (m / kTcK) & 1, left, p.err, p.wait_ns) &&
+                    on = __all_sync(0xffffffffu, wait_or_leave(&full[a], (m / kTcK) & 1, left, p.err, p.wait_ns) &&
                                                      (m < kTcS || wait_or_leave(&freed[s], ((m / kTcS) & 1) ^ 1, left, p.err, p.wait_ns)));
-                    if (!ok) break;
+                    if (!on) break;
                     tc05::fence_after_sync();
                     if (lane == 0) {
                         const uint64_t qd = tc05::smem_desc(smem, 16, 1024);
@@ -555,7 +581,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
                 }
             } else {
                 // -------------------------------------------------------- weights: a key per thread
-                bool ok = true;
+                bool on = true;
                 const int turn = static_cast<int>(((warp >> 2) + 1 + n) & 1);   // the group's tiles: t % 2 = turn
                 const int low = low_s;
                 const bool same = exp_hi_s - exp_lo_s <= 8;
@@ -568,8 +594,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
                     const uint64_t ks = pair(scale, scale);
                     e_next = scale_byte(slot_at(next, t + 2));
                     next = entry(t + 4);
-                    ok = __all_sync(0xffffffffu, ok && wait_or_leave(&scored[s], (m / kTcS) & 1, left, p.err, p.wait_ns));
-                    if (!ok) break;
+                    on = __all_sync(0xffffffffu, wait_or_leave(&scored[s], (m / kTcS) & 1, left, p.err, p.wait_ns));
+                    if (!on) break;
                     tc05::fence_after_sync();
                     const int key = k0 + t * kTcKeys + mine;
                     const bool whole = k0 + (t + 1) * kTcKeys <= low;
@@ -614,15 +640,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
                 }
             }
             n += tiles;
-            tc05::fence_before_sync();
-            __syncthreads();
-            tc05::fence_after_sync();
-            if (*left) break;
+            if (!ok) break;
         }
-        if (*left) break;
         pos += tiles;
     }
+    tc05::fence_before_sync();
     __syncthreads();
+    tc05::fence_after_sync();
     if (warp == 13 && *left)   // copies that nobody waited for land before the block's memory is given back
         for (uint32_t m = issued > kTcRaw ? issued - kTcRaw : 0; m < issued; ++m) mbar_wait(&brought[m % kTcRaw], (m / kTcRaw) & 1);
     if (warp == 12) {
