@@ -202,11 +202,12 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 2) weigh_kernel(const Params
 // fp16 in shared memory, with the fence that the tensor cores then need and that waits for the next
 // tiles' loads too: 107.)  One thread issues the MMAs, and two groups of four warps take the tiles' scores in
 // turn, a key per thread: its row becomes weights and their sum.
-// 8 requests x 32 rows of 32 heads over up to 32768 keys take 57 us with add_kernel's 5: 24 % of the tensor
-// pipe, 26 % of the ALU.  A tile of 128 keys takes an SM 0.85 us, the converting warps' chain from codes to tensor memory, and
-// a span's start inside a request some 6 us.
+// 8 requests x 32 rows of 32 heads over up to 32768 keys take 47 us with add_kernel's 5.  A tile of 128 keys takes an SM
+// 0.77 us, the chain from codes to weights (no pipe is more than a third busy), and the start of a run of keys of one
+// request and kv head 4 to 5: its rows, then their factors.  A span of several runs has fewer tiles for that (53.5 us without).
 constexpr int kTcKeys = 128, kTcRows = 128;   // keys of a tile, query rows at a time
 constexpr int kTcThreads = 448;               // warps 0-3 convert, 4-11 weigh, 12 issues, 13 copies
+constexpr int kTcStart = 6;                   // stand-in tiles before a run's first: what starting it takes
 constexpr int kTcBatch = 1024;                // requests whose tiles are numbered in shared memory
 constexpr int kTcRaw = 4, kTcK = 2, kTcS = 3; // tiles of codes in shared memory; of keys, and of scores, in tensor memory
 
@@ -278,14 +279,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
         tc05::tmem_alloc(&tmem_slot, 512);
         tc05::tmem_relinquish();
     }
-    // ---- the sequence: off[b] = tiles of one kv head before request b
+    // ---- the sequence: off[b] = tiles of one kv head before request b, stand-ins among them
     for (int b0 = 0, before = 0; b0 < p.batch; b0 += kTcThreads) {
         const int b = b0 + threadIdx.x;
         int v = 0;
         if (b < p.batch) {
             const Req r = load_req(p, b, blockIdx.x == 0);
             reqs[b] = r;
-            v = (r.L + kTcKeys - 1) / kTcKeys;
+            v = r.L > 0 ? (r.L + kTcKeys - 1) / kTcKeys + kTcStart : 0;
         }
         int incl = v;
         for (int o = 1; o < 32; o <<= 1) {
@@ -330,8 +331,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
         }
         const Req req = reqs[b];
         const int of_b = off[b + 1] - off[b], in_b = static_cast<int>(pos - static_cast<int64_t>(off[b]) * p.hkv);
-        const int kh = in_b / of_b, t0 = in_b - kh * of_b;
-        const int tiles = static_cast<int>(min(static_cast<int64_t>(of_b - t0), pos_end - pos)), k0 = t0 * kTcKeys;
+        const int kh = in_b / of_b, at_b = in_b - kh * of_b, k0 = max(0, at_b - kTcStart) * kTcKeys;
+        const int part_of = static_cast<int>(min(static_cast<int64_t>(of_b - at_b), pos_end - pos));
+        const int tiles = part_of - max(0, kTcStart - at_b);
+        pos += part_of;
+        if (tiles <= 0) continue;
         const int rows = req.n * p.g;
         const bool report = kh == 0;
         float *part = wp.part + (static_cast<int64_t>(kh) * p.batch + b) * p.tab.max_len;
@@ -642,7 +646,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
             n += tiles;
             if (!ok) break;
         }
-        pos += tiles;
     }
     tc05::fence_before_sync();
     __syncthreads();
@@ -723,12 +726,12 @@ __global__ void __launch_bounds__(256) finish_kernel(const Params p, const Weigh
     wp.acc_out[first + mine] = before + ((s[0] + s[kFinishKeys]) + (s[2 * kFinishKeys] + s[3 * kFinishKeys]));
 }
 
-// The tensor cores' tiles cost the same for few rows as for many, and a span that starts inside a request starts
+// The tensor cores' tiles cost the same for few rows as for many, and a run of keys of one request and kv head starts
 // slowly; the other kernel's blocks are short, but take each row's time.  So the first is taken for many rows, or
 // where an SM has many tiles.  Measured (8 kv heads of 128, us; tensor cores / not): 16 requests x 4096 keys (27 tiles
-// per SM), 4 rows per kv head 36.9 / 39.0, 32 rows 36.9 / 47.1, 128 rows 41 / 84; 8 x 16384 (54 tiles), 4 rows 58 / 70; 16 x
-// 2048 (13 tiles), 4 rows 27.6 / 20.6, 32 rows 26.9 / 24.6, 64 rows 28.7 / 32.7; 64 x 512, 32 rows 36.9 / 24.9, 128 rows
-// 45 / 47; 4 x 4096, 32 rows 22.6 / 14.4, 64 rows 22.6 / 18.5, 128 rows 24.7 / 26.6; 1 x 4096, 64 rows 14.5 / 16.5.
+// per SM), 4 rows per kv head 36.9 / 39.0, 32 rows 36.8 / 47.1, 128 rows 39 / 84; 8 x 16384 (54 tiles), 4 rows 55 / 70; 16 x
+// 2048 (13 tiles), 4 rows 24.7 / 20.6, 32 rows 24.7 / 24.6, 64 rows 26.7 / 32.7; 64 x 512, 32 rows 33.2 / 24.9, 64 rows
+// 34.9 / 33.3, 128 rows 41 / 47; 4 x 4096, 32 rows 18.5 / 14.4, 64 rows 18.7 / 18.5, 128 rows 20.5 / 26.6.
 constexpr int kManyRows = 64, kManyTiles = 20;
 
 }  // namespace
