@@ -389,7 +389,7 @@ class DecodeStep:
                 n += 1                               # gather or build_indices
             if not self.fused or pb.gather or self.quant is not None:
                 n += (1 if self.quant is None else self.quant.store_launches(self.wl.batch)) if pb.spec.stores else 0
-            # attention (+ merge when requests can split; a 4-bit call without one takes the least workspace)
+            # attention (+ merge when requests can split; a call over a quantised pool without one takes the least workspace)
             n += 1 + (1 if pb.ws_bytes > (256 if pb.quant else 0) else 0)
             n += 1 if pb.quant and self.wl.batch > 1024 else 0   # (the tile table of a large batch)
         return n

@@ -666,6 +666,25 @@ def test_weights_of_few_rows_of_many_keys(B, D, ps, H, g, lens, rows, total):
     check(cache, q, None, None, rows, acc=acc)
 
 
+@pytest.mark.parametrize("batch", [1024, 1025])
+def test_weights_of_the_largest_batches(B, batch):
+    """As many requests as are numbered in shared memory, and one more; some without keys or rows."""
+    rng = np.random.default_rng(34)
+    lens = rng.integers(0, 200, batch)
+    lens[[0, 7, 8, batch - 1]] = [130, 0, 0, 129]
+    rows = np.minimum(rng.integers(0, 4, batch), lens)
+    cache = Cache(rng, [int(x) for x in lens], 16, 1, 64)
+    q = to_bf16(values(rng, (int(rows.sum()), 2, 64)))
+    rows = [int(x) for x in rows]
+    out, lse, e = extend(B, cache, q, rows)
+    assert e == 0
+    acc, err = table_of(cache, rng, 0.0), err_word()
+    a = cache.args(B, "table", q, None, lse=lse, qo_indptr=i32(np.concatenate([[0], np.cumsum(rows)])), acc_out=acc, total_kv=1 << 22)
+    B.pkv_byte_weights(a, torch.empty(B.pkv_byte_weights_workspace_size(a), dtype=torch.uint8, device=DEV), err)
+    assert err.item() == 0
+    check(cache, q, None, None, rows, acc=acc, only=set(range(0, batch, 9)) | {0, 7, 8, 1023, batch - 1})
+
+
 @pytest.mark.parametrize("more", [0, 60])
 @pytest.mark.parametrize("tiny", [2.0 ** -4, 2.0 ** -100])
 def test_weights_of_extreme_rows(B, more, tiny):
