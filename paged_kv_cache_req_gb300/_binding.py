@@ -1,10 +1,10 @@
 """Thin ctypes binding over libpkv.so: argument marshalling only.
 
-Every function has the name of the C entry point it calls (see include/pkv.h),
-takes torch tensors that already live on the GPU, passes their data pointers,
-sizes and the current CUDA stream, and raises :class:`PkvError` on a non-OK
-status.  No step of the computation runs here: there is no CPU fallback, and a
-missing or unloadable libpkv.so raises at import time.
+Every function has the name of the C entry point it calls (see include/pkv.h; those over
+an 8-bit pool, pkv_byte_*, also go by pkv_q8_*), takes torch tensors that already live on
+the GPU, passes their data pointers, sizes and the current CUDA stream, and raises
+:class:`PkvError` on a non-OK status.  No step of the computation runs here: there is no CPU
+fallback, and a missing or unloadable libpkv.so raises at import time.
 """
 from __future__ import annotations
 
@@ -734,6 +734,20 @@ def pkv_byte_extend(args: ByteArgs, workspace: torch.Tensor, err_flags, stream=N
 
 def pkv_byte_weights(args: ByteArgs, workspace: torch.Tensor, err_flags, stream=None):
     _quant_attend(_lib.pkv_byte_weights, "pkv_byte_weights", args, workspace, err_flags, stream)
+
+
+# The calls over an 8-bit pool by the name of their format, in the way of pkv_quant_* (their C names hold no digits).
+pkv_q8_tile_bytes = pkv_byte_tile_bytes
+pkv_q8_store_workspace_size = pkv_byte_store_workspace_size
+pkv_q8_store = pkv_byte_store
+pkv_q8_gather = pkv_byte_gather
+make_q8_args = make_byte_args
+pkv_q8_decode_workspace_size = pkv_byte_decode_workspace_size
+pkv_q8_decode = pkv_byte_decode
+pkv_q8_extend_workspace_size = pkv_byte_extend_workspace_size
+pkv_q8_extend = pkv_byte_extend
+pkv_q8_weights_workspace_size = pkv_byte_weights_workspace_size
+pkv_q8_weights = pkv_byte_weights
 
 
 def pkv_evict_workspace_size(batch: int, max_seq_len: int, page_size: int) -> int:
