@@ -316,7 +316,7 @@ def prepare(case, seed):
         st["cu"] = torch.zeros(batch + 1, dtype=torch.int32, device=dev)
         if own:
             from paged_kv_cache_req_gb300 import _binding as B
-            st["workspace"] = torch.empty(B.pkv_byte_store_workspace_size(st["pool"].shape[0], ps), dtype=torch.uint8, device=dev)
+            st["workspace"] = torch.empty(B.pkv_q8_store_workspace_size(st["pool"].shape[0], ps), dtype=torch.uint8, device=dev)
         return st
     _fill(st, gen, lens)
     rows = _rows(case)
@@ -365,9 +365,9 @@ def prepare(case, seed):
             kw.update(qo_indptr=st["qo_indptr"], max_q_len=int(rows.max()))
             if case["bounds"] == "given":
                 kw.update(kv_end=st["ends"])
-        size = {"decode": B.pkv_byte_decode_workspace_size, "extend": B.pkv_byte_extend_workspace_size,
-                "weigh": B.pkv_byte_weights_workspace_size if case.get("rows_hi") else B.pkv_byte_decode_workspace_size}[case["op"]]
-        st["args"] = B.make_byte_args(layout, st["q"], st["pool"], st["out"], **kw)
+        size = {"decode": B.pkv_q8_decode_workspace_size, "extend": B.pkv_q8_extend_workspace_size,
+                "weigh": B.pkv_q8_weights_workspace_size if case.get("rows_hi") else B.pkv_q8_decode_workspace_size}[case["op"]]
+        st["args"] = B.make_q8_args(layout, st["q"], st["pool"], st["out"], **kw)
         st["workspace"] = torch.empty(size(st["args"]), dtype=torch.uint8, device=dev)
     return st
 
@@ -536,16 +536,16 @@ def run(state):
         return _plain_write(state) if op == "write" else _plain_evict(state) if op == "evict" else _plain_attention(state)
     from paged_kv_cache_req_gb300 import _binding as B
     if op == "decode":
-        B.pkv_byte_decode(state["args"], state["workspace"], state["err"])
+        B.pkv_q8_decode(state["args"], state["workspace"], state["err"])
         return {"out": state["out"], "lse": state["lse"]}
     if op == "extend":
-        B.pkv_byte_extend(state["args"], state["workspace"], state["err"])
+        B.pkv_q8_extend(state["args"], state["workspace"], state["err"])
         return {"out": state["out"], "lse": state["lse"]}
     if op == "weigh":
         if case["rows_hi"]:
-            B.pkv_byte_weights(state["args"], state["workspace"], state["err"])
+            B.pkv_q8_weights(state["args"], state["workspace"], state["err"])
             return {"acc": state["acc_out"]}
-        B.pkv_byte_decode(state["args"], state["workspace"], state["err"])
+        B.pkv_q8_decode(state["args"], state["workspace"], state["err"])
         return {"out": state["out"], "lse": state["lse"], "acc": state["acc_out"]}
     if op == "evict":
         B.pkv_evict(state["table"], state["row"], state["lens"], state["acc"], state["budget"], state["free"],
@@ -555,9 +555,9 @@ def run(state):
                     seq_lens_out=state["lens_out"], free_state_out=state["state_out"])
         return {"table": state["table_out"], "acc": state["acc_out"], "lens": state["lens_out"], "free": state["free"],
                 "state": state["state_out"]}
-    B.pkv_byte_store(state["pool"], state["k_new"], state["v_new"], state["slot"], state["workspace"], state["err"],
+    B.pkv_q8_store(state["pool"], state["k_new"], state["v_new"], state["slot"], state["workspace"], state["err"],
                    page_size=case["ps"])
-    B.pkv_byte_gather(state["pool"], state["table"], state["row"], state["back"], state["back_max"], state["k_out"],
+    B.pkv_q8_gather(state["pool"], state["table"], state["row"], state["back"], state["back_max"], state["k_out"],
                     state["v_out"], state["cu"], state["err"], page_size=case["ps"], kv_start=state["start"])
     return {"k": state["k_out"], "v": state["v_out"], "cu": state["cu"]}
 
