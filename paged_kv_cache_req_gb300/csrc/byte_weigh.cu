@@ -21,6 +21,13 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
     return d;
 }
 
+// Factors from scores to base-2 logits of two rows and a key's scale.  The two are joined before the score: a score times
+// a row's factor alone may be past fp32 (queries near 2^123 over keys near 2^-123).  Finite, so that a score of 0 stays 0.
+__device__ __forceinline__ uint64_t factors(uint64_t f, uint64_t ks) {
+    const float2 x = unpair(mul2(f, ks));
+    return pair(fminf(x.x, 3.4e38f), fminf(x.y, 3.4e38f));
+}
+
 // Place in its row of the k-th 16 bytes of lane (r, c)'s dims: the four c of two rows lie in eight bank groups.
 __device__ __forceinline__ int q_chunk(int row, int c, int k) { return (4 * k + c) ^ ((row & 1) << 2); }
 template <int D>
@@ -157,7 +164,7 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 2) weigh_kernel(const Params
                 for (int kt = 0; kt < 2; ++kt)
 #pragma unroll
                     for (int u = 0; u < 2; ++u) {
-                        const float2 y = unpair(fma2(mul2(pair(s[kt][2 * u], s[kt][2 * u + 1]), f), ks[kt][u], lse));
+                        const float2 y = unpair(fma2(pair(s[kt][2 * u], s[kt][2 * u + 1]), factors(f, ks[kt][u]), lse));
                         float x0 = ex2(y.x), x1 = ex2(y.y);
                         if (!whole) {
                             const int key = key0 + kt * 16 + r + 8 * u;
@@ -629,8 +636,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
                                 const ulonglong2 f = *reinterpret_cast<const ulonglong2 *>(&f_s[c0 + e]);
                                 const ulonglong2 l = *reinterpret_cast<const ulonglong2 *>(&minus_lse_s[c0 + e]);
                                 const int4 end = *reinterpret_cast<const int4 *>(&end_s[c0 + e]);
-                                const float2 y0 = unpair(fma2(mul2(pair(x[e], x[e + 1]), f.x), ks, l.x));
-                                const float2 y1 = unpair(fma2(mul2(pair(x[e + 2], x[e + 3]), f.y), ks, l.y));
+                                const float2 y0 = unpair(fma2(pair(x[e], x[e + 1]), factors(f.x, ks), l.x));
+                                const float2 y1 = unpair(fma2(pair(x[e + 2], x[e + 3]), factors(f.y, ks), l.y));
                                 sum0 = add2(sum0, pair(key < end.x ? ex2(y0.x) : 0.f, key < end.y ? ex2(y0.y) : 0.f));
                                 sum1 = add2(sum1, pair(key < end.z ? ex2(y1.x) : 0.f, key < end.w ? ex2(y1.y) : 0.f));
                             }

@@ -1,0 +1,43 @@
+"""The calls over an 8-bit pool at the ends of what they allow: queries and keys near either end of
+bf16's range."""
+import numpy as np
+import pytest
+import torch
+
+import _byte_ref as R
+from test_gpu_byte import B, Cache, DEV, check, decode, err_word, extend, host, i32, table_of, to_bf16, values  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+
+def weights(B, cache, q, lse, rows, ends=None, **kw):
+    """pkv_byte_weights of the rows -> (acc, flags)."""
+    acc, err = table_of(cache, None, 0.0), err_word()
+    a = cache.args(B, "table", q, None, lse=lse, qo_indptr=i32(np.concatenate([[0], np.cumsum(rows)])),
+                   kv_end=None if ends is None else i32(ends), acc_out=acc, **kw)
+    B.pkv_byte_weights(a, torch.empty(B.pkv_byte_weights_workspace_size(a), dtype=torch.uint8, device=DEV), err)
+    return acc, err.item()
+
+
+def against(rng, big, lens, rows, g, ps=16, D=64, H=2):
+    """A cache whose keys are around `big`, and rows that bring the scores back; all of them finite."""
+    cache = Cache(rng, lens, ps, H, D, spread=big)
+    q = to_bf16(R.bf16(values(rng, (sum(rows), H * g, D)) / np.float32(big)))
+    assert torch.isfinite(q).all() and all(np.isfinite(cache.pool.read(s, 0)).all() for s in cache.slots)
+    return cache, q
+
+
+@pytest.mark.parametrize("total", [0, 1 << 22])
+@pytest.mark.parametrize("rows,g", [([5, 2], 2), ([40, 33], 2), ([32, 32], 1)])
+def test_weights_of_large_queries_over_small_keys(B, rows, g, total):
+    """Scores are moderate, though a score times the query's factor alone is past fp32: tiles that all rows see
+    and tiles at a bound, in both kernels."""
+    rng = np.random.default_rng(50 + sum(rows))
+    cache, q = against(rng, 2.0 ** -123, [700, 130], rows, g)
+    ends = np.concatenate([rng.integers(l // 2, l + 1, n) for l, n in zip(cache.lens, rows)])
+    out, lse, e = extend(B, cache, q, rows, "table", ends)
+    assert e == 0
+    check(cache, q, out, lse, rows, ends)
+    acc, e = weights(B, cache, q, lse, rows, ends, total_kv=total)
+    assert e == 0
+    check(cache, q, None, None, rows, ends, acc=acc)
