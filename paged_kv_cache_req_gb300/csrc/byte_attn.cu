@@ -344,7 +344,8 @@ struct Quant8 {
 
     template <int NT>
     __device__ __forceinline__ static void start(const Params &p, const Work &w, State<NT> &st, const uint32_t (&ahead)[D / 8], int lane) {
-        start_segment<D, NT>(p, w, st, ahead, lane);
+        // (queries below 2^-119 have factors below fp32's normal numbers; large keys' scales bring them back)
+        start_segment<D, NT>(p, w, st, ahead, lane, 0.f);
         st.unit = kNoUnit;
         if (p.logits) {   // (one query row per request)
             const int row = w.rb * 8 * NT + 2 * (lane & 3);

@@ -512,10 +512,11 @@ __device__ __forceinline__ void load_q(const Params &p, const Work &s, int n, ui
 }
 
 // q fragments, score factors and bounds of a segment's rows; a fresh softmax state.  At NT =
-// 1 the rows of q are in `ahead`, loaded a tile ago.
+// 1 the rows of q are in `ahead`, loaded a tile ago.  Factors are at least `least`: a normal number
+// where masked scores (-inf) are multiplied by them, 0 for formats whose keys have scales to join first.
 template <int D, int NT, class State>
 __device__ __forceinline__ void start_segment(const Params &p, const Work &s, State &st, const uint32_t (&ahead)[D / 8],
-                                              int lane) {
+                                              int lane, float least = 1.2e-38f) {
     const int r = lane >> 2, c = lane & 3;
     const float gk = p.k_scale ? p.k_scale[s.kh] : 1.f;
     const float small = fminf(p.scale_log2, gk), large = fmaxf(p.scale_log2, gk);
@@ -551,7 +552,7 @@ __device__ __forceinline__ void start_segment(const Params &p, const Work &s, St
             // kept normal and finite, so that -inf (a masked key) stays -inf and 0 stays 0
             // (the power of two joins the factor that it brings nearer to 1: scale x g alone may be 0)
             const float down = __int_as_float((127 - ev) << 23);
-            st.f[n][v] = fminf(fmaxf(ev < 0 ? small * down * large : large * down * small, 1.2e-38f), 3.4e38f);
+            st.f[n][v] = fminf(fmaxf(ev < 0 ? small * down * large : large * down * small, least), 3.4e38f);
             const int rv = s.rb * 8 * NT + n * 8 + 2 * c + v, tv = token_of(p, rv);
             int end = s.L;   // rows past the last (zeros, never written) ask for no masking
             if (tv < s.n) {

@@ -41,3 +41,28 @@ def test_weights_of_large_queries_over_small_keys(B, rows, g, total):
     acc, e = weights(B, cache, q, lse, rows, ends, total_kv=total)
     assert e == 0
     check(cache, q, None, None, rows, ends, acc=acc)
+
+
+@pytest.mark.parametrize("chunk", [0, 64])
+@pytest.mark.parametrize("ps,rows", [(64, None), (16, None), (4, None), (1, None), (16, [7, 4]), (64, [64, 20])])
+def test_small_queries_over_large_keys(B, ps, rows, chunk):
+    """Scores are moderate, though the query's factor alone is below fp32's normal numbers."""
+    rng = np.random.default_rng(60 + ps + chunk)
+    n = [1, 1] if rows is None else rows
+    cache, q = against(rng, 2.0 ** 122, [700, 130], n, 2, ps=ps)
+    if rows is None:
+        out, lse, e = decode(B, cache, q, kv_chunk=chunk)
+        assert e == 0
+        check(cache, q, out, lse)
+        acc = table_of(cache, None, 0.0)
+        out, lse, e = decode(B, cache, q, kv_chunk=chunk, acc_out=acc)
+        assert e == 0
+        check(cache, q, out, lse, acc=acc)
+        return
+    out, lse, e = extend(B, cache, q, rows, kv_chunk=chunk)
+    assert e == 0
+    check(cache, q, out, lse, rows)
+    for total in (0, 1 << 22):
+        acc, e = weights(B, cache, q, lse, rows, total_kv=total)
+        assert e == 0
+        check(cache, q, None, None, rows, acc=acc)
