@@ -580,6 +580,10 @@ class BudgetedDecode:
     come from one free list and go back to it.  ``width`` bounds a request's tokens between two
     evictions; positions that are rotated into q and k are the caller's to count, as an eviction
     makes ``seq_lens`` smaller.  Every buffer stays where it is, so step() and evict() can be captured.
+
+    A prefill() or step() for which the free list has too few pages raises PKV_DEVERR_CAPACITY in ``err``
+    and changes nothing else: lengths, table, weights, free list and pool stay as they were, and the
+    output is zeros (lse -inf).  After an eviction the same call may be made again.
     """
 
     def __init__(self, batch, num_q_heads, num_kv_heads, head_dim, page_size, num_pages, width, budget, keep_first=4,
@@ -593,12 +597,18 @@ class BudgetedDecode:
         self.r2t = torch.zeros((batch, width), dtype=torch.int32, device=dev)
         self.acc = torch.zeros((batch, width), dtype=torch.float32, device=dev)
         self.rows = torch.arange(batch, dtype=torch.int32, device=dev)
-        self.seq_lens, self.prefix_lens, self.last_loc = i32(0), i32(0), i32(0)
+        self.last_loc = i32(0)
+        self.lens = torch.zeros((2, batch), dtype=torch.int32, device=dev)    # each request's keys; those that attention sees
+        self.start = torch.zeros((3, batch), dtype=torch.int32, device=dev)   # both as a refused call leaves them; new slots
+        self.seq_lens, self.seen_lens = self.lens
+        self.prefix_lens, _, self.new_loc = self.start
+        self.start_is = torch.tensor([[0], [0], [-1]], dtype=torch.int32, device=dev)
+        self.start_keys = torch.tensor([[True], [False], [False]], device=dev)
+        self.before_row = self.rows.long() * width - 1     # index of the column before each row's first
         self.budget, self.keep_first, self.keep_last = i32(budget), i32(keep_first), i32(keep_last)
         self.free_pages = torch.arange(num_pages, dtype=torch.int32, device=dev)
         self.free_state = torch.tensor([0, num_pages], dtype=torch.int32, device=dev)
         self.err = torch.zeros(1, dtype=torch.int32, device=dev)
-        self.new_loc = i32(0)
         self.q = torch.zeros((batch, num_q_heads, head_dim), dtype=torch.bfloat16, device=dev)
         self.k_new = torch.zeros((batch, num_kv_heads, head_dim), dtype=torch.bfloat16, device=dev)
         self.v_new = torch.zeros_like(self.k_new)
@@ -610,34 +620,43 @@ class BudgetedDecode:
 
     def _args(self, q, out, lse, **kw):
         return self.pool.args(B.PKV_LAYOUT_REQ_TO_TOKEN, q, out, sm_scale=self.sm_scale, max_seq_len=self.width, lse=lse,
-                              seq_lens=self.seq_lens, req_to_token=self.r2t, req_pool_idx=self.rows, **kw)
+                              seq_lens=self.seen_lens, req_to_token=self.r2t, req_pool_idx=self.rows, **kw)
 
     def _grow(self, new_lens, new_loc, k_new, v_new):
-        """Each request by new_lens [B] tokens: slots, table columns, rows."""
-        self.prefix_lens.copy_(self.seq_lens)
-        self.seq_lens.add_(new_lens)
-        last = (self.prefix_lens - 1).clamp_(min=0).long()
-        self.last_loc.copy_(self.r2t.gather(1, last[:, None])[:, 0])
-        B.pkv_alloc_extend(self.prefix_lens, self.seq_lens, self.last_loc, self.page_size, self.num_pages, self.free_pages,
+        """Each request by new_lens [B] tokens, at slots new_loc (-1 all of them): slots, table columns, rows -> whether
+        there was room (bool [1], on the device).  A refused allocation writes no slot, and rows of slot -1 are not stored."""
+        torch.where(self.start_keys, self.seq_lens, self.start_is, out=self.start)
+        lens = self.prefix_lens + new_lens
+        torch.take(self.r2t, (self.before_row + self.prefix_lens).clamp_(0, self.r2t.numel() - 1), out=self.last_loc)
+        B.pkv_alloc_extend(self.prefix_lens, lens, self.last_loc, self.page_size, self.num_pages, self.free_pages,
                            self.free_state, new_loc, self.err)
+        room = new_loc[:1] >= 0
+        torch.where(room, lens, self.start[:2], out=self.lens)
         B.pkv_write_req_to_token(self.r2t, self.rows, self.prefix_lens, self.seq_lens, new_loc, self.err)
         self.pool.store(k_new, v_new, new_loc, self.err)
+        return room
 
     def prefill(self, q, k_new, v_new, new_lens):
         """new_lens: each request's new tokens (host integers), whose rows q, k_new, v_new hold in order -> out."""
         total = sum(new_lens)
+        if len(new_lens) != self.batch or min(new_lens) < 0 or q.shape[0] != total:
+            raise ValueError("new_lens must count q's rows, request by request")
+        out = torch.zeros_like(q)
+        if total == 0:
+            return out
         at = np.concatenate([[0], np.cumsum(new_lens)]).astype(np.int32)
         up = lambda x: torch.from_numpy(np.ascontiguousarray(x)).to(self.device)  # noqa: E731
-        self._grow(up(np.asarray(new_lens, dtype=np.int32)), torch.full((total,), -1, dtype=torch.int32, device=self.device), k_new, v_new)
-        out, lse = torch.empty_like(q), torch.empty(q.shape[:2], dtype=torch.float32, device=self.device)
-        args = self._args(q, out, lse, qo_indptr=up(at), max_q_len=max(new_lens))
+        room = self._grow(up(np.asarray(new_lens, dtype=np.int32)), torch.full((total,), -1, dtype=torch.int32, device=self.device),
+                          k_new, v_new)
+        lse = torch.empty(q.shape[:2], dtype=torch.float32, device=self.device)
+        args = self._args(q, out, lse, qo_indptr=up(at) * room, max_q_len=max(new_lens))
         B.pkv_byte_extend(args, torch.empty(B.pkv_byte_extend_workspace_size(args), dtype=torch.uint8, device=self.device), self.err)
         seen = [min(n, self.window) for n in new_lens]
         if not sum(seen):
             return out
         rows = up(np.concatenate([np.arange(e - n, e) for e, n in zip(at[1:], seen)]))
-        args = self._args(q[rows], None, lse[rows], qo_indptr=up(np.concatenate([[0], np.cumsum(seen)]).astype(np.int32)),
-                          acc_in=self.acc, acc_out=self.acc)
+        first = up(np.concatenate([[0], np.cumsum(seen)]).astype(np.int32)) * room
+        args = self._args(q[rows], None, lse[rows], qo_indptr=first, acc_in=self.acc, acc_out=self.acc)
         B.pkv_byte_weights(args, torch.empty(B.pkv_byte_weights_workspace_size(args), dtype=torch.uint8, device=self.device), self.err)
         return out
 
