@@ -581,9 +581,10 @@ class BudgetedDecode:
     evictions; positions that are rotated into q and k are the caller's to count, as an eviction
     makes ``seq_lens`` smaller.  Every buffer stays where it is, so step() and evict() can be captured.
 
-    A prefill() or step() for which the free list has too few pages raises PKV_DEVERR_CAPACITY in ``err``
-    and changes nothing else: lengths, table, weights, free list and pool stay as they were, and the
-    output is zeros (lse -inf).  After an eviction the same call may be made again.
+    A prefill() or step() for which the free list has too few pages raises PKV_DEVERR_CAPACITY in ``err``,
+    one that would take a request past ``width`` PKV_DEVERR_RANGE.  It changes nothing else: lengths, table,
+    weights, free list and pool stay as they were, and the output is zeros (lse -inf).  After an
+    eviction the same call may be made again.
     """
 
     def __init__(self, batch, num_q_heads, num_kv_heads, head_dim, page_size, num_pages, width, budget, keep_first=4,
@@ -627,6 +628,7 @@ class BudgetedDecode:
         there was room (bool [1], on the device).  A refused allocation writes no slot, and rows of slot -1 are not stored."""
         torch.where(self.start_keys, self.seq_lens, self.start_is, out=self.start)
         lens = self.prefix_lens + new_lens
+        lens.masked_fill_(lens > self.width, -1)       # past the table: no length, so the allocation refuses the call
         torch.take(self.r2t, (self.before_row + self.prefix_lens).clamp_(0, self.r2t.numel() - 1), out=self.last_loc)
         B.pkv_alloc_extend(self.prefix_lens, lens, self.last_loc, self.page_size, self.num_pages, self.free_pages,
                            self.free_state, new_loc, self.err)

@@ -106,3 +106,31 @@ def test_a_full_pool(B, ps, pages, steps, graph):
     step()
     r.grown(before, "step after the eviction")
     r.prefill([3, 0, 1])
+
+
+@pytest.mark.parametrize("graph", [False, True])
+@pytest.mark.parametrize("ps,width", [(16, 205), (64, 256), (1, 203)])
+def test_a_request_as_long_as_its_row(B, ps, width, graph):
+    """Steps up to the table's width, further ones and a prefill that are refused, an eviction, and the step again."""
+    r = Run(B, 90 + ps, ps, 64, 2, 2, 3 * -(-width // ps), width)
+    r.prefill([30, width - 3, 50])
+    step = r.loop.step
+    for i in range(3):
+        before = host(r.loop.acc).astype(np.float64)
+        r.next_rows()
+        if graph and i == 0:
+            step = captured(r.loop)
+        step()
+        r.grown(before, "step %d" % i)
+    assert r.m.lens.max() == width
+    r.next_rows()
+    for i in range(3):
+        r.refused(step, B.PKV_DEVERR_RANGE, "step past the width")
+        assert not r.loop.out.any() and torch.isneginf(r.loop.lse).all()
+    q, k, v = r.rows(width)
+    r.refused(lambda: r.loop.prefill(q, k, v, [width, 0, 0]), B.PKV_DEVERR_RANGE, "prefill past the width")
+    r.evict()
+    before = host(r.loop.acc).astype(np.float64)
+    r.next_rows()
+    step()
+    r.grown(before, "step after the eviction")
