@@ -620,8 +620,9 @@ class BudgetedDecode:
         self.evict_workspace = torch.empty(B.pkv_evict_workspace_size(batch, width, page_size), dtype=torch.uint8, device=dev)
 
     def _args(self, q, out, lse, **kw):
-        return self.pool.args(B.PKV_LAYOUT_REQ_TO_TOKEN, q, out, sm_scale=self.sm_scale, max_seq_len=self.width, lse=lse,
-                              seq_lens=self.seen_lens, req_to_token=self.r2t, req_pool_idx=self.rows, **kw)
+        kw.setdefault("max_seq_len", self.width)
+        return self.pool.args(B.PKV_LAYOUT_REQ_TO_TOKEN, q, out, sm_scale=self.sm_scale, lse=lse, seq_lens=self.seen_lens,
+                              req_to_token=self.r2t, req_pool_idx=self.rows, **kw)
 
     def _grow(self, new_lens, new_loc, k_new, v_new):
         """Each request by new_lens [B] tokens, at slots new_loc (-1 all of them): slots, table columns, rows -> whether
@@ -648,17 +649,21 @@ class BudgetedDecode:
             return out
         at = np.concatenate([[0], np.cumsum(new_lens)]).astype(np.int32)
         up = lambda x: torch.from_numpy(np.ascontiguousarray(x)).to(self.device)  # noqa: E731
+        # what the requests will hold, from the device: the workspaces are sized by it, not by the table
+        # (the uploads below wait for the stream too)
+        keys = [n + m for n, m in zip(self.seq_lens.tolist(), new_lens)]
+        bounds = dict(max_seq_len=min(self.width, max(keys)), total_kv=sum(keys))
         room = self._grow(up(np.asarray(new_lens, dtype=np.int32)), torch.full((total,), -1, dtype=torch.int32, device=self.device),
                           k_new, v_new)
         lse = torch.empty(q.shape[:2], dtype=torch.float32, device=self.device)
-        args = self._args(q, out, lse, qo_indptr=up(at) * room, max_q_len=max(new_lens))
+        args = self._args(q, out, lse, qo_indptr=up(at) * room, max_q_len=max(new_lens), **bounds)
         B.pkv_byte_extend(args, torch.empty(B.pkv_byte_extend_workspace_size(args), dtype=torch.uint8, device=self.device), self.err)
         seen = [min(n, self.window) for n in new_lens]
         if not sum(seen):
             return out
         rows = up(np.concatenate([np.arange(e - n, e) for e, n in zip(at[1:], seen)]))
         first = up(np.concatenate([[0], np.cumsum(seen)]).astype(np.int32)) * room
-        args = self._args(q[rows], None, lse[rows], qo_indptr=first, acc_in=self.acc, acc_out=self.acc)
+        args = self._args(q[rows], None, lse[rows], qo_indptr=first, max_q_len=max(seen), acc_in=self.acc, acc_out=self.acc, **bounds)
         B.pkv_byte_weights(args, torch.empty(B.pkv_byte_weights_workspace_size(args), dtype=torch.uint8, device=self.device), self.err)
         return out
 

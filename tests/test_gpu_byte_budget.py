@@ -134,3 +134,20 @@ def test_a_request_as_long_as_its_row(B, ps, width, graph):
     r.next_rows()
     step()
     r.grown(before, "step after the eviction")
+
+
+@pytest.mark.parametrize("new", [[300, 2] + [0] * 30, [5] * 32, [0] * 31 + [1]])
+def test_prefill_workspaces_follow_the_keys(B, new):
+    """32 rows of 16384 columns, nearly all of them empty: what a prefill takes is by its keys, not by the table."""
+    from paged_kv_cache_req_gb300.engine import BudgetedDecode
+    rng, H, D = np.random.default_rng(100), 2, 64
+    loop = BudgetedDecode(32, 2 * H, H, D, 16, 200, 16384, 1024, window=8)
+    for turn in range(2):
+        q, k, v = (to_bf16(values(rng, (sum(new), h, D))) for h in (2 * H, H, H))
+        torch.cuda.synchronize()
+        torch.cuda.reset_peak_memory_stats()
+        before = torch.cuda.memory_allocated()
+        out = loop.prefill(q, k, v, new)
+        assert loop.check_errors() == 0 and torch.isfinite(out).all()
+        # K and V of 32 x 16384 keys in bf16 are 256 MB
+        assert torch.cuda.max_memory_allocated() - before < 64 << 20
