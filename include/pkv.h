@@ -745,8 +745,9 @@ size_t pkv_byte_decode_workspace_size(const pkv_byte_args *args);
  * As pkv_quant_extend, with the pool's values for K and V; acc_in and acc_out must be NULL
  * (pkv_byte_weights gives the weights of its rows).  Requests with more than 128 (row, query
  * head) pairs per kv head have their keys and values copied out of the pool into the workspace
- * as bf16 (exactly), which total_kv sizes; their weights are bf16 in the product with V (2^-9
- * relative), and a row that sees a key whose V holds a NaN may be NaN in all its dims there.
+ * as bf16, which total_kv sizes: exactly, but that values of 2^128 become the largest bf16 and those below
+ * 2^-133, the least, are rounded.  Their weights are bf16 in the product with V (2^-9 relative), and a
+ * row that sees a key whose V holds a NaN may be NaN in all its dims there.
  */
 pkv_status pkv_byte_extend(const pkv_byte_args *args, void *workspace, size_t workspace_bytes, int32_t *err_flags,
                          pkv_stream_t stream);

@@ -394,6 +394,13 @@ struct Quant8 {
             }
     }
 
+    // Two fp32 as bf16, at most its largest number: a value of 2^128 (code 256 at the largest scale) would be infinite, and
+    // times the weight of a row that does not see its key, 0, NaN.  NaN stays.
+    __device__ __forceinline__ static uint32_t to_bf16x2(float lo, float hi) {
+        uint32_t r;
+        asm("cvt.rn.satfinite.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+        return r;
+    }
     // Sixteen dims of a held row: both as bf16, which has the range for any scale.
     struct Block {
         uint4 codes;
@@ -417,7 +424,7 @@ struct Quant8 {
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const float2 f = quant::f16x2_to_f32(i % 2 ? byte::hi_to_f16(w[i / 2]) : byte::lo_to_f16(w[i / 2]));
-            x[i] = any ? (is_v ? 0u : 0x7fff7fffu) : pack_bf16x2(f.x * s, f.y * s);
+            x[i] = any ? (is_v ? 0u : 0x7fff7fffu) : to_bf16x2(f.x * s, f.y * s);
         }
     }
 };

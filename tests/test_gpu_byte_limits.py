@@ -66,3 +66,33 @@ def test_small_queries_over_large_keys(B, ps, rows, chunk):
         acc, e = weights(B, cache, q, lse, rows, total_kv=total)
         assert e == 0
         check(cache, q, None, None, rows, acc=acc)
+
+
+def rows_of_one(rng, cache, n, g):
+    return to_bf16(values(rng, (n, cache.H * g, cache.D)))
+
+
+@pytest.mark.parametrize("D,ps", [(64, 16), (128, 64)])
+def test_held_keys_the_largest_value_that_few_rows_see(B, D, ps):
+    """A value that stands for 2^128 in V: rows that do not see its key are as if it were not there."""
+    rng = np.random.default_rng(70 + D)
+    L, n, g, late = 300, 200, 2, 290
+    cache = Cache(rng, [L, 200], ps, 1, D)
+    t = R.tile_of(ps)
+    slot = cache.slots[0][late]
+    cache.pool.E[slot // t, 0, 1] = 247
+    cache.pool.codes[slot // t, 0, 1] = 0
+    for dim, code in ((5, 0x78), (9, 0xf8)):      # 256 and -256, times 2^120
+        cache.pool.codes[slot // t, 0, 1, slot % t, dim] = code
+    q = rows_of_one(rng, cache, n + 200, g)
+    out, lse, e = extend(B, cache, q, [n, 200])
+    assert e == 0
+    first = late - (L - n)                        # the first row that sees the key
+    qh, k, v = host(q).astype(np.float64), cache.pool.read(cache.slots[0], 0), cache.pool.read(cache.slots[0], 1)
+    ref, rl, _, tol, lt, _ = R.attention(qh[:first], k, v, np.arange(L - n + 1, L - n + 1 + first), D ** -0.5, np.ones(1), True)
+    R.assert_within(host(out)[:first], ref, tol, "rows that do not see it")
+    R.assert_within(host(lse)[:first], rl, lt, "their lse")
+    rest = [d for d in range(D) if d not in (5, 9)]
+    ref, rl, _, tol, lt, _ = R.attention(qh[first:n], k, v, np.arange(late + 1, L + 1), D ** -0.5, np.ones(1), True)
+    R.assert_within(host(out)[first:n][..., rest], ref[..., rest], tol[..., rest], "the other dims of rows that see it")
+    check(cache, q, out, lse, [n, 200], only=[1], held=True)
