@@ -44,7 +44,8 @@
 // keeps its bits: weights are held times 2^7 for that, as high as 2^15 with a maximum that is
 // raised past 2^8 only (one raised past 2^4, with a lift of 11, costs 8 %: 1,195 -> 1,293 us at 8192 rows
 // over 16384 keys).  kBf16V (the 8-bit pool, whose scales need bf16's range): V and P bf16, as for
-// the bf16 pool.
+// the bf16 pool.  bf16 keeps its bits at any size, so these weights are held times 2^-16: their sums with V
+// stay inside fp32 for any V (from 2^105 on they did not at 2^7).
 #include <algorithm>
 
 #include "extend_held.cuh"
@@ -61,7 +62,8 @@ constexpr int kProducerWarp = 8, kQkWarp = 9, kPvWarp = 10, kEpiWarp0 = 11, kVPr
 constexpr float kLn2 = 0.69314718055994531f;
 constexpr float kLog2e = 1.44269504088896341f;
 constexpr float kLazy = 8.f;
-constexpr float kLift = 7.f;               // kHeld: log2 of what the fp16 weights are held times
+// kHeld: log2 of what the weights are held times, in fp16 and in bf16
+constexpr float held_lift(bool bf16) { return bf16 ? -16.f : 7.f; }
 constexpr int kRing = 8;                   // slots of the item queue
 constexpr int kItemReaders = 16;           // warps that read every queued item
 constexpr int kMostItems = 1 << 29;        // at which the item counts saturate
@@ -1041,9 +1043,10 @@ ext_kernel(const Params p, const __grid_constant__ CUtensorMap tmq, const __grid
                     mx = top * scale;   // scores are unscaled up to here (the scale is positive)
                 }
                 bool raise = m == -INFINITY && mx != -INFINITY;
-                if (kHeld) {   // m is kLift below the maximum; raised by the exponent that a weight would have
-                    raise |= fmaf(top, scale, -m) > kLift + kLazy;
-                    mx -= kLift;
+                if (kHeld) {   // m is the lift below the maximum; raised by the exponent that a weight would have
+                    constexpr float lift = held_lift(kBf16V);
+                    raise |= fmaf(top, scale, -m) > lift + kLazy;
+                    mx -= lift;
                 } else {
                     raise |= mx > m + kLazy;
                 }

@@ -96,3 +96,15 @@ def test_held_keys_the_largest_value_that_few_rows_see(B, D, ps):
     ref, rl, _, tol, lt, _ = R.attention(qh[first:n], k, v, np.arange(late + 1, L + 1), D ** -0.5, np.ones(1), True)
     R.assert_within(host(out)[first:n][..., rest], ref[..., rest], tol[..., rest], "the other dims of rows that see it")
     check(cache, q, out, lse, [n, 200], only=[1], held=True)
+
+
+@pytest.mark.parametrize("D,ps,rows", [(64, 16, [200, 20]), (128, 64, [300, 300])])
+@pytest.mark.parametrize("big", [2.0 ** 112, 2.0 ** 123, 2.0 ** -100])
+def test_held_keys_large_and_small_values(B, D, ps, rows, big):
+    """V near the ends of the range: the sums of the rows stay inside fp32."""
+    rng = np.random.default_rng(71 + D)
+    cache = Cache(rng, [500, 310], ps, 2, D, v_scale=lambda t: np.full(len(t), np.float32(big)))
+    q = rows_of_one(rng, cache, sum(rows), 2)
+    out, lse, e = extend(B, cache, q, rows)
+    assert e == 0
+    check(cache, q, out, lse, rows, held=True)
