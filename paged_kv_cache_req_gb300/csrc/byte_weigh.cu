@@ -745,9 +745,9 @@ constexpr int kManyRows = 64, kManyTiles = 20;
 
 pkv_status launch_weigh(const char *who, const Params &p, const WeighParams &wp, int head_dim, int64_t rows, int64_t keys, cudaStream_t s) {
     const unsigned L = static_cast<unsigned>(p.tab.max_len), B = static_cast<unsigned>(p.batch), H = static_cast<unsigned>(p.hkv);
-    if (L == 0) return ok();
     pkv_status st;
-    const bool many = rows >= kManyRows || keys * p.hkv / kTcKeys >= static_cast<int64_t>(kManyTiles) * std::max(1, sm_count());
+    // (max_seq_len 0: the blocks of weigh_kernel that check the requests)
+    const bool many = L > 0 && (rows >= kManyRows || keys * p.hkv / kTcKeys >= static_cast<int64_t>(kManyTiles) * std::max(1, sm_count()));
     if (many && p.batch <= kTcBatch) {
         Params q = p;
         if (boxes(p.t_shift, head_dim)) {   // the pool as lines of 128 bytes; a box is K's of a tile and head
@@ -766,9 +766,9 @@ pkv_status launch_weigh(const char *who, const Params &p, const WeighParams &wp,
         st = launch_status(launch_chained(kern, dim3(static_cast<unsigned>(std::max(1, sm_count()))), dim3(kTcThreads), smem, s, q, wp), who);
     } else {
         auto *kern = head_dim == 128 ? weigh_kernel<128> : weigh_kernel<64>;
-        st = launch_status(launch_chained(kern, dim3((L + kWeighKeys - 1) / kWeighKeys, H, B), dim3(kWeighWarps * 32), 0, s, p, wp), who);
+        st = launch_status(launch_chained(kern, dim3(std::max(1u, (L + kWeighKeys - 1) / kWeighKeys), H, B), dim3(kWeighWarps * 32), 0, s, p, wp), who);
     }
-    if (st != PKV_OK) return st;
+    if (st != PKV_OK || L == 0) return st;
     return launch_status(launch_chained(add_kernel, dim3((L + 255) / 256, B), dim3(256), 0, s, p, wp), who);
 }
 

@@ -108,3 +108,34 @@ def test_held_keys_large_and_small_values(B, D, ps, rows, big):
     out, lse, e = extend(B, cache, q, rows)
     assert e == 0
     check(cache, q, out, lse, rows, held=True)
+
+
+def test_weights_check_a_call_without_keys(B):
+    """max_seq_len of 0: what the requests say is looked at as by the other calls."""
+    rng = np.random.default_rng(72)
+    cache = Cache(rng, [40, 50], 16, 1, 64)
+    q = rows_of_one(rng, cache, 4, 2)
+    lse = torch.zeros((4, 2), device=DEV)
+    none = i32([0, 0])
+
+    def call(**kw):
+        kw.setdefault("kv_end", i32([0] * 4))
+        out = torch.empty_like(q)
+        got = []
+        for fn, size, more in ((B.pkv_byte_extend, B.pkv_byte_extend_workspace_size, {}),
+                               (B.pkv_byte_weights, B.pkv_byte_weights_workspace_size, dict(acc_out=table_of(cache, rng, 7.0)))):
+            fields = dict(lse=lse, qo_indptr=i32([0, 2, 4]), max_seq_len=0)
+            fields.update(kw, **more)
+            a = cache.args(B, "table", q, out, **fields)
+            err = err_word()
+            fn(a, torch.empty(size(a), dtype=torch.uint8, device=DEV), err)
+            got.append(err.item())
+        assert (host(fields["acc_out"]) == 7).all()
+        assert got[0] == got[1], got
+        return got[1]
+
+    assert call(seq_lens=none) == 0
+    assert call() == 4
+    assert call(seq_lens=none, req_pool_idx=i32([cache.rpi[0], 55])) == 1
+    assert call(seq_lens=none, qo_indptr=i32([0, 2, 9])) == 1
+    assert call(seq_lens=i32([0, -1])) == 1
