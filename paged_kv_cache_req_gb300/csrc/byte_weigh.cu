@@ -28,6 +28,13 @@ __device__ __forceinline__ uint64_t factors(uint64_t f, uint64_t ks) {
     return pair(fminf(x.x, 3.4e38f), fminf(x.y, 3.4e38f));
 }
 
+// Given bounds of a request without keys are 0 (the block's threads look at them).
+__device__ __forceinline__ void check_bounds_of_none(const Params &p, const Req &req) {
+    if (req.L > 0 || !p.qo_indptr || !p.kv_end) return;
+    for (int tok = threadIdx.x; tok < req.n; tok += blockDim.x)
+        if (__ldg(p.kv_end + req.qo0 + tok) != 0) raise_flag(p.err, PKV_DEVERR_RANGE);
+}
+
 // Place in its row of the k-th 16 bytes of lane (r, c)'s dims: the four c of two rows lie in eight bank groups.
 __device__ __forceinline__ int q_chunk(int row, int c, int k) { return (4 * k + c) ^ ((row & 1) << 2); }
 template <int D>
@@ -45,6 +52,7 @@ __global__ void __launch_bounds__(kWeighWarps * 32, 2) weigh_kernel(const Params
     const int b = blockIdx.z, kh = blockIdx.y, warp = threadIdx.x >> 5, lane = threadIdx.x & 31, r = lane >> 2, c = lane & 3;
     const Req req = load_req(p, b, blockIdx.x == 0 && kh == 0 && threadIdx.x == 0);
     const int k0 = blockIdx.x * kWeighKeys + warp * 64;
+    if (blockIdx.x == 0 && kh == 0) check_bounds_of_none(p, req);
     if (static_cast<int>(blockIdx.x) * kWeighKeys >= req.L) return;
     const int rows = req.n * p.g;
     constexpr int KS = D / 16;
@@ -315,6 +323,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_many_kernel(const __grid_
     __syncthreads();
     tc05::fence_after_sync();
     pdl_launch_next();   // (no sooner: a kernel that takes tensor memory must not come between)
+    for (int b = blockIdx.x; b < p.batch; b += gridDim.x) check_bounds_of_none(p, reqs[b]);
     const uint32_t tbase = tmem_slot;
     volatile int *left = &left_s;
     const int64_t all = static_cast<int64_t>(off[p.batch]) * p.hkv, per = (all + gridDim.x - 1) / gridDim.x;

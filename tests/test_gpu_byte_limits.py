@@ -139,3 +139,23 @@ def test_weights_check_a_call_without_keys(B):
     assert call(seq_lens=none, req_pool_idx=i32([cache.rpi[0], 55])) == 1
     assert call(seq_lens=none, qo_indptr=i32([0, 2, 9])) == 1
     assert call(seq_lens=i32([0, -1])) == 1
+
+
+@pytest.mark.parametrize("total", [0, 1 << 22])
+@pytest.mark.parametrize("n", [3, 600])
+def test_weights_check_the_bounds_of_requests_without_keys(B, total, n):
+    """A bound that is not 0 for a row of a request without keys is outside; the other requests get theirs."""
+    rng = np.random.default_rng(73 + n)
+    rows = [2, n, 5]
+    cache = Cache(rng, [300, 0, 70], 16, 2, 64)
+    q = rows_of_one(rng, cache, sum(rows), 2)
+    ends = np.concatenate([[300, 7], np.zeros(n), [70, 1, 0, 69, 30]]).astype(np.int32)
+    out, lse, e = extend(B, cache, q, rows, "table", ends)
+    assert e == 0
+    want, e = weights(B, cache, q, lse, rows, ends, total_kv=total)
+    assert e == 0
+    for at, end in ((2, 1), (2 + n - 1, -1), (2 + n // 2, 2 ** 31 - 1)):
+        bad = ends.copy()
+        bad[at] = end
+        acc, e = weights(B, cache, q, lse, rows, bad, total_kv=total)
+        assert e == 1 and torch.equal(acc, want), (at, end)
