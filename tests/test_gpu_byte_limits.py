@@ -1,5 +1,5 @@
-"""The calls over an 8-bit pool at the ends of what they allow: queries and keys near either end of
-bf16's range."""
+"""The calls over an 8-bit pool at the ends of what they allow: queries, keys and values near the
+ends of bf16's range, calls and requests without keys, waits that run out."""
 import numpy as np
 import pytest
 import torch
@@ -159,3 +159,46 @@ def test_weights_check_the_bounds_of_requests_without_keys(B, total, n):
         bad[at] = end
         acc, e = weights(B, cache, q, lse, rows, bad, total_kv=total)
         assert e == 1 and torch.equal(acc, want), (at, end)
+
+
+def cold():
+    """Whatever lay in L2 is gone."""
+    torch.empty(1 << 29, dtype=torch.uint8, device=DEV).zero_()
+
+
+@pytest.mark.parametrize("call", ["decode", "decode of few", "extend", "held", "weights"])
+def test_waits_run_out_when_nothing_is_cached(B, call):
+    """With a limit of 1 ns a wait is one look, before copies from memory can have landed: the flag says so, and the
+    next call is right."""
+    rng = np.random.default_rng(74)
+    cache = Cache(rng, [2000] * (3 if call == "decode of few" else 24), 16, 2, 128)
+    n = {"extend": 2, "held": 90, "weights": 40}.get(call, 1)
+    rows = [n] * len(cache.lens)
+    q = rows_of_one(rng, cache, sum(rows), 4)
+    out, lse, err = torch.empty_like(q), torch.empty(q.shape[:2], device=DEV), err_word()
+    kw = {} if n == 1 else dict(qo_indptr=i32(np.concatenate([[0], np.cumsum(rows)])))
+    good = decode(B, cache, q) if n == 1 else extend(B, cache, q, rows)
+    assert good[2] == 0
+    acc = table_of(cache, None, 0.0)
+    if call == "weights":
+        kw.update(acc_out=acc)
+        lse = good[1]
+    a = cache.args(B, "table", q, out, lse=lse, **kw)
+    fn, size = {1: (B.pkv_byte_decode, B.pkv_byte_decode_workspace_size)}.get(n, (B.pkv_byte_extend, B.pkv_byte_extend_workspace_size))
+    if call == "weights":
+        fn, size = B.pkv_byte_weights, B.pkv_byte_weights_workspace_size
+    ws = torch.empty(size(a), dtype=torch.uint8, device=DEV)
+    cold()
+    B.pkv_set_wait_limit(1)
+    try:
+        fn(a, ws, err)
+        assert err.item() == B.PKV_DEVERR_TIMEOUT
+    finally:
+        B.pkv_set_wait_limit(0)
+    err.zero_()
+    fn(a, ws, err)
+    assert err.item() == 0
+    if call == "weights":
+        check(cache, q, None, None, rows, acc=acc, only=[0, len(rows) - 1])
+    else:
+        assert torch.equal(out, good[0]) and torch.equal(lse, good[1])
