@@ -870,9 +870,9 @@ def measure(opts, world, rank, local, dist, one_thread_baseline=False):
 
 
 # Every other recipe, measured after the headline on the same GPU (N = 1): workload,
-# cross-attention mode, timed steps.  Each entry carries its own clocks, roofline,
-# traffic and CPU baseline; the configurations the oracle runs in seconds also carry
-# a 1-thread oracle time.
+# cross-attention mode, timed steps.  Each has a line of its own on stderr, with its clocks,
+# roofline, traffic and CPU baseline (and a 1-thread oracle time where the oracle runs in
+# seconds); the line on stdout, which is read whole, holds their values only.
 PER_CONFIG = (
     ("tiny_gqa", "paged", 200, False),
     ("qwen3_0p6b", "paged", 200, False),
@@ -907,10 +907,10 @@ def per_config_entries(args, world, rank, local, dist):
         torch.cuda.empty_cache()
         if line is None:
             continue
-        for k in ("n_gpus", "higher_is_better", "scaling", "vs_baseline", "data", "warmup"):
-            line.pop(k, None)
-        key = name if name != "whisper_encdec" else "whisper_encdec_" + cross
-        out[key + ("_fused" if fused else "")] = line
+        key = (name if name != "whisper_encdec" else "whisper_encdec_" + cross) + ("_fused" if fused else "")
+        print(json.dumps({"per_config": key, **line}), file=sys.stderr, flush=True)
+        out[key] = {"value": line["value"], "unit": line["unit"], "ms_per_step": line["ms_per_step"],
+                    "frac": (line.get("roofline") or {}).get("frac")}
     return out
 
 
