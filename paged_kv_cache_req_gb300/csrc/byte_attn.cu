@@ -16,7 +16,8 @@
 // V's conversion, so that one gives the pair of keys that the MMA wants.
 //
 // What bounds it: with one row per head a large call reads the pool at 6.3 TB/s (64 requests x 16384 keys, 8 heads of
-// 128: 340 us; 4096 keys: 101 us, of which 16 are the table, first copies, uneven ends and the merge).  With 9 to 16
+// 128: 344 us; 4096 keys: 97 us, of which 16 are the table, first copies, uneven ends and the merge).  On pages of 8, 4, 2
+// and 1 the copies of small pieces bound it, made by the warps that do the math: 397, 425, 484 and 633 us.  With 9 to 16
 // rows, 16 x 16384 keys take 105 us for 302 MB: 32 % of the tensor pipe, warps waiting for their own last instruction
 // (8 warps of 250 registers).  With heads of 64 dims instructions bound it: 64 x 1500 keys x 20 heads in 52 us, 48 % of the ALU.
 #include "byte_weigh.cuh"

@@ -39,7 +39,8 @@ takes no ``scales``.
 ``BudgetedDecode`` is a serving loop of its own: prefills and decode steps over an 8-bit pool,
 which count what each key receives, and evictions that keep every request within a budget.
 
-Nothing here computes: every step runs in libpkv's kernels.
+No attention, quantisation, allocation or eviction is computed here: that runs in libpkv's kernels.
+``BudgetedDecode`` keeps its requests' lengths with a few torch operators per call.
 """
 from __future__ import annotations
 
